@@ -369,6 +369,115 @@ ret_status retnet_decode_step(const retnet_stack_desc *d, const retnet_layer_wei
                               float *const *S, float *const *z, void *X, void *ws,
                               size_t ws_bytes, ret_stream_t stream);
 
+/* ---- After the stack: LayerNorm with its gradients, the logits' scores, distillation ----
+ *
+ * The pages train and evaluate a language model ([eepw]) but give no formulas
+ * for its ends; the ones below are the readings taken.  Rows (i, j),
+ * 0 <= i < n0, 0 <= j < n1, numbered r = i n1 + j, start at element
+ * i s[0] + j s[1] of a tensor (two strides >= 0, such as a [B, N, d] view or
+ * logits[:, :-1] of a [B, N, V] tensor); a row's values are contiguous.  Rows
+ * of an output must not overlap one another (RET_EINVAL).  Per-row vectors
+ * (mean, loss, ...) are contiguous [n0 n1].  No row, stride or base pointer
+ * needs more than its element's alignment (16-byte aligned rows run faster).
+ * None of these calls changes an input. */
+
+/* LayerNorm of each row of d values (1 <= d <= 2^24; fp32 arithmetic):
+ *   y = (x - mean) rstd w + b,   rstd = 1 / sqrt(var + eps), biased variance.
+ * x, y in `dtype`; w, b: fp32 [d] or NULL (1 and 0); mean, rstd: fp32 [n0 n1],
+ * written where not NULL (the backward needs both).  y may be x itself (same
+ * pointer and strides); other overlaps are refused (RET_EINVAL). */
+typedef struct {
+  int64_t n0, n1;  /* rows                                             */
+  int d;           /* values of a row                                  */
+  ret_dtype dtype; /* x, y, dy, dx                                     */
+  float eps;       /* >= 0                                             */
+  int64_t sx[2];   /* element strides of x                             */
+  int64_t sg[2];   /* of dy (backward only)                            */
+  int64_t so[2];   /* of y (forward) or dx (backward)                  */
+} retnet_layernorm_desc;
+
+ret_status retnet_layernorm_fwd(const retnet_layernorm_desc *d, const void *x, const float *w,
+                                const float *b, void *y, float *mean, float *rstd,
+                                ret_stream_t stream);
+
+/* Gradients, with h = (x - mean) rstd and g = dy w (w NULL: 1):
+ *   dx = rstd (g - mean(g) - h mean(g h)),  dw = sum_rows dy h,  db = sum_rows dy.
+ * mean, rstd: as the forward wrote them.  dw, db: fp32 [d], NULL = not wanted;
+ * zero where there are no rows.  The sums over the rows are added in a fixed
+ * order: equal calls give equal bits.  dx may be x or dy itself.  ws:
+ * retnet_layernorm_bwd_workspace_size(d) bytes, 256-byte aligned. */
+size_t retnet_layernorm_bwd_workspace_size(const retnet_layernorm_desc *d);
+ret_status retnet_layernorm_bwd(const retnet_layernorm_desc *d, const void *x, const void *dy,
+                                const float *w, const float *mean, const float *rstd, void *dx,
+                                float *dw, float *db, void *ws, size_t ws_bytes,
+                                ret_stream_t stream);
+
+/* Largest `top` of the two calls below, and distillation's largest V. */
+#define RETNET_MAX_TOP 128
+#define RETNET_MAX_DISTILL_V (1 << 20)
+
+typedef struct {
+  int64_t n0, n1;     /* rows                                                   */
+  int V;              /* logits of a row, 1 .. 2^30                             */
+  ret_dtype dtype;    /* of the logits and of their gradient                    */
+  double temperature; /* T > 0                                                  */
+  int top;            /* alternatives wanted / entries of the teacher's list    */
+  int id_bytes;       /* 4 or 8: int32 or int64 `tokens` / `ids`                */
+  int tail;           /* distillation: 1 = with the rest bucket                 */
+  int64_t sx[2];      /* element strides of the logits                          */
+  int64_t sd[2];      /* of their gradient (distillation)                       */
+} retnet_logits_desc;
+
+/* Scores of logits x [n0 n1][V] at temperature T: with m = max x and
+ * z = sum e^((x - m) / T),
+ *   logprob[r] = (x_t - m) / T - ln z of the given token t = tokens[r],
+ *   entropy[r] = ln z - sum_j p_j (x_j - m) / T,
+ *   the `top` largest logits, equal ones by the lower id first, as
+ *   top_id[r][top] (int64) and top_logprob[r][top].
+ * Any output may be NULL; tokens may be NULL (then logprob must be).
+ *   - A logit of -infinity is a masked token: it has probability 0 and is no
+ *     alternative; missing alternatives have id -1 and log probability
+ *     -infinity.  A row of masked tokens alone has log probabilities of
+ *     -infinity and entropy 0.
+ *   - A NaN or +infinity in a row makes its results NaN (ids -1).
+ *   - A negative token asks for nothing (logprob 0); one >= V gives NaN. */
+ret_status retnet_token_logprobs(const retnet_logits_desc *d, const void *x, const void *tokens,
+                                 float *logprob, float *entropy, float *top_logprob,
+                                 int64_t *top_id, ret_stream_t stream);
+
+/* Distillation of the student's logits x [n0 n1][V] from the teacher's list
+ * ids [n0 n1][top], values [n0 n1][top] (fp32; both contiguous), 1 <= top.
+ * q = softmax(x / T).  The teacher's p over the listed tokens:
+ *   tail 0: softmax(values / T) over the list, p_rest = 0;
+ *   tail 1: e^values (log probabilities at temperature T over the whole
+ *           vocabulary), p_rest = max(0, 1 - sum p) (0 if all V are listed).
+ * Loss of a row and its gradient:
+ *   loss[r] = T^2 [ sum_k p_k ln(p_k / q_k) + p_rest ln(p_rest / q_rest) ],
+ *   dx_j = weight[r] T (q_j - p_j) for a listed token,
+ *          weight[r] T (q_j - p_rest q_j / q_rest) for any other,
+ * where weight[r] is the gradient of the caller's loss with respect to
+ * loss[r] (fp32, NULL = 1).
+ *   - A negative id is an absent entry; of an id listed twice the first entry
+ *     counts; an id >= V makes the row's loss and gradient NaN.
+ *   - A row whose weight is 0 has a gradient of zeros, whatever it holds.
+ *   - A logit of -infinity has q = 0 and, if not listed, gradient 0.  A NaN or
+ *     +infinity makes the row NaN.  A row of -infinity alone has the loss
+ *     +infinity and gradient 0; a row without a teacher (tail 0, no entry
+ *     above -infinity) has loss and gradient 0.
+ * _fwd writes loss and stats [n0 n1][2] = ln sum e^(x/T) over the vocabulary
+ * and over the tokens that are not listed (either may be NULL); _bwd takes
+ * stats and writes dx; _step does both and reads each row from memory once.
+ * dx may be x itself.  V <= RETNET_MAX_DISTILL_V (else RET_EUNSUPPORTED). */
+ret_status retnet_distill_fwd(const retnet_logits_desc *d, const void *x, const void *ids,
+                              const float *values, float *loss, float *stats,
+                              ret_stream_t stream);
+ret_status retnet_distill_bwd(const retnet_logits_desc *d, const void *x, const void *ids,
+                              const float *values, const float *weight, const float *stats,
+                              void *dx, ret_stream_t stream);
+ret_status retnet_distill_step(const retnet_logits_desc *d, const void *x, const void *ids,
+                               const float *values, const float *weight, float *loss,
+                               float *stats, void *dx, ret_stream_t stream);
+
 /* Human-readable text of a status code (static storage). */
 const char *retention_status_string(ret_status s);
 

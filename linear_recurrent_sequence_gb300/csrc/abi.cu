@@ -1264,6 +1264,244 @@ ret_status retention_gemm_bf16(const void *A, const void *Bm, void *C, int M, in
   return RET_OK;
 }
 
+// ---------------------------------------- LayerNorm, logits, distillation
+// Strides of a row set: `width` contiguous values a row.
+static bool rowset_ok(int64_t n0, int64_t n1, const int64_t s[2]) {
+  return n0 >= 0 && n1 >= 0 && s[0] >= 0 && s[1] >= 0;
+}
+
+// Do the rows of an output stay clear of one another?
+static bool rows_disjoint(int64_t n0, int64_t n1, const int64_t s[2], int64_t width) {
+  if (n0 == 0 || n1 == 0) return true;
+  const int64_t span1 = (n1 - 1) * s[1] + width, span0 = (n0 - 1) * s[0] + width;
+  const bool in1 = n1 == 1 || s[1] >= width, in0 = n0 == 1 || s[0] >= width;
+  return (in1 && (n0 == 1 || s[0] >= span1)) || (in0 && (n1 == 1 || s[1] >= span0));
+}
+
+// Row counts whose products and extents stay within 62 bits.
+static bool rows_countable(int64_t n0, int64_t n1) {
+  return n0 <= ((int64_t)1 << 40) && n1 <= ((int64_t)1 << 40) &&
+         (n0 == 0 || n1 <= ((int64_t)1 << 40) / n0);
+}
+
+static bool strides_bounded(const int64_t s[2]) {
+  return s[0] < ((int64_t)1 << 46) && s[1] < ((int64_t)1 << 46);
+}
+
+// Bytes from the first to the last value of the rows (0 without rows), or
+// SIZE_MAX / 4 where they do not fit.
+static size_t rows_extent(int64_t n0, int64_t n1, const int64_t s[2], int64_t width, size_t esz) {
+  if (n0 == 0 || n1 == 0) return 0;
+  const double e = ((double)(n0 - 1) * (double)s[0] + (double)(n1 - 1) * (double)s[1] + (double)width) * (double)esz;
+  if (e > 4e18) return SIZE_MAX / 4;
+  return ((size_t)(n0 - 1) * (size_t)s[0] + (size_t)(n1 - 1) * (size_t)s[1] + (size_t)width) * esz;
+}
+
+static bool same_rows(int64_t n0, int64_t n1, const int64_t a[2], const int64_t b[2]) {
+  return (n0 <= 1 || a[0] == b[0]) && (n1 <= 1 || a[1] == b[1]);
+}
+
+// An output may be an input (same pointer and strides) or clear of it.
+static bool in_place_or_clear(int64_t n0, int64_t n1, const void *in, const int64_t si[2],
+                              const void *out, const int64_t so[2], int64_t width, size_t esz) {
+  if (in == out && same_rows(n0, n1, si, so)) return true;
+  return !overlaps(in, rows_extent(n0, n1, si, width, esz), out, rows_extent(n0, n1, so, width, esz));
+}
+
+static bool elem_aligned(const void *p, size_t esz) {
+  return reinterpret_cast<uintptr_t>(p) % esz == 0;
+}
+
+// Rows (i, j) as the kernels take them: one stride where two fold into one.
+static RowSet row_set(int64_t n0, int64_t n1, const int64_t s[2]) {
+  RowSet r;
+  r.n0 = n0; r.n1 = n1; r.s0 = s[0]; r.s1 = s[1];
+  if (n1 == 1) { r.n1 = n0; r.n0 = 1; r.s1 = s[0]; r.s0 = 0; }
+  else if (n0 > 1 && s[0] == n1 * s[1]) { r.n1 = n0 * n1; r.n0 = 1; r.s0 = 0; }
+  return r;
+}
+
+static bool ln_ok(const retnet_layernorm_desc *d) {
+  if (!d || d->d < 1 || d->d > (1 << 24)) return false;
+  if (d->dtype != RET_F32 && d->dtype != RET_BF16) return false;
+  if (!(d->eps >= 0.f) || isinf(d->eps)) return false;
+  return rowset_ok(d->n0, d->n1, d->sx) && rowset_ok(d->n0, d->n1, d->sg) &&
+         rowset_ok(d->n0, d->n1, d->so) && rows_countable(d->n0, d->n1) &&
+         strides_bounded(d->sx) && strides_bounded(d->sg) && strides_bounded(d->so);
+}
+
+static LnArgs ln_args(const retnet_layernorm_desc *d) {
+  LnArgs a;
+  a.sx = row_set(d->n0, d->n1, d->sx);
+  a.sg = row_set(d->n0, d->n1, d->sg);
+  a.so = row_set(d->n0, d->n1, d->so);
+  a.rows = d->n0 * d->n1;
+  a.d = d->d;
+  a.eps = d->eps;
+  return a;
+}
+
+ret_status retnet_layernorm_fwd(const retnet_layernorm_desc *d, const void *x, const float *w,
+                                const float *b, void *y, float *mean, float *rstd,
+                                ret_stream_t stream) {
+  RET_RANGE("retnet_layernorm_fwd");
+  if (!ln_ok(d) || !rows_disjoint(d->n0, d->n1, d->so, d->d)) return RET_EINVAL;
+  LnArgs a = ln_args(d);
+  if (a.rows == 0) return RET_OK;
+  const size_t esz = d->dtype == RET_BF16 ? 2 : 4;
+  if (!x || !y || !elem_aligned(x, esz) || !elem_aligned(y, esz)) return RET_EINVAL;
+  if (!in_place_or_clear(d->n0, d->n1, x, d->sx, y, d->so, d->d, esz)) return RET_EINVAL;
+  a.x = x; a.out = y; a.w = w; a.b = b; a.mean = mean; a.rstd = rstd;
+  cudaStream_t st = (cudaStream_t)stream;
+  RET_CUDA(RET_TIMED_LAUNCH(kKLnFwd, st, launch_layernorm_rows(a, d->dtype == RET_BF16, st)));
+  return RET_OK;
+}
+
+size_t retnet_layernorm_bwd_workspace_size(const retnet_layernorm_desc *d) {
+  if (!ln_ok(d)) return 0;
+  return align256(layernorm_bwd_bytes(d->n0 * d->n1, d->d)) + 256;
+}
+
+ret_status retnet_layernorm_bwd(const retnet_layernorm_desc *d, const void *x, const void *dy,
+                                const float *w, const float *mean, const float *rstd, void *dx,
+                                float *dw, float *db, void *ws, size_t ws_bytes,
+                                ret_stream_t stream) {
+  RET_RANGE("retnet_layernorm_bwd");
+  if (!ln_ok(d) || !rows_disjoint(d->n0, d->n1, d->so, d->d)) return RET_EINVAL;
+  ret_status rs = check_ws(ws, ws_bytes, retnet_layernorm_bwd_workspace_size(d));
+  if (rs != RET_OK) return rs;
+  LnArgs a = ln_args(d);
+  cudaStream_t st = (cudaStream_t)stream;
+  float *stat = at<float>(ws, 0), *part = stat + 2 * (size_t)a.rows;
+  const bool bf16 = d->dtype == RET_BF16, sums = dw || db;
+  int groups = 0;
+  if (a.rows > 0) {
+    const size_t esz = bf16 ? 2 : 4;
+    if (!x || !dy || !dx || !mean || !rstd || !elem_aligned(x, esz) || !elem_aligned(dy, esz) ||
+        !elem_aligned(dx, esz))
+      return RET_EINVAL;
+    if (!in_place_or_clear(d->n0, d->n1, x, d->sx, dx, d->so, d->d, esz) ||
+        !in_place_or_clear(d->n0, d->n1, dy, d->sg, dx, d->so, d->d, esz))
+      return RET_EINVAL;
+    a.x = x; a.dy = dy; a.out = dx; a.w = w;
+    a.mean = const_cast<float *>(mean);
+    a.rstd = const_cast<float *>(rstd);
+    const LnBwdPlan pl = layernorm_bwd_plan(a, bf16);
+    groups = pl.groups;
+    if (pl.two_pass)
+      RET_CUDA(RET_TIMED_LAUNCH(kKLnBwdStat, st, launch_layernorm_bwd_stat(a, bf16, pl, stat, st)));
+    RET_CUDA(RET_TIMED_LAUNCH(kKLnBwd, st, launch_layernorm_bwd(a, bf16, pl, stat, sums ? part : nullptr, st)));
+  }
+  if (sums)
+    RET_CUDA(RET_TIMED_LAUNCH(kKLnBwdSum, st, launch_layernorm_bwd_sum(part, groups, a.d, dw, db, st)));
+  return RET_OK;
+}
+
+static bool logits_ok(const retnet_logits_desc *d) {
+  if (!d || d->V < 1 || d->V > (1 << 30)) return false;
+  if (d->dtype != RET_F32 && d->dtype != RET_BF16) return false;
+  if (!finite_pos(d->temperature)) return false;
+  // 1 / T, log2(e) / T and T^2 have to be ordinary fp32 numbers
+  if (d->temperature < 1e-15 || d->temperature > 1e15) return false;
+  if (d->top < 0 || d->top > RETNET_MAX_TOP) return false;
+  if (d->id_bytes != 4 && d->id_bytes != 8) return false;
+  if (d->tail != 0 && d->tail != 1) return false;
+  return rowset_ok(d->n0, d->n1, d->sx) && rowset_ok(d->n0, d->n1, d->sd) &&
+         rows_countable(d->n0, d->n1) && strides_bounded(d->sx) && strides_bounded(d->sd);
+}
+
+static float scale_of(const retnet_logits_desc *d) {
+  return (float)(1.4426950408889634 / d->temperature);
+}
+
+ret_status retnet_token_logprobs(const retnet_logits_desc *d, const void *x, const void *tokens,
+                                 float *logprob, float *entropy, float *top_logprob,
+                                 int64_t *top_id, ret_stream_t stream) {
+  RET_RANGE("retnet_token_logprobs");
+  if (!logits_ok(d)) return RET_EINVAL;
+  LogprobArgs a;
+  a.rows = d->n0 * d->n1;
+  if (a.rows == 0) return RET_OK;
+  const size_t esz = d->dtype == RET_BF16 ? 2 : 4;
+  if (!x || !elem_aligned(x, esz) || (logprob && !tokens)) return RET_EINVAL;
+  if (tokens && !elem_aligned(tokens, (size_t)d->id_bytes)) return RET_EINVAL;
+  a.x = x;
+  a.sx = row_set(d->n0, d->n1, d->sx);
+  a.V = d->V;
+  a.top = top_logprob || top_id ? d->top : 0;
+  a.id64 = d->id_bytes == 8;
+  a.inv_t = (float)(1.0 / d->temperature);
+  a.scale = scale_of(d);
+  a.tokens = logprob ? tokens : nullptr;
+  a.logprob = logprob;
+  a.entropy = entropy;
+  a.top_logprob = top_logprob;
+  a.top_id = reinterpret_cast<long long *>(top_id);
+  cudaStream_t st = (cudaStream_t)stream;
+  RET_CUDA(RET_TIMED_LAUNCH(kKLogprobs, st, launch_token_logprobs(a, d->dtype == RET_BF16, st)));
+  return RET_OK;
+}
+
+static ret_status distill_impl(const retnet_logits_desc *d, const void *x, const void *ids,
+                               const float *values, const float *weight, float *loss, float *stats,
+                               void *dx, int what, ret_stream_t stream) {
+  if (!logits_ok(d) || d->top < 1) return RET_EINVAL;
+  const bool grad = (what & kDistillBwd) != 0;
+  if (grad && !rows_disjoint(d->n0, d->n1, d->sd, d->V)) return RET_EINVAL;
+  if (d->V > RETNET_MAX_DISTILL_V) return RET_EUNSUPPORTED;
+  DistillArgs a;
+  a.rows = d->n0 * d->n1;
+  if (a.rows == 0) return RET_OK;
+  const size_t esz = d->dtype == RET_BF16 ? 2 : 4;
+  if (!x || !ids || !values || !elem_aligned(x, esz) || !elem_aligned(ids, (size_t)d->id_bytes))
+    return RET_EINVAL;
+  if (grad && (!dx || !elem_aligned(dx, esz) ||
+               !in_place_or_clear(d->n0, d->n1, x, d->sx, dx, d->sd, d->V, esz)))
+    return RET_EINVAL;
+  if (what == kDistillBwd && !stats) return RET_EINVAL;
+  a.x = x;
+  a.dx = dx;
+  a.sx = row_set(d->n0, d->n1, d->sx);
+  a.sd = row_set(d->n0, d->n1, d->sd);
+  a.V = d->V;
+  a.top = d->top;
+  a.id64 = d->id_bytes == 8;
+  a.tail = d->tail;
+  a.inv_t = (float)(1.0 / d->temperature);
+  a.scale = scale_of(d);
+  a.t = (float)d->temperature;
+  a.ids = ids;
+  a.values = values;
+  a.weight = weight;
+  a.loss = loss;
+  a.stats = stats;
+  cudaStream_t st = (cudaStream_t)stream;
+  RET_CUDA(RET_TIMED_LAUNCH(kKDistill, st, launch_distill(a, d->dtype == RET_BF16, what, st)));
+  return RET_OK;
+}
+
+ret_status retnet_distill_fwd(const retnet_logits_desc *d, const void *x, const void *ids,
+                              const float *values, float *loss, float *stats,
+                              ret_stream_t stream) {
+  RET_RANGE("retnet_distill_fwd");
+  return distill_impl(d, x, ids, values, nullptr, loss, stats, nullptr, kDistillFwd, stream);
+}
+
+ret_status retnet_distill_bwd(const retnet_logits_desc *d, const void *x, const void *ids,
+                              const float *values, const float *weight, const float *stats,
+                              void *dx, ret_stream_t stream) {
+  RET_RANGE("retnet_distill_bwd");
+  return distill_impl(d, x, ids, values, weight, nullptr, const_cast<float *>(stats), dx,
+                      kDistillBwd, stream);
+}
+
+ret_status retnet_distill_step(const retnet_logits_desc *d, const void *x, const void *ids,
+                               const float *values, const float *weight, float *loss, float *stats,
+                               void *dx, ret_stream_t stream) {
+  RET_RANGE("retnet_distill_step");
+  return distill_impl(d, x, ids, values, weight, loss, stats, dx, kDistillStep, stream);
+}
+
 const char *retention_status_string(ret_status s) {
   switch (s) {
     case RET_OK: return "ok";

@@ -17,7 +17,9 @@ const char *kNames[kKernelCount] = {
     "gemm_simt", "chunk_tc", "gemm_tc", "state_pass", "swish_gate",
     "bwd_rows", "bwd_values", "unrotate",
     "layernorm", "residual_add", "gelu", "gemm_skinny", "skinny_reduce",
-    "state_combine", "state_simt", "bwd_prep", "bwd_finish", "parallel_tc"};
+    "state_combine", "state_simt", "bwd_prep", "bwd_finish", "parallel_tc",
+    "layernorm_fwd", "layernorm_bwd_stat", "layernorm_bwd", "layernorm_bwd_sum",
+    "token_logprobs", "distill"};
 
 struct Slot {
   std::vector<cudaEvent_t> start, stop;

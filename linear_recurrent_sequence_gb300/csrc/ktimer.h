@@ -31,6 +31,12 @@ enum KernelId {
   kKBwdPrep,
   kKBwdFinish,
   kKParallelTc,
+  kKLnFwd,
+  kKLnBwdStat,
+  kKLnBwd,
+  kKLnBwdSum,
+  kKLogprobs,
+  kKDistill,
   kKernelCount
 };
 

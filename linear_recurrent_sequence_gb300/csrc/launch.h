@@ -216,6 +216,71 @@ cudaError_t launch_layernorm(const void *x, const float *w, const float *b, void
 cudaError_t launch_residual_add(void *y, const void *r, long long n, cudaStream_t st);
 cudaError_t launch_gelu(void *y, long long n, cudaStream_t st);
 
+// Rows (i, j) of a strided matrix, i < n0, j < n1, numbered r = i n1 + j:
+// row r starts at element i s0 + j s1, its values are contiguous.
+struct RowSet {
+  long long n0 = 1, n1 = 0, s0 = 0, s1 = 0;
+};
+
+// layernorm.cu: LayerNorm and its gradients over `rows` rows of d values.
+// Forward: x -> out = y, mean and rstd written where not null.  Backward:
+// x, dy, mean, rstd -> out = dx and, per CTA, partial sums of dw and db
+// (part [groups][2][d], null = not wanted) that launch_layernorm_bwd_sum
+// adds.  A two-pass plan (rows too long for registers) first writes stat
+// [rows][2].  out may be x or dy themselves.
+struct LnArgs {
+  const void *x = nullptr, *dy = nullptr;
+  void *out = nullptr;
+  const float *w = nullptr, *b = nullptr;
+  float *mean = nullptr, *rstd = nullptr;
+  RowSet sx, sg, so;
+  long long rows = 0;
+  int d = 0;
+  float eps = 0.f;
+};
+struct LnBwdPlan {
+  bool vec = false, two_pass = false;
+  int nv = 1, threads = 0, groups = 0;
+};
+cudaError_t launch_layernorm_rows(const LnArgs &a, int bf16, cudaStream_t st);
+LnBwdPlan layernorm_bwd_plan(const LnArgs &a, int bf16);
+size_t layernorm_bwd_bytes(long long rows, int d);  // stat and part
+cudaError_t launch_layernorm_bwd_stat(const LnArgs &a, int bf16, const LnBwdPlan &pl, float *stat,
+                                      cudaStream_t st);
+cudaError_t launch_layernorm_bwd(const LnArgs &a, int bf16, const LnBwdPlan &pl, const float *stat,
+                                 float *part, cudaStream_t st);
+cudaError_t launch_layernorm_bwd_sum(const float *part, int groups, int d, float *dw, float *db,
+                                     cudaStream_t st);
+
+// logits.cu: one pass over each row of logits [rows][V] (bf16 or fp32).
+struct LogprobArgs {
+  const void *x = nullptr;
+  RowSet sx;
+  long long rows = 0;
+  int V = 0, top = 0, id64 = 1;
+  float inv_t = 1.f, scale = 1.f;  // 1 / temperature, log2(e) / temperature
+  const void *tokens = nullptr;    // [rows] int32 / int64, null = none
+  float *logprob = nullptr, *entropy = nullptr, *top_logprob = nullptr;
+  long long *top_id = nullptr;
+};
+cudaError_t launch_token_logprobs(const LogprobArgs &a, int bf16, cudaStream_t st);
+
+// distill.cu: the loss against a teacher's list and its gradient.
+enum { kDistillFwd = 1, kDistillBwd = 2, kDistillStep = 3 };
+struct DistillArgs {
+  const void *x = nullptr;
+  void *dx = nullptr;
+  RowSet sx, sd;
+  long long rows = 0;
+  int V = 0, top = 0, id64 = 1, tail = 0;
+  float inv_t = 1.f, scale = 1.f, t = 1.f;
+  const void *ids = nullptr;       // [rows][top]
+  const float *values = nullptr;   // [rows][top]
+  const float *weight = nullptr;   // [rows], null = 1
+  float *loss = nullptr, *stats = nullptr;  // [rows], [rows][2]
+};
+cudaError_t launch_distill(const DistillArgs &a, int bf16, int what, cudaStream_t st);
+
 // gemm_skinny.cu: C[M,N] = A[M,K] B[K,N] for M <= 16 rows (bf16 row-major,
 // fp32 accumulation), split over K into fp32 partials [split][M][N] that
 // launch_skinny_reduce adds in order into bf16 C.  Needs N % 8 == 0 and a

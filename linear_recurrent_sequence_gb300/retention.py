@@ -21,6 +21,9 @@ STATUS = {0: "RET_OK", 1: "RET_EINVAL", 2: "RET_EUNSUPPORTED", 3: "RET_EWORKSPAC
           4: "RET_ECUDA", 5: "RET_ETIMEOUT"}
 MAX_HEADS = 256
 
+MAX_TOP = 128
+
+_I64x2 = ctypes.c_int64 * 2
 _I64x3 = ctypes.c_int64 * 3
 
 
@@ -49,6 +52,19 @@ class BlockDesc(ctypes.Structure):
 
 class StackDesc(ctypes.Structure):
     _fields_ = [("block", BlockDesc), ("n_layers", ctypes.c_int)]
+
+
+class LayerNormDesc(ctypes.Structure):
+    _fields_ = [("n0", ctypes.c_int64), ("n1", ctypes.c_int64), ("d", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("eps", ctypes.c_float),
+                ("sx", _I64x2), ("sg", _I64x2), ("so", _I64x2)]
+
+
+class LogitsDesc(ctypes.Structure):
+    _fields_ = [("n0", ctypes.c_int64), ("n1", ctypes.c_int64), ("V", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("temperature", ctypes.c_double), ("top", ctypes.c_int),
+                ("id_bytes", ctypes.c_int), ("tail", ctypes.c_int),
+                ("sx", _I64x2), ("sd", _I64x2)]
 
 
 LAYER_KEYS = ("ln1_w", "ln1_b", "WQ", "WK", "WV", "WG", "WO", "ln2_w", "ln2_b", "W1", "W2")
@@ -102,6 +118,14 @@ _SIGS = {
                                           ctypes.POINTER(ctypes.c_void_p),
                                           ctypes.POINTER(ctypes.c_void_p), _P, _P,
                                           ctypes.c_size_t, _P]),
+    "retnet_layernorm_fwd": (ctypes.c_int, [ctypes.POINTER(LayerNormDesc)] + [_P] * 7),
+    "retnet_layernorm_bwd_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(LayerNormDesc)]),
+    "retnet_layernorm_bwd": (ctypes.c_int, [ctypes.POINTER(LayerNormDesc)] + [_P] * 9 +
+                             [ctypes.c_size_t, _P]),
+    "retnet_token_logprobs": (ctypes.c_int, [ctypes.POINTER(LogitsDesc)] + [_P] * 7),
+    "retnet_distill_fwd": (ctypes.c_int, [ctypes.POINTER(LogitsDesc)] + [_P] * 6),
+    "retnet_distill_bwd": (ctypes.c_int, [ctypes.POINTER(LogitsDesc)] + [_P] * 7),
+    "retnet_distill_step": (ctypes.c_int, [ctypes.POINTER(LogitsDesc)] + [_P] * 8),
     "retention_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "retention_last_cuda_error": (ctypes.c_int, []),
     "retention_poll_status": (ctypes.c_int, [_P, _P]),
@@ -518,6 +542,226 @@ def gemm_bf16(A, B, out=None, workspace=None, stream=None):
     _check(lib.retention_gemm_bf16(_ptr(A), _ptr(B), _ptr(out), M, N, K, _ptr(workspace),
                                    workspace.numel(), _stream(stream)), "retention_gemm_bf16")
     return out
+
+
+def _row_strides(name, lead, *tensors):
+    """(n0, n1) and each tensor's two element strides for rows along the last
+    dimension.  ``lead`` is their common shape without it; more than two
+    leading dimensions are folded where every tensor's strides allow it."""
+    for t in tensors:
+        if t.shape[:-1] != lead:
+            raise ValueError(f"{name}: leading shapes {tuple(lead)} and {tuple(t.shape[:-1])} differ")
+        if t.stride(-1) != 1 and t.shape[-1] > 1:
+            raise ValueError(f"{name}: the last dimension must be contiguous")
+    dims = [(n, [t.stride(i) for t in tensors]) for i, n in enumerate(lead) if n != 1]
+    if any(n == 0 for n in lead):
+        return 0, 0, [(0, 0)] * len(tensors)
+    i = 0
+    while len(dims) > 2 and i + 1 < len(dims):
+        (n0, s0), (n1, s1) = dims[i], dims[i + 1]
+        if all(a == n1 * b for a, b in zip(s0, s1)):
+            dims[i:i + 2] = [(n0 * n1, s1)]
+        else:
+            i += 1
+    if len(dims) > 2:
+        raise ValueError(f"{name}: rows of shape {tuple(lead)} do not fold into two strides")
+    dims = [(1, [0] * len(tensors))] * (2 - len(dims)) + dims
+    return dims[0][0], dims[1][0], list(zip(dims[0][1], dims[1][1]))
+
+
+def _f32(name, t, shape):
+    """Checks for a contiguous fp32 tensor of the given shape (None passes)."""
+    if t is not None and (t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous fp32 tensor of shape {tuple(shape)}")
+
+
+def _like(name, t, x):
+    """Checks a tensor given by the caller for x's shape and dtype."""
+    if t.shape != x.shape or t.dtype != x.dtype:
+        raise ValueError(f"{name} must have the shape {tuple(x.shape)} and dtype {x.dtype}")
+
+
+def _ptrs(*tensors):
+    """Device addresses as _ptr gives them (the current device asked for once)."""
+    dev = torch.cuda.current_device() if tensors[0].is_cuda else -1
+    return [None if t is None else t.data_ptr() if t.get_device() == dev >= 0 else _ptr(t)
+            for t in tensors]
+
+
+def _ln_desc(x, eps, dy, out):
+    n0, n1, st = _row_strides("layernorm", x.shape[:-1], x, out if dy is None else dy, out)
+    return LayerNormDesc(n0, n1, x.shape[-1], _dtype_code(x.dtype), eps, *st)
+
+
+def layernorm_fwd(x, w=None, b=None, *, eps=1e-5, out=None, mean=None, rstd=None, stream=None):
+    """LayerNorm over the last dimension of x (bf16 or fp32, any two row
+    strides): y = (x - mean) rstd w + b with fp32 gains w and biases b (None: 1
+    and 0).  Returns (y, mean, rstd); mean and rstd, fp32 of x.shape[:-1], are
+    what layernorm_bwd takes.  out may be x itself."""
+    lead, d = x.shape[:-1], x.shape[-1:]
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if mean is None:
+        mean = torch.empty(lead, dtype=torch.float32, device=x.device)
+    if rstd is None:
+        rstd = torch.empty(lead, dtype=torch.float32, device=x.device)
+    _like("out", out, x)
+    for name, t, shape in (("w", w, d), ("b", b, d), ("mean", mean, lead), ("rstd", rstd, lead)):
+        _f32(name, t, shape)
+    desc = _ln_desc(x, eps, None, out)
+    st = lib.retnet_layernorm_fwd(ctypes.byref(desc), *_ptrs(x, w, b, out, mean, rstd),
+                                  _stream(stream))
+    _check(st, "retnet_layernorm_fwd")
+    return out, mean, rstd
+
+
+def layernorm_bwd(x, dy, w, mean, rstd, *, dx=None, dw=None, db=None, workspace=None, stream=None):
+    """Gradients of layernorm_fwd: returns (dx, dw, db), dx in x's dtype, dw
+    and db fp32 (w may be None; dw and db are the sums all the same).  The sums
+    over the rows are added in a fixed order.  dx may be x or dy itself."""
+    lead, d = x.shape[:-1], x.shape[-1:]
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if dw is None:
+        dw = torch.empty(d, dtype=torch.float32, device=x.device)
+    if db is None:
+        db = torch.empty(d, dtype=torch.float32, device=x.device)
+    _like("dy", dy, x)
+    _like("dx", dx, x)
+    for name, t, shape in (("w", w, d), ("mean", mean, lead), ("rstd", rstd, lead), ("dw", dw, d),
+                           ("db", db, d)):
+        _f32(name, t, shape)
+    desc = _ln_desc(x, 0.0, dy, dx)
+    if workspace is None:
+        workspace = torch.empty(lib.retnet_layernorm_bwd_workspace_size(ctypes.byref(desc)),
+                                dtype=torch.uint8, device=x.device)
+    st = lib.retnet_layernorm_bwd(ctypes.byref(desc),
+                                  *_ptrs(x, dy, w, mean, rstd, dx, dw, db, workspace),
+                                  workspace.numel(), _stream(stream))
+    _check(st, "retnet_layernorm_bwd")
+    return dx, dw, db
+
+
+def _ids(name, t, shape):
+    """Bytes of an id of a contiguous int32 or int64 tensor of the given shape."""
+    if t.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"{name} must be int32 or int64, got {t.dtype}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}")
+    return t.element_size()
+
+
+def token_logprobs(logits, tokens=None, *, top=0, temperature=1.0, logprob=None, entropy=None,
+                   top_logprobs=None, top_ids=None, stream=None):
+    """Log probabilities under softmax(logits / temperature) over the last
+    dimension (bf16 or fp32, any two row strides): of the given tokens (int32 or
+    int64 of logits.shape[:-1]; negative = none, 0), the entropy, and the `top`
+    (<= MAX_TOP) largest with their ids, equal logits by the lower id.  Returns
+    (logprob, entropy, top_logprobs, top_ids); logprob is None without tokens
+    and the last two are None for top=0.  A logit of -inf is a masked token; the
+    missing alternatives of a row have id -1."""
+    lead, V, dev = logits.shape[:-1], logits.shape[-1], logits.device
+    id_bytes = 8
+    if tokens is not None:
+        id_bytes = _ids("tokens", tokens, lead)
+        if logprob is None:
+            logprob = torch.empty(lead, dtype=torch.float32, device=dev)
+    elif logprob is not None:
+        raise ValueError("logprob needs tokens")
+    if entropy is None:
+        entropy = torch.empty(lead, dtype=torch.float32, device=dev)
+    if top:
+        shape = (*lead, top)
+        if top_logprobs is None:
+            top_logprobs = torch.empty(shape, dtype=torch.float32, device=dev)
+        if top_ids is None:
+            top_ids = torch.empty(shape, dtype=torch.int64, device=dev)
+        if _ids("top_ids", top_ids, shape) != 8:
+            raise TypeError("top_ids must be int64")
+        _f32("top_logprobs", top_logprobs, shape)
+    else:
+        top_logprobs = top_ids = None
+    _f32("logprob", logprob, lead)
+    _f32("entropy", entropy, lead)
+    n0, n1, s = _row_strides("logits", lead, logits)
+    d = LogitsDesc(n0, n1, V, _dtype_code(logits.dtype), temperature, top, id_bytes, 0, s[0], s[0])
+    st = lib.retnet_token_logprobs(
+        ctypes.byref(d), *_ptrs(logits, tokens, logprob, entropy, top_logprobs, top_ids),
+        _stream(stream))
+    _check(st, "retnet_token_logprobs")
+    return logprob, entropy, top_logprobs, top_ids
+
+
+def _distill_desc(student, ids, values, temperature, tail, dstudent):
+    lead, top = student.shape[:-1], ids.shape[-1]
+    id_bytes = _ids("ids", ids, (*lead, top))
+    _f32("values", values, (*lead, top))
+    n0, n1, s = _row_strides("student", lead, student, student if dstudent is None else dstudent)
+    return LogitsDesc(n0, n1, student.shape[-1], _dtype_code(student.dtype), temperature, top,
+                      id_bytes, tail, s[0], s[1])
+
+
+def distill_fwd(student, ids, values, *, temperature=1.0, tail=False, loss=None, stats=None,
+                stream=None):
+    """Distillation loss of each row of the student's logits (bf16 or fp32,
+    any two row strides) against a teacher's list: ids (int32 or int64, negative
+    = absent) and values (fp32), both [.., k] with k <= MAX_TOP.  With tail
+    False the teacher is softmax(values / temperature) over the list; with tail
+    True the values are log probabilities over the whole vocabulary and the
+    tokens that are not listed form one more bucket.  Returns (loss, stats):
+    the loss times temperature^2, fp32 of student.shape[:-1], and what
+    distill_bwd needs, [.., 2]."""
+    lead = student.shape[:-1]
+    if loss is None:
+        loss = torch.empty(lead, dtype=torch.float32, device=student.device)
+    if stats is None:
+        stats = torch.empty((*lead, 2), dtype=torch.float32, device=student.device)
+    _f32("loss", loss, lead)
+    _f32("stats", stats, (*lead, 2))
+    d = _distill_desc(student, ids, values, temperature, tail, None)
+    st = lib.retnet_distill_fwd(ctypes.byref(d), *_ptrs(student, ids, values, loss, stats),
+                                _stream(stream))
+    _check(st, "retnet_distill_fwd")
+    return loss, stats
+
+
+def distill_bwd(student, ids, values, weight, stats, *, temperature=1.0, tail=False, dstudent=None,
+                stream=None):
+    """Gradient with respect to the student's logits, in their dtype: weight
+    (fp32, or None for 1) is the gradient of the caller's loss with respect to
+    each row's; rows of weight 0 get zeros.  dstudent may be student itself."""
+    lead = student.shape[:-1]
+    if dstudent is None:
+        dstudent = torch.empty(student.shape, dtype=student.dtype, device=student.device)
+    _like("dstudent", dstudent, student)
+    _f32("weight", weight, lead)
+    _f32("stats", stats, (*lead, 2))
+    d = _distill_desc(student, ids, values, temperature, tail, dstudent)
+    st = lib.retnet_distill_bwd(ctypes.byref(d),
+                                *_ptrs(student, ids, values, weight, stats, dstudent),
+                                _stream(stream))
+    _check(st, "retnet_distill_bwd")
+    return dstudent
+
+
+def distill_step(student, ids, values, weight=None, *, temperature=1.0, tail=False, loss=None,
+                 dstudent=None, stream=None):
+    """distill_fwd and distill_bwd in one call that reads the logits from
+    memory once: returns (loss, dstudent).  dstudent may be student itself."""
+    lead = student.shape[:-1]
+    if loss is None:
+        loss = torch.empty(lead, dtype=torch.float32, device=student.device)
+    if dstudent is None:
+        dstudent = torch.empty(student.shape, dtype=student.dtype, device=student.device)
+    _like("dstudent", dstudent, student)
+    _f32("weight", weight, lead)
+    _f32("loss", loss, lead)
+    d = _distill_desc(student, ids, values, temperature, tail, dstudent)
+    st = lib.retnet_distill_step(ctypes.byref(d),
+                                 *_ptrs(student, ids, values, weight, loss, None, dstudent),
+                                 _stream(stream))
+    _check(st, "retnet_distill_step")
+    return loss, dstudent
 
 
 def poll_status(workspace, stream=None):
