@@ -239,8 +239,8 @@ struct LnArgs {
   float eps = 0.f;
 };
 struct LnBwdPlan {
-  bool vec = false, two_pass = false;
-  int nv = 1, threads = 0, groups = 0;
+  bool vec = false, wide = false, two_pass = false;
+  int tpr = 0, threads = 0, groups = 0;  // threads a row, of a CTA; CTAs
 };
 cudaError_t launch_layernorm_rows(const LnArgs &a, int bf16, cudaStream_t st);
 LnBwdPlan layernorm_bwd_plan(const LnArgs &a, int bf16);

@@ -9,6 +9,7 @@
 // The variance is the mean square of the deviations, taken after the mean:
 // a row with a large level loses nothing to cancellation.
 #include <algorithm>
+#include <type_traits>
 
 #include "launch.h"
 #include "rows.cuh"
@@ -19,86 +20,306 @@ namespace {
 
 constexpr int kMaxWarps = 32;
 
-// Sums of N values over the threads that share a row: one warp, or the CTA
-// through red (one barrier; consecutive calls alternate between two
-// buffers, so a warp that is ahead cannot overwrite what another still reads).
-template <int N>
-__device__ __forceinline__ void row_sums(float (&x)[N], float (*red)[kMaxWarps], bool one_warp) {
+// Sums of N values over the `tpr` threads that share a row: a power of two up
+// to 32 lanes of a warp, or whole warps that exchange through red (consecutive
+// calls alternate between two buffers, so a warp that is ahead cannot
+// overwrite what another still reads).  They meet at the CTA's barrier, or
+// with kNamed (several row groups in a CTA) at named barrier 1 + group.  A
+// kernel with named barriers reserves all 16 of a CTA, and only four such
+// CTAs fit an SM.
+constexpr int kRed = 128;  // 8 places a row group, or one group's 32 warps
+
+template <int N, bool kNamed>
+__device__ __forceinline__ void row_sums(float (&x)[N], float (*red)[kRed], int tpr) {
+  if (tpr < 32) {
+    for (int s = tpr >> 1; s > 0; s >>= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], s);
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < N; ++i) x[i] = warp_sum(x[i]);
-  if (one_warp) return;
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  if (tpr == 32) return;
+  const int nw = tpr >> 5, lane = threadIdx.x & 31;
+  const int group = kNamed ? threadIdx.x / tpr : 0, w = (threadIdx.x - group * tpr) >> 5;
   if (lane == 0)
 #pragma unroll
-    for (int i = 0; i < N; ++i) red[i][w] = x[i];
-  __syncthreads();
+    for (int i = 0; i < N; ++i) red[i][group * 8 + w] = x[i];
+  if (kNamed)
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(tpr) : "memory");
+  else
+    __syncthreads();
+  if (nw <= 8) {  // (places without a warp hold 0)
 #pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = warp_sum(lane < nw ? red[i][lane] : 0.f);
+    for (int i = 0; i < N; ++i) {
+      const float4 p = *reinterpret_cast<const float4 *>(&red[i][group * 8]);
+      const float4 q = *reinterpret_cast<const float4 *>(&red[i][group * 8 + 4]);
+      x[i] = ((p.x + p.y) + (p.z + p.w)) + ((q.x + q.y) + (q.z + q.w));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = warp_sum(lane < nw ? red[i][lane] : 0.f);
+  }
 }
 
-// One row per CTA of up to 1024 threads, NV vectors of VEC values a thread,
-// the row in registers between the three uses of it.
-template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(1024)
-ln_fwd_kernel(const LnArgs a) {
-  __shared__ float red[2][1][kMaxWarps];
+// Zeros in the exchange buffers, before their first use.
+__device__ __forceinline__ void clear_red(float *red, int n) {
+  for (int i = threadIdx.x; i < n; i += blockDim.x) red[i] = 0.f;
+  __syncthreads();
+}
+
+// VEC fp32 parameters (16-byte aligned where VEC > 1), `other` where p is
+// null (kThere: it is known not to be).
+template <int VEC, bool kThere = false>
+__device__ __forceinline__ void load_param(const float *p, int c, float other, float (&f)[VEC]) {
+  if (!kThere && !p) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) f[j] = other;
+  } else if (VEC == 1) {
+    f[0] = p[c];
+  } else {
+#pragma unroll
+    for (int j = 0; j + 3 < VEC; j += 4) {
+      const float4 v = *reinterpret_cast<const float4 *>(p + c + j);
+      f[j] = v.x; f[j + 1] = v.y; f[j + 2] = v.z; f[j + 3] = v.w;
+    }
+  }
+}
+
+// VEC values at a time as packed pairs (or one value).
+template <int VEC>
+struct Pairs {
+  static constexpr int N = VEC > 1 ? VEC / 2 : 1;
+  float2 v[N];
+  __device__ __forceinline__ Pairs() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = make_float2(0.f, 0.f);
+  }
+  __device__ __forceinline__ explicit Pairs(const float (&f)[VEC]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = make_float2(f[VEC > 1 ? 2 * i : 0], VEC > 1 ? f[VEC > 1 ? 2 * i + 1 : 0] : 0.f);
+  }
+  __device__ __forceinline__ void put(float (&f)[VEC]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      f[VEC > 1 ? 2 * i : 0] = v[i].x;
+      if (VEC > 1) f[VEC > 1 ? 2 * i + 1 : 0] = v[i].y;
+    }
+  }
+};
+
+template <int VEC>
+__device__ __forceinline__ float2 padd(float2 a, float2 b) {
+  return VEC > 1 ? tc::add2(a, b) : make_float2(__fadd_rn(a.x, b.x), 0.f);
+}
+template <int VEC>
+__device__ __forceinline__ float2 pmul(float2 a, float2 b) {
+  return VEC > 1 ? tc::mul2(a, b) : make_float2(__fmul_rn(a.x, b.x), 0.f);
+}
+template <int VEC>
+__device__ __forceinline__ float2 pfma(float2 a, float2 b, float2 c) {
+  return VEC > 1 ? tc::fma2(a, b, c) : make_float2(fmaf(a.x, b.x, c.x), 0.f);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// A thread's own vectors of the rows ahead, on their way through shared
+// memory by asynchronous copies: slots [stage][vector][thread].  Only the
+// thread that copied a vector reads it, so no barrier is needed.  A vector
+// past the row's end, or of a row past the last one, arrives as zeros.
+// bf16 rows off the 16-byte boundary have no copies of 2 bytes: their values
+// are loaded straight into registers (kCopies false).
+template <typename T, int VEC, int kVectors, int kStages>
+struct RowRing {
+  static constexpr bool kCopies = VEC > 1 || sizeof(T) == 4;
+  static constexpr int kBytes = VEC * (int)sizeof(T);
+  uint8_t *slot;  // of this thread in stage 0, vector 0
+  int pitch;      // bytes of all threads' slots of one vector
+  T direct[kCopies ? 1 : kVectors];
+  __device__ __forceinline__ RowRing(uint8_t *dyn)
+      : slot(dyn + threadIdx.x * kBytes), pitch((int)blockDim.x * kBytes) {}
+  __device__ __forceinline__ void copy(int stage, int v, const T *p, bool in) {
+    const uint32_t dst = tc::smem_u32(slot + (stage * kVectors + v) * pitch);
+    const int n = in ? kBytes : 0;
+    if (kBytes == 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(p), "r"(n) : "memory");
+    else if (kCopies)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(p), "r"(n) : "memory");
+  }
+  __device__ __forceinline__ void load(int v, const T *p, bool in) {
+    if (!kCopies) direct[kCopies ? 0 : v] = in ? *p : T(0.f);
+  }
+  __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  // The oldest of the kStages groups committed last has arrived.
+  __device__ __forceinline__ void wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+  }
+  __device__ __forceinline__ Pairs<VEC> get(int stage, int v) const {
+    float f[VEC];
+    Elems<T, VEC> e;
+    if (kCopies)
+      e = *reinterpret_cast<const Elems<T, VEC> *>(slot + (stage * kVectors + v) * pitch);
+    else
+      *reinterpret_cast<T *>(&e) = direct[kCopies ? 0 : v];
+    e.get(f);
+    return Pairs<VEC>(f);
+  }
+};
+
+// Offsets of row r and its successors; r moves on in equal steps.
+struct RowCursor {
+  RowSet s;
+  long long r, off;
+  __device__ __forceinline__ RowCursor(const RowSet &set, long long first)
+      : s(set), r(first), off(row_offset(set, first)) {}
+  __device__ __forceinline__ void advance(long long step) {
+    r += step;
+    off = s.n0 == 1 ? off + step * s.s1 : row_offset(s, r);
+  }
+  __device__ __forceinline__ long long at(int k) const {
+    return k == 0 ? off : s.n0 == 1 ? off + k * s.s1 : row_offset(s, r + k);
+  }
+};
+
+// VEC values from packed pairs to the row.
+template <typename T, int VEC>
+__device__ __forceinline__ void store_pairs(const Pairs<VEC> &p, T *o) {
+  float f[VEC];
+  p.put(f);
+  Elems<T, VEC> e;
+  e.set(f);
+  e.store(o);
+}
+
+template <int VEC>
+__device__ __forceinline__ Pairs<VEC> param_pairs(const float *p, int c, float other) {
+  float f[VEC];
+  load_param<VEC>(p, c, other, f);
+  return Pairs<VEC>(f);
+}
+
+// R rows at a time by tpr threads (blockDim / tpr such groups in a CTA), NV
+// vectors of VEC values a thread and row.  The rows are read from their ring
+// slots once and stay in registers between the three uses of them, while the
+// next kStages - 1 sets of rows are on their way: loads are in flight all the
+// time.  kKeep: the gains and biases of the thread's columns stay in registers
+// (from L1 they would be four times the row's own traffic).
+template <typename T, int VEC, int NV, int R, int kStages, bool kKeep, int kThreads>
+__global__ void __launch_bounds__(kThreads)
+ln_fwd_kernel(const LnArgs a, int tpr) {
+  extern __shared__ __align__(16) uint8_t dyn[];
+  __shared__ __align__(16) float red[2][R][kRed];
   pdl_launch_dependents();
   pdl_wait();
-  const bool one_warp = blockDim.x == 32;
-  const int step = blockDim.x * VEC, t0 = threadIdx.x * VEC;
+  if (tpr > 32) clear_red(&red[0][0][0], 2 * R * kRed);
+  constexpr int NP = Pairs<VEC>::N;
+  const int t = threadIdx.x % tpr, group = threadIdx.x / tpr, groups = blockDim.x / tpr;
+  const int step = tpr * VEC, t0 = t * VEC;
   const float inv_d = 1.f / (float)a.d;
-  for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
-    const T *x = reinterpret_cast<const T *>(a.x) + row_offset(a.sx, r);
-    T *y = reinterpret_cast<T *>(a.out) + row_offset(a.so, r);
-    float v[NV][VEC];
-    float s[1] = {0.f};
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = t0 + i * step;
-      if (c < a.d) {
-        Elems<T, VEC> e;
-        e.load(x + c);
-        e.get(v[i]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) v[i][j] = 0.f;
-      }
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) s[0] += v[i][j];
-    }
-    row_sums<1>(s, red[0], one_warp);
-    const float mean = s[0] * inv_d;
-    float q[1] = {0.f};
+  float2 wk[kKeep ? NV : 1][NP], bk[kKeep ? NV : 1][NP];
+  if (kKeep)
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (t0 + i * step < a.d)
+      if (t0 + i * step < a.d) {
+        const Pairs<VEC> w = param_pairs<VEC>(a.w, t0 + i * step, 1.f);
+        const Pairs<VEC> b = param_pairs<VEC>(a.b, t0 + i * step, 0.f);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          v[i][j] -= mean;
-          q[0] = fmaf(v[i][j], v[i][j], q[0]);
+        for (int j = 0; j < NP; ++j) {
+          wk[kKeep ? i : 0][j] = w.v[j];
+          bk[kKeep ? i : 0][j] = b.v[j];
         }
-    row_sums<1>(q, red[1], one_warp);
-    const float rstd = rsqrtf(fmaf(q[0], inv_d, a.eps));
-    if (threadIdx.x == 0) {
-      if (a.mean) a.mean[r] = mean;
-      if (a.rstd) a.rstd[r] = rstd;
-    }
+      }
+  using Ring = RowRing<T, VEC, R * NV, kStages>;
+  Ring ring(dyn);
+  const long long first = ((long long)blockIdx.x * groups + group) * R;
+  const long long stride = (long long)gridDim.x * groups * R;
+  const T *x = reinterpret_cast<const T *>(a.x) + t0;
+  T *y = reinterpret_cast<T *>(a.out) + t0;
+  RowCursor cx(a.sx, first), cy(a.so, first);
+  // Copies (or loads) the rows at the cursor and moves it on.
+  auto ahead = [&](int stage) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = t0 + i * step;
-      if (c < a.d) {
-        float o[VEC];
+    for (int k = 0; k < R; ++k) {
+      const bool row = cx.r + k < a.rows;
+      const T *p = row ? x + cx.at(k) : x;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float h = v[i][j] * rstd;
-          const float g = a.w ? a.w[c + j] : 1.f;
-          o[j] = a.b ? fmaf(h, g, a.b[c + j]) : h * g;
-        }
-        Elems<T, VEC> e;
-        e.set(o);
-        e.store(y + c);
+      for (int i = 0; i < NV; ++i) {
+        const bool in = row && t0 + i * step < a.d;
+        if (Ring::kCopies)
+          ring.copy(stage, k * NV + i, in ? p + i * step : reinterpret_cast<const T *>(a.x), in);
+        else
+          ring.load(k * NV + i, p + i * step, in);
       }
     }
+    if (Ring::kCopies) ring.commit();
+    cx.advance(stride);
+  };
+  if (Ring::kCopies)
+    for (int k = 0; k < kStages - 1; ++k) ahead(k);
+  int stage = 0;
+  // Every thread of a warp takes part in each row's sums; past the last row
+  // it works on zeros and writes nothing.
+  for (long long r = first; r - group * R < a.rows; r += stride) {
+    // the slot that the previous turn read takes the rows furthest ahead
+    ahead(stage == 0 ? kStages - 1 : stage - 1);
+    if (Ring::kCopies) ring.wait();
+    float2 v[R][NV][NP];
+    float s[R], q[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      float2 s2 = both(0.f);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const Pairs<VEC> p = ring.get(stage, k * NV + i);
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+          v[k][i][j] = p.v[j];
+          s2 = padd<VEC>(s2, p.v[j]);
+        }
+      }
+      s[k] = s2.x + s2.y;
+    }
+    row_sums<R, false>(s, red[0], tpr);
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      s[k] *= inv_d;
+      float2 s2 = both(0.f);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const float2 nm = both(t0 + i * step < a.d ? -s[k] : 0.f);  // zeros past the end stay zeros
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+          v[k][i][j] = padd<VEC>(v[k][i][j], nm);
+          s2 = pfma<VEC>(v[k][i][j], v[k][i][j], s2);
+        }
+      }
+      q[k] = s2.x + s2.y;
+    }
+    row_sums<R, false>(q, red[1], tpr);
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const bool live = r + k < a.rows;
+      const float rstd = rsqrtf(fmaf(q[k], inv_d, a.eps));
+      if (t == 0 && live) {
+        if (a.mean) a.mean[r + k] = s[k];
+        if (a.rstd) a.rstd[r + k] = rstd;
+      }
+      const float2 rr = both(rstd);
+      T *o = y + cy.at(k);
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (t0 + i * step < a.d && live) {
+          const Pairs<VEC> w = kKeep ? Pairs<VEC>() : param_pairs<VEC>(a.w, t0 + i * step, 1.f);
+          const Pairs<VEC> b = kKeep ? Pairs<VEC>() : param_pairs<VEC>(a.b, t0 + i * step, 0.f);
+          Pairs<VEC> n;
+#pragma unroll
+          for (int j = 0; j < NP; ++j)
+            n.v[j] = pfma<VEC>(pmul<VEC>(v[k][i][j], rr), kKeep ? wk[kKeep ? i : 0][j] : w.v[j],
+                               kKeep ? bk[kKeep ? i : 0][j] : b.v[j]);
+          store_pairs<T, VEC>(n, o + i * step);
+        }
+    }
+    cy.advance(stride);
+    stage = stage + 1 == kStages ? 0 : stage + 1;
   }
 }
 
@@ -107,9 +328,10 @@ ln_fwd_kernel(const LnArgs a) {
 template <typename T, int VEC>
 __global__ void __launch_bounds__(1024)
 ln_fwd_long_kernel(const LnArgs a) {
-  __shared__ float red[2][1][kMaxWarps];
+  __shared__ float red[2][1][kRed];
   pdl_launch_dependents();
   pdl_wait();
+  clear_red(&red[0][0][0], 2 * kRed);
   const int step = blockDim.x * VEC, t0 = threadIdx.x * VEC;
   const float inv_d = 1.f / (float)a.d;
   for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
@@ -124,7 +346,7 @@ ln_fwd_long_kernel(const LnArgs a) {
 #pragma unroll
       for (int j = 0; j < VEC; ++j) s[0] += v[j];
     }
-    row_sums<1>(s, red[0], false);
+    row_sums<1, false>(s, red[0], blockDim.x);
     const float mean = s[0] * inv_d;
     for (int c = t0; c < a.d; c += step) {
       e.load(x + c);
@@ -132,7 +354,7 @@ ln_fwd_long_kernel(const LnArgs a) {
 #pragma unroll
       for (int j = 0; j < VEC; ++j) q[0] = fmaf(v[j] - mean, v[j] - mean, q[0]);
     }
-    row_sums<1>(q, red[1], false);
+    row_sums<1, false>(q, red[1], blockDim.x);
     const float rstd = rsqrtf(fmaf(q[0], inv_d, a.eps));
     if (threadIdx.x == 0) {
       if (a.mean) a.mean[r] = mean;
@@ -141,88 +363,184 @@ ln_fwd_long_kernel(const LnArgs a) {
     for (int c = t0; c < a.d; c += step) {
       e.load(x + c);
       e.get(v);
+      float w[VEC], b[VEC];
+      load_param<VEC>(a.w, c, 1.f, w);
+      load_param<VEC>(a.b, c, 0.f, b);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float h = (v[j] - mean) * rstd;
-        const float g = a.w ? a.w[c + j] : 1.f;
-        v[j] = a.b ? fmaf(h, g, a.b[c + j]) : h * g;
-      }
+      for (int j = 0; j < VEC; ++j) v[j] = fmaf((v[j] - mean) * rstd, w[j], b[j]);
       e.set(v);
       e.store(y + c);
     }
   }
 }
 
-// dx of the CTA's rows, and the sums of dy h and dy over them: each thread
-// keeps the sums of its own NV x VEC columns in registers and writes them to
-// part[blockIdx][2][d] once at the end.
-template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(1024)
-ln_bwd_kernel(const LnArgs a, float *__restrict__ part) {
-  __shared__ float red[2][2][kMaxWarps];
+// dx of the CTA's rows, and the sums of dy h and dy over them: R rows at a
+// time by tpr threads, blockDim / tpr such groups in a CTA.  Each thread keeps
+// the sums of its own NV x VEC columns in registers for the whole call; the
+// rows come through the ring and are read from it twice, before and after
+// the rows' sums.  kKeep: so do the gains of the thread's columns.
+template <typename T, int VEC, int NV, int R, int kStages, bool kKeep, int kThreads>
+__global__ void __launch_bounds__(kThreads)
+ln_bwd_kernel(const LnArgs a, int tpr, float *__restrict__ part) {
+  extern __shared__ __align__(16) uint8_t dyn[];  // ring, then the CTA's sums
+  __shared__ __align__(16) float red[2][2 * R][kRed];
   pdl_launch_dependents();
   pdl_wait();
-  const bool one_warp = blockDim.x == 32;
-  const int step = blockDim.x * VEC, t0 = threadIdx.x * VEC;
+  if (tpr > 32) clear_red(&red[0][0][0], 4 * R * kRed);
+  constexpr int NP = Pairs<VEC>::N;
+  const int t = threadIdx.x % tpr, group = threadIdx.x / tpr, groups = blockDim.x / tpr;
+  const int step = tpr * VEC, t0 = t * VEC;
   const float inv_d = 1.f / (float)a.d;
-  float aw[NV][VEC], ab[NV][VEC];
+  float2 aw[NV][NP], ab[NV][NP], wk[kKeep ? NV : 1][NP];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) aw[i][j] = ab[i][j] = 0.f;
-  int par = 0;
-  for (long long r = blockIdx.x; r < a.rows; r += gridDim.x, par ^= 1) {
-    const T *x = reinterpret_cast<const T *>(a.x) + row_offset(a.sx, r);
-    const T *dy = reinterpret_cast<const T *>(a.dy) + row_offset(a.sg, r);
-    T *dx = reinterpret_cast<T *>(a.out) + row_offset(a.so, r);
-    const float mean = a.mean[r], rstd = a.rstd[r];
-    float h[NV][VEC], g[NV][VEC];
-    float s[2] = {0.f, 0.f};
+    for (int j = 0; j < NP; ++j) aw[i][j] = ab[i][j] = both(0.f);
+  if (kKeep)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = t0 + i * step;
-      if (c < a.d) {
-        Elems<T, VEC> ex, eg;
-        ex.load(x + c);
-        eg.load(dy + c);
-        ex.get(h[i]);
-        eg.get(g[i]);
+      Pairs<VEC> w;
+      if (t0 + i * step < a.d) w = param_pairs<VEC>(a.w, t0 + i * step, 1.f);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          h[i][j] = (h[i][j] - mean) * rstd;
-          aw[i][j] = fmaf(g[i][j], h[i][j], aw[i][j]);
-          ab[i][j] += g[i][j];
-          if (a.w) g[i][j] *= a.w[c + j];
-          s[0] += g[i][j];
-          s[1] = fmaf(g[i][j], h[i][j], s[1]);
+      for (int j = 0; j < NP; ++j) wk[kKeep ? i : 0][j] = w.v[j];
+    }
+  using Ring = RowRing<T, VEC, 2 * R * NV, kStages>;
+  Ring ring(dyn);
+  const long long first = ((long long)blockIdx.x * groups + group) * R;
+  const long long stride = (long long)gridDim.x * groups * R;
+  const T *x = reinterpret_cast<const T *>(a.x) + t0, *dy = reinterpret_cast<const T *>(a.dy) + t0;
+  T *dx = reinterpret_cast<T *>(a.out) + t0;
+  RowCursor cx(a.sx, first), cg(a.sg, first), co(a.so, first);
+  auto ahead = [&](int stage) {
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const bool row = cx.r + k < a.rows;
+      const T *p = row ? x + cx.at(k) : x, *g = row ? dy + cg.at(k) : dy;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const bool in = row && t0 + i * step < a.d;
+        if (Ring::kCopies) {
+          ring.copy(stage, 2 * (k * NV + i), in ? p + i * step : reinterpret_cast<const T *>(a.x), in);
+          ring.copy(stage, 2 * (k * NV + i) + 1, in ? g + i * step : reinterpret_cast<const T *>(a.dy), in);
+        } else {
+          ring.load(2 * (k * NV + i), p + i * step, in);
+          ring.load(2 * (k * NV + i) + 1, g + i * step, in);
         }
       }
     }
-    row_sums<2>(s, red[par], one_warp);
-    const float c1 = s[0] * inv_d, c2 = s[1] * inv_d;
+    if (Ring::kCopies) ring.commit();
+    cx.advance(stride);
+    cg.advance(stride);
+  };
+  if (Ring::kCopies)
+    for (int k = 0; k < kStages - 1; ++k) ahead(k);
+  float mean_n[R], rstd_n[R];  // of the next rows
+  auto stats = [&](long long r) {
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      mean_n[k] = r + k < a.rows ? a.mean[r + k] : 0.f;
+      rstd_n[k] = r + k < a.rows ? a.rstd[r + k] : 0.f;
+    }
+  };
+  stats(first);
+  int par = 0, stage = 0;
+  // As in the forward, threads past the last row work on zeros.
+  for (long long r = first; r - group * R < a.rows; r += stride, par ^= 1) {
+    float2 nm[R], rr[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      nm[k] = both(-mean_n[k]);
+      rr[k] = both(rstd_n[k]);
+    }
+    stats(r + stride);
+    // the slot that the previous turn read takes the rows furthest ahead
+    ahead(stage == 0 ? kStages - 1 : stage - 1);
+    if (Ring::kCopies) ring.wait();
+    float s[2 * R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      float2 s0 = both(0.f), s1 = both(0.f);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const Pairs<VEC> px = ring.get(stage, 2 * (k * NV + i)), g = ring.get(stage, 2 * (k * NV + i) + 1);
+        Pairs<VEC> w;
+        if (!kKeep && t0 + i * step < a.d) w = param_pairs<VEC>(a.w, t0 + i * step, 1.f);
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+          const float2 h = pmul<VEC>(padd<VEC>(px.v[j], nm[k]), rr[k]);
+          aw[i][j] = pfma<VEC>(g.v[j], h, aw[i][j]);
+          ab[i][j] = padd<VEC>(ab[i][j], g.v[j]);
+          const float2 gw = pmul<VEC>(g.v[j], kKeep ? wk[kKeep ? i : 0][j] : w.v[j]);
+          s0 = padd<VEC>(s0, gw);
+          s1 = pfma<VEC>(gw, h, s1);
+        }
+      }
+      s[2 * k] = s0.x + s0.y;
+      s[2 * k + 1] = s1.x + s1.y;
+    }
+    row_sums<2 * R, true>(s, red[par], tpr);
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      // dx = rstd (g - c1 - h c2)
+      const float2 c1 = both(-s[2 * k] * inv_d), c2 = both(-s[2 * k + 1] * inv_d);
+      const bool live = r + k < a.rows;
+      T *o = dx + co.at(k);
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (t0 + i * step < a.d && live) {
+          const Pairs<VEC> px = ring.get(stage, 2 * (k * NV + i));
+          const Pairs<VEC> w = kKeep ? Pairs<VEC>() : param_pairs<VEC>(a.w, t0 + i * step, 1.f);
+          Pairs<VEC> g = ring.get(stage, 2 * (k * NV + i) + 1);
+#pragma unroll
+          for (int j = 0; j < NP; ++j) {
+            const float2 h = pmul<VEC>(padd<VEC>(px.v[j], nm[k]), rr[k]);
+            const float2 gw = pmul<VEC>(g.v[j], kKeep ? wk[kKeep ? i : 0][j] : w.v[j]);
+            g.v[j] = pmul<VEC>(rr[k], padd<VEC>(gw, pfma<VEC>(h, c2, c1)));
+          }
+          store_pairs<T, VEC>(g, o + i * step);
+        }
+    }
+    co.advance(stride);
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+  }
+  if (!part) return;
+  // The sums of each warp (rows of fewer than 32 threads) or row group go to
+  // shared memory; the CTA adds them in order.
+  for (int k = tpr; k < 32; k <<= 1)
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        aw[i][j].x += __shfl_xor_sync(0xffffffffu, aw[i][j].x, k);
+        ab[i][j].x += __shfl_xor_sync(0xffffffffu, ab[i][j].x, k);
+        aw[i][j].y += __shfl_xor_sync(0xffffffffu, aw[i][j].y, k);
+        ab[i][j].y += __shfl_xor_sync(0xffffffffu, ab[i][j].y, k);
+      }
+  const int unit_threads = tpr < 32 ? 32 : tpr, units = blockDim.x / unit_threads;
+  float *out = part + (size_t)blockIdx.x * 2 * a.d, *sums = reinterpret_cast<float *>(dyn);
+  float *mine = units > 1 ? sums + (size_t)(threadIdx.x / unit_threads) * 2 * a.d : out;
+  __syncthreads();  // every copy to the ring has been read
+  if (tpr >= 32 || (int)(threadIdx.x & 31) < tpr)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = t0 + i * step;
-      if (c < a.d) {
+      if (c < a.d)
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) g[i][j] = rstd * (g[i][j] - fmaf(h[i][j], c2, c1));
-        Elems<T, VEC> e;
-        e.set(g[i]);
-        e.store(dx + c);
-      }
+        for (int j = 0; j < NP; ++j) {
+          mine[c + 2 * j] = aw[i][j].x;
+          mine[a.d + c + 2 * j] = ab[i][j].x;
+          if (VEC > 1) {
+            mine[c + 2 * j + 1] = aw[i][j].y;
+            mine[a.d + c + 2 * j + 1] = ab[i][j].y;
+          }
+        }
     }
-  }
-  if (!part) return;
-  float *pw = part + (size_t)blockIdx.x * 2 * a.d, *pb = pw + a.d;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = t0 + i * step;
-    if (c < a.d)
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        pw[c + j] = aw[i][j];
-        pb[c + j] = ab[i][j];
-      }
+  if (units == 1) return;
+  __syncthreads();
+  for (int c = threadIdx.x; c < 2 * a.d; c += blockDim.x) {
+    float v = sums[c];
+    for (int k = 1; k < units; ++k) v += sums[(size_t)k * 2 * a.d + c];
+    out[c] = v;
   }
 }
 
@@ -232,9 +550,10 @@ ln_bwd_kernel(const LnArgs a, float *__restrict__ part) {
 template <typename T, int VEC>
 __global__ void __launch_bounds__(1024)
 ln_bwd_stat_kernel(const LnArgs a, float *__restrict__ stat) {
-  __shared__ float red[2][2][kMaxWarps];
+  __shared__ float red[2][2][kRed];
   pdl_launch_dependents();
   pdl_wait();
+  clear_red(&red[0][0][0], 4 * kRed);
   int par = 0;
   for (long long r = blockIdx.x; r < a.rows; r += gridDim.x, par ^= 1) {
     const T *x = reinterpret_cast<const T *>(a.x) + row_offset(a.sx, r);
@@ -248,14 +567,16 @@ ln_bwd_stat_kernel(const LnArgs a, float *__restrict__ stat) {
       float h[VEC], g[VEC];
       ex.get(h);
       eg.get(g);
+      float w[VEC];
+      load_param<VEC>(a.w, c, 1.f, w);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        if (a.w) g[j] *= a.w[c + j];
+        g[j] *= w[j];
         s[0] += g[j];
         s[1] = fmaf(g[j], (h[j] - mean) * rstd, s[1]);
       }
     }
-    row_sums<2>(s, red[par], false);
+    row_sums<2, false>(s, red[par], blockDim.x);
     if (threadIdx.x < 2) stat[2 * r + threadIdx.x] = s[threadIdx.x] / (float)a.d;
   }
 }
@@ -269,10 +590,8 @@ ln_bwd_cols_kernel(const LnArgs a, const float *__restrict__ stat, float *__rest
   if (c >= a.d) return;
   float aw[VEC], ab[VEC], w[VEC];
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) {
-    aw[j] = ab[j] = 0.f;
-    w[j] = a.w ? a.w[c + j] : 1.f;
-  }
+  for (int j = 0; j < VEC; ++j) aw[j] = ab[j] = 0.f;
+  load_param<VEC>(a.w, c, 1.f, w);
   for (long long r = blockIdx.y; r < a.rows; r += gridDim.y) {
     const float mean = a.mean[r], rstd = a.rstd[r], c1 = stat[2 * r], c2 = stat[2 * r + 1];
     Elems<T, VEC> ex, eg;
@@ -335,34 +654,63 @@ bool rows_aligned(const void *p, const RowSet &s, int esz) {
          (s.n0 == 1 || s.s0 * esz % 16 == 0);
 }
 
-int threads_for(int d, int per_thread, int most) {
-  const int t = (d + per_thread - 1) / per_thread;
-  const int r = (t + 31) / 32 * 32;
-  return r > most ? most : r;
+bool param_aligned(const float *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// Threads a row for n vectors with at most `most` a thread: lanes of a warp
+// (a power of two) or whole warps.
+int threads_per_row(int n, int most) {
+  const int t = (n + most - 1) / most;
+  if (t > 16) return (t + 31) / 32 * 32;
+  int p = 1;
+  while (p < t) p *= 2;
+  return p;
 }
 
-template <typename T, int VEC, int NV>
-cudaError_t fwd(const LnArgs &a, cudaStream_t st) {
-  const long long cap = 1LL << 30;
-  return launch_k(ln_fwd_kernel<T, VEC, NV>, dim3((unsigned)(a.rows < cap ? a.rows : cap)),
-                  dim3(threads_for(a.d, VEC * NV, 1024)), 0, st, true, a);
+template <typename Kern, typename... Args>
+cudaError_t launch_with(Kern kern, int grid, int threads, size_t smem, cudaStream_t st, Args... args) {
+  if (smem > 32 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_k(kern, dim3(grid), dim3(threads), smem, st, true, args...);
+}
+
+template <typename T, int VEC, int NV, int R, int kStages, bool kKeep, int kThreads>
+cudaError_t fwd(const LnArgs &a, int tpr, int per_sm, cudaStream_t st) {
+  const int threads = tpr > 32 ? tpr : 128, rows = threads / tpr * R;
+  const size_t smem = RowRing<T, VEC, 1, 1>::kCopies ? (size_t)kStages * R * NV * threads * VEC * sizeof(T) : 0;
+  // CTAs that stay for the whole call, per_sm threads an SM, less where the
+  // rings fill its shared memory.
+  const long long fit = std::max<long long>(1, std::min<long long>(per_sm / threads, smem ? 220 * 1024 / (smem + 1024) : 32));
+  const long long want = (a.rows + rows - 1) / rows, most = sm_count() * fit;
+  return launch_with(ln_fwd_kernel<T, VEC, NV, R, kStages, kKeep, kThreads>,
+                     (int)std::min(want, most), threads, smem, st, a, tpr);
 }
 
 template <typename T, int VEC>
 cudaError_t fwd_any(const LnArgs &a, cudaStream_t st) {
-  if (a.d <= 512 * VEC) return fwd<T, VEC, 1>(a, st);
-  if (a.d <= 2048 * VEC) return fwd<T, VEC, 4>(a, st);
+  const int n = (a.d + VEC - 1) / VEC;
+  const int t8 = threads_per_row(n, 8 / VEC), t16 = threads_per_row(n, 16 / VEC);
+  // 8 values a thread while that leaves the SMs with at most 1024 threads each,
+  // else two rows of 16; above 8192 values a row one row of 16 or 32.
+  if (t8 <= 1024 && a.rows * t8 <= (long long)sm_count() * 1024)
+    return fwd<T, VEC, 8 / VEC, 1, 2, false, 1024>(a, t8, 1024, st);
+  if (t16 <= 512) return fwd<T, VEC, 16 / VEC, 2, sizeof(T) == 4 ? 2 : 3, true, 512>(a, t16, 512, st);
+  if (t16 <= 1024) return fwd<T, VEC, 16 / VEC, 1, 3, false, 1024>(a, t16, 1024, st);
+  if constexpr (VEC == 8)
+    if (t16 <= 2048) return fwd<T, 8, 4, 1, 2, false, 1024>(a, threads_per_row(n, 4), 1024, st);
   const long long cap = 1LL << 30;
   return launch_k(ln_fwd_long_kernel<T, VEC>, dim3((unsigned)(a.rows < cap ? a.rows : cap)),
                   dim3(1024), 0, st, true, a);
 }
 
-// Values a thread of the backward keeps (the sums of its columns stay in
-// registers for the whole call); wider rows take the two-pass form.
-template <typename T, int VEC, int NV>
+template <typename T, int VEC, int NV, int R, int kStages, bool kKeep, int kThreads>
 cudaError_t bwd(const LnArgs &a, const LnBwdPlan &pl, float *part, cudaStream_t st) {
-  return launch_k(ln_bwd_kernel<T, VEC, NV>, dim3(pl.groups), dim3(pl.threads), 0, st, true, a,
-                  part);
+  const int units = pl.threads / std::max(pl.tpr, 32);
+  const size_t smem = std::max(units > 1 ? (size_t)units * 2 * a.d * sizeof(float) : 0,
+                               RowRing<T, VEC, 1, 1>::kCopies ? (size_t)kStages * 2 * R * NV * pl.threads * VEC * sizeof(T) : 0);
+  return launch_with(ln_bwd_kernel<T, VEC, NV, R, kStages, kKeep, kThreads>, pl.groups, pl.threads,
+                     smem, st, a, pl.tpr, part);
 }
 
 template <typename T, int VEC>
@@ -373,7 +721,9 @@ cudaError_t bwd_any(const LnArgs &a, const LnBwdPlan &pl, const float *stat, flo
     return launch_k(ln_bwd_cols_kernel<T, VEC>, dim3((a.d + cols - 1) / cols, pl.groups), dim3(256),
                     0, st, true, a, stat, part);
   }
-  return pl.nv == 1 ? bwd<T, VEC, 1>(a, pl, part, st) : bwd<T, VEC, 8>(a, pl, part, st);
+  if constexpr (VEC == 8)
+    if (pl.wide) return bwd<T, 8, 4, 1, 3, false, 512>(a, pl, part, st);
+  return bwd<T, VEC, 16 / VEC, VEC == 8 ? 2 : 1, 3, true, 512>(a, pl, part, st);
 }
 
 template <typename T, int VEC>
@@ -390,7 +740,8 @@ constexpr int kTwoPassGroups = 64;
 cudaError_t launch_layernorm_rows(const LnArgs &a, int bf16, cudaStream_t st) {
   if (a.rows == 0) return cudaSuccess;
   const int esz = bf16 ? 2 : 4, vec = 16 / esz;
-  const bool v = a.d % vec == 0 && rows_aligned(a.x, a.sx, esz) && rows_aligned(a.out, a.so, esz);
+  const bool v = a.d % vec == 0 && rows_aligned(a.x, a.sx, esz) && rows_aligned(a.out, a.so, esz) &&
+                 param_aligned(a.w) && param_aligned(a.b);
   if (bf16) return v ? fwd_any<__nv_bfloat16, 8>(a, st) : fwd_any<__nv_bfloat16, 1>(a, st);
   return v ? fwd_any<float, 4>(a, st) : fwd_any<float, 1>(a, st);
 }
@@ -399,21 +750,34 @@ LnBwdPlan layernorm_bwd_plan(const LnArgs &a, int bf16) {
   LnBwdPlan pl;
   const int esz = bf16 ? 2 : 4, vec = 16 / esz;
   pl.vec = a.d % vec == 0 && rows_aligned(a.x, a.sx, esz) && rows_aligned(a.dy, a.sg, esz) &&
-           rows_aligned(a.out, a.so, esz);
-  const int V = pl.vec ? vec : 1;
-  pl.nv = a.d <= 1024 * V ? 1 : 8;
-  pl.two_pass = a.d > (pl.vec ? 1024 * V : 8192);
-  pl.threads = threads_for(a.d, V * pl.nv, 1024);
-  // CTAs (each writes one row of partial sums): 1024 threads an SM.
-  long long want = pl.two_pass ? kTwoPassGroups
-                               : (long long)sm_count() * (pl.threads >= 1024 ? 1 : 1024 / pl.threads);
-  pl.groups = (int)(a.rows < want ? a.rows : want);
+           rows_aligned(a.out, a.so, esz) && param_aligned(a.w);
+  // Columns a thread: 16, above 8192 columns 32 (bf16), else two passes.
+  const int V = pl.vec ? vec : 1, n = (a.d + V - 1) / V;
+  pl.tpr = threads_per_row(n, 16 / V);
+  if (pl.tpr > 512) {
+    pl.wide = V == 8 && pl.tpr <= 1024;
+    pl.two_pass = !pl.wide;
+    pl.tpr = threads_per_row(n, 32 / V);
+  }
+  if (pl.two_pass) {
+    pl.groups = (int)std::min<long long>(a.rows, kTwoPassGroups);
+    return pl;
+  }
+  // One CTA of up to 512 threads an SM: as many row groups as fit, for few
+  // rows no more than share out over all SMs.  (At most 15 groups of several
+  // warps: each has a named barrier.)
+  const long long sms = sm_count(), R = V == 8 && !pl.wide ? 2 : 1;
+  const int most = 512;
+  const long long fit = pl.tpr > 32 ? std::min(most / pl.tpr, 15) : most / pl.tpr;
+  long long at_once = std::min(fit, std::max<long long>(1, a.rows / (sms * R)));
+  while (pl.tpr < 32 && at_once * pl.tpr % 32) ++at_once;
+  pl.threads = (int)at_once * pl.tpr;
+  pl.groups = (int)std::min((a.rows + at_once * R - 1) / (at_once * R), sms);
   return pl;
 }
 
 size_t layernorm_bwd_bytes(long long rows, int d) {
-  // CTAs of one warp each, or the two-pass form's groups
-  const long long most = std::max((long long)sm_count() * 32, (long long)kTwoPassGroups);
+  const long long most = std::max(sm_count(), kTwoPassGroups);
   return ((size_t)(rows < most ? rows : most) * 2 * d + (size_t)rows * 2) * sizeof(float);
 }
 

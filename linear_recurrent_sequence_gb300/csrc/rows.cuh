@@ -4,6 +4,7 @@
 
 #include "common.cuh"
 #include "launch.h"
+#include "tc.cuh"
 
 namespace ret {
 
@@ -14,6 +15,17 @@ __device__ __forceinline__ long long row_offset(const RowSet &s, long long r) {
   return i * s.s0 + (r - i * s.n1) * s.s1;
 }
 
+// 16 bytes of a row that is read once: not kept in L1, which is left to the
+// parameters that every row reads.
+__device__ __forceinline__ uint4 load_stream(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
 // VEC consecutive elements of type T as floats.  VEC is 16 / sizeof(T) (the
 // address is then 16-byte aligned) or 1.
 template <typename T, int VEC>
@@ -22,10 +34,7 @@ struct Elems;
 template <>
 struct Elems<__nv_bfloat16, 8> {
   uint4 raw;
-  __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
-    raw = *reinterpret_cast<const uint4 *>(p);
-  }
-  __device__ __forceinline__ void fill(uint32_t w) { raw = make_uint4(w, w, w, w); }
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { raw = load_stream(p); }
   __device__ __forceinline__ void get(float (&f)[8]) const {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
@@ -52,7 +61,9 @@ template <>
 struct Elems<float, 4> {
   float4 raw;
   __device__ __forceinline__ void load(const float *p) {
-    raw = *reinterpret_cast<const float4 *>(p);
+    const uint4 v = load_stream(p);
+    raw = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+                      __uint_as_float(v.w));
   }
   __device__ __forceinline__ void get(float (&f)[4]) const {
     f[0] = raw.x; f[1] = raw.y; f[2] = raw.z; f[3] = raw.w;
