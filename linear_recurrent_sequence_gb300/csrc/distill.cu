@@ -12,8 +12,10 @@
 // 1 - sum q_k.
 //
 // Bound by memory: the loss reads each logit once, the gradient reads it and
-// writes a value.  Loss and gradient in one call: the second reading of the
-// row finds it in L2.
+// writes a value.  Eight warps of a CTA walk over its slice of the row while a
+// ninth reads the list, gathers its logits and forms the teacher's
+// probabilities; the listed logits' own softmax joins the others', so that the
+// gradient can start at once while the ninth warp adds up the loss.
 #include "launch.h"
 #include "logits.cuh"
 
@@ -21,26 +23,23 @@ namespace ret {
 
 namespace {
 
-constexpr int kThreads = 512;
 constexpr int kUnroll = 4;
 constexpr int kMaxTop = RETNET_MAX_TOP;
 
-// The list of a row and the row's constants.
+constexpr int kThreads = kRowThreads + 32;  // and the list's warp
+constexpr int kPer = kMaxTop / 32;          // its entries a lane: lane + 32 i
+
+// The list of a row.
 struct ListShared {
   int id[kMaxTop];      // the token, or -1: absent, out of range, listed before
   float x[kMaxTop];     // the student's logit
   float p[kMaxTop];     // the teacher's probability and its logarithm
   float ln_p[kMaxTop];
-  int repeated, outside, no_teacher;
+  int outside, no_teacher;
   float p_rest;
-  // ln q_j = ((x_j - a) log2(e) / T - b) ln 2, and with a_rest, b_rest in
-  // place of a, b  ln (q_j / q_rest): each relative to its own maximum
-  float a, b, a_rest, b_rest;
-  float c, c_rest;      // T w and T w p_rest
-  Softmax joined[kThreads / 32];
+  Softmax top;          // of the listed logits
+  Softmax parts[kRowWarps], mine;
 };
-
-__device__ __forceinline__ float nan_value() { return __int_as_float(0x7fffffff); }
 
 // p ln(p / q) - p + q from ln p and ln q.  Near p = q the difference of the
 // logarithms d gives p (d - 1 + e^-d) by its series, exact to 2^-24 for |d| < 1/2.
@@ -54,50 +53,90 @@ __device__ __forceinline__ float loss_term(float p, float ln_p, float ln_q) {
   } else {
     g = d + expm1f(-d);
   }
-  return p * g;
+  return __fmul_rn(p, g);  // (no contraction: the same bits wherever this is inlined)
 }
 
-// The tokens of row r: validity, the bit of each in `bits`, the student's
-// logits.  Bit position of token i: i - head + kVec, so that vector v of the
-// row has the kVec bits from (v + 1) kVec.
+// The list warp: the tokens of row r, and the bit of each in `bits`.  Bit
+// position of token i: i - head + kVec, so that vector v of the row has the kVec
+// bits from (v + 1) kVec.
 template <typename T>
-__device__ __forceinline__ void read_list(const DistillArgs &a, long long r, const LogitRow<T> &row,
-                                          unsigned *bits, int words, ListShared &sh) {
+__device__ __forceinline__ void read_ids(const DistillArgs &a, long long r, const LogitRow<T> &row,
+                                         unsigned *bits, int words, ListShared &sh) {
   constexpr int kVec = LogitRow<T>::kVec;
-  for (int i = threadIdx.x; i < words; i += kThreads) bits[i] = 0u;
-  if (threadIdx.x == 0) sh.repeated = sh.outside = 0;
-  __syncthreads();
-  const int k = threadIdx.x;
-  int id = -1;
-  if (k < a.top) {
-    const long long v = a.id64 ? reinterpret_cast<const long long *>(a.ids)[r * a.top + k]
-                               : (long long)reinterpret_cast<const int *>(a.ids)[r * a.top + k];
-    if (v >= a.V) sh.outside = 1;
-    if (v >= 0 && v < a.V) {
-      id = (int)v;
-      const int at = id - row.head + kVec;
-      if (atomicOr(&bits[at >> 5], 1u << (at & 31)) >> (at & 31) & 1u) sh.repeated = 1;
+  const int lane = threadIdx.x & 31;
+  for (int i = lane; i < words / 4; i += 32) reinterpret_cast<uint4 *>(bits)[i] = make_uint4(0, 0, 0, 0);
+  __syncwarp();
+  bool outside = false, repeated = false;
+  int id[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int k = lane + 32 * i;
+    id[i] = -1;
+    if (k < a.top) {
+      const long long v = a.id64 ? reinterpret_cast<const long long *>(a.ids)[r * a.top + k]
+                                 : (long long)reinterpret_cast<const int *>(a.ids)[r * a.top + k];
+      outside |= v >= a.V;
+      if (v >= 0 && v < a.V) id[i] = (int)v;
     }
-    sh.id[k] = id;
+    sh.id[k] = id[i];
   }
-  __syncthreads();
-  if (sh.repeated && k < a.top && id >= 0)
-    for (int j = 0; j < k; ++j)
-      if (sh.id[j] == id) id = -1;
-  if (sh.repeated) {
-    __syncthreads();
-    if (k < a.top) sh.id[k] = id;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (id[i] >= 0) {
+      const int at = id[i] - row.head + kVec;
+      repeated |= (atomicOr(&bits[at >> 5], 1u << (at & 31)) >> (at & 31) & 1u) != 0;
+    }
+  outside = __any_sync(0xffffffffu, outside);
+  if (__any_sync(0xffffffffu, repeated)) {  // (also orders the ids' stores before their loads)
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      for (int j = 0; j < lane + 32 * i; ++j)
+        if (sh.id[j] == id[i]) id[i] = -1;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sh.id[lane + 32 * i] = id[i];
   }
-  if (k < a.top) sh.x[k] = id >= 0 ? logit_of(row.p[id]) : -INFINITY;
-  __syncthreads();
+  if (lane == 0) sh.outside = outside;
+  __syncwarp();
+}
+
+// The list warp: the listed logits and their softmax.  `wants(id)`: whether
+// this CTA uses the token's logit.  (The gradient alone uses those of its own
+// slice: where it is written over the logits, another CTA may be past its
+// slice already.)
+template <typename T, typename F>
+__device__ __forceinline__ void read_logits(const DistillArgs &a, const LogitRow<T> &row,
+                                            ListShared &sh, F wants) {
+  const int lane = threadIdx.x & 31;
+  float x[kPer], m = -INFINITY, z = 0.f;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int id = sh.id[lane + 32 * i];
+    x[i] = id >= 0 && wants(id) ? logit_of(row.p[id]) : -INFINITY;
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    sh.x[lane + 32 * i] = x[i];
+    bad |= !(x[i] <= kFltMax);
+    m = fmaxf(m, x[i]);
+  }
+  m = redux_max(m);
+  const float mm = m > -INFINITY ? m : 0.f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) z += ex2((x[i] - mm) * a.scale);
+  z = warp_sum(z);
+  bad = __any_sync(0xffffffffu, bad);
+  if (lane == 0) sh.top = {m, z, 0.f, bad};
 }
 
 // A sum in two floats: hi + lo, |lo| below an ulp of hi.
 struct TwoFloat {
   float hi, lo;
   __device__ __forceinline__ void add(float x) {
-    const float t = hi + x, b = t - hi;
-    lo += (hi - (t - b)) + (x - b);
+    const float t = __fadd_rn(hi, x), b = __fsub_rn(t, hi);
+    lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(x, b)));
     hi = t;
   }
   // e^v for v > -80, to about 2^-28 of it: with v log2(e) = n + r in two
@@ -106,26 +145,25 @@ struct TwoFloat {
   __device__ __forceinline__ void add_exp(float v) {
     constexpr float kLog2e = 1.44269502f, kLog2eLo = 1.92596303e-8f;  // log2(e) in two floats
     constexpr float kLn2 = 0.693147182f, kLn2Lo = -1.90465421e-9f;    // ln 2
-    const float t = v * kLog2e, t_lo = fmaf(v, kLog2eLo, fmaf(v, kLog2e, -t));
-    const float n = rintf(t), r = t - n;
-    const float z = r * kLn2, z_lo = fmaf(r, kLn2, -z) + fmaf(r, kLn2Lo, t_lo * kLn2);
+    const float t = __fmul_rn(v, kLog2e), t_lo = fmaf(v, kLog2eLo, fmaf(v, kLog2e, -t));
+    const float n = rintf(t), r = __fsub_rn(t, n);
+    const float z = __fmul_rn(r, kLn2);
+    const float z_lo = __fadd_rn(fmaf(r, kLn2, -z), fmaf(r, kLn2Lo, __fmul_rn(t_lo, kLn2)));
     const float q = z * z * (1.f / 2.f + z * (1.f / 6.f + z * (1.f / 24.f + z * (1.f / 120.f + z * (1.f / 720.f + z * (1.f / 5040.f))))));
     const float s = exp2f(n);
     add(s);
-    add(s * z);
-    add(s * fmaf(z_lo, 1.f + z, q));
+    add(__fmul_rn(s, z));
+    add(__fmul_rn(s, fmaf(z_lo, 1.f + z, q)));
   }
 };
 
-// The teacher's probabilities (warp 0; a lane has the entries lane + 32 i).
-__device__ __forceinline__ void teacher(const DistillArgs &a, long long r, ListShared &sh) {
-  const int lane = threadIdx.x;
-  constexpr int kPer = kMaxTop / 32;
-  float v[kPer], p[kPer], m = -INFINITY, sum = 0.f;
+// The list warp: the teacher's probabilities.
+__device__ __forceinline__ void teacher(const DistillArgs &a, float (&v)[kPer], ListShared &sh) {
+  const int lane = threadIdx.x & 31;
+  float p[kPer], m = -INFINITY, sum = 0.f;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int k = lane + 32 * i;
-    v[i] = k < a.top && sh.id[k] >= 0 ? a.values[r * a.top + k] : -INFINITY;
+    if (sh.id[lane + 32 * i] < 0) v[i] = -INFINITY;
     m = max_nan(m, v[i]);
   }
   float ln_sum = 0.f;
@@ -134,7 +172,7 @@ __device__ __forceinline__ void teacher(const DistillArgs &a, long long r, ListS
     for (int s = 16; s > 0; s >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, s));
     const bool none = m == -INFINITY;  // no probabilities: the row counts for nothing
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) v[i] = none ? -INFINITY : (v[i] - m) * a.inv_t;
+    for (int i = 0; i < kPer; ++i) v[i] = none ? -INFINITY : __fmul_rn(v[i] - m, a.inv_t);
     if (lane == 0) sh.no_teacher = none;
   } else if (lane == 0) {
     sh.no_teacher = 0;
@@ -178,82 +216,86 @@ __device__ __forceinline__ void teacher(const DistillArgs &a, long long r, ListS
   if (lane == 0) sh.p_rest = rest;
 }
 
-// Warp 0: the student's normaliser from the softmax `rest` of the tokens
-// that are not listed and the listed logits; the row's loss and statistics.
+// What a row's threads need of it: ln q_j = ((x_j - a) log2(e) / T - b) ln 2, and
+// with a_rest, b_rest in place of a, b  ln (q_j / q_rest), each relative to its
+// own maximum; c = T w and c_rest = T w p_rest.
+struct RowConstants {
+  float a, b, a_rest, b_rest, c, c_rest;
+  bool bad, empty;
+};
+
+// From the softmax `rest` of the tokens that are not listed and that of the
+// listed ones.
+__device__ __forceinline__ RowConstants row_constants(const DistillArgs &a, float weight,
+                                                      const Softmax &rest, const ListShared &sh) {
+  RowConstants k;
+  const Softmax top = sh.top;
+  const float m = fmaxf(rest.m, top.m);
+  k.bad = rest.bad || top.bad || sh.outside;
+  k.empty = m == -INFINITY;
+  k.a = k.empty ? 0.f : m;
+  const float z = fmaf(rest.s, ex2((rest.m - k.a) * a.scale), __fmul_rn(top.s, ex2((top.m - k.a) * a.scale)));
+  k.b = k.empty ? 0.f : log2f(z);
+  const bool none = sh.no_teacher || (k.empty && !k.bad), some = rest.s > 0.f;
+  k.a_rest = some ? rest.m : 0.f;
+  k.b_rest = some ? log2f(rest.s) : 0.f;
+  const float w = weight * a.t;
+  k.c = k.bad ? nan_value() : none ? 0.f : w;
+  k.c_rest = none || !some ? 0.f : w * sh.p_rest;
+  return k;
+}
+
+// From the statistics that the forward saved.
+__device__ __forceinline__ RowConstants saved_constants(const DistillArgs &a, long long r, float weight,
+                                                        bool outside, bool no_teacher, float p_rest) {
+  RowConstants k;
+  const float lse = a.stats[2 * r], lse_rest = a.stats[2 * r + 1];
+  const float w = weight * a.t;
+  const bool none = no_teacher || lse == -INFINITY;
+  const bool no_rest = none || lse_rest == -INFINITY;
+  // a: a level near the row's logits; b: what its rounding left out
+  constexpr float kLog2e = 1.4426950408889634f;
+  k.a = none ? 0.f : lse * a.t;
+  k.b = none ? 0.f : -fmaf(k.a, a.inv_t, -lse) * kLog2e;
+  k.a_rest = no_rest ? 0.f : lse_rest * a.t;
+  k.b_rest = no_rest ? 0.f : -fmaf(k.a_rest, a.inv_t, -lse_rest) * kLog2e;
+  k.c = outside ? nan_value() : none ? 0.f : w;
+  k.c_rest = no_rest ? 0.f : w * p_rest;
+  return k;
+}
+
+// The list warp: the row's loss and statistics.
 __device__ __forceinline__ void row_loss(const DistillArgs &a, long long r, const Softmax &rest,
-                                         ListShared &sh) {
-  const int lane = threadIdx.x;
-  constexpr int kPer = kMaxTop / 32;
-  float x[kPer], m = rest.m;
-  bool bad = rest.bad;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int k = lane + 32 * i;
-    x[i] = k < a.top && sh.id[k] >= 0 ? sh.x[k] : -INFINITY;
-    bad |= !(x[i] <= 3.402823466e38f);
-    m = fmaxf(m, x[i]);
-  }
-  m = warp_max(m);
-  bad = __any_sync(0xffffffffu, bad) || sh.outside;
-  const bool empty = m == -INFINITY;
-  if (empty) m = 0.f;
-  float z = 0.f;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) z += ex2((x[i] - m) * a.scale);
-  z = warp_sum(z);
-  const float dr = rest.m - m;  // -infinity where nothing is left
-  z += rest.s * ex2(dr * a.scale);
-  const float ln_z = logf(z);
-  const float ln_qr = rest.s > 0.f ? dr * a.inv_t + (logf(rest.s) - ln_z) : -INFINITY;
+                                         const RowConstants &c, const ListShared &sh) {
+  const int lane = threadIdx.x & 31;
+  constexpr float kLn2 = 0.6931471805599453f;
+  const float ln_z = __fmul_rn(c.b, kLn2);
+  const float ln_qr = rest.s > 0.f ? fmaf(rest.m - c.a, a.inv_t, fmaf(c.b_rest, kLn2, -ln_z)) : -INFINITY;
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int k = lane + 32 * i;
     if (k < a.top && sh.id[k] >= 0)
-      sum += loss_term(sh.p[k], sh.ln_p[k], empty ? -INFINITY : (x[i] - m) * a.inv_t - ln_z);
+      sum += loss_term(sh.p[k], sh.ln_p[k], c.empty ? -INFINITY : fmaf(sh.x[k] - c.a, a.inv_t, -ln_z));
   }
   sum = warp_sum(sum);
-  const float pr = sh.p_rest;
-  sum += loss_term(pr, logf(pr), empty ? -INFINITY : ln_qr);
   if (lane == 0) {
-    if (a.loss) a.loss[r] = bad ? nan_value() : sh.no_teacher ? 0.f : sum * (a.t * a.t);
+    const float pr = sh.p_rest;
+    sum += loss_term(pr, logf(pr), c.empty ? -INFINITY : ln_qr);
+    if (a.loss) a.loss[r] = c.bad ? nan_value() : sh.no_teacher ? 0.f : sum * (a.t * a.t);
     if (a.stats) {
-      a.stats[2 * r] = bad && !sh.outside ? nan_value() : empty ? -INFINITY : fmaf(m, a.inv_t, ln_z);
-      a.stats[2 * r + 1] = bad && !sh.outside ? nan_value() : fmaf(m, a.inv_t, ln_qr + ln_z);
+      const bool bad = rest.bad || sh.top.bad;
+      a.stats[2 * r] = bad ? nan_value() : c.empty ? -INFINITY : fmaf(c.a, a.inv_t, ln_z);
+      a.stats[2 * r + 1] = bad ? nan_value() : fmaf(c.a, a.inv_t, ln_qr + ln_z);
     }
-    const float w = (a.weight ? a.weight[r] : 1.f) * a.t;
-    sh.a = m;
-    sh.b = empty ? 0.f : log2f(z);
-    sh.a_rest = rest.s > 0.f ? rest.m : 0.f;
-    sh.b_rest = rest.s > 0.f ? log2f(rest.s) : 0.f;
-    const bool none = sh.no_teacher || (empty && !bad);
-    sh.c = bad ? nan_value() : none ? 0.f : w;
-    sh.c_rest = none || !(rest.s > 0.f) ? 0.f : w * pr;
   }
-}
-
-// The row's constants from the statistics that the forward saved.
-__device__ __forceinline__ void row_constants(const DistillArgs &a, long long r, ListShared &sh) {
-  const float lse = a.stats[2 * r], lse_rest = a.stats[2 * r + 1];
-  const float w = (a.weight ? a.weight[r] : 1.f) * a.t;
-  const bool none = sh.no_teacher || lse == -INFINITY;
-  const bool no_rest = none || lse_rest == -INFINITY;
-  // a: a level near the row's logits; b: what its rounding left out
-  constexpr float kLog2e = 1.4426950408889634f;
-  sh.a = none ? 0.f : lse * a.t;
-  sh.b = none ? 0.f : -fmaf(sh.a, a.inv_t, -lse) * kLog2e;
-  sh.a_rest = no_rest ? 0.f : lse_rest * a.t;
-  sh.b_rest = no_rest ? 0.f : -fmaf(sh.a_rest, a.inv_t, -lse_rest) * kLog2e;
-  sh.c = sh.outside ? nan_value() : none ? 0.f : w;
-  sh.c_rest = no_rest ? 0.f : w * sh.p_rest;
 }
 
 // The gradient of a token that is not listed.
 struct RestGradient {
   float a, b, a_rest, b_rest, c, c_rest, scale;
-  __device__ __forceinline__ RestGradient(const ListShared &sh, float sc)
-      : a(-sh.a), b(-sh.b), a_rest(-sh.a_rest), b_rest(-sh.b_rest), c(sh.c), c_rest(-sh.c_rest),
-        scale(sc) {}
+  __device__ __forceinline__ RestGradient(const RowConstants &k, float sc)
+      : a(-k.a), b(-k.b), a_rest(-k.a_rest), b_rest(-k.b_rest), c(k.c), c_rest(-k.c_rest), scale(sc) {}
   template <bool kTail>
   __device__ __forceinline__ float2 at(float2 x) const {
     const float2 s2 = make_float2(scale, scale);
@@ -267,152 +309,316 @@ struct RestGradient {
   }
 };
 
-// The gradient row; x may be dx.
-template <typename T, bool kTail>
-__device__ __forceinline__ void write_gradient(const DistillArgs &a, const LogitRow<T> &row, T *dx,
-                                               bool zero, const ListShared &sh) {
+// The CTA's slice of a row in shared memory, a thread's own vectors at
+// [vector][thread]: only the thread that copied one reads it.  The copies are
+// kGroups groups of kUnroll vectors a thread.
+constexpr int kGroups = 4;
+constexpr int kSliceBytes = kGroups * kUnroll * kRowThreads * 16;
+
+template <typename T>
+struct StagedSlice {
+  uint8_t *slot;
+  __device__ __forceinline__ StagedSlice(uint8_t *base) : slot(base + threadIdx.x * 16) {}
+  __device__ __forceinline__ void copy(const LogitRow<T> &row, const RowSlice &slice) {
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j) {
+        const int n = g * kUnroll + j, at = slice.v0 + threadIdx.x + n * kRowThreads;
+        if (at < slice.v1)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(slot + n * kRowThreads * 16)),
+                       "l"(row.p + row.index(at))
+                       : "memory");
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  }
+  // Groups 0 .. g have arrived.
+  template <int g>
+  __device__ __forceinline__ void wait() const {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kGroups - 1 - g) : "memory");
+  }
+  __device__ __forceinline__ void get(int n, LogitVec<T> &v) const {
+    v.raw = *reinterpret_cast<const decltype(v.raw) *>(slot + n * kRowThreads * 16);
+  }
+};
+
+// The eight warps: the gradient of the CTA's slice of the row, from the logits
+// in shared memory (kStaged) or from x itself (whose first group is in
+// `ahead`); x may be dx.
+template <typename T, bool kTail, bool kStaged>
+__device__ __forceinline__ void write_gradient(const LogitRow<T> &row, const RowSlice &slice,
+                                               const StagedSlice<T> &staged, T *dx, bool zero,
+                                               const RestGradient &rest, const LogitVec<T> *ahead) {
   constexpr int kVec = LogitRow<T>::kVec;
   const int tid = threadIdx.x;
-  const RestGradient rest(sh, a.scale);
   const bool vec = ((reinterpret_cast<uintptr_t>(dx) ^ reinterpret_cast<uintptr_t>(row.p)) & 15) == 0;
-  for (int i = tid; i < row.nvec; i += kUnroll * kThreads) {
-    LogitVec<T> v[kUnroll];
+  auto put = [&](int at, LogitVec<T> &v) {
+    float f[kVec];
+    if (zero) {
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j) {
-      const int at = i + j * kThreads;
-      if (at < row.nvec && !zero) v[j].load(row.p + row.index(at));
-    }
+      for (int e = 0; e < kVec; ++e) f[e] = 0.f;
+    } else {
+      v.get(f);
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j) {
-      const int at = i + j * kThreads;
-      if (at >= row.nvec) continue;
-      float f[kVec];
-      if (zero) {
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) f[e] = 0.f;
-      } else {
-        v[j].get(f);
-#pragma unroll
-        for (int e = 0; e < kVec; e += 2) {
-          const float2 g = rest.template at<kTail>(make_float2(f[e], f[e + 1]));
-          f[e] = g.x;
-          f[e + 1] = g.y;
-        }
-      }
-      T *o = dx + row.index(at);
-      if (vec) {
-        v[j].set(f);
-        v[j].store(o);
-      } else {
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-          Elems<T, 1> one;
-          const float g1[1] = {f[e]};
-          one.set(g1);
-          one.store(o + e);
-        }
+      for (int e = 0; e < kVec; e += 2) {
+        const float2 g = rest.template at<kTail>(make_float2(f[e], f[e + 1]));
+        f[e] = g.x;
+        f[e + 1] = g.y;
       }
     }
-  }
-  for (int which = 0; which < 2; ++which) {
-    const int i = which ? row.tail_index() + tid : tid;
-    if (tid < (which ? row.tail : row.head)) {
-      const float x = zero ? 0.f : logit_of(row.p[i]);
-      const float g1[1] = {zero ? 0.f : rest.template at<kTail>(make_float2(x, x)).x};
-      Elems<T, 1> one;
-      one.set(g1);
-      one.store(dx + i);
+    T *o = dx + row.index(at);
+    if (vec) {
+      v.set(f);
+      v.store(o);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        Elems<T, 1> one;
+        const float g1[1] = {f[e]};
+        one.set(g1);
+        one.store(o + e);
+      }
+    }
+  };
+  int i = slice.v0 + tid;
+  if (kStaged) {
+    for (int n = 0; i < slice.v1; i += kRowThreads, ++n) {
+      LogitVec<T> v;
+      staged.get(n, v);
+      put(i, v);
+    }
+  } else {
+    if (ahead) {
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j)
+        if (i + j * kRowThreads < slice.v1) {
+          LogitVec<T> v = ahead[j];
+          put(i + j * kRowThreads, v);
+        }
+      i += kUnroll * kRowThreads;
+    }
+    for (; i + (kUnroll - 1) * kRowThreads < slice.v1; i += kUnroll * kRowThreads) {
+      LogitVec<T> v[kUnroll];
+      if (!zero)
+#pragma unroll
+        for (int j = 0; j < kUnroll; ++j) v[j].load(row.p + row.index(i + j * kRowThreads));
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j) put(i + j * kRowThreads, v[j]);
+    }
+    for (; i < slice.v1; i += kRowThreads) {
+      LogitVec<T> v;
+      if (!zero) v.load(row.p + row.index(i));
+      put(i, v);
     }
   }
-  if (zero) return;
-  __syncthreads();  // the listed tokens' gradients replace what stands there
-  if (tid < a.top && sh.id[tid] >= 0) {
-    const float q = ex2(fmaf(sh.x[tid] - sh.a, a.scale, -sh.b));
-    const float g1[1] = {sh.c * (q - sh.p[tid])};
+  const int single = slice.single(row);
+  if (single >= 0) {
+    const float x = zero ? 0.f : logit_of(row.p[single]);
+    const float g1[1] = {zero ? 0.f : rest.template at<kTail>(make_float2(x, x)).x};
     Elems<T, 1> one;
     one.set(g1);
-    one.store(dx + sh.id[tid]);
+    one.store(dx + single);
   }
 }
 
-template <typename T, int kWhat, bool kTail>
-__global__ void __launch_bounds__(kThreads)
+// The eight warps: the slice of the row filled with one value.
+template <typename T>
+__device__ __forceinline__ void fill_slice(const LogitRow<T> &row, const RowSlice &slice, T *dx, float x) {
+  const int i0 = slice.first ? 0 : row.index(slice.v0), i1 = slice.last ? row.V : row.index(slice.v1);
+  Elems<T, 1> one;
+  const float g1[1] = {x};
+  one.set(g1);
+  for (int i = i0 + threadIdx.x; i < i1; i += kRowThreads) one.store(dx + i);
+}
+
+// Barrier 1: the list is ready.  Its warp goes on without waiting.
+__device__ __forceinline__ void list_ready() {
+  __threadfence_block();
+  asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory");
+}
+__device__ __forceinline__ void wait_list() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+
+template <typename T, int kWhat, bool kTail, bool kStaged>
+__global__ void __launch_bounds__(kThreads, kStaged ? 3 : 4)
 distill_kernel(const DistillArgs a, int words) {
   constexpr int kVec = LogitRow<T>::kVec;
-  extern __shared__ unsigned bits[];
+  constexpr bool kFwd = (kWhat & kDistillFwd) != 0, kBwd = (kWhat & kDistillBwd) != 0;
+  extern __shared__ __align__(16) uint8_t dyn[];  // the bits, then the staged slice
   __shared__ ListShared sh;
   pdl_launch_dependents();
   pdl_wait();
-  const int tid = threadIdx.x;
-  for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
+  unsigned *bits = reinterpret_cast<unsigned *>(dyn);
+  StagedSlice<T> staged(dyn + (size_t)words * 4);
+  const uint32_t ctas = cluster_size(), rank = cluster_rank();
+  const int tid = threadIdx.x, lane = tid & 31;
+  const bool walks = tid < kRowThreads;
+  for (long long r = blockIdx.x / ctas; r < a.rows; r += gridDim.x / ctas) {
     const LogitRow<T> row(reinterpret_cast<const T *>(a.x) + row_offset(a.sx, r), a.V);
-    T *dx = (kWhat & kDistillBwd) ? reinterpret_cast<T *>(a.dx) + row_offset(a.sd, r) : nullptr;
-    const bool zero = (kWhat & kDistillBwd) && a.weight && a.weight[r] == 0.f;
-    if (kWhat == kDistillBwd && zero) {
-      write_gradient<T, kTail>(a, row, dx, true, sh);
+    const RowSlice slice(row, ctas, rank);
+    T *dx = kBwd ? reinterpret_cast<T *>(a.dx) + row_offset(a.sd, r) : nullptr;
+    const float weight = kBwd && a.weight ? a.weight[r] : 1.f;
+    const bool zero = kBwd && weight == 0.f;
+    if (!kFwd && zero) {
+      if (walks) write_gradient<T, kTail, false>(row, slice, staged, dx, true, RestGradient({}, 0.f), nullptr);
       continue;
     }
-    read_list(a, r, row, bits, words, sh);
-    if (tid < 32) teacher(a, r, sh);
-    if (kWhat & kDistillFwd) {
-      // the softmax of the tokens that are not listed
-      const uint8_t *bytes = reinterpret_cast<const uint8_t *>(bits);
-      Softmax acc = Softmax::none();
-      for (int i = tid; i < row.nvec; i += kUnroll * kThreads) {
-        LogitVec<T> v[kUnroll];
+    Softmax part = {-INFINITY, 0.f, 0.f, 0};
+    LogitVec<T> ahead[kStaged ? 1 : kUnroll];  // the first group, on its way while the list is read
+    int i = slice.v0 + (tid & ~31);            // of the warp's first lane: the loops are the warp's
+    if (!walks) {
+      float values[kPer];
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        values[j] = lane + 32 * j < a.top ? a.values[r * a.top + lane + 32 * j] : -INFINITY;
+      read_ids(a, r, row, bits, words, sh);
+      if (kFwd) list_ready();
+      read_logits(a, row, sh, [&](int id) { return kFwd || slice.has(row, id); });
+      // (the gradient alone may be written over the logits: only from here on)
+      if (!kFwd && !kTail) list_ready();
+      teacher(a, values, sh);
+      if (!kFwd && kTail) list_ready();
+    } else {
+      if (kStaged) {
+        staged.copy(row, slice);
+      } else {
 #pragma unroll
         for (int j = 0; j < kUnroll; ++j) {
-          const int at = i + j * kThreads;
-          if (at < row.nvec)
-            v[j].load(row.p + row.index(at));
+          const int at = i + lane + j * kRowThreads;
+          if (at < slice.v1)
+            ahead[kStaged ? 0 : j].load(row.p + row.index(at));
           else
-            v[j].fill_masked();
+            ahead[kStaged ? 0 : j].fill_masked();
         }
+      }
+      wait_list();  // for the bits; for the gradient alone: its logits, with the rest bucket p_rest
+      if (kFwd) {
+        // the softmax of the tokens that are not listed
+        const uint8_t *bytes = reinterpret_cast<const uint8_t *>(bits);
+        auto hide = [&](int at, LogitVec<T> &v) {
+          const unsigned hit = kVec == 8 ? bytes[at + 1] : (bytes[(at + 1) >> 1] >> (4 * ((at + 1) & 1))) & 15u;
+          if (hit)
+            for (int e = 0; e < kVec; ++e)
+              if (hit >> e & 1u) v.mask(e);
+        };
+        WarpSoftmax acc;
+        // One group of vectors, from slots n.. (kStaged), from `ahead` or from the row.
+        auto group = [&](int n, bool first) {
+          if (i >= slice.v1) return;
+          LogitVec<T> v[kUnroll];
 #pragma unroll
-        for (int j = 0; j < kUnroll; ++j) {
-          const int at = i + j * kThreads + 1;
-          if (at <= row.nvec) {
-            const unsigned hit = kVec == 8 ? bytes[at] : (bytes[at >> 1] >> (4 * (at & 1))) & 15u;
-            if (hit)
-              for (int e = 0; e < kVec; ++e)
-                if (hit >> e & 1u) v[j].mask(e);
+          for (int j = 0; j < kUnroll; ++j) {
+            const int at = i + lane + j * kRowThreads;
+            const bool in = at < slice.v1;
+            if (!kStaged && first)
+              v[j] = ahead[kStaged ? 0 : j];
+            else if (!in)
+              v[j].fill_masked();
+            else if (kStaged)
+              staged.get(n + j, v[j]);
+            else
+              v[j].load(row.p + row.index(at));
+          }
+#pragma unroll
+          for (int j = 0; j < kUnroll; ++j)
+            if (i + lane + j * kRowThreads < slice.v1) hide(i + lane + j * kRowThreads, v[j]);
+          acc.group<T, kUnroll, false>(v, a.scale);
+          i += kUnroll * kRowThreads;
+        };
+        if (kStaged) {
+          staged.template wait<0>();
+          group(0, false);
+          staged.template wait<1>();
+          group(kUnroll, false);
+          staged.template wait<2>();
+          group(2 * kUnroll, false);
+          staged.template wait<3>();
+          group(3 * kUnroll, false);
+        } else {
+          group(0, true);
+          while (i < slice.v1) group(0, false);
+        }
+        if (tid < 32) {
+          const int single = slice.single(row), at = single - row.head + kVec;
+          const bool counts = single >= 0 && !(bits[at >> 5] >> (at & 31) & 1u);
+          acc.single<false>(counts ? logit_of(row.p[single]) : -INFINITY, a.scale);
+        }
+        part = acc.all<false>();
+      }
+    }
+    RowConstants k;
+    if (kFwd) {
+      const Softmax rest = join_row<false>(part, a.scale, ctas, sh.parts, &sh.mine);
+      if (ctas > 1) cluster_have_read();
+      if (kBwd || !walks) k = row_constants(a, weight, rest, sh);
+      if (!walks && rank == 0) row_loss(a, r, rest, k, sh);
+    } else {
+      if (walks && !kTail)
+        k = saved_constants(a, r, weight, sh.outside, false, 0.f);  // the teacher is looked at below
+      else
+        k = saved_constants(a, r, weight, sh.outside, sh.no_teacher, sh.p_rest);
+    }
+    if (kBwd) {
+      if (walks)
+        write_gradient<T, kTail, kStaged>(row, slice, staged, dx, zero, RestGradient(k, a.scale),
+                                          kFwd || kStaged ? nullptr : ahead);
+      __syncthreads();
+      // A row without a teacher, where the gradient did not wait to know it.
+      const bool blank = !kFwd && !kTail && sh.no_teacher && !sh.outside && a.stats[2 * r] == a.stats[2 * r];
+      if (blank && walks) fill_slice(row, slice, dx, 0.f);
+      // The listed tokens' gradients replace what stands there; each is written
+      // by the CTA whose slice it is in.
+      if (!walks && !zero)
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          const int id = sh.id[lane + 32 * j];
+          if (id >= 0 && slice.has(row, id) && !blank) {
+            const float q = ex2(fmaf(sh.x[lane + 32 * j] - k.a, a.scale, -k.b));
+            const float g1[1] = {k.c * (q - sh.p[lane + 32 * j])};
+            Elems<T, 1> one;
+            one.set(g1);
+            one.store(dx + id);
           }
         }
-        acc.group<T, kUnroll, false>(v, a.scale);
-      }
-      for (int which = 0; which < 2; ++which) {
-        const int i = which ? row.tail_index() + tid : tid, at = i - row.head + kVec;
-        if (tid < (which ? row.tail : row.head) && !(bits[at >> 5] >> (at & 31) & 1u)) {
-          const float x = logit_of(row.p[i]);
-          acc.raise(x, a.scale);
-          acc.take(x, a.scale);
-        }
-      }
-      const Softmax rest = join_cta(acc, a.scale, sh.joined);
-      if (tid < 32) row_loss(a, r, rest, sh);
-    } else if (tid < 32) {
-      __syncwarp();
-      if (tid == 0) row_constants(a, r, sh);
     }
-    if (kWhat & kDistillBwd) {
-      __syncthreads();
-      write_gradient<T, kTail>(a, row, dx, zero, sh);
-    }
-    __syncthreads();  // the row's list has been read
+    // the row's list has been read, its part of the softmax by the other CTAs too
+    if (ctas > 1 && kFwd) cluster_wait_read();
+    __syncthreads();
   }
+}
+
+template <typename T, int kWhat, bool kTail, bool kStaged>
+cudaError_t launch_as(const DistillArgs &a, int ctas, size_t smem, int words, cudaStream_t st) {
+  auto kern = distill_kernel<T, kWhat, kTail, kStaged>;
+  static std::atomic<unsigned> done{0};
+  if (smem > 32 * 1024) {
+    const cudaError_t e = allow_big_smem(reinterpret_cast<const void *>(kern), done);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_rows(kern, a.rows, ctas, kThreads, smem, st, a, words);
 }
 
 template <typename T, int kWhat>
 cudaError_t launch(const DistillArgs &a, cudaStream_t st) {
-  const int words = (a.V + 2 * LogitRow<T>::kVec + 31) / 32;
-  const size_t smem = (size_t)words * 4;
-  auto kern = a.tail ? distill_kernel<T, kWhat, true> : distill_kernel<T, kWhat, false>;
-  if (smem > 32 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
+  const int words = ((a.V + 2 * LogitRow<T>::kVec + 31) / 32 + 3) / 4 * 4;
+  const size_t bits = (size_t)words * 4;
+  const long long row_bytes = (long long)a.V * sizeof(T);
+  const int sms = device_sms();
+  // A slice that fits in shared memory while a cluster of 8 can share the row
+  // (loss and gradient together; the loss alone has the same slices, so that
+  // both calls give the same bits).
+  int ctas = row_ctas(a.rows, row_bytes, kWhat == kDistillBwd ? 1LL << 40 : kSliceBytes,
+                      (kWhat == kDistillBwd ? 4LL : 3LL) * sms);
+  if constexpr (kWhat == kDistillStep) {
+    const long long vecs = (row_bytes / 16 + ctas - 1) / ctas;
+    if (vecs * 16 <= kSliceBytes && bits <= 64 * 1024) {
+      const size_t smem = bits + (size_t)((vecs + kRowThreads - 1) / kRowThreads) * kRowThreads * 16;
+      return a.tail ? launch_as<T, kDistillStep, true, true>(a, ctas, smem, words, st)
+                    : launch_as<T, kDistillStep, false, true>(a, ctas, smem, words, st);
+    }
   }
-  const dim3 grid((unsigned)(a.rows < (1LL << 30) ? a.rows : (1LL << 30)));
-  return launch_k(kern, grid, dim3(kThreads), smem, st, true, a, words);
+  return a.tail ? launch_as<T, kWhat, true, false>(a, ctas, bits, words, st)
+                : launch_as<T, kWhat, false, false>(a, ctas, bits, words, st);
 }
 
 }  // namespace

@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <utility>
 
 #include "common.cuh"
@@ -29,6 +30,13 @@ cudaError_t launch_k(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
   cfg.numAttrs = pdl ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
+
+// SMs of the current device (asked once per device).
+int device_sms();
+
+// Lets a kernel use all of an SM's shared memory a CTA can have (once per
+// kernel and device).
+cudaError_t allow_big_smem(const void *kern, std::atomic<unsigned> &done);
 
 enum ScaleMode { kScaleNone = 0, kScaleArray = 1, kScaleXi = 2, kScaleZeta = 3 };
 

@@ -640,14 +640,6 @@ ln_bwd_sum_kernel(const float *__restrict__ part, int G, int d, float *__restric
   if (cx == 0 && co < d) out[co] = s;
 }
 
-int sm_count() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
-    return 1;
-  return sms;
-}
-
 // 16-byte vectors need every row of every operand on a 16-byte boundary.
 bool rows_aligned(const void *p, const RowSet &s, int esz) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (s.n1 == 1 || s.s1 * esz % 16 == 0) &&
@@ -666,13 +658,15 @@ int threads_per_row(int n, int most) {
   return p;
 }
 
-template <typename Kern, typename... Args>
-cudaError_t launch_with(Kern kern, int grid, int threads, size_t smem, cudaStream_t st, Args... args) {
+// One `done` word per kernel: kKern is part of the type.
+template <auto kKern, typename... Args>
+cudaError_t launch_with(int grid, int threads, size_t smem, cudaStream_t st, Args... args) {
+  static std::atomic<unsigned> done{0};
   if (smem > 32 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = allow_big_smem(reinterpret_cast<const void *>(kKern), done);
     if (e != cudaSuccess) return e;
   }
-  return launch_k(kern, dim3(grid), dim3(threads), smem, st, true, args...);
+  return launch_k(kKern, dim3(grid), dim3(threads), smem, st, true, args...);
 }
 
 template <typename T, int VEC, int NV, int R, int kStages, bool kKeep, int kThreads>
@@ -682,9 +676,9 @@ cudaError_t fwd(const LnArgs &a, int tpr, int per_sm, cudaStream_t st) {
   // CTAs that stay for the whole call, per_sm threads an SM, less where the
   // rings fill its shared memory.
   const long long fit = std::max<long long>(1, std::min<long long>(per_sm / threads, smem ? 220 * 1024 / (smem + 1024) : 32));
-  const long long want = (a.rows + rows - 1) / rows, most = sm_count() * fit;
-  return launch_with(ln_fwd_kernel<T, VEC, NV, R, kStages, kKeep, kThreads>,
-                     (int)std::min(want, most), threads, smem, st, a, tpr);
+  const long long want = (a.rows + rows - 1) / rows, most = device_sms() * fit;
+  return launch_with<ln_fwd_kernel<T, VEC, NV, R, kStages, kKeep, kThreads>>(
+      (int)std::min(want, most), threads, smem, st, a, tpr);
 }
 
 template <typename T, int VEC>
@@ -693,7 +687,7 @@ cudaError_t fwd_any(const LnArgs &a, cudaStream_t st) {
   const int t8 = threads_per_row(n, 8 / VEC), t16 = threads_per_row(n, 16 / VEC);
   // 8 values a thread while that leaves the SMs with at most 1024 threads each,
   // else two rows of 16; above 8192 values a row one row of 16 or 32.
-  if (t8 <= 1024 && a.rows * t8 <= (long long)sm_count() * 1024)
+  if (t8 <= 1024 && a.rows * t8 <= (long long)device_sms() * 1024)
     return fwd<T, VEC, 8 / VEC, 1, 2, false, 1024>(a, t8, 1024, st);
   if (t16 <= 512) return fwd<T, VEC, 16 / VEC, 2, sizeof(T) == 4 ? 2 : 3, true, 512>(a, t16, 512, st);
   if (t16 <= 1024) return fwd<T, VEC, 16 / VEC, 1, 3, false, 1024>(a, t16, 1024, st);
@@ -709,8 +703,8 @@ cudaError_t bwd(const LnArgs &a, const LnBwdPlan &pl, float *part, cudaStream_t 
   const int units = pl.threads / std::max(pl.tpr, 32);
   const size_t smem = std::max(units > 1 ? (size_t)units * 2 * a.d * sizeof(float) : 0,
                                RowRing<T, VEC, 1, 1>::kCopies ? (size_t)kStages * 2 * R * NV * pl.threads * VEC * sizeof(T) : 0);
-  return launch_with(ln_bwd_kernel<T, VEC, NV, R, kStages, kKeep, kThreads>, pl.groups, pl.threads,
-                     smem, st, a, pl.tpr, part);
+  return launch_with<ln_bwd_kernel<T, VEC, NV, R, kStages, kKeep, kThreads>>(
+      pl.groups, pl.threads, smem, st, a, pl.tpr, part);
 }
 
 template <typename T, int VEC>
@@ -766,7 +760,7 @@ LnBwdPlan layernorm_bwd_plan(const LnArgs &a, int bf16) {
   // One CTA of up to 512 threads an SM: as many row groups as fit, for few
   // rows no more than share out over all SMs.  (At most 15 groups of several
   // warps: each has a named barrier.)
-  const long long sms = sm_count(), R = V == 8 && !pl.wide ? 2 : 1;
+  const long long sms = device_sms(), R = V == 8 && !pl.wide ? 2 : 1;
   const int most = 512;
   const long long fit = pl.tpr > 32 ? std::min(most / pl.tpr, 15) : most / pl.tpr;
   long long at_once = std::min(fit, std::max<long long>(1, a.rows / (sms * R)));
@@ -777,7 +771,7 @@ LnBwdPlan layernorm_bwd_plan(const LnArgs &a, int bf16) {
 }
 
 size_t layernorm_bwd_bytes(long long rows, int d) {
-  const long long most = std::max(sm_count(), kTwoPassGroups);
+  const long long most = std::max(device_sms(), kTwoPassGroups);
   return ((size_t)(rows < most ? rows : most) * 2 * d + (size_t)rows * 2) * sizeof(float);
 }
 

@@ -8,13 +8,15 @@
 // Bound by memory: each logit is read once (2 or 4 bytes) and costs one
 // exponential and about six other operations.
 //
-// The alternatives cost no second pass.  The running maxima of the CTA's
-// threads, each over its own V / kThreads values, give a lower bound of the
-// k-th largest logit: the k-th largest of them (found bit by bit with
-// counting barriers).  Only the threads whose maximum reaches the bound hold
-// candidates, k of them up to ties, so only their values are read again
-// (from the caches), and the few that reach the bound are ranked against one
-// another.
+// The alternatives cost no second pass.  The maxima of the CTA's threads, each
+// of its own values, give a lower bound of the k-th largest logit: the k-th
+// largest of them, which one warp finds by bisection.  Only the threads whose
+// maximum reaches the bound hold candidates, k of them up to ties, so only
+// their values are read again (from the caches), and the few that reach the
+// bound are ranked against one another.  Where a cluster shares a row, each CTA
+// finds the k largest of its slice, and ranks its own among all of them.
+#include <type_traits>
+
 #include "launch.h"
 #include "logits.cuh"
 
@@ -22,9 +24,10 @@ namespace ret {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kCand = 1024;  // candidates ranked at once; more take the exact search
+constexpr int kCand = 1024;  // candidates ranked at once, and vectors that hold
+constexpr int kQueue = 512;  // some; more take the exact search
 constexpr int kUnroll = 4;
+constexpr int kMaxTop = RETNET_MAX_TOP;
 
 // Unsigned integer that orders as the value does (-0 counts as +0).
 template <typename T>
@@ -43,107 +46,164 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 }
 
 struct TopShared {
-  unsigned long long cand[kCand];
-  int count;
-  int warp_total[kThreads / 32];
+  alignas(16) unsigned long long cand[kCand];  // in a cluster also [ctas][kMaxTop]
+  unsigned long long sorted[kMaxTop];  // this CTA's, in order
+  uint4 raw[kQueue];                   // vectors that hold candidates
+  int at[kQueue];                      // and their numbers
+  uint32_t own[kRowThreads];
+  uint32_t bound;
+  int count, queued, listed;
+  int warp_total[kRowWarps];
 };
 
-// Calls f(key, index, valid) for the values of the warp's threads in `mask`,
-// one thread's values after another, spread over the lanes.
-template <typename T, typename F>
-__device__ __forceinline__ void each_value(const LogitRow<T> &row, unsigned mask, F f) {
+// The largest b in [lo, hi] with count_ge(b) >= k, or any b with count_ge(b)
+// == k (count_ge(lo) >= k is known).
+template <typename C>
+__device__ __forceinline__ uint32_t kth_key(uint32_t lo, uint32_t hi, int k, C count_ge) {
+  while (lo < hi) {
+    const uint32_t mid = lo + (hi - lo + 1) / 2;
+    const int n = count_ge(mid);
+    if (n >= k)
+      lo = mid;
+    else
+      hi = mid - 1;
+    if (n == k) break;
+  }
+  return lo;
+}
+
+// Fills sh.cand with the (key, ~index) pairs of the slice's k largest values
+// and at most kCand in all; returns their number (fewer than k only where
+// the slice has fewer values above -infinity).  own: this thread's maximum.
+template <typename T>
+__device__ int top_candidates(const LogitRow<T> &row, const RowSlice &slice, int single, float own,
+                              int k, TopShared &sh) {
+  const uint32_t mine = order_key<T>(own), masked = order_key<T>(-INFINITY);
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  sh.own[threadIdx.x] = mine;
+  if (threadIdx.x == 0) sh.count = sh.queued = 0;
+  __syncthreads();
+  if (wid == 0) {
+    uint32_t q[kRowWarps], lo = 0xffffffffu, hi = 0;
+#pragma unroll
+    for (int i = 0; i < kRowWarps; ++i) {
+      q[i] = sh.own[lane + 32 * i];
+      lo = min(lo, q[i]);
+      hi = max(hi, q[i]);
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    const uint32_t b = kth_key(lo, hi, k, [&](uint32_t t) {
+      int c = 0;
+#pragma unroll
+      for (int i = 0; i < kRowWarps; ++i) c += q[i] >= t;
+      return __reduce_add_sync(0xffffffffu, c);
+    });
+    if (lane == 0) sh.bound = max(b, masked + 1);  // masked values are no candidates
+  }
+  __syncthreads();
+  uint32_t bound = sh.bound;
+  auto push = [&](float x, int idx) {
+    const int at = atomicAdd(&sh.count, 1);
+    if (at < kCand) sh.cand[at] = ((unsigned long long)order_key<T>(x) << 32) | (uint32_t)~idx;
+  };
   constexpr int kVec = LogitRow<T>::kVec;
-  const int lane = threadIdx.x & 31, wbase = threadIdx.x & ~31;
-  while (mask) {
-    const int t = wbase + __ffs(mask) - 1;
-    mask &= mask - 1;
-    if (lane == 0 && t < row.head) f(order_key<T>(logit_of(row.p[t])), t);
-    if (lane == 0 && t < row.tail)
-      f(order_key<T>(logit_of(row.p[row.tail_index() + t])), row.tail_index() + t);
-    for (int i = t + lane * kThreads; i < row.nvec; i += 32 * kThreads) {
+  // The values from `least` up.  A warp goes through the values of its threads
+  // that hold some, four threads at a time, and queues the vectors with some.
+  auto collect = [&](uint32_t least) {
+    const float value = key_value<T>(least);
+    unsigned mask = __ballot_sync(0xffffffffu, mine >= least);
+    const int base = slice.v0 + (threadIdx.x & ~31) + lane * kRowThreads;
+    while (mask) {
+      int t[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        t[j] = mask ? base + __ffs(mask) - 1 : slice.v1;
+        mask &= mask - 1;
+      }
+      for (int more = t[0] - lane * kRowThreads; more < slice.v1; more += 32 * kRowThreads) {
+        LogitVec<T> v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (t[j] < slice.v1) v[j].load(row.p + row.index(t[j]));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const LogitVec<T> one[1] = {v[j]};
+          if (t[j] < slice.v1 && LogitVec<T>::max_of(one) >= value) {
+            const int at = atomicAdd(&sh.queued, 1);
+            if (at < kQueue) {
+              sh.raw[at] = *reinterpret_cast<const uint4 *>(&v[j].raw);
+              sh.at[at] = t[j];
+            }
+          }
+          t[j] = min(t[j], slice.v1) + 32 * kRowThreads;
+        }
+      }
+    }
+    if (single >= 0) {
+      const float x = logit_of(row.p[single]);
+      if (x >= value) push(x, single);
+    }
+    __syncthreads();
+    const int queued = sh.queued;
+    for (int i = threadIdx.x; i < min(queued, kQueue); i += kRowThreads) {
       LogitVec<T> v;
-      v.load(row.p + row.index(i));
+      *reinterpret_cast<uint4 *>(&v.raw) = sh.raw[i];
       float x[kVec];
       v.get(x);
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) f(order_key<T>(x[j]), row.index(i) + j);
+      for (int j = 0; j < kVec; ++j)
+        if (x[j] >= value) push(x[j], row.index(sh.at[i]) + j);
     }
-  }
-}
-
-// The largest b with at least k of the CTA's values of `count_ge(b)`.
-template <typename T, typename C>
-__device__ __forceinline__ uint32_t kth_key(int k, C count_ge) {
-  uint32_t best = 0;
-  for (int bit = sizeof(T) == 2 ? 15 : 31; bit >= 0; --bit) {
-    const uint32_t t = best | (1u << bit);
-    const int n = count_ge(t);
-    if (n >= k) best = t;
-    if (n == k) break;
-  }
-  return best;
-}
-
-// Fills sh.cand with the (key, ~index) pairs of the row's k largest values
-// and at most kCand in all; returns their number (fewer than k only where
-// the row has fewer values above -infinity).  own: this thread's maximum.
-template <typename T>
-__device__ int top_candidates(const LogitRow<T> &row, float own, int k, TopShared &sh) {
-  const uint32_t mine = order_key<T>(own), masked = order_key<T>(-INFINITY);
-  uint32_t bound = kth_key<T>(k, [&](uint32_t t) { return __syncthreads_count(mine >= t); });
-  // At least one above the masked values.
-  bound = max(bound, masked + 1);
-  auto push = [&](uint32_t key, int idx, uint32_t least) {
-    if (key >= least) {
-      const int at = atomicAdd(&sh.count, 1);
-      if (at < kCand) sh.cand[at] = ((unsigned long long)key << 32) | (uint32_t)~idx;
-    }
+    __syncthreads();
+    return queued > kQueue ? kCand + 1 : sh.count;
   };
-  auto collect = [&](uint32_t least) {
+  auto restart = [&] {
     __syncthreads();
-    if (threadIdx.x == 0) sh.count = 0;
+    if (threadIdx.x == 0) sh.count = sh.queued = 0;
     __syncthreads();
-    each_value(row, __ballot_sync(0xffffffffu, mine >= least),
-               [&](uint32_t key, int idx) { push(key, idx, least); });
-    __syncthreads();
-    return sh.count;
   };
-  int n = collect(bound);
-  if (n <= kCand) return n;
-  // Many values reach the bound: equal ones (a mask of the type's lowest
-  // value), or large ones that few threads hold.  Take the values above it,
-  // if need be above the exact k-th largest, and then of the values at it
+  // Where too many values reach the bound, equal ones (a mask of the type's
+  // lowest value) or large ones that few threads hold: take the values above
+  // it, if need be above the exact k-th largest, and then of the values at it
   // the first ones in index order.
-  n = collect(bound + 1);
-  if (n > kCand) {
-    bound = kth_key<T>(k, [&](uint32_t t) {
-      __syncthreads();
-      if (threadIdx.x == 0) sh.count = 0;
-      __syncthreads();
-      int c = 0;
-      each_value(row, __ballot_sync(0xffffffffu, mine >= t),
-                 [&](uint32_t key, int) { c += key >= t; });
-      if (c) atomicAdd(&sh.count, c);
-      __syncthreads();
-      return sh.count;
-    });
-    n = collect(bound + 1);  // fewer than k, or k where the search ended early
+  int n = 0;
+  uint32_t least = bound;
+#pragma unroll 1
+  for (int turn = 0;; ++turn) {
+    n = collect(least);
+    if (turn == 0 && n <= kCand) return n;
+    if (n <= kCand) break;
+    if (turn == 1)
+      bound = kth_key(bound, sizeof(T) == 2 ? 0xffffu : 0xffffffffu, k, [&](uint32_t t) {
+        restart();
+        int c = 0;
+        if (mine >= t) {
+          for (int i = slice.v0 + threadIdx.x; i < slice.v1; i += kRowThreads)
+#pragma unroll 1
+            for (int j = 0; j < kVec; ++j) c += order_key<T>(logit_of(row.p[row.index(i) + j])) >= t;
+          if (single >= 0) c += order_key<T>(logit_of(row.p[single])) >= t;
+        }
+        if (c) atomicAdd(&sh.count, c);
+        __syncthreads();
+        return sh.count;
+      });
+    restart();
+    least = bound + 1;
   }
   int need = k - n;
-  constexpr int kVec = LogitRow<T>::kVec;
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  const int tiles = (row.nvec + kThreads - 1) / kThreads;
+  const int tiles = (slice.v1 - slice.v0 + kRowThreads - 1) / kRowThreads;
   for (int tile = -1; tile <= tiles && need > 0; ++tile) {
-    // head values, tiles of one vector a thread, tail values
+    // values before the vectors, tiles of one vector a thread, values after
     uint32_t hit = 0;
     int base = 0;
     if (tile < 0 || tile == tiles) {
-      const int cnt = tile < 0 ? row.head : row.tail;
-      base = (tile < 0 ? 0 : row.tail_index()) + threadIdx.x;
-      hit = (int)threadIdx.x < cnt && order_key<T>(logit_of(row.p[base])) == bound;
+      base = single;
+      hit = (tile < 0 ? threadIdx.x < 8 : threadIdx.x >= 8) && single >= 0 &&
+            order_key<T>(logit_of(row.p[single])) == bound;
     } else {
-      const int i = tile * kThreads + threadIdx.x;
-      if (i < row.nvec && mine >= bound) {
+      const int i = slice.v0 + tile * kRowThreads + threadIdx.x;
+      if (i < slice.v1 && mine >= bound) {
         LogitVec<T> v;
         v.load(row.p + row.index(i));
         float x[kVec];
@@ -164,7 +224,7 @@ __device__ int top_candidates(const LogitRow<T> &row, float own, int k, TopShare
     if (lane == 31) sh.warp_total[wid] = incl;
     __syncthreads();
     int before = incl - c, total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < kRowWarps; ++w) {
       if (w < wid) before += sh.warp_total[w];
       total += sh.warp_total[w];
     }
@@ -181,88 +241,145 @@ __device__ int top_candidates(const LogitRow<T> &row, float own, int k, TopShare
   return n;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, bool kEntropy, bool kTop>
+__global__ void __launch_bounds__(kRowThreads, 5)
 token_logprobs_kernel(const LogprobArgs a) {
-  __shared__ Softmax joined[kThreads / 32];
-  __shared__ TopShared sh;
+  __shared__ Softmax parts[kRowWarps], mine;
+  __shared__ std::conditional_t<kTop, TopShared, int> shared_top;
+  TopShared &sh = reinterpret_cast<TopShared &>(shared_top);  // used with kTop only
   pdl_launch_dependents();
   pdl_wait();
-  for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
+  const uint32_t ctas = cluster_size(), rank = cluster_rank();
+  const int tid = threadIdx.x, lane = tid & 31;
+  for (long long r = blockIdx.x / ctas; r < a.rows; r += gridDim.x / ctas) {
     const LogitRow<T> row(reinterpret_cast<const T *>(a.x) + row_offset(a.sx, r), a.V);
-    const int tid = threadIdx.x;
+    const RowSlice slice(row, ctas, rank);
+    const int single = slice.single(row);
     long long token = -1;
     float xt = 0.f;
-    if (tid == 0 && a.tokens) {
+    if (tid == 0 && rank == 0 && a.tokens) {
       token = a.id64 ? reinterpret_cast<const long long *>(a.tokens)[r]
                      : (long long)reinterpret_cast<const int *>(a.tokens)[r];
       if (token >= 0 && token < a.V) xt = logit_of(row.p[token]);
     }
-    Softmax acc = Softmax::none();
-    for (int i = tid; i < row.nvec; i += kUnroll * kThreads) {
+    WarpSoftmax acc;
+    int i = slice.v0 + (tid & ~31);  // of the warp's first lane: the loops are the warp's
+    for (; i + 31 + (kUnroll - 1) * kRowThreads < slice.v1; i += kUnroll * kRowThreads) {
+      LogitVec<T> v[kUnroll];
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j) v[j].load(row.p + row.index(i + lane + j * kRowThreads));
+      acc.group<T, kUnroll, kEntropy>(v, a.scale);
+    }
+    if (i < slice.v1) {
       LogitVec<T> v[kUnroll];
 #pragma unroll
       for (int j = 0; j < kUnroll; ++j) {
-        const int at = i + j * kThreads;
-        if (at < row.nvec)
+        const int at = i + lane + j * kRowThreads;
+        if (at < slice.v1)
           v[j].load(row.p + row.index(at));
         else
           v[j].fill_masked();
       }
-      acc.group<T, kUnroll, true>(v, a.scale);
+      acc.group<T, kUnroll, kEntropy>(v, a.scale);
     }
-    if (tid < row.head) {
-      const float x = logit_of(row.p[tid]);
-      acc.raise(x, a.scale);
-      acc.take(x, a.scale);
-    }
-    if (tid < row.tail) {
-      const float x = logit_of(row.p[row.tail_index() + tid]);
-      acc.raise(x, a.scale);
-      acc.take(x, a.scale);
-    }
-    const Softmax all = join_cta(acc, a.scale, joined);
+    if (tid < 32) acc.single<kEntropy>(single >= 0 ? logit_of(row.p[single]) : -INFINITY, a.scale);
+    const Softmax all = join_row<kEntropy>(acc.all<kEntropy>(), a.scale, ctas, parts, &mine);
+    if (ctas > 1 && !kTop) cluster_have_read();
     const bool empty = !(all.m > -INFINITY);
     const float lnz = logf(all.s);
-    if (tid == 0) {
-      float lp = 0.f, ent = empty ? 0.f : lnz - 0.6931471805599453f * (all.u / all.s);
+    if (tid == 0 && rank == 0) {
+      float lp = 0.f;
       if (token >= a.V || all.bad)
-        lp = token < 0 ? 0.f : __int_as_float(0x7fffffff);
+        lp = token < 0 ? 0.f : nan_value();
       else if (token >= 0)
         lp = empty ? -INFINITY : (xt - all.m) * a.inv_t - lnz;
-      if (all.bad) ent = __int_as_float(0x7fffffff);
       if (a.logprob) a.logprob[r] = lp;
-      if (a.entropy) a.entropy[r] = ent;
+      if (kEntropy)
+        a.entropy[r] = all.bad ? nan_value() : empty ? 0.f : lnz - 0.6931471805599453f * (all.u / all.s);
     }
-    if (a.top > 0) {
-      const int n = all.bad || empty ? 0 : top_candidates(row, acc.m, a.top, sh);
-      for (int i = tid; i < n; i += kThreads) {
-        const unsigned long long key = sh.cand[i];
-        int rank = 0;
-        for (int j = 0; j < n; ++j) rank += sh.cand[j] > key;
-        if (rank < a.top) {
-          const float x = key_value<T>((uint32_t)(key >> 32));
-          if (a.top_logprob) a.top_logprob[r * a.top + rank] = (x - all.m) * a.inv_t - lnz;
-          if (a.top_id) a.top_id[r * a.top + rank] = (long long)(uint32_t)~(uint32_t)key;
+    if (kTop) {
+      const bool none = all.bad || empty;
+      int n = none ? 0 : top_candidates(row, slice, single, acc.own, a.top, sh);
+      auto put = [&](unsigned long long key, int at) {
+        const float x = key_value<T>((uint32_t)(key >> 32));
+        if (a.top_logprob) a.top_logprob[r * a.top + at] = (x - all.m) * a.inv_t - lnz;
+        if (a.top_id) a.top_id[r * a.top + at] = (long long)(uint32_t)~(uint32_t)key;
+      };
+      for (int c = tid; c < n; c += kRowThreads) {
+        const unsigned long long key = sh.cand[c];
+        int at = 0, j = 0;
+        for (; j + 3 < n; j += 4) {
+          const ulonglong2 p = *reinterpret_cast<const ulonglong2 *>(sh.cand + j);
+          const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(sh.cand + j + 2);
+          at += (p.x > key) + (p.y > key) + (q.x > key) + (q.y > key);
         }
+        for (; j < n; ++j) at += sh.cand[j] > key;
+        if (at >= a.top) continue;
+        if (ctas == 1)
+          put(key, at);
+        else
+          sh.sorted[at] = key;
       }
-      for (int i = n + tid; i < a.top; i += kThreads) {
-        if (a.top_logprob)
-          a.top_logprob[r * a.top + i] = all.bad ? __int_as_float(0x7fffffff) : -INFINITY;
-        if (a.top_id) a.top_id[r * a.top + i] = -1;
+      n = min(n, a.top);
+      if (ctas > 1) {
+        if (tid == 0) sh.listed = n;
+        cluster_sync();
+        // the CTAs' lists, in order, beside one another: a warp for each
+        if (tid >> 5 < (int)ctas) {
+          const uint32_t c = tid >> 5;
+          const int there = (int)cluster_word(&sh.listed, c);
+#pragma unroll
+          for (int j = 0; j < 2 * kMaxTop / 32; ++j)
+            if (lane + 32 * j < 2 * there)
+              reinterpret_cast<uint32_t *>(sh.cand)[2 * kMaxTop * c + lane + 32 * j] =
+                  cluster_word(reinterpret_cast<const uint32_t *>(sh.sorted) + lane + 32 * j, c);
+          if (lane == 0) sh.warp_total[c] = there;
+        }
+        __syncthreads();
+        cluster_have_read();
+        int total = 0;
+        for (uint32_t c = 0; c < ctas; ++c) total += sh.warp_total[c];
+        if (tid < n) {
+          const unsigned long long key = sh.sorted[tid];
+          int at = 0;  // how many of each list come before key: of its own, tid
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            if (c >= (int)ctas) continue;
+            const int there = sh.warp_total[c];
+            int lo = 0;
+#pragma unroll
+            for (int step = kMaxTop; step > 0; step >>= 1)
+              if (lo + step <= there && sh.cand[kMaxTop * c + lo + step - 1] > key) lo += step;
+            at += lo;
+          }
+          if (at < a.top) put(key, at);
+        }
+        n = rank == 0 ? min(total, a.top) : a.top;
+      }
+      for (int c = n + tid; c < a.top; c += kRowThreads) {
+        if (a.top_logprob) a.top_logprob[r * a.top + c] = all.bad ? nan_value() : -INFINITY;
+        if (a.top_id) a.top_id[r * a.top + c] = -1;
       }
     }
-    __syncthreads();  // the shared lists of this row have been read
+    // the shared lists of this row have been read, by the other CTAs too
+    if (ctas > 1) cluster_wait_read();
+    __syncthreads();
   }
+}
+
+template <typename T>
+cudaError_t launch(const LogprobArgs &a, cudaStream_t st) {
+  const int ctas = row_ctas(a.rows, (long long)a.V * sizeof(T), 1LL << 40, 4LL * device_sms());
+  auto kern = a.entropy ? (a.top > 0 ? token_logprobs_kernel<T, true, true> : token_logprobs_kernel<T, true, false>)
+                        : (a.top > 0 ? token_logprobs_kernel<T, false, true> : token_logprobs_kernel<T, false, false>);
+  return launch_rows(kern, a.rows, ctas, kRowThreads, 0, st, a);
 }
 
 }  // namespace
 
 cudaError_t launch_token_logprobs(const LogprobArgs &a, int bf16, cudaStream_t st) {
   if (a.rows == 0) return cudaSuccess;
-  const dim3 grid((unsigned)(a.rows < (1LL << 30) ? a.rows : (1LL << 30)));
-  return bf16 ? launch_k(token_logprobs_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, st, true, a)
-              : launch_k(token_logprobs_kernel<float>, grid, dim3(kThreads), 0, st, true, a);
+  return bf16 ? launch<__nv_bfloat16>(a, st) : launch<float>(a, st);
 }
 
 }  // namespace ret

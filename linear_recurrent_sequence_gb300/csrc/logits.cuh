@@ -80,95 +80,228 @@ struct LogitVec<float> : Elems<float, 4> {
 __device__ __forceinline__ float logit_of(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float logit_of(float x) { return x; }
 
-// Running softmax of the values seen: m the largest, s = sum 2^y and
-// u = sum y 2^y with y = (x - m) log2(e) / T.  The exponent is the scaled
-// difference, so that neither a mask of the type's lowest value nor a large
-// level overflows; below -1000 it is cut (2^y is 0 there, and y 2^y must not
-// become infinity times zero).  A NaN or +infinity sets bad: its row has no
-// distribution.
+__device__ __forceinline__ float redux_max(float x) {  // over the warp; a NaN counts as absent
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ float nan_value() { return __int_as_float(0x7fffffff); }
+constexpr float kFltMax = 3.402823466e38f;
+
+// Softmax of a set of values: m the largest, s = sum 2^y and u = sum y 2^y
+// with y = (x - m) log2(e) / T.  A NaN or +infinity among them sets bad: they
+// have no distribution.
 struct Softmax {
   float m, s, u;
-  bool bad;
+  int bad;
+};
 
-  static __device__ __forceinline__ Softmax none() { return {-INFINITY, 0.f, 0.f, false}; }
+// The softmax of the values that a warp's threads walk over.  m is the same in
+// all lanes (one reduction of the lanes' maxima for each group of vectors), so
+// the sums are moved to a new maximum by a branch that the whole warp takes,
+// and seldom; the sums are packed pairs of a lane's own.
+// The exponent is the scaled difference, so that neither a mask of the type's
+// lowest value nor a large level overflows; below -1000 it is cut where
+// y 2^y is wanted (2^y is 0 there, and y 2^y must not become infinity times zero).
+struct WarpSoftmax {
+  float m = -INFINITY, own = -INFINITY;  // own: the lane's largest value, NaN if it met one
+  float2 s = {0.f, 0.f}, u = {0.f, 0.f};
 
-  // Raises the maximum to at least x.
-  __device__ __forceinline__ void raise(float x, float scale) {
-    if (!(x <= 3.402823466e38f)) {
-      bad = true;
-    } else if (x > m) {
-      if (m > -INFINITY) {
-        const float dy = fmaxf((m - x) * scale, -1000.f), f = ex2(dy);
-        u = fmaf(dy, s, u) * f;
-        s *= f;
-      }
-      m = x;
-    }
-  }
-  __device__ __forceinline__ void add(const Softmax &o, float scale) {
-    bad |= o.bad;
-    Softmax b = o;
-    if (b.m > m) {
-      raise(b.m, scale);
-    } else {
-      b.raise(m, scale);
-    }
-    s += b.s;
-    u += b.u;
-  }
-  // x: at most m.
-  __device__ __forceinline__ void take(float x, float scale) {
-    const float y = fmaxf((x - (m > -INFINITY ? m : 0.f)) * scale, -1000.f), e = ex2(y);
-    s += e;
-    u = fmaf(y, e, u);
-  }
   template <typename T, int N, bool kEntropy>
   __device__ __forceinline__ void group(const LogitVec<T> (&v)[N], float scale) {
-    raise(LogitVec<T>::max_of(v), scale);
+    const float top = LogitVec<T>::max_of(v);
+    own = max_nan(own, top);
+    raise<kEntropy>(redux_max(top), scale);
     const float mm = m > -INFINITY ? -m : 0.f;
     constexpr int kVec = 16 / (int)sizeof(T);
-    float2 s2 = make_float2(0.f, 0.f), u2 = make_float2(0.f, 0.f);
     const float2 mm2 = make_float2(mm, mm), sc2 = make_float2(scale, scale);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       float f[kVec];
       v[i].get(f);
 #pragma unroll
-      for (int j = 0; j < kVec; j += 2) {
-        float2 y = tc::mul2(tc::add2(make_float2(f[j], f[j + 1]), mm2), sc2);
-        if (kEntropy) y = make_float2(fmaxf(y.x, -1000.f), fmaxf(y.y, -1000.f));
-        const float2 e = make_float2(ex2(y.x), ex2(y.y));
-        s2 = tc::add2(s2, e);
-        if (kEntropy) u2 = tc::fma2(y, e, u2);
-      }
+      for (int j = 0; j < kVec; j += 2) take<kEntropy>(make_float2(f[j], f[j + 1]), mm2, sc2);
     }
-    s += s2.x + s2.y;
-    if (kEntropy) u += u2.x + u2.y;
   }
-  __device__ __forceinline__ void add_lanes(float scale) {
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) {
-      Softmax o;
-      o.m = __shfl_xor_sync(0xffffffffu, m, k);
-      o.s = __shfl_xor_sync(0xffffffffu, s, k);
-      o.u = __shfl_xor_sync(0xffffffffu, u, k);
-      o.bad = __shfl_xor_sync(0xffffffffu, (int)bad, k) != 0;
-      add(o, scale);
+  // One value a lane (-infinity: none).
+  template <bool kEntropy>
+  __device__ __forceinline__ void single(float x, float scale) {
+    own = max_nan(own, x);
+    raise<kEntropy>(redux_max(x), scale);
+    const float mm = m > -INFINITY ? -m : 0.f;
+    take<kEntropy>(make_float2(x, -INFINITY), make_float2(mm, mm), make_float2(scale, scale));
+  }
+  // The warp's result, in all lanes.
+  template <bool kEntropy>
+  __device__ __forceinline__ Softmax all() const {
+    Softmax r;
+    r.m = m;
+    r.s = warp_sum(s.x + s.y);
+    r.u = kEntropy ? warp_sum(u.x + u.y) : 0.f;
+    r.bad = __any_sync(0xffffffffu, !(own <= kFltMax));
+    return r;
+  }
+
+ private:
+  template <bool kEntropy>
+  __device__ __forceinline__ void raise(float top, float scale) {
+    if (!(top > m)) return;
+    if (m > -INFINITY) {
+      const float dy = fmaxf((m - top) * scale, -1000.f), f = ex2(dy);
+      const float2 f2 = make_float2(f, f);
+      if (kEntropy) u = tc::mul2(tc::fma2(make_float2(dy, dy), s, u), f2);
+      s = tc::mul2(s, f2);
     }
+    m = top;
+  }
+  template <bool kEntropy>
+  __device__ __forceinline__ void take(float2 x, float2 mm, float2 scale) {
+    float2 y = tc::mul2(tc::add2(x, mm), scale);
+    if (kEntropy) y = make_float2(fmaxf(y.x, -1000.f), fmaxf(y.y, -1000.f));
+    const float2 e = make_float2(ex2(y.x), ex2(y.y));
+    s = tc::add2(s, e);
+    if (kEntropy) u = tc::fma2(y, e, u);
   }
 };
 
-// Joins the CTA's threads' sums (buf: one entry per warp); the result is the
-// same in every thread.  Joining two lanes gives both the same bits (the
-// operands only change sides).
-__device__ __forceinline__ Softmax join_cta(Softmax a, float scale, Softmax *buf) {
-  a.add_lanes(scale);
-  const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) buf[threadIdx.x >> 5] = a;
+// Joins up to eight parts, one in each of lanes 0..7 (and again in every
+// eight lanes after them; an absent part has m = -infinity and zeros).
+template <bool kEntropy>
+__device__ __forceinline__ Softmax join_eight(const Softmax &p, float scale) {
+  Softmax r;
+  r.m = redux_max(p.m);
+  const bool some = p.m > -INFINITY;
+  const float dy = some ? fmaxf((p.m - r.m) * scale, -1000.f) : 0.f, f = some ? ex2(dy) : 0.f;
+  // (no contraction: the same bits wherever this is inlined)
+  r.s = __fmul_rn(p.s, f);
+  r.u = kEntropy ? __fmul_rn(fmaf(dy, p.s, p.u), f) : 0.f;
+#pragma unroll
+  for (int k = 4; k > 0; k >>= 1) {
+    r.s += __shfl_xor_sync(0xffffffffu, r.s, k);
+    if (kEntropy) r.u += __shfl_xor_sync(0xffffffffu, r.u, k);
+  }
+  r.bad = __any_sync(0xffffffffu, p.bad);
+  return r;
+}
+
+// ------------------------------------------------------------ clusters
+// A row may be shared by the CTAs of a cluster, a slice of vectors each.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Halves of a barrier after which this CTA's shared memory is its own again:
+// every CTA arrives when it has read the others', and waits before it writes
+// what they read (or ends).  It orders no memory, so it does not wait for
+// the stores of results.
+__device__ __forceinline__ void cluster_have_read() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait_read() {
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+// A 32-bit word of CTA `rank`'s shared memory, at the place of `local` in this one's.
+__device__ __forceinline__ uint32_t cluster_word(const void *local, uint32_t rank) {
+  uint32_t at, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(tc::smem_u32(local)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+
+constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
+
+// Joins the CTA's warps, and the cluster's CTAs where there are several: the
+// same result in every thread (warps past kRowWarps bring nothing).  parts: shared, [kRowWarps]; mine: shared, one.
+// In a cluster the caller then has to arrive and wait (cluster_have_read,
+// cluster_wait_read) before `mine` is written again.
+template <bool kEntropy>
+__device__ __forceinline__ Softmax join_row(const Softmax &warp, float scale, uint32_t ctas,
+                                            Softmax *parts, Softmax *mine) {
+  const int lane = threadIdx.x & 31;
+  if (lane == 0 && threadIdx.x < kRowThreads) parts[threadIdx.x >> 5] = warp;
   __syncthreads();
-  Softmax b = lane < nw ? buf[lane] : Softmax::none();
-  b.add_lanes(scale);
-  return b;
+  Softmax r = join_eight<kEntropy>(parts[lane & (kRowWarps - 1)], scale);
+  if (ctas == 1) return r;
+  if (threadIdx.x == 0) *mine = r;
+  cluster_sync();
+  Softmax p = {-INFINITY, 0.f, 0.f, 0};
+  const uint32_t c = lane & 7;
+  if (c < ctas) {
+    p.m = __uint_as_float(cluster_word(&mine->m, c));
+    p.s = __uint_as_float(cluster_word(&mine->s, c));
+    p.u = __uint_as_float(cluster_word(&mine->u, c));
+    p.bad = (int)cluster_word(&mine->bad, c);
+  }
+  return join_eight<kEntropy>(p, scale);
+}
+
+// The vectors of a row that this CTA walks over, and whether it also has the
+// values before (first) and after (last) them: lanes 0..7 and 8..15 of warp 0
+// have one of those each.
+struct RowSlice {
+  int v0, v1;
+  bool first, last;
+  template <typename T>
+  __device__ __forceinline__ RowSlice(const LogitRow<T> &row, uint32_t ctas, uint32_t rank) {
+    const int each = (row.nvec + (int)ctas - 1) / (int)ctas;
+    v0 = min((int)rank * each, row.nvec);
+    v1 = min(v0 + each, row.nvec);
+    first = rank == 0;
+    last = rank + 1 == ctas;
+  }
+  template <typename T>
+  __device__ __forceinline__ bool has(const LogitRow<T> &row, int i) const {
+    if (i < row.head) return first;
+    if (i >= row.tail_index()) return last;
+    const int v = (i - row.head) / LogitRow<T>::kVec;
+    return v >= v0 && v < v1;
+  }
+  // Index of the single value of this thread, -1 if it has none.
+  template <typename T>
+  __device__ __forceinline__ int single(const LogitRow<T> &row) const {
+    const int t = threadIdx.x;
+    if (t < 8) return first && t < row.head ? t : -1;
+    return t < 16 && last && t - 8 < row.tail ? row.tail_index() + t - 8 : -1;
+  }
+};
+
+// CTAs a row: as many as bring a slice down to `most` bytes, and more while
+// all of them fit the SMs at once (`slots`) and slices stay above 8 KB.
+inline int row_ctas(long long rows, long long row_bytes, long long most, long long slots) {
+  int c = 1;
+  while (c < 8 && (row_bytes / c > most || (rows * 2 * c <= slots && row_bytes / (2 * c) >= 8 * 1024)))
+    c *= 2;
+  return c;
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_rows(void (*kern)(KArgs...), long long rows, int ctas, int threads, size_t smem,
+                        cudaStream_t st, Args &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  const long long most = (1LL << 30) / ctas;
+  cfg.gridDim = dim3((unsigned)((rows < most ? rows : most) * ctas));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = ctas > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
 }  // namespace ret

@@ -8,6 +8,7 @@ fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -187,7 +188,14 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
+# The current stream's handle without a Stream object around it, where this
+# torch has that (3 us less per call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
+    if stream is None and _raw_stream is not None:
+        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
 
@@ -544,18 +552,17 @@ def gemm_bf16(A, B, out=None, workspace=None, stream=None):
     return out
 
 
-def _row_strides(name, lead, *tensors):
-    """(n0, n1) and each tensor's two element strides for rows along the last
-    dimension.  ``lead`` is their common shape without it; more than two
+def _row_strides(name, shape, *strides):
+    """(n0, n1) and the two element strides of each tensor for rows along the
+    last dimension, from their common shape and their strides.  More than two
     leading dimensions are folded where every tensor's strides allow it."""
-    for t in tensors:
-        if t.shape[:-1] != lead:
-            raise ValueError(f"{name}: leading shapes {tuple(lead)} and {tuple(t.shape[:-1])} differ")
-        if t.stride(-1) != 1 and t.shape[-1] > 1:
+    lead = shape[:-1]
+    for s in strides:
+        if s[-1] != 1 and shape[-1] > 1:
             raise ValueError(f"{name}: the last dimension must be contiguous")
-    dims = [(n, [t.stride(i) for t in tensors]) for i, n in enumerate(lead) if n != 1]
-    if any(n == 0 for n in lead):
-        return 0, 0, [(0, 0)] * len(tensors)
+    if 0 in lead:
+        return 0, 0, [(0, 0)] * len(strides)
+    dims = [(n, [s[i] for s in strides]) for i, n in enumerate(lead) if n != 1]
     i = 0
     while len(dims) > 2 and i + 1 < len(dims):
         (n0, s0), (n1, s1) = dims[i], dims[i + 1]
@@ -565,7 +572,7 @@ def _row_strides(name, lead, *tensors):
             i += 1
     if len(dims) > 2:
         raise ValueError(f"{name}: rows of shape {tuple(lead)} do not fold into two strides")
-    dims = [(1, [0] * len(tensors))] * (2 - len(dims)) + dims
+    dims = [(1, [0] * len(strides))] * (2 - len(dims)) + dims
     return dims[0][0], dims[1][0], list(zip(dims[0][1], dims[1][1]))
 
 
@@ -588,9 +595,15 @@ def _ptrs(*tensors):
             for t in tensors]
 
 
-def _ln_desc(x, eps, dy, out):
-    n0, n1, st = _row_strides("layernorm", x.shape[:-1], x, out if dy is None else dy, out)
-    return LayerNormDesc(n0, n1, x.shape[-1], _dtype_code(x.dtype), eps, *st)
+# The descriptors below depend on shapes, strides and options alone, and a
+# program calls with the same ones over and over: building one costs 5 us,
+# finding it here less than one.
+@functools.lru_cache(maxsize=256)
+def _ln_desc(shape, dtype, eps, sx, sg, so):
+    """(descriptor, workspace bytes of the backward)."""
+    n0, n1, st = _row_strides("layernorm", shape, sx, sg, so)
+    d = LayerNormDesc(n0, n1, shape[-1], _dtype_code(dtype), eps, *st)
+    return d, int(lib.retnet_layernorm_bwd_workspace_size(ctypes.byref(d)))
 
 
 def layernorm_fwd(x, w=None, b=None, *, eps=1e-5, out=None, mean=None, rstd=None, stream=None):
@@ -598,17 +611,22 @@ def layernorm_fwd(x, w=None, b=None, *, eps=1e-5, out=None, mean=None, rstd=None
     strides): y = (x - mean) rstd w + b with fp32 gains w and biases b (None: 1
     and 0).  Returns (y, mean, rstd); mean and rstd, fp32 of x.shape[:-1], are
     what layernorm_bwd takes.  out may be x itself."""
-    lead, d = x.shape[:-1], x.shape[-1:]
+    shape = x.shape
+    lead, d = shape[:-1], shape[-1:]
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    else:
+        _like("out", out, x)
     if mean is None:
         mean = torch.empty(lead, dtype=torch.float32, device=x.device)
     if rstd is None:
         rstd = torch.empty(lead, dtype=torch.float32, device=x.device)
-    _like("out", out, x)
-    for name, t, shape in (("w", w, d), ("b", b, d), ("mean", mean, lead), ("rstd", rstd, lead)):
-        _f32(name, t, shape)
-    desc = _ln_desc(x, eps, None, out)
+    _f32("w", w, d)
+    _f32("b", b, d)
+    _f32("mean", mean, lead)
+    _f32("rstd", rstd, lead)
+    so = out.stride()
+    desc, _ = _ln_desc(shape, x.dtype, eps, x.stride(), so, so)
     st = lib.retnet_layernorm_fwd(ctypes.byref(desc), *_ptrs(x, w, b, out, mean, rstd),
                                   _stream(stream))
     _check(st, "retnet_layernorm_fwd")
@@ -619,22 +637,25 @@ def layernorm_bwd(x, dy, w, mean, rstd, *, dx=None, dw=None, db=None, workspace=
     """Gradients of layernorm_fwd: returns (dx, dw, db), dx in x's dtype, dw
     and db fp32 (w may be None; dw and db are the sums all the same).  The sums
     over the rows are added in a fixed order.  dx may be x or dy itself."""
-    lead, d = x.shape[:-1], x.shape[-1:]
+    shape = x.shape
+    lead, d = shape[:-1], shape[-1:]
     if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dx = torch.empty(shape, dtype=x.dtype, device=x.device)
+    else:
+        _like("dx", dx, x)
     if dw is None:
         dw = torch.empty(d, dtype=torch.float32, device=x.device)
     if db is None:
         db = torch.empty(d, dtype=torch.float32, device=x.device)
     _like("dy", dy, x)
-    _like("dx", dx, x)
-    for name, t, shape in (("w", w, d), ("mean", mean, lead), ("rstd", rstd, lead), ("dw", dw, d),
-                           ("db", db, d)):
-        _f32(name, t, shape)
-    desc = _ln_desc(x, 0.0, dy, dx)
+    _f32("w", w, d)
+    _f32("mean", mean, lead)
+    _f32("rstd", rstd, lead)
+    _f32("dw", dw, d)
+    _f32("db", db, d)
+    desc, nbytes = _ln_desc(shape, x.dtype, 0.0, x.stride(), dy.stride(), dx.stride())
     if workspace is None:
-        workspace = torch.empty(lib.retnet_layernorm_bwd_workspace_size(ctypes.byref(desc)),
-                                dtype=torch.uint8, device=x.device)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
     st = lib.retnet_layernorm_bwd(ctypes.byref(desc),
                                   *_ptrs(x, dy, w, mean, rstd, dx, dw, db, workspace),
                                   workspace.numel(), _stream(stream))
@@ -644,11 +665,17 @@ def layernorm_bwd(x, dy, w, mean, rstd, *, dx=None, dw=None, db=None, workspace=
 
 def _ids(name, t, shape):
     """Bytes of an id of a contiguous int32 or int64 tensor of the given shape."""
-    if t.dtype not in (torch.int32, torch.int64):
+    if t.dtype is not torch.int64 and t.dtype is not torch.int32:
         raise TypeError(f"{name} must be int32 or int64, got {t.dtype}")
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}")
-    return t.element_size()
+    return 8 if t.dtype is torch.int64 else 4
+
+
+@functools.lru_cache(maxsize=256)
+def _logits_desc(shape, dtype, temperature, top, id_bytes, tail, sx, sd):
+    n0, n1, s = _row_strides("logits", shape, sx, sd)
+    return LogitsDesc(n0, n1, shape[-1], _dtype_code(dtype), temperature, top, id_bytes, tail, *s)
 
 
 def token_logprobs(logits, tokens=None, *, top=0, temperature=1.0, logprob=None, entropy=None,
@@ -660,7 +687,8 @@ def token_logprobs(logits, tokens=None, *, top=0, temperature=1.0, logprob=None,
     (logprob, entropy, top_logprobs, top_ids); logprob is None without tokens
     and the last two are None for top=0.  A logit of -inf is a masked token; the
     missing alternatives of a row have id -1."""
-    lead, V, dev = logits.shape[:-1], logits.shape[-1], logits.device
+    shape, dev = logits.shape, logits.device
+    lead = shape[:-1]
     id_bytes = 8
     if tokens is not None:
         id_bytes = _ids("tokens", tokens, lead)
@@ -671,20 +699,20 @@ def token_logprobs(logits, tokens=None, *, top=0, temperature=1.0, logprob=None,
     if entropy is None:
         entropy = torch.empty(lead, dtype=torch.float32, device=dev)
     if top:
-        shape = (*lead, top)
+        tops = (*lead, top)
         if top_logprobs is None:
-            top_logprobs = torch.empty(shape, dtype=torch.float32, device=dev)
+            top_logprobs = torch.empty(tops, dtype=torch.float32, device=dev)
         if top_ids is None:
-            top_ids = torch.empty(shape, dtype=torch.int64, device=dev)
-        if _ids("top_ids", top_ids, shape) != 8:
+            top_ids = torch.empty(tops, dtype=torch.int64, device=dev)
+        if _ids("top_ids", top_ids, tops) != 8:
             raise TypeError("top_ids must be int64")
-        _f32("top_logprobs", top_logprobs, shape)
+        _f32("top_logprobs", top_logprobs, tops)
     else:
         top_logprobs = top_ids = None
     _f32("logprob", logprob, lead)
     _f32("entropy", entropy, lead)
-    n0, n1, s = _row_strides("logits", lead, logits)
-    d = LogitsDesc(n0, n1, V, _dtype_code(logits.dtype), temperature, top, id_bytes, 0, s[0], s[0])
+    s = logits.stride()
+    d = _logits_desc(shape, logits.dtype, temperature, top, id_bytes, False, s, s)
     st = lib.retnet_token_logprobs(
         ctypes.byref(d), *_ptrs(logits, tokens, logprob, entropy, top_logprobs, top_ids),
         _stream(stream))
@@ -693,12 +721,13 @@ def token_logprobs(logits, tokens=None, *, top=0, temperature=1.0, logprob=None,
 
 
 def _distill_desc(student, ids, values, temperature, tail, dstudent):
-    lead, top = student.shape[:-1], ids.shape[-1]
-    id_bytes = _ids("ids", ids, (*lead, top))
-    _f32("values", values, (*lead, top))
-    n0, n1, s = _row_strides("student", lead, student, student if dstudent is None else dstudent)
-    return LogitsDesc(n0, n1, student.shape[-1], _dtype_code(student.dtype), temperature, top,
-                      id_bytes, tail, s[0], s[1])
+    shape, top = student.shape, ids.shape[-1]
+    lists = (*shape[:-1], top)
+    id_bytes = _ids("ids", ids, lists)
+    _f32("values", values, lists)
+    s = student.stride()
+    return _logits_desc(shape, student.dtype, temperature, top, id_bytes, bool(tail), s,
+                        s if dstudent is None else dstudent.stride())
 
 
 def distill_fwd(student, ids, values, *, temperature=1.0, tail=False, loss=None, stats=None,
@@ -712,12 +741,13 @@ def distill_fwd(student, ids, values, *, temperature=1.0, tail=False, loss=None,
     the loss times temperature^2, fp32 of student.shape[:-1], and what
     distill_bwd needs, [.., 2]."""
     lead = student.shape[:-1]
+    pairs = (*lead, 2)
     if loss is None:
         loss = torch.empty(lead, dtype=torch.float32, device=student.device)
     if stats is None:
-        stats = torch.empty((*lead, 2), dtype=torch.float32, device=student.device)
+        stats = torch.empty(pairs, dtype=torch.float32, device=student.device)
     _f32("loss", loss, lead)
-    _f32("stats", stats, (*lead, 2))
+    _f32("stats", stats, pairs)
     d = _distill_desc(student, ids, values, temperature, tail, None)
     st = lib.retnet_distill_fwd(ctypes.byref(d), *_ptrs(student, ids, values, loss, stats),
                                 _stream(stream))
@@ -733,7 +763,8 @@ def distill_bwd(student, ids, values, weight, stats, *, temperature=1.0, tail=Fa
     lead = student.shape[:-1]
     if dstudent is None:
         dstudent = torch.empty(student.shape, dtype=student.dtype, device=student.device)
-    _like("dstudent", dstudent, student)
+    else:
+        _like("dstudent", dstudent, student)
     _f32("weight", weight, lead)
     _f32("stats", stats, (*lead, 2))
     d = _distill_desc(student, ids, values, temperature, tail, dstudent)
@@ -753,7 +784,8 @@ def distill_step(student, ids, values, weight=None, *, temperature=1.0, tail=Fal
         loss = torch.empty(lead, dtype=torch.float32, device=student.device)
     if dstudent is None:
         dstudent = torch.empty(student.shape, dtype=student.dtype, device=student.device)
-    _like("dstudent", dstudent, student)
+    else:
+        _like("dstudent", dstudent, student)
     _f32("weight", weight, lead)
     _f32("loss", loss, lead)
     d = _distill_desc(student, ids, values, temperature, tail, dstudent)
