@@ -26,6 +26,7 @@ namespace {
 constexpr int kUnroll = 4;
 constexpr int kMaxTop = RETNET_MAX_TOP;
 
+constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
 constexpr int kThreads = kRowThreads + 32;  // and the list's warp
 constexpr int kPer = kMaxTop / 32;          // its entries a lane: lane + 32 i
 
@@ -501,6 +502,7 @@ distill_kernel(const DistillArgs a, int words) {
             for (int e = 0; e < kVec; ++e)
               if (hit >> e & 1u) v.mask(e);
         };
+        const Scale sc(a.scale);
         WarpSoftmax acc;
         // One group of vectors, from slots n.. (kStaged), from `ahead` or from the row.
         auto group = [&](int n, bool first) {
@@ -522,7 +524,7 @@ distill_kernel(const DistillArgs a, int words) {
 #pragma unroll
           for (int j = 0; j < kUnroll; ++j)
             if (i + lane + j * kRowThreads < slice.v1) hide(i + lane + j * kRowThreads, v[j]);
-          acc.group<T, kUnroll, false>(v, a.scale);
+          acc.group<T, kUnroll, false>(v, sc);
           i += kUnroll * kRowThreads;
         };
         if (kStaged) {
@@ -541,14 +543,14 @@ distill_kernel(const DistillArgs a, int words) {
         if (tid < 32) {
           const int single = slice.single(row), at = single - row.head + kVec;
           const bool counts = single >= 0 && !(bits[at >> 5] >> (at & 31) & 1u);
-          acc.single<false>(counts ? logit_of(row.p[single]) : -INFINITY, a.scale);
+          acc.single<false>(counts ? logit_of(row.p[single]) : -INFINITY, sc);
         }
-        part = acc.all<false>();
+        part = acc.all<false>(sc);
       }
     }
     RowConstants k;
     if (kFwd) {
-      const Softmax rest = join_row<false>(part, a.scale, ctas, sh.parts, &sh.mine);
+      const Softmax rest = join_row<false, kRowWarps>(part, a.scale, ctas, sh.parts, &sh.mine);
       if (ctas > 1) cluster_have_read();
       if (kBwd || !walks) k = row_constants(a, weight, rest, sh);
       if (!walks && rank == 0) row_loss(a, r, rest, k, sh);

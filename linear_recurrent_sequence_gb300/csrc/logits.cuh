@@ -39,6 +39,15 @@ struct LogitVec;
 template <>
 struct LogitVec<__nv_bfloat16> : Elems<__nv_bfloat16, 8> {
   __device__ __forceinline__ void fill_masked() { raw = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
+  __device__ __forceinline__ void floor_at(float x) {
+    const __nv_bfloat162 f = __float2bfloat162_rn(x);
+    uint32_t *w = &raw.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]), f);
+      w[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+  }
   __device__ __forceinline__ void mask(int j) {
     uint32_t *w = &raw.x;
 #pragma unroll
@@ -61,6 +70,9 @@ struct LogitVec<__nv_bfloat16> : Elems<__nv_bfloat16, 8> {
 template <>
 struct LogitVec<float> : Elems<float, 4> {
   __device__ __forceinline__ void fill_masked() { raw = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); }
+  __device__ __forceinline__ void floor_at(float x) {
+    raw = make_float4(fmaxf(raw.x, x), fmaxf(raw.y, x), fmaxf(raw.z, x), fmaxf(raw.w, x));
+  }
   __device__ __forceinline__ void mask(int j) {
     if (j == 0) raw.x = -INFINITY;
     if (j == 1) raw.y = -INFINITY;
@@ -97,48 +109,77 @@ struct Softmax {
   int bad;
 };
 
+// The temperature's scale log2(e) / T and what follows from it: scaled logits
+// up to `high` in size keep y = x scale - m scale well inside fp32, and `low`
+// stands for a logit below it (its 2^y is 0, and y 2^y is not infinity times
+// zero as it would be for -infinity).
+struct Scale {
+  float scale, high, low;
+  __device__ __forceinline__ explicit Scale(float sc)
+      : scale(sc), high(1e30f / fmaxf(sc, 1.f)), low(-1e36f / fmaxf(sc, 1.f)) {}
+};
+
 // The softmax of the values that a warp's threads walk over.  m is the same in
 // all lanes (one reduction of the lanes' maxima for each group of vectors), so
 // the sums are moved to a new maximum by a branch that the whole warp takes,
 // and seldom; the sums are packed pairs of a lane's own.
-// The exponent is the scaled difference, so that neither a mask of the type's
-// lowest value nor a large level overflows; below -1000 it is cut where
-// y 2^y is wanted (2^y is 0 there, and y 2^y must not become infinity times zero).
+// One fused multiply-add gives a pair's exponents: they are relative to the
+// rounded product m scale, which all() corrects.  Where the maximum is beyond
+// `high` (a row masked throughout with the type's lowest value) the product
+// would overflow, and the difference is taken first.
 struct WarpSoftmax {
   float m = -INFINITY, own = -INFINITY;  // own: the lane's largest value, NaN if it met one
   float2 s = {0.f, 0.f}, u = {0.f, 0.f};
 
   template <typename T, int N, bool kEntropy>
-  __device__ __forceinline__ void group(const LogitVec<T> (&v)[N], float scale) {
+  __device__ __forceinline__ void group(const LogitVec<T> (&v)[N], const Scale &c) {
     const float top = LogitVec<T>::max_of(v);
     own = max_nan(own, top);
-    raise<kEntropy>(redux_max(top), scale);
-    const float mm = m > -INFINITY ? -m : 0.f;
+    raise<kEntropy>(redux_max(top), c.scale);
     constexpr int kVec = 16 / (int)sizeof(T);
-    const float2 mm2 = make_float2(mm, mm), sc2 = make_float2(scale, scale);
+    if (fabsf(m) <= c.high) {
+      const float2 sc2 = make_float2(c.scale, c.scale), mm2 = make_float2(-__fmul_rn(m, c.scale), -__fmul_rn(m, c.scale));
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      float f[kVec];
-      v[i].get(f);
+      for (int i = 0; i < N; ++i) {
+        LogitVec<T> w = v[i];
+        if (kEntropy) w.floor_at(c.low);
+        float f[kVec];
+        w.get(f);
 #pragma unroll
-      for (int j = 0; j < kVec; j += 2) take<kEntropy>(make_float2(f[j], f[j + 1]), mm2, sc2);
+        for (int j = 0; j < kVec; j += 2) take<kEntropy>(tc::fma2(make_float2(f[j], f[j + 1]), sc2, mm2));
+      }
+    } else if (m > -INFINITY) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        float f[kVec];
+        v[i].get(f);
+#pragma unroll
+        for (int j = 0; j < kVec; j += 2) take_far<kEntropy>(f[j], f[j + 1], c.scale);
+      }
     }
   }
   // One value a lane (-infinity: none).
   template <bool kEntropy>
-  __device__ __forceinline__ void single(float x, float scale) {
+  __device__ __forceinline__ void single(float x, const Scale &c) {
     own = max_nan(own, x);
-    raise<kEntropy>(redux_max(x), scale);
-    const float mm = m > -INFINITY ? -m : 0.f;
-    take<kEntropy>(make_float2(x, -INFINITY), make_float2(mm, mm), make_float2(scale, scale));
+    raise<kEntropy>(redux_max(x), c.scale);
+    if (fabsf(m) <= c.high)
+      take<kEntropy>(make_float2(fmaf(fmaxf(x, c.low), c.scale, -__fmul_rn(m, c.scale)), -1000.f));
+    else if (m > -INFINITY)
+      take_far<kEntropy>(x, -INFINITY, c.scale);
   }
   // The warp's result, in all lanes.
   template <bool kEntropy>
-  __device__ __forceinline__ Softmax all() const {
+  __device__ __forceinline__ Softmax all(const Scale &c) const {
     Softmax r;
     r.m = m;
     r.s = warp_sum(s.x + s.y);
     r.u = kEntropy ? warp_sum(u.x + u.y) : 0.f;
+    if (fabsf(m) <= c.high) {
+      const float off = fmaf(m, c.scale, -__fmul_rn(m, c.scale)), f = ex2(-off);
+      r.u = __fmul_rn(fmaf(-off, r.s, r.u), f);
+      r.s = __fmul_rn(r.s, f);
+    }
     r.bad = __any_sync(0xffffffffu, !(own <= kFltMax));
     return r;
   }
@@ -148,7 +189,8 @@ struct WarpSoftmax {
   __device__ __forceinline__ void raise(float top, float scale) {
     if (!(top > m)) return;
     if (m > -INFINITY) {
-      const float dy = fmaxf((m - top) * scale, -1000.f), f = ex2(dy);
+      // (a difference of infinities is one of values far apart: -1000 too)
+      const float dy = fmaxf(__fsub_rn(__fmul_rn(m, scale), __fmul_rn(top, scale)), -1000.f), f = ex2(dy);
       const float2 f2 = make_float2(f, f);
       if (kEntropy) u = tc::mul2(tc::fma2(make_float2(dy, dy), s, u), f2);
       s = tc::mul2(s, f2);
@@ -156,12 +198,14 @@ struct WarpSoftmax {
     m = top;
   }
   template <bool kEntropy>
-  __device__ __forceinline__ void take(float2 x, float2 mm, float2 scale) {
-    float2 y = tc::mul2(tc::add2(x, mm), scale);
-    if (kEntropy) y = make_float2(fmaxf(y.x, -1000.f), fmaxf(y.y, -1000.f));
+  __device__ __forceinline__ void take(float2 y) {
     const float2 e = make_float2(ex2(y.x), ex2(y.y));
     s = tc::add2(s, e);
     if (kEntropy) u = tc::fma2(y, e, u);
+  }
+  template <bool kEntropy>
+  __device__ __forceinline__ void take_far(float a, float b, float scale) {
+    take<kEntropy>(make_float2(fmaxf((a - m) * scale, -1000.f), fmaxf((b - m) * scale, -1000.f)));
   }
 };
 
@@ -218,19 +262,20 @@ __device__ __forceinline__ uint32_t cluster_word(const void *local, uint32_t ran
   return v;
 }
 
-constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
-
-// Joins the CTA's warps, and the cluster's CTAs where there are several: the
-// same result in every thread (warps past kRowWarps bring nothing).  parts: shared, [kRowWarps]; mine: shared, one.
+// Joins the CTA's first kWarps (at most 8) warps, and the cluster's CTAs where
+// there are several: the same result in every thread.  parts: shared,
+// [kWarps]; mine: shared, one.
 // In a cluster the caller then has to arrive and wait (cluster_have_read,
 // cluster_wait_read) before `mine` is written again.
-template <bool kEntropy>
+template <bool kEntropy, int kWarps>
 __device__ __forceinline__ Softmax join_row(const Softmax &warp, float scale, uint32_t ctas,
                                             Softmax *parts, Softmax *mine) {
   const int lane = threadIdx.x & 31;
-  if (lane == 0 && threadIdx.x < kRowThreads) parts[threadIdx.x >> 5] = warp;
+  if (lane == 0 && threadIdx.x < kWarps * 32) parts[threadIdx.x >> 5] = warp;
   __syncthreads();
-  Softmax r = join_eight<kEntropy>(parts[lane & (kRowWarps - 1)], scale);
+  Softmax r = {-INFINITY, 0.f, 0.f, 0};
+  if ((lane & 7) < kWarps) r = parts[lane & 7];
+  r = join_eight<kEntropy>(r, scale);
   if (ctas == 1) return r;
   if (threadIdx.x == 0) *mine = r;
   cluster_sync();

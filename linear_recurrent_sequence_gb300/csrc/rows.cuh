@@ -11,7 +11,8 @@ namespace ret {
 // Element offset of row r of an n0 x n1 set of rows.
 __device__ __forceinline__ long long row_offset(const RowSet &s, long long r) {
   if (s.n0 == 1) return r * s.s1;
-  const long long i = r / s.n1;
+  // (a 64-bit division costs over a hundred instructions)
+  const long long i = (r | s.n1) >> 32 ? r / s.n1 : (long long)((uint32_t)r / (uint32_t)s.n1);
   return i * s.s0 + (r - i * s.n1) * s.s1;
 }
 
