@@ -1372,7 +1372,7 @@ ret_status retnet_layernorm_bwd(const retnet_layernorm_desc *d, const void *x, c
   if (rs != RET_OK) return rs;
   LnArgs a = ln_args(d);
   cudaStream_t st = (cudaStream_t)stream;
-  float *stat = at<float>(ws, 0), *part = stat + 2 * (size_t)a.rows;
+  float *part = at<float>(ws, 0);
   const bool bf16 = d->dtype == RET_BF16, sums = dw || db;
   int groups = 0;
   if (a.rows > 0) {
@@ -1388,6 +1388,7 @@ ret_status retnet_layernorm_bwd(const retnet_layernorm_desc *d, const void *x, c
     a.rstd = const_cast<float *>(rstd);
     const LnBwdPlan pl = layernorm_bwd_plan(a, bf16);
     groups = pl.groups;
+    float *stat = part + (size_t)groups * 2 * a.d;
     if (pl.two_pass)
       RET_CUDA(RET_TIMED_LAUNCH(kKLnBwdStat, st, launch_layernorm_bwd_stat(a, bf16, pl, stat, st)));
     RET_CUDA(RET_TIMED_LAUNCH(kKLnBwd, st, launch_layernorm_bwd(a, bf16, pl, stat, sums ? part : nullptr, st)));

@@ -301,10 +301,10 @@ struct RestGradient {
   __device__ __forceinline__ float2 at(float2 x) const {
     const float2 s2 = make_float2(scale, scale);
     const float2 q = tc::fma2(tc::add2(x, make_float2(a, a)), s2, make_float2(b, b));
-    float2 g = make_float2(c * ex2(q.x), c * ex2(q.y));
+    float2 g = tc::mul2(make_float2(c, c), make_float2(ex2(q.x), ex2(q.y)));
     if (kTail) {
       const float2 o = tc::fma2(tc::add2(x, make_float2(a_rest, a_rest)), s2, make_float2(b_rest, b_rest));
-      g = make_float2(fmaf(c_rest, ex2(o.x), g.x), fmaf(c_rest, ex2(o.y), g.y));
+      g = tc::fma2(make_float2(c_rest, c_rest), make_float2(ex2(o.x), ex2(o.y)), g);
     }
     return g;
   }
