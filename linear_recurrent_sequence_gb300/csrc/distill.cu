@@ -315,6 +315,10 @@ struct RestGradient {
 // kGroups groups of kUnroll vectors a thread.
 constexpr int kGroups = 4;
 constexpr int kSliceBytes = kGroups * kUnroll * kRowThreads * 16;
+// Shared memory of a CTA of which three fit an SM.  (1500 x 131072 bf16, whose
+// bits would leave two: 198 us with the second reading from L2, 209 staged;
+// 4096 x 65536: 262 and 208.)
+constexpr size_t kStagedMost = 73 * 1024;
 
 template <typename T>
 struct StagedSlice {
@@ -441,7 +445,7 @@ __device__ __forceinline__ void list_ready() {
 __device__ __forceinline__ void wait_list() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
 
 template <typename T, int kWhat, bool kTail, bool kStaged>
-__global__ void __launch_bounds__(kThreads, kStaged ? 3 : 4)
+__global__ void __launch_bounds__(kThreads, kStaged ? 3 : kWhat == kDistillFwd ? 6 : 4)
 distill_kernel(const DistillArgs a, int words) {
   constexpr int kVec = LogitRow<T>::kVec;
   constexpr bool kFwd = (kWhat & kDistillFwd) != 0, kBwd = (kWhat & kDistillBwd) != 0;
@@ -613,8 +617,8 @@ cudaError_t launch(const DistillArgs &a, cudaStream_t st) {
                       (kWhat == kDistillBwd ? 4LL : 3LL) * sms);
   if constexpr (kWhat == kDistillStep) {
     const long long vecs = (row_bytes / 16 + ctas - 1) / ctas;
-    if (vecs * 16 <= kSliceBytes && bits <= 64 * 1024) {
-      const size_t smem = bits + (size_t)((vecs + kRowThreads - 1) / kRowThreads) * kRowThreads * 16;
+    const size_t smem = bits + (size_t)((vecs + kRowThreads - 1) / kRowThreads) * kRowThreads * 16;
+    if (vecs * 16 <= kSliceBytes && smem <= kStagedMost) {
       return a.tail ? launch_as<T, kDistillStep, true, true>(a, ctas, smem, words, st)
                     : launch_as<T, kDistillStep, false, true>(a, ctas, smem, words, st);
     }
