@@ -489,6 +489,7 @@ ln_bwd_kernel(const LnArgs a, int tpr, float *__restrict__ part) {
     for (int k = 0; k < R; ++k) {
       // dx = rstd (g - c1 - h c2)
       const float2 c1 = both(-s[2 * k] * inv_d), c2 = both(-s[2 * k + 1] * inv_d);
+      const float2 rc2 = both(__fmul_rn(rr[k].x, c2.x));  // h c2 = (x - mean) rstd c2
       const bool live = r + k < a.rows;
       T *o = dx + co.at(k);
 #pragma unroll
@@ -505,9 +506,8 @@ ln_bwd_kernel(const LnArgs a, int tpr, float *__restrict__ part) {
           Pairs<VEC> g = ring.get(stage, 2 * (k * NV + i) + 1);
 #pragma unroll
           for (int j = 0; j < NP; ++j) {
-            const float2 h = pmul<VEC>(padd<VEC>(px.v[j], nm[k]), rr[k]);
             const float2 gw = pmul<VEC>(g.v[j], kKeep ? wk[kKeep ? i : 0][j] : w.v[j]);
-            g.v[j] = pmul<VEC>(rr[k], padd<VEC>(gw, pfma<VEC>(h, c2, c1)));
+            g.v[j] = pmul<VEC>(rr[k], padd<VEC>(gw, pfma<VEC>(padd<VEC>(px.v[j], nm[k]), rc2, c1)));
           }
           store_pairs<T, VEC>(g, o + i * step);
         }
