@@ -10,8 +10,8 @@
 //
 // The alternatives cost no second pass.  Split among more than k groups of the
 // CTA's threads, the values have a k-th largest of the groups' maxima that is a
-// lower bound of the k-th largest logit: 32 groups of eight lanes for k <= 32
-// (each warp finds the bound for itself by bisection with ballots), the 256
+// lower bound of the k-th largest logit: 32 groups of neighbouring lanes for
+// k <= 32 (each warp finds the bound for itself by bisection with ballots), all
 // threads beyond (one warp finds it).  Only the threads whose maximum reaches
 // the bound hold candidates, so only their values are read again (from the
 // caches), and the few that reach the bound are ranked against one another.
@@ -54,10 +54,10 @@ template <int kT>
 struct TopShared {
   alignas(16) unsigned long long cand[kCand];  // in a cluster also [ctas][kMaxTop]
   unsigned long long sorted[kMaxTop];  // this CTA's, in order
-  uint32_t own[kT < 32 ? 32 : kT];           // the threads' maxima, or the groups'
+  uint32_t own[kT];                    // the threads' maxima, or the groups'
   uint32_t bound;
   int count, listed;
-  int warp_total[8];
+  int warp_total[kWarps<kT> < 8 ? 8 : kWarps<kT>];
 };
 
 // The largest b in [lo, hi] with count_ge(b) >= k, or any b with count_ge(b)
@@ -141,11 +141,39 @@ __device__ int top_candidates(const LogitRow<T> &row, const RowSlice &slice, int
     if (at < kCand) sh.cand[at] = ((unsigned long long)order_key<T>(x) << 32) | (uint32_t)~idx;
   };
   constexpr int kVec = LogitRow<T>::kVec;
-  // The values from `least` up.  A warp goes through the values of its threads
+  auto push_from = [&](const LogitVec<T> &v, float value, int at) {
+    const LogitVec<T> one[1] = {v};
+    if (!(LogitVec<T>::max_of(one) >= value)) return;
+    float x[kVec];
+    v.get(x);
+#pragma unroll
+    for (int e = 0; e < kVec; ++e)
+      if (x[e] >= value) push(x[e], row.index(at) + e);
+  };
+  // The values from `least` up.  In a short slice each thread that holds some
+  // reads its own again (4096 rows of 1000, 20 alternatives: 22 us, the other
+  // way 30).  In a longer one a warp goes through the values of its threads
   // that hold some, two threads at a time.
+  const bool few = slice.v1 - slice.v0 <= 2 * kUnroll * kT;
   auto collect = [&](uint32_t least) {
     const float value = key_value<T>(least);
     unsigned mask = __ballot_sync(0xffffffffu, mine >= least);
+    if (few) {
+      if (mine >= least)
+#pragma unroll 1
+        for (int i = slice.v0 + threadIdx.x; i < slice.v1; i += kUnroll * kT) {
+          LogitVec<T> v[kUnroll];
+#pragma unroll
+          for (int j = 0; j < kUnroll; ++j)
+            if (i + j * kT < slice.v1)
+              v[j].load(row.p + row.index(i + j * kT));
+            else
+              v[j].fill_masked();
+#pragma unroll
+          for (int j = 0; j < kUnroll; ++j) push_from(v[j], value, i + j * kT);
+        }
+      mask = 0;
+    }
     const int base = slice.v0 + (threadIdx.x & ~31) + lane * kT;
     while (mask) {
       int t[2];
@@ -161,14 +189,7 @@ __device__ int top_candidates(const LogitRow<T> &row, const RowSlice &slice, int
           if (t[j] < slice.v1) v[j].load(row.p + row.index(t[j]));
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const LogitVec<T> one[1] = {v[j]};
-          if (t[j] < slice.v1 && LogitVec<T>::max_of(one) >= value) {
-            float x[kVec];
-            v[j].get(x);
-#pragma unroll
-            for (int e = 0; e < kVec; ++e)
-              if (x[e] >= value) push(x[e], row.index(t[j]) + e);
-          }
+          if (t[j] < slice.v1) push_from(v[j], value, t[j]);
           t[j] = min(t[j], slice.v1) + 32 * kT;
         }
       }
@@ -264,7 +285,7 @@ __device__ int top_candidates(const LogitRow<T> &row, const RowSlice &slice, int
 }
 
 template <typename T, bool kEntropy, bool kTop, int kT>
-__global__ void __launch_bounds__(kT, 1280 / kT)
+__global__ void __launch_bounds__(kT, kT == 512 ? 2 : 1280 / kT)
 token_logprobs_kernel(const LogprobArgs a) {
   __shared__ Softmax parts[kWarps<kT>], mine;
   __shared__ std::conditional_t<kTop, TopShared<kT>, int> shared_top;
@@ -390,21 +411,34 @@ token_logprobs_kernel(const LogprobArgs a) {
   }
 }
 
+// CTAs of kT threads a row: as many as the SMs hold at once.
+template <typename T>
+int ctas_of(const LogprobArgs &a, int threads) {
+  return row_ctas(a.rows, (long long)a.V * sizeof(T), 1LL << 40, 1024LL / threads * device_sms());
+}
+
 template <typename T, int kT>
 cudaError_t launch_as(const LogprobArgs &a, cudaStream_t st) {
-  // As many CTAs a row as the SMs hold at once.
-  const int ctas = row_ctas(a.rows, (long long)a.V * sizeof(T), 1LL << 40, 1024LL / kT * device_sms());
   auto kern = a.entropy ? (a.top > 0 ? token_logprobs_kernel<T, true, true, kT> : token_logprobs_kernel<T, true, false, kT>)
                         : (a.top > 0 ? token_logprobs_kernel<T, false, true, kT> : token_logprobs_kernel<T, false, false, kT>);
-  return launch_rows(kern, a.rows, ctas, kT, 0, st, a);
+  return launch_rows(kern, a.rows, ctas_of<T>(a, kT), kT, 0, st, a);
 }
 
 template <typename T>
 cudaError_t launch(const LogprobArgs &a, cudaStream_t st) {
+  const long long bytes = (long long)a.V * sizeof(T);
+  // Rows that two CTAs of 512 threads an SM hold at once: 512 threads, for
+  // slices longer than one group of loads and for many alternatives.  256 rows
+  // of 65536, bf16, 5 alternatives: 10.6 us, with 256 threads 15.6; 301 of 50001,
+  // fp32, 128 alternatives: 21.6 and 33.9.  Where one group is the slice or
+  // more rows follow, 256: 8 rows of 131072 without alternatives 4.4 us, with
+  // 512 threads 6.1; 4096 of 65536 with 128 alternatives 194 and 226.
+  if (a.rows <= 2 * device_sms() && (a.top > kGroups || bytes / ctas_of<T>(a, 512) > 512 * kUnroll * 16))
+    return launch_as<T, 512>(a, st);
   // Short rows: half the threads, since most of their cost is the row's and not
-  // the walk's.  4096 rows, bf16, 20 alternatives: V = 1000 30 us with 128
-  // threads, 50 with 256; fp32 2000 x 50001 86 against 75.
-  const bool narrow = a.top <= kGroups && (long long)a.V * sizeof(T) <= 32 * 1024;
+  // the walk's.  4096 rows, bf16, 20 alternatives: V = 1000 22 us with 128
+  // threads; fp32 2000 x 50001 86 us against 75 with 256.
+  const bool narrow = a.top <= kGroups && bytes <= 32 * 1024;
   return narrow ? launch_as<T, 128>(a, st) : launch_as<T, 256>(a, st);
 }
 

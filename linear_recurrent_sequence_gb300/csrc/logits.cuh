@@ -209,10 +209,11 @@ struct WarpSoftmax {
   }
 };
 
-// Joins up to eight parts, one in each of lanes 0..7 (and again in every
-// eight lanes after them; an absent part has m = -infinity and zeros).
-template <bool kEntropy>
-__device__ __forceinline__ Softmax join_eight(const Softmax &p, float scale) {
+// Joins up to kLanes parts (a power of two), one in each of the first kLanes
+// lanes and again in every kLanes after them; an absent part has m = -infinity
+// and zeros.
+template <bool kEntropy, int kLanes>
+__device__ __forceinline__ Softmax join_lanes(const Softmax &p, float scale) {
   Softmax r;
   r.m = redux_max(p.m);
   const bool some = p.m > -INFINITY;
@@ -221,7 +222,7 @@ __device__ __forceinline__ Softmax join_eight(const Softmax &p, float scale) {
   r.s = __fmul_rn(p.s, f);
   r.u = kEntropy ? __fmul_rn(fmaf(dy, p.s, p.u), f) : 0.f;
 #pragma unroll
-  for (int k = 4; k > 0; k >>= 1) {
+  for (int k = kLanes / 2; k > 0; k >>= 1) {
     r.s += __shfl_xor_sync(0xffffffffu, r.s, k);
     if (kEntropy) r.u += __shfl_xor_sync(0xffffffffu, r.u, k);
   }
@@ -262,7 +263,7 @@ __device__ __forceinline__ uint32_t cluster_word(const void *local, uint32_t ran
   return v;
 }
 
-// Joins the CTA's first kWarps (at most 8) warps, and the cluster's CTAs where
+// Joins the CTA's first kWarps warps, and the cluster's CTAs where
 // there are several: the same result in every thread.  parts: shared,
 // [kWarps]; mine: shared, one.
 // In a cluster the caller then has to arrive and wait (cluster_have_read,
@@ -273,9 +274,7 @@ __device__ __forceinline__ Softmax join_row(const Softmax &warp, float scale, ui
   const int lane = threadIdx.x & 31;
   if (lane == 0 && threadIdx.x < kWarps * 32) parts[threadIdx.x >> 5] = warp;
   __syncthreads();
-  Softmax r = {-INFINITY, 0.f, 0.f, 0};
-  if ((lane & 7) < kWarps) r = parts[lane & 7];
-  r = join_eight<kEntropy>(r, scale);
+  Softmax r = join_lanes<kEntropy, kWarps>(parts[lane & (kWarps - 1)], scale);
   if (ctas == 1) return r;
   if (threadIdx.x == 0) *mine = r;
   cluster_sync();
@@ -287,7 +286,7 @@ __device__ __forceinline__ Softmax join_row(const Softmax &warp, float scale, ui
     p.u = __uint_as_float(cluster_word(&mine->u, c));
     p.bad = (int)cluster_word(&mine->bad, c);
   }
-  return join_eight<kEntropy>(p, scale);
+  return join_lanes<kEntropy, 8>(p, scale);
 }
 
 // The vectors of a row that this CTA walks over, and whether it also has the

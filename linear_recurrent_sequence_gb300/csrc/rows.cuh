@@ -99,12 +99,6 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-__device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, s));
-  return x;
-}
-
 // 2^x, flushed to zero below 2^-126 (the hardware's approximation).
 __device__ __forceinline__ float ex2(float x) {
   float y;
