@@ -120,46 +120,111 @@ __device__ __forceinline__ float2 pfma(float2 a, float2 b, float2 c) {
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// A thread's own vectors of the rows ahead, on their way through shared
-// memory by asynchronous copies: slots [stage][vector][thread].  Only the
-// thread that copied a vector reads it, so no barrier is needed.  A vector
-// past the row's end, or of a row past the last one, arrives as zeros.
-// bf16 rows off the 16-byte boundary have no copies of 2 bytes: their values
-// are loaded straight into registers (kCopies false).
-template <typename T, int VEC, int kVectors, int kStages>
+// The row group that a thread belongs to: its tpr threads, this thread's place
+// among them, and its first column and column step with VEC values a vector.
+struct RowGroup {
+  int tpr, group, t, t0, step, d;
+  __device__ __forceinline__ RowGroup(int threads, int vec, int width)
+      : tpr(threads), group(threadIdx.x / threads), t(threadIdx.x % threads), t0(t * vec), step(threads * vec), d(width) {}
+  __device__ __forceinline__ bool has(int i) const { return t0 + i * step < d; }
+};
+
+// The rows ahead, kRows at a time, on their way through shared memory by
+// asynchronous copies.  copy_row() is called by all threads of the row group
+// for row n of a stage; after wait() view() gives a thread its vectors (`in`:
+// the row is live and has vector i).
+template <typename T, int VEC, int NV, int kRows, int kStages, bool kNamed>
 struct RowRing {
-  static constexpr bool kCopies = VEC > 1 || sizeof(T) == 4;
+  // A thread copies the vectors that it reads: slots [stage][row][vector]
+  // [thread], and no barrier.  What is past the row's end, or of a row that is
+  // not there, arrives as zeros.
   static constexpr int kBytes = VEC * (int)sizeof(T);
+  static size_t bytes(int, int threads, int) { return (size_t)kStages * kRows * NV * threads * kBytes; }
+  const RowGroup &g;
+  const T *base;  // a valid address
   uint8_t *slot;  // of this thread in stage 0, vector 0
   int pitch;      // bytes of all threads' slots of one vector
-  T direct[kCopies ? 1 : kVectors];
-  __device__ __forceinline__ RowRing(uint8_t *dyn)
-      : slot(dyn + threadIdx.x * kBytes), pitch((int)blockDim.x * kBytes) {}
-  __device__ __forceinline__ void copy(int stage, int v, const T *p, bool in) {
-    const uint32_t dst = tc::smem_u32(slot + (stage * kVectors + v) * pitch);
-    const int n = in ? kBytes : 0;
-    if (kBytes == 16)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(p), "r"(n) : "memory");
-    else if (kCopies)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(p), "r"(n) : "memory");
-  }
-  __device__ __forceinline__ void load(int v, const T *p, bool in) {
-    if (!kCopies) direct[kCopies ? 0 : v] = in ? *p : T(0.f);
+  struct View {
+    const uint8_t *p;
+    int pitch;
+    __device__ __forceinline__ Pairs<VEC> get(int i, bool) const {
+      float f[VEC];
+      reinterpret_cast<const Elems<T, VEC> *>(p + i * pitch)->get(f);
+      return Pairs<VEC>(f);
+    }
+  };
+  __device__ __forceinline__ RowRing(const RowGroup &group, uint8_t *dyn, const void *any)
+      : g(group), base(reinterpret_cast<const T *>(any)), slot(dyn + threadIdx.x * kBytes), pitch((int)blockDim.x * kBytes) {}
+  __device__ __forceinline__ void copy_row(int stage, int n, const T *row, bool live) {
+    const T *p = row + g.t0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const bool in = live && g.has(i);
+      const uint32_t dst = tc::smem_u32(slot + ((stage * kRows + n) * NV + i) * pitch);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(in ? p + i * g.step : base), "r"(in ? kBytes : 0) : "memory");
+    }
   }
   __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
   // The oldest of the kStages groups committed last has arrived.
   __device__ __forceinline__ void wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
   }
-  __device__ __forceinline__ Pairs<VEC> get(int stage, int v) const {
-    float f[VEC];
-    Elems<T, VEC> e;
-    if (kCopies)
-      e = *reinterpret_cast<const Elems<T, VEC> *>(slot + (stage * kVectors + v) * pitch);
+  __device__ __forceinline__ View view(int stage, int n) const {
+    return {slot + (stage * kRows + n) * NV * pitch, pitch};
+  }
+};
+
+// Bytes of the 16-byte words that cover a row that begins anywhere in the first,
+// and of the offset of its start (in 16 more).
+__host__ __device__ __forceinline__ int span_pitch(int row_bytes) { return (row_bytes + 15) / 16 * 16 + 32; }
+
+// Rows off the 16-byte boundary: the group copies the aligned 16-byte words
+// that cover the row (the first may begin before the row, in the same word;
+// nothing past its end is read), and each thread reads its values one by one
+// from where the row begins in them.  Read straight from memory, a value costs
+// an asynchronous copy of its own (12008 x 1537 fp32: 49 instructions a value).
+template <typename T, int NV, int kRows, int kStages, bool kNamed>
+struct RowRing<T, 1, NV, kRows, kStages, kNamed> {
+  static size_t bytes(int d, int threads, int tpr) {
+    return (size_t)kStages * kRows * (threads / tpr) * span_pitch(d * (int)sizeof(T));
+  }
+  const RowGroup &g;
+  uint8_t *rows;
+  int pitch;
+  struct View {
+    const T *p;
+    int step;
+    __device__ __forceinline__ Pairs<1> get(int i, bool in) const {
+      const float f[1] = {in ? (float)p[i * step] : 0.f};
+      return Pairs<1>(f);
+    }
+  };
+  __device__ __forceinline__ RowRing(const RowGroup &group, uint8_t *dyn, const void *)
+      : g(group), rows(dyn + (size_t)group.group * kStages * kRows * span_pitch(group.d * (int)sizeof(T))),
+        pitch(span_pitch(group.d * (int)sizeof(T))) {}
+  __device__ __forceinline__ void copy_row(int stage, int n, const T *row, bool live) {
+    if (!live) return;
+    uint8_t *to = rows + (stage * kRows + n) * pitch;
+    const int lead = (int)(reinterpret_cast<uintptr_t>(row) & 15u), span = lead + g.d * (int)sizeof(T);
+    const uint8_t *from = reinterpret_cast<const uint8_t *>(row) - lead;
+    if (g.t == 0) *reinterpret_cast<int *>(to + pitch - 16) = lead;
+    for (int b = g.t * 16; b < span; b += g.tpr * 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(to + b)), "l"(from + b), "r"(min(16, span - b)) : "memory");
+  }
+  __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  __device__ __forceinline__ void wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+    if (g.tpr <= 32)
+      __syncwarp();
+    else if (kNamed)
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + g.group), "r"(g.tpr) : "memory");
     else
-      *reinterpret_cast<T *>(&e) = direct[kCopies ? 0 : v];
-    e.get(f);
-    return Pairs<VEC>(f);
+      __syncthreads();
+  }
+  __device__ __forceinline__ View view(int stage, int n) const {
+    const uint8_t *at = rows + (stage * kRows + n) * pitch;
+    const int lead = *reinterpret_cast<const int *>(at + pitch - 16);
+    return {reinterpret_cast<const T *>(at + lead) + g.t0, g.step};
   }
 };
 
@@ -210,8 +275,8 @@ ln_fwd_kernel(const LnArgs a, int tpr) {
   pdl_wait();
   if (tpr > 32) clear_red(&red[0][0][0], 2 * R * kRed);
   constexpr int NP = Pairs<VEC>::N;
-  const int t = threadIdx.x % tpr, group = threadIdx.x / tpr, groups = blockDim.x / tpr;
-  const int step = tpr * VEC, t0 = t * VEC;
+  const RowGroup g(tpr, VEC, a.d);
+  const int t = g.t, group = g.group, groups = blockDim.x / tpr, step = g.step, t0 = g.t0;
   const float inv_d = 1.f / (float)a.d;
   float2 wk[kKeep ? NV : 1][NP], bk[kKeep ? NV : 1][NP];
   if (kKeep)
@@ -226,48 +291,39 @@ ln_fwd_kernel(const LnArgs a, int tpr) {
           bk[kKeep ? i : 0][j] = b.v[j];
         }
       }
-  using Ring = RowRing<T, VEC, R * NV, kStages>;
-  Ring ring(dyn);
+  RowRing<T, VEC, NV, R, kStages, false> ring(g, dyn, a.x);
   const long long first = ((long long)blockIdx.x * groups + group) * R;
   const long long stride = (long long)gridDim.x * groups * R;
-  const T *x = reinterpret_cast<const T *>(a.x) + t0;
+  const T *x = reinterpret_cast<const T *>(a.x);
   T *y = reinterpret_cast<T *>(a.out) + t0;
   RowCursor cx(a.sx, first), cy(a.so, first);
-  // Copies (or loads) the rows at the cursor and moves it on.
+  // Copies the rows at the cursor and moves it on.
   auto ahead = [&](int stage) {
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-      const bool row = cx.r + k < a.rows;
-      const T *p = row ? x + cx.at(k) : x;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const bool in = row && t0 + i * step < a.d;
-        if (Ring::kCopies)
-          ring.copy(stage, k * NV + i, in ? p + i * step : reinterpret_cast<const T *>(a.x), in);
-        else
-          ring.load(k * NV + i, p + i * step, in);
-      }
+      const bool live = cx.r + k < a.rows;
+      ring.copy_row(stage, k, live ? x + cx.at(k) : x, live);
     }
-    if (Ring::kCopies) ring.commit();
+    ring.commit();
     cx.advance(stride);
   };
-  if (Ring::kCopies)
-    for (int k = 0; k < kStages - 1; ++k) ahead(k);
+  for (int k = 0; k < kStages - 1; ++k) ahead(k);
   int stage = 0;
   // Every thread of a warp takes part in each row's sums; past the last row
   // it works on zeros and writes nothing.
   for (long long r = first; r - group * R < a.rows; r += stride) {
     // the slot that the previous turn read takes the rows furthest ahead
     ahead(stage == 0 ? kStages - 1 : stage - 1);
-    if (Ring::kCopies) ring.wait();
+    ring.wait();
     float2 v[R][NV][NP];
     float s[R], q[R];
 #pragma unroll
     for (int k = 0; k < R; ++k) {
+      const auto from = ring.view(stage, k);
       float2 s2 = both(0.f);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const Pairs<VEC> p = ring.get(stage, k * NV + i);
+        const Pairs<VEC> p = from.get(i, g.has(i) && r + k < a.rows);
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
           v[k][i][j] = p.v[j];
@@ -389,8 +445,8 @@ ln_bwd_kernel(const LnArgs a, int tpr, float *__restrict__ part) {
   pdl_wait();
   if (tpr > 32) clear_red(&red[0][0][0], 4 * R * kRed);
   constexpr int NP = Pairs<VEC>::N;
-  const int t = threadIdx.x % tpr, group = threadIdx.x / tpr, groups = blockDim.x / tpr;
-  const int step = tpr * VEC, t0 = t * VEC;
+  const RowGroup grp(tpr, VEC, a.d);
+  const int group = grp.group, groups = blockDim.x / tpr, step = grp.step, t0 = grp.t0;
   const float inv_d = 1.f / (float)a.d;
   float2 aw[NV][NP], ab[NV][NP], wk[kKeep ? NV : 1][NP];
 #pragma unroll
@@ -405,36 +461,24 @@ ln_bwd_kernel(const LnArgs a, int tpr, float *__restrict__ part) {
 #pragma unroll
       for (int j = 0; j < NP; ++j) wk[kKeep ? i : 0][j] = w.v[j];
     }
-  using Ring = RowRing<T, VEC, 2 * R * NV, kStages>;
-  Ring ring(dyn);
+  RowRing<T, VEC, NV, 2 * R, kStages, true> ring(grp, dyn, a.x);
   const long long first = ((long long)blockIdx.x * groups + group) * R;
   const long long stride = (long long)gridDim.x * groups * R;
-  const T *x = reinterpret_cast<const T *>(a.x) + t0, *dy = reinterpret_cast<const T *>(a.dy) + t0;
+  const T *x = reinterpret_cast<const T *>(a.x), *dy = reinterpret_cast<const T *>(a.dy);
   T *dx = reinterpret_cast<T *>(a.out) + t0;
   RowCursor cx(a.sx, first), cg(a.sg, first), co(a.so, first);
   auto ahead = [&](int stage) {
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-      const bool row = cx.r + k < a.rows;
-      const T *p = row ? x + cx.at(k) : x, *g = row ? dy + cg.at(k) : dy;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const bool in = row && t0 + i * step < a.d;
-        if (Ring::kCopies) {
-          ring.copy(stage, 2 * (k * NV + i), in ? p + i * step : reinterpret_cast<const T *>(a.x), in);
-          ring.copy(stage, 2 * (k * NV + i) + 1, in ? g + i * step : reinterpret_cast<const T *>(a.dy), in);
-        } else {
-          ring.load(2 * (k * NV + i), p + i * step, in);
-          ring.load(2 * (k * NV + i) + 1, g + i * step, in);
-        }
-      }
+      const bool live = cx.r + k < a.rows;
+      ring.copy_row(stage, 2 * k, live ? x + cx.at(k) : x, live);
+      ring.copy_row(stage, 2 * k + 1, live ? dy + cg.at(k) : dy, live);
     }
-    if (Ring::kCopies) ring.commit();
+    ring.commit();
     cx.advance(stride);
     cg.advance(stride);
   };
-  if (Ring::kCopies)
-    for (int k = 0; k < kStages - 1; ++k) ahead(k);
+  for (int k = 0; k < kStages - 1; ++k) ahead(k);
   float mean_n[R], rstd_n[R];  // of the next rows
   auto stats = [&](long long r) {
 #pragma unroll
@@ -456,15 +500,17 @@ ln_bwd_kernel(const LnArgs a, int tpr, float *__restrict__ part) {
     stats(r + stride);
     // the slot that the previous turn read takes the rows furthest ahead
     ahead(stage == 0 ? kStages - 1 : stage - 1);
-    if (Ring::kCopies) ring.wait();
+    ring.wait();
     float s[2 * R];
     float2 hk[kHold ? R : 1][kHold ? NV : 1][NP], gk[kHold ? R : 1][kHold ? NV : 1][NP];
 #pragma unroll
     for (int k = 0; k < R; ++k) {
+      const auto fx = ring.view(stage, 2 * k), fg = ring.view(stage, 2 * k + 1);
       float2 s0 = both(0.f), s1 = both(0.f);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const Pairs<VEC> px = ring.get(stage, 2 * (k * NV + i)), g = ring.get(stage, 2 * (k * NV + i) + 1);
+        const bool in = grp.has(i) && r + k < a.rows;
+        const Pairs<VEC> px = fx.get(i, in), g = fg.get(i, in);
         Pairs<VEC> w;
         if (!kKeep && t0 + i * step < a.d) w = param_pairs<VEC>(a.w, t0 + i * step, 1.f);
 #pragma unroll
@@ -501,9 +547,9 @@ ln_bwd_kernel(const LnArgs a, int tpr, float *__restrict__ part) {
             g.v[j] = pmul<VEC>(rr[k], padd<VEC>(gk[kHold ? k : 0][kHold ? i : 0][j], pfma<VEC>(hk[kHold ? k : 0][kHold ? i : 0][j], c2, c1)));
           store_pairs<T, VEC>(g, o + i * step);
         } else if (t0 + i * step < a.d && live) {
-          const Pairs<VEC> px = ring.get(stage, 2 * (k * NV + i));
+          const Pairs<VEC> px = ring.view(stage, 2 * k).get(i, true);
           const Pairs<VEC> w = kKeep ? Pairs<VEC>() : param_pairs<VEC>(a.w, t0 + i * step, 1.f);
-          Pairs<VEC> g = ring.get(stage, 2 * (k * NV + i) + 1);
+          Pairs<VEC> g = ring.view(stage, 2 * k + 1).get(i, true);
 #pragma unroll
           for (int j = 0; j < NP; ++j) {
             const float2 gw = pmul<VEC>(g.v[j], kKeep ? wk[kKeep ? i : 0][j] : w.v[j]);
@@ -531,6 +577,7 @@ ln_bwd_kernel(const LnArgs a, int tpr, float *__restrict__ part) {
   const int unit_threads = tpr < 32 ? 32 : tpr, units = blockDim.x / unit_threads;
   float *out = part + (size_t)blockIdx.x * 2 * a.d, *sums = reinterpret_cast<float *>(dyn);
   float *mine = units > 1 ? sums + (size_t)(threadIdx.x / unit_threads) * 2 * a.d : out;
+  asm volatile("cp.async.wait_all;" ::: "memory");  // zeros for rows past the last one
   __syncthreads();  // every copy to the ring has been read
   if (tpr >= 32 || (int)(threadIdx.x & 31) < tpr)
 #pragma unroll
@@ -684,10 +731,10 @@ cudaError_t launch_with(int grid, int threads, size_t smem, cudaStream_t st, Arg
 template <typename T, int VEC, int NV, int R, int kStages, bool kKeep, int kThreads>
 cudaError_t fwd(const LnArgs &a, int tpr, int per_sm, cudaStream_t st) {
   const int threads = tpr > 32 ? tpr : 128, rows = threads / tpr * R;
-  const size_t smem = RowRing<T, VEC, 1, 1>::kCopies ? (size_t)kStages * R * NV * threads * VEC * sizeof(T) : 0;
+  const size_t smem = RowRing<T, VEC, NV, R, kStages, false>::bytes(a.d, threads, tpr);
   // CTAs that stay for the whole call, per_sm threads an SM, less where the
   // rings fill its shared memory.
-  const long long fit = std::max<long long>(1, std::min<long long>(per_sm / threads, smem ? 220 * 1024 / (smem + 1024) : 32));
+  const long long fit = std::max<long long>(1, std::min<long long>(per_sm / threads, 220 * 1024 / (smem + 1024)));
   const long long want = (a.rows + rows - 1) / rows, most = device_sms() * fit;
   return launch_with<ln_fwd_kernel<T, VEC, NV, R, kStages, kKeep, kThreads>>(
       (int)std::min(want, most), threads, smem, st, a, tpr);
@@ -710,11 +757,13 @@ cudaError_t fwd_any(const LnArgs &a, cudaStream_t st) {
                   dim3(1024), 0, st, true, a);
 }
 
+constexpr int kBwdStages = 3;
+
 template <typename T, int VEC, int NV, int R, int kStages, bool kKeep, int kThreads, bool kHold>
 cudaError_t bwd(const LnArgs &a, const LnBwdPlan &pl, float *part, cudaStream_t st) {
   const int units = pl.threads / std::max(pl.tpr, 32);
   const size_t smem = std::max(units > 1 ? (size_t)units * 2 * a.d * sizeof(float) : 0,
-                               RowRing<T, VEC, 1, 1>::kCopies ? (size_t)kStages * 2 * R * NV * pl.threads * VEC * sizeof(T) : 0);
+                               RowRing<T, VEC, NV, 2 * R, kStages, true>::bytes(a.d, pl.threads, pl.tpr));
   return launch_with<ln_bwd_kernel<T, VEC, NV, R, kStages, kKeep, kThreads, kHold>>(
       pl.groups, pl.threads, smem, st, a, pl.tpr, part);
 }
@@ -728,8 +777,8 @@ cudaError_t bwd_any(const LnArgs &a, const LnBwdPlan &pl, const float *stat, flo
                     0, st, true, a, stat, part);
   }
   if constexpr (VEC == 8)
-    if (pl.wide) return bwd<T, 8, 4, 1, 3, false, 512, false>(a, pl, part, st);
-  return bwd<T, VEC, 16 / VEC, VEC == 8 ? 2 : 1, 3, true, 512, VEC == 1>(a, pl, part, st);
+    if (pl.wide) return bwd<T, 8, 4, 1, kBwdStages, false, 512, false>(a, pl, part, st);
+  return bwd<T, VEC, 16 / VEC, VEC == 8 ? 2 : 1, kBwdStages, true, 512, VEC == 1>(a, pl, part, st);
 }
 
 template <typename T, int VEC>
@@ -774,7 +823,12 @@ LnBwdPlan layernorm_bwd_plan(const LnArgs &a, int bf16) {
   // warps: each has a named barrier.)
   const long long sms = device_sms(), R = V == 8 && !pl.wide ? 2 : 1;
   const int most = 512;
-  const long long fit = pl.tpr > 32 ? std::min(most / pl.tpr, 15) : most / pl.tpr;
+  long long fit = pl.tpr > 32 ? std::min(most / pl.tpr, 15) : most / pl.tpr;
+  if (!pl.vec) {  // (short rows: no more than 192 KB of them, in whole warps)
+    fit = std::min<long long>(fit, 192 * 1024 / (kBwdStages * 2 * span_pitch(a.d * esz)));
+    if (pl.tpr < 32) fit = fit * pl.tpr / 32 * 32 / pl.tpr;
+    fit = std::max<long long>(fit, 1);
+  }
   long long at_once = std::min(fit, std::max<long long>(1, a.rows / (sms * R)));
   while (pl.tpr < 32 && at_once * pl.tpr % 32) ++at_once;
   pl.threads = (int)at_once * pl.tpr;
