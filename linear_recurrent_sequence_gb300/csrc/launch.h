@@ -247,7 +247,7 @@ struct LnArgs {
   float eps = 0.f;
 };
 struct LnBwdPlan {
-  bool vec = false, wide = false, two_pass = false;
+  bool vec = false, narrow = false, wide = false, two_pass = false;
   int tpr = 0, threads = 0, groups = 0;  // threads a row, of a CTA; CTAs
 };
 cudaError_t launch_layernorm_rows(const LnArgs &a, int bf16, cudaStream_t st);

@@ -121,48 +121,68 @@ __device__ __forceinline__ float2 pfma(float2 a, float2 b, float2 c) {
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // The row group that a thread belongs to: its tpr threads, this thread's place
-// among them, and its first column and column step with VEC values a vector.
+// among them, and its NV vectors of VEC values.  With whole warps a row
+// (kWarps) each warp has NV * 32 neighbouring vectors, so that the steps
+// between a thread's vectors are constants and at most one warp is not full
+// (8001 x 4097 bf16 forward: 52 us, with the group's vectors interleaved 74).
+template <int VEC, int NV, bool kWarps>
 struct RowGroup {
-  int tpr, group, t, t0, step, d;
-  __device__ __forceinline__ RowGroup(int threads, int vec, int width)
-      : tpr(threads), group(threadIdx.x / threads), t(threadIdx.x % threads), t0(t * vec), step(threads * vec), d(width) {}
-  __device__ __forceinline__ bool has(int i) const { return t0 + i * step < d; }
+  int tpr, group, t, t0, left;  // left: columns from the first one on
+  bool full;                    // this warp has all of its vectors
+  __device__ __forceinline__ RowGroup(int threads, int d)
+      : tpr(threads), group(threadIdx.x / threads), t(threadIdx.x % threads) {
+    t0 = (kWarps ? t / 32 * 32 * NV + t % 32 : t) * VEC;
+    left = d - t0;
+    full = kWarps && __all_sync(0xffffffffu, (NV - 1) * step() < left);
+  }
+  __device__ __forceinline__ int step() const { return (kWarps ? 32 : tpr) * VEC; }
+  __device__ __forceinline__ bool has(int i) const { return i * step() < left; }
+  // f(i, whether vector i is there) for each vector; `there`: any of them is.
+  template <typename F>
+  __device__ __forceinline__ void each(bool there, F f) const {
+    if (kWarps && full && there) {  // as in all warps but the last
+#pragma unroll
+      for (int i = 0; i < NV; ++i) f(i, std::true_type());
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) f(i, there && has(i));
+    }
+  }
 };
 
 // The rows ahead, kRows at a time, on their way through shared memory by
 // asynchronous copies.  copy_row() is called by all threads of the row group
 // for row n of a stage; after wait() view() gives a thread its vectors (`in`:
 // the row is live and has vector i).
-template <typename T, int VEC, int NV, int kRows, int kStages, bool kNamed>
+template <typename T, int VEC, int NV, bool kWarps, int kRows, int kStages, bool kNamed>
 struct RowRing {
-  // A thread copies the vectors that it reads: slots [stage][row][vector]
-  // [thread], and no barrier.  What is past the row's end, or of a row that is
+  // A thread copies the vectors that it reads: slots [stage][row][warp][vector]
+  // [lane], and no barrier.  What is past the row's end, or of a row that is
   // not there, arrives as zeros.
   static constexpr int kBytes = VEC * (int)sizeof(T);
   static size_t bytes(int, int threads, int) { return (size_t)kStages * kRows * NV * threads * kBytes; }
-  const RowGroup &g;
+  static constexpr int kStep = 32 * kBytes;  // from one vector of a thread to the next
+  const RowGroup<VEC, NV, kWarps> &g;
   const T *base;  // a valid address
-  uint8_t *slot;  // of this thread in stage 0, vector 0
-  int pitch;      // bytes of all threads' slots of one vector
+  uint8_t *slot;  // of this thread in stage 0, row 0
+  int pitch;      // bytes of all threads' slots of one row
   struct View {
     const uint8_t *p;
-    int pitch;
     __device__ __forceinline__ Pairs<VEC> get(int i, bool) const {
       float f[VEC];
-      reinterpret_cast<const Elems<T, VEC> *>(p + i * pitch)->get(f);
+      reinterpret_cast<const Elems<T, VEC> *>(p + i * kStep)->get(f);
       return Pairs<VEC>(f);
     }
   };
-  __device__ __forceinline__ RowRing(const RowGroup &group, uint8_t *dyn, const void *any)
-      : g(group), base(reinterpret_cast<const T *>(any)), slot(dyn + threadIdx.x * kBytes), pitch((int)blockDim.x * kBytes) {}
+  __device__ __forceinline__ RowRing(const RowGroup<VEC, NV, kWarps> &group, uint8_t *dyn, const void *any, int)
+      : g(group), base(reinterpret_cast<const T *>(any)),
+        slot(dyn + (threadIdx.x / 32 * 32 * NV + threadIdx.x % 32) * kBytes), pitch((int)blockDim.x * NV * kBytes) {}
   __device__ __forceinline__ void copy_row(int stage, int n, const T *row, bool live) {
     const T *p = row + g.t0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const bool in = live && g.has(i);
-      const uint32_t dst = tc::smem_u32(slot + ((stage * kRows + n) * NV + i) * pitch);
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(in ? p + i * g.step : base), "r"(in ? kBytes : 0) : "memory");
-    }
+    const uint32_t dst = tc::smem_u32(slot + (stage * kRows + n) * pitch);
+    g.each(live, [&](int i, auto in) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * kStep), "l"(in ? p + i * g.step() : base), "r"(in ? kBytes : 0) : "memory");
+    });
   }
   __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
   // The oldest of the kStages groups committed last has arrived.
@@ -170,7 +190,7 @@ struct RowRing {
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
   }
   __device__ __forceinline__ View view(int stage, int n) const {
-    return {slot + (stage * kRows + n) * NV * pitch, pitch};
+    return {slot + (stage * kRows + n) * pitch};
   }
 };
 
@@ -181,35 +201,55 @@ __host__ __device__ __forceinline__ int span_pitch(int row_bytes) { return (row_
 // Rows off the 16-byte boundary: the group copies the aligned 16-byte words
 // that cover the row (the first may begin before the row, in the same word;
 // nothing past its end is read), and each thread reads its values one by one
-// from where the row begins in them.  Read straight from memory, a value costs
-// an asynchronous copy of its own (12008 x 1537 fp32: 49 instructions a value).
-template <typename T, int NV, int kRows, int kStages, bool kNamed>
-struct RowRing<T, 1, NV, kRows, kStages, kNamed> {
+// from where the row begins in them.  (With an asynchronous copy of its own
+// for each value 3003 x 1537 fp32 took 14.0 us forward, so 9.8.)
+template <typename T, int NV, bool kWarps, int kRows, int kStages, bool kNamed>
+struct RowRing<T, 1, NV, kWarps, kRows, kStages, kNamed> {
   static size_t bytes(int d, int threads, int tpr) {
     return (size_t)kStages * kRows * (threads / tpr) * span_pitch(d * (int)sizeof(T));
   }
-  const RowGroup &g;
+  const RowGroup<1, NV, kWarps> &g;
   uint8_t *rows;
-  int pitch;
+  int bytes_, pitch;
   struct View {
     const T *p;
     int step;
     __device__ __forceinline__ Pairs<1> get(int i, bool in) const {
-      const float f[1] = {in ? (float)p[i * step] : 0.f};
+      const float f[1] = {in ? (float)p[i * (kWarps ? 32 : step)] : 0.f};
       return Pairs<1>(f);
     }
   };
-  __device__ __forceinline__ RowRing(const RowGroup &group, uint8_t *dyn, const void *)
-      : g(group), rows(dyn + (size_t)group.group * kStages * kRows * span_pitch(group.d * (int)sizeof(T))),
-        pitch(span_pitch(group.d * (int)sizeof(T))) {}
+  __device__ __forceinline__ RowRing(const RowGroup<1, NV, kWarps> &group, uint8_t *dyn, const void *, int d)
+      : g(group), bytes_(d * (int)sizeof(T)), pitch(span_pitch(d * (int)sizeof(T))) {
+    rows = dyn + (size_t)group.group * kStages * kRows * pitch;
+  }
   __device__ __forceinline__ void copy_row(int stage, int n, const T *row, bool live) {
     if (!live) return;
     uint8_t *to = rows + (stage * kRows + n) * pitch;
-    const int lead = (int)(reinterpret_cast<uintptr_t>(row) & 15u), span = lead + g.d * (int)sizeof(T);
+    const int lead = (int)(reinterpret_cast<uintptr_t>(row) & 15u), span = lead + bytes_;
     const uint8_t *from = reinterpret_cast<const uint8_t *>(row) - lead;
     if (g.t == 0) *reinterpret_cast<int *>(to + pitch - 16) = lead;
-    for (int b = g.t * 16; b < span; b += g.tpr * 16)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(to + b)), "l"(from + b), "r"(min(16, span - b)) : "memory");
+    const uint32_t dst = tc::smem_u32(to);
+    auto word = [&](int b, int n) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + b), "l"(from + b), "r"(n) : "memory");
+    };
+    if (kWarps) {
+      // (a warp has as many bytes as its vectors, then one word may be left)
+      constexpr int kWords = NV * (int)sizeof(T) / 16;
+      const int b0 = (g.t / 32 * kWords * 32 + g.t % 32) * 16;
+      if (b0 + kWords * 512 <= span) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) word(b0 + i * 512, 16);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+          if (b0 + i * 512 < span) word(b0 + i * 512, min(16, span - b0 - i * 512));
+      }
+      const int last = g.tpr * kWords * 16;
+      if (g.t == 0 && last < span) word(last, span - last);
+    } else {
+      for (int b = g.t * 16; b < span; b += g.tpr * 16) word(b, min(16, span - b));
+    }
   }
   __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
   __device__ __forceinline__ void wait() {
@@ -224,7 +264,7 @@ struct RowRing<T, 1, NV, kRows, kStages, kNamed> {
   __device__ __forceinline__ View view(int stage, int n) const {
     const uint8_t *at = rows + (stage * kRows + n) * pitch;
     const int lead = *reinterpret_cast<const int *>(at + pitch - 16);
-    return {reinterpret_cast<const T *>(at + lead) + g.t0, g.step};
+    return {reinterpret_cast<const T *>(at + lead) + g.t0, g.step()};
   }
 };
 
@@ -266,7 +306,13 @@ __device__ __forceinline__ Pairs<VEC> param_pairs(const float *p, int c, float o
 // next kStages - 1 sets of rows are on their way: loads are in flight all the
 // time.  kKeep: the gains and biases of the thread's columns stay in registers
 // (from L1 they would be four times the row's own traffic).
-template <typename T, int VEC, int NV, int R, int kStages, bool kKeep, int kThreads>
+// Bound by memory: 16384 x 4096 bf16 42.9 us, 6.3 TB/s; fp32 8192 x 2048 23.8 us,
+// 5.6 TB/s.  Value by value (rows off the 16-byte boundary) by the instructions
+// a value takes: fp32 8192 x 2047 25.4 us, bf16 8192 x 2047 18.6 us, bf16 8001 x
+// 4097 51.7 us, where a ninth warp has one column.  kWarps: a warp's vectors are
+// neighbours; for 16-byte vectors those of the whole group interleave (42.9 us,
+// with kWarps 45.8).
+template <typename T, int VEC, int NV, int R, int kStages, bool kKeep, int kThreads, bool kWarps>
 __global__ void __launch_bounds__(kThreads)
 ln_fwd_kernel(const LnArgs a, int tpr) {
   extern __shared__ __align__(16) uint8_t dyn[];
@@ -275,27 +321,27 @@ ln_fwd_kernel(const LnArgs a, int tpr) {
   pdl_wait();
   if (tpr > 32) clear_red(&red[0][0][0], 2 * R * kRed);
   constexpr int NP = Pairs<VEC>::N;
-  const RowGroup g(tpr, VEC, a.d);
-  const int t = g.t, group = g.group, groups = blockDim.x / tpr, step = g.step, t0 = g.t0;
+  const RowGroup<VEC, NV, kWarps> g(tpr, a.d);
+  const int group = g.group, groups = blockDim.x / tpr;
   const float inv_d = 1.f / (float)a.d;
   float2 wk[kKeep ? NV : 1][NP], bk[kKeep ? NV : 1][NP];
   if (kKeep)
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (t0 + i * step < a.d) {
-        const Pairs<VEC> w = param_pairs<VEC>(a.w, t0 + i * step, 1.f);
-        const Pairs<VEC> b = param_pairs<VEC>(a.b, t0 + i * step, 0.f);
+      if (g.has(i)) {
+        const Pairs<VEC> w = param_pairs<VEC>(a.w, g.t0 + i * g.step(), 1.f);
+        const Pairs<VEC> b = param_pairs<VEC>(a.b, g.t0 + i * g.step(), 0.f);
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
           wk[kKeep ? i : 0][j] = w.v[j];
           bk[kKeep ? i : 0][j] = b.v[j];
         }
       }
-  RowRing<T, VEC, NV, R, kStages, false> ring(g, dyn, a.x);
+  RowRing<T, VEC, NV, kWarps, R, kStages, false> ring(g, dyn, a.x, a.d);
   const long long first = ((long long)blockIdx.x * groups + group) * R;
   const long long stride = (long long)gridDim.x * groups * R;
   const T *x = reinterpret_cast<const T *>(a.x);
-  T *y = reinterpret_cast<T *>(a.out) + t0;
+  T *y = reinterpret_cast<T *>(a.out) + g.t0;
   RowCursor cx(a.sx, first), cy(a.so, first);
   // Copies the rows at the cursor and moves it on.
   auto ahead = [&](int stage) {
@@ -321,15 +367,14 @@ ln_fwd_kernel(const LnArgs a, int tpr) {
     for (int k = 0; k < R; ++k) {
       const auto from = ring.view(stage, k);
       float2 s2 = both(0.f);
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const Pairs<VEC> p = from.get(i, g.has(i) && r + k < a.rows);
+      g.each(r + k < a.rows, [&](int i, auto in) {
+        const Pairs<VEC> p = from.get(i, in);
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
           v[k][i][j] = p.v[j];
           s2 = padd<VEC>(s2, p.v[j]);
         }
-      }
+      });
       s[k] = s2.x + s2.y;
     }
     row_sums<R, false>(s, red[0], tpr);
@@ -337,15 +382,14 @@ ln_fwd_kernel(const LnArgs a, int tpr) {
     for (int k = 0; k < R; ++k) {
       s[k] *= inv_d;
       float2 s2 = both(0.f);
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const float2 nm = both(t0 + i * step < a.d ? -s[k] : 0.f);  // zeros past the end stay zeros
+      g.each(true, [&](int i, auto in) {
+        const float2 nm = both(in ? -s[k] : 0.f);  // zeros past the end stay zeros
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
           v[k][i][j] = padd<VEC>(v[k][i][j], nm);
           s2 = pfma<VEC>(v[k][i][j], v[k][i][j], s2);
         }
-      }
+      });
       q[k] = s2.x + s2.y;
     }
     row_sums<R, false>(q, red[1], tpr);
@@ -353,24 +397,23 @@ ln_fwd_kernel(const LnArgs a, int tpr) {
     for (int k = 0; k < R; ++k) {
       const bool live = r + k < a.rows;
       const float rstd = rsqrtf(fmaf(q[k], inv_d, a.eps));
-      if (t == 0 && live) {
+      if (g.t == 0 && live) {
         if (a.mean) a.mean[r + k] = s[k];
         if (a.rstd) a.rstd[r + k] = rstd;
       }
       const float2 rr = both(rstd);
       T *o = y + cy.at(k);
+      g.each(live, [&](int i, auto in) {
+        if (!in) return;
+        const Pairs<VEC> w = kKeep ? Pairs<VEC>() : param_pairs<VEC>(a.w, g.t0 + i * g.step(), 1.f);
+        const Pairs<VEC> b = kKeep ? Pairs<VEC>() : param_pairs<VEC>(a.b, g.t0 + i * g.step(), 0.f);
+        Pairs<VEC> n;
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (t0 + i * step < a.d && live) {
-          const Pairs<VEC> w = kKeep ? Pairs<VEC>() : param_pairs<VEC>(a.w, t0 + i * step, 1.f);
-          const Pairs<VEC> b = kKeep ? Pairs<VEC>() : param_pairs<VEC>(a.b, t0 + i * step, 0.f);
-          Pairs<VEC> n;
-#pragma unroll
-          for (int j = 0; j < NP; ++j)
-            n.v[j] = pfma<VEC>(pmul<VEC>(v[k][i][j], rr), kKeep ? wk[kKeep ? i : 0][j] : w.v[j],
-                               kKeep ? bk[kKeep ? i : 0][j] : b.v[j]);
-          store_pairs<T, VEC>(n, o + i * step);
-        }
+        for (int j = 0; j < NP; ++j)
+          n.v[j] = pfma<VEC>(pmul<VEC>(v[k][i][j], rr), kKeep ? wk[kKeep ? i : 0][j] : w.v[j],
+                             kKeep ? bk[kKeep ? i : 0][j] : b.v[j]);
+        store_pairs<T, VEC>(n, o + i * g.step());
+      });
     }
     cy.advance(stride);
     stage = stage + 1 == kStages ? 0 : stage + 1;
@@ -430,13 +473,19 @@ ln_fwd_long_kernel(const LnArgs a) {
 
 // dx of the CTA's rows, and the sums of dy h and dy over them: R rows at a
 // time by tpr threads, blockDim / tpr such groups in a CTA.  Each thread keeps
-// the sums of its own NV x VEC columns in registers for the whole call; the
-// rows come through the ring and are read from it twice, before and after
-// the rows' sums.  kKeep: so do the gains of the thread's columns.  kHold: h and
-// dy w stay in registers between the two uses instead (8192 x 4096 bf16: 45 us
-// one row at a time with it, 44 two rows at a time without; 8001 x 4097, value
-// by value: 101 with it, 114 without).
-template <typename T, int VEC, int NV, int R, int kStages, bool kKeep, int kThreads, bool kHold>
+// the sums of its own NV x VEC columns in registers for the whole call: that is
+// what leaves one CTA of 512 threads an SM, and bounds the kernel by the issue
+// of 16 warps' instructions rather than by memory (8192 x 4096 bf16: 43 us with
+// the sum over CTAs, 4.7 TB/s; fp32 8192 x 2048: 37 us, 5.5 TB/s).  Sums kept in
+// shared memory, or added by atomics, would cost each value a read and a write
+// there, and atomics an order that changes.
+// The rows come through the ring and are read from it twice, before and after
+// the rows' sums.  kKeep: the gains of the thread's columns are in registers
+// too.  kHold: h and dy w stay in registers between the two uses instead
+// (8192 x 4096 bf16: 45 us one row at a time with it, 44 two rows at a time
+// without); values read one by one are held always, since others' copies take
+// their place.
+template <typename T, int VEC, int NV, int R, int kStages, bool kKeep, int kThreads, bool kHold, bool kWarps>
 __global__ void __launch_bounds__(kThreads)
 ln_bwd_kernel(const LnArgs a, int tpr, float *__restrict__ part) {
   extern __shared__ __align__(16) uint8_t dyn[];  // ring, then the CTA's sums
@@ -445,8 +494,8 @@ ln_bwd_kernel(const LnArgs a, int tpr, float *__restrict__ part) {
   pdl_wait();
   if (tpr > 32) clear_red(&red[0][0][0], 4 * R * kRed);
   constexpr int NP = Pairs<VEC>::N;
-  const RowGroup grp(tpr, VEC, a.d);
-  const int group = grp.group, groups = blockDim.x / tpr, step = grp.step, t0 = grp.t0;
+  const RowGroup<VEC, NV, kWarps> grp(tpr, a.d);
+  const int group = grp.group, groups = blockDim.x / tpr;
   const float inv_d = 1.f / (float)a.d;
   float2 aw[NV][NP], ab[NV][NP], wk[kKeep ? NV : 1][NP];
 #pragma unroll
@@ -457,15 +506,15 @@ ln_bwd_kernel(const LnArgs a, int tpr, float *__restrict__ part) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       Pairs<VEC> w;
-      if (t0 + i * step < a.d) w = param_pairs<VEC>(a.w, t0 + i * step, 1.f);
+      if (grp.has(i)) w = param_pairs<VEC>(a.w, grp.t0 + i * grp.step(), 1.f);
 #pragma unroll
       for (int j = 0; j < NP; ++j) wk[kKeep ? i : 0][j] = w.v[j];
     }
-  RowRing<T, VEC, NV, 2 * R, kStages, true> ring(grp, dyn, a.x);
+  RowRing<T, VEC, NV, kWarps, 2 * R, kStages, true> ring(grp, dyn, a.x, a.d);
   const long long first = ((long long)blockIdx.x * groups + group) * R;
   const long long stride = (long long)gridDim.x * groups * R;
   const T *x = reinterpret_cast<const T *>(a.x), *dy = reinterpret_cast<const T *>(a.dy);
-  T *dx = reinterpret_cast<T *>(a.out) + t0;
+  T *dx = reinterpret_cast<T *>(a.out) + grp.t0;
   RowCursor cx(a.sx, first), cg(a.sg, first), co(a.so, first);
   auto ahead = [&](int stage) {
 #pragma unroll
@@ -507,12 +556,10 @@ ln_bwd_kernel(const LnArgs a, int tpr, float *__restrict__ part) {
     for (int k = 0; k < R; ++k) {
       const auto fx = ring.view(stage, 2 * k), fg = ring.view(stage, 2 * k + 1);
       float2 s0 = both(0.f), s1 = both(0.f);
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const bool in = grp.has(i) && r + k < a.rows;
+      grp.each(r + k < a.rows, [&](int i, auto in) {
         const Pairs<VEC> px = fx.get(i, in), g = fg.get(i, in);
         Pairs<VEC> w;
-        if (!kKeep && t0 + i * step < a.d) w = param_pairs<VEC>(a.w, t0 + i * step, 1.f);
+        if (!kKeep && in) w = param_pairs<VEC>(a.w, grp.t0 + i * grp.step(), 1.f);
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
           const float2 h = pmul<VEC>(padd<VEC>(px.v[j], nm[k]), rr[k]);
@@ -526,7 +573,7 @@ ln_bwd_kernel(const LnArgs a, int tpr, float *__restrict__ part) {
             gk[kHold ? k : 0][kHold ? i : 0][j] = gw;
           }
         }
-      }
+      });
       s[2 * k] = s0.x + s0.y;
       s[2 * k + 1] = s1.x + s1.y;
     }
@@ -538,25 +585,26 @@ ln_bwd_kernel(const LnArgs a, int tpr, float *__restrict__ part) {
       const float2 rc2 = both(__fmul_rn(rr[k].x, c2.x));  // h c2 = (x - mean) rstd c2
       const bool live = r + k < a.rows;
       T *o = dx + co.at(k);
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (kHold && t0 + i * step < a.d && live) {
-          Pairs<VEC> g;
+      const auto fx = ring.view(stage, 2 * k), fg = ring.view(stage, 2 * k + 1);
+      grp.each(live, [&](int i, auto in) {
+        if (!in) return;
+        Pairs<VEC> g;
+        if (kHold) {
 #pragma unroll
           for (int j = 0; j < NP; ++j)
             g.v[j] = pmul<VEC>(rr[k], padd<VEC>(gk[kHold ? k : 0][kHold ? i : 0][j], pfma<VEC>(hk[kHold ? k : 0][kHold ? i : 0][j], c2, c1)));
-          store_pairs<T, VEC>(g, o + i * step);
-        } else if (t0 + i * step < a.d && live) {
-          const Pairs<VEC> px = ring.view(stage, 2 * k).get(i, true);
-          const Pairs<VEC> w = kKeep ? Pairs<VEC>() : param_pairs<VEC>(a.w, t0 + i * step, 1.f);
-          Pairs<VEC> g = ring.view(stage, 2 * k + 1).get(i, true);
+        } else {
+          const Pairs<VEC> px = fx.get(i, true);
+          const Pairs<VEC> w = kKeep ? Pairs<VEC>() : param_pairs<VEC>(a.w, grp.t0 + i * grp.step(), 1.f);
+          g = fg.get(i, true);
 #pragma unroll
           for (int j = 0; j < NP; ++j) {
             const float2 gw = pmul<VEC>(g.v[j], kKeep ? wk[kKeep ? i : 0][j] : w.v[j]);
             g.v[j] = pmul<VEC>(rr[k], padd<VEC>(gw, pfma<VEC>(padd<VEC>(px.v[j], nm[k]), rc2, c1)));
           }
-          store_pairs<T, VEC>(g, o + i * step);
         }
+        store_pairs<T, VEC>(g, o + i * grp.step());
+      });
     }
     co.advance(stride);
     stage = stage + 1 == kStages ? 0 : stage + 1;
@@ -582,8 +630,8 @@ ln_bwd_kernel(const LnArgs a, int tpr, float *__restrict__ part) {
   if (tpr >= 32 || (int)(threadIdx.x & 31) < tpr)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = t0 + i * step;
-      if (c < a.d)
+      const int c = grp.t0 + i * grp.step();
+      if (grp.has(i))
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
           mine[c + 2 * j] = aw[i][j].x;
@@ -731,13 +779,19 @@ cudaError_t launch_with(int grid, int threads, size_t smem, cudaStream_t st, Arg
 template <typename T, int VEC, int NV, int R, int kStages, bool kKeep, int kThreads>
 cudaError_t fwd(const LnArgs &a, int tpr, int per_sm, cudaStream_t st) {
   const int threads = tpr > 32 ? tpr : 128, rows = threads / tpr * R;
-  const size_t smem = RowRing<T, VEC, NV, R, kStages, false>::bytes(a.d, threads, tpr);
+  const size_t smem = RowRing<T, VEC, NV, true, R, kStages, false>::bytes(a.d, threads, tpr);
   // CTAs that stay for the whole call, per_sm threads an SM, less where the
   // rings fill its shared memory.
   const long long fit = std::max<long long>(1, std::min<long long>(per_sm / threads, 220 * 1024 / (smem + 1024)));
   const long long want = (a.rows + rows - 1) / rows, most = device_sms() * fit;
-  return launch_with<ln_fwd_kernel<T, VEC, NV, R, kStages, kKeep, kThreads>>(
-      (int)std::min(want, most), threads, smem, st, a, tpr);
+  const int grid = (int)std::min(want, most);
+  // (values one by one in whole warps: kWarps; below 32 threads no wide rows)
+  if constexpr (VEC == 1)
+    if (tpr >= 32)
+      return launch_with<ln_fwd_kernel<T, VEC, NV, R, kStages, kKeep, kThreads, true>>(grid, threads, smem, st, a, tpr);
+  if constexpr (VEC > 1 || NV == 8 || R == 2)
+    return launch_with<ln_fwd_kernel<T, VEC, NV, R, kStages, kKeep, kThreads, false>>(grid, threads, smem, st, a, tpr);
+  return cudaErrorInvalidValue;
 }
 
 template <typename T, int VEC>
@@ -748,6 +802,10 @@ cudaError_t fwd_any(const LnArgs &a, cudaStream_t st) {
   // else two rows of 16; above 8192 values a row one row of 16 or 32.
   if (t8 <= 1024 && a.rows * t8 <= (long long)device_sms() * 1024)
     return fwd<T, VEC, 8 / VEC, 1, 2, false, 1024>(a, t8, 1024, st);
+  // Short rows off the 16-byte boundary: one row of 8 (65536 rows, bf16: d = 31
+  // 7.3 us, two rows of 16 13.3; d = 255 24.4 and 26.7; d = 127 18.7 and 16.7).
+  if constexpr (VEC == 1)
+    if (t8 == 32 || t8 <= 8) return fwd<T, VEC, 8, 1, 3, true, 1024>(a, t8, 1536, st);
   if (t16 <= 512) return fwd<T, VEC, 16 / VEC, 2, sizeof(T) == 4 ? 2 : 3, true, 512>(a, t16, 512, st);
   if (t16 <= 1024) return fwd<T, VEC, 16 / VEC, 1, 3, false, 1024>(a, t16, 1024, st);
   if constexpr (VEC == 8)
@@ -763,8 +821,12 @@ template <typename T, int VEC, int NV, int R, int kStages, bool kKeep, int kThre
 cudaError_t bwd(const LnArgs &a, const LnBwdPlan &pl, float *part, cudaStream_t st) {
   const int units = pl.threads / std::max(pl.tpr, 32);
   const size_t smem = std::max(units > 1 ? (size_t)units * 2 * a.d * sizeof(float) : 0,
-                               RowRing<T, VEC, NV, 2 * R, kStages, true>::bytes(a.d, pl.threads, pl.tpr));
-  return launch_with<ln_bwd_kernel<T, VEC, NV, R, kStages, kKeep, kThreads, kHold>>(
+                               RowRing<T, VEC, NV, true, 2 * R, kStages, true>::bytes(a.d, pl.threads, pl.tpr));
+  if constexpr (NV * VEC < 32)  // (32 values a thread: wide rows only)
+    if (pl.tpr < 32 || VEC > 1)
+      return launch_with<ln_bwd_kernel<T, VEC, NV, R, kStages, kKeep, kThreads, kHold, false>>(
+          pl.groups, pl.threads, smem, st, a, pl.tpr, part);
+  return launch_with<ln_bwd_kernel<T, VEC, NV, R, kStages, kKeep, kThreads, kHold, true>>(
       pl.groups, pl.threads, smem, st, a, pl.tpr, part);
 }
 
@@ -778,6 +840,8 @@ cudaError_t bwd_any(const LnArgs &a, const LnBwdPlan &pl, const float *stat, flo
   }
   if constexpr (VEC == 8)
     if (pl.wide) return bwd<T, 8, 4, 1, kBwdStages, false, 512, false>(a, pl, part, st);
+  if constexpr (VEC == 1)
+    if (pl.narrow) return bwd<T, 1, 8, 1, kBwdStages, true, 512, true>(a, pl, part, st);
   return bwd<T, VEC, 16 / VEC, VEC == 8 ? 2 : 1, kBwdStages, true, 512, VEC == 1>(a, pl, part, st);
 }
 
@@ -806,9 +870,11 @@ LnBwdPlan layernorm_bwd_plan(const LnArgs &a, int bf16) {
   const int esz = bf16 ? 2 : 4, vec = 16 / esz;
   pl.vec = a.d % vec == 0 && rows_aligned(a.x, a.sx, esz) && rows_aligned(a.dy, a.sg, esz) &&
            rows_aligned(a.out, a.so, esz) && param_aligned(a.w);
-  // Columns a thread: 16, above 8192 columns 32 (bf16), else two passes.
+  // Columns a thread: 16 (up to 256 values off the 16-byte boundary 8: 65536 x
+  // 31 bf16 12.2 us, with 16 17.5), above 8192 columns 32 (bf16), else two passes.
   const int V = pl.vec ? vec : 1, n = (a.d + V - 1) / V;
-  pl.tpr = threads_per_row(n, 16 / V);
+  pl.narrow = !pl.vec && a.d <= 256;
+  pl.tpr = threads_per_row(n, pl.narrow ? 8 : 16 / V);
   if (pl.tpr > 512) {
     pl.wide = V == 8 && pl.tpr <= 1024;
     pl.two_pass = !pl.wide;
