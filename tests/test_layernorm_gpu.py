@@ -158,6 +158,36 @@ def test_in_place(R, d):
         assert all(torch.equal(p, q) for p, q in zip(got, (dx, dw, db)))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,d", [(611, 1), (611, 45), (611, 131), (611, 255), (611, 321), (611, 513),
+                                    (611, 1031), (211, 4097), (13, 8193)])
+def test_rows_off_the_16_byte_boundary(R, dtype, rows, d):
+    """Rows that begin anywhere in a 16-byte word, x, dy and the outputs at
+    different places, and what lies between the rows: NaN, and left alone."""
+    g = gen(11 + d)
+    w, b = 1.0 + rand(g, d, scale=0.1), rand(g, d, scale=0.1)
+
+    def rows_at(offset, pitch, fill=float("nan")):
+        flat = torch.full((rows * pitch + 16,), fill, dtype=dtype, device="cuda")
+        return flat, flat[offset:offset + rows * pitch].view(rows, pitch)[:, :d]
+
+    for ox, og, oy, pad in ((1, 2, 3, 0), (7, 0, 5, 3), (3, 3, 3, 5)):
+        x, dy = rows_at(ox, d + pad)[1], rows_at(og, d + pad)[1]
+        x.copy_(rand(g, rows, d))
+        dy.copy_(rand(g, rows, d, scale=0.1))
+        y, mean, rstd, dx, dw, db = check(R, x, dy, w, b)
+        flat, out = rows_at(oy, d + 7, 5.0)
+        assert torch.equal(R.layernorm_fwd(x, w, b, out=out)[0], y)
+        out.fill_(5.0)
+        assert bool((flat == 5.0).all())
+        got = R.layernorm_bwd(x, dy, w, mean, rstd, dx=out)
+        assert all(torch.equal(p, q) for p, q in zip(got, (dx, dw, db)))
+        out.fill_(5.0)
+        assert bool((flat == 5.0).all())
+        x2 = x.clone()
+        assert torch.equal(R.layernorm_fwd(x2, w, b, out=x2)[0], y)
+
+
 def test_large_level_and_small_spread(R):
     """A level of 1000 standard deviations: the deviations' mean square keeps
     the variance to the rounding of x - mean (mean error 80 u of the level)."""
