@@ -374,7 +374,7 @@ token_logprobs_kernel(const LogprobArgs a) {
           const int there = (int)cluster_word(&sh.listed, c);
 #pragma unroll
           for (int j = 0; j < 2 * kMaxTop / 32; ++j)
-            if (lane + 32 * j < 2 * there)
+            if (lane + 32 * j < 2 * a.top)  // (those past its length are not looked at)
               reinterpret_cast<uint32_t *>(sh.cand)[2 * kMaxTop * c + lane + 32 * j] =
                   cluster_word(reinterpret_cast<const uint32_t *>(sh.sorted) + lane + 32 * j, c);
           if (lane == 0) sh.warp_total[c] = there;
@@ -383,20 +383,19 @@ token_logprobs_kernel(const LogprobArgs a) {
         cluster_have_read();
         int total = 0;
         for (uint32_t c = 0; c < ctas; ++c) total += sh.warp_total[c];
-        if (tid < n) {
-          const unsigned long long key = sh.sorted[tid];
-          int at = 0;  // how many of each list come before key: of its own, tid
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            if (c >= (int)ctas) continue;
+        // how many of each list come before a key: a thread for each key and list
+        const int first = 1 << (31 - __clz(a.top)), lists = 31 - __clz((int)ctas);  // (a power of two)
+        for (int j0 = 0; j0 < n; j0 += kT >> lists) {
+          const int j = j0 + (tid >> lists), c = tid & ((int)ctas - 1);
+          const unsigned long long key = j < n ? sh.sorted[j] : 0;
+          int at = 0;
+          if (j < n) {
             const int there = sh.warp_total[c];
-            int lo = 0;
-#pragma unroll
-            for (int step = kMaxTop; step > 0; step >>= 1)
-              if (lo + step <= there && sh.cand[kMaxTop * c + lo + step - 1] > key) lo += step;
-            at += lo;
+            for (int step = first; step > 0; step >>= 1)
+              if (at + step <= there && sh.cand[kMaxTop * c + at + step - 1] > key) at += step;
           }
-          if (at < a.top) put(key, at);
+          for (int k = (int)ctas >> 1; k > 0; k >>= 1) at += __shfl_xor_sync(0xffffffffu, at, k);
+          if (c == 0 && j < n && at < a.top) put(key, at);
         }
         n = rank == 0 ? min(total, a.top) : a.top;
       }
