@@ -124,7 +124,8 @@ __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 // among them, and its NV vectors of VEC values.  With whole warps a row
 // (kWarps) each warp has NV * 32 neighbouring vectors, so that the steps
 // between a thread's vectors are constants and at most one warp is not full
-// (8001 x 4097 bf16 forward: 52 us, with the group's vectors interleaved 74).
+// (8001 x 4097 bf16 forward, two rows of 16: 52 us, with the group's vectors
+// interleaved 74).
 template <int VEC, int NV, bool kWarps>
 struct RowGroup {
   int tpr, group, t, t0, left;  // left: columns from the first one on
@@ -309,7 +310,7 @@ __device__ __forceinline__ Pairs<VEC> param_pairs(const float *p, int c, float o
 // Bound by memory: 16384 x 4096 bf16 42.9 us, 6.3 TB/s; fp32 8192 x 2048 23.8 us,
 // 5.6 TB/s.  Value by value (rows off the 16-byte boundary) by the instructions
 // a value takes: fp32 8192 x 2047 25.4 us, bf16 8192 x 2047 18.6 us, bf16 8001 x
-// 4097 51.7 us, where a ninth warp has one column.  kWarps: a warp's vectors are
+// 4097 35.3 us.  kWarps: a warp's vectors are
 // neighbours; for 16-byte vectors those of the whole group interleave (42.9 us,
 // with kWarps 45.8).
 template <typename T, int VEC, int NV, int R, int kStages, bool kKeep, int kThreads, bool kWarps>
@@ -797,19 +798,27 @@ cudaError_t fwd(const LnArgs &a, int tpr, int per_sm, cudaStream_t st) {
 template <typename T, int VEC>
 cudaError_t fwd_any(const LnArgs &a, cudaStream_t st) {
   const int n = (a.d + VEC - 1) / VEC;
-  const int t8 = threads_per_row(n, 8 / VEC), t16 = threads_per_row(n, 16 / VEC);
-  // 8 values a thread while that leaves the SMs with at most 1024 threads each,
-  // else two rows of 16; above 8192 values a row one row of 16 or 32.
+  const int t8 = threads_per_row(n, 8 / VEC), t16 = threads_per_row(n, 16 / VEC), t32 = threads_per_row(n, 32 / VEC);
+  // Few rows: 8 values a thread while that leaves the SMs with at most 1024
+  // threads each.
   if (t8 <= 1024 && a.rows * t8 <= (long long)device_sms() * 1024)
     return fwd<T, VEC, 8 / VEC, 1, 2, false, 1024>(a, t8, 1024, st);
   // Short rows off the 16-byte boundary: one row of 8 (65536 rows, bf16: d = 31
   // 7.3 us, two rows of 16 13.3; d = 255 24.4 and 26.7; d = 127 18.7 and 16.7).
   if constexpr (VEC == 1)
     if (t8 == 32 || t8 <= 8) return fwd<T, VEC, 8, 1, 3, true, 1024>(a, t8, 1536, st);
-  if (t16 <= 512) return fwd<T, VEC, 16 / VEC, 2, sizeof(T) == 4 ? 2 : 3, true, 512>(a, t16, 512, st);
-  if (t16 <= 1024) return fwd<T, VEC, 16 / VEC, 1, 3, false, 1024>(a, t16, 1024, st);
+  // Else two rows of 16 values a thread or one of 32, gains and biases in
+  // registers either way.  Rows of 32: above 4096 values (8192 rows, bf16: d =
+  // 5120 28.0 us, two of 16 40.3; 8192 43.8 and 48.3; 4096 x 16384 46.0; at 4096
+  // two of 16 are better, 42.9 and 46.8 for 16384 rows), and for bf16 off the
+  // 16-byte boundary where no more than an eighth more places stay empty (8192 x
+  // 3001 24.2 and 27.8; 8001 x 4097 35.3 and 51.7; not 8192 x 1535, 16.8 and 15.4).
+  const bool one = a.d > 4096 || (VEC == 1 && sizeof(T) == 2 && t32 >= 32 && t32 * 16 <= t16 * 9);
+  constexpr int kStages = sizeof(T) == 4 ? 2 : 3;
+  if (one && t32 <= 512) return fwd<T, VEC, 32 / VEC, 1, kStages, true, 512>(a, t32, 512, st);
+  if (t16 <= 512) return fwd<T, VEC, 16 / VEC, 2, kStages, true, 512>(a, t16, 512, st);
   if constexpr (VEC == 8)
-    if (t16 <= 2048) return fwd<T, 8, 4, 1, 2, false, 1024>(a, threads_per_row(n, 4), 1024, st);
+    if (t32 <= 1024) return fwd<T, 8, 4, 1, 2, false, 1024>(a, t32, 1024, st);
   const long long cap = 1LL << 30;
   return launch_k(ln_fwd_long_kernel<T, VEC>, dim3((unsigned)(a.rows < cap ? a.rows : cap)),
                   dim3(1024), 0, st, true, a);
@@ -839,7 +848,8 @@ cudaError_t bwd_any(const LnArgs &a, const LnBwdPlan &pl, const float *stat, flo
                     0, st, true, a, stat, part);
   }
   if constexpr (VEC == 8)
-    if (pl.wide) return bwd<T, 8, 4, 1, kBwdStages, false, 512, false>(a, pl, part, st);
+    // (two stages: three would leave L1 no room for the gains; 4096 x 16384 118 us and 134)
+    if (pl.wide) return bwd<T, 8, 4, 1, 2, false, 512, false>(a, pl, part, st);
   if constexpr (VEC == 1)
     if (pl.narrow) return bwd<T, 1, 8, 1, kBwdStages, true, 512, true>(a, pl, part, st);
   return bwd<T, VEC, 16 / VEC, VEC == 8 ? 2 : 1, kBwdStages, true, 512, VEC == 1>(a, pl, part, st);
