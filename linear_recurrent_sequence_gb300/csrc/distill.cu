@@ -65,21 +65,24 @@ __device__ __forceinline__ void read_ids(const DistillArgs &a, long long r, cons
                                          unsigned *bits, int words, ListShared &sh) {
   constexpr int kVec = LogitRow<T>::kVec;
   const int lane = threadIdx.x & 31;
+  bool outside = false, repeated = false;
+  long long v[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const long long k = r * a.top + lane + 32 * i;
+    v[i] = -1;
+    if (lane + 32 * i < a.top)
+      v[i] = a.id64 ? reinterpret_cast<const long long *>(a.ids)[k] : (long long)reinterpret_cast<const int *>(a.ids)[k];
+  }
+  // (while the ids are on their way)
   for (int i = lane; i < words / 4; i += 32) reinterpret_cast<uint4 *>(bits)[i] = make_uint4(0, 0, 0, 0);
   __syncwarp();
-  bool outside = false, repeated = false;
   int id[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int k = lane + 32 * i;
-    id[i] = -1;
-    if (k < a.top) {
-      const long long v = a.id64 ? reinterpret_cast<const long long *>(a.ids)[r * a.top + k]
-                                 : (long long)reinterpret_cast<const int *>(a.ids)[r * a.top + k];
-      outside |= v >= a.V;
-      if (v >= 0 && v < a.V) id[i] = (int)v;
-    }
-    sh.id[k] = id[i];
+    outside |= v[i] >= a.V;
+    id[i] = v[i] >= 0 && v[i] < a.V ? (int)v[i] : -1;
+    sh.id[lane + 32 * i] = id[i];
   }
 #pragma unroll
   for (int i = 0; i < kPer; ++i)
