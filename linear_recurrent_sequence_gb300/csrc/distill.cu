@@ -28,11 +28,12 @@ constexpr int kMaxTop = RETNET_MAX_TOP;
 
 constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
 constexpr int kThreads = kRowThreads + 32;  // and the list's warp
+constexpr int kRowBits = 65536;             // tokens up to which the row has its bits
 constexpr int kPer = kMaxTop / 32;          // its entries a lane: lane + 32 i
 
 // The list of a row.
 struct ListShared {
-  int id[kMaxTop];      // the token, or -1: absent, out of range, listed before
+  alignas(16) int id[kMaxTop];  // the token, or -1: absent, out of range, listed before
   float x[kMaxTop];     // the student's logit
   float p[kMaxTop];     // the teacher's probability and its logarithm
   float ln_p[kMaxTop];
@@ -57,15 +58,35 @@ __device__ __forceinline__ float loss_term(float p, float ln_p, float ln_q) {
   return __fmul_rn(p, g);  // (no contraction: the same bits wherever this is inlined)
 }
 
-// The list warp: the tokens of row r, and the bit of each in `bits`.  Bit
-// position of token i: i - head + kVec, so that vector v of the row has the kVec
-// bits from (v + 1) kVec.
+// A bit for each token of the row, or of the CTA's slice alone where those of
+// the row would leave fewer CTAs an SM (1500 x 131072 bf16, loss and gradient:
+// 151 us, with the row's 195).  The row's own tell whether a token is listed
+// twice, which the list warp has to look for otherwise (4096 x 65536: 195 us,
+// with the slice's 197).  Vector v of the row has the kVec bits from (v - v0 +
+// 1) kVec, v0 the slice's first or 0.
+struct ListBits {
+  unsigned *words;
+  int n, v0;
+  bool row;
+  template <typename T>
+  __device__ __forceinline__ ListBits(unsigned *w, int count, const LogitRow<T> &r, const RowSlice &slice)
+      : words(w), n(count), v0(0), row(count * 32 >= r.V + 2 * LogitRow<T>::kVec) {
+    if (!row) v0 = slice.v0;
+  }
+  // Where token i has its bit.
+  template <typename T>
+  __device__ __forceinline__ int at(const LogitRow<T> &r, int i) const {
+    return i - r.index(v0) + LogitRow<T>::kVec;
+  }
+};
+
+// The list warp: the tokens of row r and their bits.  Returns whether one may be
+// listed twice.
 template <typename T>
-__device__ __forceinline__ void read_ids(const DistillArgs &a, long long r, const LogitRow<T> &row,
-                                         unsigned *bits, int words, ListShared &sh) {
-  constexpr int kVec = LogitRow<T>::kVec;
+__device__ __forceinline__ bool read_ids(const DistillArgs &a, long long r, const LogitRow<T> &row,
+                                         const RowSlice &slice, const ListBits &bits, ListShared &sh) {
   const int lane = threadIdx.x & 31;
-  bool outside = false, repeated = false;
+  bool outside = false, repeated = !bits.row;
   long long v[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -75,33 +96,42 @@ __device__ __forceinline__ void read_ids(const DistillArgs &a, long long r, cons
       v[i] = a.id64 ? reinterpret_cast<const long long *>(a.ids)[k] : (long long)reinterpret_cast<const int *>(a.ids)[k];
   }
   // (while the ids are on their way)
-  for (int i = lane; i < words / 4; i += 32) reinterpret_cast<uint4 *>(bits)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = lane; i < bits.n / 4; i += 32) reinterpret_cast<uint4 *>(bits.words)[i] = make_uint4(0, 0, 0, 0);
   __syncwarp();
-  int id[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     outside |= v[i] >= a.V;
-    id[i] = v[i] >= 0 && v[i] < a.V ? (int)v[i] : -1;
-    sh.id[lane + 32 * i] = id[i];
+    const int id = v[i] >= 0 && v[i] < a.V ? (int)v[i] : -1;
+    sh.id[lane + 32 * i] = id;
+    if (id >= 0 && (bits.row || slice.has(row, id))) {
+      const int at = bits.at(row, id);
+      repeated |= (atomicOr(&bits.words[at >> 5], 1u << (at & 31)) >> (at & 31) & 1u) != 0;
+    }
   }
+  outside = __any_sync(0xffffffffu, outside);
+  if (lane == 0) sh.outside = outside;
+  return __any_sync(0xffffffffu, repeated);
+}
+
+// The list warp: of a token that is listed more than once the first entry counts.
+__device__ __forceinline__ void drop_repeated(const DistillArgs &a, ListShared &sh) {
+  const int lane = threadIdx.x & 31;
+  bool again[kPer] = {};
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (32 * i >= a.top) break;
+    const int id = sh.id[lane + 32 * i];
+    again[i] = (__match_any_sync(0xffffffffu, id) & ((1u << lane) - 1)) != 0;
+    for (int j = 0; j < 32 * i; j += 4) {
+      const int4 q = *reinterpret_cast<const int4 *>(sh.id + j);
+      again[i] |= q.x == id || q.y == id || q.z == id || q.w == id;
+    }
+  }
+  __syncwarp();
 #pragma unroll
   for (int i = 0; i < kPer; ++i)
-    if (id[i] >= 0) {
-      const int at = id[i] - row.head + kVec;
-      repeated |= (atomicOr(&bits[at >> 5], 1u << (at & 31)) >> (at & 31) & 1u) != 0;
-    }
-  outside = __any_sync(0xffffffffu, outside);
-  if (__any_sync(0xffffffffu, repeated)) {  // (also orders the ids' stores before their loads)
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      for (int j = 0; j < lane + 32 * i; ++j)
-        if (sh.id[j] == id[i]) id[i] = -1;
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) sh.id[lane + 32 * i] = id[i];
-  }
-  if (lane == 0) sh.outside = outside;
+    if (again[i]) sh.id[lane + 32 * i] = -1;
   __syncwarp();
 }
 
@@ -318,10 +348,6 @@ struct RestGradient {
 // kGroups groups of kUnroll vectors a thread.
 constexpr int kGroups = 4;
 constexpr int kSliceBytes = kGroups * kUnroll * kRowThreads * 16;
-// Shared memory of a CTA of which three fit an SM.  (1500 x 131072 bf16, whose
-// bits would leave two: 198 us with the second reading from L2, 209 staged;
-// 4096 x 65536: 262 and 208.)
-constexpr size_t kStagedMost = 73 * 1024;
 
 template <typename T>
 struct StagedSlice {
@@ -456,7 +482,6 @@ distill_kernel(const DistillArgs a, int words) {
   __shared__ ListShared sh;
   pdl_launch_dependents();
   pdl_wait();
-  unsigned *bits = reinterpret_cast<unsigned *>(dyn);
   StagedSlice<T> staged(dyn + (size_t)words * 4);
   const uint32_t ctas = cluster_size(), rank = cluster_rank();
   const int tid = threadIdx.x, lane = tid & 31;
@@ -464,6 +489,7 @@ distill_kernel(const DistillArgs a, int words) {
   for (long long r = blockIdx.x / ctas; r < a.rows; r += gridDim.x / ctas) {
     const LogitRow<T> row(reinterpret_cast<const T *>(a.x) + row_offset(a.sx, r), a.V);
     const RowSlice slice(row, ctas, rank);
+    const ListBits bits(reinterpret_cast<unsigned *>(dyn), words, row, slice);
     T *dx = kBwd ? reinterpret_cast<T *>(a.dx) + row_offset(a.sd, r) : nullptr;
     const float weight = kBwd && a.weight ? a.weight[r] : 1.f;
     const bool zero = kBwd && weight == 0.f;
@@ -479,8 +505,9 @@ distill_kernel(const DistillArgs a, int words) {
 #pragma unroll
       for (int j = 0; j < kPer; ++j)
         values[j] = lane + 32 * j < a.top ? a.values[r * a.top + lane + 32 * j] : -INFINITY;
-      read_ids(a, r, row, bits, words, sh);
+      const bool repeated = read_ids(a, r, row, slice, bits, sh);
       if (kFwd) list_ready();
+      if (repeated) drop_repeated(a, sh);
       read_logits(a, row, sh, [&](int id) { return kFwd || slice.has(row, id); });
       // (the gradient alone may be written over the logits: only from here on)
       if (!kFwd && !kTail) list_ready();
@@ -502,9 +529,10 @@ distill_kernel(const DistillArgs a, int words) {
       wait_list();  // for the bits; for the gradient alone: its logits, with the rest bucket p_rest
       if (kFwd) {
         // the softmax of the tokens that are not listed
-        const uint8_t *bytes = reinterpret_cast<const uint8_t *>(bits);
+        const uint8_t *bytes = reinterpret_cast<const uint8_t *>(bits.words);
         auto hide = [&](int at, LogitVec<T> &v) {
-          const unsigned hit = kVec == 8 ? bytes[at + 1] : (bytes[(at + 1) >> 1] >> (4 * ((at + 1) & 1))) & 15u;
+          const int n = at - bits.v0 + 1;
+          const unsigned hit = kVec == 8 ? bytes[n] : (bytes[n >> 1] >> (4 * (n & 1))) & 15u;
           if (hit)
             for (int e = 0; e < kVec; ++e)
               if (hit >> e & 1u) v.mask(e);
@@ -548,8 +576,8 @@ distill_kernel(const DistillArgs a, int words) {
           while (i < slice.v1) group(0, false);
         }
         if (tid < 32) {
-          const int single = slice.single(row), at = single - row.head + kVec;
-          const bool counts = single >= 0 && !(bits[at >> 5] >> (at & 31) & 1u);
+          const int single = slice.single(row), at = bits.at(row, single);
+          const bool counts = single >= 0 && !(bits.words[at >> 5] >> (at & 31) & 1u);
           acc.single<false>(counts ? logit_of(row.p[single]) : -INFINITY, sc);
         }
         part = acc.all<false>(sc);
@@ -609,8 +637,7 @@ cudaError_t launch_as(const DistillArgs &a, int ctas, size_t smem, int words, cu
 
 template <typename T, int kWhat>
 cudaError_t launch(const DistillArgs &a, cudaStream_t st) {
-  const int words = ((a.V + 2 * LogitRow<T>::kVec + 31) / 32 + 3) / 4 * 4;
-  const size_t bits = (size_t)words * 4;
+  constexpr int kVec = LogitRow<T>::kVec;
   const long long row_bytes = (long long)a.V * sizeof(T);
   const int sms = device_sms();
   // A slice that fits in shared memory while a cluster of 8 can share the row
@@ -618,10 +645,13 @@ cudaError_t launch(const DistillArgs &a, cudaStream_t st) {
   // both calls give the same bits).
   int ctas = row_ctas(a.rows, row_bytes, kWhat == kDistillBwd ? 1LL << 40 : kSliceBytes,
                       (kWhat == kDistillBwd ? 4LL : 3LL) * sms);
+  const int vecs = (a.V / kVec + ctas - 1) / ctas;  // of a slice
+  auto words_of = [](int tokens) { return ((tokens + 2 * kVec + 31) / 32 + 3) / 4 * 4; };
+  const int words = words_of(a.V <= kRowBits ? a.V : vecs * kVec);
+  const size_t bits = (size_t)words * 4;
   if constexpr (kWhat == kDistillStep) {
-    const long long vecs = (row_bytes / 16 + ctas - 1) / ctas;
-    const size_t smem = bits + (size_t)((vecs + kRowThreads - 1) / kRowThreads) * kRowThreads * 16;
-    if (vecs * 16 <= kSliceBytes && smem <= kStagedMost) {
+    if (vecs * 16 <= kSliceBytes) {
+      const size_t smem = bits + (size_t)((vecs + kRowThreads - 1) / kRowThreads) * kRowThreads * 16;
       return a.tail ? launch_as<T, kDistillStep, true, true>(a, ctas, smem, words, st)
                     : launch_as<T, kDistillStep, false, true>(a, ctas, smem, words, st);
     }
