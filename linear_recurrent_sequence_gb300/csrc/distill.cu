@@ -80,13 +80,14 @@ struct ListBits {
   }
 };
 
-// The list warp: the tokens of row r and their bits.  Returns whether one may be
-// listed twice.
-template <typename T>
-__device__ __forceinline__ bool read_ids(const DistillArgs &a, long long r, const LogitRow<T> &row,
-                                         const RowSlice &slice, const ListBits &bits, ListShared &sh) {
+// The list warp: the tokens of row r and their bits.  each(i, id) for the
+// lane's entries; outside: one of them is past the vocabulary; repeated: one of
+// them may be listed twice.
+template <typename T, typename F>
+__device__ __forceinline__ void read_ids(const DistillArgs &a, long long r, const LogitRow<T> &row,
+                                         const RowSlice &slice, const ListBits &bits, ListShared &sh,
+                                         bool &outside, bool &repeated, F each) {
   const int lane = threadIdx.x & 31;
-  bool outside = false, repeated = !bits.row;
   long long v[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -103,14 +104,12 @@ __device__ __forceinline__ bool read_ids(const DistillArgs &a, long long r, cons
     outside |= v[i] >= a.V;
     const int id = v[i] >= 0 && v[i] < a.V ? (int)v[i] : -1;
     sh.id[lane + 32 * i] = id;
+    each(i, id);
     if (id >= 0 && (bits.row || slice.has(row, id))) {
       const int at = bits.at(row, id);
       repeated |= (atomicOr(&bits.words[at >> 5], 1u << (at & 31)) >> (at & 31) & 1u) != 0;
     }
   }
-  outside = __any_sync(0xffffffffu, outside);
-  if (lane == 0) sh.outside = outside;
-  return __any_sync(0xffffffffu, repeated);
 }
 
 // The list warp: of a token that is listed more than once the first entry counts.
@@ -135,21 +134,12 @@ __device__ __forceinline__ void drop_repeated(const DistillArgs &a, ListShared &
   __syncwarp();
 }
 
-// The list warp: the listed logits and their softmax.  `wants(id)`: whether
-// this CTA uses the token's logit.  (The gradient alone uses those of its own
-// slice: where it is written over the logits, another CTA may be past its
-// slice already.)
-template <typename T, typename F>
-__device__ __forceinline__ void read_logits(const DistillArgs &a, const LogitRow<T> &row,
-                                            ListShared &sh, F wants) {
+// The list warp: the listed logits x (-infinity where there is none) and their
+// softmax.
+__device__ __forceinline__ void listed_softmax(const DistillArgs &a, ListShared &sh, const float (&x)[kPer]) {
   const int lane = threadIdx.x & 31;
-  float x[kPer], m = -INFINITY, z = 0.f;
+  float m = -INFINITY, z = 0.f;
   bool bad = false;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int id = sh.id[lane + 32 * i];
-    x[i] = id >= 0 && wants(id) ? logit_of(row.p[id]) : -INFINITY;
-  }
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     sh.x[lane + 32 * i] = x[i];
@@ -466,12 +456,10 @@ __device__ __forceinline__ void fill_slice(const LogitRow<T> &row, const RowSlic
   for (int i = i0 + threadIdx.x; i < i1; i += kRowThreads) one.store(dx + i);
 }
 
-// Barrier 1: the list is ready.  Its warp goes on without waiting.
-__device__ __forceinline__ void list_ready() {
-  __threadfence_block();
-  asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory");
-}
-__device__ __forceinline__ void wait_list() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+// Barrier 1: the list is ready.  (Its warp waits too, which orders its shared
+// memory for the others; to arrive after a fence instead would wait for all of
+// its loads: 4096 x 65536 bf16, loss and gradient, 195 us.)
+__device__ __forceinline__ void list_ready() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
 
 template <typename T, int kWhat, bool kTail, bool kStaged>
 __global__ void __launch_bounds__(kThreads, kStaged ? 3 : kWhat == kDistillFwd ? 6 : 4)
@@ -505,10 +493,32 @@ distill_kernel(const DistillArgs a, int words) {
 #pragma unroll
       for (int j = 0; j < kPer; ++j)
         values[j] = lane + 32 * j < a.top ? a.values[r * a.top + lane + 32 * j] : -INFINITY;
-      const bool repeated = read_ids(a, r, row, slice, bits, sh);
+      // The listed logits: for the loss after the list is ready, which the walk
+      // waits for (before: 4096 x 65536 bf16, loss and gradient, 205 us, so 195);
+      // for the gradient alone at once (2048 x 65536: 89 us, later 92), and only
+      // those of the CTA's own slice: where it is written over the logits,
+      // another CTA may be past its slice already.
+      T raw[kPer];
+      auto gather = [&](int j, int id) {
+        raw[j] = T(-INFINITY);
+        if (id >= 0 && (kFwd || slice.has(row, id))) raw[j] = row.p[id];
+      };
+      bool outside = false, repeated = !bits.row;
+      read_ids(a, r, row, slice, bits, sh, outside, repeated, [&](int j, int id) {
+        if (!kFwd) gather(j, id);
+      });
       if (kFwd) list_ready();
-      if (repeated) drop_repeated(a, sh);
-      read_logits(a, row, sh, [&](int id) { return kFwd || slice.has(row, id); });
+      outside = __any_sync(0xffffffffu, outside);
+      if (lane == 0) sh.outside = outside;
+      if (__any_sync(0xffffffffu, repeated)) drop_repeated(a, sh);
+      float x[kPer];
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int id = sh.id[lane + 32 * j];
+        if (kFwd) gather(j, id);
+        x[j] = id >= 0 ? logit_of(raw[j]) : -INFINITY;
+      }
+      listed_softmax(a, sh, x);
       // (the gradient alone may be written over the logits: only from here on)
       if (!kFwd && !kTail) list_ready();
       teacher(a, values, sh);
@@ -526,7 +536,7 @@ distill_kernel(const DistillArgs a, int words) {
             ahead[kStaged ? 0 : j].fill_masked();
         }
       }
-      wait_list();  // for the bits; for the gradient alone: its logits, with the rest bucket p_rest
+      list_ready();  // for the bits; for the gradient alone: its logits, with the rest bucket p_rest
       if (kFwd) {
         // the softmax of the tokens that are not listed
         const uint8_t *bytes = reinterpret_cast<const uint8_t *>(bits.words);
