@@ -12,10 +12,17 @@
 // 1 - sum q_k.
 //
 // Bound by memory: the loss reads each logit once, the gradient reads it and
-// writes a value.  Eight warps of a CTA walk over its slice of the row while a
-// ninth reads the list, gathers its logits and forms the teacher's
-// probabilities; the listed logits' own softmax joins the others', so that the
-// gradient can start at once while the ninth warp adds up the loss.
+// writes a value.  bf16, a list of 64: the loss of 1024 x 65536 27.4 us, 4.9 TB/s;
+// the gradient of 2048 x 65536 89 us, 6.0 TB/s; both of 4096 x 65536 197 us, 5.5
+// TB/s (with a second reading from the L2 instead of shared memory 262 us); 8 x
+// 32768 6 us, latency.
+//
+// Eight warps of a CTA walk over its slice of the row while a ninth reads the
+// list, gathers its logits and forms the teacher's probabilities; the listed
+// logits' own softmax joins the others', so that the gradient can start at once
+// while the ninth warp adds up the loss.  The walk waits for the list's bits:
+// clearing them while the ids are on their way, and not before, made 210 us of
+// loss and gradient into 195.
 #include "launch.h"
 #include "logits.cuh"
 
@@ -60,9 +67,8 @@ __device__ __forceinline__ float loss_term(float p, float ln_p, float ln_q) {
 
 // A bit for each token of the row, or of the CTA's slice alone where those of
 // the row would leave fewer CTAs an SM (1500 x 131072 bf16, loss and gradient:
-// 151 us, with the row's 195).  The row's own tell whether a token is listed
-// twice, which the list warp has to look for otherwise (4096 x 65536: 195 us,
-// with the slice's 197).  Vector v of the row has the kVec bits from (v - v0 +
+// 152 us, with the row's 195).  The row's own tell whether a token is listed
+// twice, which the list warp has to look for otherwise (4096 x 65536 2 us more).  Vector v of the row has the kVec bits from (v - v0 +
 // 1) kVec, v0 the slice's first or 0.
 struct ListBits {
   unsigned *words;
@@ -458,9 +464,11 @@ __device__ __forceinline__ void fill_slice(const LogitRow<T> &row, const RowSlic
 
 // Barrier 1: the list is ready.  (Its warp waits too, which orders its shared
 // memory for the others; to arrive after a fence instead would wait for all of
-// its loads: 4096 x 65536 bf16, loss and gradient, 195 us.)
+// its loads.)
 __device__ __forceinline__ void list_ready() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
 
+// CTAs an SM: three where their slices fill its shared memory, four for the
+// gradient alone, six (40 registers a thread) for the loss alone.
 template <typename T, int kWhat, bool kTail, bool kStaged>
 __global__ void __launch_bounds__(kThreads, kStaged ? 3 : kWhat == kDistillFwd ? 6 : 4)
 distill_kernel(const DistillArgs a, int words) {
@@ -494,7 +502,7 @@ distill_kernel(const DistillArgs a, int words) {
       for (int j = 0; j < kPer; ++j)
         values[j] = lane + 32 * j < a.top ? a.values[r * a.top + lane + 32 * j] : -INFINITY;
       // The listed logits: for the loss after the list is ready, which the walk
-      // waits for (before: 4096 x 65536 bf16, loss and gradient, 205 us, so 195);
+      // waits for (before: 4096 x 65536 bf16, loss and gradient, 205 us, so 197);
       // for the gradient alone at once (2048 x 65536: 89 us, later 92), and only
       // those of the CTA's own slice: where it is written over the logits,
       // another CTA may be past its slice already.
