@@ -378,7 +378,9 @@ ret_status retnet_decode_step(const retnet_stack_desc *d, const retnet_layer_wei
  * logits[:, :-1] of a [B, N, V] tensor); a row's values are contiguous.  Rows
  * of an output must not overlap one another (RET_EINVAL).  Per-row vectors
  * (mean, loss, ...) are contiguous [n0 n1].  No row, stride or base pointer
- * needs more than its element's alignment (16-byte aligned rows run faster).
+ * needs more than its element's alignment (16-byte aligned rows run faster;
+ * LayerNorm reads others in the aligned 16-byte words that cover them, so the
+ * bytes of the first word before a row are read too, and not looked at).
  * None of these calls changes an input. */
 
 /* LayerNorm of each row of d values (1 <= d <= 2^24; fp32 arithmetic):

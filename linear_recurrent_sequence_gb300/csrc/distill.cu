@@ -468,7 +468,8 @@ __device__ __forceinline__ void fill_slice(const LogitRow<T> &row, const RowSlic
 __device__ __forceinline__ void list_ready() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
 
 // CTAs an SM: three where their slices fill its shared memory, four for the
-// gradient alone, six (40 registers a thread) for the loss alone.
+// gradient alone, six for the loss alone (1024 x 65536 bf16 27.4 us, with four
+// 33.8).
 template <typename T, int kWhat, bool kTail, bool kStaged>
 __global__ void __launch_bounds__(kThreads, kStaged ? 3 : kWhat == kDistillFwd ? 6 : 4)
 distill_kernel(const DistillArgs a, int words) {
