@@ -166,6 +166,39 @@ def test_in_place(R, dtype, V, tail):
 
 
 @pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dtype,V", [(torch.bfloat16, 70001), (torch.float32, 70001), (torch.bfloat16, 131080),
+                                     (torch.float32, 300007)])
+def test_repeated_ids_and_in_place_in_large_vocabularies(R, dtype, V, tail):
+    """Entries of one token far apart in the list (the first counts, the same
+    bits as without the others), at both ends of the row and between, and
+    gradients over the logits where several CTAs share a row."""
+    g = gen(V)
+    x = (2.0 * randn(g, 2, V + 3)).to(dtype)[:, 3:]
+    ids, values = teacher_of(g, x, 100, 1.0, tail)
+    ids[0, :4] = torch.tensor([V - 1, 0, V // 2, V // 2 + 1], device="cuda")
+    for r in range(2):  # distinct to begin with
+        seen = set()
+        for j, i in enumerate(ids[r].tolist()):
+            if i in seen:
+                ids[r, j] = -1
+            seen.add(i)
+    ids[0, [40, 95]], ids[0, 64], ids[1, [1, 33, 99]] = V - 1, V // 2, -1
+    once = ids.clone()
+    once[0, [40, 95, 64]] = -1
+    loss, stats, grad, grad2 = check(R, x, once, values, 1.0, tail)
+    twice = R.distill_fwd(x, ids, values, tail=tail)
+    assert torch.equal(twice[0], loss) and torch.equal(twice[1], stats)
+    assert torch.equal(R.distill_bwd(x, ids, values, None, stats, tail=tail), grad)
+    assert torch.equal(R.distill_step(x, ids, values, tail=tail)[1], grad2)
+    # copies whose rows lie as x's do: where a row begins in its first 16 bytes
+    # decides in which order it is summed
+    a, b = (torch.empty(2, V + 3, dtype=dtype, device="cuda")[:, 3:].copy_(x) for _ in range(2))
+    assert torch.equal(R.distill_bwd(a, ids, values, None, stats, tail=tail, dstudent=a), grad)
+    R.distill_step(b, ids, values, tail=tail, dstudent=b)
+    assert torch.equal(b, grad2)
+
+
+@pytest.mark.parametrize("tail", [False, True])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_masked_tokens_and_short_lists(R, dtype, tail):
     """-inf and lowest-value logits, absent entries, an empty list, repeated

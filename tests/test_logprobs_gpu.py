@@ -89,6 +89,22 @@ def test_sizes(R, dtype, rows, V, top):
     check(R, logits(g, rows, V, dtype=dtype), top)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,V,top", [(1000, 20011, 5), (400, 9001, 100), (200, 40011, 40),
+                                        (330, 2001, 33), (290, 20000, 2)])
+def test_many_rows_with_masks_and_ties(R, dtype, rows, V, top):
+    """Rows in several turns of the CTAs; among them rows with masked tokens,
+    with the type's lowest value, masked throughout, and of few distinct values."""
+    g = gen(rows + V)
+    x = logits(g, rows, V, dtype=dtype)
+    x[1::7] = torch.where(torch.rand(x[1::7].shape, generator=g, device="cuda") < 0.5, -INF, x[1::7].float()).to(dtype)
+    x[2::7, V // 2:] = torch.finfo(dtype).min
+    x[3::7] = -INF
+    x[4::7] = x[4::7].round()
+    x[5::7] = 1.5
+    check(R, x, top, tokens=torch.randint(0, V // 2, (rows,), generator=g, device="cuda"))
+
+
 @pytest.mark.parametrize("T", [0.01, 0.7, 3.0, 100.0])
 def test_temperature(R, T):
     g = gen(2)
