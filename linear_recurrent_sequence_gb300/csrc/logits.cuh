@@ -109,14 +109,15 @@ struct Softmax {
   int bad;
 };
 
-// The temperature's scale log2(e) / T and what follows from it: scaled logits
-// up to `high` in size keep y = x scale - m scale well inside fp32, and `low`
-// stands for a logit below it (its 2^y is 0, and y 2^y is not infinity times
-// zero as it would be for -infinity).
+// The temperature's scale log2(e) / T and what follows from it.  Up to `high`
+// in size a maximum m has m scale within 2^22, so that the product's rounding,
+// which the exponents below carry until all() takes it out, is at most 1/8.
+// `low` stands for a logit below it (its 2^y is 0, and y 2^y is not infinity
+// times zero as it would be for -infinity).
 struct Scale {
   float scale, high, low;
   __device__ __forceinline__ explicit Scale(float sc)
-      : scale(sc), high(1e30f / fmaxf(sc, 1.f)), low(-1e36f / fmaxf(sc, 1.f)) {}
+      : scale(sc), high(4194304.f / sc), low(-1e36f / fmaxf(sc, 1.f)) {}
 };
 
 // The softmax of the values that a warp's threads walk over.  m is the same in
@@ -125,8 +126,9 @@ struct Scale {
 // and seldom; the sums are packed pairs of a lane's own.
 // One fused multiply-add gives a pair's exponents: they are relative to the
 // rounded product m scale, which all() corrects.  Where the maximum is beyond
-// `high` (a row masked throughout with the type's lowest value) the product
-// would overflow, and the difference is taken first.
+// `high` (so far only values of a finite mask, or a low temperature) the
+// rounding would be as large as any exponent, and the difference is taken
+// first; the exponents are then relative to m itself.
 struct WarpSoftmax {
   float m = -INFINITY, own = -INFINITY;  // own: the lane's largest value, NaN if it met one
   float2 s = {0.f, 0.f}, u = {0.f, 0.f};
@@ -135,7 +137,7 @@ struct WarpSoftmax {
   __device__ __forceinline__ void group(const LogitVec<T> (&v)[N], const Scale &c) {
     const float top = LogitVec<T>::max_of(v);
     own = max_nan(own, top);
-    raise<kEntropy>(redux_max(top), c.scale);
+    raise<kEntropy>(redux_max(top), c);
     constexpr int kVec = 16 / (int)sizeof(T);
     if (fabsf(m) <= c.high) {
       const float2 sc2 = make_float2(c.scale, c.scale), mm2 = make_float2(-__fmul_rn(m, c.scale), -__fmul_rn(m, c.scale));
@@ -162,7 +164,7 @@ struct WarpSoftmax {
   template <bool kEntropy>
   __device__ __forceinline__ void single(float x, const Scale &c) {
     own = max_nan(own, x);
-    raise<kEntropy>(redux_max(x), c.scale);
+    raise<kEntropy>(redux_max(x), c);
     if (fabsf(m) <= c.high)
       take<kEntropy>(make_float2(fmaf(fmaxf(x, c.low), c.scale, -__fmul_rn(m, c.scale)), -1000.f));
     else if (m > -INFINITY)
@@ -185,12 +187,19 @@ struct WarpSoftmax {
   }
 
  private:
+  // The exponent that moves the sums from m to `top`, each as group() refers to it.
+  __device__ __forceinline__ float shift(float top, const Scale &c) const {
+    const float pm = __fmul_rn(m, c.scale), pt = __fmul_rn(top, c.scale);
+    const bool near_m = fabsf(m) <= c.high, near_top = fabsf(top) <= c.high;
+    if (near_m) return near_top ? __fsub_rn(pm, pt) : -fmaf(top, c.scale, -pm);
+    return near_top ? fmaf(m, c.scale, -pt) : __fmul_rn(__fsub_rn(m, top), c.scale);
+  }
   template <bool kEntropy>
-  __device__ __forceinline__ void raise(float top, float scale) {
+  __device__ __forceinline__ void raise(float top, const Scale &c) {
     if (!(top > m)) return;
     if (m > -INFINITY) {
       // (a difference of infinities is one of values far apart: -1000 too)
-      const float dy = fmaxf(__fsub_rn(__fmul_rn(m, scale), __fmul_rn(top, scale)), -1000.f), f = ex2(dy);
+      const float dy = fmaxf(shift(top, c), -1000.f), f = ex2(dy);
       const float2 f2 = make_float2(f, f);
       if (kEntropy) u = tc::mul2(tc::fma2(make_float2(dy, dy), s, u), f2);
       s = tc::mul2(s, f2);
