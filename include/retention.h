@@ -469,6 +469,8 @@ ret_status retnet_token_logprobs(const retnet_logits_desc *d, const void *x, con
  * _fwd writes loss and stats [n0 n1][2] = ln sum e^(x/T) over the vocabulary
  * and over the tokens that are not listed (either may be NULL); _bwd takes
  * stats and writes dx; _step does both and reads each row from memory once.
+ * Where a row's stats are beyond 256 in size, too coarse in fp32 for its
+ * probabilities, _bwd forms them again from x (a second reading).
  * dx may be x itself.  V <= RETNET_MAX_DISTILL_V (else RET_EUNSUPPORTED). */
 ret_status retnet_distill_fwd(const retnet_logits_desc *d, const void *x, const void *ids,
                               const float *values, float *loss, float *stats,

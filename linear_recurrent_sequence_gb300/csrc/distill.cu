@@ -84,6 +84,23 @@ struct ListBits {
   __device__ __forceinline__ int at(const LogitRow<T> &r, int i) const {
     return i - r.index(v0) + LogitRow<T>::kVec;
   }
+  // Masks the listed tokens of vector v.
+  template <typename T>
+  __device__ __forceinline__ void hide(int v, LogitVec<T> &x) const {
+    constexpr int kVec = LogitRow<T>::kVec;
+    const uint8_t *bytes = reinterpret_cast<const uint8_t *>(words);
+    const int n = v - v0 + 1;
+    const unsigned hit = kVec == 8 ? bytes[n] : (bytes[n >> 1] >> (4 * (n & 1))) & 15u;
+    if (hit)
+      for (int e = 0; e < kVec; ++e)
+        if (hit >> e & 1u) x.mask(e);
+  }
+  // The logit of token i, -infinity where it is listed (or i negative).
+  template <typename T>
+  __device__ __forceinline__ float unlisted(const LogitRow<T> &r, int i) const {
+    const int b = at(r, i);
+    return i >= 0 && !(words[b >> 5] >> (b & 31) & 1u) ? logit_of(r.p[i]) : -INFINITY;
+  }
 };
 
 // The list warp: the tokens of row r and their bits.  each(i, id) for the
@@ -254,18 +271,21 @@ struct RowConstants {
   bool bad, empty;
 };
 
-// From the softmax `rest` of the tokens that are not listed and that of the
-// listed ones.
-__device__ __forceinline__ RowConstants row_constants(const DistillArgs &a, float weight,
+// The softmax of all tokens from that of those not listed and the listed ones'.
+__device__ __forceinline__ Softmax whole_row(const Softmax &rest, const Softmax &top, float scale) {
+  const float m = fmaxf(rest.m, top.m), to = m > -INFINITY ? m : 0.f;
+  const float z = fmaf(rest.s, ex2((rest.m - to) * scale), __fmul_rn(top.s, ex2((top.m - to) * scale)));
+  return {m, z, 0.f, rest.bad || top.bad};
+}
+
+// From the softmax of all tokens and that of those not listed.
+__device__ __forceinline__ RowConstants row_constants(const DistillArgs &a, float weight, const Softmax &all,
                                                       const Softmax &rest, const ListShared &sh) {
   RowConstants k;
-  const Softmax top = sh.top;
-  const float m = fmaxf(rest.m, top.m);
-  k.bad = rest.bad || top.bad || sh.outside;
-  k.empty = m == -INFINITY;
-  k.a = k.empty ? 0.f : m;
-  const float z = fmaf(rest.s, ex2((rest.m - k.a) * a.scale), __fmul_rn(top.s, ex2((top.m - k.a) * a.scale)));
-  k.b = k.empty ? 0.f : log2f(z);
+  k.bad = all.bad || sh.outside;
+  k.empty = all.m == -INFINITY;
+  k.a = k.empty ? 0.f : all.m;
+  k.b = k.empty ? 0.f : log2f(all.s);
   const bool none = sh.no_teacher || (k.empty && !k.bad), some = rest.s > 0.f;
   k.a_rest = some ? rest.m : 0.f;
   k.b_rest = some ? log2f(rest.s) : 0.f;
@@ -275,11 +295,24 @@ __device__ __forceinline__ RowConstants row_constants(const DistillArgs &a, floa
   return k;
 }
 
+// The saved statistics are fp32 numbers of the size of x / T, and their rounding
+// is a relative error of q: 2^-16 for those up to 256, the largest that are used.
+// Beyond (a level, a finite mask, a low temperature) the row is walked over
+// before its gradient, as for loss and gradient together: 2048 x 65536 bf16 170
+// us where all rows are such, with the rest bucket 254 (90 and 95 us else).
+constexpr float kSavedMost = 256.f;
+
+// (NaN: a row that has no distribution, known from them.)
+template <bool kTail>
+__device__ __forceinline__ bool saved_too_coarse(float lse, float lse_rest, const ListShared &sh) {
+  if (lse != lse) return false;
+  return !(fabsf(lse) <= kSavedMost) || (kTail && sh.p_rest > 0.f && !(fabsf(lse_rest) <= kSavedMost));
+}
+
 // From the statistics that the forward saved.
-__device__ __forceinline__ RowConstants saved_constants(const DistillArgs &a, long long r, float weight,
+__device__ __forceinline__ RowConstants saved_constants(const DistillArgs &a, float lse, float lse_rest, float weight,
                                                         bool outside, bool no_teacher, float p_rest) {
   RowConstants k;
-  const float lse = a.stats[2 * r], lse_rest = a.stats[2 * r + 1];
   const float w = weight * a.t;
   const bool none = no_teacher || lse == -INFINITY;
   const bool no_rest = none || lse_rest == -INFINITY;
@@ -452,6 +485,42 @@ __device__ __forceinline__ void write_gradient(const LogitRow<T> &row, const Row
   }
 }
 
+// The softmax of the row's tokens (kRest: of those that are not listed), by all
+// of its CTAs' threads, a vector at a time: for the few rows whose saved
+// statistics do not serve.
+template <typename T, bool kRest>
+__device__ __forceinline__ Softmax walk_again(const LogitRow<T> &row, const RowSlice &slice, const ListBits &bits,
+                                              float scale, uint32_t ctas, ListShared &sh) {
+  Softmax part = {-INFINITY, 0.f, 0.f, 0};
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (tid < kRowThreads) {
+    const Scale sc(scale);
+    WarpSoftmax acc;
+#pragma unroll 1
+    for (int i = slice.v0 + (tid & ~31); i < slice.v1; i += kRowThreads) {
+      LogitVec<T> v[1];
+      v[0].fill_masked();
+      if (i + lane < slice.v1) {
+        v[0].load(row.p + row.index(i + lane));
+        if (kRest) bits.hide(i + lane, v[0]);
+      }
+      acc.group<T, 1, false>(v, sc);
+    }
+    if (tid < 32) {
+      const int single = slice.single(row);
+      acc.single<false>(kRest ? bits.unlisted(row, single) : single >= 0 ? logit_of(row.p[single]) : -INFINITY, sc);
+    }
+    part = acc.all<false>(sc);
+  }
+  const Softmax all = join_row<false, kRowWarps>(part, scale, ctas, sh.parts, &sh.mine);
+  if (ctas > 1) {
+    cluster_have_read();
+    cluster_wait_read();
+  }
+  __syncthreads();
+  return all;
+}
+
 // The eight warps: the slice of the row filled with one value.
 template <typename T>
 __device__ __forceinline__ void fill_slice(const LogitRow<T> &row, const RowSlice &slice, T *dx, float x) {
@@ -473,7 +542,6 @@ __device__ __forceinline__ void list_ready() { asm volatile("bar.sync 1, %0;" ::
 template <typename T, int kWhat, bool kTail, bool kStaged>
 __global__ void __launch_bounds__(kThreads, kStaged ? 3 : kWhat == kDistillFwd ? 6 : 4)
 distill_kernel(const DistillArgs a, int words) {
-  constexpr int kVec = LogitRow<T>::kVec;
   constexpr bool kFwd = (kWhat & kDistillFwd) != 0, kBwd = (kWhat & kDistillBwd) != 0;
   extern __shared__ __align__(16) uint8_t dyn[];  // the bits, then the staged slice
   __shared__ ListShared sh;
@@ -494,6 +562,8 @@ distill_kernel(const DistillArgs a, int words) {
       if (walks) write_gradient<T, kTail, false>(row, slice, staged, dx, true, RestGradient({}, 0.f), nullptr);
       continue;
     }
+    // (asked for before the logits, so that they are there with the list)
+    const float lse = kFwd ? 0.f : a.stats[2 * r], lse_rest = kFwd || !kTail ? -INFINITY : a.stats[2 * r + 1];
     Softmax part = {-INFINITY, 0.f, 0.f, 0};
     LogitVec<T> ahead[kStaged ? 1 : kUnroll];  // the first group, on its way while the list is read
     int i = slice.v0 + (tid & ~31);            // of the warp's first lane: the loops are the warp's
@@ -548,14 +618,6 @@ distill_kernel(const DistillArgs a, int words) {
       list_ready();  // for the bits; for the gradient alone: its logits, with the rest bucket p_rest
       if (kFwd) {
         // the softmax of the tokens that are not listed
-        const uint8_t *bytes = reinterpret_cast<const uint8_t *>(bits.words);
-        auto hide = [&](int at, LogitVec<T> &v) {
-          const int n = at - bits.v0 + 1;
-          const unsigned hit = kVec == 8 ? bytes[n] : (bytes[n >> 1] >> (4 * (n & 1))) & 15u;
-          if (hit)
-            for (int e = 0; e < kVec; ++e)
-              if (hit >> e & 1u) v.mask(e);
-        };
         const Scale sc(a.scale);
         WarpSoftmax acc;
         // One group of vectors, from slots n.. (kStaged), from `ahead` or from the row.
@@ -577,7 +639,7 @@ distill_kernel(const DistillArgs a, int words) {
           }
 #pragma unroll
           for (int j = 0; j < kUnroll; ++j)
-            if (i + lane + j * kRowThreads < slice.v1) hide(i + lane + j * kRowThreads, v[j]);
+            if (i + lane + j * kRowThreads < slice.v1) bits.hide(i + lane + j * kRowThreads, v[j]);
           acc.group<T, kUnroll, false>(v, sc);
           i += kUnroll * kRowThreads;
         };
@@ -594,11 +656,7 @@ distill_kernel(const DistillArgs a, int words) {
           group(0, true);
           while (i < slice.v1) group(0, false);
         }
-        if (tid < 32) {
-          const int single = slice.single(row), at = bits.at(row, single);
-          const bool counts = single >= 0 && !(bits.words[at >> 5] >> (at & 31) & 1u);
-          acc.single<false>(counts ? logit_of(row.p[single]) : -INFINITY, sc);
-        }
+        if (tid < 32) acc.single<false>(bits.unlisted(row, slice.single(row)), sc);
         part = acc.all<false>(sc);
       }
     }
@@ -606,13 +664,19 @@ distill_kernel(const DistillArgs a, int words) {
     if (kFwd) {
       const Softmax rest = join_row<false, kRowWarps>(part, a.scale, ctas, sh.parts, &sh.mine);
       if (ctas > 1) cluster_have_read();
-      if (kBwd || !walks) k = row_constants(a, weight, rest, sh);
+      if (kBwd || !walks) k = row_constants(a, weight, whole_row(rest, sh.top, a.scale), rest, sh);
       if (!walks && rank == 0) row_loss(a, r, rest, k, sh);
+    } else if (saved_too_coarse<kTail>(lse, lse_rest, sh)) {
+      // (the same in all CTAs of the row; nothing has been written over it yet)
+      const Softmax all = walk_again<T, false>(row, slice, bits, a.scale, ctas, sh);
+      Softmax rest = {-INFINITY, 0.f, 0.f, 0};
+      if (kTail) rest = walk_again<T, true>(row, slice, bits, a.scale, ctas, sh);
+      k = row_constants(a, weight, all, rest, sh);
     } else {
       if (walks && !kTail)
-        k = saved_constants(a, r, weight, sh.outside, false, 0.f);  // the teacher is looked at below
+        k = saved_constants(a, lse, lse_rest, weight, sh.outside, false, 0.f);  // the teacher is looked at below
       else
-        k = saved_constants(a, r, weight, sh.outside, sh.no_teacher, sh.p_rest);
+        k = saved_constants(a, lse, lse_rest, weight, sh.outside, sh.no_teacher, sh.p_rest);
     }
     if (kBwd) {
       if (walks)
@@ -620,7 +684,7 @@ distill_kernel(const DistillArgs a, int words) {
                                           kFwd || kStaged ? nullptr : ahead);
       __syncthreads();
       // A row without a teacher, where the gradient did not wait to know it.
-      const bool blank = !kFwd && !kTail && sh.no_teacher && !sh.outside && a.stats[2 * r] == a.stats[2 * r];
+      const bool blank = !kFwd && !kTail && sh.no_teacher && !sh.outside && lse == lse;
       if (blank && walks) fill_slice(row, slice, dx, 0.f);
       // The listed tokens' gradients replace what stands there; each is written
       // by the CTA whose slice it is in.

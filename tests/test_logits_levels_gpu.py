@@ -107,3 +107,67 @@ def test_distillation(R, c, T, dtype, tail):
         got2, got_grad = R.distill_step(x, ids, values, temperature=T, tail=tail)
         assert torch.equal(got2, got)
         D.check_grad(got_grad, grad, size, torch.ones(7, device="cuda"), 160.0)
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T", [0.1, 1.0, 2.0])
+@pytest.mark.parametrize("c", LEVELS)
+def test_gradient_from_saved_statistics(R, c, T, dtype, tail):
+    """The gradient from the forward's statistics, an fp32 number of the size
+    of the level: the probabilities have to keep their digits.  Over the
+    logits too, and with rows of weight 0 among them."""
+    g = L.gen(20)
+    for V, k in ((37, 5), (5003, 20), (70001, 64)):
+        x = rows_at(g, c, V, dtype)
+        ids = torch.rand(7, V, generator=g, device="cuda")
+        ids[:, [0, V // 3, V - 1]] += 1.0
+        ids = ids.topk(k, dim=-1).indices
+        values = torch.log_softmax(torch.randn(7, k + 1, generator=g, device="cuda"), -1)[:, :k].contiguous()
+        weight = torch.rand(7, generator=g, device="cuda")
+        weight[2] = 0.0
+        _, grad, size, _ = reference(x, ids, values, T, tail)
+        _, stats = R.distill_fwd(x, ids, values, temperature=T, tail=tail)
+        got = R.distill_bwd(x, ids, values, weight, stats, temperature=T, tail=tail)
+        D.check_grad(got, grad, size, weight, 160.0)
+        over = x.clone()
+        R.distill_bwd(over, ids, values, weight, stats, temperature=T, tail=tail, dstudent=over)
+        D.check_grad(over, grad, size, weight, 160.0)
+
+
+def test_statistics_beyond_fp32(R):
+    """Levels that x / T takes out of fp32's range: q is uniform all the same."""
+    for c in (3e38, -3e38):
+        x = torch.full((2, 4099), c, device="cuda")
+        ids = torch.tensor([[3, 700], [4098, -1]], device="cuda")
+        values = torch.log(torch.tensor([[0.5, 0.25], [0.5, 0.25]], device="cuda"))
+        for tail in (False, True):
+            _, stats = R.distill_fwd(x, ids, values, temperature=0.5, tail=tail)
+            got = R.distill_bwd(x, ids, values, None, stats, temperature=0.5, tail=tail)
+            want = D.reference(torch.zeros_like(x), ids, values, 0.5, tail)
+            D.check_grad(got, want[1], want[2], torch.ones(2, device="cuda"))
+
+
+@pytest.mark.parametrize("tail", [False, True])
+def test_gradient_of_rows_at_several_levels(R, tail):
+    """Many rows a CTA, ordinary and far ones in turn, rows without a teacher
+    and of NaN among them."""
+    g = L.gen(21)
+    x = (2.0 * torch.randn(1400, 3001, generator=g, device="cuda"))
+    x[1::3] += 5e4
+    x[2::9] = -1e9
+    x[5] = float("nan")
+    x[8] = -L.INF
+    ids = torch.rand(1400, 3001, generator=g, device="cuda").topk(10, dim=-1).indices
+    values = torch.log_softmax(torch.randn(1400, 11, generator=g, device="cuda"), -1)[:, :10].contiguous()
+    ids[4] = -1
+    _, stats = R.distill_fwd(x, ids, values, tail=tail)
+    got = R.distill_bwd(x, ids, values, None, stats, tail=tail)
+    _, step = R.distill_step(x, ids, values, tail=tail)
+    assert bool(torch.isnan(got[5]).all()) and float(got[8].abs().max()) == 0
+    if not tail:
+        assert float(got[4].abs().max()) == 0
+    rows = [r for r in range(1400) if r not in (4, 5, 8)]
+    _, grad, size, _ = D.reference(x[rows], ids[rows], values[rows], 1.0, tail)
+    D.check_grad(got[rows], grad, size, torch.ones(len(rows), device="cuda"), 256.0)
+    D.check_grad(step[rows], grad, size, torch.ones(len(rows), device="cuda"), 256.0)
