@@ -51,10 +51,12 @@ struct ListShared {
 };
 
 // p ln(p / q) - p + q from ln p and ln q.  Near p = q the difference of the
-// logarithms d gives p (d - 1 + e^-d) by its series, exact to 2^-24 for |d| < 1/2.
+// logarithms d gives p (d - 1 + e^-d) by its series, exact to 2^-24 for |d| < 1/2;
+// where q is over e^8 times p (and e^-d may be beyond fp32) q itself is added.
 __device__ __forceinline__ float loss_term(float p, float ln_p, float ln_q) {
   if (p == 0.f) return expf(ln_q);
   const float d = ln_p - ln_q;
+  if (d < -8.f) return fmaf(p, d - 1.f, expf(ln_q));
   float g;
   if (fabsf(d) < 0.5f) {
     g = 1.f / 2.f - d * (1.f / 6.f - d * (1.f / 24.f - d * (1.f / 120.f - d * (1.f / 720.f - d * (1.f / 5040.f - d * (1.f / 40320.f - d * (1.f / 362880.f)))))));
