@@ -7,6 +7,7 @@ fallback implementation.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -253,9 +254,23 @@ def workspace_size(desc):
     return int(lib.retention_workspace_size(ctypes.byref(desc)))
 
 
-def new_workspace(nbytes, device):
+def _on(stream):
+    """Context in which memory for one call is allocated: in the order of the
+    stream that the call runs on.  A block of the current stream's would be given
+    to its next allocation as soon as the call returns, and would be zeroed at
+    any time, while a call on another stream still uses it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    return torch.cuda.stream(stream)
+
+
+def new_workspace(nbytes, device, stream=None):
+    """A workspace for calls on the given stream (None: the current one)."""
     # zeroed once: its first bytes hold the device status word
-    return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+    with _on(stream):
+        return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
 def _prep(q, k, v, out, out_dtype):
@@ -276,7 +291,7 @@ def chunkwise_fwd(q, k, v, gamma, *, chunk=64, norm_flags=0, gn_eps=1e-6, pos0=0
     d, g = make_desc(q, k, v, out, gamma, chunk=chunk, norm_flags=norm_flags, gn_eps=gn_eps,
                      pos0=pos0, rotate=rotate, theta_base=theta_base)
     if workspace is None:
-        workspace = new_workspace(workspace_size(d), q.device)
+        workspace = new_workspace(workspace_size(d), q.device, stream)
     st = lib.retention_chunkwise_fwd(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(S_in),
                                      _ptr(z_in), _ptr(S_out), _ptr(z_out), _ptr(out),
                                      _ptr(workspace), workspace.numel(), _stream(stream))
@@ -302,7 +317,7 @@ def chunkwise_state(k, v, gamma, *, pos0=0, rotate=True, theta_base=10000.0, S_i
         z_out = torch.empty(B, H, dk, dtype=torch.float32, device=k.device)
     d, g = make_desc(k, k, v, v, gamma, pos0=pos0, rotate=rotate, theta_base=theta_base)
     if workspace is None:
-        workspace = new_workspace(state_workspace_size(d), k.device)
+        workspace = new_workspace(state_workspace_size(d), k.device, stream)
     st = lib.retention_chunkwise_state(ctypes.byref(d), _ptr(k), _ptr(v), _ptr(S_in),
                                        _ptr(z_in), _ptr(S_out), _ptr(z_out), _ptr(workspace),
                                        workspace.numel(), _stream(stream))
@@ -350,7 +365,7 @@ def chunkwise_bwd(q, k, v, dO, gamma, *, norm_flags=0, pos0=0, rotate=True,
     d, g = make_desc(q, k, v, dO, gamma, norm_flags=norm_flags, gn_eps=None, pos0=pos0,
                      rotate=rotate, theta_base=theta_base)
     if workspace is None:
-        workspace = new_workspace(backward_workspace_size(d), q.device)
+        workspace = new_workspace(backward_workspace_size(d), q.device, stream)
     st = lib.retention_chunkwise_bwd(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(S_in),
                                      _ptr(dO), _ptr(dS_out), _ptr(dq), _ptr(dk), _ptr(dv),
                                      _ptr(dS_in), _ptr(workspace), workspace.numel(),
@@ -380,7 +395,7 @@ def parallel_fwd(q, k, v, gamma, *, norm_flags=0, gn_eps=1e-6, pos0=0, rotate=Tr
     d, g = make_desc(q, k, v, out, gamma, norm_flags=norm_flags, gn_eps=gn_eps, pos0=pos0,
                      rotate=rotate, theta_base=theta_base)
     if workspace is None:
-        workspace = new_workspace(workspace_size(d), q.device)
+        workspace = new_workspace(workspace_size(d), q.device, stream)
     st = lib.retention_parallel_fwd(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(out),
                                     _ptr(workspace), workspace.numel(), _stream(stream))
     _check(st, "retention_parallel_fwd")
@@ -399,7 +414,7 @@ def recurrent_step(q, k, v, S, gamma, *, z=None, pos, norm_flags=0, gn_eps=1e-6,
     d, g = make_desc(q4, k4, v4, out, gamma, norm_flags=norm_flags, gn_eps=gn_eps, pos0=pos,
                      rotate=rotate, theta_base=theta_base)
     if workspace is None:
-        workspace = new_workspace(256, q.device)
+        workspace = new_workspace(256, q.device, stream)
     st = lib.retention_recurrent_step(ctypes.byref(d), _ptr(q4), _ptr(k4), _ptr(v4), _ptr(S),
                                       _ptr(z), _ptr(out), _ptr(workspace), workspace.numel(),
                                       _stream(stream))
@@ -442,7 +457,7 @@ def msr_layer_fwd(X, WQ, WK, WV, WG, WO, *, H, d_k, d_v, gamma, chunk=128, norm_
     if out is None:
         out = torch.empty((B, N, dm), dtype=torch.bfloat16, device=X.device)
     if workspace is None:
-        workspace = new_workspace(int(lib.msr_workspace_size(ctypes.byref(m))), X.device)
+        workspace = new_workspace(int(lib.msr_workspace_size(ctypes.byref(m))), X.device, stream)
     for name, t in (("X", X), ("WQ", WQ), ("WK", WK), ("WV", WV), ("WG", WG), ("WO", WO)):
         if t.dtype != torch.bfloat16 or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous bf16 tensor")
@@ -477,7 +492,7 @@ def retnet_block_fwd(X, ln1_w, ln1_b, WQ, WK, WV, WG, WO, ln2_w, ln2_b, W1, W2, 
         out = torch.empty((B, N, dm), dtype=torch.bfloat16, device=X.device)
     if workspace is None:
         workspace = new_workspace(int(lib.retnet_block_workspace_size(ctypes.byref(d))),
-                                  X.device)
+                                  X.device, stream)
     for name, t in (("X", X), ("WQ", WQ), ("WK", WK), ("WV", WV), ("WG", WG), ("WO", WO),
                     ("W1", W1), ("W2", W2)):
         if t.dtype != torch.bfloat16 or not t.is_contiguous():
@@ -522,7 +537,7 @@ def retnet_decode_step(X, layers, S, z=None, *, H, d_k, d_v, gamma, pos, norm_fl
                       gn_eps=gn_eps, ln_eps=ln_eps, theta_base=theta_base)
     if workspace is None:
         workspace = new_workspace(int(lib.retnet_decode_workspace_size(ctypes.byref(d))),
-                                  X.device)
+                                  X.device, stream)
     recs = (LayerWeights * max(n, 1))()
     for i, L in enumerate(layers):
         for k in LAYER_KEYS:
@@ -546,7 +561,8 @@ def gemm_bf16(A, B, out=None, workspace=None, stream=None):
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
     if workspace is None:
-        workspace = new_workspace(int(lib.retention_gemm_workspace_size(M, N, K)), A.device)
+        workspace = new_workspace(int(lib.retention_gemm_workspace_size(M, N, K)), A.device,
+                                  stream)
     _check(lib.retention_gemm_bf16(_ptr(A), _ptr(B), _ptr(out), M, N, K, _ptr(workspace),
                                    workspace.numel(), _stream(stream)), "retention_gemm_bf16")
     return out
@@ -655,7 +671,8 @@ def layernorm_bwd(x, dy, w, mean, rstd, *, dx=None, dw=None, db=None, workspace=
     _f32("db", db, d)
     desc, nbytes = _ln_desc(shape, x.dtype, 0.0, x.stride(), dy.stride(), dx.stride())
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+        with _on(stream):
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
     st = lib.retnet_layernorm_bwd(ctypes.byref(desc),
                                   *_ptrs(x, dy, w, mean, rstd, dx, dw, db, workspace),
                                   workspace.numel(), _stream(stream))
