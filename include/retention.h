@@ -455,10 +455,11 @@ ret_status retnet_token_logprobs(const retnet_logits_desc *d, const void *x, con
  *           vocabulary), p_rest = max(0, 1 - sum p) (0 if all V are listed).
  * Loss of a row and its gradient:
  *   loss[r] = T^2 [ sum_k p_k ln(p_k / q_k) + p_rest ln(p_rest / q_rest) ],
- *   dx_j = weight[r] T (q_j - p_j) for a listed token,
- *          weight[r] T (q_j - p_rest q_j / q_rest) for any other,
- * where weight[r] is the gradient of the caller's loss with respect to
- * loss[r] (fp32, NULL = 1).
+ *   dx_j = weight[r] T (P q_j - p_j) for a listed token,
+ *          weight[r] T (P q_j - p_rest q_j / q_rest) for any other,
+ * where P = sum p + p_rest is 1 unless the listed log probabilities of tail 1
+ * add up to more, or all V tokens are listed, and weight[r] is the gradient of
+ * the caller's loss with respect to loss[r] (fp32, NULL = 1).
  *   - A negative id is an absent entry; of an id listed twice the first entry
  *     counts; an id >= V makes the row's loss and gradient NaN.
  *   - A row whose weight is 0 has a gradient of zeros, whatever it holds.

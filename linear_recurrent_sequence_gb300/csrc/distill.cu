@@ -10,6 +10,9 @@
 // the difference of large ones.  q_r is summed over the tokens that are not
 // listed (a bit per token in shared memory tells which), not taken as
 // 1 - sum q_k.
+// Log probabilities that add up to more than 1 (rounded or scaled ones), or those
+// of all V tokens, leave no p_r that makes up for it: with P = sum p the loss is
+// T^2 (P - 1) more, and P q_j takes the place of q_j in its gradient.
 //
 // Bound by memory: the loss reads each logit once, the gradient reads it and
 // writes a value.  bf16, a list of 64: the loss of 1024 x 65536 27.4 us, 4.9 TB/s;
@@ -45,7 +48,7 @@ struct ListShared {
   float p[kMaxTop];     // the teacher's probability and its logarithm
   float ln_p[kMaxTop];
   int outside, no_teacher;
-  float p_rest;
+  float p_rest, over;   // over: sum p + p_rest - 1
   Softmax top;          // of the listed logits
   Softmax parts[kRowWarps], mine;
 };
@@ -240,7 +243,7 @@ __device__ __forceinline__ void teacher(const DistillArgs &a, float (&v)[kPer], 
       sh.p[lane + 32 * i] = p[i] * inv;
       sh.ln_p[lane + 32 * i] = v[i] - ln_sum;
     }
-  float rest = 0.f;
+  float rest = 0.f, over = 0.f;
   if (a.tail) {
     // 1 - sum p is small for a teacher that is sure of its list, so the sum
     // is formed in two floats.  A list of all tokens leaves nothing.
@@ -260,9 +263,15 @@ __device__ __forceinline__ void teacher(const DistillArgs &a, float (&v)[kPer], 
       two.lo += lo;
     }
     rest = (1.f - two.hi) - two.lo;
-    if (rest < 0.f || listed == a.V) rest = 0.f;  // NaN stays NaN
+    if (rest < 0.f || listed == a.V) {  // NaN stays NaN
+      over = -rest;
+      rest = 0.f;
+    }
   }
-  if (lane == 0) sh.p_rest = rest;
+  if (lane == 0) {
+    sh.p_rest = rest;
+    sh.over = over;
+  }
 }
 
 // What a row's threads need of it: ln q_j = ((x_j - a) log2(e) / T - b) ln 2, and
@@ -347,6 +356,7 @@ __device__ __forceinline__ void row_loss(const DistillArgs &a, long long r, cons
   if (lane == 0) {
     const float pr = sh.p_rest;
     sum += loss_term(pr, logf(pr), c.empty ? -INFINITY : ln_qr);
+    sum += sh.over;
     if (a.loss) a.loss[r] = c.bad ? nan_value() : sh.no_teacher ? 0.f : sum * (a.t * a.t);
     if (a.stats) {
       const bool bad = rest.bad || sh.top.bad;
@@ -356,11 +366,11 @@ __device__ __forceinline__ void row_loss(const DistillArgs &a, long long r, cons
   }
 }
 
-// The gradient of a token that is not listed.
+// The gradient of a token that is not listed; total: sum p + p_rest.
 struct RestGradient {
   float a, b, a_rest, b_rest, c, c_rest, scale;
-  __device__ __forceinline__ RestGradient(const RowConstants &k, float sc)
-      : a(-k.a), b(-k.b), a_rest(-k.a_rest), b_rest(-k.b_rest), c(k.c), c_rest(-k.c_rest), scale(sc) {}
+  __device__ __forceinline__ RestGradient(const RowConstants &k, float sc, float total)
+      : a(-k.a), b(-k.b), a_rest(-k.a_rest), b_rest(-k.b_rest), c(k.c * total), c_rest(-k.c_rest), scale(sc) {}
   template <bool kTail>
   __device__ __forceinline__ float2 at(float2 x) const {
     const float2 s2 = make_float2(scale, scale);
@@ -561,7 +571,7 @@ distill_kernel(const DistillArgs a, int words) {
     const float weight = kBwd && a.weight ? a.weight[r] : 1.f;
     const bool zero = kBwd && weight == 0.f;
     if (!kFwd && zero) {
-      if (walks) write_gradient<T, kTail, false>(row, slice, staged, dx, true, RestGradient({}, 0.f), nullptr);
+      if (walks) write_gradient<T, kTail, false>(row, slice, staged, dx, true, RestGradient({}, 0.f, 1.f), nullptr);
       continue;
     }
     // (asked for before the logits, so that they are there with the list)
@@ -682,7 +692,8 @@ distill_kernel(const DistillArgs a, int words) {
     }
     if (kBwd) {
       if (walks)
-        write_gradient<T, kTail, kStaged>(row, slice, staged, dx, zero, RestGradient(k, a.scale),
+        write_gradient<T, kTail, kStaged>(row, slice, staged, dx, zero,
+                                          RestGradient(k, a.scale, kTail ? 1.f + sh.over : 1.f),
                                           kFwd || kStaged ? nullptr : ahead);
       __syncthreads();
       // A row without a teacher, where the gradient did not wait to know it.
@@ -690,18 +701,20 @@ distill_kernel(const DistillArgs a, int words) {
       if (blank && walks) fill_slice(row, slice, dx, 0.f);
       // The listed tokens' gradients replace what stands there; each is written
       // by the CTA whose slice it is in.
-      if (!walks && !zero)
+      if (!walks && !zero) {
+        const float total = kTail ? 1.f + sh.over : 1.f;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
           const int id = sh.id[lane + 32 * j];
           if (id >= 0 && slice.has(row, id) && !blank) {
             const float q = ex2(fmaf(sh.x[lane + 32 * j] - k.a, a.scale, -k.b));
-            const float g1[1] = {k.c * (q - sh.p[lane + 32 * j])};
+            const float g1[1] = {k.c * fmaf(total, q, -sh.p[lane + 32 * j])};
             Elems<T, 1> one;
             one.set(g1);
             one.store(dx + id);
           }
         }
+      }
     }
     // the row's list has been read, its part of the softmax by the other CTAs too
     if (ctas > 1 && kFwd) cluster_wait_read();
