@@ -10,6 +10,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import operator
 import os
 
 import torch
@@ -613,7 +614,8 @@ def _ptrs(*tensors):
 
 # The descriptors below depend on shapes, strides and options alone, and a
 # program calls with the same ones over and over: building one costs 5 us,
-# finding it here less than one.
+# finding it here less than one.  Options are plain numbers by then: a tensor
+# would be found by its identity, whatever it holds now.
 @functools.lru_cache(maxsize=256)
 def _ln_desc(shape, dtype, eps, sx, sg, so):
     """(descriptor, workspace bytes of the backward)."""
@@ -642,7 +644,7 @@ def layernorm_fwd(x, w=None, b=None, *, eps=1e-5, out=None, mean=None, rstd=None
     _f32("mean", mean, lead)
     _f32("rstd", rstd, lead)
     so = out.stride()
-    desc, _ = _ln_desc(shape, x.dtype, eps, x.stride(), so, so)
+    desc, _ = _ln_desc(shape, x.dtype, float(eps), x.stride(), so, so)
     st = lib.retnet_layernorm_fwd(ctypes.byref(desc), *_ptrs(x, w, b, out, mean, rstd),
                                   _stream(stream))
     _check(st, "retnet_layernorm_fwd")
@@ -706,7 +708,7 @@ def token_logprobs(logits, tokens=None, *, top=0, temperature=1.0, logprob=None,
     missing alternatives of a row have id -1."""
     shape, dev = logits.shape, logits.device
     lead = shape[:-1]
-    id_bytes = 8
+    top, id_bytes = operator.index(top), 8
     if tokens is not None:
         id_bytes = _ids("tokens", tokens, lead)
         if logprob is None:
@@ -729,7 +731,7 @@ def token_logprobs(logits, tokens=None, *, top=0, temperature=1.0, logprob=None,
     _f32("logprob", logprob, lead)
     _f32("entropy", entropy, lead)
     s = logits.stride()
-    d = _logits_desc(shape, logits.dtype, temperature, top, id_bytes, False, s, s)
+    d = _logits_desc(shape, logits.dtype, float(temperature), top, id_bytes, False, s, s)
     st = lib.retnet_token_logprobs(
         ctypes.byref(d), *_ptrs(logits, tokens, logprob, entropy, top_logprobs, top_ids),
         _stream(stream))
@@ -743,7 +745,7 @@ def _distill_desc(student, ids, values, temperature, tail, dstudent):
     id_bytes = _ids("ids", ids, lists)
     _f32("values", values, lists)
     s = student.stride()
-    return _logits_desc(shape, student.dtype, temperature, top, id_bytes, bool(tail), s,
+    return _logits_desc(shape, student.dtype, float(temperature), top, id_bytes, bool(tail), s,
                         s if dstudent is None else dstudent.stride())
 
 
