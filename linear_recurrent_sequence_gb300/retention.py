@@ -617,8 +617,8 @@ def _ptrs(*tensors):
 # finding it here less than one.  Options are plain numbers by then: a tensor
 # would be found by its identity, whatever it holds now.
 @functools.lru_cache(maxsize=256)
-def _ln_desc(shape, dtype, eps, sx, sg, so):
-    """(descriptor, workspace bytes of the backward)."""
+def _ln_desc(shape, dtype, eps, sx, sg, so, device):
+    """(descriptor, workspace bytes of the backward on that device)."""
     n0, n1, st = _row_strides("layernorm", shape, sx, sg, so)
     d = LayerNormDesc(n0, n1, shape[-1], _dtype_code(dtype), eps, *st)
     return d, int(lib.retnet_layernorm_bwd_workspace_size(ctypes.byref(d)))
@@ -644,7 +644,7 @@ def layernorm_fwd(x, w=None, b=None, *, eps=1e-5, out=None, mean=None, rstd=None
     _f32("mean", mean, lead)
     _f32("rstd", rstd, lead)
     so = out.stride()
-    desc, _ = _ln_desc(shape, x.dtype, float(eps), x.stride(), so, so)
+    desc, _ = _ln_desc(shape, x.dtype, float(eps), x.stride(), so, so, x.device)
     st = lib.retnet_layernorm_fwd(ctypes.byref(desc), *_ptrs(x, w, b, out, mean, rstd),
                                   _stream(stream))
     _check(st, "retnet_layernorm_fwd")
@@ -671,7 +671,7 @@ def layernorm_bwd(x, dy, w, mean, rstd, *, dx=None, dw=None, db=None, workspace=
     _f32("rstd", rstd, lead)
     _f32("dw", dw, d)
     _f32("db", db, d)
-    desc, nbytes = _ln_desc(shape, x.dtype, 0.0, x.stride(), dy.stride(), dx.stride())
+    desc, nbytes = _ln_desc(shape, x.dtype, 0.0, x.stride(), dy.stride(), dx.stride(), x.device)
     if workspace is None:
         with _on(stream):
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)

@@ -32,7 +32,9 @@ def calls(monkeypatch):
     monkeypatch.setattr(R, "lib", Library(R.lib))
     monkeypatch.setattr(R, "_ptrs", lambda *ts: [None if t is None else t.data_ptr() for t in ts])
     monkeypatch.setattr(R, "_stream", lambda s: None)
-    return R, given
+    yield R, given
+    R._ln_desc.cache_clear()  # (sizes and descriptors of the stand-in)
+    R._logits_desc.cache_clear()
 
 
 def test_options_as_tensors_are_read_at_each_call(calls):
@@ -61,3 +63,27 @@ def test_options_as_tensors_are_read_at_each_call(calls):
         assert given[-1].top == want and out[3].shape == (3, want)
     with pytest.raises(TypeError):
         R.token_logprobs(x, top=2.5)
+
+
+def test_workspace_size_is_that_of_the_device(calls, monkeypatch):
+    """layernorm_bwd's workspace depends on the device's SMs: tensors of equal
+    shapes on two unlike devices (here the host and torch's meta device) get
+    each its own."""
+    R, given = calls
+    sizes = {"cpu": 4096, "meta": 8192}
+    made, real = [], torch.empty
+    now = []
+    lib = R.lib
+    lib.__dict__["retnet_layernorm_bwd_workspace_size"] = lambda d: sizes[now[-1]]
+
+    def empty(*a, **k):
+        if k.get("dtype") is torch.uint8:
+            made.append((a[0], str(k["device"])))
+        return real(*a, **k)
+
+    monkeypatch.setattr(torch, "empty", empty)
+    for dev in ("cpu", "meta", "cpu"):
+        now.append(dev)
+        x, stat = torch.zeros(5, 72, device=dev), torch.zeros(5, device=dev)
+        R.layernorm_bwd(x, x, None, stat, stat)
+        assert made[-1] == (sizes[dev], dev)
