@@ -376,7 +376,8 @@ ret_status retnet_decode_step(const retnet_stack_desc *d, const retnet_layer_wei
  * 0 <= i < n0, 0 <= j < n1, numbered r = i n1 + j, start at element
  * i s[0] + j s[1] of a tensor (two strides >= 0, such as a [B, N, d] view or
  * logits[:, :-1] of a [B, N, V] tensor); a row's values are contiguous.  Rows
- * of an output must not overlap one another (RET_EINVAL).  Per-row vectors
+ * of an output must not overlap one another (RET_EINVAL); they may lie between
+ * the rows of an input that has the same strides.  Per-row vectors
  * (mean, loss, ...) are contiguous [n0 n1].  No row, stride or base pointer
  * needs more than its element's alignment (16-byte aligned rows run faster;
  * LayerNorm reads others in the aligned 16-byte words that cover them, so the

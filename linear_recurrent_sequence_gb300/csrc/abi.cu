@@ -1301,11 +1301,41 @@ static bool same_rows(int64_t n0, int64_t n1, const int64_t a[2], const int64_t 
   return (n0 <= 1 || a[0] == b[0]) && (n1 <= 1 || a[1] == b[1]);
 }
 
-// An output may be an input (same pointer and strides) or clear of it.
+// Do rows with these strides (disjoint ones) share no value with the same rows
+// `shift` elements further on?  They do where shift + a s0 + b s1 is closer to 0
+// than `width` for some |a| < n0, |b| < n1: of the outer dimension's steps only the
+// two around -shift / stride come near enough, and of the inner one's likewise.
+static bool rows_between(int64_t n0, int64_t n1, const int64_t s[2], int64_t width, int64_t shift) {
+  const bool inner1 = n0 == 1 || (n1 > 1 && s[0] >= s[1]);
+  const int64_t n[2] = {inner1 ? n0 : n1, inner1 ? n1 : n0};
+  const int64_t st[2] = {inner1 ? s[0] : s[1], inner1 ? s[1] : s[0]};
+  auto around = [](int64_t at, int64_t count, int64_t step) {
+    if (count == 1) return (int64_t)0;
+    return -at / step - (at > 0 && at % step ? 1 : 0);  // the floor of -at / step
+  };
+  const int64_t a0 = around(shift, n[0], st[0]);
+  for (int64_t a = a0; a <= a0 + (n[0] > 1); ++a) {
+    if (a <= -n[0] || a >= n[0]) continue;
+    const int64_t at = shift + (n[0] > 1 ? a * st[0] : 0), b0 = around(at, n[1], st[1]);
+    for (int64_t b = b0; b <= b0 + (n[1] > 1); ++b) {
+      if (b <= -n[1] || b >= n[1]) continue;
+      const int64_t off = at + (n[1] > 1 ? b * st[1] : 0);
+      if (off < width && off > -width) return false;
+    }
+  }
+  return true;
+}
+
+// An output may be an input (same pointer and strides) or clear of it: outside
+// of its extent, or with the same strides between its rows.
 static bool in_place_or_clear(int64_t n0, int64_t n1, const void *in, const int64_t si[2],
                               const void *out, const int64_t so[2], int64_t width, size_t esz) {
-  if (in == out && same_rows(n0, n1, si, so)) return true;
-  return !overlaps(in, rows_extent(n0, n1, si, width, esz), out, rows_extent(n0, n1, so, width, esz));
+  const bool same = same_rows(n0, n1, si, so);
+  if (in == out && same) return true;
+  if (!overlaps(in, rows_extent(n0, n1, si, width, esz), out, rows_extent(n0, n1, so, width, esz)))
+    return true;
+  const int64_t bytes = (int64_t)((uintptr_t)out - (uintptr_t)in);
+  return same && rows_between(n0, n1, so, width, bytes / (int64_t)esz);
 }
 
 static bool elem_aligned(const void *p, size_t esz) {
