@@ -546,9 +546,10 @@ def retnet_decode_step(X, layers, S, z=None, *, H, d_k, d_v, gamma, pos, norm_fl
             want = torch.float32 if k.startswith("ln") else torch.bfloat16
             if t.dtype != want or not t.is_contiguous():
                 raise ValueError(f"layer {i} {k}: contiguous {want} expected")
-            setattr(recs[i], k, t.data_ptr())
-    Sp = (ctypes.c_void_p * max(n, 1))(*[s.data_ptr() for s in S])
-    zp = None if z is None else (ctypes.c_void_p * max(n, 1))(*[t.data_ptr() for t in z])
+        for k, p in zip(LAYER_KEYS, _ptrs(*(L[k] for k in LAYER_KEYS))):
+            setattr(recs[i], k, p)
+    Sp = (ctypes.c_void_p * max(n, 1))(*_ptrs(*S))
+    zp = None if z is None else (ctypes.c_void_p * max(n, 1))(*_ptrs(*z))
     st = lib.retnet_decode_step(ctypes.byref(d), recs, Sp, zp, _ptr(X), _ptr(workspace),
                                 workspace.numel(), _stream(stream))
     _check(st, "retnet_decode_step")
@@ -607,7 +608,7 @@ def _like(name, t, x):
 
 def _ptrs(*tensors):
     """Device addresses as _ptr gives them (the current device asked for once)."""
-    dev = torch.cuda.current_device() if tensors[0].is_cuda else -1
+    dev = torch.cuda.current_device() if tensors and tensors[0].is_cuda else -1
     return [None if t is None else t.data_ptr() if t.get_device() == dev >= 0 else _ptr(t)
             for t in tensors]
 
