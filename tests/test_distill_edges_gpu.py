@@ -1,6 +1,7 @@
 """GPU tests of the distillation loss where a teacher's probability is at the
 bottom of fp32 and where the listed probabilities add up to more than 1, against
-the formulas in 64 bits.  Tolerances: those of test_distill_gpu.py."""
+the formulas in 64 bits; the cross entropy that a list of one token is.
+Tolerances: those of test_distill_gpu.py."""
 import pytest
 import torch
 
@@ -98,3 +99,21 @@ def test_gradient_against_differences_beyond_one(R, V, k, how):
         fd = (f[0] - 8 * f[1] + 8 * f[2] - f[3]) / (12 * h)
         want = (grad.double() * v.double()).sum(-1)
         assert bool(((fd - want).abs() <= 2e-3 * grad.double().norm(dim=-1) + 4e-4).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_one_listed_token_is_cross_entropy(R, dtype):
+    """Next-token cross entropy with ignored positions: loss, and the gradient
+    of the mean over the others."""
+    g = D.gen(41)
+    x = (2.0 * torch.randn(3, 5, 5003, generator=g, device="cuda")).to(dtype)
+    tokens = torch.randint(0, 5003, (3, 5), generator=g, device="cuda")
+    tokens[0, 4] = tokens[2, 0] = -100
+    there = tokens >= 0
+    weight = torch.full((3, 5), 1.0 / float(there.sum()), device="cuda")
+    loss, grad = R.distill_step(x, tokens[..., None], torch.zeros(3, 5, 1, device="cuda"), weight)
+    lp = x.double().log_softmax(-1)
+    D.check_loss(loss, torch.where(there, -lp.gather(-1, tokens.clamp(min=0)[..., None])[..., 0], 0.0), 1.0)
+    one = torch.zeros_like(lp).scatter_(-1, tokens.clamp(min=0)[..., None], 1.0)
+    D.check_grad(grad, (lp.exp() - one) * there[..., None], lp.exp() + one, weight)
+    assert float(grad[~there].float().abs().max()) == 0
