@@ -464,6 +464,9 @@ ret_status retnet_token_logprobs(const retnet_logits_desc *d, const void *x, con
  *   - A negative id is an absent entry; of an id listed twice the first entry
  *     counts; an id >= V makes the row's loss and gradient NaN.
  *   - A row whose weight is 0 has a gradient of zeros, whatever it holds.
+ *   - A list of one token (top 1, tail 0, T 1, any finite value) is the cross
+ *     entropy -ln q_t of that token with its gradient; a negative id, such as
+ *     the -100 of an ignored position, has loss and gradient 0.
  *   - A logit of -infinity has q = 0 and, if not listed, gradient 0.  A NaN or
  *     +infinity makes the row NaN.  A row of -infinity alone has the loss
  *     +infinity and gradient 0; a row without a teacher (tail 0, no entry

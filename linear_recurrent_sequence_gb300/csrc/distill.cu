@@ -15,10 +15,11 @@
 // T^2 (P - 1) more, and P q_j takes the place of q_j in its gradient.
 //
 // Bound by memory: the loss reads each logit once, the gradient reads it and
-// writes a value.  bf16, a list of 64: the loss of 1024 x 65536 27.4 us, 4.9 TB/s;
-// the gradient of 2048 x 65536 89 us, 6.0 TB/s; both of 4096 x 65536 197 us, 5.5
+// writes a value.  bf16, a list of 64: the loss of 1024 x 65536 27.6 us, 4.9 TB/s;
+// the gradient of 2048 x 65536 89.5 us, 6.0 TB/s; both of 4096 x 65536 199 us, 5.4
 // TB/s (with a second reading from the L2 instead of shared memory 262 us); 8 x
-// 32768 6 us, latency.
+// 32768 6.1 us, latency.  fp32: the loss of 1024 x 50001 44.5 us, 4.6 TB/s, both of
+// 1500 x 50001 131 us, 4.6 TB/s.
 //
 // Eight warps of a CTA walk over its slice of the row while a ninth reads the
 // list, gathers its logits and forms the teacher's probabilities; the listed
@@ -183,7 +184,8 @@ __device__ __forceinline__ void listed_softmax(const DistillArgs &a, ListShared 
   if (lane == 0) sh.top = {m, z, 0.f, bad};
 }
 
-// A sum in two floats: hi + lo, |lo| below an ulp of hi.
+// A sum in two floats: hi + lo, |lo| below an ulp of hi (Knuth's exact sum of
+// two floats for each term).
 struct TwoFloat {
   float hi, lo;
   __device__ __forceinline__ void add(float x) {
@@ -191,9 +193,11 @@ struct TwoFloat {
     lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(x, b)));
     hi = t;
   }
-  // e^v for v > -80, to about 2^-28 of it: with v log2(e) = n + r in two
-  // floats and z = r ln 2, the three parts 2^n, 2^n z and 2^n (e^z - 1 - z),
-  // the last by its series (|z| < 0.35).
+  // e^v for v > -80: with v log2(e) = n + r in two floats and z = r ln 2, the
+  // three parts 2^n, 2^n z and 2^n (e^z - 1 - z), the last by its series
+  // (|z| < 0.35).  Relative to e^v the error is up to 2^-26 for v > -1 and 2^-22
+  // far below (z's low part is not multiplied by the series), where e^v itself is
+  // small: absolutely it stays below 2^-26.6, which is what 1 - sum p needs.
   __device__ __forceinline__ void add_exp(float v) {
     constexpr float kLog2e = 1.44269502f, kLog2eLo = 1.92596303e-8f;  // log2(e) in two floats
     constexpr float kLn2 = 0.693147182f, kLn2Lo = -1.90465421e-9f;    // ln 2
@@ -550,7 +554,8 @@ __device__ __forceinline__ void list_ready() { asm volatile("bar.sync 1, %0;" ::
 
 // CTAs an SM: three where their slices fill its shared memory, four for the
 // gradient alone, six for the loss alone (1024 x 65536 bf16 27.4 us, with four
-// 33.8).
+// 33.8; the 32 registers that six leave spill 40 to 52 bytes a thread, the 56 of
+// four up to 32).
 template <typename T, int kWhat, bool kTail, bool kStaged>
 __global__ void __launch_bounds__(kThreads, kStaged ? 3 : kWhat == kDistillFwd ? 6 : 4)
 distill_kernel(const DistillArgs a, int words) {

@@ -477,11 +477,11 @@ ln_fwd_long_kernel(const LnArgs a) {
 // dx of the CTA's rows, and the sums of dy h and dy over them: R rows at a
 // time by tpr threads, blockDim / tpr such groups in a CTA.  Each thread keeps
 // the sums of its own NV x VEC columns in registers for the whole call: that is
-// what leaves one CTA of 512 threads an SM, and bounds the kernel by the issue
-// of 16 warps' instructions rather than by memory (8192 x 4096 bf16: 43 us with
-// the sum over CTAs, 4.7 TB/s; fp32 8192 x 2048: 37 us, 5.5 TB/s).  Sums kept in
-// shared memory, or added by atomics, would cost each value a read and a write
-// there, and atomics an order that changes.
+// what leaves one CTA of 512 threads an SM, and bounds the kernel by the latency
+// of each row's steps at 16 warps rather than by memory (8192 x 4096 bf16: 58% of
+// the issue slots, 48% of DRAM; 43 us with the sum over CTAs, 4.7 TB/s; fp32 8192 x
+// 2048: 37 us, 5.5 TB/s).  Sums kept in shared memory, or added by atomics, would
+// cost each value a read and a write there, and atomics an order that changes.
 // The rows come through the ring and are read from it twice, before and after
 // the rows' sums.  kKeep: the gains of the thread's columns are in registers
 // too.  kHold: h and dy w stay in registers between the two uses instead

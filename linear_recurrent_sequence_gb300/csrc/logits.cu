@@ -6,8 +6,8 @@
 // -infinity is a masked token: probability 0, never an alternative.
 //
 // Bound by memory: each logit is read once (2 or 4 bytes) and costs one
-// exponential and about six other operations.  4096 x 65536 bf16: 84 us without
-// alternatives, 6.3 TB/s, 98 us with five; fp32 2000 x 50001 74 us, 5.4 TB/s.  Few
+// exponential and about six other operations.  4096 x 65536 bf16: 85 us without
+// alternatives, 6.3 TB/s, 99 us with five; fp32 2000 x 50001 74 us, 5.4 TB/s.  Few
 // rows are bound by the latency of the row's steps: 8 x 131072 bf16 4.4 us, with
 // 20 alternatives 10.2 us.
 //
@@ -299,6 +299,8 @@ __device__ __forceinline__ void prefetch_row(const T *p, int V, int bytes) {
 
 // soon: how many rows are walked over at once, 0 where the row after them is
 // not to be asked for.
+// (The 48 registers of 1280 threads an SM spill 8 to 100 bytes a thread where
+// there are alternatives.)
 template <typename T, bool kEntropy, bool kTop, int kT>
 __global__ void __launch_bounds__(kT, kT == 512 ? 2 : 1280 / kT)
 token_logprobs_kernel(const LogprobArgs a, int soon) {

@@ -757,9 +757,10 @@ def distill_fwd(student, ids, values, *, temperature=1.0, tail=False, loss=None,
     = absent) and values (fp32), both [.., k] with k <= MAX_TOP.  With tail
     False the teacher is softmax(values / temperature) over the list; with tail
     True the values are log probabilities over the whole vocabulary and the
-    tokens that are not listed form one more bucket.  Returns (loss, stats):
-    the loss times temperature^2, fp32 of student.shape[:-1], and what
-    distill_bwd needs, [.., 2]."""
+    tokens that are not listed form one more bucket.  A list of one token with
+    tail False is the cross entropy of that token.  Returns (loss, stats): the
+    loss times temperature^2, fp32 of student.shape[:-1], and what distill_bwd
+    needs, [.., 2]."""
     lead = student.shape[:-1]
     pairs = (*lead, 2)
     if loss is None:
@@ -779,7 +780,8 @@ def distill_bwd(student, ids, values, weight, stats, *, temperature=1.0, tail=Fa
                 stream=None):
     """Gradient with respect to the student's logits, in their dtype: weight
     (fp32, or None for 1) is the gradient of the caller's loss with respect to
-    each row's; rows of weight 0 get zeros.  dstudent may be student itself."""
+    each row's; rows of weight 0 get zeros.  Rows whose stats are beyond 256 in
+    size are read a second time.  dstudent may be student itself."""
     lead = student.shape[:-1]
     if dstudent is None:
         dstudent = torch.empty(student.shape, dtype=student.dtype, device=student.device)
