@@ -497,6 +497,142 @@ int retention_last_cuda_error(void);
  * SYNCHRONISES `stream`.  Returns RET_OK or the first device-side error. */
 ret_status retention_poll_status(void *ws, ret_stream_t stream);
 
+/* ---- A selective state space layer: norm, short convolution, selective scan ----
+ *
+ * The linear recurrence with a decay that depends on the token, and the two
+ * operators around it, in the forms that retention has: prompts, one token,
+ * gradients.  Tensors [B][N][E] have a batch and a token stride (>= 0, in
+ * elements) and contiguous channels, so that they may be column slices of a
+ * wider projection; they need no more than their element's alignment (rows on
+ * 16-byte boundaries run faster).  `lengths`: int32 or int64 [B], or NULL: the
+ * tokens of a padded batch's sequences, on the device, clamped to 0 .. N.  What
+ * lies behind them is not looked at (it may be NaN), the state after the call
+ * is the one after the sequence's own tokens, and rows of an output or a
+ * gradient behind them are zeros.
+ * Outputs must not overlap one another or an input (RET_EINVAL) unless a call
+ * says so; rows of equal strides may lie between one another's. */
+
+#define RETNET_MAX_STATES 64
+
+typedef struct {
+  int B, N, E;       /* sequences (<= 65535), tokens (<= 2^24), channels (<= 2^24) */
+  int S, G;          /* states of a channel (1 .. RETNET_MAX_STATES); groups: E % G == 0 */
+  ret_dtype dtype;   /* x, dt, z, B, C, y and their gradients                   */
+  int softplus;      /* 1: delta = softplus(dt + bias), 0: delta = dt + bias    */
+  int len_bytes;     /* 4 or 8: int32 or int64 lengths                          */
+  int64_t sx[2], sdt[2], sz[2], sy[2];     /* (batch, token) of x, dt, z, y     */
+  int64_t sdy[2], sdx[2], sddt[2], sdz[2]; /* gradients (backward only)         */
+  int64_t sB[3], sC[3];                    /* (batch, token, group); states contiguous */
+} retnet_scan_desc;
+
+/* Selective scan: for channel e of group e / (E / G), with
+ * delta_t = softplus(dt_t + bias),
+ *   h_t[s] = e^(delta_t A[s]) h_{t-1}[s] + delta_t x_t B_t[s],
+ *   y_t = (sum_s C_t[s] h_t[s] + D x_t) silu(z_t).
+ * fp32 arithmetic and states.  A: fp32 [E][S], finite, and delta_t A <= 0: the
+ * products of many tokens' decays are formed, which would overflow where they
+ * grow (without softplus this needs steps >= 0).  D, bias: fp32 [E],
+ * NULL = 0.  z NULL: no gate.  h_in: fp32 [B][E][S], NULL = 0; h_out: the state
+ * after the last token, or NULL.  ws:
+ * retnet_selective_scan_workspace_size(d) bytes, 256-byte aligned (NULL where 0). */
+size_t retnet_selective_scan_workspace_size(const retnet_scan_desc *d);
+ret_status retnet_selective_scan_fwd(const retnet_scan_desc *d, const void *x, const void *dt,
+                                     const float *A, const void *B, const void *C, const float *D,
+                                     const void *z, const float *bias, const float *h_in,
+                                     const void *lengths, void *y, float *h_out, void *ws,
+                                     size_t ws_bytes, ret_stream_t stream);
+
+/* One token (d->N = 1): x, dt, z, y [B][E], B, C [B][G][S].  h_out may be h_in
+ * itself. */
+ret_status retnet_selective_scan_step(const retnet_scan_desc *d, const void *x, const void *dt,
+                                      const float *A, const void *B, const void *C, const float *D,
+                                      const void *z, const float *bias, const float *h_in, void *y,
+                                      float *h_out, ret_stream_t stream);
+
+/* Gradients of the forward from its inputs (the states are computed again).
+ * dy: gradient of y; dh_out: of h_out, NULL = 0.  dx, ddt and (with z) dz as
+ * [B][N][E] with their strides, dB and dC contiguous [B][N][G][S], in dtype; dA
+ * [E][S], dD, dbias [E] (sums over all tokens) and dh_in [B][E][S] fp32, NULL =
+ * not wanted.  All sums are added in a fixed order: equal calls give equal bits. */
+size_t retnet_selective_scan_bwd_workspace_size(const retnet_scan_desc *d);
+ret_status retnet_selective_scan_bwd(const retnet_scan_desc *d, const void *x, const void *dt,
+                                     const float *A, const void *B, const void *C, const float *D,
+                                     const void *z, const float *bias, const float *h_in,
+                                     const void *lengths, const void *dy, const float *dh_out,
+                                     void *dx, void *ddt, float *dA, void *dB, void *dC, float *dD,
+                                     void *dz, float *dbias, float *dh_in, void *ws,
+                                     size_t ws_bytes, ret_stream_t stream);
+
+typedef struct {
+  int B, N, E;     /* sequences (<= 65535), tokens (<= 2^24), channels (<= 2^24) */
+  int W;           /* taps, 2 .. 4                                             */
+  ret_dtype dtype; /* x, y, states and their gradients                         */
+  int silu;        /* 1: y = silu(pre), 0: y = pre                             */
+  int len_bytes;   /* 4 or 8: int32 or int64 lengths                           */
+  int64_t sx[2];   /* (batch, token) strides of x                              */
+  int64_t sg[2];   /* of dy (backward only)                                    */
+  int64_t so[2];   /* of y (forward) or dx (backward)                          */
+} retnet_conv_desc;
+
+/* Short causal convolution of each channel:
+ *   pre_t = b + sum_k w[k] x_{t-W+1+k},   y_t = silu(pre_t).
+ * w: fp32 [E][W], the last tap the token's own; b: fp32 [E] or NULL.  state_in:
+ * [B][W-1][E] in dtype, the inputs before the first token, the oldest first
+ * (NULL = 0); state_out likewise after the last one (NULL = not wanted; it may
+ * be state_in itself).  One token is a call with N = 1. */
+ret_status retnet_causal_conv_fwd(const retnet_conv_desc *d, const void *x, const float *w,
+                                  const float *b, const void *state_in, const void *lengths, void *y,
+                                  void *state_out, ret_stream_t stream);
+
+/* Gradients: dx, dw [E][W], db [E] (fp32, NULL = not wanted, sums in a fixed
+ * order), dstate_in [B][W-1][E] (NULL = not wanted).  dstate_out: gradient of
+ * state_out, NULL = 0. */
+size_t retnet_causal_conv_bwd_workspace_size(const retnet_conv_desc *d);
+ret_status retnet_causal_conv_bwd(const retnet_conv_desc *d, const void *x, const float *w,
+                                  const float *b, const void *state_in, const void *lengths,
+                                  const void *dy, const void *dstate_out, void *dx, float *dw,
+                                  float *db, void *dstate_in, void *ws, size_t ws_bytes,
+                                  ret_stream_t stream);
+
+typedef struct {
+  int64_t n0, n1;  /* rows, as for LayerNorm                                   */
+  int d;           /* values of a row, 1 .. 2^24                               */
+  ret_dtype dtype; /* of the rows                                              */
+  float eps;       /* >= 0                                                     */
+  int group;       /* 8-bit output: columns of a scale, a multiple of 8; 0 = d */
+  int64_t sx[2];   /* element strides of x (backward: of h)                    */
+  int64_t sr[2];   /* of the residual (backward: of dh)                        */
+  int64_t sh[2];   /* of h                                                     */
+  int64_t sg[2];   /* of dy                                                    */
+  int64_t so[2];   /* of y, of the 8-bit output or of dx                       */
+} retnet_rmsnorm_desc;
+
+/* Root-mean-square norm with the residual's addition before it:
+ *   h = x + r, rounded to dtype (r NULL: h is x, and is not written),
+ *   y = h rstd w,   rstd = 1 / sqrt(mean(h^2) + eps).
+ * w: fp32 [d], NULL = 1.  rstd: fp32 [n0 n1], written where not NULL.  h may be
+ * x or r itself, and so may y (same pointer and strides), but not both. */
+ret_status retnet_rmsnorm_fwd(const retnet_rmsnorm_desc *d, const void *x, const void *r,
+                              const float *w, void *h, void *y, float *rstd, ret_stream_t stream);
+
+/* The same with y as e4m3 values q (one byte each, strides so) and a scale for
+ * each `group` columns, scales [n0 n1][ceil(d / group)] contiguous:
+ *   scale = max |y| / 448 over the group,   q = y / scale rounded to nearest;
+ * a group of zeros has scale 0. */
+ret_status retnet_rmsnorm_quant(const retnet_rmsnorm_desc *d, const void *x, const void *r,
+                                const float *w, void *h, void *q, float *scales,
+                                ret_stream_t stream);
+
+/* Gradients, with n = h rstd and g = dy w:
+ *   dx = rstd (g - n mean(g n)) + dh,   dw = sum_rows dy n,
+ * where dh is the gradient that reaches h itself (NULL = 0); dx is the gradient
+ * of x and of r.  dw: fp32 [d], NULL = not wanted, a sum in a fixed order.  dx
+ * may be h, dy or dh itself. */
+size_t retnet_rmsnorm_bwd_workspace_size(const retnet_rmsnorm_desc *d);
+ret_status retnet_rmsnorm_bwd(const retnet_rmsnorm_desc *d, const void *h, const void *dy,
+                              const void *dh, const float *w, const float *rstd, void *dx, float *dw,
+                              void *ws, size_t ws_bytes, ret_stream_t stream);
+
 /* ---- Instrumentation (no counterpart on the pages; a measuring aid). ----
  * The library counts every kernel it launches.  With the timer enabled it
  * also records a CUDA event pair on the launch stream around each launch,

@@ -1533,6 +1533,461 @@ ret_status retnet_distill_step(const retnet_logits_desc *d, const void *x, const
   return distill_impl(d, x, ids, values, weight, loss, stats, dx, kDistillStep, stream);
 }
 
+// ------------------------------- selective scan, causal convolution, RMS norm
+// What a call touches: rows of `width` contiguous values with two strides.
+struct Span {
+  const void *p;
+  int64_t n0, n1, s[2], width;
+  size_t esz;
+};
+
+static Span span_of(const void *p, int64_t n0, int64_t n1, const int64_t s[2], int64_t width, size_t esz) {
+  return {p, n0, n1, {s[0], s[1]}, width, esz};
+}
+static Span span_flat(const void *p, int64_t n, size_t esz) { return {p, 1, 1, {0, 0}, n, esz}; }
+
+static bool spans_clear(const Span &a, const Span &b) {
+  const size_t na = rows_extent(a.n0, a.n1, a.s, a.width, a.esz), nb = rows_extent(b.n0, b.n1, b.s, b.width, b.esz);
+  if (!overlaps(a.p, na, b.p, nb)) return true;
+  // rows of equal strides may lie between one another's
+  if (a.n0 != b.n0 || a.n1 != b.n1 || a.width != b.width || a.esz != b.esz || !same_rows(a.n0, a.n1, a.s, b.s)) return false;
+  const int64_t bytes = (int64_t)((uintptr_t)b.p - (uintptr_t)a.p);
+  return rows_between(a.n0, a.n1, a.s, a.width, bytes / (int64_t)a.esz);
+}
+
+// Outputs clear of one another and of every input.
+static bool outputs_clear(const Span *in, int n_in, const Span *out, int n_out) {
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = 0; j < n_in; ++j)
+      if (!spans_clear(out[i], in[j])) return false;
+    for (int j = 0; j < i; ++j)
+      if (!spans_clear(out[i], out[j])) return false;
+  }
+  return true;
+}
+
+static bool seq_ok(int B, int N, int E, ret_dtype dtype, int len_bytes) {
+  return B >= 0 && B <= 65535 && N >= 0 && N <= (1 << 24) && E >= 1 && E <= (1 << 24) &&
+         (dtype == RET_F32 || dtype == RET_BF16) && (len_bytes == 4 || len_bytes == 8);
+}
+
+static bool seq_strides_ok(int B, int N, const int64_t s[2]) { return rowset_ok(B, N, s) && strides_bounded(s); }
+
+static bool scan_ok(const retnet_scan_desc *d) {
+  if (!d || !seq_ok(d->B, d->N, d->E, d->dtype, d->len_bytes)) return false;
+  if (d->S < 1 || d->S > RETNET_MAX_STATES || d->G < 1 || d->E % d->G) return false;
+  if (d->softplus != 0 && d->softplus != 1) return false;
+  const int64_t *all[] = {d->sx, d->sdt, d->sz, d->sy, d->sdy, d->sdx, d->sddt, d->sdz, d->sB, d->sC};
+  for (const int64_t *s : all)
+    if (!seq_strides_ok(d->B, d->N, s)) return false;
+  return d->sB[2] >= 0 && d->sC[2] >= 0 && d->sB[2] < ((int64_t)1 << 46) && d->sC[2] < ((int64_t)1 << 46);
+}
+
+static ScanArgs scan_args(const retnet_scan_desc *d, const void *x, const void *dt, const float *A,
+                          const void *B, const void *C, const float *D, const void *z,
+                          const float *bias, const float *h_in, const void *lengths) {
+  ScanArgs a;
+  a.B = d->B; a.N = d->N; a.E = d->E; a.S = d->S; a.G = d->G; a.softplus = d->softplus;
+  a.x = x; a.dt = dt; a.z = z; a.Bm = B; a.Cm = C; a.A = A; a.D = D; a.bias = bias; a.h_in = h_in;
+  a.lengths = lengths;
+  a.len64 = d->len_bytes == 8;
+  for (int i = 0; i < 2; ++i) {
+    a.sx[i] = d->sx[i]; a.sdt[i] = d->sdt[i]; a.sz[i] = d->sz[i]; a.sy[i] = d->sy[i];
+    a.sdy[i] = d->sdy[i]; a.sdx[i] = d->sdx[i]; a.sddt[i] = d->sddt[i]; a.sdz[i] = d->sdz[i];
+  }
+  for (int i = 0; i < 3; ++i) { a.sB[i] = d->sB[i]; a.sC[i] = d->sC[i]; }
+  return a;
+}
+
+// The inputs that every form of the scan reads, as spans (returns their number).
+static int scan_inputs(const retnet_scan_desc *d, const ScanArgs &a, Span *in) {
+  const size_t esz = d->dtype == RET_BF16 ? 2 : 4;
+  int n = 0;
+  in[n++] = span_of(a.x, a.B, a.N, d->sx, a.E, esz);
+  in[n++] = span_of(a.dt, a.B, a.N, d->sdt, a.E, esz);
+  if (a.z) in[n++] = span_of(a.z, a.B, a.N, d->sz, a.E, esz);
+  in[n++] = span_of(a.Bm, a.B, a.N, d->sB, (int64_t)(a.G - 1) * d->sB[2] + a.S, esz);
+  in[n++] = span_of(a.Cm, a.B, a.N, d->sC, (int64_t)(a.G - 1) * d->sC[2] + a.S, esz);
+  in[n++] = span_flat(a.A, (int64_t)a.E * a.S, 4);
+  if (a.D) in[n++] = span_flat(a.D, a.E, 4);
+  if (a.bias) in[n++] = span_flat(a.bias, a.E, 4);
+  if (a.lengths) in[n++] = span_flat(a.lengths, a.B, (size_t)d->len_bytes);
+  return n;
+}
+
+// Pointers that every form needs where there are tokens, and their alignment.
+static bool scan_pointers_ok(const retnet_scan_desc *d, const ScanArgs &a) {
+  const size_t esz = d->dtype == RET_BF16 ? 2 : 4;
+  return a.x && a.dt && a.Bm && a.Cm && elem_aligned(a.x, esz) && elem_aligned(a.dt, esz) &&
+         elem_aligned(a.Bm, esz) && elem_aligned(a.Cm, esz) && elem_aligned(a.z, esz) &&
+         elem_aligned(a.D, 4) && elem_aligned(a.bias, 4) && elem_aligned(a.h_in, 4) &&
+         elem_aligned(a.lengths, (size_t)d->len_bytes);
+}
+
+// A grid of at most 2^31 - 1 CTAs along x for blocks of `channels` and `tokens`.
+static bool scan_grid_ok(const retnet_scan_desc *d, int channels, int tokens) {
+  const int64_t Eg = d->E / d->G, blocks = d->G * ((Eg + channels - 1) / channels);
+  return blocks * (((int64_t)d->N + tokens - 1) / tokens) < ((int64_t)1 << 31);
+}
+
+size_t retnet_selective_scan_workspace_size(const retnet_scan_desc *d) {
+  if (!scan_ok(d)) return 0;
+  const size_t n = scan_fwd_bytes(scan_args(d, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr));
+  return n ? align256(n) : 0;
+}
+
+ret_status retnet_selective_scan_fwd(const retnet_scan_desc *d, const void *x, const void *dt,
+                                     const float *A, const void *B, const void *C, const float *D,
+                                     const void *z, const float *bias, const float *h_in,
+                                     const void *lengths, void *y, float *h_out, void *ws,
+                                     size_t ws_bytes, ret_stream_t stream) {
+  RET_RANGE("retnet_selective_scan_fwd");
+  if (!scan_ok(d) || !rows_disjoint(d->B, d->N, d->sy, d->E)) return RET_EINVAL;
+  ret_status rs = check_ws(ws, ws_bytes, retnet_selective_scan_workspace_size(d));
+  if (rs != RET_OK) return rs;
+  if (d->B == 0) return RET_OK;
+  ScanArgs a = scan_args(d, x, dt, A, B, C, D, z, bias, h_in, lengths);
+  a.y = y;
+  a.h_out = h_out;
+  const size_t esz = d->dtype == RET_BF16 ? 2 : 4;
+  const int64_t states = (int64_t)a.B * a.E * a.S;
+  if (!A || !elem_aligned(A, 4) || !elem_aligned(h_out, 4)) return RET_EINVAL;
+  if (a.N > 0 && (!scan_pointers_ok(d, a) || !y || !elem_aligned(y, esz))) return RET_EINVAL;
+  Span in[12], out[2];
+  int ni = scan_inputs(d, a, in), no = 0;
+  if (h_in) in[ni++] = span_flat(h_in, states, 4);
+  out[no++] = span_of(y, a.B, a.N, d->sy, a.E, esz);
+  if (h_out) out[no++] = span_flat(h_out, states, 4);
+  if (!outputs_clear(in, ni, out, no)) return RET_EINVAL;
+  if (!scan_grid_ok(d, 1, 1 << 24)) return RET_EUNSUPPORTED;
+  cudaStream_t st = (cudaStream_t)stream;
+  const int bf16 = d->dtype == RET_BF16;
+  ScanSegs seg = scan_fwd_plan(a);
+  if (seg.count > 1) {
+    seg.loc = at<float>(ws, 0);
+    seg.sum = seg.loc + (size_t)(seg.count - 1) * states;
+    RET_CUDA(RET_TIMED_LAUNCH(kKScanStates, st, launch_scan_states(a, bf16, seg, st)));
+  }
+  RET_CUDA(RET_TIMED_LAUNCH(kKScanFwd, st, launch_scan_fwd(a, bf16, seg, st)));
+  return RET_OK;
+}
+
+ret_status retnet_selective_scan_step(const retnet_scan_desc *d, const void *x, const void *dt,
+                                      const float *A, const void *B, const void *C, const float *D,
+                                      const void *z, const float *bias, const float *h_in, void *y,
+                                      float *h_out, ret_stream_t stream) {
+  RET_RANGE("retnet_selective_scan_step");
+  if (!scan_ok(d) || d->N != 1 || !rows_disjoint(d->B, 1, d->sy, d->E)) return RET_EINVAL;
+  if (d->B == 0) return RET_OK;
+  ScanArgs a = scan_args(d, x, dt, A, B, C, D, z, bias, h_in, nullptr);
+  a.y = y;
+  a.h_out = h_out;
+  const size_t esz = d->dtype == RET_BF16 ? 2 : 4;
+  const int64_t states = (int64_t)a.B * a.E * a.S;
+  if (!A || !elem_aligned(A, 4) || !scan_pointers_ok(d, a) || !h_in || !h_out || !elem_aligned(h_out, 4) || !y ||
+      !elem_aligned(y, esz))
+    return RET_EINVAL;
+  Span in[12], out[2];
+  int ni = scan_inputs(d, a, in);
+  if (h_in != h_out) in[ni++] = span_flat(h_in, states, 4);
+  out[0] = span_of(y, a.B, 1, d->sy, a.E, esz);
+  out[1] = span_flat(h_out, states, 4);
+  if (!outputs_clear(in, ni, out, 2)) return RET_EINVAL;
+  cudaStream_t st = (cudaStream_t)stream;
+  RET_CUDA(RET_TIMED_LAUNCH(kKScanStep, st, launch_scan_step(a, d->dtype == RET_BF16, st)));
+  return RET_OK;
+}
+
+size_t retnet_selective_scan_bwd_workspace_size(const retnet_scan_desc *d) {
+  if (!scan_ok(d)) return 0;
+  const ScanArgs a = scan_args(d, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr);
+  return align256(scan_bwd_plan(a).total * sizeof(float)) + 256;
+}
+
+ret_status retnet_selective_scan_bwd(const retnet_scan_desc *d, const void *x, const void *dt,
+                                     const float *A, const void *B, const void *C, const float *D,
+                                     const void *z, const float *bias, const float *h_in,
+                                     const void *lengths, const void *dy, const float *dh_out,
+                                     void *dx, void *ddt, float *dA, void *dB, void *dC, float *dD,
+                                     void *dz, float *dbias, float *dh_in, void *ws,
+                                     size_t ws_bytes, ret_stream_t stream) {
+  RET_RANGE("retnet_selective_scan_bwd");
+  if (!scan_ok(d) || !rows_disjoint(d->B, d->N, d->sdx, d->E) || !rows_disjoint(d->B, d->N, d->sddt, d->E) ||
+      (z && !rows_disjoint(d->B, d->N, d->sdz, d->E)))
+    return RET_EINVAL;
+  ret_status rs = check_ws(ws, ws_bytes, retnet_selective_scan_bwd_workspace_size(d));
+  if (rs != RET_OK) return rs;
+  ScanArgs a = scan_args(d, x, dt, A, B, C, D, z, bias, h_in, lengths);
+  a.dy = dy; a.dh_out = dh_out; a.dx = dx; a.ddt = ddt; a.dz = dz; a.dBm = dB; a.dCm = dC;
+  a.dA = dA; a.dD = dD; a.dbias = dbias; a.dh_in = dh_in;
+  const size_t esz = d->dtype == RET_BF16 ? 2 : 4;
+  const int64_t states = (int64_t)a.B * a.E * a.S, bc = (int64_t)a.B * a.N * a.G * a.S;
+  if (!A || !elem_aligned(A, 4) || !elem_aligned(dh_out, 4) || !elem_aligned(dA, 4) || !elem_aligned(dD, 4) ||
+      !elem_aligned(dbias, 4) || !elem_aligned(dh_in, 4))
+    return RET_EINVAL;
+  const bool tokens = a.B > 0 && a.N > 0;
+  if (tokens && (!scan_pointers_ok(d, a) || !dy || !dx || !ddt || !dB || !dC || (z && !dz) || !elem_aligned(dy, esz) ||
+                 !elem_aligned(dx, esz) || !elem_aligned(ddt, esz) || !elem_aligned(dz, esz) ||
+                 !elem_aligned(dB, esz) || !elem_aligned(dC, esz)))
+    return RET_EINVAL;
+  Span in[13], out[9];
+  int ni = scan_inputs(d, a, in), no = 0;
+  in[ni++] = span_of(dy, a.B, a.N, d->sdy, a.E, esz);
+  if (h_in) in[ni++] = span_flat(h_in, states, 4);
+  if (dh_out) in[ni++] = span_flat(dh_out, states, 4);
+  out[no++] = span_of(dx, a.B, a.N, d->sdx, a.E, esz);
+  out[no++] = span_of(ddt, a.B, a.N, d->sddt, a.E, esz);
+  if (z) out[no++] = span_of(dz, a.B, a.N, d->sdz, a.E, esz);
+  out[no++] = span_flat(dB, bc, esz);
+  out[no++] = span_flat(dC, bc, esz);
+  if (dA) out[no++] = span_flat(dA, (int64_t)a.E * a.S, 4);
+  if (dD) out[no++] = span_flat(dD, a.E, 4);
+  if (dbias) out[no++] = span_flat(dbias, a.E, 4);
+  if (dh_in) out[no++] = span_flat(dh_in, states, 4);
+  if (!outputs_clear(in, ni, out, no)) return RET_EINVAL;
+  cudaStream_t st = (cudaStream_t)stream;
+  const int bf16 = d->dtype == RET_BF16;
+  ScanBwdPlan pl = scan_bwd_plan(a);
+  if (!scan_grid_ok(d, 8, pl.chunk) || states / 256 >= ((int64_t)1 << 31) || bc / 128 >= ((int64_t)1 << 31))
+    return RET_EUNSUPPORTED;
+  float *w = at<float>(ws, 0);
+  if (tokens) RET_CUDA(RET_TIMED_LAUNCH(kKScanBwdChunks, st, launch_scan_bwd_chunks(a, bf16, pl, w, st)));
+  if (a.B > 0) RET_CUDA(RET_TIMED_LAUNCH(kKScanBwdCarry, st, launch_scan_bwd_carry(a, pl, w, st)));
+  if (tokens) {
+    RET_CUDA(RET_TIMED_LAUNCH(kKScanBwd, st, launch_scan_bwd(a, bf16, pl, w, st)));
+    RET_CUDA(RET_TIMED_LAUNCH(kKScanBwdBc, st, launch_scan_bwd_bc(a, bf16, pl, w, st)));
+  }
+  ColSum cs;
+  cs.count = tokens ? pl.chunks * a.B : 0;
+  const int64_t rows = (int64_t)pl.chunks * a.B;
+  const float *parts[3] = {w, w + pl.dd, w + pl.dd + rows * a.E};
+  float *outs[3] = {dA, dD, dbias};
+  for (int i = 0; i < 3; ++i) {
+    cs.part[i] = parts[i];
+    cs.out[i] = outs[i];
+    cs.cols[i] = i == 0 ? a.E * a.S : a.E;
+    cs.stride[i] = cs.cols[i];
+  }
+  RET_CUDA(RET_TIMED_LAUNCH(kKColSum, st, launch_colsum(cs, st)));
+  return RET_OK;
+}
+
+static bool conv_ok(const retnet_conv_desc *d) {
+  if (!d || !seq_ok(d->B, d->N, d->E, d->dtype, d->len_bytes)) return false;
+  if (d->W < 2 || d->W > 4 || (d->silu != 0 && d->silu != 1)) return false;
+  return seq_strides_ok(d->B, d->N, d->sx) && seq_strides_ok(d->B, d->N, d->sg) && seq_strides_ok(d->B, d->N, d->so) &&
+         rows_disjoint(d->B, d->N, d->so, d->E);
+}
+
+static ConvArgs conv_args(const retnet_conv_desc *d, const void *x, const float *w, const float *b,
+                          const void *state_in, const void *lengths) {
+  ConvArgs a;
+  a.B = d->B; a.N = d->N; a.E = d->E; a.W = d->W; a.silu = d->silu;
+  a.x = x; a.w = w; a.b = b; a.state_in = state_in; a.lengths = lengths;
+  a.len64 = d->len_bytes == 8;
+  for (int i = 0; i < 2; ++i) { a.sx[i] = d->sx[i]; a.sg[i] = d->sg[i]; a.so[i] = d->so[i]; }
+  return a;
+}
+
+ret_status retnet_causal_conv_fwd(const retnet_conv_desc *d, const void *x, const float *w,
+                                  const float *b, const void *state_in, const void *lengths, void *y,
+                                  void *state_out, ret_stream_t stream) {
+  RET_RANGE("retnet_causal_conv_fwd");
+  if (!conv_ok(d)) return RET_EINVAL;
+  if (d->B == 0) return RET_OK;
+  ConvArgs a = conv_args(d, x, w, b, state_in, lengths);
+  a.out = y;
+  a.state_out = state_out;
+  const size_t esz = d->dtype == RET_BF16 ? 2 : 4;
+  const int64_t states = (int64_t)a.B * (a.W - 1) * a.E;
+  if (!w || !elem_aligned(w, 4) || !elem_aligned(b, 4) || !elem_aligned(state_in, esz) || !elem_aligned(state_out, esz) ||
+      !elem_aligned(lengths, (size_t)d->len_bytes))
+    return RET_EINVAL;
+  if (a.N > 0 && (!x || !y || !elem_aligned(x, esz) || !elem_aligned(y, esz))) return RET_EINVAL;
+  const Span in[] = {span_of(x, a.B, a.N, d->sx, a.E, esz), span_flat(w, (int64_t)a.E * a.W, 4), span_flat(b, a.E, 4),
+                     span_flat(lengths, a.B, (size_t)d->len_bytes),
+                     span_flat(state_in == state_out ? nullptr : state_in, states, esz)};
+  const Span out[] = {span_of(y, a.B, a.N, d->so, a.E, esz), span_flat(state_out, states, esz)};
+  if (!outputs_clear(in, 5, out, 2)) return RET_EINVAL;
+  cudaStream_t st = (cudaStream_t)stream;
+  RET_CUDA(RET_TIMED_LAUNCH(kKConvFwd, st, launch_conv_fwd(a, d->dtype == RET_BF16, st)));
+  return RET_OK;
+}
+
+size_t retnet_causal_conv_bwd_workspace_size(const retnet_conv_desc *d) {
+  if (!conv_ok(d)) return 0;
+  if (d->B == 0) return 256;
+  const ConvArgs a = conv_args(d, nullptr, nullptr, nullptr, nullptr, nullptr);
+  return align256((size_t)conv_bwd_runs(a) * a.E * (a.W + 1) * sizeof(float)) + 256;
+}
+
+ret_status retnet_causal_conv_bwd(const retnet_conv_desc *d, const void *x, const float *w,
+                                  const float *b, const void *state_in, const void *lengths,
+                                  const void *dy, const void *dstate_out, void *dx, float *dw,
+                                  float *db, void *dstate_in, void *ws, size_t ws_bytes,
+                                  ret_stream_t stream) {
+  RET_RANGE("retnet_causal_conv_bwd");
+  if (!conv_ok(d)) return RET_EINVAL;
+  ret_status rs = check_ws(ws, ws_bytes, retnet_causal_conv_bwd_workspace_size(d));
+  if (rs != RET_OK) return rs;
+  ConvArgs a = conv_args(d, x, w, b, state_in, lengths);
+  a.dy = dy; a.dstate_out = dstate_out; a.out = dx; a.dstate_in = dstate_in;
+  const size_t esz = d->dtype == RET_BF16 ? 2 : 4;
+  const int64_t states = (int64_t)a.B * (a.W - 1) * a.E;
+  if (!w || !elem_aligned(w, 4) || !elem_aligned(b, 4) || !elem_aligned(dw, 4) || !elem_aligned(db, 4) ||
+      !elem_aligned(state_in, esz) || !elem_aligned(dstate_in, esz) || !elem_aligned(dstate_out, esz) ||
+      !elem_aligned(lengths, (size_t)d->len_bytes))
+    return RET_EINVAL;
+  if (a.B > 0 && a.N > 0 && (!x || !dy || !dx || !elem_aligned(x, esz) || !elem_aligned(dy, esz) || !elem_aligned(dx, esz)))
+    return RET_EINVAL;
+  const Span in[] = {span_of(x, a.B, a.N, d->sx, a.E, esz), span_of(dy, a.B, a.N, d->sg, a.E, esz),
+                     span_flat(w, (int64_t)a.E * a.W, 4), span_flat(b, a.E, 4),
+                     span_flat(lengths, a.B, (size_t)d->len_bytes), span_flat(state_in, states, esz),
+                     span_flat(dstate_out, states, esz)};
+  const Span out[] = {span_of(dx, a.B, a.N, d->so, a.E, esz), span_flat(dstate_in, states, esz),
+                      span_flat(dw, (int64_t)a.E * a.W, 4), span_flat(db, a.E, 4)};
+  if (!outputs_clear(in, 7, out, 4)) return RET_EINVAL;
+  cudaStream_t st = (cudaStream_t)stream;
+  float *part = at<float>(ws, 0);
+  const int runs = a.B > 0 ? conv_bwd_runs(a) : 0;
+  if (a.B > 0)
+    RET_CUDA(RET_TIMED_LAUNCH(kKConvBwd, st, launch_conv_bwd(a, d->dtype == RET_BF16, dw || db ? part : nullptr, st)));
+  ColSum cs;
+  cs.count = runs;
+  cs.part[0] = part;
+  cs.part[1] = part + (size_t)runs * a.E * a.W;
+  cs.out[0] = dw;
+  cs.out[1] = db;
+  cs.cols[0] = a.E * a.W;
+  cs.cols[1] = a.E;
+  for (int i = 0; i < 2; ++i) cs.stride[i] = cs.cols[i];
+  if (dw || db) RET_CUDA(RET_TIMED_LAUNCH(kKColSum, st, launch_colsum(cs, st)));
+  return RET_OK;
+}
+
+static bool rms_ok(const retnet_rmsnorm_desc *d) {
+  if (!d || d->d < 1 || d->d > (1 << 24)) return false;
+  if (d->dtype != RET_F32 && d->dtype != RET_BF16) return false;
+  if (!(d->eps >= 0.f) || !isfinite(d->eps)) return false;
+  if (d->group < 0 || d->group % 8) return false;
+  if (!rows_countable(d->n0, d->n1)) return false;
+  const int64_t *all[] = {d->sx, d->sr, d->sh, d->sg, d->so};
+  for (const int64_t *s : all)
+    if (!rowset_ok(d->n0, d->n1, s) || !strides_bounded(s)) return false;
+  return rows_disjoint(d->n0, d->n1, d->so, d->d);
+}
+
+static RmsArgs rms_args(const retnet_rmsnorm_desc *d) {
+  RmsArgs a;
+  a.sx = row_set(d->n0, d->n1, d->sx);
+  a.sr = row_set(d->n0, d->n1, d->sr);
+  a.sdh = a.sr;
+  a.sh = row_set(d->n0, d->n1, d->sh);
+  a.sg = row_set(d->n0, d->n1, d->sg);
+  a.so = row_set(d->n0, d->n1, d->so);
+  a.rows = d->n0 * d->n1;
+  a.d = d->d;
+  a.eps = d->eps;
+  a.group = d->group && d->group < d->d ? d->group : d->d;
+  a.groups = (d->d + a.group - 1) / a.group;
+  return a;
+}
+
+static ret_status rms_fwd_impl(const retnet_rmsnorm_desc *d, const void *x, const void *r, const float *w,
+                               void *h, void *out, float *rstd, float *scales, bool quant,
+                               ret_stream_t stream) {
+  if (!rms_ok(d) || (r && !rows_disjoint(d->n0, d->n1, d->sh, d->d))) return RET_EINVAL;
+  RmsArgs a = rms_args(d);
+  if (a.rows == 0) return RET_OK;
+  const size_t esz = d->dtype == RET_BF16 ? 2 : 4, osz = quant ? 1 : esz;
+  if (!x || !out || (r && !h) || (quant && !scales) || !elem_aligned(x, esz) || !elem_aligned(r, esz) ||
+      !elem_aligned(h, esz) || !elem_aligned(out, osz) || !elem_aligned(w, 4) || !elem_aligned(rstd, 4) || !elem_aligned(scales, 4))
+    return RET_EINVAL;
+  const Span X = span_of(x, d->n0, d->n1, d->sx, a.d, esz), R = span_of(r, d->n0, d->n1, d->sr, a.d, esz);
+  const Span H = span_of(r ? h : nullptr, d->n0, d->n1, d->sh, a.d, esz), O = span_of(out, d->n0, d->n1, d->so, a.d, osz);
+  const Span flat[] = {span_flat(w, a.d, 4)};
+  const Span outs[] = {H, O, span_flat(rstd, a.rows, 4), span_flat(scales, a.rows * a.groups, 4)};
+  if (!outputs_clear(flat, 1, outs, 4)) return RET_EINVAL;
+  if (!spans_clear(outs[2], X) || !spans_clear(outs[2], R) || !spans_clear(outs[3], X) || !spans_clear(outs[3], R)) return RET_EINVAL;
+  // h and y may each be an input itself
+  auto fits = [&](const Span &o, const Span &i) {
+    return spans_clear(o, i) || (o.p == i.p && o.esz == i.esz && same_rows(d->n0, d->n1, o.s, i.s));
+  };
+  if (!fits(H, X) || !fits(H, R) || !fits(O, X) || !fits(O, R)) return RET_EINVAL;
+  a.x = x; a.r = r; a.h = h; a.out = out; a.w = w; a.rstd = rstd; a.scales = scales;
+  cudaStream_t st = (cudaStream_t)stream;
+  const int bf16 = d->dtype == RET_BF16;
+  if (quant)
+    RET_CUDA(RET_TIMED_LAUNCH(kKRmsQuant, st, launch_rmsnorm_quant(a, bf16, st)));
+  else
+    RET_CUDA(RET_TIMED_LAUNCH(kKRmsFwd, st, launch_rmsnorm_fwd(a, bf16, st)));
+  return RET_OK;
+}
+
+ret_status retnet_rmsnorm_fwd(const retnet_rmsnorm_desc *d, const void *x, const void *r,
+                              const float *w, void *h, void *y, float *rstd, ret_stream_t stream) {
+  RET_RANGE("retnet_rmsnorm_fwd");
+  return rms_fwd_impl(d, x, r, w, h, y, rstd, nullptr, false, stream);
+}
+
+ret_status retnet_rmsnorm_quant(const retnet_rmsnorm_desc *d, const void *x, const void *r,
+                                const float *w, void *h, void *q, float *scales,
+                                ret_stream_t stream) {
+  RET_RANGE("retnet_rmsnorm_quant");
+  return rms_fwd_impl(d, x, r, w, h, q, nullptr, scales, true, stream);
+}
+
+size_t retnet_rmsnorm_bwd_workspace_size(const retnet_rmsnorm_desc *d) {
+  if (!rms_ok(d)) return 0;
+  return align256(rmsnorm_bwd_bytes(d->n0 * d->n1, d->d)) + 256;
+}
+
+ret_status retnet_rmsnorm_bwd(const retnet_rmsnorm_desc *d, const void *h, const void *dy,
+                              const void *dh, const float *w, const float *rstd, void *dx, float *dw,
+                              void *ws, size_t ws_bytes, ret_stream_t stream) {
+  RET_RANGE("retnet_rmsnorm_bwd");
+  if (!rms_ok(d)) return RET_EINVAL;
+  ret_status rs = check_ws(ws, ws_bytes, retnet_rmsnorm_bwd_workspace_size(d));
+  if (rs != RET_OK) return rs;
+  RmsArgs a = rms_args(d);
+  cudaStream_t st = (cudaStream_t)stream;
+  float *part = at<float>(ws, 0);
+  const int bf16 = d->dtype == RET_BF16;
+  int groups = 0;
+  if (!elem_aligned(w, 4) || !elem_aligned(dw, 4)) return RET_EINVAL;
+  if (a.rows > 0) {
+    const size_t esz = bf16 ? 2 : 4;
+    if (!h || !dy || !dx || !rstd || !elem_aligned(h, esz) || !elem_aligned(dy, esz) || !elem_aligned(dh, esz) ||
+        !elem_aligned(dx, esz) || !elem_aligned(rstd, 4))
+      return RET_EINVAL;
+    if (!in_place_or_clear(d->n0, d->n1, h, d->sx, dx, d->so, d->d, esz) ||
+        !in_place_or_clear(d->n0, d->n1, dy, d->sg, dx, d->so, d->d, esz) ||
+        !in_place_or_clear(d->n0, d->n1, dh, d->sr, dx, d->so, d->d, esz))
+      return RET_EINVAL;
+    const Span in[] = {span_flat(w, a.d, 4), span_flat(rstd, a.rows, 4)};
+    const Span out[] = {span_of(dx, d->n0, d->n1, d->so, a.d, esz), span_flat(dw, a.d, 4)};
+    if (!outputs_clear(in, 2, out, 2)) return RET_EINVAL;
+    a.x = h; a.dy = dy; a.dh = dh; a.out = dx; a.w = w;
+    a.rstd = const_cast<float *>(rstd);
+    const RmsBwdPlan pl = rmsnorm_bwd_plan(a, bf16);
+    groups = pl.groups;
+    float *stat = part + (size_t)groups * a.d;
+    if (pl.two_pass)
+      RET_CUDA(RET_TIMED_LAUNCH(kKRmsBwdStat, st, launch_rmsnorm_bwd_stat(a, bf16, pl, stat, st)));
+    RET_CUDA(RET_TIMED_LAUNCH(kKRmsBwd, st, launch_rmsnorm_bwd(a, bf16, pl, stat, dw ? part : nullptr, st)));
+  }
+  if (dw) {
+    ColSum cs;
+    cs.count = groups;
+    cs.part[0] = part;
+    cs.out[0] = dw;
+    cs.cols[0] = a.d;
+    cs.stride[0] = a.d;
+    RET_CUDA(RET_TIMED_LAUNCH(kKColSum, st, launch_colsum(cs, st)));
+  }
+  return RET_OK;
+}
+
 const char *retention_status_string(ret_status s) {
   switch (s) {
     case RET_OK: return "ok";

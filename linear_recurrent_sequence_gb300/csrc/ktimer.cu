@@ -19,7 +19,10 @@ const char *kNames[kKernelCount] = {
     "layernorm", "residual_add", "gelu", "gemm_skinny", "skinny_reduce",
     "state_combine", "state_simt", "bwd_prep", "bwd_finish", "parallel_tc",
     "layernorm_fwd", "layernorm_bwd_stat", "layernorm_bwd", "layernorm_bwd_sum",
-    "token_logprobs", "distill"};
+    "token_logprobs", "distill",
+    "scan_states", "scan_fwd", "scan_step", "scan_bwd_chunks", "scan_bwd_carry", "scan_bwd",
+    "scan_bwd_bc", "column_sums", "causal_conv_fwd", "causal_conv_bwd",
+    "rmsnorm_fwd", "rmsnorm_quant", "rmsnorm_bwd_stat", "rmsnorm_bwd"};
 
 struct Slot {
   std::vector<cudaEvent_t> start, stop;

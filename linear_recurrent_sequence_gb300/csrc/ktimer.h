@@ -37,6 +37,20 @@ enum KernelId {
   kKLnBwdSum,
   kKLogprobs,
   kKDistill,
+  kKScanStates,
+  kKScanFwd,
+  kKScanStep,
+  kKScanBwdChunks,
+  kKScanBwdCarry,
+  kKScanBwd,
+  kKScanBwdBc,
+  kKColSum,
+  kKConvFwd,
+  kKConvBwd,
+  kKRmsFwd,
+  kKRmsQuant,
+  kKRmsBwdStat,
+  kKRmsBwd,
   kKernelCount
 };
 

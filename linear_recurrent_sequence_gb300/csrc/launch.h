@@ -289,6 +289,105 @@ struct DistillArgs {
 };
 cudaError_t launch_distill(const DistillArgs &a, int bf16, int what, cudaStream_t st);
 
+// scan_fwd.cu, scan_bwd.cu: the selective scan over [B][N][E] channels with S
+// states each, and its gradients.  Strides in elements: (batch, token) of the
+// channels' tensors, (batch, token, group) of B and C.  A [E][S], states
+// [B][E][S], D, bias [E]: contiguous fp32.
+struct ScanArgs {
+  int B = 0, N = 0, E = 0, S = 0, G = 1, softplus = 1;
+  const void *x = nullptr, *dt = nullptr, *z = nullptr, *Bm = nullptr, *Cm = nullptr, *dy = nullptr;
+  const float *A = nullptr, *D = nullptr, *bias = nullptr, *h_in = nullptr, *dh_out = nullptr;
+  const void *lengths = nullptr;  // [B] int32 / int64, null = N
+  int len64 = 0;
+  void *y = nullptr, *dx = nullptr, *ddt = nullptr, *dz = nullptr, *dBm = nullptr, *dCm = nullptr;
+  float *h_out = nullptr, *dA = nullptr, *dD = nullptr, *dbias = nullptr, *dh_in = nullptr;
+  long long sx[2] = {}, sdt[2] = {}, sz[2] = {}, sdy[2] = {}, sy[2] = {}, sdx[2] = {}, sddt[2] = {},
+            sdz[2] = {}, sB[3] = {}, sC[3] = {};
+};
+// Segments of a sequence that run at once; loc [count-1][B][E][S]: the state
+// that each segment but the last leaves behind from a zero state, sum
+// [count-1][B][E]: its step sizes added up.
+struct ScanSegs {
+  int count = 1, len = 0;
+  float *loc = nullptr, *sum = nullptr;
+};
+ScanSegs scan_fwd_plan(const ScanArgs &a);
+size_t scan_fwd_bytes(const ScanArgs &a);  // loc and sum
+cudaError_t launch_scan_states(const ScanArgs &a, int bf16, const ScanSegs &seg, cudaStream_t st);
+cudaError_t launch_scan_fwd(const ScanArgs &a, int bf16, const ScanSegs &seg, cudaStream_t st);
+// Gradients, in chunks of `chunk` tokens that run on their own once the states
+// at their ends are known.  h, g [chunks][B][E][S]: first what a chunk alone
+// adds to the state after it (h) and to the state's gradient before it (g),
+// then the state before it and the gradient that arrives behind it; dA's
+// partial sums take h's place.  sum [chunks][B][E]: step sizes added up.
+// bc [blocks][B][N][G][2][S]: a channel block's share of dB and dC.  dd
+// [2][chunks][B][E]: partial sums of dD and dbias.
+struct ScanBwdPlan {
+  int chunk = 0, chunks = 0, blocks = 0;
+  size_t g = 0, sum = 0, bc = 0, dd = 0, total = 0;  // offsets in floats (h at 0)
+};
+ScanBwdPlan scan_bwd_plan(const ScanArgs &a);
+cudaError_t launch_scan_bwd_chunks(const ScanArgs &a, int bf16, const ScanBwdPlan &pl, float *ws, cudaStream_t st);
+cudaError_t launch_scan_bwd_carry(const ScanArgs &a, const ScanBwdPlan &pl, float *ws, cudaStream_t st);
+cudaError_t launch_scan_bwd(const ScanArgs &a, int bf16, const ScanBwdPlan &pl, float *ws, cudaStream_t st);
+cudaError_t launch_scan_bwd_bc(const ScanArgs &a, int bf16, const ScanBwdPlan &pl, const float *ws, cudaStream_t st);
+
+// colsum.cu: out[c] = sum_p part[p * stride + c], p < count, in a fixed order.
+// Up to three such sums of one count in a launch (out null = none).
+struct ColSum {
+  const float *part[3] = {};
+  long long stride[3] = {};
+  int cols[3] = {}, count = 0;
+  float *out[3] = {};
+};
+cudaError_t launch_colsum(const ColSum &c, cudaStream_t st);
+
+// One token: x, dt, z, y [B][E], B, C [B][G][S]; h_out may be h_in.
+cudaError_t launch_scan_step(const ScanArgs &a, int bf16, cudaStream_t st);
+
+// conv.cu: the short causal convolution over [B][N][E], W taps (2 to 4), and
+// its gradients.  w [E][W], b [E] fp32; states [B][W-1][E] contiguous in the
+// tensors' type, null = zeros / not wanted.
+struct ConvArgs {
+  int B = 0, N = 0, E = 0, W = 0, silu = 1;
+  const void *x = nullptr, *dy = nullptr, *state_in = nullptr, *dstate_out = nullptr;
+  const float *w = nullptr, *b = nullptr;
+  const void *lengths = nullptr;
+  int len64 = 0;
+  void *out = nullptr, *state_out = nullptr, *dstate_in = nullptr;  // out: y or dx
+  long long sx[2] = {}, sg[2] = {}, so[2] = {};                    // of x, dy, out: (batch, token)
+};
+cudaError_t launch_conv_fwd(const ConvArgs &a, int bf16, cudaStream_t st);
+// Partial sums of dw and db: part [runs][E][W] and then [runs][E], a run of
+// tokens each (null = not wanted).
+int conv_bwd_runs(const ConvArgs &a);
+cudaError_t launch_conv_bwd(const ConvArgs &a, int bf16, float *part, cudaStream_t st);
+
+// rmsnorm.cu: h = x + r (r null: x), y = h rstd w over rows of d values.
+struct RmsArgs {
+  const void *x = nullptr, *r = nullptr, *dy = nullptr, *dh = nullptr;
+  void *h = nullptr, *out = nullptr;  // out: y, e4m3 values or dx
+  const float *w = nullptr;
+  float *rstd = nullptr, *scales = nullptr;
+  RowSet sx, sr, sh, sg, sdh, so;
+  long long rows = 0;
+  int d = 0, group = 0, groups = 1;  // group: columns of a scale
+  float eps = 0.f;
+};
+cudaError_t launch_rmsnorm_fwd(const RmsArgs &a, int bf16, cudaStream_t st);
+cudaError_t launch_rmsnorm_quant(const RmsArgs &a, int bf16, cudaStream_t st);
+// x holds h.  dw's partial sums: part [groups][d]; stat [rows] for rows too
+// long for registers.
+struct RmsBwdPlan {
+  bool vec = false, two_pass = false;
+  int values = 0, tpr = 0, groups = 0;  // values a thread, threads a row; CTAs
+};
+RmsBwdPlan rmsnorm_bwd_plan(const RmsArgs &a, int bf16);
+size_t rmsnorm_bwd_bytes(long long rows, int d);
+cudaError_t launch_rmsnorm_bwd_stat(const RmsArgs &a, int bf16, const RmsBwdPlan &pl, float *stat, cudaStream_t st);
+cudaError_t launch_rmsnorm_bwd(const RmsArgs &a, int bf16, const RmsBwdPlan &pl, const float *stat, float *part,
+                               cudaStream_t st);
+
 // gemm_skinny.cu: C[M,N] = A[M,K] B[K,N] for M <= 16 rows (bf16 row-major,
 // fp32 accumulation), split over K into fp32 partials [split][M][N] that
 // launch_skinny_reduce adds in order into bf16 C.  Needs N % 8 == 0 and a

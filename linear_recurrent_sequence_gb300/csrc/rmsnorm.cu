@@ -1,0 +1,539 @@
+// Root-mean-square norm over rows of d values, with the residual's addition
+// before it, an 8-bit output with scales, and its gradients:
+//   h = x + r (rounded to the rows' type, and what is kept is normalised),
+//   rstd = 1 / sqrt(mean(h^2) + eps),   y = h rstd w;
+//   with n = h rstd and g = dy w:   dh_total = rstd (g - n mean(g n)) + dh,   dw = sum_rows dy n.
+// fp32 arithmetic for bf16 and fp32 rows.  Bound by memory: up to four row
+// elements move per value.
+#include <algorithm>
+
+#include <cuda_fp8.h>
+
+#include "launch.h"
+#include "rows.cuh"
+
+namespace ret {
+
+namespace {
+
+constexpr float kE4m3Max = 448.f;
+
+// Sum (or maximum) over the tpr threads of a row: a power of two up to 32
+// lanes, or all of the CTA's threads (several warps), through red.
+template <bool kMax>
+__device__ __forceinline__ float row_join(float x, float *red, int tpr) {
+  auto join = [](float p, float q) { return kMax ? fmaxf(p, q) : p + q; };
+  for (int s = min(tpr, 32) >> 1; s > 0; s >>= 1) x = join(x, __shfl_xor_sync(0xffffffffu, x, s));
+  if (tpr <= 32) return x;
+  const int lane = threadIdx.x & 31, nw = tpr >> 5;
+  if (lane == 0) red[threadIdx.x >> 5] = x;
+  __syncthreads();
+  x = lane < nw ? red[lane] : 0.f;  // (maxima here are never negative)
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) x = join(x, __shfl_xor_sync(0xffffffffu, x, s));
+  return x;
+}
+
+template <int V>
+__device__ __forceinline__ void load_gain(const float *w, int c, float (&f)[V]) {
+  if (!w) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] = 1.f;
+  } else if constexpr (V == 1) {
+    f[0] = w[c];
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; j += 4) {
+      const float4 v = *reinterpret_cast<const float4 *>(w + c + j);
+      f[j] = v.x; f[j + 1] = v.y; f[j + 2] = v.z; f[j + 3] = v.w;
+    }
+  }
+}
+
+// e4m3 values of V floats (rounded to nearest, beyond +-448 that).
+template <int V>
+__device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&f)[V]) {
+  if constexpr (V == 1) {
+    *p = __nv_cvt_float_to_fp8(f[0], __NV_SATFINITE, __NV_E4M3);
+  } else {
+    uint32_t w[V / 4];
+#pragma unroll
+    for (int j = 0; j < V; j += 4) {
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[j], f[j + 1]), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[j + 2], f[j + 3]), __NV_SATFINITE, __NV_E4M3);
+      w[j / 4] = lo | hi << 16;
+    }
+    if constexpr (V == 4)
+      *reinterpret_cast<uint32_t *>(p) = w[0];
+    else
+      *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+  }
+}
+
+// Rounds to the rows' type, as what is kept of the sum is.
+template <typename T, int V>
+__device__ __forceinline__ void add_rounded(const Elems<T, V> &a, const Elems<T, V> &b, Elems<T, V> &h) {
+  float f[V], g[V];
+  a.get(f);
+  b.get(g);
+#pragma unroll
+  for (int j = 0; j < V; ++j) f[j] += g[j];
+  h.set(f);
+}
+
+// tpr threads a row, NV vectors of V values a thread, interleaved; the row
+// stays in registers.  kQuant: e4m3 output.
+template <typename T, int V, int NV, bool kQuant>
+__global__ void __launch_bounds__(512)
+rms_fwd_kernel(const RmsArgs a, int tpr) {
+  extern __shared__ unsigned amax[];  // [rows of the CTA][groups]
+  __shared__ float red[2][32];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int row_in = threadIdx.x / tpr, t = threadIdx.x - row_in * tpr, per = blockDim.x / tpr;
+  const float inv_d = 1.f / (float)a.d;
+  for (long long r0 = (long long)blockIdx.x * per; r0 < a.rows; r0 += (long long)gridDim.x * per) {
+    const long long r = r0 + row_in;
+    const bool live = r < a.rows;
+    Elems<T, V> h[NV];
+    float s = 0.f;
+    if (kQuant) {
+      for (int i = threadIdx.x; i < per * a.groups; i += blockDim.x) amax[i] = 0u;
+    }
+    if (live) {
+      const T *x = reinterpret_cast<const T *>(a.x) + row_offset(a.sx, r);
+      const T *q = a.r ? reinterpret_cast<const T *>(a.r) + row_offset(a.sr, r) : nullptr;
+      T *ho = a.r ? reinterpret_cast<T *>(a.h) + row_offset(a.sh, r) : nullptr;
+      Elems<T, V> rv[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * tpr + t) * V;
+        if (c < a.d) {
+          h[i].load(x + c);
+          if (q) rv[i].load(q + c);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * tpr + t) * V;
+        if (c < a.d) {
+          if (q) {
+            add_rounded<T, V>(h[i], rv[i], h[i]);
+            h[i].store(ho + c);
+          }
+          float f[V];
+          h[i].get(f);
+#pragma unroll
+          for (int j = 0; j < V; ++j) s = fmaf(f[j], f[j], s);
+        }
+      }
+    }
+    s = row_join<false>(s, red[0], tpr);
+    const float rstd = rsqrtf(fmaf(s, inv_d, a.eps));
+    if (live && t == 0 && a.rstd) a.rstd[r] = rstd;
+    if (!kQuant) {
+      if (live) {
+        T *y = reinterpret_cast<T *>(a.out) + row_offset(a.so, r);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int c = (i * tpr + t) * V;
+          if (c < a.d) {
+            float f[V], w[V];
+            h[i].get(f);
+            load_gain<V>(a.w, c, w);
+#pragma unroll
+            for (int j = 0; j < V; ++j) f[j] = f[j] * rstd * w[j];
+            h[i].set(f);
+            h[i].store(y + c);
+          }
+        }
+      }
+      if (tpr > 32) __syncthreads();  // red is free again
+    } else {
+      if (tpr <= 32) __syncthreads();  // the maxima are cleared (wider rows met in the sum)
+      unsigned *top = amax + row_in * a.groups;
+      float f[NV][V];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * tpr + t) * V;
+        if (live && c < a.d) {
+          float w[V], m = 0.f;
+          h[i].get(f[i]);
+          load_gain<V>(a.w, c, w);
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            f[i][j] = f[i][j] * rstd * w[j];
+            m = fmaxf(m, fabsf(f[i][j]));
+          }
+          // (a maximum does not depend on the order of its atomics)
+          atomicMax(top + c / a.group, __float_as_uint(m));
+        }
+      }
+      __syncthreads();
+      if (live) {
+        uint8_t *y = reinterpret_cast<uint8_t *>(a.out) + row_offset(a.so, r);
+        for (int i = t; i < a.groups; i += tpr) a.scales[r * a.groups + i] = __uint_as_float(top[i]) / kE4m3Max;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int c = (i * tpr + t) * V;
+          if (c < a.d) {
+            const float scale = __uint_as_float(top[c / a.group]) / kE4m3Max;
+#pragma unroll
+            for (int j = 0; j < V; ++j) f[i][j] = scale > 0.f ? f[i][j] / scale : f[i][j];
+            store_e4m3<V>(y + c, f[i]);
+          }
+        }
+      }
+      __syncthreads();  // red and the maxima are free again
+    }
+  }
+}
+
+// Rows too long for registers: read again for the output (the kept sum, or x).
+template <typename T, int V, bool kQuant>
+__global__ void __launch_bounds__(1024)
+rms_fwd_long_kernel(const RmsArgs a) {
+  __shared__ float red[2][32];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int step = blockDim.x * V, first = threadIdx.x * V;
+  for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
+    const T *x = reinterpret_cast<const T *>(a.x) + row_offset(a.sx, r);
+    const T *q = a.r ? reinterpret_cast<const T *>(a.r) + row_offset(a.sr, r) : nullptr;
+    T *ho = a.r ? reinterpret_cast<T *>(a.h) + row_offset(a.sh, r) : nullptr;
+    float s = 0.f, f[V], w[V];
+    Elems<T, V> e, o;
+    for (int c = first; c < a.d; c += step) {
+      e.load(x + c);
+      if (q) {
+        o.load(q + c);
+        add_rounded<T, V>(e, o, e);
+        e.store(ho + c);
+      }
+      e.get(f);
+#pragma unroll
+      for (int j = 0; j < V; ++j) s = fmaf(f[j], f[j], s);
+    }
+    s = row_join<false>(s, red[0], blockDim.x);
+    const float rstd = rsqrtf(s / (float)a.d + a.eps);
+    if (threadIdx.x == 0 && a.rstd) a.rstd[r] = rstd;
+    const T *from = q ? ho : x;  // (each thread reads what it wrote itself)
+    if (!kQuant) {
+      T *y = reinterpret_cast<T *>(a.out) + row_offset(a.so, r);
+      for (int c = first; c < a.d; c += step) {
+        e.load(from + c);
+        e.get(f);
+        load_gain<V>(a.w, c, w);
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[j] = f[j] * rstd * w[j];
+        e.set(f);
+        e.store(y + c);
+      }
+    } else {
+      uint8_t *y = reinterpret_cast<uint8_t *>(a.out) + row_offset(a.so, r);
+      // a warp for each group, or all of them for wide ones (what others kept
+      // of the sum is visible since they met above)
+      const bool wide = a.group > 1024;
+      const int lead = (wide ? threadIdx.x : threadIdx.x & 31) * V, hop = (wide ? blockDim.x : 32) * V;
+      for (int g = wide ? 0 : threadIdx.x >> 5; g < a.groups; g += wide ? 1 : blockDim.x >> 5) {
+        const int c1 = min(a.d, (g + 1) * a.group);
+        float m = 0.f;
+        for (int c = g * a.group + lead; c < c1; c += hop) {
+          e.load(from + c);
+          e.get(f);
+          load_gain<V>(a.w, c, w);
+#pragma unroll
+          for (int j = 0; j < V; ++j) m = fmaxf(m, fabsf(f[j] * rstd * w[j]));
+        }
+        m = row_join<true>(m, red[1], wide ? blockDim.x : 32);
+        const float scale = m / kE4m3Max;
+        if (lead == 0) a.scales[r * a.groups + g] = scale;
+        for (int c = g * a.group + lead; c < c1; c += hop) {
+          e.load(from + c);
+          e.get(f);
+          load_gain<V>(a.w, c, w);
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            f[j] = f[j] * rstd * w[j];
+            if (scale > 0.f) f[j] /= scale;
+          }
+          store_e4m3<V>(y + c, f);
+        }
+        if (wide) __syncthreads();  // red is free again
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// dx of the rows of the CTA, and its sums of dy n: a thread keeps those of its
+// own columns in registers.
+template <typename T, int V, int NV>
+__global__ void __launch_bounds__(512)
+rms_bwd_kernel(const RmsArgs a, int tpr, float *__restrict__ part) {
+  extern __shared__ float sums[];  // [rows of the CTA][d] where there are several
+  __shared__ float red[2][32];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int row_in = threadIdx.x / tpr, t = threadIdx.x - row_in * tpr, per = blockDim.x / tpr;
+  const float inv_d = 1.f / (float)a.d;
+  float dw[NV][V];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < V; ++j) dw[i][j] = 0.f;
+  int par = 0;
+  for (long long r0 = (long long)blockIdx.x * per; r0 < a.rows; r0 += (long long)gridDim.x * per, par ^= 1) {
+    const long long r = r0 + row_in;
+    const bool live = r < a.rows;
+    Elems<T, V> h[NV], g[NV], p[NV];
+    float s = 0.f, rstd = 0.f;
+    if (live) {
+      const T *x = reinterpret_cast<const T *>(a.x) + row_offset(a.sx, r);
+      const T *dy = reinterpret_cast<const T *>(a.dy) + row_offset(a.sg, r);
+      const T *dh = a.dh ? reinterpret_cast<const T *>(a.dh) + row_offset(a.sdh, r) : nullptr;
+      rstd = a.rstd[r];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * tpr + t) * V;
+        if (c < a.d) {
+          h[i].load(x + c);
+          g[i].load(dy + c);
+          if (dh) p[i].load(dh + c);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * tpr + t) * V;
+        if (c < a.d) {
+          float f[V], q[V], w[V];
+          h[i].get(f);
+          g[i].get(q);
+          load_gain<V>(a.w, c, w);
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            const float n = f[j] * rstd;
+            dw[i][j] = fmaf(q[j], n, dw[i][j]);
+            s = fmaf(q[j] * w[j], n, s);
+          }
+        }
+      }
+    }
+    s = row_join<false>(s, red[par], tpr);
+    const float k = -s * inv_d;
+    if (live) {
+      T *dx = reinterpret_cast<T *>(a.out) + row_offset(a.so, r);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * tpr + t) * V;
+        if (c < a.d) {
+          float f[V], q[V], w[V], o[V];
+          h[i].get(f);
+          g[i].get(q);
+          load_gain<V>(a.w, c, w);
+          if (a.dh) p[i].get(o);
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            const float v = fmaf(f[j] * rstd, k, q[j] * w[j]);
+            o[j] = a.dh ? fmaf(v, rstd, o[j]) : v * rstd;
+          }
+          h[i].set(o);
+          h[i].store(dx + c);
+        }
+      }
+    }
+  }
+  if (!part) return;
+  float *out = part + (size_t)blockIdx.x * a.d;
+  float *mine = per > 1 ? sums + (size_t)row_in * a.d : out;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * tpr + t) * V;
+    if (c < a.d)
+#pragma unroll
+      for (int j = 0; j < V; ++j) mine[c + j] = dw[i][j];
+  }
+  if (per == 1) return;
+  __syncthreads();
+  for (int c = threadIdx.x; c < a.d; c += blockDim.x) {
+    float v = sums[c];
+    for (int i = 1; i < per; ++i) v += sums[(size_t)i * a.d + c];
+    out[c] = v;
+  }
+}
+
+// Rows too long for registers, in two passes: mean(g n) of each row, then dx
+// and the column sums by blocks of columns.
+template <typename T, int V>
+__global__ void __launch_bounds__(1024)
+rms_bwd_stat_kernel(const RmsArgs a, float *__restrict__ stat) {
+  __shared__ float red[32];
+  pdl_launch_dependents();
+  pdl_wait();
+  for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
+    const T *x = reinterpret_cast<const T *>(a.x) + row_offset(a.sx, r);
+    const T *dy = reinterpret_cast<const T *>(a.dy) + row_offset(a.sg, r);
+    const float rstd = a.rstd[r];
+    float s = 0.f;
+    for (int c = threadIdx.x * V; c < a.d; c += blockDim.x * V) {
+      Elems<T, V> h, g;
+      h.load(x + c);
+      g.load(dy + c);
+      float f[V], q[V], w[V];
+      h.get(f);
+      g.get(q);
+      load_gain<V>(a.w, c, w);
+#pragma unroll
+      for (int j = 0; j < V; ++j) s = fmaf(q[j] * w[j], f[j] * rstd, s);
+    }
+    s = row_join<false>(s, red, blockDim.x);
+    if (threadIdx.x == 0) stat[r] = s / (float)a.d;
+    __syncthreads();
+  }
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(256)
+rms_bwd_cols_kernel(const RmsArgs a, const float *__restrict__ stat, float *__restrict__ part) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int c = (blockIdx.x * blockDim.x + threadIdx.x) * V;
+  if (c >= a.d) return;
+  float dw[V], w[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) dw[j] = 0.f;
+  load_gain<V>(a.w, c, w);
+  for (long long r = blockIdx.y; r < a.rows; r += gridDim.y) {
+    const float rstd = a.rstd[r], k = -stat[r];
+    Elems<T, V> h, g, p;
+    h.load(reinterpret_cast<const T *>(a.x) + row_offset(a.sx, r) + c);
+    g.load(reinterpret_cast<const T *>(a.dy) + row_offset(a.sg, r) + c);
+    if (a.dh) p.load(reinterpret_cast<const T *>(a.dh) + row_offset(a.sdh, r) + c);
+    float f[V], q[V], o[V];
+    h.get(f);
+    g.get(q);
+    if (a.dh) p.get(o);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float n = f[j] * rstd, v = fmaf(n, k, q[j] * w[j]);
+      dw[j] = fmaf(q[j], n, dw[j]);
+      o[j] = a.dh ? fmaf(v, rstd, o[j]) : v * rstd;
+    }
+    h.set(o);
+    h.store(reinterpret_cast<T *>(a.out) + row_offset(a.so, r) + c);
+  }
+  if (!part) return;
+#pragma unroll
+  for (int j = 0; j < V; ++j) part[(size_t)blockIdx.y * a.d + c + j] = dw[j];
+}
+
+// 16-byte vectors need every row of every operand on a 16-byte boundary.
+bool rows_on(const void *p, const RowSet &s, int esz, int bytes) {
+  return reinterpret_cast<uintptr_t>(p) % bytes == 0 && (s.n1 == 1 || s.s1 * esz % bytes == 0) &&
+         (s.n0 == 1 || s.s0 * esz % bytes == 0);
+}
+
+// Threads a row for n vectors, NV a thread: lanes of a warp (a power of two) or whole warps.
+int threads_per_row(int n, int most) {
+  const int t = (n + most - 1) / most;
+  if (t > 16) return (t + 31) / 32 * 32;
+  int p = 1;
+  while (p < t) p *= 2;
+  return p;
+}
+
+template <typename T, int V, bool kQuant>
+cudaError_t fwd_any(const RmsArgs &a, cudaStream_t st) {
+  const int n = (a.d + V - 1) / V, sms = device_sms();
+  // At most 512 threads a row: 8, 16 or 32 values a thread.
+  auto go = [&](auto nv) {
+    constexpr int NV = decltype(nv)::value;
+    const int tpr = threads_per_row(n, NV), threads = tpr > 32 ? tpr : 128, per = threads / tpr;
+    const long long want = (a.rows + per - 1) / per, most = (long long)sms * (2048 / threads) * 4;
+    const size_t smem = kQuant ? (size_t)per * a.groups * 4 : 0;
+    return launch_k(rms_fwd_kernel<T, V, NV, kQuant>, dim3((unsigned)std::min(want, most)), dim3(threads), smem, st, true, a, tpr);
+  };
+  if (a.d <= 512 * 8) return go(std::integral_constant<int, 8 / V>());
+  if (a.d <= 512 * 16) return go(std::integral_constant<int, 16 / V>());
+  if (a.d <= 512 * 32) return go(std::integral_constant<int, 32 / V>());
+  const long long cap = 1LL << 30;
+  return launch_k(rms_fwd_long_kernel<T, V, kQuant>, dim3((unsigned)std::min(a.rows, cap)), dim3(1024), 0, st, true, a);
+}
+
+template <bool kQuant>
+cudaError_t launch_fwd(const RmsArgs &a, int bf16, cudaStream_t st) {
+  if (a.rows == 0) return cudaSuccess;
+  const int esz = bf16 ? 2 : 4, vec = 16 / esz;
+  const bool v = a.d % vec == 0 && rows_on(a.x, a.sx, esz, 16) && (!a.r || (rows_on(a.r, a.sr, esz, 16) && rows_on(a.h, a.sh, esz, 16))) &&
+                 rows_on(a.out, a.so, kQuant ? 1 : esz, kQuant ? vec : 16) && reinterpret_cast<uintptr_t>(a.w) % 16 == 0;
+  if (bf16) return v ? fwd_any<__nv_bfloat16, 8, kQuant>(a, st) : fwd_any<__nv_bfloat16, 1, kQuant>(a, st);
+  return v ? fwd_any<float, 4, kQuant>(a, st) : fwd_any<float, 1, kQuant>(a, st);
+}
+
+constexpr int kTwoPassGroups = 64;
+
+template <typename T, int V>
+cudaError_t bwd_any(const RmsArgs &a, const RmsBwdPlan &pl, const float *stat, float *part, cudaStream_t st) {
+  if (pl.two_pass) {
+    const int cols = 256 * V;
+    return launch_k(rms_bwd_cols_kernel<T, V>, dim3((a.d + cols - 1) / cols, pl.groups), dim3(256), 0, st, true, a, stat, part);
+  }
+  const int threads = pl.tpr > 32 ? pl.tpr : 128, per = threads / pl.tpr;
+  const size_t smem = per > 1 ? (size_t)per * a.d * sizeof(float) : 0;
+  if constexpr (V == 8)
+    if (pl.values == 32)
+      return launch_k(rms_bwd_kernel<T, V, 32 / V>, dim3(pl.groups), dim3(threads), smem, st, true, a, pl.tpr, part);
+  if (pl.values == 16)
+    return launch_k(rms_bwd_kernel<T, V, 16 / V>, dim3(pl.groups), dim3(threads), smem, st, true, a, pl.tpr, part);
+  return launch_k(rms_bwd_kernel<T, V, 8 / V>, dim3(pl.groups), dim3(threads), smem, st, true, a, pl.tpr, part);
+}
+
+template <typename T, int V>
+cudaError_t stat_any(const RmsArgs &a, float *stat, cudaStream_t st) {
+  const long long cap = 1LL << 30;
+  return launch_k(rms_bwd_stat_kernel<T, V>, dim3((unsigned)std::min(a.rows, cap)), dim3(1024), 0, st, true, a, stat);
+}
+
+}  // namespace
+
+cudaError_t launch_rmsnorm_fwd(const RmsArgs &a, int bf16, cudaStream_t st) { return launch_fwd<false>(a, bf16, st); }
+cudaError_t launch_rmsnorm_quant(const RmsArgs &a, int bf16, cudaStream_t st) { return launch_fwd<true>(a, bf16, st); }
+
+RmsBwdPlan rmsnorm_bwd_plan(const RmsArgs &a, int bf16) {
+  RmsBwdPlan pl;
+  const int esz = bf16 ? 2 : 4, vec = 16 / esz;
+  pl.vec = a.d % vec == 0 && rows_on(a.x, a.sx, esz, 16) && rows_on(a.dy, a.sg, esz, 16) &&
+           (!a.dh || rows_on(a.dh, a.sdh, esz, 16)) && rows_on(a.out, a.so, esz, 16) && reinterpret_cast<uintptr_t>(a.w) % 16 == 0;
+  const int V = pl.vec ? vec : 1, n = (a.d + V - 1) / V;
+  // At most 512 threads a row with 8 or 16 values each, for 16-byte vectors of
+  // bf16 (whose rows take half the registers) 32.
+  pl.values = a.d <= 512 * 8 ? 8 : a.d <= 512 * 16 ? 16 : 32;
+  if (a.d > 512 * (V == 8 ? 32 : 16)) {
+    pl.two_pass = true;
+    pl.groups = (int)std::min<long long>(a.rows, kTwoPassGroups);
+    return pl;
+  }
+  pl.tpr = threads_per_row(n, pl.values / V);
+  const int threads = pl.tpr > 32 ? pl.tpr : 128, per = threads / pl.tpr;
+  const long long want = (a.rows + per - 1) / per, most = (long long)device_sms() * std::min(8, std::max(1, 1024 / threads));
+  pl.groups = (int)std::min(want, most);
+  return pl;
+}
+
+size_t rmsnorm_bwd_bytes(long long rows, int d) {
+  const long long most = std::max<long long>((long long)device_sms() * 8, kTwoPassGroups);
+  return ((size_t)std::min(rows, most) * d + (size_t)rows) * sizeof(float);
+}
+
+cudaError_t launch_rmsnorm_bwd_stat(const RmsArgs &a, int bf16, const RmsBwdPlan &pl, float *stat, cudaStream_t st) {
+  if (bf16) return pl.vec ? stat_any<__nv_bfloat16, 8>(a, stat, st) : stat_any<__nv_bfloat16, 1>(a, stat, st);
+  return pl.vec ? stat_any<float, 4>(a, stat, st) : stat_any<float, 1>(a, stat, st);
+}
+
+cudaError_t launch_rmsnorm_bwd(const RmsArgs &a, int bf16, const RmsBwdPlan &pl, const float *stat, float *part,
+                               cudaStream_t st) {
+  if (bf16) return pl.vec ? bwd_any<__nv_bfloat16, 8>(a, pl, stat, part, st) : bwd_any<__nv_bfloat16, 1>(a, pl, stat, part, st);
+  return pl.vec ? bwd_any<float, 4>(a, pl, stat, part, st) : bwd_any<float, 1>(a, pl, stat, part, st);
+}
+
+}  // namespace ret

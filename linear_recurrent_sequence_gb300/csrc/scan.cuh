@@ -1,0 +1,120 @@
+// Building blocks of the selective scan kernels: step sizes, gates, sums over
+// the lanes that share a channel, rows of a state.
+#pragma once
+
+#include "common.cuh"
+#include "launch.h"
+#include "rows.cuh"
+#include "tc.cuh"
+
+namespace ret {
+namespace scan {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 1 / x by the hardware's approximation (2^-23 of itself).
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 1 / (1 + e^-x); 0 and 1 at the ends (the exponential of a very negative x is
+// infinite, and its reciprocal 0).
+__device__ __forceinline__ float sigmoid(float x) { return rcp(1.f + ex2(-kLog2e * x)); }
+__device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
+
+// ln(1 + e^x) = max(x, 0) + ln(1 + e), e = e^-|x| in (0, 1], where
+// ln(1 + e) = 2 artanh(s), s = e / (2 + e) <= 1/3, by its series in s^2 up to
+// s^15 (the next term is below 2^-27 of the sum).  A difference quotient of
+// ln(1 + e) would lose the small e of small step sizes.
+__device__ __forceinline__ float softplus(float x) {
+  const float e = ex2(-kLog2e * fabsf(x));
+  const float s = e * rcp(2.f + e), q = s * s;
+  float p = 2.f / 15.f;
+  p = fmaf(p, q, 2.f / 13.f);
+  p = fmaf(p, q, 2.f / 11.f);
+  p = fmaf(p, q, 2.f / 9.f);
+  p = fmaf(p, q, 2.f / 7.f);
+  p = fmaf(p, q, 2.f / 5.f);
+  p = fmaf(p, q, 2.f / 3.f);
+  p = fmaf(p, q, 2.f);
+  const float l = fmaf(p, s, fmaxf(x, 0.f));
+  return x != x ? x : l;  // (a maximum drops a NaN)
+}
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+template <typename T>
+__device__ __forceinline__ float to_float(T x);
+template <>
+__device__ __forceinline__ float to_float<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ float to_float<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+template <typename T>
+__device__ __forceinline__ T from_float(float x);
+template <>
+__device__ __forceinline__ float from_float<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// Sums of each of N values over groups of L neighbouring lanes times `kStep`
+// (L, N powers of two); the lanes share them out: with lane index i in its
+// group, v[j] of the result is the sum of value (i % min(L, N)) * N / min(L, N) + j
+// for j < N / min(L, N).  Each step halves the values a lane still has to send.
+template <int N, int L, int kStep = 1>
+__device__ __forceinline__ void share_sums(float (&v)[N]) {
+  const int lane = threadIdx.x & 31;
+  constexpr int M = L < N ? L : N;
+  int n = N;
+#pragma unroll
+  for (int d = M / 2; d >= 1; d >>= 1) {
+    const bool up = (lane & (d * kStep)) != 0;
+    n >>= 1;
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j)
+      if (j < n) {
+        const float keep = up ? v[n + j] : v[j], send = up ? v[j] : v[n + j];
+        v[j] = keep + __shfl_xor_sync(0xffffffffu, send, d * kStep);
+      }
+  }
+#pragma unroll
+  for (int d = M; d < L; d <<= 1)
+#pragma unroll
+    for (int j = 0; j < N / M; ++j) v[j] += __shfl_xor_sync(0xffffffffu, v[j], d * kStep);
+}
+
+// Four states s0 .. s0 + 3 of a row of S (the missing ones 0).  kVec: the row
+// begins on a 16-byte boundary and S is a multiple of 4.
+__device__ __forceinline__ float4 load_states(const float *row, int s0, int S, bool vec) {
+  if (vec) return s0 < S ? *reinterpret_cast<const float4 *>(row + s0) : make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 v;
+  v.x = s0 < S ? row[s0] : 0.f;
+  v.y = s0 + 1 < S ? row[s0 + 1] : 0.f;
+  v.z = s0 + 2 < S ? row[s0 + 2] : 0.f;
+  v.w = s0 + 3 < S ? row[s0 + 3] : 0.f;
+  return v;
+}
+
+__device__ __forceinline__ void store_states(float *row, int s0, int S, bool vec, float4 v) {
+  if (vec) {
+    if (s0 < S) *reinterpret_cast<float4 *>(row + s0) = v;
+    return;
+  }
+  if (s0 < S) row[s0] = v.x;
+  if (s0 + 1 < S) row[s0 + 1] = v.y;
+  if (s0 + 2 < S) row[s0 + 2] = v.z;
+  if (s0 + 3 < S) row[s0 + 3] = v.w;
+}
+
+// Tokens of sequence b: its length within [0, N].
+__device__ __forceinline__ int tokens_of(const ScanArgs &a, int b) {
+  if (!a.lengths) return a.N;
+  const long long n = a.len64 ? reinterpret_cast<const long long *>(a.lengths)[b]
+                              : (long long)reinterpret_cast<const int *>(a.lengths)[b];
+  return (int)(n < 0 ? 0 : n > a.N ? a.N : n);
+}
+
+}  // namespace scan
+}  // namespace ret

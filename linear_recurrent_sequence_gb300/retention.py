@@ -7,6 +7,7 @@ fallback implementation.
 """
 from __future__ import annotations
 
+import collections
 import contextlib
 import ctypes
 import functools
@@ -25,6 +26,7 @@ STATUS = {0: "RET_OK", 1: "RET_EINVAL", 2: "RET_EUNSUPPORTED", 3: "RET_EWORKSPAC
 MAX_HEADS = 256
 
 MAX_TOP = 128
+MAX_STATES = 64
 
 _I64x2 = ctypes.c_int64 * 2
 _I64x3 = ctypes.c_int64 * 3
@@ -68,6 +70,27 @@ class LogitsDesc(ctypes.Structure):
                 ("dtype", ctypes.c_int), ("temperature", ctypes.c_double), ("top", ctypes.c_int),
                 ("id_bytes", ctypes.c_int), ("tail", ctypes.c_int),
                 ("sx", _I64x2), ("sd", _I64x2)]
+
+
+class ScanDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("N", ctypes.c_int), ("E", ctypes.c_int),
+                ("S", ctypes.c_int), ("G", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("softplus", ctypes.c_int), ("len_bytes", ctypes.c_int),
+                ("sx", _I64x2), ("sdt", _I64x2), ("sz", _I64x2), ("sy", _I64x2),
+                ("sdy", _I64x2), ("sdx", _I64x2), ("sddt", _I64x2), ("sdz", _I64x2),
+                ("sB", _I64x3), ("sC", _I64x3)]
+
+
+class ConvDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("N", ctypes.c_int), ("E", ctypes.c_int),
+                ("W", ctypes.c_int), ("dtype", ctypes.c_int), ("silu", ctypes.c_int),
+                ("len_bytes", ctypes.c_int), ("sx", _I64x2), ("sg", _I64x2), ("so", _I64x2)]
+
+
+class RmsNormDesc(ctypes.Structure):
+    _fields_ = [("n0", ctypes.c_int64), ("n1", ctypes.c_int64), ("d", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("eps", ctypes.c_float), ("group", ctypes.c_int),
+                ("sx", _I64x2), ("sr", _I64x2), ("sh", _I64x2), ("sg", _I64x2), ("so", _I64x2)]
 
 
 LAYER_KEYS = ("ln1_w", "ln1_b", "WQ", "WK", "WV", "WG", "WO", "ln2_w", "ln2_b", "W1", "W2")
@@ -129,6 +152,22 @@ _SIGS = {
     "retnet_distill_fwd": (ctypes.c_int, [ctypes.POINTER(LogitsDesc)] + [_P] * 6),
     "retnet_distill_bwd": (ctypes.c_int, [ctypes.POINTER(LogitsDesc)] + [_P] * 7),
     "retnet_distill_step": (ctypes.c_int, [ctypes.POINTER(LogitsDesc)] + [_P] * 8),
+    "retnet_selective_scan_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(ScanDesc)]),
+    "retnet_selective_scan_fwd": (ctypes.c_int, [ctypes.POINTER(ScanDesc)] + [_P] * 13 +
+                                  [ctypes.c_size_t, _P]),
+    "retnet_selective_scan_step": (ctypes.c_int, [ctypes.POINTER(ScanDesc)] + [_P] * 12),
+    "retnet_selective_scan_bwd_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(ScanDesc)]),
+    "retnet_selective_scan_bwd": (ctypes.c_int, [ctypes.POINTER(ScanDesc)] + [_P] * 22 +
+                                  [ctypes.c_size_t, _P]),
+    "retnet_causal_conv_fwd": (ctypes.c_int, [ctypes.POINTER(ConvDesc)] + [_P] * 8),
+    "retnet_causal_conv_bwd_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(ConvDesc)]),
+    "retnet_causal_conv_bwd": (ctypes.c_int, [ctypes.POINTER(ConvDesc)] + [_P] * 12 +
+                               [ctypes.c_size_t, _P]),
+    "retnet_rmsnorm_fwd": (ctypes.c_int, [ctypes.POINTER(RmsNormDesc)] + [_P] * 7),
+    "retnet_rmsnorm_quant": (ctypes.c_int, [ctypes.POINTER(RmsNormDesc)] + [_P] * 7),
+    "retnet_rmsnorm_bwd_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(RmsNormDesc)]),
+    "retnet_rmsnorm_bwd": (ctypes.c_int, [ctypes.POINTER(RmsNormDesc)] + [_P] * 8 +
+                           [ctypes.c_size_t, _P]),
     "retention_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "retention_last_cuda_error": (ctypes.c_int, []),
     "retention_poll_status": (ctypes.c_int, [_P, _P]),
@@ -816,6 +855,359 @@ def distill_step(student, ids, values, weight=None, *, temperature=1.0, tail=Fal
                                  _stream(stream))
     _check(st, "retnet_distill_step")
     return loss, dstudent
+
+
+def _seq_strides(name, t, lead, E):
+    """(batch, token) element strides of a [B, N, E] or [B, E] tensor."""
+    s = t.stride()
+    if s[-1] != 1 and E > 1:
+        raise ValueError(f"{name}: the channels must be contiguous")
+    return (s[0], s[1] if lead == 2 else 0)
+
+
+def _seq_like(name, t, x):
+    """Checks a tensor for x's shape and dtype and gives its strides (None: x's)."""
+    if t is None:
+        return (0, 0)
+    _like(name, t, x)
+    return _seq_strides(name, t, x.dim() - 1, x.shape[-1])
+
+
+def _lengths(lengths, B):
+    """Bytes of a length (8 without lengths)."""
+    if lengths is None:
+        return 8
+    return _ids("lengths", lengths, (B,))
+
+
+# As the descriptors above: found by shapes, strides and options alone.  The
+# workspaces depend on the device's SMs too.
+@functools.lru_cache(maxsize=256)
+def _scan_desc(shape, S, G, dtype, softplus, len_bytes, strides, sB, sC, device):
+    """(descriptor, workspace bytes of the forward and of the backward)."""
+    B, N, E = shape
+    d = ScanDesc(B, N, E, S, G, _dtype_code(dtype), softplus, len_bytes, *strides, sB, sC)
+    return (d, int(lib.retnet_selective_scan_workspace_size(ctypes.byref(d))),
+            int(lib.retnet_selective_scan_bwd_workspace_size(ctypes.byref(d))))
+
+
+def _scan_call(x, dt, A, B, C, D, z, dt_bias, softplus, lengths, step=False, **like):
+    """The descriptor of a scan, after checks of its tensors; like: the strides'
+    names of more tensors of x's shape."""
+    lead = 1 if step else 2
+    if x.dim() != lead + 1:
+        raise ValueError(f"x must be {'[B, E]' if step else '[B, N, E]'}, got {tuple(x.shape)}")
+    rows, E = tuple(x.shape[:-1]), x.shape[-1]
+    if A.dim() != 2:
+        raise ValueError(f"A must be [E, S], got {tuple(A.shape)}")
+    S = A.shape[1]
+    _f32("A", A, (E, S))
+    _f32("D", D, (E,))
+    _f32("dt_bias", dt_bias, (E,))
+    strides = dict(sx=_seq_strides("x", x, lead, E), sdt=_seq_like("dt", dt, x), sz=_seq_like("z", z, x))
+    strides.update({k: _seq_like(k[1:], t, x) for k, t in like.items()})
+    groups = []
+    for name, t in (("B", B), ("C", C)):
+        if t.dim() == lead + 1:
+            t = t.unsqueeze(lead)
+        if t.dim() != lead + 2 or tuple(t.shape[:lead]) != rows or t.shape[-1] != S or t.dtype != x.dtype:
+            raise ValueError(f"{name} must have the shape {rows + ('groups', S)} and dtype {x.dtype}")
+        s = t.stride()
+        if s[-1] != 1 and S > 1:
+            raise ValueError(f"{name}: the states must be contiguous")
+        groups.append((t.shape[lead], (s[0], s[1] if lead == 2 else 0, s[lead])))
+    (G, sB), (GC, sC) = groups
+    if GC != G or G < 1 or E % G:
+        raise ValueError(f"B and C must have equal groups that divide the {E} channels")
+    order = ("sx", "sdt", "sz", "sy", "sdy", "sdx", "sddt", "sdz")
+    shape = (rows[0], 1 if step else rows[1], E)
+    return _scan_desc(shape, S, G, x.dtype, bool(softplus), _lengths(lengths, rows[0]),
+                      tuple(strides.get(k, (0, 0)) for k in order), sB, sC, x.device)
+
+
+def selective_scan_fwd(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, softplus=True, h_in=None,
+                       lengths=None, out=None, h_out=None, workspace=None, stream=None):
+    """Selective state space scan of x, dt [B, N, E] (bf16 or fp32, any batch and
+    token strides) with A [E, S] fp32 (S <= MAX_STATES) and B, C [B, N, G, S] (or
+    [B, N, S]): with delta = softplus(dt + dt_bias),
+        h_t = exp(delta_t A) h_(t-1) + delta_t x_t B_t,
+        y_t = (C_t . h_t + D x_t) silu(z_t).
+    D, dt_bias fp32 [E]; z like x; h_in fp32 [B, E, S] (None: 0); lengths int32
+    or int64 [B] on the device: tokens of each sequence of a padded batch, rows
+    of y behind them are zeros.  Returns (y, the states after the last tokens)."""
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    desc, nbytes, _ = _scan_call(x, dt, A, B, C, D, z, dt_bias, softplus, lengths, sy=out)
+    states = (x.shape[0], x.shape[2], A.shape[1])
+    if h_out is None:
+        h_out = torch.empty(states, dtype=torch.float32, device=x.device)
+    _f32("h_in", h_in, states)
+    _f32("h_out", h_out, states)
+    if workspace is None and nbytes:
+        with _on(stream):
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    st = lib.retnet_selective_scan_fwd(
+        ctypes.byref(desc), *_ptrs(x, dt, A, B, C, D, z, dt_bias, h_in, lengths, out, h_out, workspace),
+        0 if workspace is None else workspace.numel(), _stream(stream))
+    _check(st, "retnet_selective_scan_fwd")
+    return out, h_out
+
+
+def selective_scan_step(x, dt, A, B, C, h, *, D=None, z=None, dt_bias=None, softplus=True, h_out=None,
+                        out=None, stream=None):
+    """One token of selective_scan_fwd: x, dt, z [B, E], B, C [B, G, S] (or [B, S]);
+    the states h fp32 [B, E, S] are updated in place, or written to h_out.
+    Returns y [B, E]."""
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    desc, _, _ = _scan_call(x, dt, A, B, C, D, z, dt_bias, softplus, None, step=True, sy=out)
+    states = (*x.shape, A.shape[1])
+    _f32("h", h, states)
+    _f32("h_out", h_out, states)
+    st = lib.retnet_selective_scan_step(
+        ctypes.byref(desc), *_ptrs(x, dt, A, B, C, D, z, dt_bias, h, out, h if h_out is None else h_out),
+        _stream(stream))
+    _check(st, "retnet_selective_scan_step")
+    return out
+
+
+ScanGrads = collections.namedtuple("ScanGrads", "dx ddt dA dB dC dD dz ddt_bias dh_in")
+
+
+def selective_scan_bwd(x, dt, A, B, C, dy, *, D=None, z=None, dt_bias=None, softplus=True, h_in=None,
+                       dh_out=None, lengths=None, dx=None, ddt=None, dA=None, dB=None, dC=None, dD=None,
+                       dz=None, ddt_bias=None, dh_in=None, workspace=None, stream=None):
+    """Gradients of selective_scan_fwd from its inputs, dy (like x) and dh_out
+    (fp32, of the states after the last tokens, None: 0).  Returns a ScanGrads:
+    dx, ddt, dz like x, dB, dC like B (contiguous), dA, dD, ddt_bias, dh_in fp32;
+    None where the input was None.  All sums are added in a fixed order."""
+    dev = x.device
+
+    def new(given, like):
+        if given is None and like is not None:
+            given = torch.empty(like.shape, dtype=like.dtype, device=dev)
+        return given if like is not None else None
+
+    dx, ddt, dz = new(dx, x), new(ddt, dt), new(dz, z)
+    dA, dB, dC = new(dA, A), new(dB, B), new(dC, C)
+    dD, ddt_bias, dh_in = new(dD, D), new(ddt_bias, dt_bias), new(dh_in, h_in)
+    desc, _, nbytes = _scan_call(x, dt, A, B, C, D, z, dt_bias, softplus, lengths, sdy=dy, sdx=dx, sddt=ddt,
+                                 sdz=dz)
+    E, states = x.shape[2], (x.shape[0], x.shape[2], A.shape[1])
+    for name, t, shape in (("dA", dA, A.shape), ("dD", dD, (E,)), ("ddt_bias", ddt_bias, (E,)),
+                           ("h_in", h_in, states), ("dh_in", dh_in, states), ("dh_out", dh_out, states)):
+        _f32(name, t, shape)
+    for name, t, like in (("dB", dB, B), ("dC", dC, C)):
+        _like(name, t, like)
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    if workspace is None:
+        with _on(stream):
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    st = lib.retnet_selective_scan_bwd(
+        ctypes.byref(desc),
+        *_ptrs(x, dt, A, B, C, D, z, dt_bias, h_in, lengths, dy, dh_out, dx, ddt, dA, dB, dC, dD, dz,
+               ddt_bias, dh_in, workspace), workspace.numel(), _stream(stream))
+    _check(st, "retnet_selective_scan_bwd")
+    return ScanGrads(dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dh_in)
+
+
+@functools.lru_cache(maxsize=256)
+def _conv_desc(shape, W, dtype, silu, len_bytes, sx, sg, so, device):
+    """(descriptor, workspace bytes of the backward)."""
+    d = ConvDesc(*shape, W, _dtype_code(dtype), silu, len_bytes, sx, sg, so)
+    return d, int(lib.retnet_causal_conv_bwd_workspace_size(ctypes.byref(d)))
+
+
+def _conv_call(x, w, b, silu, lengths, states, dy=None, out=None, step=False):
+    """(descriptor, workspace bytes) of a convolution after checks of its
+    tensors; states: (name, tensor) of kept inputs and their gradients."""
+    lead = 1 if step else 2
+    if x.dim() != lead + 1:
+        raise ValueError(f"x must be {'[B, E]' if step else '[B, N, E]'}, got {tuple(x.shape)}")
+    B, E = x.shape[0], x.shape[-1]
+    if w.dim() != 2:
+        raise ValueError(f"w must be [E, taps], got {tuple(w.shape)}")
+    W = w.shape[1]
+    _f32("w", w, (E, W))
+    _f32("b", b, (E,))
+    for name, t in states:
+        if t is not None and (t.shape != (B, W - 1, E) or t.dtype != x.dtype or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous tensor of shape {(B, W - 1, E)} and dtype {x.dtype}")
+    shape = (B, 1 if step else x.shape[1], E)
+    return _conv_desc(shape, W, x.dtype, bool(silu), _lengths(lengths, B), _seq_strides("x", x, lead, E),
+                      _seq_like("dy", dy, x), _seq_like("out", out, x), x.device)
+
+
+def causal_conv_fwd(x, w, b=None, *, silu=True, state_in=None, lengths=None, out=None, state_out=None,
+                    stream=None):
+    """Causal convolution of each channel of x [B, N, E] (bf16 or fp32, any batch
+    and token strides) with w [E, taps] fp32 (2 to 4 taps, the last one the
+    token's own) and b fp32 [E], then silu.  state_in [B, taps - 1, E] in x's
+    dtype: the inputs before the first token, the oldest first (None: 0).
+    lengths as for selective_scan_fwd.  Returns (y, the last taps - 1 inputs of
+    each sequence); state_out may be state_in."""
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if state_out is None:
+        state_out = torch.empty((x.shape[0], w.shape[-1] - 1, x.shape[-1]), dtype=x.dtype, device=x.device)
+    desc, _ = _conv_call(x, w, b, silu, lengths, (("state_in", state_in), ("state_out", state_out)), out=out)
+    st = lib.retnet_causal_conv_fwd(ctypes.byref(desc),
+                                    *_ptrs(x, w, b, state_in, lengths, out, state_out), _stream(stream))
+    _check(st, "retnet_causal_conv_fwd")
+    return out, state_out
+
+
+def causal_conv_step(x, w, b, state, *, silu=True, state_out=None, out=None, stream=None):
+    """One token of causal_conv_fwd: x [B, E]; the state [B, taps - 1, E] is
+    updated in place, or written to state_out.  Returns y [B, E]."""
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if state_out is None:
+        state_out = state
+    desc, _ = _conv_call(x, w, b, silu, None, (("state", state), ("state_out", state_out)), out=out, step=True)
+    st = lib.retnet_causal_conv_fwd(ctypes.byref(desc), *_ptrs(x, w, b, state, None, out, state_out),
+                                    _stream(stream))
+    _check(st, "retnet_causal_conv_fwd")
+    return out
+
+
+def causal_conv_bwd(x, w, b, dy, *, silu=True, state_in=None, dstate_out=None, lengths=None, dx=None,
+                    dw=None, db=None, dstate_in=None, workspace=None, stream=None):
+    """Gradients of causal_conv_fwd from its inputs, dy (like x) and dstate_out
+    (of the state after the last token, None: 0).  Returns (dx, dw, db,
+    dstate_in); db is None without b, dstate_in without state_in.  The sums over
+    the tokens are added in a fixed order."""
+    dev = x.device
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    if dw is None:
+        dw = torch.empty(w.shape, dtype=torch.float32, device=dev)
+    if b is None:
+        db = None
+    elif db is None:
+        db = torch.empty(b.shape, dtype=torch.float32, device=dev)
+    if state_in is None:
+        dstate_in = None
+    elif dstate_in is None:
+        dstate_in = torch.empty(state_in.shape, dtype=x.dtype, device=dev)
+    states = (("state_in", state_in), ("dstate_out", dstate_out), ("dstate_in", dstate_in))
+    desc, nbytes = _conv_call(x, w, b, silu, lengths, states, dy=dy, out=dx)
+    _f32("dw", dw, w.shape)
+    _f32("db", db, (x.shape[-1],))
+    if workspace is None:
+        with _on(stream):
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    st = lib.retnet_causal_conv_bwd(
+        ctypes.byref(desc), *_ptrs(x, w, b, state_in, lengths, dy, dstate_out, dx, dw, db, dstate_in, workspace),
+        workspace.numel(), _stream(stream))
+    _check(st, "retnet_causal_conv_bwd")
+    return dx, dw, db, dstate_in
+
+
+@functools.lru_cache(maxsize=256)
+def _rms_desc(shape, dtype, eps, group, sx, sr, sh, sg, so, device):
+    """(descriptor, workspace bytes of the backward on that device)."""
+    n0, n1, st = _row_strides("rmsnorm", shape, sx, sr, sh, sg, so)
+    d = RmsNormDesc(n0, n1, shape[-1], _dtype_code(dtype), eps, group, *st)
+    return d, int(lib.retnet_rmsnorm_bwd_workspace_size(ctypes.byref(d)))
+
+
+def _rms_sum(x, w, residual, residual_out):
+    """Checks of the norm's inputs; gives where their sum is kept (x without a
+    residual)."""
+    _f32("w", w, x.shape[-1:])
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out needs a residual")
+        return x
+    _like("residual", residual, x)
+    if residual_out is None:
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _like("residual_out", residual_out, x)
+    return residual_out
+
+
+def rmsnorm_fwd(x, w=None, *, residual=None, eps=1e-5, out=None, residual_out=None, rstd=None, stream=None):
+    """Root-mean-square norm over the last dimension (bf16 or fp32, any two row
+    strides) of h = x + residual, rounded to x's dtype: y = h rstd w with rstd =
+    1 / sqrt(mean(h^2) + eps) and fp32 gains w (None: 1).  Returns (y, h, rstd): h
+    (x itself without a residual) and rstd, fp32 of x.shape[:-1], are what
+    rmsnorm_bwd takes.  residual_out, where h is kept, and out may be x or
+    residual, but not the same one."""
+    h = _rms_sum(x, w, residual, residual_out)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    else:
+        _like("out", out, x)
+    if rstd is None:
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    _f32("rstd", rstd, x.shape[:-1])
+    sx, so = x.stride(), out.stride()
+    desc, _ = _rms_desc(x.shape, x.dtype, float(eps), 0, sx, sx if residual is None else residual.stride(),
+                        h.stride(), so, so, x.device)
+    st = lib.retnet_rmsnorm_fwd(
+        ctypes.byref(desc), *_ptrs(x, residual, w, None if residual is None else h, out, rstd), _stream(stream))
+    _check(st, "retnet_rmsnorm_fwd")
+    return out, h, rstd
+
+
+def rmsnorm_quant(x, w=None, *, residual=None, eps=1e-5, group=0, out=None, scales=None, residual_out=None,
+                  stream=None):
+    """rmsnorm_fwd with y as e4m3 values q (torch.float8_e4m3fn) and an fp32
+    scale for each `group` columns (a multiple of 8; 0: the whole row): y = q
+    scale, scale = max |y| / 448.  Returns (q, scales, h), scales of x.shape[:-1]
+    + (groups,)."""
+    h = _rms_sum(x, w, residual, residual_out)
+    group, d = operator.index(group), x.shape[-1]
+    if out is None:
+        out = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+    elif out.shape != x.shape or out.dtype != torch.float8_e4m3fn:
+        raise ValueError(f"out must have the shape {tuple(x.shape)} and dtype torch.float8_e4m3fn")
+    if group < 0 or group % 8:
+        raise ValueError(f"group must be 0 or a multiple of 8, got {group}")
+    shape = (*x.shape[:-1], -(-d // group) if group else 1)
+    if scales is None:
+        scales = torch.empty(shape, dtype=torch.float32, device=x.device)
+    _f32("scales", scales, shape)
+    sx, so = x.stride(), out.stride()
+    desc, _ = _rms_desc(x.shape, x.dtype, float(eps), group, sx, sx if residual is None else residual.stride(),
+                        h.stride(), so, so, x.device)
+    st = lib.retnet_rmsnorm_quant(
+        ctypes.byref(desc), *_ptrs(x, residual, w, None if residual is None else h, out, scales),
+        _stream(stream))
+    _check(st, "retnet_rmsnorm_quant")
+    return out, scales, h
+
+
+def rmsnorm_bwd(h, dy, w, rstd, *, dh=None, dx=None, dw=None, workspace=None, stream=None):
+    """Gradients of rmsnorm_fwd: returns (dx, dw); dx, in h's dtype, is the
+    gradient of x and of the residual: that of the norm and dh, which reaches h
+    itself (None: 0).  dw fp32 (w may be None; dw is the sum all the same), added
+    in a fixed order.  dx may be h, dy or dh."""
+    shape, d = h.shape, h.shape[-1:]
+    if dx is None:
+        dx = torch.empty(shape, dtype=h.dtype, device=h.device)
+    else:
+        _like("dx", dx, h)
+    if dw is None:
+        dw = torch.empty(d, dtype=torch.float32, device=h.device)
+    _like("dy", dy, h)
+    if dh is not None:
+        _like("dh", dh, h)
+    _f32("w", w, d)
+    _f32("rstd", rstd, shape[:-1])
+    _f32("dw", dw, d)
+    s = h.stride()
+    desc, nbytes = _rms_desc(shape, h.dtype, 0.0, 0, s, s if dh is None else dh.stride(), s, dy.stride(),
+                             dx.stride(), h.device)
+    if workspace is None:
+        with _on(stream):
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=h.device)
+    st = lib.retnet_rmsnorm_bwd(ctypes.byref(desc), *_ptrs(h, dy, dh, w, rstd, dx, dw, workspace),
+                                workspace.numel(), _stream(stream))
+    _check(st, "retnet_rmsnorm_bwd")
+    return dx, dw
 
 
 def poll_status(workspace, stream=None):
