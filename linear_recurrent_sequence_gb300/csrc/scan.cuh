@@ -2,6 +2,8 @@
 // the lanes that share a channel, rows of a state.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "launch.h"
 #include "rows.cuh"
@@ -114,6 +116,126 @@ __device__ __forceinline__ int tokens_of(const ScanArgs &a, int b) {
   const long long n = a.len64 ? reinterpret_cast<const long long *>(a.lengths)[b]
                               : (long long)reinterpret_cast<const int *>(a.lengths)[b];
   return (int)(n < 0 ? 0 : n > a.N ? a.N : n);
+}
+
+constexpr int kScan = 128, kLoad = 128, kThreads = kScan + kLoad;
+
+// Channels of a CTA (grid.x counts the blocks of all groups) and tokens at a
+// time.  The tile's step sizes take the most shared memory: channels x tokens.
+template <int L>
+struct Block {
+  static constexpr int kChannels = kScan / L;
+  static constexpr int kTile = L <= 4 ? 8 * L : 32;
+  static constexpr int SP = 4 * L;
+  static __host__ __device__ int per_group(int E, int G) { return (E / G + kChannels - 1) / kChannels; }
+};
+
+// Two neighbouring channels of a row.
+template <typename T>
+struct Two {
+  T a, b;
+};
+// kPair: the row begins on the pair's boundary.  n: channels that are there.
+template <typename T, bool kPair>
+__device__ __forceinline__ Two<T> load_two(const T *p, int n) {
+  Two<T> v;
+  if (kPair) {
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t w = n > 0 ? *reinterpret_cast<const uint32_t *>(p) : 0u;
+      v = *reinterpret_cast<const Two<T> *>(&w);
+    } else {
+      const float2 w = n > 0 ? *reinterpret_cast<const float2 *>(p) : make_float2(0.f, 0.f);
+      v.a = w.x;
+      v.b = w.y;
+    }
+  } else {
+    v.a = n > 0 ? p[0] : from_float<T>(0.f);
+    v.b = n > 1 ? p[1] : from_float<T>(0.f);
+  }
+  return v;
+}
+
+template <typename T, bool kPair>
+__device__ __forceinline__ void store_two(T *p, int n, float a, float b) {
+  if (kPair) {
+    if (n > 0) {
+      if constexpr (sizeof(T) == 2)
+        *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(a, b);
+      else
+        *reinterpret_cast<float2 *>(p) = make_float2(a, b);
+    }
+  } else {
+    if (n > 0) p[0] = from_float<T>(a);
+    if (n > 1) p[1] = from_float<T>(b);
+  }
+}
+
+
+// Four neighbouring channels of a row as they were read; kVec: the row begins on
+// the four's boundary.  n: channels that are there.
+template <typename T>
+struct Four {
+  T v[4];
+};
+template <typename T, bool kVec>
+__device__ __forceinline__ Four<T> load_four(const T *p, int n) {
+  Four<T> f;
+  if (kVec) {
+    if constexpr (sizeof(T) == 2) {
+      const uint2 w = n > 0 ? *reinterpret_cast<const uint2 *>(p) : make_uint2(0u, 0u);
+      f = *reinterpret_cast<const Four<T> *>(&w);
+    } else {
+      const float4 w = n > 0 ? *reinterpret_cast<const float4 *>(p) : make_float4(0.f, 0.f, 0.f, 0.f);
+      f = *reinterpret_cast<const Four<T> *>(&w);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f.v[i] = i < n ? p[i] : from_float<T>(0.f);
+  }
+  return f;
+}
+
+template <typename T, bool kVec>
+__device__ __forceinline__ void store_four(T *p, int n, const float (&f)[4]) {
+  if (kVec) {
+    if (n > 0) {
+      if constexpr (sizeof(T) == 2) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+        *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+      } else {
+        *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) p[i] = from_float<T>(f[i]);
+  }
+}
+
+// Lanes a channel: four states a lane.
+inline int lanes_of(int S) {
+  int L = 1;
+  while (4 * L < S) L *= 2;
+  return L;
+}
+
+template <typename F>
+cudaError_t by_lanes(int S, F f) {
+  switch (lanes_of(S)) {
+    case 1: return f(std::integral_constant<int, 1>());
+    case 2: return f(std::integral_constant<int, 2>());
+    case 4: return f(std::integral_constant<int, 4>());
+    case 8: return f(std::integral_constant<int, 8>());
+    default: return f(std::integral_constant<int, 16>());
+  }
+}
+
+// Does every row of a tensor (and, with E / G a multiple of it, every block of
+// channels) begin on a boundary of `step` channels?
+inline bool rows_on(const ScanArgs &a, const void *p, const long long s[2], int step, int esz) {
+  return !p || (reinterpret_cast<uintptr_t>(p) % (step * esz) == 0 && (a.N <= 1 || s[1] % step == 0) &&
+                (a.B <= 1 || s[0] % step == 0));
 }
 
 }  // namespace scan

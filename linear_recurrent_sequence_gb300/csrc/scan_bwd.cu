@@ -26,109 +26,176 @@ namespace {
 
 using namespace scan;
 
-constexpr int kThreads = 128;
+constexpr int kMain = 128;   // threads of the chunk's CTA
 constexpr int kTile = 8;
 
 template <int L>
 struct Geo {
   static constexpr int SP = 4 * L;                           // states with padding
-  static constexpr int kChunk = 16 * L < 64 ? 16 * L : 64;   // tokens
-  static constexpr int kBlock = 2 * kThreads / L;            // channels of a CTA
+  static constexpr int kChunk = 16 * L < 64 ? 16 * L : 64;   // tokens: two tiles of the first pass
+  static constexpr int kBlock = 2 * kMain / L;               // channels of a CTA
   static constexpr int kTiles = kChunk / kTile;
+  static constexpr bool kTwice = L < 16;                     // B and C twice in shared memory, as pairs
   static __host__ __device__ int per_group(int E, int G) { return (E / G + kBlock - 1) / kBlock; }
 };
 
-// What a chunk alone adds: one channel's four states a thread.
-template <typename T, int L>
-__global__ void __launch_bounds__(kThreads)
-scan_bwd_chunks_kernel(const ScanArgs a, const ScanBwdPlan pl, float *__restrict__ ws) {
-  constexpr int CC = kThreads / L, SP = 4 * L, TT = 16, NE = TT / L, NB = (TT * SP + kThreads - 1) / kThreads;
-  __shared__ __align__(16) float4 dus[TT][CC];  // delta, u, ds
-  __shared__ __align__(16) float bm[TT][SP], cm[TT][SP];
-  pdl_launch_dependents();
+template <int L>
+struct ChunksSmem {
+  float4 du[2][Block<L>::kTile][Block<L>::kChannels];  // delta, delta, u, u
+  float2 ds[2][Block<L>::kTile][Block<L>::kChannels];  // ds, ds
+  float bm[2][Block<L>::kTile][Block<L>::SP], cm[2][Block<L>::kTile][Block<L>::SP];
+};
+
+// What the chunks alone add: `run` chunks one after another by one CTA, half of
+// whose warps load and prepare the tokens ahead, as in the forward.
+template <typename T, int L, bool kPair>
+__global__ void __launch_bounds__(kThreads, 2)
+scan_bwd_chunks_kernel(const ScanArgs a, const ScanBwdPlan pl, int run, float *__restrict__ ws) {
+  using K = Block<L>;
+  constexpr int CC = K::kChannels, TT = K::kTile, SP = K::SP;
+  static_assert(Geo<L>::kChunk == 2 * TT, "a chunk is two tiles");
+  extern __shared__ __align__(16) uint8_t dyn[];
+  ChunksSmem<L> &sm = *reinterpret_cast<ChunksSmem<L> *>(dyn);
   pdl_wait();
-  const int tid = threadIdx.x, Eg = a.E / a.G, per = (Eg + CC - 1) / CC, blocks = a.G * per;
-  const int k = blockIdx.x / blocks, blk = blockIdx.x - k * blocks, group = blk / per, c0 = (blk - group * per) * CC;
-  const int b = blockIdx.y, n = tokens_of(a, b), t0 = k * pl.chunk, live = min(n, t0 + pl.chunk);
-  const int ci = tid / L, s0 = tid % L * 4, e = group * Eg + min(c0 + ci, Eg - 1);
-  const bool vec = a.S % 4 == 0;
-  const float4 A4 = load_states(a.A + (size_t)e * a.S, s0, a.S, vec && reinterpret_cast<uintptr_t>(a.A) % 16 == 0);
-  const float2 A2[2] = {make_float2(A4.x * kLog2e, A4.y * kLog2e), make_float2(A4.z * kLog2e, A4.w * kLog2e)};
-  float2 h[2] = {both(0.f), both(0.f)}, P[2] = {both(1.f), both(1.f)}, g[2] = {both(0.f), both(0.f)};
-  const int lc = tid % CC, lt = tid / CC, le = group * Eg + min(c0 + lc, Eg - 1);
-  const bool there = c0 + lc < Eg;
+  const int per = K::per_group(a.E, a.G), Eg = a.E / a.G;
+  const int blocks = a.G * per, first = blockIdx.x / blocks * run, blk = blockIdx.x % blocks;
+  const int group = blk / per, c0 = (blk - group * per) * CC, b = blockIdx.y;
+  const int n = tokens_of(a, b), t0 = first * pl.chunk, t1 = min(a.N, t0 + run * pl.chunk), live = min(t1, n);
+  // (every chunk writes what it adds, those behind the sequence's end nothing)
+  const int tiles = (min(first + run, pl.chunks) - first) * 2;
+
+  if (threadIdx.x < kScan) {
+    const int tid = threadIdx.x, ci = tid / L, s0 = tid % L * 4;
+    const bool own = c0 + ci < Eg, vec = a.S % 4 == 0;
+    const int e = group * Eg + min(c0 + ci, Eg - 1);
+    const float4 A4 = load_states(a.A + (size_t)e * a.S, s0, a.S, vec && reinterpret_cast<uintptr_t>(a.A) % 16 == 0);
+    const float2 A2[2] = {make_float2(A4.x * kLog2e, A4.y * kLog2e), make_float2(A4.z * kLog2e, A4.w * kLog2e)};
+    float2 h[2] = {both(0.f), both(0.f)}, P[2] = {both(1.f), both(1.f)}, g[2] = {both(0.f), both(0.f)};
+    float sum = 0.f;
+    __syncthreads();
+    for (int i = 0; i < tiles; ++i) {
+      const int buf = i & 1;
+      if (t0 + i * TT < live) {
+#pragma unroll 8
+        for (int j = 0; j < TT; ++j) {
+          const float4 v = sm.du[buf][j][ci];
+          const float2 dd = make_float2(v.x, v.y), uu = make_float2(v.z, v.w), ds = sm.ds[buf][j][ci];
+          const float4 B4 = *reinterpret_cast<const float4 *>(&sm.bm[buf][j][s0]), C4 = *reinterpret_cast<const float4 *>(&sm.cm[buf][j][s0]);
+          const float2 Bv[2] = {make_float2(B4.x, B4.y), make_float2(B4.z, B4.w)};
+          const float2 Cv[2] = {make_float2(C4.x, C4.y), make_float2(C4.z, C4.w)};
+          sum += v.x;
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const float2 w = tc::mul2(dd, A2[p]), d = make_float2(ex2(w.x), ex2(w.y));
+            h[p] = tc::fma2(d, h[p], tc::mul2(uu, Bv[p]));
+            P[p] = tc::mul2(P[p], d);
+            g[p] = tc::fma2(P[p], tc::mul2(ds, Cv[p]), g[p]);
+          }
+        }
+      }
+      __syncthreads();
+      if (i & 1) {
+        const size_t at = ((size_t)(first + i / 2) * a.B + b) * a.E + e;
+        if (own) {
+          store_states(ws + at * a.S, s0, a.S, vec, make_float4(h[0].x, h[0].y, h[1].x, h[1].y));
+          store_states(ws + pl.g + at * a.S, s0, a.S, vec, make_float4(g[0].x, g[0].y, g[1].x, g[1].y));
+          if (s0 == 0) ws[pl.sum + at] = sum;
+        }
+        h[0] = h[1] = g[0] = g[1] = both(0.f);
+        P[0] = P[1] = both(1.f);
+        sum = 0.f;
+      }
+    }
+    pdl_launch_dependents();
+    return;
+  }
+
+  constexpr int NP = TT * CC / 2 / kLoad, TS = 2 * kLoad / CC;
+  constexpr int NB = (TT * SP + kLoad - 1) / kLoad;
+  const int tid = threadIdx.x - kScan, lc = tid % (CC / 2) * 2, lt = tid / (CC / 2);
+  const int there = min(2, max(0, Eg - c0 - lc));
+  const int le = group * Eg + min(c0 + lc, Eg - 1);
   const T *x = reinterpret_cast<const T *>(a.x) + b * a.sx[0] + le;
   const T *dt = reinterpret_cast<const T *>(a.dt) + b * a.sdt[0] + le;
   const T *dy = reinterpret_cast<const T *>(a.dy) + b * a.sdy[0] + le;
   const T *z = a.z ? reinterpret_cast<const T *>(a.z) + b * a.sz[0] + le : nullptr;
   const T *Bp = reinterpret_cast<const T *>(a.Bm) + b * a.sB[0] + group * a.sB[2];
   const T *Cp = reinterpret_cast<const T *>(a.Cm) + b * a.sC[0] + group * a.sC[2];
-  const float bias = a.bias ? a.bias[le] : 0.f;
-  float dsum = 0.f;
-  for (int t = t0; t < live; t += TT) {
-    __syncthreads();
+  const int l1 = there > 1;
+  const float bias[2] = {a.bias ? a.bias[le] : 0.f, a.bias ? a.bias[le + l1] : 0.f};
+  struct Raw {
+    Two<T> x[NP], z[NP], d[NP], y[NP];
+    T B[NB], C[NB];
+  };
+  auto load = [&](int i, Raw &r) {
+    const int t = t0 + i * TT;
+    if (i >= tiles || t >= live) return;
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      const int at = t + lt + i * L;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (there && at < live) {
-        v.x = to_float(dt[at * a.sdt[1]]) + bias;
-        if (a.softplus) v.x = softplus(v.x);
-        v.y = v.x * to_float(x[at * a.sx[1]]);
-        v.z = to_float(dy[at * a.sdy[1]]);
-        if (z) v.z *= silu(to_float(z[at * a.sz[1]]));
-      }
-      dsum += v.x;
-      dus[lt + i * L][lc] = v;
+    for (int j = 0; j < NP; ++j) {
+      const int at = t + lt + j * TS, m = at < live ? there : 0;
+      r.x[j] = load_two<T, kPair>(x + at * a.sx[1], m);
+      r.d[j] = load_two<T, kPair>(dt + at * a.sdt[1], m);
+      r.y[j] = load_two<T, kPair>(dy + at * a.sdy[1], m);
+      r.z[j] = load_two<T, kPair>(z + at * a.sz[1], z ? m : 0);
     }
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const int j = tid + i * kThreads, at = t + j / SP, s = j % SP;
-      if (j < TT * SP) {
-        const bool in = at < live && s < a.S;
-        (&bm[0][0])[j] = in ? to_float(Bp[at * a.sB[1] + s]) : 0.f;
-        (&cm[0][0])[j] = in ? to_float(Cp[at * a.sC[1] + s]) : 0.f;
+    for (int j = 0; j < NB; ++j) {
+      const int o = tid + j * kLoad, at = t + o / SP, s = o % SP;
+      const bool in = (NB * kLoad == TT * SP || o < TT * SP) && at < live && s < a.S;
+      r.B[j] = in ? Bp[at * a.sB[1] + s] : from_float<T>(0.f);
+      r.C[j] = in ? Cp[at * a.sC[1] + s] : from_float<T>(0.f);
+    }
+  };
+  auto put = [&](int i, const Raw &r) {
+    const int buf = i & 1, t = t0 + i * TT;
+    if (i >= tiles || t >= live) return;
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      const int at = lt + j * TS;
+      const float xs[2] = {to_float(r.x[j].a), to_float(r.x[j].b)}, zs[2] = {to_float(r.z[j].a), to_float(r.z[j].b)};
+      const float ys[2] = {to_float(r.y[j].a), to_float(r.y[j].b)};
+      float d[2] = {to_float(r.d[j].a) + bias[0], to_float(r.d[j].b) + bias[1]};
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        if (a.softplus) d[c] = softplus(d[c]);
+        if (!(c < there && t + at < live)) d[c] = 0.f;
+        const float u = d[c] * xs[c], ds = z ? ys[c] * silu(zs[c]) : ys[c];
+        sm.du[buf][at][lc + c] = make_float4(d[c], d[c], u, u);
+        sm.ds[buf][at][lc + c] = both(ds);
       }
     }
-    __syncthreads();
 #pragma unroll
-    for (int j = 0; j < TT; ++j) {
-      const float4 v = dus[j][ci];
-      const float4 B4 = *reinterpret_cast<const float4 *>(&bm[j][s0]), C4 = *reinterpret_cast<const float4 *>(&cm[j][s0]);
-      const float2 Bv[2] = {make_float2(B4.x, B4.y), make_float2(B4.z, B4.w)};
-      const float2 Cv[2] = {make_float2(C4.x, C4.y), make_float2(C4.z, C4.w)};
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const float2 w = tc::mul2(both(v.x), A2[p]), d = make_float2(ex2(w.x), ex2(w.y));
-        h[p] = tc::fma2(d, h[p], tc::mul2(both(v.y), Bv[p]));
-        P[p] = tc::mul2(P[p], d);
-        g[p] = tc::fma2(P[p], tc::mul2(both(v.z), Cv[p]), g[p]);
+    for (int j = 0; j < NB; ++j) {
+      const int o = tid + j * kLoad;
+      if (NB * kLoad == TT * SP || o < TT * SP) {
+        (&sm.bm[buf][0][0])[o] = to_float(r.B[j]);
+        (&sm.cm[buf][0][0])[o] = to_float(r.C[j]);
       }
     }
-  }
-  const size_t at = ((size_t)k * a.B + b) * a.E;
-  if (c0 + ci < Eg) {
-    store_states(ws + (at + e) * a.S, s0, a.S, vec, make_float4(h[0].x, h[0].y, h[1].x, h[1].y));
-    store_states(ws + pl.g + (at + e) * a.S, s0, a.S, vec, make_float4(g[0].x, g[0].y, g[1].x, g[1].y));
-  }
+  };
+  Raw next, after;
+  load(0, next);
+  load(1, after);
+  put(0, next);
+  next = after;
   __syncthreads();
-  float *red = reinterpret_cast<float *>(&dus[0][0]);
-  red[lt * CC + lc] = dsum;
-  __syncthreads();
-  if (tid < CC && there) {
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < L; ++i) s += red[i * CC + tid];
-    ws[pl.sum + at + le] = s;
+  for (int i = 0; i < tiles; ++i) {
+    load(i + 2, after);
+    put(i + 1, next);
+    __syncthreads();
+    next = after;
   }
+  pdl_launch_dependents();
 }
 
 // The state before each chunk (y = 0) and the gradient that arrives behind it
-// (y = 1), in the places of what the chunks add; also dh_in.
+// (y = 1), in the places of what the chunks add; also dh_in.  Eight chunks'
+// values are read before any of them is replaced.
 __global__ void __launch_bounds__(256)
 scan_bwd_carry_kernel(const ScanArgs a, const ScanBwdPlan pl, float *__restrict__ ws) {
   pdl_launch_dependents();
   pdl_wait();
+  constexpr int U = 8;
   const long long n = (long long)a.B * a.E * a.S, i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= n) return;
   const long long be = i / a.S;
@@ -136,48 +203,51 @@ scan_bwd_carry_kernel(const ScanArgs a, const ScanBwdPlan pl, float *__restrict_
   const float A2 = a.A[(size_t)e * a.S + s] * kLog2e;
   const float *sum = ws + pl.sum + be;
   const long long step = (long long)a.B * a.E;
-  if (blockIdx.y == 0) {
-    float v = a.h_in ? a.h_in[i] : 0.f;
-    float *at = ws + i;
-    for (int k = 0; k < pl.chunks; ++k) {
-      const float l = at[k * n], w = ex2(sum[k * step] * A2);
-      at[k * n] = v;
-      v = fmaf(w, v, l);
+  const bool back = blockIdx.y != 0;
+  float *at = ws + (back ? pl.g : 0) + i;
+  const float *from = back ? a.dh_out : a.h_in;
+  float v = from ? from[i] : 0.f;
+  for (int k0 = 0; k0 < pl.chunks; k0 += U) {
+    float l[U], w[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int k = back ? pl.chunks - 1 - k0 - j : k0 + j;
+      const bool in = k0 + j < pl.chunks;
+      l[j] = in ? at[k * n] : 0.f;
+      w[j] = in ? sum[k * step] : 0.f;
     }
-  } else {
-    float v = a.dh_out ? a.dh_out[i] : 0.f;
-    float *at = ws + pl.g + i;
-    for (int k = pl.chunks - 1; k >= 0; --k) {
-      const float l = at[k * n], w = ex2(sum[k * step] * A2);
-      at[k * n] = v;
-      v = fmaf(w, v, l);
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int k = back ? pl.chunks - 1 - k0 - j : k0 + j;
+      if (k0 + j < pl.chunks) {
+        at[k * n] = v;
+        v = fmaf(ex2(w[j] * A2), v, l[j]);
+      }
     }
-    if (a.dh_in) a.dh_in[i] = v;
   }
+  if (back && a.dh_in) a.dh_in[i] = v;
 }
 
-template <typename T, int L>
-struct BwdSmem {
+template <int L>
+struct MainSmem {
   using G = Geo<L>;
-  static constexpr int kD = 0;                                     // delta [chunk][block]
-  static constexpr int kU = kD + G::kChunk * G::kBlock;            // u
-  static constexpr int kDs = kU + G::kChunk * G::kBlock;           // ds
-  static constexpr int kB = kDs + G::kChunk * G::kBlock;           // B [chunk][SP]
-  static constexpr int kC = kB + G::kChunk * G::SP;                // C
-  static constexpr int kStart = kC + G::kChunk * G::SP;            // [tiles][2][threads] float4
-  static constexpr int kSums = kStart + G::kTiles * 2 * kThreads * 4;  // [2][3][tile][block]: s, q, r
-  static constexpr int kBc = kSums + 2 * 3 * kTile * G::kBlock;    // [2][warps][tile][2][SP]
-  static constexpr int kFloats = kBc + 2 * (kThreads / 32) * kTile * 2 * G::SP;
+  float d[G::kChunk][G::kBlock], u[G::kChunk][G::kBlock], ds[G::kChunk][G::kBlock];  // delta, u, ds
+  float b[G::kChunk][G::SP * (G::kTwice ? 2 : 1)], c[G::kChunk][G::SP * (G::kTwice ? 2 : 1)];
+  float4 start[G::kTiles][2][kMain];           // the state before a tile: channel 0, 1
+  float sums[3][kTile][G::kBlock];             // sum C h, sum g B, sum g p A log2(e)
+  float bc[kMain / 32][kTile][2][G::SP];       // a warp's share of dB and dC
 };
 
-template <typename T, int L>
-__global__ void __launch_bounds__(kThreads, 2)
+// One chunk of a block of channels.  f32x2 pairs are the thread's two channels:
+// delta, u and ds come as pairs out of shared memory, B and C are kept there
+// twice each (but for S > 32, where that would leave room for one CTA an SM).
+template <typename T, int L, bool kVec>
+__global__ void __launch_bounds__(kMain, 2)
 scan_bwd_kernel(const ScanArgs a, const ScanBwdPlan pl, float *__restrict__ ws) {
   using G = Geo<L>;
-  using M = BwdSmem<T, L>;
-  constexpr int CC = G::kBlock, SP = G::SP, TC = G::kChunk;
-  extern __shared__ __align__(16) float sm[];
-  pdl_launch_dependents();
+  constexpr int CC = G::kBlock, SP = G::SP, TC = G::kChunk, QC = CC / 4;  // quads of channels
+  extern __shared__ __align__(16) uint8_t dyn[];
+  MainSmem<L> &sm = *reinterpret_cast<MainSmem<L> *>(dyn);
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, Eg = a.E / a.G;
   const int per = G::per_group(a.E, a.G), blocks = a.G * per;
@@ -185,151 +255,210 @@ scan_bwd_kernel(const ScanArgs a, const ScanBwdPlan pl, float *__restrict__ ws) 
   const int b = blockIdx.y, n = tokens_of(a, b), t0 = k * TC, live = min(n, t0 + TC), t1 = min(a.N, t0 + TC);
   const size_t bk = (size_t)k * a.B + b;
 
-  // ---- delta, u, ds, B and C of the chunk (zeros past the sequence's end)
-  for (int j = tid; j < TC * CC; j += kThreads) {
-    const int at = t0 + j / CC, c = j % CC;
-    float d = 0.f, u = 0.f, ds = 0.f;
-    if (c0 + c < Eg && at < live) {
-      const int e = group * Eg + c0 + c;
-      d = to_float(reinterpret_cast<const T *>(a.dt)[b * a.sdt[0] + at * a.sdt[1] + e]) + (a.bias ? a.bias[e] : 0.f);
-      if (a.softplus) d = softplus(d);
-      u = d * to_float(reinterpret_cast<const T *>(a.x)[b * a.sx[0] + at * a.sx[1] + e]);
-      ds = to_float(reinterpret_cast<const T *>(a.dy)[b * a.sdy[0] + at * a.sdy[1] + e]);
-      if (a.z) ds *= silu(to_float(reinterpret_cast<const T *>(a.z)[b * a.sz[0] + at * a.sz[1] + e]));
-    }
-    sm[M::kD + j] = d;
-    sm[M::kU + j] = u;
-    sm[M::kDs + j] = ds;
+  // ---- a quad of channels, as loader of their tokens and writer of their gradients
+  const int qc = tid % QC * 4, qt = tid / QC;  // channel in the block, first token
+  constexpr int QS = kMain / QC;               // tokens between a thread's
+  const int there = min(4, max(0, Eg - c0 - qc)), qe = group * Eg + min(c0 + qc, Eg - 1);
+  const T *x = reinterpret_cast<const T *>(a.x) + b * a.sx[0] + qe;
+  const T *dt = reinterpret_cast<const T *>(a.dt) + b * a.sdt[0] + qe;
+  const T *dy = reinterpret_cast<const T *>(a.dy) + b * a.sdy[0] + qe;
+  const T *z = a.z ? reinterpret_cast<const T *>(a.z) + b * a.sz[0] + qe : nullptr;
+  float bias[4], Dv[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    bias[i] = a.bias && i < there ? a.bias[qe + i] : 0.f;
+    Dv[i] = a.D && i < there ? a.D[qe + i] : 0.f;
   }
-  for (int j = tid; j < TC * SP; j += kThreads) {
-    const int at = t0 + j / SP, s = j % SP;
-    const bool in = at < live && s < a.S;
-    sm[M::kB + j] = in ? to_float(reinterpret_cast<const T *>(a.Bm)[b * a.sB[0] + at * a.sB[1] + group * a.sB[2] + s]) : 0.f;
-    sm[M::kC + j] = in ? to_float(reinterpret_cast<const T *>(a.Cm)[b * a.sC[0] + at * a.sC[1] + group * a.sC[2] + s]) : 0.f;
+
+  // delta, u, ds, B and C of the chunk (zeros past the sequence's end)
+  constexpr int NQ = TC / QS, UQ = NQ < 4 ? NQ : 4;  // quads a thread, of which at once
+#pragma unroll 1
+  for (int j0 = 0; j0 < NQ; j0 += UQ) {
+    Four<T> xr[UQ], dr[UQ], yr[UQ], zr[UQ];
+#pragma unroll
+    for (int j = 0; j < UQ; ++j) {
+      const int at = t0 + qt + (j0 + j) * QS, m = at < live ? there : 0;
+      xr[j] = load_four<T, kVec>(x + at * a.sx[1], m);
+      dr[j] = load_four<T, kVec>(dt + at * a.sdt[1], m);
+      yr[j] = load_four<T, kVec>(dy + at * a.sdy[1], m);
+      zr[j] = load_four<T, kVec>(z + at * a.sz[1], z ? m : 0);
+    }
+#pragma unroll
+    for (int j = 0; j < UQ; ++j) {
+      const int t = qt + (j0 + j) * QS;
+      float d[4], u[4], ds[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        d[i] = to_float(dr[j].v[i]) + bias[i];
+        if (a.softplus) d[i] = softplus(d[i]);
+        if (!(i < there && t0 + t < live)) d[i] = 0.f;
+        u[i] = d[i] * to_float(xr[j].v[i]);
+        ds[i] = to_float(yr[j].v[i]);
+        if (z) ds[i] *= silu(to_float(zr[j].v[i]));
+      }
+      *reinterpret_cast<float4 *>(&sm.d[t][qc]) = make_float4(d[0], d[1], d[2], d[3]);
+      *reinterpret_cast<float4 *>(&sm.u[t][qc]) = make_float4(u[0], u[1], u[2], u[3]);
+      *reinterpret_cast<float4 *>(&sm.ds[t][qc]) = make_float4(ds[0], ds[1], ds[2], ds[3]);
+    }
+  }
+  {
+    const T *Bp = reinterpret_cast<const T *>(a.Bm) + b * a.sB[0] + group * a.sB[2];
+    const T *Cp = reinterpret_cast<const T *>(a.Cm) + b * a.sC[0] + group * a.sC[2];
+    constexpr int NB = (TC * SP + kMain - 1) / kMain;
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const int o = tid + j * kMain, t = o / SP, s = o % SP, at = t0 + t;
+      if (NB * kMain > TC * SP && o >= TC * SP) break;
+      const bool in = at < live && s < a.S;
+      const float Bv = in ? to_float(Bp[at * a.sB[1] + s]) : 0.f, Cv = in ? to_float(Cp[at * a.sC[1] + s]) : 0.f;
+      if (G::kTwice) {
+        *reinterpret_cast<float2 *>(&sm.b[t][2 * s]) = both(Bv);
+        *reinterpret_cast<float2 *>(&sm.c[t][2 * s]) = both(Cv);
+      } else {
+        sm.b[t][s] = Bv;
+        sm.c[t][s] = Cv;
+      }
+    }
   }
 
   // ---- four states of channels ca, ca + 1
   const int s0 = lane % L * 4, ca = tid / L * 2;
   const bool vec = a.S % 4 == 0;
-  float2 A2[2][2], h[2][2], ag[2][2], dA[2][2];
+  float2 A2[4], h[4], ag[4], dA[4];
   bool own[2];
   int ech[2];
+  {
+    float A[2][4], hv[2][4], gv[2][4];
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    own[c] = c0 + ca + c < Eg;
-    const int e = ech[c] = group * Eg + min(c0 + ca + c, Eg - 1);
-    const float4 A4 = load_states(a.A + (size_t)e * a.S, s0, a.S, vec && reinterpret_cast<uintptr_t>(a.A) % 16 == 0);
-    // (0 for a channel that is not there: it takes part in the sums over channels)
-    const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float4 h4 = own[c] ? load_states(ws + (bk * a.E + e) * a.S, s0, a.S, vec) : none;
-    const float4 g4 = own[c] ? load_states(ws + pl.g + (bk * a.E + e) * a.S, s0, a.S, vec) : none;
-    A2[c][0] = make_float2(A4.x * kLog2e, A4.y * kLog2e);
-    A2[c][1] = make_float2(A4.z * kLog2e, A4.w * kLog2e);
-    h[c][0] = make_float2(h4.x, h4.y);
-    h[c][1] = make_float2(h4.z, h4.w);
-    ag[c][0] = make_float2(g4.x, g4.y);
-    ag[c][1] = make_float2(g4.z, g4.w);
-    dA[c][0] = dA[c][1] = both(0.f);
+    for (int c = 0; c < 2; ++c) {
+      own[c] = c0 + ca + c < Eg;
+      const int e = ech[c] = group * Eg + min(c0 + ca + c, Eg - 1);
+      // (0 for a channel that is not there: it takes part in the sums over channels)
+      const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+      const float4 A4 = load_states(a.A + (size_t)e * a.S, s0, a.S, vec && reinterpret_cast<uintptr_t>(a.A) % 16 == 0);
+      const float4 h4 = own[c] ? load_states(ws + (bk * a.E + e) * a.S, s0, a.S, vec) : none;
+      const float4 g4 = own[c] ? load_states(ws + pl.g + (bk * a.E + e) * a.S, s0, a.S, vec) : none;
+      A[c][0] = A4.x; A[c][1] = A4.y; A[c][2] = A4.z; A[c][3] = A4.w;
+      hv[c][0] = h4.x; hv[c][1] = h4.y; hv[c][2] = h4.z; hv[c][3] = h4.w;
+      gv[c][0] = g4.x; gv[c][1] = g4.y; gv[c][2] = g4.z; gv[c][3] = g4.w;
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      A2[s] = make_float2(A[0][s] * kLog2e, A[1][s] * kLog2e);
+      h[s] = make_float2(hv[0][s], hv[1][s]);
+      ag[s] = make_float2(gv[0][s], gv[1][s]);
+      dA[s] = both(0.f);
+    }
   }
   __syncthreads();
-  auto pairs = [&](int base, int t, float2 (&v)[2]) {
-    const float4 f = *reinterpret_cast<const float4 *>(&sm[base + t * SP + s0]);
-    v[0] = make_float2(f.x, f.y);
-    v[1] = make_float2(f.z, f.w);
+  auto per_state = [&](const float *row, float2 (&v)[4]) {
+    if (G::kTwice) {
+      const float4 p = *reinterpret_cast<const float4 *>(row + 2 * s0), q = *reinterpret_cast<const float4 *>(row + 2 * s0 + 4);
+      v[0] = make_float2(p.x, p.y);
+      v[1] = make_float2(p.z, p.w);
+      v[2] = make_float2(q.x, q.y);
+      v[3] = make_float2(q.z, q.w);
+    } else {
+      const float4 p = *reinterpret_cast<const float4 *>(row + s0);
+      v[0] = both(p.x);
+      v[1] = both(p.y);
+      v[2] = both(p.z);
+      v[3] = both(p.w);
+    }
   };
-  auto chans = [&](int base, int t) { return *reinterpret_cast<const float2 *>(&sm[base + t * CC + ca]); };
-  float4 *start = reinterpret_cast<float4 *>(sm + M::kStart);
+  auto chans = [&](const float *row) { return *reinterpret_cast<const float2 *>(row + ca); };
 
   // ---- forwards: the state before every tile
   const int tiles = live > t0 ? (live - t0 + kTile - 1) / kTile : 0;
   for (int i = 0; i < tiles; ++i) {
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-      start[(i * 2 + c) * kThreads + tid] = make_float4(h[c][0].x, h[c][0].y, h[c][1].x, h[c][1].y);
+    sm.start[i][0][tid] = make_float4(h[0].x, h[1].x, h[2].x, h[3].x);
+    sm.start[i][1][tid] = make_float4(h[0].y, h[1].y, h[2].y, h[3].y);
     if (i + 1 == tiles) break;
 #pragma unroll
     for (int j = 0; j < kTile; ++j) {
       const int t = i * kTile + j;
-      float2 B[2];
-      pairs(M::kB, t, B);
-      const float2 d = chans(M::kD, t), u = chans(M::kU, t);
+      float2 B[4];
+      per_state(sm.b[t], B);
+      const float2 d = chans(sm.d[t]), u = chans(sm.u[t]);
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const float2 w = tc::mul2(both(c ? d.y : d.x), A2[c][p]);
-          h[c][p] = tc::fma2(make_float2(ex2(w.x), ex2(w.y)), h[c][p], tc::mul2(both(c ? u.y : u.x), B[p]));
-        }
+      for (int s = 0; s < 4; ++s) {
+        const float2 w = tc::mul2(d, A2[s]);
+        h[s] = tc::fma2(make_float2(ex2(w.x), ex2(w.y)), h[s], tc::mul2(u, B[s]));
+      }
     }
   }
 
   // ---- backwards, tile by tile
-  constexpr int kChans = CC > kThreads ? CC / kThreads : 1;  // of a thread in the outputs' pass
-  float sD[kChans], sBias[kChans];
+  float sD[4] = {}, sBias[4] = {};
+  constexpr int NW = kTile / QS > 0 ? kTile / QS : 1;  // quads of a tile a thread writes
+  // What a lane got of the sums of 8 values v = j * 2 + c (tokens j, channels c).
+  auto put_sums = [&](float (*to)[CC], int j0, float (&v)[8]) {
+    share_sums<8, L>(v);
+    constexpr int W = L < 8 ? L : 8;
+    if (lane % L < W)
 #pragma unroll
-  for (int i = 0; i < kChans; ++i) sD[i] = sBias[i] = 0.f;
-  for (int i = tiles - 1, buf = 0; i >= 0; --i, buf ^= 1) {
-    float2 dec[kTile][2][2], hs[kTile][2][2];
+      for (int m = 0; m < 8 / W; ++m) {
+        const int idx = lane % L * (8 / W) + m;
+        to[j0 + idx / 2][ca + idx % 2] = v[m];
+      }
+  };
+  // The same for sums over the warp's channels of values v = j * 4 + s.
+  auto put_bc = [&](int which, int j0, float (&v)[8]) {
+    share_sums<8, 32 / L, L>(v);
+    constexpr int W = 32 / L < 8 ? 32 / L : 8;
+    if (lane / L < W)
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const float4 f = start[(i * 2 + c) * kThreads + tid];
-      h[c][0] = make_float2(f.x, f.y);
-      h[c][1] = make_float2(f.z, f.w);
+      for (int m = 0; m < 8 / W; ++m) {
+        const int idx = lane / L * (8 / W) + m;
+        sm.bc[warp][j0 + idx / 4][which][s0 + idx % 4] = v[m];
+      }
+  };
+  for (int i = tiles - 1; i >= 0; --i) {
+    // (the channels' rows for the outputs, on their way meanwhile)
+    Four<T> xr[NW], dr[NW], yr[NW], zr[NW];
+    const bool writes = QS <= kTile || qt < kTile;
+#pragma unroll
+    for (int m = 0; m < NW; ++m) {
+      const int at = t0 + i * kTile + qt + m * QS, c = writes && at < live ? there : 0;
+      xr[m] = load_four<T, kVec>(x + at * a.sx[1], c);
+      dr[m] = load_four<T, kVec>(dt + at * a.sdt[1], a.softplus ? c : 0);
+      yr[m] = load_four<T, kVec>(dy + at * a.sdy[1], z ? c : 0);
+      zr[m] = load_four<T, kVec>(z + at * a.sz[1], z ? c : 0);
     }
-    float *sums = sm + M::kSums + buf * 3 * kTile * CC;
-    float *bcp = sm + M::kBc + (buf * (kThreads / 32) + warp) * kTile * 2 * SP;
-    // What a lane got of the sums of 8 values v = j * 2 + c (tokens j, channels c).
-    auto put_sums = [&](float *to, int j0, float (&v)[8]) {
-      share_sums<8, L>(v);
-      constexpr int W = L < 8 ? L : 8;
-      if (lane % L < W)
-#pragma unroll
-        for (int m = 0; m < 8 / W; ++m) {
-          const int idx = lane % L * (8 / W) + m;
-          to[(j0 + idx / 2) * CC + ca + idx % 2] = v[m];
-        }
-    };
-    // The same for sums over the warp's channels of values v = j * 4 + s.
-    auto put_bc = [&](int which, int j0, float (&v)[8]) {
-      share_sums<8, 32 / L, L>(v);
-      constexpr int W = 32 / L < 8 ? 32 / L : 8;
-      if (lane / L < W)
-#pragma unroll
-        for (int m = 0; m < 8 / W; ++m) {
-          const int idx = lane / L * (8 / W) + m;
-          bcp[((j0 + idx / 4) * 2 + which) * SP + s0 + idx % 4] = v[m];
-        }
-    };
+    float2 dec[kTile][4], hs[kTile][4];  // decays, and the states before each token
+    {
+      const float4 p = sm.start[i][0][tid], q = sm.start[i][1][tid];
+      h[0] = make_float2(p.x, q.x);
+      h[1] = make_float2(p.y, q.y);
+      h[2] = make_float2(p.z, q.z);
+      h[3] = make_float2(p.w, q.w);
+    }
 #pragma unroll
     for (int j0 = 0; j0 < kTile; j0 += 4) {
       float sv[8], cv[8];
 #pragma unroll
       for (int j = j0; j < j0 + 4; ++j) {
         const int t = i * kTile + j;
-        float2 B[2], C[2];
-        pairs(M::kB, t, B);
-        pairs(M::kC, t, C);
-        const float2 d = chans(M::kD, t), u = chans(M::kU, t), ds = chans(M::kDs, t);
-        float2 dc[2];
+        float2 B[4], C[4];
+        per_state(sm.b[t], B);
+        per_state(sm.c[t], C);
+        const float2 d = chans(sm.d[t]), u = chans(sm.u[t]), ds = chans(sm.ds[t]);
+        float2 sum = both(0.f);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float2 s = both(0.f);
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const float2 w = tc::mul2(both(c ? d.y : d.x), A2[c][p]);
-            dec[j][c][p] = make_float2(ex2(w.x), ex2(w.y));
-            hs[j][c][p] = h[c][p];
-            h[c][p] = tc::fma2(dec[j][c][p], h[c][p], tc::mul2(both(c ? u.y : u.x), B[p]));
-            s = p ? tc::fma2(h[c][p], C[p], s) : tc::mul2(h[c][p], C[p]);
-            dc[p] = c ? tc::fma2(both(ds.y), h[c][p], dc[p]) : tc::mul2(both(ds.x), h[c][p]);
-          }
-          sv[(j - j0) * 2 + c] = s.x + s.y;
+        for (int s = 0; s < 4; ++s) {
+          const float2 w = tc::mul2(d, A2[s]);
+          dec[j][s] = make_float2(ex2(w.x), ex2(w.y));
+          hs[j][s] = h[s];
+          h[s] = tc::fma2(dec[j][s], h[s], tc::mul2(u, B[s]));
+          sum = s ? tc::fma2(h[s], C[s], sum) : tc::mul2(h[s], C[s]);
+          const float2 dc = tc::mul2(ds, h[s]);
+          cv[(j & 1) * 4 + s] = dc.x + dc.y;
         }
-        const int o = (j & 1) * 4;
-        cv[o] = dc[0].x; cv[o + 1] = dc[0].y; cv[o + 2] = dc[1].x; cv[o + 3] = dc[1].y;
+        sv[(j - j0) * 2] = sum.x;
+        sv[(j - j0) * 2 + 1] = sum.y;
         if (j & 1) put_bc(1, j - 1, cv);
       }
-      put_sums(sums, j0, sv);
+      put_sums(sm.sums[0], j0, sv);
     }
 #pragma unroll
     for (int j0 = kTile - 4; j0 >= 0; j0 -= 4) {
@@ -337,106 +466,106 @@ scan_bwd_kernel(const ScanArgs a, const ScanBwdPlan pl, float *__restrict__ ws) 
 #pragma unroll
       for (int j = j0 + 3; j >= j0; --j) {
         const int t = i * kTile + j;
-        float2 B[2], C[2];
-        pairs(M::kB, t, B);
-        pairs(M::kC, t, C);
-        const float2 d = chans(M::kD, t), u = chans(M::kU, t), ds = chans(M::kDs, t);
-        float2 db[2];
+        float2 B[4], C[4];
+        per_state(sm.b[t], B);
+        per_state(sm.c[t], C);
+        const float2 d = chans(sm.d[t]), u = chans(sm.u[t]), ds = chans(sm.ds[t]);
+        float2 q = both(0.f), r = both(0.f);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float2 q = both(0.f), r = both(0.f);
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const float2 g = tc::fma2(both(c ? ds.y : ds.x), C[p], ag[c][p]);
-            ag[c][p] = tc::mul2(dec[j][c][p], g);
-            const float2 gp = tc::mul2(ag[c][p], hs[j][c][p]);  // g e^(delta A) h_before
-            q = p ? tc::fma2(g, B[p], q) : tc::mul2(g, B[p]);
-            r = p ? tc::fma2(gp, A2[c][p], r) : tc::mul2(gp, A2[c][p]);
-            dA[c][p] = tc::fma2(both(c ? d.y : d.x), gp, dA[c][p]);
-            db[p] = c ? tc::fma2(both(u.y), g, db[p]) : tc::mul2(both(u.x), g);
-          }
-          qv[(j - j0) * 2 + c] = q.x + q.y;
-          rv[(j - j0) * 2 + c] = r.x + r.y;
+        for (int s = 0; s < 4; ++s) {
+          const float2 g = tc::fma2(ds, C[s], ag[s]);
+          ag[s] = tc::mul2(dec[j][s], g);
+          const float2 gp = tc::mul2(ag[s], hs[j][s]);  // g e^(delta A) h_before
+          q = s ? tc::fma2(g, B[s], q) : tc::mul2(g, B[s]);
+          r = s ? tc::fma2(gp, A2[s], r) : tc::mul2(gp, A2[s]);
+          dA[s] = tc::fma2(d, gp, dA[s]);
+          const float2 db = tc::mul2(u, g);
+          bv[(j & 1) * 4 + s] = db.x + db.y;
         }
-        const int o = (j & 1) * 4;
-        bv[o] = db[0].x; bv[o + 1] = db[0].y; bv[o + 2] = db[1].x; bv[o + 3] = db[1].y;
+        qv[(j - j0) * 2] = q.x;
+        qv[(j - j0) * 2 + 1] = q.y;
+        rv[(j - j0) * 2] = r.x;
+        rv[(j - j0) * 2 + 1] = r.y;
         if (!(j & 1)) put_bc(0, j, bv);
       }
-      put_sums(sums + kTile * CC, j0, qv);
-      put_sums(sums + 2 * kTile * CC, j0, rv);
+      put_sums(sm.sums[1], j0, qv);
+      put_sums(sm.sums[2], j0, rv);
     }
     __syncthreads();
-    // the channels' outputs
+    // the channels' gradients
 #pragma unroll
-    for (int m = 0; m < kTile * CC / kThreads; ++m) {
-      const int j = tid + m * kThreads, c = j % CC, tt = i * kTile + j / CC, at = t0 + tt;
-      if (c0 + c < Eg && at < live) {
-        const int e = group * Eg + c0 + c;
-        const float xv = to_float(reinterpret_cast<const T *>(a.x)[b * a.sx[0] + at * a.sx[1] + e]);
-        const float d = sm[M::kD + tt * CC + c], ds = sm[M::kDs + tt * CC + c];
-        const float s = sums[j], q = sums[kTile * CC + j], r = sums[2 * kTile * CC + j];
-        const float Dv = a.D ? a.D[e] : 0.f;
-        float ddt = fmaf(xv, q, r * 0.6931471805599453f);
-        if (a.softplus)
-          ddt *= sigmoid(to_float(reinterpret_cast<const T *>(a.dt)[b * a.sdt[0] + at * a.sdt[1] + e]) + (a.bias ? a.bias[e] : 0.f));
-        reinterpret_cast<T *>(a.dx)[b * a.sdx[0] + at * a.sdx[1] + e] = from_float<T>(fmaf(d, q, Dv * ds));
-        reinterpret_cast<T *>(a.ddt)[b * a.sddt[0] + at * a.sddt[1] + e] = from_float<T>(ddt);
-        if (a.z) {
-          const float zv = to_float(reinterpret_cast<const T *>(a.z)[b * a.sz[0] + at * a.sz[1] + e]);
-          const float dyv = to_float(reinterpret_cast<const T *>(a.dy)[b * a.sdy[0] + at * a.sdy[1] + e]);
-          const float sg = sigmoid(zv);
-          reinterpret_cast<T *>(a.dz)[b * a.sdz[0] + at * a.sdz[1] + e] =
-              from_float<T>(dyv * fmaf(Dv, xv, s) * sg * fmaf(zv, 1.f - sg, 1.f));
+    for (int m = 0; m < NW; ++m) {
+      const int j = qt + m * QS, at = t0 + i * kTile + j;
+      if (writes && at < live) {
+        float ddx[4], ddt[4], ddz[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float xv = to_float(xr[m].v[c]), d = sm.d[i * kTile + j][qc + c], ds = sm.ds[i * kTile + j][qc + c];
+          const float s = sm.sums[0][j][qc + c], q = sm.sums[1][j][qc + c], r = sm.sums[2][j][qc + c];
+          ddt[c] = fmaf(xv, q, r * 0.6931471805599453f);  // (r has A log2(e) for A)
+          if (a.softplus) ddt[c] *= sigmoid(to_float(dr[m].v[c]) + bias[c]);
+          ddx[c] = fmaf(d, q, Dv[c] * ds);
+          if (z) {
+            const float zv = to_float(zr[m].v[c]), sg = sigmoid(zv);
+            ddz[c] = to_float(yr[m].v[c]) * fmaf(Dv[c], xv, s) * sg * fmaf(zv, 1.f - sg, 1.f);
+          }
+          if (c < there) {
+            sD[c] = fmaf(ds, xv, sD[c]);
+            sBias[c] += ddt[c];
+          }
         }
-        sD[m % kChans] = fmaf(ds, xv, sD[m % kChans]);
-        sBias[m % kChans] += ddt;
+        store_four<T, kVec>(reinterpret_cast<T *>(a.dx) + b * a.sdx[0] + at * a.sdx[1] + qe, there, ddx);
+        store_four<T, kVec>(reinterpret_cast<T *>(a.ddt) + b * a.sddt[0] + at * a.sddt[1] + qe, there, ddt);
+        if (z) store_four<T, kVec>(reinterpret_cast<T *>(a.dz) + b * a.sdz[0] + at * a.sdz[1] + qe, there, ddz);
       }
     }
     // this block's share of dB and dC
-    for (int j = tid; j < kTile * 2 * SP; j += kThreads) {
-      const int s = j % SP, w = j / SP % 2, at = t0 + i * kTile + j / (2 * SP);
-      const float *p = sm + M::kBc + buf * (kThreads / 32) * kTile * 2 * SP + j;
-      float v = 0.f;
 #pragma unroll
-      for (int m = 0; m < kThreads / 32; ++m) v += p[m * kTile * 2 * SP];
-      if (s < a.S && at < live)
-        ws[pl.bc + ((((size_t)(blk - group * per) * a.B + b) * a.N + at) * a.G + group) * 2 * a.S + w * a.S + s] = v;
+    for (int m = 0; m < (kTile * 2 * SP + kMain - 1) / kMain; ++m) {
+      const int o = tid + m * kMain;
+      if (o < kTile * 2 * SP) {
+        const int s = o % SP, w = o / SP % 2, at = t0 + i * kTile + o / (2 * SP);
+        float v = 0.f;
+#pragma unroll
+        for (int q = 0; q < kMain / 32; ++q) v += (&sm.bc[q][0][0][0])[o];
+        if (s < a.S && at < live)
+          ws[pl.bc + ((((size_t)(blk - group * per) * a.B + b) * a.N + at) * a.G + group) * 2 * a.S + w * a.S + s] = v;
+      }
     }
+    __syncthreads();
   }
+  pdl_launch_dependents();
   // ---- rows past the sequence's end
-  for (int j = tid; j < (t1 - max(live, t0)) * CC; j += kThreads) {
-    const int at = max(live, t0) + j / CC, c = j % CC;
-    if (c0 + c < Eg) {
-      const int e = group * Eg + c0 + c;
-      reinterpret_cast<T *>(a.dx)[b * a.sdx[0] + at * a.sdx[1] + e] = from_float<T>(0.f);
-      reinterpret_cast<T *>(a.ddt)[b * a.sddt[0] + at * a.sddt[1] + e] = from_float<T>(0.f);
-      if (a.z) reinterpret_cast<T *>(a.dz)[b * a.sdz[0] + at * a.sdz[1] + e] = from_float<T>(0.f);
-    }
+  const int end = max(live, t0);
+  const float zero[4] = {};
+  for (int at = end + qt; at < t1; at += QS) {
+    store_four<T, kVec>(reinterpret_cast<T *>(a.dx) + b * a.sdx[0] + at * a.sdx[1] + qe, there, zero);
+    store_four<T, kVec>(reinterpret_cast<T *>(a.ddt) + b * a.sddt[0] + at * a.sddt[1] + qe, there, zero);
+    if (z) store_four<T, kVec>(reinterpret_cast<T *>(a.dz) + b * a.sdz[0] + at * a.sdz[1] + qe, there, zero);
   }
-  for (int j = tid; j < (t1 - max(live, t0)) * 2 * a.S; j += kThreads) {
-    const int at = max(live, t0) + j / (2 * a.S);
+  for (int j = tid; j < (t1 - end) * 2 * a.S; j += kMain) {
+    const int at = end + j / (2 * a.S);
     ws[pl.bc + ((((size_t)(blk - group * per) * a.B + b) * a.N + at) * a.G + group) * 2 * a.S + j % (2 * a.S)] = 0.f;
   }
   // ---- the chunk's sums of dA, dD and dbias
-#pragma unroll
-  for (int c = 0; c < 2; ++c)
-    if (own[c])
-      store_states(ws + (bk * a.E + ech[c]) * a.S, s0, a.S, vec, make_float4(dA[c][0].x, dA[c][0].y, dA[c][1].x, dA[c][1].y));
+  if (own[0]) store_states(ws + (bk * a.E + ech[0]) * a.S, s0, a.S, vec, make_float4(dA[0].x, dA[1].x, dA[2].x, dA[3].x));
+  if (own[1]) store_states(ws + (bk * a.E + ech[1]) * a.S, s0, a.S, vec, make_float4(dA[0].y, dA[1].y, dA[2].y, dA[3].y));
   __syncthreads();
+  float *red = &sm.d[0][0];  // [2][QS][CC]
 #pragma unroll
-  for (int i = 0; i < kChans; ++i) {
-    sm[(i * kThreads + tid) * 2] = sD[i];
-    sm[(i * kThreads + tid) * 2 + 1] = sBias[i];
+  for (int c = 0; c < 4; ++c) {
+    red[qt * CC + qc + c] = sD[c];
+    red[(QS + qt) * CC + qc + c] = sBias[c];
   }
   __syncthreads();
-  for (int c = tid; c < CC; c += kThreads)
+  for (int c = tid; c < CC; c += kMain)
     if (c0 + c < Eg) {
       const int e = group * Eg + c0 + c;
       float v0 = 0.f, v1 = 0.f;
-      // (threads c, c + CC, .. had this channel; with CC > kThreads one had it alone)
-      for (int j = c; j < kThreads * kChans; j += CC) {
-        v0 += sm[j * 2];
-        v1 += sm[j * 2 + 1];
+#pragma unroll 4
+      for (int j = 0; j < QS; ++j) {
+        v0 += red[j * CC + c];
+        v1 += red[(QS + j) * CC + c];
       }
       ws[pl.dd + bk * a.E + e] = v0;
       ws[pl.dd + ((size_t)pl.chunks * a.B + bk) * a.E + e] = v1;
@@ -459,13 +588,55 @@ scan_bwd_bc_kernel(const ScanArgs a, const ScanBwdPlan pl, const float *__restri
   out[row * a.S + (j < a.S ? j : j - a.S)] = from_float<T>(v);
 }
 
-template <typename F>
-cudaError_t by_lanes(int S, F f) {
-  if (S <= 4) return f(std::integral_constant<int, 1>());
-  if (S <= 8) return f(std::integral_constant<int, 2>());
-  if (S <= 16) return f(std::integral_constant<int, 4>());
-  if (S <= 32) return f(std::integral_constant<int, 8>());
-  return f(std::integral_constant<int, 16>());
+// Vectors of `step` channels in every tensor?
+bool vectors_ok(const ScanArgs &a, int esz, int step, bool outputs) {
+  return a.E / a.G % step == 0 && rows_on(a, a.x, a.sx, step, esz) && rows_on(a, a.dt, a.sdt, step, esz) &&
+         rows_on(a, a.dy, a.sdy, step, esz) && rows_on(a, a.z, a.sz, step, esz) &&
+         (!outputs || (rows_on(a, a.dx, a.sdx, step, esz) && rows_on(a, a.ddt, a.sddt, step, esz) &&
+                       (!a.z || rows_on(a, a.dz, a.sdz, step, esz))));
+}
+
+// Chunks that a CTA of the first pass takes one after another: up to 8, so
+// that its loads run ahead, while all SMs keep two CTAs.
+template <typename T, int L, bool kPair>
+cudaError_t chunks_with(const ScanArgs &a, const ScanBwdPlan &pl, float *ws, cudaStream_t st) {
+  static std::atomic<unsigned> done{0};
+  auto kern = scan_bwd_chunks_kernel<T, L, kPair>;
+  const cudaError_t e = allow_big_smem(reinterpret_cast<const void *>(kern), done);
+  if (e != cudaSuccess) return e;
+  const long long blocks = (long long)a.G * Block<L>::per_group(a.E, a.G);
+  int run = 8;
+  while (run > 1 && blocks * a.B * ((pl.chunks + run - 1) / run) < 4LL * device_sms()) run /= 2;
+  const dim3 grid((unsigned)(blocks * ((pl.chunks + run - 1) / run)), a.B);
+  return launch_k(kern, grid, dim3(kThreads), sizeof(ChunksSmem<L>), st, true, a, pl, run, ws);
+}
+
+template <typename T, int L, bool kVec>
+cudaError_t main_with(const ScanArgs &a, const ScanBwdPlan &pl, float *ws, cudaStream_t st) {
+  static std::atomic<unsigned> done{0};
+  auto kern = scan_bwd_kernel<T, L, kVec>;
+  const cudaError_t e = allow_big_smem(reinterpret_cast<const void *>(kern), done);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)(a.G * pl.blocks) * pl.chunks, a.B);
+  return launch_k(kern, grid, dim3(kMain), sizeof(MainSmem<L>), st, true, a, pl, ws);
+}
+
+template <typename T>
+cudaError_t chunks_any(const ScanArgs &a, const ScanBwdPlan &pl, float *ws, cudaStream_t st) {
+  const bool pair = vectors_ok(a, sizeof(T), 2, false);
+  return by_lanes(a.S, [&](auto l) {
+    constexpr int L = decltype(l)::value;
+    return pair ? chunks_with<T, L, true>(a, pl, ws, st) : chunks_with<T, L, false>(a, pl, ws, st);
+  });
+}
+
+template <typename T>
+cudaError_t main_any(const ScanArgs &a, const ScanBwdPlan &pl, float *ws, cudaStream_t st) {
+  const bool vec = vectors_ok(a, sizeof(T), 4, true);
+  return by_lanes(a.S, [&](auto l) {
+    constexpr int L = decltype(l)::value;
+    return vec ? main_with<T, L, true>(a, pl, ws, st) : main_with<T, L, false>(a, pl, ws, st);
+  });
 }
 
 }  // namespace
@@ -490,13 +661,7 @@ ScanBwdPlan scan_bwd_plan(const ScanArgs &a) {
 }
 
 cudaError_t launch_scan_bwd_chunks(const ScanArgs &a, int bf16, const ScanBwdPlan &pl, float *ws, cudaStream_t st) {
-  return by_lanes(a.S, [&](auto l) {
-    constexpr int L = decltype(l)::value, CC = kThreads / L;
-    const int blocks = a.G * ((a.E / a.G + CC - 1) / CC);
-    const dim3 grid((unsigned)blocks * pl.chunks, a.B);
-    return bf16 ? launch_k(scan_bwd_chunks_kernel<__nv_bfloat16, L>, grid, dim3(kThreads), 0, st, true, a, pl, ws)
-                : launch_k(scan_bwd_chunks_kernel<float, L>, grid, dim3(kThreads), 0, st, true, a, pl, ws);
-  });
+  return bf16 ? chunks_any<__nv_bfloat16>(a, pl, ws, st) : chunks_any<float>(a, pl, ws, st);
 }
 
 cudaError_t launch_scan_bwd_carry(const ScanArgs &a, const ScanBwdPlan &pl, float *ws, cudaStream_t st) {
@@ -504,21 +669,8 @@ cudaError_t launch_scan_bwd_carry(const ScanArgs &a, const ScanBwdPlan &pl, floa
   return launch_k(scan_bwd_carry_kernel, dim3((unsigned)((n + 255) / 256), 2), dim3(256), 0, st, true, a, pl, ws);
 }
 
-template <typename T, int L>
-static cudaError_t bwd_with(const ScanArgs &a, const ScanBwdPlan &pl, float *ws, cudaStream_t st) {
-  static std::atomic<unsigned> done{0};
-  auto kern = scan_bwd_kernel<T, L>;
-  const cudaError_t e = allow_big_smem(reinterpret_cast<const void *>(kern), done);
-  if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)(a.G * pl.blocks) * pl.chunks, a.B);
-  return launch_k(kern, grid, dim3(kThreads), BwdSmem<T, L>::kFloats * sizeof(float), st, true, a, pl, ws);
-}
-
 cudaError_t launch_scan_bwd(const ScanArgs &a, int bf16, const ScanBwdPlan &pl, float *ws, cudaStream_t st) {
-  return by_lanes(a.S, [&](auto l) {
-    constexpr int L = decltype(l)::value;
-    return bf16 ? bwd_with<__nv_bfloat16, L>(a, pl, ws, st) : bwd_with<float, L>(a, pl, ws, st);
-  });
+  return bf16 ? main_any<__nv_bfloat16>(a, pl, ws, st) : main_any<float>(a, pl, ws, st);
 }
 
 cudaError_t launch_scan_bwd_bc(const ScanArgs &a, int bf16, const ScanBwdPlan &pl, const float *ws, cudaStream_t st) {

@@ -20,59 +20,104 @@ namespace {
 
 using namespace scan;
 
-constexpr int kThreads = 128;
-constexpr int kTile = 16;  // tokens at a time
-
-// Channels of a CTA; grid.x counts the blocks of all groups.
 template <int L>
-struct Block {
-  static constexpr int kChannels = kThreads / L;
-  static __host__ __device__ int per_group(int E, int G) { return (E / G + kChannels - 1) / kChannels; }
+struct FwdSmem {
+  float4 du[2][Block<L>::kTile][Block<L>::kChannels];  // delta, delta, u, u
+  float bm[2][Block<L>::kTile][Block<L>::SP], cm[2][Block<L>::kTile][Block<L>::SP];
+  float ysum[2][Block<L>::kTile][Block<L>::kChannels];
 };
 
+// Half of the CTA's warps walk the recurrence; the others load the tokens two
+// tiles ahead, work out step sizes and inputs, and finish the outputs of the
+// tile before: with one sequence an SM has no more than one recurrence warp a
+// scheduler, and everything else that a token needs runs beside it.
 // kStates: only the states that the segments leave behind.
-template <typename T, int L, bool kStates>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, int L, bool kStates, bool kPair>
+__global__ void __launch_bounds__(kThreads, 2)
 scan_fwd_kernel(const ScanArgs a, const ScanSegs seg) {
-  constexpr int CC = Block<L>::kChannels, NE = kTile / L, SP = 4 * L, NB = (kTile * SP + kThreads - 1) / kThreads;
-  __shared__ __align__(16) float2 du[2][kTile][CC];
-  __shared__ __align__(16) float bm[2][kTile][SP], cm[kStates ? 1 : 2][kTile][SP];
-  __shared__ float ysum[kStates ? 1 : 2][kTile][CC];
-  pdl_launch_dependents();
+  using K = Block<L>;
+  constexpr int CC = K::kChannels, TT = K::kTile, SP = K::SP;
+  extern __shared__ __align__(16) uint8_t dyn[];
+  FwdSmem<L> &sm = *reinterpret_cast<FwdSmem<L> *>(dyn);
   pdl_wait();
-  const int tid = threadIdx.x, per = Block<L>::per_group(a.E, a.G), Eg = a.E / a.G;
+  const int per = K::per_group(a.E, a.G), Eg = a.E / a.G;
   const int group = blockIdx.x / per, c0 = (blockIdx.x - group * per) * CC;  // within the group
   const int b = blockIdx.z, k = blockIdx.y;
   const int n = tokens_of(a, b), t0 = k * seg.len, t1 = min(a.N, t0 + seg.len), live = min(t1, n);
+  const int tiles = live > t0 ? (live - t0 + TT - 1) / TT : 0;
 
-  // As owner of four states of a channel ...
-  const int ci = tid / L, s0 = tid % L * 4;
-  const bool own = c0 + ci < Eg;
-  const int e = group * Eg + min(c0 + ci, Eg - 1);
-  const bool vec = a.S % 4 == 0;
-  float4 A4 = load_states(a.A + (size_t)e * a.S, s0, a.S, vec && reinterpret_cast<uintptr_t>(a.A) % 16 == 0);
-  const float2 A01 = make_float2(A4.x * kLog2e, A4.y * kLog2e), A23 = make_float2(A4.z * kLog2e, A4.w * kLog2e);
-  float2 h01 = both(0.f), h23 = both(0.f);
-  const size_t row = ((size_t)b * a.E + e) * a.S;
-  if (!kStates) {
-    // the state that the segments before this one leave behind
-    if (a.h_in) {
-      const float4 h = load_states(a.h_in + row, s0, a.S, vec && reinterpret_cast<uintptr_t>(a.h_in) % 16 == 0);
-      h01 = make_float2(h.x, h.y);
-      h23 = make_float2(h.z, h.w);
+  if (threadIdx.x < kScan) {
+    // ---- four states of a channel
+    const int tid = threadIdx.x, ci = tid / L, s0 = tid % L * 4;
+    const bool own = c0 + ci < Eg, vec = a.S % 4 == 0;
+    const int e = group * Eg + min(c0 + ci, Eg - 1);
+    const float4 A4 = load_states(a.A + (size_t)e * a.S, s0, a.S, vec && reinterpret_cast<uintptr_t>(a.A) % 16 == 0);
+    const float2 A01 = make_float2(A4.x * kLog2e, A4.y * kLog2e), A23 = make_float2(A4.z * kLog2e, A4.w * kLog2e);
+    float2 h01 = both(0.f), h23 = both(0.f);
+    const size_t row = ((size_t)b * a.E + e) * a.S;
+    if (!kStates) {
+      // the state that the segments before this one leave behind
+      if (a.h_in) {
+        const float4 h = load_states(a.h_in + row, s0, a.S, vec && reinterpret_cast<uintptr_t>(a.h_in) % 16 == 0);
+        h01 = make_float2(h.x, h.y);
+        h23 = make_float2(h.z, h.w);
+      }
+      for (int i = 0; i < k; ++i) {
+        const float2 d = both(seg.sum[((size_t)i * a.B + b) * a.E + e]);
+        const float4 l = load_states(seg.loc + (size_t)i * a.B * a.E * a.S + row, s0, a.S, vec);
+        const float2 w01 = tc::mul2(d, A01), w23 = tc::mul2(d, A23);
+        h01 = tc::fma2(make_float2(ex2(w01.x), ex2(w01.y)), h01, make_float2(l.x, l.y));
+        h23 = tc::fma2(make_float2(ex2(w23.x), ex2(w23.y)), h23, make_float2(l.z, l.w));
+      }
     }
-    for (int i = 0; i < k; ++i) {
-      const float2 d = both(seg.sum[((size_t)i * a.B + b) * a.E + e]);
-      const float4 l = load_states(seg.loc + (size_t)i * a.B * a.E * a.S + row, s0, a.S, vec);
-      const float2 w01 = tc::mul2(d, A01), w23 = tc::mul2(d, A23);
-      h01 = tc::fma2(make_float2(ex2(w01.x), ex2(w01.y)), h01, make_float2(l.x, l.y));
-      h23 = tc::fma2(make_float2(ex2(w23.x), ex2(w23.y)), h23, make_float2(l.z, l.w));
+    __syncthreads();
+    for (int i = 0; i < tiles; ++i) {
+      const int buf = i & 1;
+#pragma unroll
+      for (int q = 0; q < TT; q += 4) {
+        float yq[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 v = sm.du[buf][q + j][ci];
+          const float4 B4 = *reinterpret_cast<const float4 *>(&sm.bm[buf][q + j][s0]);
+          const float2 dd = make_float2(v.x, v.y), uu = make_float2(v.z, v.w);
+          const float2 w01 = tc::mul2(dd, A01), w23 = tc::mul2(dd, A23);
+          const float2 i01 = tc::mul2(uu, make_float2(B4.x, B4.y)), i23 = tc::mul2(uu, make_float2(B4.z, B4.w));
+          h01 = tc::fma2(make_float2(ex2(w01.x), ex2(w01.y)), h01, i01);
+          h23 = tc::fma2(make_float2(ex2(w23.x), ex2(w23.y)), h23, i23);
+          if (!kStates) {
+            const float4 C4 = *reinterpret_cast<const float4 *>(&sm.cm[buf][q + j][s0]);
+            const float2 s = tc::fma2(h23, make_float2(C4.z, C4.w), tc::mul2(h01, make_float2(C4.x, C4.y)));
+            yq[j] = s.x + s.y;
+          }
+        }
+        if (!kStates) {
+          share_sums<4, L>(yq);
+          constexpr int M = L < 4 ? L : 4;
+          if (tid % L < M)
+#pragma unroll
+            for (int j = 0; j < 4 / M; ++j) sm.ysum[buf][q + tid % M * (4 / M) + j][ci] = yq[j];
+        }
+      }
+      __syncthreads();
     }
+    pdl_launch_dependents();
+    const float4 h4 = make_float4(h01.x, h01.y, h23.x, h23.y);
+    if (kStates) {
+      if (own) store_states(seg.loc + (size_t)k * a.B * a.E * a.S + row, s0, a.S, vec, h4);
+    } else if (k == seg.count - 1 && own && a.h_out) {
+      store_states(a.h_out + row, s0, a.S, vec && reinterpret_cast<uintptr_t>(a.h_out) % 16 == 0, h4);
+    }
+    if (kStates) __syncthreads();
+    return;
   }
 
-  // ... and as loader of one channel's tokens, NE of each tile.
-  const int lc = tid % CC, lt = tid / CC;
-  const bool there = c0 + lc < Eg;
+  // ---- two channels' tokens, NP of each tile
+  constexpr int NP = TT * CC / 2 / kLoad, TS = 2 * kLoad / CC;  // pairs a thread; tokens between them
+  constexpr int NB = (TT * SP + kLoad - 1) / kLoad;
+  static_assert(NP * kLoad * 2 == TT * CC && NP * TS == TT, "whole tiles");
+  const int tid = threadIdx.x - kScan, lc = tid % (CC / 2) * 2, lt = tid / (CC / 2);
+  const int there = min(2, max(0, Eg - c0 - lc));  // channels of this pair
   const int le = group * Eg + min(c0 + lc, Eg - 1);
   const T *x = reinterpret_cast<const T *>(a.x) + b * a.sx[0] + le;
   const T *dt = reinterpret_cast<const T *>(a.dt) + b * a.sdt[0] + le;
@@ -80,131 +125,124 @@ scan_fwd_kernel(const ScanArgs a, const ScanSegs seg) {
   const T *Bp = reinterpret_cast<const T *>(a.Bm) + b * a.sB[0] + group * a.sB[2];
   const T *Cp = reinterpret_cast<const T *>(a.Cm) + b * a.sC[0] + group * a.sC[2];
   T *y = reinterpret_cast<T *>(a.y) + b * a.sy[0] + le;
-  const float bias = a.bias ? a.bias[le] : 0.f, Dv = !kStates && a.D ? a.D[le] : 0.f;
-  T xn[NE], dn[NE], zn[NE], bn[NB], cn[NB];
-  float xc[NE], zc[NE];
-  float dsum = 0.f;
+  const int l1 = there > 1;
+  const float bias[2] = {a.bias ? a.bias[le] : 0.f, a.bias ? a.bias[le + l1] : 0.f};
+  const float Dv[2] = {!kStates && a.D ? a.D[le] : 0.f, !kStates && a.D ? a.D[le + l1] : 0.f};
+  float dsum[2] = {0.f, 0.f};
 
-  auto load = [&](int t) {
+  struct Raw {
+    Two<T> x[NP], z[NP], d[NP];
+    T B[NB], C[NB];
+  };
+  struct Kept {
+    Two<T> x[NP], z[NP];
+  };
+  auto load = [&](int i, Raw &r) {
+    if (i >= tiles) return;
+    const int t = t0 + i * TT;
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      const int at = t + lt + i * L;
-      const bool in = there && at < live;
-      xn[i] = in ? x[at * a.sx[1]] : from_float<T>(0.f);
-      dn[i] = in ? dt[at * a.sdt[1]] : from_float<T>(0.f);
-      if (!kStates) zn[i] = z && in ? z[at * a.sz[1]] : from_float<T>(0.f);
+    for (int j = 0; j < NP; ++j) {
+      const int at = t + lt + j * TS, m = at < live ? there : 0;
+      r.x[j] = load_two<T, kPair>(x + at * a.sx[1], m);
+      r.d[j] = load_two<T, kPair>(dt + at * a.sdt[1], m);
+      if (!kStates) r.z[j] = load_two<T, kPair>(z + at * a.sz[1], z ? m : 0);
     }
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const int j = tid + i * kThreads, at = t + j / SP, s = j % SP;
-      const bool in = (NB * kThreads == kTile * SP || j < kTile * SP) && at < live && s < a.S;
-      bn[i] = in ? Bp[at * a.sB[1] + s] : from_float<T>(0.f);
-      if (!kStates) cn[i] = in ? Cp[at * a.sC[1] + s] : from_float<T>(0.f);
+    for (int j = 0; j < NB; ++j) {
+      const int o = tid + j * kLoad, at = t + o / SP, s = o % SP;
+      const bool in = (NB * kLoad == TT * SP || o < TT * SP) && at < live && s < a.S;
+      r.B[j] = in ? Bp[at * a.sB[1] + s] : from_float<T>(0.f);
+      if (!kStates) r.C[j] = in ? Cp[at * a.sC[1] + s] : from_float<T>(0.f);
     }
   };
-  // What was loaded for the tile at t becomes delta, u, B and C; past the end
-  // delta and u are 0 and leave the state as it is.
-  auto put = [&](int t, int buf) {
-    float part = 0.f;
+  // What was loaded for tile i becomes delta, u, B and C; past the end delta and
+  // u are 0 and leave the state as it is.
+  auto put = [&](int i, const Raw &r) {
+    const int buf = i & 1, t = t0 + i * TT;
+    float part[2] = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      const int at = lt + i * L;
-      float d = to_float(dn[i]) + bias;
-      if (a.softplus) d = softplus(d);
-      if (!(there && t + at < live)) d = 0.f;
-      const float xf = to_float(xn[i]);
-      du[buf][at][lc] = make_float2(d, d * xf);
-      if (kStates) part += d;
-      if (!kStates) {
-        xc[i] = xf;
-        zc[i] = to_float(zn[i]);
+    for (int j = 0; j < NP; ++j) {
+      const int at = lt + j * TS;
+      const float xs[2] = {to_float(r.x[j].a), to_float(r.x[j].b)};
+      float d[2] = {to_float(r.d[j].a) + bias[0], to_float(r.d[j].b) + bias[1]};
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        if (a.softplus) d[c] = softplus(d[c]);
+        if (!(c < there && t + at < live)) d[c] = 0.f;
+        const float u = d[c] * xs[c];
+        sm.du[buf][at][lc + c] = make_float4(d[c], d[c], u, u);
+        if (kStates) part[c] += d[c];
       }
     }
-    dsum += part;
+    if (kStates) {
+      dsum[0] += part[0];
+      dsum[1] += part[1];
+    }
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const int j = tid + i * kThreads;
-      if (NB * kThreads == kTile * SP || j < kTile * SP) {
-        (&bm[buf][0][0])[j] = to_float(bn[i]);
-        if (!kStates) (&cm[buf][0][0])[j] = to_float(cn[i]);
+    for (int j = 0; j < NB; ++j) {
+      const int o = tid + j * kLoad;
+      if (NB * kLoad == TT * SP || o < TT * SP) {
+        (&sm.bm[buf][0][0])[o] = to_float(r.B[j]);
+        if (!kStates) (&sm.cm[buf][0][0])[o] = to_float(r.C[j]);
       }
     }
   };
+  auto finish = [&](int i, const Kept &r) {
+    const int buf = i & 1, t = t0 + i * TT;
+#pragma unroll
+    for (int j = 0; j < (kStates ? 0 : NP); ++j) {
+      const int at = lt + j * TS;
+      const float2 s = *reinterpret_cast<const float2 *>(&sm.ysum[buf][at][lc]);
+      float v0 = fmaf(Dv[0], to_float(r.x[j].a), s.x), v1 = fmaf(Dv[1], to_float(r.x[j].b), s.y);
+      if (z) {
+        v0 *= silu(to_float(r.z[j].a));
+        v1 *= silu(to_float(r.z[j].b));
+      }
+      const bool in = t + at < live;
+      if (t + at < t1) store_two<T, kPair>(y + (t + at) * a.sy[1], there, in ? v0 : 0.f, in ? v1 : 0.f);
+    }
+  };
+  auto keep = [&](const Raw &r, Kept &q) {
+#pragma unroll
+    for (int j = 0; j < (kStates ? 0 : NP); ++j) {
+      q.x[j] = r.x[j];
+      q.z[j] = r.z[j];
+    }
+  };
 
-  float xo[NE], zo[NE];
-  int buf = 0;
-  load(t0);
-  put(t0, 0);
+  Raw next, after;
+  Kept cur, done;
+  load(0, next);
+  load(1, after);
+  if (tiles > 0) put(0, next);
+  keep(next, cur);
+  next = after;
   __syncthreads();
-  for (int t = t0; t < live; t += kTile, buf ^= 1) {
-#pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      xo[i] = xc[i];
-      zo[i] = zc[i];
-    }
-    const bool more = t + kTile < live;
-    if (more) load(t + kTile);
-#pragma unroll
-    for (int q = 0; q < kTile; q += 4) {
-      float yq[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 v = du[buf][q + j][ci];
-        const float4 B4 = *reinterpret_cast<const float4 *>(&bm[buf][q + j][s0]);
-        const float2 dd = both(v.x), uu = both(v.y);
-        const float2 w01 = tc::mul2(dd, A01), w23 = tc::mul2(dd, A23);
-        const float2 i01 = tc::mul2(uu, make_float2(B4.x, B4.y)), i23 = tc::mul2(uu, make_float2(B4.z, B4.w));
-        h01 = tc::fma2(make_float2(ex2(w01.x), ex2(w01.y)), h01, i01);
-        h23 = tc::fma2(make_float2(ex2(w23.x), ex2(w23.y)), h23, i23);
-        if (!kStates) {
-          const float4 C4 = *reinterpret_cast<const float4 *>(&cm[buf][q + j][s0]);
-          const float2 s = tc::fma2(h23, make_float2(C4.z, C4.w), tc::mul2(h01, make_float2(C4.x, C4.y)));
-          yq[j] = s.x + s.y;
-        }
-      }
-      if (!kStates) {
-        share_sums<4, L>(yq);
-        constexpr int M = L < 4 ? L : 4;
-#pragma unroll
-        for (int j = 0; j < 4 / M; ++j)
-          if (tid % L < M) ysum[buf][q + tid % M * (4 / M) + j][ci] = yq[j];
-      }
-    }
-    if (more) put(t + kTile, buf ^ 1);
+  for (int i = 0; i < tiles; ++i) {
+    load(i + 2, after);
+    if (i > 0) finish(i - 1, done);
+    if (i + 1 < tiles) put(i + 1, next);
     __syncthreads();
-    if (!kStates) {
-#pragma unroll
-      for (int i = 0; i < NE; ++i) {
-        const int at = t + lt + i * L;
-        if (there && at < t1) {
-          float v = fmaf(Dv, xo[i], ysum[buf][lt + i * L][lc]);
-          if (z) v *= silu(zo[i]);
-          y[at * a.sy[1]] = from_float<T>(at < live ? v : 0.f);
-        }
-      }
-    }
+    done = cur;
+    keep(next, cur);
+    next = after;
   }
+  if (tiles > 0) finish(tiles - 1, done);
+  pdl_launch_dependents();
   if (!kStates) {  // whole tiles past the sequence's end
-    const int done = live > t0 ? t0 + (live - t0 + kTile - 1) / kTile * kTile : t0;
-    for (int at = done + lt; at < t1; at += L)
-      if (there) y[at * a.sy[1]] = from_float<T>(0.f);
-  }
-  if (kStates) {
-    if (own) store_states(seg.loc + (size_t)k * a.B * a.E * a.S + row, s0, a.S, vec, make_float4(h01.x, h01.y, h23.x, h23.y));
-    // the loaders' sums of a channel, in order
+    for (int at = t0 + tiles * TT + lt; at < t1; at += TS) store_two<T, kPair>(y + at * a.sy[1], there, 0.f, 0.f);
+  } else {
+    // the loaders' sums of a channel, in order (the walk over the tiles is over)
+    float *red = &sm.ysum[0][0][0];
+    red[lt * CC + lc] = dsum[0];
+    red[lt * CC + lc + 1] = dsum[1];
     __syncthreads();
-    float *red = reinterpret_cast<float *>(&du[0][0][0]);
-    red[lt * CC + lc] = dsum;
-    __syncthreads();
-    if (tid < CC && there) {
+    if (tid < CC && c0 + tid < Eg) {
       float s = 0.f;
 #pragma unroll
-      for (int i = 0; i < L; ++i) s += red[i * CC + tid];
-      seg.sum[((size_t)k * a.B + b) * a.E + le] = s;
+      for (int i = 0; i < TS; ++i) s += red[i * CC + tid];
+      seg.sum[((size_t)k * a.B + b) * a.E + group * Eg + c0 + tid] = s;
     }
-  } else if (k == seg.count - 1 && own && a.h_out) {
-    store_states(a.h_out + row, s0, a.S, vec && reinterpret_cast<uintptr_t>(a.h_out) % 16 == 0,
-                 make_float4(h01.x, h01.y, h23.x, h23.y));
   }
 }
 
@@ -263,30 +301,29 @@ scan_step_kernel(const ScanArgs a) {
   }
 }
 
-// Lanes a channel: four states a lane.
-int lanes_of(int S) {
-  int L = 1;
-  while (4 * L < S) L *= 2;
-  return L;
+// Pairs of channels are read and written at once where every row of every
+// tensor (and every block of channels) begins on a pair's boundary.
+bool pairs_ok(const ScanArgs &a, int esz, bool states) {
+  return a.E / a.G % 2 == 0 && rows_on(a, a.x, a.sx, 2, esz) && rows_on(a, a.dt, a.sdt, 2, esz) &&
+         (states || (rows_on(a, a.z, a.sz, 2, esz) && rows_on(a, a.y, a.sy, 2, esz)));
 }
 
-template <typename F>
-cudaError_t by_lanes(int S, F f) {
-  switch (lanes_of(S)) {
-    case 1: return f(std::integral_constant<int, 1>());
-    case 2: return f(std::integral_constant<int, 2>());
-    case 4: return f(std::integral_constant<int, 4>());
-    case 8: return f(std::integral_constant<int, 8>());
-    default: return f(std::integral_constant<int, 16>());
-  }
+template <typename T, int L, bool kStates, bool kPair>
+cudaError_t scan_with(const ScanArgs &a, const ScanSegs &seg, int segs, cudaStream_t st) {
+  static std::atomic<unsigned> done{0};
+  auto kern = scan_fwd_kernel<T, L, kStates, kPair>;
+  const cudaError_t e = allow_big_smem(reinterpret_cast<const void *>(kern), done);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(a.G * Block<L>::per_group(a.E, a.G), segs, a.B);
+  return launch_k(kern, grid, dim3(kThreads), sizeof(FwdSmem<L>), st, true, a, seg);
 }
 
 template <typename T, bool kStates>
 cudaError_t scan_any(const ScanArgs &a, const ScanSegs &seg, int segs, cudaStream_t st) {
   return by_lanes(a.S, [&](auto l) {
     constexpr int L = decltype(l)::value;
-    const dim3 grid(a.G * Block<L>::per_group(a.E, a.G), segs, a.B);
-    return launch_k(scan_fwd_kernel<T, L, kStates>, grid, dim3(kThreads), 0, st, true, a, seg);
+    return pairs_ok(a, sizeof(T), kStates) ? scan_with<T, L, kStates, true>(a, seg, segs, st)
+                                           : scan_with<T, L, kStates, false>(a, seg, segs, st);
   });
 }
 
@@ -303,9 +340,24 @@ cudaError_t step_any(const ScanArgs &a, cudaStream_t st) {
 
 }  // namespace
 
+// Segments only where a sequence's channels leave most SMs without a CTA: the
+// exponentials of all but the last segment are then taken twice.
 ScanSegs scan_fwd_plan(const ScanArgs &a) {
   ScanSegs s;
   s.len = std::max(a.N, 1);
+  int tile = 1;
+  long long ctas = 1;
+  by_lanes(a.S, [&](auto l) {
+    constexpr int L = decltype(l)::value;
+    tile = Block<L>::kTile;
+    ctas = (long long)a.G * Block<L>::per_group(a.E, a.G) * a.B;
+    return cudaSuccess;
+  });
+  const int sms = device_sms();
+  if (ctas * 2 > sms || a.N < 8 * tile) return s;
+  const long long want = std::min<long long>(2 * sms / std::max(ctas, 1LL), a.N / (4 * tile));
+  s.len = (int)((a.N + want - 1) / want + tile - 1) / tile * tile;
+  s.count = (a.N + s.len - 1) / s.len;
   return s;
 }
 
