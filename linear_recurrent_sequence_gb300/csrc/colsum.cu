@@ -9,12 +9,12 @@ namespace ret {
 
 namespace {
 
-// V columns a thread, 32 V a CTA, a warp for every 32nd part, four of whose
-// rows are on their way at once.
-template <int V>
-__global__ void __launch_bounds__(1024)
+// V columns a thread, 32 V a CTA, every P-th part a thread, eight of them on
+// their way at once.
+template <int V, int P>
+__global__ void __launch_bounds__(32 * P)
 colsum_kernel(const ColSum s) {
-  __shared__ float red[V][32][33];
+  __shared__ float red[V][P][33];
   pdl_launch_dependents();
   pdl_wait();
   const int w = blockIdx.y, cols = s.cols[w];
@@ -27,8 +27,8 @@ colsum_kernel(const ColSum s) {
   if (c < cols) {
     const float *from = s.part[w] + c;
     const long long stride = s.stride[w];
-#pragma unroll 4
-    for (int p = py; p < s.count; p += 32) {
+#pragma unroll 8
+    for (int p = py; p < s.count; p += P) {
       if constexpr (V == 4) {
         const float4 f = *reinterpret_cast<const float4 *>(from + p * stride);
         v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
@@ -40,11 +40,12 @@ colsum_kernel(const ColSum s) {
 #pragma unroll
   for (int j = 0; j < V; ++j) red[j][py][cx] = v[j];
   __syncthreads();
-  const int co = (blockIdx.x * 32 + py) * V;
+  for (int i = threadIdx.x; i < 32 * V; i += 32 * P) {
+    const int col = blockIdx.x * 32 * V + i;
+    float t = 0.f;
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const float t = warp_sum(red[j][cx][py]);
-    if (cx == 0 && co + j < cols) out[co + j] = t;
+    for (int p = 0; p < P; ++p) t += red[i % V][p][i / V];
+    if (col < cols) out[col] = t;
   }
 }
 
@@ -61,9 +62,11 @@ cudaError_t launch_colsum(const ColSum &s, cudaStream_t st) {
   bool vec = true;  // 16-byte vectors of columns
   for (int i = 0; i < n; ++i)
     vec = vec && (!s.out[i] || (s.cols[i] % 4 == 0 && s.stride[i] % 4 == 0 && reinterpret_cast<uintptr_t>(s.part[i]) % 16 == 0));
-  if (vec && most >= 4096)
-    return launch_k(colsum_kernel<4>, dim3((most + 127) / 128, n), dim3(1024), 0, st, true, s);
-  return launch_k(colsum_kernel<1>, dim3((most + 31) / 32, n), dim3(1024), 0, st, true, s);
+  // Many columns fill the SMs with 8 parts at a time, few need 32 (16384 columns
+  // and more: vectors, where they are there).
+  if (most < 16384) return launch_k(colsum_kernel<1, 32>, dim3((most + 31) / 32, n), dim3(1024), 0, st, true, s);
+  if (vec) return launch_k(colsum_kernel<4, 8>, dim3((most + 127) / 128, n), dim3(256), 0, st, true, s);
+  return launch_k(colsum_kernel<1, 8>, dim3((most + 31) / 32, n), dim3(256), 0, st, true, s);
 }
 
 }  // namespace ret

@@ -8,6 +8,7 @@
 // inputs in registers, so that each input is read once, but for the W - 1
 // tokens at the ends of a run.
 #include <algorithm>
+#include <type_traits>
 
 #include "launch.h"
 #include "scan.cuh"
@@ -20,35 +21,32 @@ using namespace scan;
 
 constexpr int kThreads = 256;
 
-// V neighbouring channels (16 bytes, 8 bytes or one value).
+// V neighbouring channels as they were read: 4, 2 or 1.
 template <typename T, int V>
-struct Chans {
-  __device__ __forceinline__ static void load(const T *p, float (&f)[V]) {
-    if constexpr (V == 1) {
-      f[0] = to_float(*p);
-    } else if constexpr (sizeof(T) * V == 16) {
-      Elems<T, V> e;
-      e.load(p);
-      e.get(f);
-    } else {
-      const uint2 r = *reinterpret_cast<const uint2 *>(p);
-      f[0] = __uint_as_float(r.x << 16);
-      f[1] = __uint_as_float(r.x & 0xffff0000u);
-      f[2] = __uint_as_float(r.y << 16);
-      f[3] = __uint_as_float(r.y & 0xffff0000u);
-    }
+struct __align__(V * sizeof(T)) Chans {
+  T v[V];
+  __device__ __forceinline__ void load(const T *p) {
+    if constexpr (V == 1)
+      v[0] = *p;
+    else if constexpr (V * sizeof(T) == 4)
+      *reinterpret_cast<uint32_t *>(v) = *reinterpret_cast<const uint32_t *>(p);
+    else if constexpr (V * sizeof(T) == 8)
+      *reinterpret_cast<uint2 *>(v) = *reinterpret_cast<const uint2 *>(p);
+    else
+      *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(p);
   }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = from_float<T>(0.f);
+  }
+  __device__ __forceinline__ float get(int i) const { return to_float(v[i]); }
   __device__ __forceinline__ static void store(T *p, const float (&f)[V]) {
-    if constexpr (V == 1) {
+    if constexpr (V == 1)
       *p = from_float<T>(f[0]);
-    } else if constexpr (sizeof(T) * V == 16) {
-      Elems<T, V> e;
-      e.set(f);
-      e.store(p);
-    } else {
-      const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
-      *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
-    }
+    else if constexpr (V == 2)
+      store_two<T, true>(p, 2, f[0], f[1]);
+    else
+      store_four<T, true>(p, 4, f);
   }
 };
 
@@ -59,35 +57,50 @@ __device__ __forceinline__ int conv_tokens(const ConvArgs &a, int b) {
   return (int)(n < 0 ? 0 : n > a.N ? a.N : n);
 }
 
+// The taps of V channels (V W neighbouring values) and their biases.
 template <int V, int W>
-__device__ __forceinline__ void load_taps(const ConvArgs &a, int e, float (&w)[W][V], float (&bias)[V]) {
+__device__ __forceinline__ void load_taps(const ConvArgs &a, int e, bool vec, float (&w)[W][V], float (&bias)[V]) {
+  float f[V * W];
+  const float *p = a.w + (size_t)e * W;
+  if (V * W % 4 == 0 && vec) {
+#pragma unroll
+    for (int i = 0; i + 3 < V * W; i += 4) {
+      const float4 q = *reinterpret_cast<const float4 *>(p + i);
+      f[i] = q.x; f[i + 1] = q.y; f[i + 2] = q.z; f[i + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V * W; ++i) f[i] = p[i];
+  }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     bias[v] = a.b ? a.b[e + v] : 0.f;
 #pragma unroll
-    for (int k = 0; k < W; ++k) w[k][v] = a.w[(size_t)(e + v) * W + k];
+    for (int k = 0; k < W; ++k) w[k][v] = f[v * W + k];
   }
 }
 
 // The input at position t >= -(W - 1) of a sequence: of the state before 0.
 template <typename T, int V, int W>
-__device__ __forceinline__ void input_at(const ConvArgs &a, int b, int e, int t, float (&f)[V]) {
-  if (t >= 0) {
-    Chans<T, V>::load(reinterpret_cast<const T *>(a.x) + b * a.sx[0] + t * a.sx[1] + e, f);
-  } else if (a.state_in) {
-    Chans<T, V>::load(reinterpret_cast<const T *>(a.state_in) + ((size_t)b * (W - 1) + (W - 1 + t)) * a.E + e, f);
-  } else {
-#pragma unroll
-    for (int v = 0; v < V; ++v) f[v] = 0.f;
-  }
+__device__ __forceinline__ Chans<T, V> input_at(const ConvArgs &a, int b, int e, int t) {
+  Chans<T, V> c;
+  if (t >= 0)
+    c.load(reinterpret_cast<const T *>(a.x) + b * a.sx[0] + t * a.sx[1] + e);
+  else if (a.state_in)
+    c.load(reinterpret_cast<const T *>(a.state_in) + ((size_t)b * (W - 1) + (W - 1 + t)) * a.E + e);
+  else
+    c.zero();
+  return c;
 }
 
 // run: tokens of a thread, at least W - 1 (then only the first run reads the
-// state, which state_out may be).
+// state, which state_out may be).  U tokens' loads are in flight; the inputs stay
+// as they were read until their turn (8192 x 4096 bf16 43 us, 3.1 TB/s; with four
+// tokens of eight channels in flight, converted at once, 124).
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(kThreads)
-conv_fwd_kernel(const ConvArgs a, int run, int runs) {
-  constexpr int U = 4;  // tokens whose loads are in flight
+conv_fwd_kernel(const ConvArgs a, int run, int runs, int vec_taps) {
+  constexpr int U = 8;
   pdl_launch_dependents();
   pdl_wait();
   const int nv = a.E / V, b = blockIdx.y;
@@ -95,18 +108,23 @@ conv_fwd_kernel(const ConvArgs a, int run, int runs) {
   if (i >= (long long)nv * runs) return;
   const int r = (int)(i / nv), e = (int)(i - (long long)r * nv) * V;
   const int n = conv_tokens(a, b), t0 = r * run, t1 = min(a.N, t0 + run), live = min(n, t1);
-  float w[W][V], bias[V], win[W][V];  // win[k]: the input W - 1 - k tokens before
-  load_taps<V, W>(a, e, w, bias);
-  if (t0 < live)
-#pragma unroll
-    for (int k = 0; k < W - 1; ++k) input_at<T, V, W>(a, b, e, t0 - (W - 1) + k, win[k + 1]);
   const T *x = reinterpret_cast<const T *>(a.x) + b * a.sx[0] + e;
   T *y = reinterpret_cast<T *>(a.out) + b * a.so[0] + e;
-  for (int t = t0; t < live; t += U) {
-    float in[U][V];
+  Chans<T, V> in[U];
 #pragma unroll
-    for (int j = 0; j < U; ++j)
-      if (t + j < live) Chans<T, V>::load(x + (t + j) * a.sx[1], in[j]);
+  for (int j = 0; j < U; ++j)
+    if (t0 + j < live) in[j].load(x + (t0 + j) * a.sx[1]);
+  float w[W][V], bias[V], win[W][V];  // win[k]: the input W - 1 - k tokens before
+  if (t0 < live) {
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) {
+      const Chans<T, V> c = input_at<T, V, W>(a, b, e, t0 - (W - 1) + k);
+#pragma unroll
+      for (int v = 0; v < V; ++v) win[k + 1][v] = c.get(v);
+    }
+    load_taps<V, W>(a, e, vec_taps, w, bias);
+  }
+  for (int t = t0; t < live; t += U) {
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       if (t + j >= live) break;
@@ -115,31 +133,40 @@ conv_fwd_kernel(const ConvArgs a, int run, int runs) {
       for (int v = 0; v < V; ++v) {
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) win[k][v] = win[k + 1][v];
-        win[W - 1][v] = in[j][v];
+        win[W - 1][v] = in[j].get(v);
         float s = bias[v];
 #pragma unroll
         for (int k = 0; k < W; ++k) s = fmaf(w[k][v], win[k][v], s);
         o[v] = a.silu ? silu(s) : s;
       }
+      if (t + j + U < live) in[j].load(x + (t + j + U) * a.sx[1]);
       Chans<T, V>::store(y + (t + j) * a.so[1], o);
     }
   }
   const float zero[V] = {};
   for (int t = max(t0, live); t < t1; ++t) Chans<T, V>::store(y + t * a.so[1], zero);
   if (r == 0 && a.state_out) {
-    float s[W - 1][V];
+    Chans<T, V> s[W - 1];
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) input_at<T, V, W>(a, b, e, n - (W - 1) + k, s[k]);
+    for (int k = 0; k < W - 1; ++k) s[k] = input_at<T, V, W>(a, b, e, n - (W - 1) + k);
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k)
-      Chans<T, V>::store(reinterpret_cast<T *>(a.state_out) + ((size_t)b * (W - 1) + k) * a.E + e, s[k]);
+    for (int k = 0; k < W - 1; ++k) {
+      float f[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) f[v] = s[k].get(v);
+      Chans<T, V>::store(reinterpret_cast<T *>(a.state_out) + ((size_t)b * (W - 1) + k) * a.E + e, f);
+    }
   }
 }
 
+// Two channels a thread, eight tokens of x and dy in flight: the taps, the
+// window, the gradients' window and the sums of a thread leave room for two
+// CTAs an SM (2 x 4096 x 4096 bf16; four channels and four tokens, one CTA an SM:
+// 222 us).
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(kThreads)
-conv_bwd_kernel(const ConvArgs a, int run, int runs, float *__restrict__ part) {
-  constexpr int U = 4;
+__global__ void __launch_bounds__(kThreads, 2)
+conv_bwd_kernel(const ConvArgs a, int run, int runs, int vec_taps, float *__restrict__ part) {
+  constexpr int U = 8;
   pdl_launch_dependents();
   pdl_wait();
   const int nv = a.E / V, b = blockIdx.y;
@@ -147,8 +174,21 @@ conv_bwd_kernel(const ConvArgs a, int run, int runs, float *__restrict__ part) {
   if (i >= (long long)nv * runs) return;
   const int r = (int)(i / nv), e = (int)(i - (long long)r * nv) * V;
   const int n = conv_tokens(a, b), t0 = r * run, t1 = min(a.N, t0 + run);
+  const T *x = reinterpret_cast<const T *>(a.x) + b * a.sx[0] + e;
+  const T *dy = reinterpret_cast<const T *>(a.dy) + b * a.sg[0] + e;
+  T *dx = reinterpret_cast<T *>(a.out) + b * a.so[0] + e;
+  const int last = t1 + W - 1, there = min(n, last);  // tokens walked, of them the sequence's
+  Chans<T, V> in[U], gr[U];
+  auto ahead = [&](int j, int t) {
+    if (t < there) {
+      in[j].load(x + t * a.sx[1]);
+      gr[j].load(dy + t * a.sg[1]);
+    }
+  };
+#pragma unroll
+  for (int j = 0; j < U; ++j) ahead(j, t0 + j);
   float w[W][V], bias[V], win[W][V], d[W][V], dw[W][V], db[V];  // d[k]: of the token k before
-  load_taps<V, W>(a, e, w, bias);
+  load_taps<V, W>(a, e, vec_taps, w, bias);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     db[v] = 0.f;
@@ -157,77 +197,95 @@ conv_bwd_kernel(const ConvArgs a, int run, int runs, float *__restrict__ part) {
   }
   if (t0 < n)
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) input_at<T, V, W>(a, b, e, t0 - (W - 1) + k, win[k + 1]);
-  const T *x = reinterpret_cast<const T *>(a.x) + b * a.sx[0] + e;
-  const T *dy = reinterpret_cast<const T *>(a.dy) + b * a.sg[0] + e;
-  T *dx = reinterpret_cast<T *>(a.out) + b * a.so[0] + e;
-  // Token t's d, and with it dx of token t - (W - 1), up to the run's last.
-  for (int t = t0; t < t1 + W - 1; t += U) {
-    float in[U][V], gr[U][V];
+    for (int k = 0; k < W - 1; ++k) {
+      const Chans<T, V> c = input_at<T, V, W>(a, b, e, t0 - (W - 1) + k);
 #pragma unroll
-    for (int j = 0; j < U; ++j)
-      if (t + j < min(n, t1 + W - 1)) {
-        Chans<T, V>::load(x + (t + j) * a.sx[1], in[j]);
-        Chans<T, V>::load(dy + (t + j) * a.sg[1], gr[j]);
-      }
+      for (int v = 0; v < V; ++v) win[k + 1][v] = c.get(v);
+    }
+  // Token at's d, and with it dx of token at - (W - 1).  kInner: a token of the run
+  // and the sequence whose dx is the run's too, and no state behind it.
+  auto step = [&](int j, int at, auto inner) {
+    constexpr bool kInner = decltype(inner)::value;
+    const int o = at - (W - 1);
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int at = t + j, o = at - (W - 1);
-      if (at >= t1 + W - 1) break;
-      float out[V];
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int k = W - 1; k > 0; --k) d[k][v] = d[k - 1][v];
+    if (kInner || at < there) {
+      const bool mine = kInner || at < t1;  // (what lies behind the run belongs to the next one's sums)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
 #pragma unroll
-        for (int k = W - 1; k > 0; --k) d[k][v] = d[k - 1][v];
-        if (at < n) {
+        for (int k = 0; k < W - 1; ++k) win[k][v] = win[k + 1][v];
+        win[W - 1][v] = in[j].get(v);
+        float dv = gr[j].get(v);
+        if (a.silu) {
+          float s = bias[v];
 #pragma unroll
-          for (int k = 0; k < W - 1; ++k) win[k][v] = win[k + 1][v];
-          win[W - 1][v] = in[j][v];
-          float dv = gr[j][v];
-          if (a.silu) {
-            float s = bias[v];
-#pragma unroll
-            for (int k = 0; k < W; ++k) s = fmaf(w[k][v], win[k][v], s);
-            const float sg = sigmoid(s);
-            dv *= sg * fmaf(s, 1.f - sg, 1.f);
-          }
-          d[0][v] = dv;
-          if (at < t1) {
-            db[v] += dv;
-#pragma unroll
-            for (int k = 0; k < W; ++k) dw[k][v] = fmaf(dv, win[k][v], dw[k][v]);
-          }
-        } else {
-          d[0][v] = 0.f;
+          for (int k = 0; k < W; ++k) s = fmaf(w[k][v], win[k][v], s);
+          const float sg = sigmoid(s);
+          dv *= sg * fmaf(s, 1.f - sg, 1.f);
         }
+        d[0][v] = dv;
+        if (mine) {
+          db[v] += dv;
+#pragma unroll
+          for (int k = 0; k < W; ++k) dw[k][v] = fmaf(dv, win[k][v], dw[k][v]);
+        }
+      }
+      ahead(j, at + U);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) d[0][v] = 0.f;
+    }
+    if (kInner || o >= t0 || (r == 0 && o < 0)) {
+      float out[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
         out[v] = 0.f;
 #pragma unroll
         for (int k = 0; k < W; ++k) out[v] = fmaf(w[k][v], d[k][v], out[v]);
       }
-      if (o >= t0 || (r == 0 && o < 0)) {
-        // what the state after the sequence passes back to the last W - 1 inputs
-        const int m = o - (n - (W - 1));
-        if (a.dstate_out && m >= 0 && m < W - 1) {
-          float s[V];
-          Chans<T, V>::load(reinterpret_cast<const T *>(a.dstate_out) + ((size_t)b * (W - 1) + m) * a.E + e, s);
+      // what the state after the sequence passes back to the last W - 1 inputs
+      const int m = o - (n - (W - 1));
+      if (!kInner && a.dstate_out && m >= 0 && m < W - 1) {
+        Chans<T, V> s;
+        s.load(reinterpret_cast<const T *>(a.dstate_out) + ((size_t)b * (W - 1) + m) * a.E + e);
 #pragma unroll
-          for (int v = 0; v < V; ++v) out[v] += s[v];
-        }
-        if (o >= 0)
-          Chans<T, V>::store(dx + o * a.so[1], out);
-        else if (a.dstate_in)
-          Chans<T, V>::store(reinterpret_cast<T *>(a.dstate_in) + ((size_t)b * (W - 1) + W - 1 + o) * a.E + e, out);
+        for (int v = 0; v < V; ++v) out[v] += s.get(v);
       }
+      if (kInner || o >= 0)
+        Chans<T, V>::store(dx + o * a.so[1], out);
+      else if (a.dstate_in)
+        Chans<T, V>::store(reinterpret_cast<T *>(a.dstate_in) + ((size_t)b * (W - 1) + W - 1 + o) * a.E + e, out);
+    }
+  };
+  for (int t = t0; t < last; t += U) {
+    if (t > t0 && t + U <= min(there, t1)) {
+#pragma unroll
+      for (int j = 0; j < U; ++j) step(j, t + j, std::true_type());
+    } else {
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+        if (t + j < last) step(j, t + j, std::false_type());
     }
   }
   if (!part) return;
   const size_t row = (size_t)b * runs + r, rows = (size_t)a.B * runs;
-  float *pb = part + rows * a.E * W;
+  float *pb = part + rows * a.E * W + row * a.E + e, *pw = part + (row * a.E + e) * W;
+  float f[V * W];
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    pb[row * a.E + e + v] = db[v];
+  for (int v = 0; v < V; ++v)
 #pragma unroll
-    for (int k = 0; k < W; ++k) part[(row * a.E + e + v) * W + k] = dw[k][v];
+    for (int k = 0; k < W; ++k) f[v * W + k] = dw[k][v];
+  if constexpr (V == 2) {  // (E is even, the workspace aligned)
+    *reinterpret_cast<float2 *>(pb) = make_float2(db[0], db[1]);
+#pragma unroll
+    for (int v = 0; v < V * W; v += 2) *reinterpret_cast<float2 *>(pw + v) = make_float2(f[v], f[v + 1]);
+  } else {
+    pb[0] = db[0];
+#pragma unroll
+    for (int v = 0; v < W; ++v) pw[v] = f[v];
   }
 }
 
@@ -243,20 +301,21 @@ int run_of(const ConvArgs &a, int nv, int most) {
   while (run > 4 && (long long)nv * a.B * ((a.N + run - 1) / run) < 1024LL * device_sms()) run /= 2;
   return run;
 }
+int taps_on(const ConvArgs &a) { return reinterpret_cast<uintptr_t>(a.w) % 16 == 0; }
 int runs_of(int N, int run) { return std::max(1, (N + run - 1) / run); }
 
 template <typename T, int V, int W>
 cudaError_t fwd(const ConvArgs &a, cudaStream_t st) {
   const int nv = a.E / V, run = run_of(a, nv, 32), runs = runs_of(a.N, run);
   const dim3 grid((unsigned)(((long long)nv * runs + kThreads - 1) / kThreads), a.B);
-  return launch_k(conv_fwd_kernel<T, V, W>, grid, dim3(kThreads), 0, st, true, a, run, runs);
+  return launch_k(conv_fwd_kernel<T, V, W>, grid, dim3(kThreads), 0, st, true, a, run, runs, taps_on(a));
 }
 
 template <typename T, int V, int W>
 cudaError_t bwd(const ConvArgs &a, float *part, cudaStream_t st) {
   const int runs = conv_bwd_runs(a) / a.B, run = std::max(4, (a.N + runs - 1) / runs);
   const dim3 grid((unsigned)(((long long)(a.E / V) * runs + kThreads - 1) / kThreads), a.B);
-  return launch_k(conv_bwd_kernel<T, V, W>, grid, dim3(kThreads), 0, st, true, a, run, runs, part);
+  return launch_k(conv_bwd_kernel<T, V, W>, grid, dim3(kThreads), 0, st, true, a, run, runs, taps_on(a), part);
 }
 
 template <typename T, int V>
@@ -271,28 +330,34 @@ cudaError_t bwd_taps(const ConvArgs &a, float *part, cudaStream_t st) {
 
 }  // namespace
 
+// V channels at a time where every row begins on their boundary.
+static bool vectors(const ConvArgs &a, int V, const void *const *flat, int n, int esz) {
+  const int by = V * esz;
+  for (int i = 0; i < n; ++i)
+    if (reinterpret_cast<uintptr_t>(flat[i]) % by) return false;
+  return a.E % V == 0 && aligned(a.x, a.sx, a.B, a.N, by, esz) && aligned(a.out, a.so, a.B, a.N, by, esz);
+}
+
 cudaError_t launch_conv_fwd(const ConvArgs &a, int bf16, cudaStream_t st) {
-  const int esz = bf16 ? 2 : 4;
-  const bool v = a.E * esz % 16 == 0 && aligned(a.x, a.sx, a.B, a.N, 16, esz) && aligned(a.out, a.so, a.B, a.N, 16, esz) &&
-                 reinterpret_cast<uintptr_t>(a.state_in) % 16 == 0 && reinterpret_cast<uintptr_t>(a.state_out) % 16 == 0;
-  if (bf16) return v ? fwd_taps<__nv_bfloat16, 8>(a, st) : fwd_taps<__nv_bfloat16, 1>(a, st);
+  const void *flat[] = {a.state_in, a.state_out};
+  const bool v = vectors(a, 4, flat, 2, bf16 ? 2 : 4);
+  if (bf16) return v ? fwd_taps<__nv_bfloat16, 4>(a, st) : fwd_taps<__nv_bfloat16, 1>(a, st);
   return v ? fwd_taps<float, 4>(a, st) : fwd_taps<float, 1>(a, st);
 }
 
 // Runs of tokens over all sequences (at most 64 tokens each, fewer where that
 // leaves less than 1024 threads an SM).
 int conv_bwd_runs(const ConvArgs &a) {
-  const int nv = std::max(1, a.E / 4);
+  const int nv = std::max(1, a.E / 2);
   return runs_of(a.N, run_of(a, nv, 64)) * a.B;
 }
 
 cudaError_t launch_conv_bwd(const ConvArgs &a, int bf16, float *part, cudaStream_t st) {
-  const int esz = bf16 ? 2 : 4, by = 4 * esz;
-  const bool v = a.E % 4 == 0 && aligned(a.x, a.sx, a.B, a.N, by, esz) && aligned(a.dy, a.sg, a.B, a.N, by, esz) &&
-                 aligned(a.out, a.so, a.B, a.N, by, esz) && reinterpret_cast<uintptr_t>(a.state_in) % by == 0 &&
-                 reinterpret_cast<uintptr_t>(a.dstate_in) % by == 0 && reinterpret_cast<uintptr_t>(a.dstate_out) % by == 0;
-  if (bf16) return v ? bwd_taps<__nv_bfloat16, 4>(a, part, st) : bwd_taps<__nv_bfloat16, 1>(a, part, st);
-  return v ? bwd_taps<float, 4>(a, part, st) : bwd_taps<float, 1>(a, part, st);
+  const int esz = bf16 ? 2 : 4;
+  const void *flat[] = {a.state_in, a.dstate_in, a.dstate_out};
+  const bool v = vectors(a, 2, flat, 3, esz) && aligned(a.dy, a.sg, a.B, a.N, 2 * esz, esz);
+  if (bf16) return v ? bwd_taps<__nv_bfloat16, 2>(a, part, st) : bwd_taps<__nv_bfloat16, 1>(a, part, st);
+  return v ? bwd_taps<float, 2>(a, part, st) : bwd_taps<float, 1>(a, part, st);
 }
 
 }  // namespace ret

@@ -70,6 +70,20 @@ __device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&f)[V]) {
   }
 }
 
+// f / scale: by the reciprocal, which has an ordinary scale's; a subnormal one's
+// may be infinite.  A group of zeros has scale 0.
+template <int V>
+__device__ __forceinline__ void scale_down(float (&f)[V], float scale) {
+  if (scale >= 1.17549435e-38f) {
+    const float inv = 1.f / scale;
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] *= inv;
+  } else if (scale > 0.f) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] /= scale;
+  }
+}
+
 // Rounds to the rows' type, as what is kept of the sum is.
 template <typename T, int V>
 __device__ __forceinline__ void add_rounded(const Elems<T, V> &a, const Elems<T, V> &b, Elems<T, V> &h) {
@@ -81,45 +95,59 @@ __device__ __forceinline__ void add_rounded(const Elems<T, V> &a, const Elems<T,
   h.set(f);
 }
 
+// The vectors of one row that a thread reads, on their way.
+template <typename T, int V, int NV>
+struct RowIn {
+  Elems<T, V> v[NV];
+  __device__ __forceinline__ void load(const T *p, int tpr, int t, int d) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * tpr + t) * V;
+      if (c < d) v[i].load(p + c);
+    }
+  }
+};
+
 // tpr threads a row, NV vectors of V values a thread, interleaved; the row
-// stays in registers.  kQuant: e4m3 output.
+// stays in registers, and the next one is on its way meanwhile.  kQuant: e4m3
+// output.
 template <typename T, int V, int NV, bool kQuant>
 __global__ void __launch_bounds__(512)
 rms_fwd_kernel(const RmsArgs a, int tpr) {
   extern __shared__ unsigned amax[];  // [rows of the CTA][groups]
   __shared__ float red[2][32];
-  pdl_launch_dependents();
   pdl_wait();
   const int row_in = threadIdx.x / tpr, t = threadIdx.x - row_in * tpr, per = blockDim.x / tpr;
   const float inv_d = 1.f / (float)a.d;
-  for (long long r0 = (long long)blockIdx.x * per; r0 < a.rows; r0 += (long long)gridDim.x * per) {
+  constexpr bool kAhead = V > 1 || NV <= 16;  // (else the registers hold one row)
+  RowIn<T, V, NV> xn, rn;
+  auto ahead = [&](long long r) {
+    if (r >= a.rows) return;
+    xn.load(reinterpret_cast<const T *>(a.x) + row_offset(a.sx, r), tpr, t, a.d);
+    if (a.r) rn.load(reinterpret_cast<const T *>(a.r) + row_offset(a.sr, r), tpr, t, a.d);
+  };
+  if (kAhead) ahead((long long)blockIdx.x * per + row_in);
+  int par = 0;
+  for (long long r0 = (long long)blockIdx.x * per; r0 < a.rows; r0 += (long long)gridDim.x * per, par ^= 1) {
     const long long r = r0 + row_in;
     const bool live = r < a.rows;
     Elems<T, V> h[NV];
     float s = 0.f;
+    if (!kAhead) ahead(r);
     if (kQuant) {
       for (int i = threadIdx.x; i < per * a.groups; i += blockDim.x) amax[i] = 0u;
     }
     if (live) {
-      const T *x = reinterpret_cast<const T *>(a.x) + row_offset(a.sx, r);
-      const T *q = a.r ? reinterpret_cast<const T *>(a.r) + row_offset(a.sr, r) : nullptr;
       T *ho = a.r ? reinterpret_cast<T *>(a.h) + row_offset(a.sh, r) : nullptr;
-      Elems<T, V> rv[NV];
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * tpr + t) * V;
         if (c < a.d) {
-          h[i].load(x + c);
-          if (q) rv[i].load(q + c);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * tpr + t) * V;
-        if (c < a.d) {
-          if (q) {
-            add_rounded<T, V>(h[i], rv[i], h[i]);
+          if (a.r) {
+            add_rounded<T, V>(xn.v[i], rn.v[i], h[i]);
             h[i].store(ho + c);
+          } else {
+            h[i] = xn.v[i];
           }
           float f[V];
           h[i].get(f);
@@ -128,7 +156,8 @@ rms_fwd_kernel(const RmsArgs a, int tpr) {
         }
       }
     }
-    s = row_join<false>(s, red[0], tpr);
+    if (kAhead) ahead(r + (long long)gridDim.x * per);
+    s = row_join<false>(s, red[par], tpr);
     const float rstd = rsqrtf(fmaf(s, inv_d, a.eps));
     if (live && t == 0 && a.rstd) a.rstd[r] = rstd;
     if (!kQuant) {
@@ -148,7 +177,6 @@ rms_fwd_kernel(const RmsArgs a, int tpr) {
           }
         }
       }
-      if (tpr > 32) __syncthreads();  // red is free again
     } else {
       if (tpr <= 32) __syncthreads();  // the maxima are cleared (wider rows met in the sum)
       unsigned *top = amax + row_in * a.groups;
@@ -156,8 +184,9 @@ rms_fwd_kernel(const RmsArgs a, int tpr) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * tpr + t) * V;
+        float m = 0.f;
         if (live && c < a.d) {
-          float w[V], m = 0.f;
+          float w[V];
           h[i].get(f[i]);
           load_gain<V>(a.w, c, w);
 #pragma unroll
@@ -165,6 +194,16 @@ rms_fwd_kernel(const RmsArgs a, int tpr) {
             f[i][j] = f[i][j] * rstd * w[j];
             m = fmaxf(m, fabsf(f[i][j]));
           }
+        }
+        // lanes of one group join first (a warp's vectors are neighbours)
+        if (tpr >= 32 && a.group % (32 * V) == 0) {
+          const unsigned top32 = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+          if ((threadIdx.x & 31) == 0 && live && c < a.d) atomicMax(top + c / a.group, top32);
+        } else if (V == 8 && tpr >= 32 && a.group == 128) {
+#pragma unroll
+          for (int k = 8; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+          if ((threadIdx.x & 15) == 0 && live && c < a.d) atomicMax(top + c / 128, __float_as_uint(m));
+        } else if (live && c < a.d) {
           // (a maximum does not depend on the order of its atomics)
           atomicMax(top + c / a.group, __float_as_uint(m));
         }
@@ -177,16 +216,15 @@ rms_fwd_kernel(const RmsArgs a, int tpr) {
         for (int i = 0; i < NV; ++i) {
           const int c = (i * tpr + t) * V;
           if (c < a.d) {
-            const float scale = __uint_as_float(top[c / a.group]) / kE4m3Max;
-#pragma unroll
-            for (int j = 0; j < V; ++j) f[i][j] = scale > 0.f ? f[i][j] / scale : f[i][j];
+            scale_down<V>(f[i], __uint_as_float(top[c / a.group]) / kE4m3Max);
             store_e4m3<V>(y + c, f[i]);
           }
         }
       }
-      __syncthreads();  // red and the maxima are free again
+      __syncthreads();  // the maxima are free again
     }
   }
+  pdl_launch_dependents();
 }
 
 // Rows too long for registers: read again for the output (the kept sum, or x).
@@ -253,10 +291,8 @@ rms_fwd_long_kernel(const RmsArgs a) {
           e.get(f);
           load_gain<V>(a.w, c, w);
 #pragma unroll
-          for (int j = 0; j < V; ++j) {
-            f[j] = f[j] * rstd * w[j];
-            if (scale > 0.f) f[j] /= scale;
-          }
+          for (int j = 0; j < V; ++j) f[j] = f[j] * rstd * w[j];
+          scale_down<V>(f, scale);
           store_e4m3<V>(y + c, f);
         }
         if (wide) __syncthreads();  // red is free again
@@ -273,7 +309,6 @@ __global__ void __launch_bounds__(512)
 rms_bwd_kernel(const RmsArgs a, int tpr, float *__restrict__ part) {
   extern __shared__ float sums[];  // [rows of the CTA][d] where there are several
   __shared__ float red[2][32];
-  pdl_launch_dependents();
   pdl_wait();
   const int row_in = threadIdx.x / tpr, t = threadIdx.x - row_in * tpr, per = blockDim.x / tpr;
   const float inv_d = 1.f / (float)a.d;
@@ -283,25 +318,32 @@ rms_bwd_kernel(const RmsArgs a, int tpr, float *__restrict__ part) {
 #pragma unroll
     for (int j = 0; j < V; ++j) dw[i][j] = 0.f;
   int par = 0;
+  constexpr bool kAhead = V == 1 ? NV <= 8 : NV * V <= 16;  // (else the registers hold one row)
+  RowIn<T, V, NV> hn, gn, pn;
+  float rn = 0.f;
+  auto ahead = [&](long long r) {
+    if (r >= a.rows) return;
+    hn.load(reinterpret_cast<const T *>(a.x) + row_offset(a.sx, r), tpr, t, a.d);
+    gn.load(reinterpret_cast<const T *>(a.dy) + row_offset(a.sg, r), tpr, t, a.d);
+    if (a.dh) pn.load(reinterpret_cast<const T *>(a.dh) + row_offset(a.sdh, r), tpr, t, a.d);
+    rn = a.rstd[r];
+  };
+  if (kAhead) ahead((long long)blockIdx.x * per + row_in);
   for (long long r0 = (long long)blockIdx.x * per; r0 < a.rows; r0 += (long long)gridDim.x * per, par ^= 1) {
     const long long r = r0 + row_in;
     const bool live = r < a.rows;
     Elems<T, V> h[NV], g[NV], p[NV];
-    float s = 0.f, rstd = 0.f;
-    if (live) {
-      const T *x = reinterpret_cast<const T *>(a.x) + row_offset(a.sx, r);
-      const T *dy = reinterpret_cast<const T *>(a.dy) + row_offset(a.sg, r);
-      const T *dh = a.dh ? reinterpret_cast<const T *>(a.dh) + row_offset(a.sdh, r) : nullptr;
-      rstd = a.rstd[r];
+    float s = 0.f;
+    if (!kAhead) ahead(r);
+    const float rstd = rn;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * tpr + t) * V;
-        if (c < a.d) {
-          h[i].load(x + c);
-          g[i].load(dy + c);
-          if (dh) p[i].load(dh + c);
-        }
-      }
+    for (int i = 0; i < NV; ++i) {
+      h[i] = hn.v[i];
+      g[i] = gn.v[i];
+      p[i] = pn.v[i];
+    }
+    if (kAhead) ahead(r + (long long)gridDim.x * per);
+    if (live) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * tpr + t) * V;
@@ -343,6 +385,7 @@ rms_bwd_kernel(const RmsArgs a, int tpr, float *__restrict__ part) {
       }
     }
   }
+  pdl_launch_dependents();
   if (!part) return;
   float *out = part + (size_t)blockIdx.x * a.d;
   float *mine = per > 1 ? sums + (size_t)row_in * a.d : out;
@@ -445,15 +488,17 @@ int threads_per_row(int n, int most) {
 template <typename T, int V, bool kQuant>
 cudaError_t fwd_any(const RmsArgs &a, cudaStream_t st) {
   const int n = (a.d + V - 1) / V, sms = device_sms();
-  // At most 512 threads a row: 8, 16 or 32 values a thread.
+  // At most 512 threads a row: 8 values a thread for few rows (all of them at
+  // once), else 16 (more bytes in flight beside the next row's), or 32.
   auto go = [&](auto nv) {
     constexpr int NV = decltype(nv)::value;
     const int tpr = threads_per_row(n, NV), threads = tpr > 32 ? tpr : 128, per = threads / tpr;
-    const long long want = (a.rows + per - 1) / per, most = (long long)sms * (2048 / threads) * 4;
+    const long long want = (a.rows + per - 1) / per, most = (long long)sms * std::max(1, 1024 / threads);
     const size_t smem = kQuant ? (size_t)per * a.groups * 4 : 0;
     return launch_k(rms_fwd_kernel<T, V, NV, kQuant>, dim3((unsigned)std::min(want, most)), dim3(threads), smem, st, true, a, tpr);
   };
-  if (a.d <= 512 * 8) return go(std::integral_constant<int, 8 / V>());
+  const bool few = a.rows * ((a.d + 7) / 8) <= (long long)sms * 1024;
+  if (a.d <= 512 * 8 && (few || a.d <= 256)) return go(std::integral_constant<int, 8 / V>());
   if (a.d <= 512 * 16) return go(std::integral_constant<int, 16 / V>());
   if (a.d <= 512 * 32) return go(std::integral_constant<int, 32 / V>());
   const long long cap = 1LL << 30;
@@ -507,7 +552,7 @@ RmsBwdPlan rmsnorm_bwd_plan(const RmsArgs &a, int bf16) {
   const int V = pl.vec ? vec : 1, n = (a.d + V - 1) / V;
   // At most 512 threads a row with 8 or 16 values each, for 16-byte vectors of
   // bf16 (whose rows take half the registers) 32.
-  pl.values = a.d <= 512 * 8 ? 8 : a.d <= 512 * 16 ? 16 : 32;
+  pl.values = a.d <= 256 ? 8 : a.d <= 512 * 16 ? 16 : 32;
   if (a.d > 512 * (V == 8 ? 32 : 16)) {
     pl.two_pass = true;
     pl.groups = (int)std::min<long long>(a.rows, kTwoPassGroups);

@@ -173,17 +173,18 @@ scan_bwd_chunks_kernel(const ScanArgs a, const ScanBwdPlan pl, int run, float *_
       }
     }
   };
-  Raw next, after;
-  load(0, next);
-  load(1, after);
-  put(0, next);
-  next = after;
+  Raw even, odd;
+  load(0, even);
+  load(1, odd);
+  put(0, even);
   __syncthreads();
-  for (int i = 0; i < tiles; ++i) {
-    load(i + 2, after);
-    put(i + 1, next);
+  for (int i = 0; i < tiles; i += 2) {  // (an even number)
+    load(i + 2, even);
+    put(i + 1, odd);
     __syncthreads();
-    next = after;
+    load(i + 3, odd);
+    put(i + 2, even);
+    __syncthreads();
   }
   pdl_launch_dependents();
 }
@@ -391,7 +392,10 @@ scan_bwd_kernel(const ScanArgs a, const ScanBwdPlan pl, float *__restrict__ ws) 
   // ---- backwards, tile by tile
   float sD[4] = {}, sBias[4] = {};
   constexpr int NW = kTile / QS > 0 ? kTile / QS : 1;  // quads of a tile a thread writes
-  // What a lane got of the sums of 8 values v = j * 2 + c (tokens j, channels c).
+  // What a lane gets of the sums of 8 values v = j * 2 + c (tokens j, channels c),
+  // and of sums over the warp's channels of values v = j * 4 + s.  (Held back to
+  // the tile's end they would cost more in spilled registers than the loads that
+  // a store holds back: 1226 us for 883.)
   auto put_sums = [&](float (*to)[CC], int j0, float (&v)[8]) {
     share_sums<8, L>(v);
     constexpr int W = L < 8 ? L : 8;
@@ -402,7 +406,6 @@ scan_bwd_kernel(const ScanArgs a, const ScanBwdPlan pl, float *__restrict__ ws) 
         to[j0 + idx / 2][ca + idx % 2] = v[m];
       }
   };
-  // The same for sums over the warp's channels of values v = j * 4 + s.
   auto put_bc = [&](int which, int j0, float (&v)[8]) {
     share_sums<8, 32 / L, L>(v);
     constexpr int W = 32 / L < 8 ? 32 / L : 8;

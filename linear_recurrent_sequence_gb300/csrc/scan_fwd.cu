@@ -73,11 +73,15 @@ scan_fwd_kernel(const ScanArgs a, const ScanSegs seg) {
     __syncthreads();
     for (int i = 0; i < tiles; ++i) {
       const int buf = i & 1;
+      // (16 tokens' outputs are stored at once: a store between them would hold
+      // back the loads behind it, and a warp alone on its scheduler has nothing
+      // else to do; 76 cycles a token with stores every 4 tokens)
+      constexpr int GT = TT < 16 ? TT : 16;
 #pragma unroll
-      for (int q = 0; q < TT; q += 4) {
-        float yq[4];
+      for (int q = 0; q < TT; q += GT) {
+        float yq[GT / 4][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < GT; ++j) {
           const float4 v = sm.du[buf][q + j][ci];
           const float4 B4 = *reinterpret_cast<const float4 *>(&sm.bm[buf][q + j][s0]);
           const float2 dd = make_float2(v.x, v.y), uu = make_float2(v.z, v.w);
@@ -88,15 +92,17 @@ scan_fwd_kernel(const ScanArgs a, const ScanSegs seg) {
           if (!kStates) {
             const float4 C4 = *reinterpret_cast<const float4 *>(&sm.cm[buf][q + j][s0]);
             const float2 s = tc::fma2(h23, make_float2(C4.z, C4.w), tc::mul2(h01, make_float2(C4.x, C4.y)));
-            yq[j] = s.x + s.y;
+            yq[j / 4][j % 4] = s.x + s.y;
+            if (j % 4 == 3) share_sums<4, L>(yq[j / 4]);
           }
         }
         if (!kStates) {
-          share_sums<4, L>(yq);
           constexpr int M = L < 4 ? L : 4;
           if (tid % L < M)
 #pragma unroll
-            for (int j = 0; j < 4 / M; ++j) sm.ysum[buf][q + tid % M * (4 / M) + j][ci] = yq[j];
+            for (int i4 = 0; i4 < GT / 4; ++i4)
+#pragma unroll
+              for (int j = 0; j < 4 / M; ++j) sm.ysum[buf][q + i4 * 4 + tid % M * (4 / M) + j][ci] = yq[i4][j];
         }
       }
       __syncthreads();
@@ -210,22 +216,26 @@ scan_fwd_kernel(const ScanArgs a, const ScanSegs seg) {
     }
   };
 
-  Raw next, after;
+  // Two buffers of what is on its way, each known by name (a copy from one to the
+  // other would wait for the loads).
+  Raw even, odd;
   Kept cur, done;
-  load(0, next);
-  load(1, after);
-  if (tiles > 0) put(0, next);
-  keep(next, cur);
-  next = after;
+  load(0, even);
+  load(1, odd);
+  if (tiles > 0) put(0, even);
+  keep(even, cur);
   __syncthreads();
-  for (int i = 0; i < tiles; ++i) {
-    load(i + 2, after);
+  auto turn = [&](int i, Raw &next, Raw &free) {  // next: tile i + 1
+    load(i + 2, free);
     if (i > 0) finish(i - 1, done);
     if (i + 1 < tiles) put(i + 1, next);
     __syncthreads();
     done = cur;
     keep(next, cur);
-    next = after;
+  };
+  for (int i = 0; i < tiles; i += 2) {
+    turn(i, odd, even);
+    if (i + 1 < tiles) turn(i + 1, even, odd);
   }
   if (tiles > 0) finish(tiles - 1, done);
   pdl_launch_dependents();
@@ -246,58 +256,78 @@ scan_fwd_kernel(const ScanArgs a, const ScanSegs seg) {
   }
 }
 
-// One token.  A lane has four states of R sequences' same channel, so that A
-// is read once for them.
+// One token.  A lane has four states of R sequences' same channel, so that A is
+// read once for them; what a sequence's channel needs once (step size, gate,
+// output) is shared out over the channel's lanes.
 constexpr int kStepThreads = 256;
 
-template <typename T, int L, int R>
+template <typename T, int L, int R, bool kVec>
 __global__ void __launch_bounds__(kStepThreads)
 scan_step_kernel(const ScanArgs a) {
   pdl_launch_dependents();
   pdl_wait();
-  constexpr int CC = kStepThreads / L;
-  const int ci = threadIdx.x / L, s0 = threadIdx.x % L * 4;
+  constexpr int CC = kStepThreads / L, M = L < R ? L : R, NR = R / M;  // lanes that have sequences, of each NR
+  const int lane = threadIdx.x & 31, ci = threadIdx.x / L, sub = threadIdx.x % L, s0 = sub * 4;
   const int c = blockIdx.x * CC + ci, e = min(c, a.E - 1), g = e / (a.E / a.G);
   const bool own = c < a.E, vec = a.S % 4 == 0;
   const bool va = vec && reinterpret_cast<uintptr_t>(a.A) % 16 == 0;
   const bool vi = vec && reinterpret_cast<uintptr_t>(a.h_in) % 16 == 0;
   const bool vo = vec && reinterpret_cast<uintptr_t>(a.h_out) % 16 == 0;
-  const int b0 = blockIdx.y * R;
+  const int b0 = blockIdx.y * R, there = min(R, a.B - b0);
+  const size_t row = ((size_t)b0 * a.E + e) * a.S, step = (size_t)a.E * a.S;
   float4 h[R];
+  Four<T> Br[R], Cr[R];
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int b = min(b0 + r, a.B - 1);
-    h[r] = load_states(a.h_in + ((size_t)b * a.E + e) * a.S, s0, a.S, vi);
+  for (int r = 0; r < R; ++r)
+    if (r < there) h[r] = load_states(a.h_in + row + r * step, s0, a.S, vi);
+  {
+    const T *Bp = reinterpret_cast<const T *>(a.Bm) + b0 * a.sB[0] + g * a.sB[2] + s0;
+    const T *Cp = reinterpret_cast<const T *>(a.Cm) + b0 * a.sC[0] + g * a.sC[2] + s0;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (r < there) {
+        Br[r] = load_four<T, kVec>(Bp + r * a.sB[0], a.S - s0);
+        Cr[r] = load_four<T, kVec>(Cp + r * a.sC[0], a.S - s0);
+      }
+  }
+  // this lane's sequences: sub NR .. sub NR + NR - 1
+  const float bias = a.bias ? a.bias[e] : 0.f, Dv = a.D ? a.D[e] : 0.f;
+  float x[NR], d[NR], gate[NR];
+#pragma unroll
+  for (int m = 0; m < NR; ++m) {
+    const int b = b0 + min(sub % M * NR + m, there - 1);
+    x[m] = to_float(reinterpret_cast<const T *>(a.x)[b * a.sx[0] + e]);
+    d[m] = to_float(reinterpret_cast<const T *>(a.dt)[b * a.sdt[0] + e]) + bias;
+    gate[m] = a.z ? to_float(reinterpret_cast<const T *>(a.z)[b * a.sz[0] + e]) : 0.f;
   }
   const float4 A4 = load_states(a.A + (size_t)e * a.S, s0, a.S, va);
-  const float bias = a.bias ? a.bias[e] : 0.f, Dv = a.D ? a.D[e] : 0.f;
+  const float As[4] = {A4.x * kLog2e, A4.y * kLog2e, A4.z * kLog2e, A4.w * kLog2e};
+#pragma unroll
+  for (int m = 0; m < NR; ++m) {
+    if (a.softplus) d[m] = softplus(d[m]);
+    gate[m] = a.z ? silu(gate[m]) : 1.f;
+  }
+  float sum[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int b = min(b0 + r, a.B - 1);
-    const float x = to_float(reinterpret_cast<const T *>(a.x)[b * a.sx[0] + e]);
-    float d = to_float(reinterpret_cast<const T *>(a.dt)[b * a.sdt[0] + e]) + bias;
-    if (a.softplus) d = softplus(d);
-    const T *Bp = reinterpret_cast<const T *>(a.Bm) + b * a.sB[0] + g * a.sB[2];
-    const T *Cp = reinterpret_cast<const T *>(a.Cm) + b * a.sC[0] + g * a.sC[2];
-    const float u = d * x, w = d * kLog2e;
+    const int from = lane / L * L + r / NR;
+    const float dr = __shfl_sync(0xffffffffu, d[r % NR], from);
+    const float u = dr * __shfl_sync(0xffffffffu, x[r % NR], from);
     float hs[4] = {h[r].x, h[r].y, h[r].z, h[r].w};
-    const float As[4] = {A4.x, A4.y, A4.z, A4.w};
-    float s[1] = {0.f};
+    sum[r] = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const bool in = s0 + j < a.S;
-      const float Bv = in ? to_float(Bp[s0 + j]) : 0.f, Cv = in ? to_float(Cp[s0 + j]) : 0.f;
-      hs[j] = fmaf(ex2(w * As[j]), hs[j], u * Bv);
-      s[0] = fmaf(hs[j], Cv, s[0]);
+      hs[j] = fmaf(ex2(dr * As[j]), hs[j], u * to_float(Br[r].v[j]));
+      sum[r] = fmaf(hs[j], to_float(Cr[r].v[j]), sum[r]);
     }
-    share_sums<1, L>(s);
-    const bool mine = own && b0 + r < a.B;
-    if (mine) store_states(a.h_out + ((size_t)b * a.E + e) * a.S, s0, a.S, vo, make_float4(hs[0], hs[1], hs[2], hs[3]));
-    if (mine && s0 == 0) {
-      float v = fmaf(Dv, x, s[0]);
-      if (a.z) v *= silu(to_float(reinterpret_cast<const T *>(a.z)[b * a.sz[0] + e]));
-      reinterpret_cast<T *>(a.y)[b * a.sy[0] + e] = from_float<T>(v);
-    }
+    if (own && r < there) store_states(a.h_out + row + r * step, s0, a.S, vo, make_float4(hs[0], hs[1], hs[2], hs[3]));
+  }
+  share_sums<R, L>(sum);
+#pragma unroll
+  for (int m = 0; m < NR; ++m) {
+    const int r = sub * NR + m;
+    if (own && r < there)
+      reinterpret_cast<T *>(a.y)[(b0 + r) * a.sy[0] + e] = from_float<T>(fmaf(Dv, x[m], sum[m]) * gate[m]);
   }
 }
 
@@ -327,14 +357,17 @@ cudaError_t scan_any(const ScanArgs &a, const ScanSegs &seg, int segs, cudaStrea
   });
 }
 
-template <typename T>
+template <typename T, int R>
 cudaError_t step_any(const ScanArgs &a, cudaStream_t st) {
+  auto on = [&](const void *p, const long long s[3]) {
+    return reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T)) == 0 && (a.B == 1 || s[0] % 4 == 0) && (a.G == 1 || s[2] % 4 == 0);
+  };
+  const bool vec = a.S % 4 == 0 && on(a.Bm, a.sB) && on(a.Cm, a.sC);
   return by_lanes(a.S, [&](auto l) {
     constexpr int L = decltype(l)::value, CC = kStepThreads / L;
-    const int nx = (a.E + CC - 1) / CC;
-    if ((long long)nx * a.B >= 16LL * device_sms())
-      return launch_k(scan_step_kernel<T, L, 4>, dim3(nx, (a.B + 3) / 4), dim3(kStepThreads), 0, st, true, a);
-    return launch_k(scan_step_kernel<T, L, 1>, dim3(nx, a.B), dim3(kStepThreads), 0, st, true, a);
+    const dim3 grid((a.E + CC - 1) / CC, (a.B + R - 1) / R);
+    return vec ? launch_k(scan_step_kernel<T, L, R, true>, grid, dim3(kStepThreads), 0, st, true, a)
+               : launch_k(scan_step_kernel<T, L, R, false>, grid, dim3(kStepThreads), 0, st, true, a);
   });
 }
 
@@ -376,7 +409,10 @@ cudaError_t launch_scan_fwd(const ScanArgs &a, int bf16, const ScanSegs &seg, cu
 }
 
 cudaError_t launch_scan_step(const ScanArgs &a, int bf16, cudaStream_t st) {
-  return bf16 ? step_any<__nv_bfloat16>(a, st) : step_any<float>(a, st);
+  // Four sequences a thread once one each would give every SM over 16 CTAs.
+  const long long ctas = ((long long)a.E * lanes_of(a.S) + kStepThreads - 1) / kStepThreads * a.B;
+  if (ctas >= 16LL * device_sms()) return bf16 ? step_any<__nv_bfloat16, 4>(a, st) : step_any<float, 4>(a, st);
+  return bf16 ? step_any<__nv_bfloat16, 1>(a, st) : step_any<float, 1>(a, st);
 }
 
 }  // namespace ret
