@@ -303,6 +303,7 @@ struct ScanArgs {
   float *h_out = nullptr, *dA = nullptr, *dD = nullptr, *dbias = nullptr, *dh_in = nullptr;
   long long sx[2] = {}, sdt[2] = {}, sz[2] = {}, sdy[2] = {}, sy[2] = {}, sdx[2] = {}, sddt[2] = {},
             sdz[2] = {}, sB[3] = {}, sC[3] = {};
+  int pair_y = 0;  // y's rows begin on a pair's boundary (set by the launcher)
 };
 // Segments of a sequence that run at once; loc [count-1][B][E][S]: the state
 // that each segment but the last leaves behind from a zero state, sum

@@ -132,7 +132,7 @@ struct Block {
 
 // Two neighbouring channels of a row.
 template <typename T>
-struct Two {
+struct __align__(2 * sizeof(T)) Two {
   T a, b;
 };
 // kPair: the row begins on the pair's boundary.  n: channels that are there.
@@ -171,10 +171,18 @@ __device__ __forceinline__ void store_two(T *p, int n, float a, float b) {
 }
 
 
+template <typename T>
+__device__ __forceinline__ void store_pair(T *p, bool pair, int n, float a, float b) {
+  if (pair)
+    store_two<T, true>(p, n, a, b);
+  else
+    store_two<T, false>(p, n, a, b);
+}
+
 // Four neighbouring channels of a row as they were read; kVec: the row begins on
 // the four's boundary.  n: channels that are there.
 template <typename T>
-struct Four {
+struct __align__(4 * sizeof(T)) Four {
   T v[4];
 };
 template <typename T, bool kVec>

@@ -35,159 +35,10 @@ struct Geo {
   static constexpr int kChunk = 16 * L < 64 ? 16 * L : 64;   // tokens: two tiles of the first pass
   static constexpr int kBlock = 2 * kMain / L;               // channels of a CTA
   static constexpr int kTiles = kChunk / kTile;
+  static_assert(kChunk == 2 * Block<L>::kTile, "a chunk is two tiles of the first pass");
   static constexpr bool kTwice = L < 16;                     // B and C twice in shared memory, as pairs
   static __host__ __device__ int per_group(int E, int G) { return (E / G + kBlock - 1) / kBlock; }
 };
-
-template <int L>
-struct ChunksSmem {
-  float4 du[2][Block<L>::kTile][Block<L>::kChannels];  // delta, delta, u, u
-  float2 ds[2][Block<L>::kTile][Block<L>::kChannels];  // ds, ds
-  float bm[2][Block<L>::kTile][Block<L>::SP], cm[2][Block<L>::kTile][Block<L>::SP];
-};
-
-// What the chunks alone add: `run` chunks one after another by one CTA, half of
-// whose warps load and prepare the tokens ahead, as in the forward.
-template <typename T, int L, bool kPair>
-__global__ void __launch_bounds__(kThreads, 2)
-scan_bwd_chunks_kernel(const ScanArgs a, const ScanBwdPlan pl, int run, float *__restrict__ ws) {
-  using K = Block<L>;
-  constexpr int CC = K::kChannels, TT = K::kTile, SP = K::SP;
-  static_assert(Geo<L>::kChunk == 2 * TT, "a chunk is two tiles");
-  extern __shared__ __align__(16) uint8_t dyn[];
-  ChunksSmem<L> &sm = *reinterpret_cast<ChunksSmem<L> *>(dyn);
-  pdl_wait();
-  const int per = K::per_group(a.E, a.G), Eg = a.E / a.G;
-  const int blocks = a.G * per, first = blockIdx.x / blocks * run, blk = blockIdx.x % blocks;
-  const int group = blk / per, c0 = (blk - group * per) * CC, b = blockIdx.y;
-  const int n = tokens_of(a, b), t0 = first * pl.chunk, t1 = min(a.N, t0 + run * pl.chunk), live = min(t1, n);
-  // (every chunk writes what it adds, those behind the sequence's end nothing)
-  const int tiles = (min(first + run, pl.chunks) - first) * 2;
-
-  if (threadIdx.x < kScan) {
-    const int tid = threadIdx.x, ci = tid / L, s0 = tid % L * 4;
-    const bool own = c0 + ci < Eg, vec = a.S % 4 == 0;
-    const int e = group * Eg + min(c0 + ci, Eg - 1);
-    const float4 A4 = load_states(a.A + (size_t)e * a.S, s0, a.S, vec && reinterpret_cast<uintptr_t>(a.A) % 16 == 0);
-    const float2 A2[2] = {make_float2(A4.x * kLog2e, A4.y * kLog2e), make_float2(A4.z * kLog2e, A4.w * kLog2e)};
-    float2 h[2] = {both(0.f), both(0.f)}, P[2] = {both(1.f), both(1.f)}, g[2] = {both(0.f), both(0.f)};
-    float sum = 0.f;
-    __syncthreads();
-    for (int i = 0; i < tiles; ++i) {
-      const int buf = i & 1;
-      if (t0 + i * TT < live) {
-#pragma unroll 8
-        for (int j = 0; j < TT; ++j) {
-          const float4 v = sm.du[buf][j][ci];
-          const float2 dd = make_float2(v.x, v.y), uu = make_float2(v.z, v.w), ds = sm.ds[buf][j][ci];
-          const float4 B4 = *reinterpret_cast<const float4 *>(&sm.bm[buf][j][s0]), C4 = *reinterpret_cast<const float4 *>(&sm.cm[buf][j][s0]);
-          const float2 Bv[2] = {make_float2(B4.x, B4.y), make_float2(B4.z, B4.w)};
-          const float2 Cv[2] = {make_float2(C4.x, C4.y), make_float2(C4.z, C4.w)};
-          sum += v.x;
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const float2 w = tc::mul2(dd, A2[p]), d = make_float2(ex2(w.x), ex2(w.y));
-            h[p] = tc::fma2(d, h[p], tc::mul2(uu, Bv[p]));
-            P[p] = tc::mul2(P[p], d);
-            g[p] = tc::fma2(P[p], tc::mul2(ds, Cv[p]), g[p]);
-          }
-        }
-      }
-      __syncthreads();
-      if (i & 1) {
-        const size_t at = ((size_t)(first + i / 2) * a.B + b) * a.E + e;
-        if (own) {
-          store_states(ws + at * a.S, s0, a.S, vec, make_float4(h[0].x, h[0].y, h[1].x, h[1].y));
-          store_states(ws + pl.g + at * a.S, s0, a.S, vec, make_float4(g[0].x, g[0].y, g[1].x, g[1].y));
-          if (s0 == 0) ws[pl.sum + at] = sum;
-        }
-        h[0] = h[1] = g[0] = g[1] = both(0.f);
-        P[0] = P[1] = both(1.f);
-        sum = 0.f;
-      }
-    }
-    pdl_launch_dependents();
-    return;
-  }
-
-  constexpr int NP = TT * CC / 2 / kLoad, TS = 2 * kLoad / CC;
-  constexpr int NB = (TT * SP + kLoad - 1) / kLoad;
-  const int tid = threadIdx.x - kScan, lc = tid % (CC / 2) * 2, lt = tid / (CC / 2);
-  const int there = min(2, max(0, Eg - c0 - lc));
-  const int le = group * Eg + min(c0 + lc, Eg - 1);
-  const T *x = reinterpret_cast<const T *>(a.x) + b * a.sx[0] + le;
-  const T *dt = reinterpret_cast<const T *>(a.dt) + b * a.sdt[0] + le;
-  const T *dy = reinterpret_cast<const T *>(a.dy) + b * a.sdy[0] + le;
-  const T *z = a.z ? reinterpret_cast<const T *>(a.z) + b * a.sz[0] + le : nullptr;
-  const T *Bp = reinterpret_cast<const T *>(a.Bm) + b * a.sB[0] + group * a.sB[2];
-  const T *Cp = reinterpret_cast<const T *>(a.Cm) + b * a.sC[0] + group * a.sC[2];
-  const int l1 = there > 1;
-  const float bias[2] = {a.bias ? a.bias[le] : 0.f, a.bias ? a.bias[le + l1] : 0.f};
-  struct Raw {
-    Two<T> x[NP], z[NP], d[NP], y[NP];
-    T B[NB], C[NB];
-  };
-  auto load = [&](int i, Raw &r) {
-    const int t = t0 + i * TT;
-    if (i >= tiles || t >= live) return;
-#pragma unroll
-    for (int j = 0; j < NP; ++j) {
-      const int at = t + lt + j * TS, m = at < live ? there : 0;
-      r.x[j] = load_two<T, kPair>(x + at * a.sx[1], m);
-      r.d[j] = load_two<T, kPair>(dt + at * a.sdt[1], m);
-      r.y[j] = load_two<T, kPair>(dy + at * a.sdy[1], m);
-      r.z[j] = load_two<T, kPair>(z + at * a.sz[1], z ? m : 0);
-    }
-#pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      const int o = tid + j * kLoad, at = t + o / SP, s = o % SP;
-      const bool in = (NB * kLoad == TT * SP || o < TT * SP) && at < live && s < a.S;
-      r.B[j] = in ? Bp[at * a.sB[1] + s] : from_float<T>(0.f);
-      r.C[j] = in ? Cp[at * a.sC[1] + s] : from_float<T>(0.f);
-    }
-  };
-  auto put = [&](int i, const Raw &r) {
-    const int buf = i & 1, t = t0 + i * TT;
-    if (i >= tiles || t >= live) return;
-#pragma unroll
-    for (int j = 0; j < NP; ++j) {
-      const int at = lt + j * TS;
-      const float xs[2] = {to_float(r.x[j].a), to_float(r.x[j].b)}, zs[2] = {to_float(r.z[j].a), to_float(r.z[j].b)};
-      const float ys[2] = {to_float(r.y[j].a), to_float(r.y[j].b)};
-      float d[2] = {to_float(r.d[j].a) + bias[0], to_float(r.d[j].b) + bias[1]};
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        if (a.softplus) d[c] = softplus(d[c]);
-        if (!(c < there && t + at < live)) d[c] = 0.f;
-        const float u = d[c] * xs[c], ds = z ? ys[c] * silu(zs[c]) : ys[c];
-        sm.du[buf][at][lc + c] = make_float4(d[c], d[c], u, u);
-        sm.ds[buf][at][lc + c] = both(ds);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      const int o = tid + j * kLoad;
-      if (NB * kLoad == TT * SP || o < TT * SP) {
-        (&sm.bm[buf][0][0])[o] = to_float(r.B[j]);
-        (&sm.cm[buf][0][0])[o] = to_float(r.C[j]);
-      }
-    }
-  };
-  Raw even, odd;
-  load(0, even);
-  load(1, odd);
-  put(0, even);
-  __syncthreads();
-  for (int i = 0; i < tiles; i += 2) {  // (an even number)
-    load(i + 2, even);
-    put(i + 1, odd);
-    __syncthreads();
-    load(i + 3, odd);
-    put(i + 2, even);
-    __syncthreads();
-  }
-  pdl_launch_dependents();
-}
 
 // The state before each chunk (y = 0) and the gradient that arrives behind it
 // (y = 1), in the places of what the chunks add; also dh_in.  Eight chunks'
@@ -591,27 +442,13 @@ scan_bwd_bc_kernel(const ScanArgs a, const ScanBwdPlan pl, const float *__restri
   out[row * a.S + (j < a.S ? j : j - a.S)] = from_float<T>(v);
 }
 
-// Vectors of `step` channels in every tensor?
-bool vectors_ok(const ScanArgs &a, int esz, int step, bool outputs) {
+// Vectors of four channels in every tensor?
+bool vectors_ok(const ScanArgs &a, int esz) {
+  constexpr int step = 4;
   return a.E / a.G % step == 0 && rows_on(a, a.x, a.sx, step, esz) && rows_on(a, a.dt, a.sdt, step, esz) &&
          rows_on(a, a.dy, a.sdy, step, esz) && rows_on(a, a.z, a.sz, step, esz) &&
-         (!outputs || (rows_on(a, a.dx, a.sdx, step, esz) && rows_on(a, a.ddt, a.sddt, step, esz) &&
-                       (!a.z || rows_on(a, a.dz, a.sdz, step, esz))));
-}
-
-// Chunks that a CTA of the first pass takes one after another: up to 8, so
-// that its loads run ahead, while all SMs keep two CTAs.
-template <typename T, int L, bool kPair>
-cudaError_t chunks_with(const ScanArgs &a, const ScanBwdPlan &pl, float *ws, cudaStream_t st) {
-  static std::atomic<unsigned> done{0};
-  auto kern = scan_bwd_chunks_kernel<T, L, kPair>;
-  const cudaError_t e = allow_big_smem(reinterpret_cast<const void *>(kern), done);
-  if (e != cudaSuccess) return e;
-  const long long blocks = (long long)a.G * Block<L>::per_group(a.E, a.G);
-  int run = 8;
-  while (run > 1 && blocks * a.B * ((pl.chunks + run - 1) / run) < 4LL * device_sms()) run /= 2;
-  const dim3 grid((unsigned)(blocks * ((pl.chunks + run - 1) / run)), a.B);
-  return launch_k(kern, grid, dim3(kThreads), sizeof(ChunksSmem<L>), st, true, a, pl, run, ws);
+         rows_on(a, a.dx, a.sdx, step, esz) && rows_on(a, a.ddt, a.sddt, step, esz) &&
+         (!a.z || rows_on(a, a.dz, a.sdz, step, esz));
 }
 
 template <typename T, int L, bool kVec>
@@ -625,17 +462,8 @@ cudaError_t main_with(const ScanArgs &a, const ScanBwdPlan &pl, float *ws, cudaS
 }
 
 template <typename T>
-cudaError_t chunks_any(const ScanArgs &a, const ScanBwdPlan &pl, float *ws, cudaStream_t st) {
-  const bool pair = vectors_ok(a, sizeof(T), 2, false);
-  return by_lanes(a.S, [&](auto l) {
-    constexpr int L = decltype(l)::value;
-    return pair ? chunks_with<T, L, true>(a, pl, ws, st) : chunks_with<T, L, false>(a, pl, ws, st);
-  });
-}
-
-template <typename T>
 cudaError_t main_any(const ScanArgs &a, const ScanBwdPlan &pl, float *ws, cudaStream_t st) {
-  const bool vec = vectors_ok(a, sizeof(T), 4, true);
+  const bool vec = vectors_ok(a, sizeof(T));
   return by_lanes(a.S, [&](auto l) {
     constexpr int L = decltype(l)::value;
     return vec ? main_with<T, L, true>(a, pl, ws, st) : main_with<T, L, false>(a, pl, ws, st);
@@ -661,10 +489,6 @@ ScanBwdPlan scan_bwd_plan(const ScanArgs &a) {
   pl.bc = pl.dd + up(2 * pl.chunks * be);
   pl.total = pl.bc + (size_t)pl.blocks * a.B * a.N * a.G * 2 * a.S;
   return pl;
-}
-
-cudaError_t launch_scan_bwd_chunks(const ScanArgs &a, int bf16, const ScanBwdPlan &pl, float *ws, cudaStream_t st) {
-  return bf16 ? chunks_any<__nv_bfloat16>(a, pl, ws, st) : chunks_any<float>(a, pl, ws, st);
 }
 
 cudaError_t launch_scan_bwd_carry(const ScanArgs &a, const ScanBwdPlan &pl, float *ws, cudaStream_t st) {

@@ -20,29 +20,60 @@ namespace {
 
 using namespace scan;
 
-template <int L>
-struct FwdSmem {
-  float4 du[2][Block<L>::kTile][Block<L>::kChannels];  // delta, delta, u, u
-  float bm[2][Block<L>::kTile][Block<L>::SP], cm[2][Block<L>::kTile][Block<L>::SP];
-  float ysum[2][Block<L>::kTile][Block<L>::kChannels];
+// What the walk over the tokens is for: the outputs, the states that segments
+// leave behind, or (for the gradients) what chunks alone add.
+enum { kOut = 0, kStates = 1, kChunks = 2 };
+
+// A tile's rows as they were read, in a ring of kRing: kAhead tiles are on their
+// way, the tile before the current one still has its outputs to be finished.
+template <typename T, int L, int kMode>
+struct __align__(16) Tile {
+  static constexpr int kAhead = sizeof(T) == 2 ? 4 : 2, kRing = kAhead + 2;
+  T x[Block<L>::kTile][Block<L>::kChannels], dt[Block<L>::kTile][Block<L>::kChannels];
+  T z[kMode == kStates ? 1 : Block<L>::kTile][Block<L>::kChannels];
+  T dy[kMode == kChunks ? Block<L>::kTile : 1][Block<L>::kChannels];
+  T B[Block<L>::kTile][Block<L>::SP], C[kMode == kStates ? 1 : Block<L>::kTile][Block<L>::SP];
 };
 
-// Half of the CTA's warps walk the recurrence; the others load the tokens two
-// tiles ahead, work out step sizes and inputs, and finish the outputs of the
+template <typename T, int L, int kMode>
+struct WalkSmem {
+  __align__(16) Tile<T, L, kMode> ring[Tile<T, L, kMode>::kRing];
+  float2 du[2][Block<L>::kTile][Block<L>::kChannels];  // delta, u
+  // sums over the states (outputs), or ds (chunks)
+  float more[kMode == kStates ? 1 : 2][Block<L>::kTile][Block<L>::kChannels];
+};
+
+template <typename T>
+__device__ __forceinline__ void four_states(const T *p, float2 (&v)[2]) {
+  const Four<T> f = load_four<T, true>(p, 4);
+  v[0] = make_float2(to_float(f.v[0]), to_float(f.v[1]));
+  v[1] = make_float2(to_float(f.v[2]), to_float(f.v[3]));
+}
+
+// Half of the CTA's warps walk the recurrence; the others keep the ring filled,
+// work out step sizes and inputs a tile ahead, and finish the outputs of the
 // tile before: with one sequence an SM has no more than one recurrence warp a
 // scheduler, and everything else that a token needs runs beside it.
-// kStates: only the states that the segments leave behind.
-template <typename T, int L, bool kStates, bool kPair>
+// Bound by shared memory and the recurrence warps' own latency: a lane reads its
+// four states' B and C for each token (as bf16 where they are: 16 bytes a lane,
+// fp32 32), which every lane-byte costs, equal or not.  Loads that wait in
+// registers instead of a ring had a tile's time to arrive: 479 us for 8192 x 4096 x
+// 16 bf16.
+// kAsync: every row begins on a 16-byte boundary and arrives by asynchronous
+// copies; else the loaders read value by value.
+template <typename T, int L, int kMode, bool kAsync>
 __global__ void __launch_bounds__(kThreads, 2)
-scan_fwd_kernel(const ScanArgs a, const ScanSegs seg) {
+scan_walk_kernel(const ScanArgs a, const ScanSegs seg, const ScanBwdPlan pl, float *__restrict__ ws) {
   using K = Block<L>;
-  constexpr int CC = K::kChannels, TT = K::kTile, SP = K::SP;
+  using Row = Tile<T, L, kMode>;
+  constexpr int CC = K::kChannels, TT = K::kTile, SP = K::SP, kAhead = Row::kAhead, kRing = Row::kRing;
   extern __shared__ __align__(16) uint8_t dyn[];
-  FwdSmem<L> &sm = *reinterpret_cast<FwdSmem<L> *>(dyn);
+  WalkSmem<T, L, kMode> &sm = *reinterpret_cast<WalkSmem<T, L, kMode> *>(dyn);
   pdl_wait();
-  const int per = K::per_group(a.E, a.G), Eg = a.E / a.G;
-  const int group = blockIdx.x / per, c0 = (blockIdx.x - group * per) * CC;  // within the group
-  const int b = blockIdx.z, k = blockIdx.y;
+  const int per = K::per_group(a.E, a.G), Eg = a.E / a.G, blocks = a.G * per;
+  const int k = blockIdx.x / blocks, blk = blockIdx.x - k * blocks;  // segment; block of channels
+  const int group = blk / per, c0 = (blk - group * per) * CC;        // within the group
+  const int b = blockIdx.y;
   const int n = tokens_of(a, b), t0 = k * seg.len, t1 = min(a.N, t0 + seg.len), live = min(t1, n);
   const int tiles = live > t0 ? (live - t0 + TT - 1) / TT : 0;
 
@@ -52,208 +83,220 @@ scan_fwd_kernel(const ScanArgs a, const ScanSegs seg) {
     const bool own = c0 + ci < Eg, vec = a.S % 4 == 0;
     const int e = group * Eg + min(c0 + ci, Eg - 1);
     const float4 A4 = load_states(a.A + (size_t)e * a.S, s0, a.S, vec && reinterpret_cast<uintptr_t>(a.A) % 16 == 0);
-    const float2 A01 = make_float2(A4.x * kLog2e, A4.y * kLog2e), A23 = make_float2(A4.z * kLog2e, A4.w * kLog2e);
-    float2 h01 = both(0.f), h23 = both(0.f);
+    const float2 A2[2] = {make_float2(A4.x * kLog2e, A4.y * kLog2e), make_float2(A4.z * kLog2e, A4.w * kLog2e)};
+    float2 h[2] = {both(0.f), both(0.f)};
+    float2 P[2] = {both(1.f), both(1.f)}, g[2] = {both(0.f), both(0.f)};  // (chunks)
+    float sum = 0.f;
     const size_t row = ((size_t)b * a.E + e) * a.S;
-    if (!kStates) {
+    if (kMode == kOut) {
       // the state that the segments before this one leave behind
       if (a.h_in) {
-        const float4 h = load_states(a.h_in + row, s0, a.S, vec && reinterpret_cast<uintptr_t>(a.h_in) % 16 == 0);
-        h01 = make_float2(h.x, h.y);
-        h23 = make_float2(h.z, h.w);
+        const float4 v = load_states(a.h_in + row, s0, a.S, vec && reinterpret_cast<uintptr_t>(a.h_in) % 16 == 0);
+        h[0] = make_float2(v.x, v.y);
+        h[1] = make_float2(v.z, v.w);
       }
       for (int i = 0; i < k; ++i) {
         const float2 d = both(seg.sum[((size_t)i * a.B + b) * a.E + e]);
         const float4 l = load_states(seg.loc + (size_t)i * a.B * a.E * a.S + row, s0, a.S, vec);
-        const float2 w01 = tc::mul2(d, A01), w23 = tc::mul2(d, A23);
-        h01 = tc::fma2(make_float2(ex2(w01.x), ex2(w01.y)), h01, make_float2(l.x, l.y));
-        h23 = tc::fma2(make_float2(ex2(w23.x), ex2(w23.y)), h23, make_float2(l.z, l.w));
+        const float2 w0 = tc::mul2(d, A2[0]), w1 = tc::mul2(d, A2[1]);
+        h[0] = tc::fma2(make_float2(ex2(w0.x), ex2(w0.y)), h[0], make_float2(l.x, l.y));
+        h[1] = tc::fma2(make_float2(ex2(w1.x), ex2(w1.y)), h[1], make_float2(l.z, l.w));
       }
     }
+    auto leave_chunk = [&](int i) {  // what chunk i of the segment adds
+      const size_t at = ((size_t)(t0 / (2 * TT) + i) * a.B + b) * a.E + e;
+      if (own) {
+        store_states(ws + at * a.S, s0, a.S, vec, make_float4(h[0].x, h[0].y, h[1].x, h[1].y));
+        store_states(ws + pl.g + at * a.S, s0, a.S, vec, make_float4(g[0].x, g[0].y, g[1].x, g[1].y));
+        if (s0 == 0) ws[pl.sum + at] = sum;
+      }
+      h[0] = h[1] = g[0] = g[1] = both(0.f);
+      P[0] = P[1] = both(1.f);
+      sum = 0.f;
+    };
     __syncthreads();
-    for (int i = 0; i < tiles; ++i) {
+    for (int i = 0, slot = 0; i < tiles; ++i, slot = slot + 1 == kRing ? 0 : slot + 1) {
       const int buf = i & 1;
-      // (16 tokens' outputs are stored at once: a store between them would hold
-      // back the loads behind it, and a warp alone on its scheduler has nothing
-      // else to do; 76 cycles a token with stores every 4 tokens)
-      constexpr int GT = TT < 16 ? TT : 16;
+      const Row &r = sm.ring[slot];
+      float part = 0.f;
+      // (a store to shared memory holds back the loads behind it, and a warp alone
+      // on its scheduler has nothing else to do: outputs of 8 tokens at a time)
+      constexpr int GT = 8;
 #pragma unroll
       for (int q = 0; q < TT; q += GT) {
         float yq[GT / 4][4];
 #pragma unroll
         for (int j = 0; j < GT; ++j) {
-          const float4 v = sm.du[buf][q + j][ci];
-          const float4 B4 = *reinterpret_cast<const float4 *>(&sm.bm[buf][q + j][s0]);
-          const float2 dd = make_float2(v.x, v.y), uu = make_float2(v.z, v.w);
-          const float2 w01 = tc::mul2(dd, A01), w23 = tc::mul2(dd, A23);
-          const float2 i01 = tc::mul2(uu, make_float2(B4.x, B4.y)), i23 = tc::mul2(uu, make_float2(B4.z, B4.w));
-          h01 = tc::fma2(make_float2(ex2(w01.x), ex2(w01.y)), h01, i01);
-          h23 = tc::fma2(make_float2(ex2(w23.x), ex2(w23.y)), h23, i23);
-          if (!kStates) {
-            const float4 C4 = *reinterpret_cast<const float4 *>(&sm.cm[buf][q + j][s0]);
-            const float2 s = tc::fma2(h23, make_float2(C4.z, C4.w), tc::mul2(h01, make_float2(C4.x, C4.y)));
+          const float2 v = sm.du[buf][q + j][ci], dd = both(v.x), uu = both(v.y);
+          float2 Bv[2], Cv[2], s;
+          four_states(&r.B[q + j][s0], Bv);
+          if (kMode != kStates) four_states(&r.C[q + j][s0], Cv);
+          if (kMode != kOut) part += v.x;
+          const float2 ds = kMode == kChunks ? both(sm.more[buf][q + j][ci]) : both(0.f);
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const float2 w = tc::mul2(dd, A2[p]), d = make_float2(ex2(w.x), ex2(w.y));
+            h[p] = tc::fma2(d, h[p], tc::mul2(uu, Bv[p]));
+            if (kMode == kOut) s = p ? tc::fma2(h[p], Cv[p], s) : tc::mul2(h[p], Cv[p]);
+            if (kMode == kChunks) {
+              P[p] = tc::mul2(P[p], d);
+              g[p] = tc::fma2(P[p], tc::mul2(ds, Cv[p]), g[p]);
+            }
+          }
+          if (kMode == kOut) {
             yq[j / 4][j % 4] = s.x + s.y;
             if (j % 4 == 3) share_sums<4, L>(yq[j / 4]);
           }
         }
-        if (!kStates) {
+        if (kMode == kOut) {
           constexpr int M = L < 4 ? L : 4;
           if (tid % L < M)
 #pragma unroll
             for (int i4 = 0; i4 < GT / 4; ++i4)
 #pragma unroll
-              for (int j = 0; j < 4 / M; ++j) sm.ysum[buf][q + i4 * 4 + tid % M * (4 / M) + j][ci] = yq[i4][j];
+              for (int j = 0; j < 4 / M; ++j) sm.more[buf][q + i4 * 4 + tid % M * (4 / M) + j][ci] = yq[i4][j];
         }
       }
       __syncthreads();
+      sum += part;
+      if (kMode == kChunks && (i & 1)) leave_chunk(i / 2);
     }
     pdl_launch_dependents();
-    const float4 h4 = make_float4(h01.x, h01.y, h23.x, h23.y);
-    if (kStates) {
-      if (own) store_states(seg.loc + (size_t)k * a.B * a.E * a.S + row, s0, a.S, vec, h4);
-    } else if (k == seg.count - 1 && own && a.h_out) {
-      store_states(a.h_out + row, s0, a.S, vec && reinterpret_cast<uintptr_t>(a.h_out) % 16 == 0, h4);
+    const float4 h4 = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
+    if (kMode == kStates) {
+      if (own) {
+        store_states(seg.loc + (size_t)k * a.B * a.E * a.S + row, s0, a.S, vec, h4);
+        if (s0 == 0) seg.sum[((size_t)k * a.B + b) * a.E + e] = sum;
+      }
+    } else if (kMode == kOut) {
+      if (k == seg.count - 1 && own && a.h_out)
+        store_states(a.h_out + row, s0, a.S, vec && reinterpret_cast<uintptr_t>(a.h_out) % 16 == 0, h4);
+    } else {  // a chunk that ends early, and those behind the sequence's end
+      for (int i = tiles / 2; i < (t1 - t0 + 2 * TT - 1) / (2 * TT); ++i) leave_chunk(i);
     }
-    if (kStates) __syncthreads();
     return;
   }
 
-  // ---- two channels' tokens, NP of each tile
+  // ---- loaders; each has two channels of NP tokens of a tile
   constexpr int NP = TT * CC / 2 / kLoad, TS = 2 * kLoad / CC;  // pairs a thread; tokens between them
-  constexpr int NB = (TT * SP + kLoad - 1) / kLoad;
   static_assert(NP * kLoad * 2 == TT * CC && NP * TS == TT, "whole tiles");
   const int tid = threadIdx.x - kScan, lc = tid % (CC / 2) * 2, lt = tid / (CC / 2);
   const int there = min(2, max(0, Eg - c0 - lc));  // channels of this pair
   const int le = group * Eg + min(c0 + lc, Eg - 1);
-  const T *x = reinterpret_cast<const T *>(a.x) + b * a.sx[0] + le;
-  const T *dt = reinterpret_cast<const T *>(a.dt) + b * a.sdt[0] + le;
-  const T *z = kStates || !a.z ? nullptr : reinterpret_cast<const T *>(a.z) + b * a.sz[0] + le;
-  const T *Bp = reinterpret_cast<const T *>(a.Bm) + b * a.sB[0] + group * a.sB[2];
-  const T *Cp = reinterpret_cast<const T *>(a.Cm) + b * a.sC[0] + group * a.sC[2];
   T *y = reinterpret_cast<T *>(a.y) + b * a.sy[0] + le;
   const int l1 = there > 1;
   const float bias[2] = {a.bias ? a.bias[le] : 0.f, a.bias ? a.bias[le + l1] : 0.f};
-  const float Dv[2] = {!kStates && a.D ? a.D[le] : 0.f, !kStates && a.D ? a.D[le + l1] : 0.f};
-  float dsum[2] = {0.f, 0.f};
+  const float Dv[2] = {kMode == kOut && a.D ? a.D[le] : 0.f, kMode == kOut && a.D ? a.D[le + l1] : 0.f};
+  const bool gate = kMode != kStates && a.z, pairs = kAsync || (a.E / a.G % 2 == 0 && a.pair_y);
 
-  struct Raw {
-    Two<T> x[NP], z[NP], d[NP];
-    T B[NB], C[NB];
-  };
-  struct Kept {
-    Two<T> x[NP], z[NP];
-  };
-  auto load = [&](int i, Raw &r) {
-    if (i >= tiles) return;
-    const int t = t0 + i * TT;
-#pragma unroll
-    for (int j = 0; j < NP; ++j) {
-      const int at = t + lt + j * TS, m = at < live ? there : 0;
-      r.x[j] = load_two<T, kPair>(x + at * a.sx[1], m);
-      r.d[j] = load_two<T, kPair>(dt + at * a.sdt[1], m);
-      if (!kStates) r.z[j] = load_two<T, kPair>(z + at * a.sz[1], z ? m : 0);
-    }
-#pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      const int o = tid + j * kLoad, at = t + o / SP, s = o % SP;
-      const bool in = (NB * kLoad == TT * SP || o < TT * SP) && at < live && s < a.S;
-      r.B[j] = in ? Bp[at * a.sB[1] + s] : from_float<T>(0.f);
-      if (!kStates) r.C[j] = in ? Cp[at * a.sC[1] + s] : from_float<T>(0.f);
+  // Rows of a tile, `width` of their values there, into the ring.
+  auto fetch_rows = [&](T *to, const void *from, long long stride, int row0, int cols, int width) {
+    constexpr int V = 16 / sizeof(T);
+    if (kAsync) {
+      const int nv = cols / V;
+      for (int o = tid; o < TT * nv; o += kLoad) {
+        const int t = o / nv, c = o - t * nv;
+        const bool in = row0 + t < live && c * V < width;
+        const T *p = reinterpret_cast<const T *>(from) + (in ? (row0 + t) * stride + c * V : 0);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(to + t * cols + c * V)), "l"(p),
+                     "r"(in ? 16 : 0)
+                     : "memory");
+      }
+    } else {
+#pragma unroll 4
+      for (int o = tid; o < TT * cols; o += kLoad) {
+        const int t = o / cols, c = o - t * cols;
+        const bool in = row0 + t < live && c < width;
+        to[o] = in ? reinterpret_cast<const T *>(from)[(row0 + t) * stride + c] : from_float<T>(0.f);
+      }
     }
   };
-  // What was loaded for tile i becomes delta, u, B and C; past the end delta and
-  // u are 0 and leave the state as it is.
-  auto put = [&](int i, const Raw &r) {
+  auto at_block = [&](const void *p, const long long s[2]) {
+    return reinterpret_cast<const T *>(p) + b * s[0] + group * Eg + c0;
+  };
+  auto fetch = [&](int i) {
+    if (i < tiles) {
+      Row &r = sm.ring[i % kRing];
+      const int t = t0 + i * TT, width = min(CC, Eg - c0);
+      fetch_rows(&r.x[0][0], at_block(a.x, a.sx), a.sx[1], t, CC, width);
+      fetch_rows(&r.dt[0][0], at_block(a.dt, a.sdt), a.sdt[1], t, CC, width);
+      if (gate) fetch_rows(&r.z[0][0], at_block(a.z, a.sz), a.sz[1], t, CC, width);
+      if (kMode == kChunks) fetch_rows(&r.dy[0][0], at_block(a.dy, a.sdy), a.sdy[1], t, CC, width);
+      fetch_rows(&r.B[0][0], reinterpret_cast<const T *>(a.Bm) + b * a.sB[0] + group * a.sB[2], a.sB[1], t, SP, a.S);
+      if (kMode != kStates)
+        fetch_rows(&r.C[0][0], reinterpret_cast<const T *>(a.Cm) + b * a.sC[0] + group * a.sC[2], a.sC[1], t, SP, a.S);
+    }
+    if (kAsync) asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto two = [&](const T(*rows)[CC], int t) { return *reinterpret_cast<const Two<T> *>(&rows[t][lc]); };
+  // Tile i's rows become delta, u (and ds); past the end delta and u are 0 and
+  // leave the state as it is.
+  auto put = [&](int i) {
     const int buf = i & 1, t = t0 + i * TT;
-    float part[2] = {0.f, 0.f};
+    const Row &r = sm.ring[i % kRing];
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
       const int at = lt + j * TS;
-      const float xs[2] = {to_float(r.x[j].a), to_float(r.x[j].b)};
-      float d[2] = {to_float(r.d[j].a) + bias[0], to_float(r.d[j].b) + bias[1]};
+      const Two<T> xr = two(r.x, at), dr = two(r.dt, at);
+      const float xs[2] = {to_float(xr.a), to_float(xr.b)};
+      float d[2] = {to_float(dr.a) + bias[0], to_float(dr.b) + bias[1]};
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         if (a.softplus) d[c] = softplus(d[c]);
         if (!(c < there && t + at < live)) d[c] = 0.f;
-        const float u = d[c] * xs[c];
-        sm.du[buf][at][lc + c] = make_float4(d[c], d[c], u, u);
-        if (kStates) part[c] += d[c];
       }
-    }
-    if (kStates) {
-      dsum[0] += part[0];
-      dsum[1] += part[1];
-    }
-#pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      const int o = tid + j * kLoad;
-      if (NB * kLoad == TT * SP || o < TT * SP) {
-        (&sm.bm[buf][0][0])[o] = to_float(r.B[j]);
-        if (!kStates) (&sm.cm[buf][0][0])[o] = to_float(r.C[j]);
+      *reinterpret_cast<float4 *>(&sm.du[buf][at][lc]) = make_float4(d[0], d[0] * xs[0], d[1], d[1] * xs[1]);
+      if (kMode == kChunks) {
+        const Two<T> yr = two(r.dy, at), zr = two(r.z, at);
+        float2 ds = make_float2(to_float(yr.a), to_float(yr.b));
+        if (gate) {
+          ds.x *= silu(to_float(zr.a));
+          ds.y *= silu(to_float(zr.b));
+        }
+        *reinterpret_cast<float2 *>(&sm.more[buf][at][lc]) = ds;
       }
     }
   };
-  auto finish = [&](int i, const Kept &r) {
+  auto finish = [&](int i) {
     const int buf = i & 1, t = t0 + i * TT;
+    const Row &r = sm.ring[i % kRing];
 #pragma unroll
-    for (int j = 0; j < (kStates ? 0 : NP); ++j) {
+    for (int j = 0; j < NP; ++j) {
       const int at = lt + j * TS;
-      const float2 s = *reinterpret_cast<const float2 *>(&sm.ysum[buf][at][lc]);
-      float v0 = fmaf(Dv[0], to_float(r.x[j].a), s.x), v1 = fmaf(Dv[1], to_float(r.x[j].b), s.y);
-      if (z) {
-        v0 *= silu(to_float(r.z[j].a));
-        v1 *= silu(to_float(r.z[j].b));
+      const float2 s = *reinterpret_cast<const float2 *>(&sm.more[buf][at][lc]);
+      const Two<T> xr = two(r.x, at), zr = two(r.z, at);
+      float v0 = fmaf(Dv[0], to_float(xr.a), s.x), v1 = fmaf(Dv[1], to_float(xr.b), s.y);
+      if (gate) {
+        v0 *= silu(to_float(zr.a));
+        v1 *= silu(to_float(zr.b));
       }
       const bool in = t + at < live;
-      if (t + at < t1) store_two<T, kPair>(y + (t + at) * a.sy[1], there, in ? v0 : 0.f, in ? v1 : 0.f);
+      if (t + at < t1) store_pair(y + (t + at) * a.sy[1], pairs, there, in ? v0 : 0.f, in ? v1 : 0.f);
     }
   };
-  auto keep = [&](const Raw &r, Kept &q) {
-#pragma unroll
-    for (int j = 0; j < (kStates ? 0 : NP); ++j) {
-      q.x[j] = r.x[j];
-      q.z[j] = r.z[j];
-    }
+  // Wait until all but the newest n tiles have arrived, then (all loaders') data is visible.
+  auto arrived = [&] {
+    if (kAsync) asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 2) : "memory");
   };
 
-  // Two buffers of what is on its way, each known by name (a copy from one to the
-  // other would wait for the loads).
-  Raw even, odd;
-  Kept cur, done;
-  load(0, even);
-  load(1, odd);
-  if (tiles > 0) put(0, even);
-  keep(even, cur);
+#pragma unroll 1
+  for (int i = 0; i < kAhead; ++i) fetch(i);
+  arrived();
+  asm volatile("bar.sync 1, %0;" ::"n"(kLoad) : "memory");
+  if (tiles > 0) put(0);
   __syncthreads();
-  auto turn = [&](int i, Raw &next, Raw &free) {  // next: tile i + 1
-    load(i + 2, free);
-    if (i > 0) finish(i - 1, done);
-    if (i + 1 < tiles) put(i + 1, next);
+#pragma unroll 1
+  for (int i = 0; i < tiles; ++i) {
+    fetch(i + kAhead);
+    if (kMode == kOut && i > 0) finish(i - 1);
+    if (i + 1 < tiles) put(i + 1);
+    arrived();
     __syncthreads();
-    done = cur;
-    keep(next, cur);
-  };
-  for (int i = 0; i < tiles; i += 2) {
-    turn(i, odd, even);
-    if (i + 1 < tiles) turn(i + 1, even, odd);
   }
-  if (tiles > 0) finish(tiles - 1, done);
+  if (kMode == kOut && tiles > 0) finish(tiles - 1);
   pdl_launch_dependents();
-  if (!kStates) {  // whole tiles past the sequence's end
-    for (int at = t0 + tiles * TT + lt; at < t1; at += TS) store_two<T, kPair>(y + at * a.sy[1], there, 0.f, 0.f);
-  } else {
-    // the loaders' sums of a channel, in order (the walk over the tiles is over)
-    float *red = &sm.ysum[0][0][0];
-    red[lt * CC + lc] = dsum[0];
-    red[lt * CC + lc + 1] = dsum[1];
-    __syncthreads();
-    if (tid < CC && c0 + tid < Eg) {
-      float s = 0.f;
-#pragma unroll
-      for (int i = 0; i < TS; ++i) s += red[i * CC + tid];
-      seg.sum[((size_t)k * a.B + b) * a.E + group * Eg + c0 + tid] = s;
-    }
-  }
+  if (kMode == kOut)  // whole tiles past the sequence's end
+    for (int at = t0 + tiles * TT + lt; at < t1; at += TS) store_pair(y + at * a.sy[1], pairs, there, 0.f, 0.f);
 }
 
 // One token.  A lane has four states of R sequences' same channel, so that A is
@@ -331,30 +374,45 @@ scan_step_kernel(const ScanArgs a) {
   }
 }
 
-// Pairs of channels are read and written at once where every row of every
-// tensor (and every block of channels) begins on a pair's boundary.
-bool pairs_ok(const ScanArgs &a, int esz, bool states) {
-  return a.E / a.G % 2 == 0 && rows_on(a, a.x, a.sx, 2, esz) && rows_on(a, a.dt, a.sdt, 2, esz) &&
-         (states || (rows_on(a, a.z, a.sz, 2, esz) && rows_on(a, a.y, a.sy, 2, esz)));
+// Asynchronous copies of 16 bytes where every row of every tensor (and every
+// block of channels, and every row of B and C) is made of whole ones.
+template <typename T>
+bool async_ok(const ScanArgs &a, int mode) {
+  constexpr int V = 16 / sizeof(T), esz = sizeof(T);
+  auto bc = [&](const void *p, const long long s[3]) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (a.N <= 1 || s[1] % V == 0) && (a.B <= 1 || s[0] % V == 0) &&
+           (a.G <= 1 || s[2] % V == 0);
+  };
+  return a.E / a.G % V == 0 && a.S % V == 0 && bc(a.Bm, a.sB) && (mode == kStates || bc(a.Cm, a.sC)) &&
+         rows_on(a, a.x, a.sx, V, esz) && rows_on(a, a.dt, a.sdt, V, esz) && (mode == kStates || rows_on(a, a.z, a.sz, V, esz)) &&
+         (mode != kChunks || rows_on(a, a.dy, a.sdy, V, esz)) && (mode != kOut || a.pair_y);
 }
 
-template <typename T, int L, bool kStates, bool kPair>
-cudaError_t scan_with(const ScanArgs &a, const ScanSegs &seg, int segs, cudaStream_t st) {
+template <typename T, int L, int kMode, bool kAsync>
+cudaError_t walk_with(const ScanArgs &a, const ScanSegs &seg, const ScanBwdPlan &pl, float *ws, cudaStream_t st) {
   static std::atomic<unsigned> done{0};
-  auto kern = scan_fwd_kernel<T, L, kStates, kPair>;
+  auto kern = scan_walk_kernel<T, L, kMode, kAsync>;
   const cudaError_t e = allow_big_smem(reinterpret_cast<const void *>(kern), done);
   if (e != cudaSuccess) return e;
-  const dim3 grid(a.G * Block<L>::per_group(a.E, a.G), segs, a.B);
-  return launch_k(kern, grid, dim3(kThreads), sizeof(FwdSmem<L>), st, true, a, seg);
+  // (the states of the last segment are nobody's entry)
+  const int segs = kMode == kStates ? seg.count - 1 : seg.count;
+  const dim3 grid((unsigned)(a.G * Block<L>::per_group(a.E, a.G)) * segs, a.B);
+  return launch_k(kern, grid, dim3(kThreads), sizeof(WalkSmem<T, L, kMode>), st, true, a, seg, pl, ws);
 }
 
-template <typename T, bool kStates>
-cudaError_t scan_any(const ScanArgs &a, const ScanSegs &seg, int segs, cudaStream_t st) {
+template <typename T, int kMode>
+cudaError_t walk_any(ScanArgs a, const ScanSegs &seg, const ScanBwdPlan &pl, float *ws, cudaStream_t st) {
+  a.pair_y = rows_on(a, a.y, a.sy, 2, sizeof(T));
+  const bool async = async_ok<T>(a, kMode);
   return by_lanes(a.S, [&](auto l) {
     constexpr int L = decltype(l)::value;
-    return pairs_ok(a, sizeof(T), kStates) ? scan_with<T, L, kStates, true>(a, seg, segs, st)
-                                           : scan_with<T, L, kStates, false>(a, seg, segs, st);
+    return async ? walk_with<T, L, kMode, true>(a, seg, pl, ws, st) : walk_with<T, L, kMode, false>(a, seg, pl, ws, st);
   });
+}
+
+template <int kMode>
+cudaError_t walk(const ScanArgs &a, int bf16, const ScanSegs &seg, const ScanBwdPlan &pl, float *ws, cudaStream_t st) {
+  return bf16 ? walk_any<__nv_bfloat16, kMode>(a, seg, pl, ws, st) : walk_any<float, kMode>(a, seg, pl, ws, st);
 }
 
 template <typename T, int R>
@@ -399,13 +457,27 @@ size_t scan_fwd_bytes(const ScanArgs &a) {
 }
 
 cudaError_t launch_scan_states(const ScanArgs &a, int bf16, const ScanSegs &seg, cudaStream_t st) {
-  return bf16 ? scan_any<__nv_bfloat16, true>(a, seg, seg.count - 1, st)
-              : scan_any<float, true>(a, seg, seg.count - 1, st);
+  return walk<kStates>(a, bf16, seg, ScanBwdPlan(), nullptr, st);
 }
 
 cudaError_t launch_scan_fwd(const ScanArgs &a, int bf16, const ScanSegs &seg, cudaStream_t st) {
-  return bf16 ? scan_any<__nv_bfloat16, false>(a, seg, seg.count, st)
-              : scan_any<float, false>(a, seg, seg.count, st);
+  return walk<kOut>(a, bf16, seg, ScanBwdPlan(), nullptr, st);
+}
+
+cudaError_t launch_scan_bwd_chunks(const ScanArgs &a, int bf16, const ScanBwdPlan &pl, float *ws, cudaStream_t st) {
+  // A CTA takes up to 8 chunks one after another, so that its loads run ahead,
+  // while all SMs keep two CTAs.
+  long long blocks = 1;
+  by_lanes(a.S, [&](auto l) {
+    blocks = (long long)a.G * Block<decltype(l)::value>::per_group(a.E, a.G);
+    return cudaSuccess;
+  });
+  int run = 8;
+  while (run > 1 && blocks * a.B * ((pl.chunks + run - 1) / run) < 4LL * device_sms()) run /= 2;
+  ScanSegs seg;
+  seg.len = run * pl.chunk;
+  seg.count = (pl.chunks + run - 1) / run;
+  return walk<kChunks>(a, bf16, seg, pl, ws, st);
 }
 
 cudaError_t launch_scan_step(const ScanArgs &a, int bf16, cudaStream_t st) {
