@@ -41,11 +41,32 @@ __device__ __forceinline__ float softplus(float x) {
   p = fmaf(p, q, 2.f / 5.f);
   p = fmaf(p, q, 2.f / 3.f);
   p = fmaf(p, q, 2.f);
-  const float l = fmaf(p, s, fmaxf(x, 0.f));
-  return x != x ? x : l;  // (a maximum drops a NaN)
+  // (NaN: s and with it the sum is NaN, whatever the maximum drops)
+  return fmaf(p, s, fmaxf(x, 0.f));
 }
 
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// The same for pairs of channels, on packed arithmetic.
+__device__ __forceinline__ float2 sigmoid2(float2 x) {
+  const float2 w = tc::mul2(both(-kLog2e), x), d = tc::add2(both(1.f), make_float2(ex2(w.x), ex2(w.y)));
+  return make_float2(rcp(d.x), rcp(d.y));
+}
+__device__ __forceinline__ float2 silu2(float2 x) { return tc::mul2(x, sigmoid2(x)); }
+__device__ __forceinline__ float2 softplus2(float2 x) {
+  const float2 w = tc::mul2(both(-kLog2e), make_float2(fabsf(x.x), fabsf(x.y))), e = make_float2(ex2(w.x), ex2(w.y));
+  const float2 d = tc::add2(both(2.f), e), s = tc::mul2(e, make_float2(rcp(d.x), rcp(d.y))), q = tc::mul2(s, s);
+  float2 p = both(2.f / 15.f);
+  p = tc::fma2(p, q, both(2.f / 13.f));
+  p = tc::fma2(p, q, both(2.f / 11.f));
+  p = tc::fma2(p, q, both(2.f / 9.f));
+  p = tc::fma2(p, q, both(2.f / 7.f));
+  p = tc::fma2(p, q, both(2.f / 5.f));
+  p = tc::fma2(p, q, both(2.f / 3.f));
+  p = tc::fma2(p, q, both(2.f));
+  // (NaN: s and with it the sum is NaN, whatever the maximum drops)
+  return tc::fma2(p, s, make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
+}
 
 template <typename T>
 __device__ __forceinline__ float to_float(T x);
@@ -170,6 +191,9 @@ __device__ __forceinline__ void store_two(T *p, int n, float a, float b) {
   }
 }
 
+
+template <typename T>
+__device__ __forceinline__ float2 to_float2(const Two<T> &v) { return make_float2(to_float(v.a), to_float(v.b)); }
 
 template <typename T>
 __device__ __forceinline__ void store_pair(T *p, bool pair, int n, float a, float b) {

@@ -140,13 +140,18 @@ scan_bwd_kernel(const ScanArgs a, const ScanBwdPlan pl, float *__restrict__ ws) 
       const int t = qt + (j0 + j) * QS;
       float d[4], u[4], ds[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        d[i] = to_float(dr[j].v[i]) + bias[i];
-        if (a.softplus) d[i] = softplus(d[i]);
-        if (!(i < there && t0 + t < live)) d[i] = 0.f;
+      for (int i = 0; i < 4; i += 2) {
+        float2 dv = make_float2(to_float(dr[j].v[i]) + bias[i], to_float(dr[j].v[i + 1]) + bias[i + 1]);
+        if (a.softplus) dv = softplus2(dv);
+        const bool in = t0 + t < live;
+        d[i] = in && i < there ? dv.x : 0.f;
+        d[i + 1] = in && i + 1 < there ? dv.y : 0.f;
         u[i] = d[i] * to_float(xr[j].v[i]);
-        ds[i] = to_float(yr[j].v[i]);
-        if (z) ds[i] *= silu(to_float(zr[j].v[i]));
+        u[i + 1] = d[i + 1] * to_float(xr[j].v[i + 1]);
+        float2 g = make_float2(to_float(yr[j].v[i]), to_float(yr[j].v[i + 1]));
+        if (z) g = tc::mul2(g, silu2(make_float2(to_float(zr[j].v[i]), to_float(zr[j].v[i + 1]))));
+        ds[i] = g.x;
+        ds[i + 1] = g.y;
       }
       *reinterpret_cast<float4 *>(&sm.d[t][qc]) = make_float4(d[0], d[1], d[2], d[3]);
       *reinterpret_cast<float4 *>(&sm.u[t][qc]) = make_float4(u[0], u[1], u[2], u[3]);

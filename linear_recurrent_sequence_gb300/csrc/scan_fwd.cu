@@ -38,7 +38,7 @@ struct __align__(16) Tile {
 template <typename T, int L, int kMode>
 struct WalkSmem {
   __align__(16) Tile<T, L, kMode> ring[Tile<T, L, kMode>::kRing];
-  float2 du[2][Block<L>::kTile][Block<L>::kChannels];  // delta, u
+  float4 du[2][Block<L>::kTile][Block<L>::kChannels];  // delta, delta, u, u
   // sums over the states (outputs), or ds (chunks)
   float more[kMode == kStates ? 1 : 2][Block<L>::kTile][Block<L>::kChannels];
 };
@@ -127,7 +127,8 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg, const ScanBwdPlan pl, flo
         float yq[GT / 4][4];
 #pragma unroll
         for (int j = 0; j < GT; ++j) {
-          const float2 v = sm.du[buf][q + j][ci], dd = both(v.x), uu = both(v.y);
+          const float4 v = sm.du[buf][q + j][ci];
+          const float2 dd = make_float2(v.x, v.y), uu = make_float2(v.z, v.w);
           float2 Bv[2], Cv[2], s;
           four_states(&r.B[q + j][s0], Bv);
           if (kMode != kStates) four_states(&r.C[q + j][s0], Cv);
@@ -185,46 +186,62 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg, const ScanBwdPlan pl, flo
   const int le = group * Eg + min(c0 + lc, Eg - 1);
   T *y = reinterpret_cast<T *>(a.y) + b * a.sy[0] + le;
   const int l1 = there > 1;
-  const float bias[2] = {a.bias ? a.bias[le] : 0.f, a.bias ? a.bias[le + l1] : 0.f};
-  const float Dv[2] = {kMode == kOut && a.D ? a.D[le] : 0.f, kMode == kOut && a.D ? a.D[le + l1] : 0.f};
+  const float2 bias = a.bias ? make_float2(a.bias[le], a.bias[le + l1]) : both(0.f);
+  const float2 Dv = kMode == kOut && a.D ? make_float2(a.D[le], a.D[le + l1]) : both(0.f);
   const bool gate = kMode != kStates && a.z, pairs = kAsync || (a.E / a.G % 2 == 0 && a.pair_y);
 
-  // Rows of a tile, `width` of their values there, into the ring.
-  auto fetch_rows = [&](T *to, const void *from, long long stride, int row0, int cols, int width) {
-    constexpr int V = 16 / sizeof(T);
-    if (kAsync) {
-      const int nv = cols / V;
-      for (int o = tid; o < TT * nv; o += kLoad) {
-        const int t = o / nv, c = o - t * nv;
-        const bool in = row0 + t < live && c * V < width;
-        const T *p = reinterpret_cast<const T *>(from) + (in ? (row0 + t) * stride + c * V : 0);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(to + t * cols + c * V)), "l"(p),
-                     "r"(in ? 16 : 0)
-                     : "memory");
+  // A tensor's rows of the tiles on their way into the ring, `cols` values wide,
+  // `width` of them there; this thread's vectors (kAsync) or values move on by a
+  // tile a call.
+  constexpr int V = kAsync ? 16 / sizeof(T) : 1;
+  struct Rows {
+    const T *p;      // this thread's first vector of the next tile
+    long long step;  // elements from one row to the next
+    int t, c;        // its row in the tile, its column
+  };
+  auto rows_of = [&](const void *from, long long first, long long stride, int cols) {
+    Rows r;
+    r.step = stride;
+    r.t = tid / (cols / V);
+    r.c = tid % (cols / V) * V;
+    r.p = reinterpret_cast<const T *>(from) + first + (t0 + r.t) * stride + r.c;
+    return r;
+  };
+  auto fetch_rows = [&](T *to, Rows &r, auto columns, int row0, int width) {
+    constexpr int cols = decltype(columns)::value, hop = kLoad / (cols / V);  // rows between a thread's
+    static_assert(cols / V <= kLoad, "a row is at most one round");
+    const T *p = r.p;
+#pragma unroll
+    for (int t = 0; t < TT; t += hop) {
+      if (hop <= TT || r.t < TT) {
+        const bool in = row0 + t + r.t < live && r.c < width;
+        T *at = to + (t + r.t) * cols + r.c;
+        if (kAsync)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(at)), "l"(in ? p : reinterpret_cast<const T *>(a.x)), "r"(in ? 16 : 0) : "memory");
+        else
+          *at = in ? *p : from_float<T>(0.f);
       }
-    } else {
-#pragma unroll 4
-      for (int o = tid; o < TT * cols; o += kLoad) {
-        const int t = o / cols, c = o - t * cols;
-        const bool in = row0 + t < live && c < width;
-        to[o] = in ? reinterpret_cast<const T *>(from)[(row0 + t) * stride + c] : from_float<T>(0.f);
-      }
+      p += hop * r.step;
     }
+    r.p += TT * r.step;
   };
-  auto at_block = [&](const void *p, const long long s[2]) {
-    return reinterpret_cast<const T *>(p) + b * s[0] + group * Eg + c0;
-  };
+  const long long at_block = (long long)group * Eg + c0;
+  const int width = min(CC, Eg - c0);
+  Rows fx = rows_of(a.x, b * a.sx[0] + at_block, a.sx[1], CC), fd = rows_of(a.dt, b * a.sdt[0] + at_block, a.sdt[1], CC);
+  Rows fz = rows_of(a.z, b * a.sz[0] + at_block, a.sz[1], CC), fy = rows_of(a.dy, b * a.sdy[0] + at_block, a.sdy[1], CC);
+  Rows fB = rows_of(a.Bm, b * a.sB[0] + group * a.sB[2], a.sB[1], SP), fC = rows_of(a.Cm, b * a.sC[0] + group * a.sC[2], a.sC[1], SP);
   auto fetch = [&](int i) {
     if (i < tiles) {
       Row &r = sm.ring[i % kRing];
-      const int t = t0 + i * TT, width = min(CC, Eg - c0);
-      fetch_rows(&r.x[0][0], at_block(a.x, a.sx), a.sx[1], t, CC, width);
-      fetch_rows(&r.dt[0][0], at_block(a.dt, a.sdt), a.sdt[1], t, CC, width);
-      if (gate) fetch_rows(&r.z[0][0], at_block(a.z, a.sz), a.sz[1], t, CC, width);
-      if (kMode == kChunks) fetch_rows(&r.dy[0][0], at_block(a.dy, a.sdy), a.sdy[1], t, CC, width);
-      fetch_rows(&r.B[0][0], reinterpret_cast<const T *>(a.Bm) + b * a.sB[0] + group * a.sB[2], a.sB[1], t, SP, a.S);
-      if (kMode != kStates)
-        fetch_rows(&r.C[0][0], reinterpret_cast<const T *>(a.Cm) + b * a.sC[0] + group * a.sC[2], a.sC[1], t, SP, a.S);
+      const int t = t0 + i * TT;
+      const std::integral_constant<int, CC> channels;
+      const std::integral_constant<int, SP> states;
+      fetch_rows(&r.x[0][0], fx, channels, t, width);
+      fetch_rows(&r.dt[0][0], fd, channels, t, width);
+      if (gate) fetch_rows(&r.z[0][0], fz, channels, t, width);
+      if (kMode == kChunks) fetch_rows(&r.dy[0][0], fy, channels, t, width);
+      fetch_rows(&r.B[0][0], fB, states, t, a.S);
+      if (kMode != kStates) fetch_rows(&r.C[0][0], fC, states, t, a.S);
     }
     if (kAsync) asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -237,22 +254,17 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg, const ScanBwdPlan pl, flo
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
       const int at = lt + j * TS;
-      const Two<T> xr = two(r.x, at), dr = two(r.dt, at);
-      const float xs[2] = {to_float(xr.a), to_float(xr.b)};
-      float d[2] = {to_float(dr.a) + bias[0], to_float(dr.b) + bias[1]};
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        if (a.softplus) d[c] = softplus(d[c]);
-        if (!(c < there && t + at < live)) d[c] = 0.f;
-      }
-      *reinterpret_cast<float4 *>(&sm.du[buf][at][lc]) = make_float4(d[0], d[0] * xs[0], d[1], d[1] * xs[1]);
+      const float2 xs = to_float2(two(r.x, at));
+      float2 d = tc::add2(to_float2(two(r.dt, at)), bias);
+      if (a.softplus) d = softplus2(d);
+      if (there < 1 || t + at >= live) d.x = 0.f;
+      if (there < 2 || t + at >= live) d.y = 0.f;
+      const float2 u = tc::mul2(d, xs);
+      sm.du[buf][at][lc] = make_float4(d.x, d.x, u.x, u.x);
+      sm.du[buf][at][lc + 1] = make_float4(d.y, d.y, u.y, u.y);
       if (kMode == kChunks) {
-        const Two<T> yr = two(r.dy, at), zr = two(r.z, at);
-        float2 ds = make_float2(to_float(yr.a), to_float(yr.b));
-        if (gate) {
-          ds.x *= silu(to_float(zr.a));
-          ds.y *= silu(to_float(zr.b));
-        }
+        float2 ds = to_float2(two(r.dy, at));
+        if (gate) ds = tc::mul2(ds, silu2(to_float2(two(r.z, at))));
         *reinterpret_cast<float2 *>(&sm.more[buf][at][lc]) = ds;
       }
     }
@@ -260,18 +272,15 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg, const ScanBwdPlan pl, flo
   auto finish = [&](int i) {
     const int buf = i & 1, t = t0 + i * TT;
     const Row &r = sm.ring[i % kRing];
+    T *to = y + (t + lt) * a.sy[1];
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
       const int at = lt + j * TS;
-      const float2 s = *reinterpret_cast<const float2 *>(&sm.more[buf][at][lc]);
-      const Two<T> xr = two(r.x, at), zr = two(r.z, at);
-      float v0 = fmaf(Dv[0], to_float(xr.a), s.x), v1 = fmaf(Dv[1], to_float(xr.b), s.y);
-      if (gate) {
-        v0 *= silu(to_float(zr.a));
-        v1 *= silu(to_float(zr.b));
-      }
+      float2 v = tc::fma2(Dv, to_float2(two(r.x, at)), *reinterpret_cast<const float2 *>(&sm.more[buf][at][lc]));
+      if (gate) v = tc::mul2(v, silu2(to_float2(two(r.z, at))));
       const bool in = t + at < live;
-      if (t + at < t1) store_pair(y + (t + at) * a.sy[1], pairs, there, in ? v0 : 0.f, in ? v1 : 0.f);
+      if (t + at < t1) store_pair(to, pairs, there, in ? v.x : 0.f, in ? v.y : 0.f);
+      to += TS * a.sy[1];
     }
   };
   // Wait until all but the newest n tiles have arrived, then (all loaders') data is visible.
@@ -406,7 +415,9 @@ cudaError_t walk_any(ScanArgs a, const ScanSegs &seg, const ScanBwdPlan &pl, flo
   const bool async = async_ok<T>(a, kMode);
   return by_lanes(a.S, [&](auto l) {
     constexpr int L = decltype(l)::value;
-    return async ? walk_with<T, L, kMode, true>(a, seg, pl, ws, st) : walk_with<T, L, kMode, false>(a, seg, pl, ws, st);
+    if constexpr (4 * L * sizeof(T) >= 16)  // (a row of states is a vector at least)
+      if (async) return walk_with<T, L, kMode, true>(a, seg, pl, ws, st);
+    return walk_with<T, L, kMode, false>(a, seg, pl, ws, st);
   });
 }
 
