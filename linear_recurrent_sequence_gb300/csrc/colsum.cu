@@ -62,10 +62,10 @@ cudaError_t launch_colsum(const ColSum &s, cudaStream_t st) {
   bool vec = true;  // 16-byte vectors of columns
   for (int i = 0; i < n; ++i)
     vec = vec && (!s.out[i] || (s.cols[i] % 4 == 0 && s.stride[i] % 4 == 0 && reinterpret_cast<uintptr_t>(s.part[i]) % 16 == 0));
-  // Many columns fill the SMs with 8 parts at a time, few need 32 (16384 columns
-  // and more: vectors, where they are there).
-  if (most < 16384) return launch_k(colsum_kernel<1, 32>, dim3((most + 31) / 32, n), dim3(1024), 0, st, true, s);
-  if (vec) return launch_k(colsum_kernel<4, 8>, dim3((most + 127) / 128, n), dim3(256), 0, st, true, s);
+  // Eight parts at a time, by vectors of columns where those are there and fill the
+  // SMs; many parts of few columns 32 at a time.
+  if (s.count > 128 && most < 16384) return launch_k(colsum_kernel<1, 32>, dim3((most + 31) / 32, n), dim3(1024), 0, st, true, s);
+  if (vec && most >= 16384) return launch_k(colsum_kernel<4, 8>, dim3((most + 127) / 128, n), dim3(256), 0, st, true, s);
   return launch_k(colsum_kernel<1, 8>, dim3((most + 31) / 32, n), dim3(256), 0, st, true, s);
 }
 

@@ -94,13 +94,13 @@ __device__ __forceinline__ Chans<T, V> input_at(const ConvArgs &a, int b, int e,
 }
 
 // run: tokens of a thread, at least W - 1 (then only the first run reads the
-// state, which state_out may be).  U tokens' loads are in flight; the inputs stay
-// as they were read until their turn (8192 x 4096 bf16 43 us, 3.1 TB/s; with four
+// state, which state_out may be).  U tokens' loads (64 bytes) are in flight; the inputs
+// stay as they were read until their turn (8192 x 4096 bf16 43 us, 3.1 TB/s; with four
 // tokens of eight channels in flight, converted at once, 124).
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
 conv_fwd_kernel(const ConvArgs a, int run, int runs, int vec_taps) {
-  constexpr int U = 8;
+  constexpr int U = V * sizeof(T) == 16 ? 4 : 8;
   pdl_launch_dependents();
   pdl_wait();
   const int nv = a.E / V, b = blockIdx.y;
@@ -124,27 +124,31 @@ conv_fwd_kernel(const ConvArgs a, int run, int runs, int vec_taps) {
     }
     load_taps<V, W>(a, e, vec_taps, w, bias);
   }
-  for (int t = t0; t < live; t += U) {
+  auto step = [&](int j, int t, bool more) {
+    float o[V];
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      if (t + j >= live) break;
-      float o[V];
+    for (int v = 0; v < V; ++v) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
+      for (int k = 0; k < W - 1; ++k) win[k][v] = win[k + 1][v];
+      win[W - 1][v] = in[j].get(v);
+      float s = bias[v];
 #pragma unroll
-        for (int k = 0; k < W - 1; ++k) win[k][v] = win[k + 1][v];
-        win[W - 1][v] = in[j].get(v);
-        float s = bias[v];
-#pragma unroll
-        for (int k = 0; k < W; ++k) s = fmaf(w[k][v], win[k][v], s);
-        o[v] = a.silu ? silu(s) : s;
-      }
-      if (t + j + U < live) in[j].load(x + (t + j + U) * a.sx[1]);
-      Chans<T, V>::store(y + (t + j) * a.so[1], o);
+      for (int k = 0; k < W; ++k) s = fmaf(w[k][v], win[k][v], s);
+      o[v] = a.silu ? silu(s) : s;
     }
-  }
+    if (more) in[j].load(x + (t + U) * a.sx[1]);
+    Chans<T, V>::store(y + t * a.so[1], o);
+  };
+  int t = t0;
+  for (; t + 2 * U <= live; t += U)
+#pragma unroll
+    for (int j = 0; j < U; ++j) step(j, t + j, true);
+  for (; t < live; t += U)
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+      if (t + j < live) step(j, t + j, t + j + U < live);
   const float zero[V] = {};
-  for (int t = max(t0, live); t < t1; ++t) Chans<T, V>::store(y + t * a.so[1], zero);
+  for (t = max(t0, live); t < t1; ++t) Chans<T, V>::store(y + t * a.so[1], zero);
   if (r == 0 && a.state_out) {
     Chans<T, V> s[W - 1];
 #pragma unroll

@@ -43,13 +43,6 @@ struct WalkSmem {
   float more[kMode == kStates ? 1 : 2][Block<L>::kTile][Block<L>::kChannels];
 };
 
-template <typename T>
-__device__ __forceinline__ void four_states(const T *p, float2 (&v)[2]) {
-  const Four<T> f = load_four<T, true>(p, 4);
-  v[0] = make_float2(to_float(f.v[0]), to_float(f.v[1]));
-  v[1] = make_float2(to_float(f.v[2]), to_float(f.v[3]));
-}
-
 // Half of the CTA's warps walk the recurrence; the others keep the ring filled,
 // work out step sizes and inputs a tile ahead, and finish the outputs of the
 // tile before: with one sequence an SM has no more than one recurrence warp a
@@ -119,43 +112,62 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg, const ScanBwdPlan pl, flo
       const int buf = i & 1;
       const Row &r = sm.ring[slot];
       float part = 0.f;
-      // (a store to shared memory holds back the loads behind it, and a warp alone
-      // on its scheduler has nothing else to do: outputs of 8 tokens at a time)
-      constexpr int GT = 8;
+      // Four tokens at a time, the next four's operands on their way: a warp alone
+      // on its scheduler has nothing else to do, and a store to shared memory
+      // holds back the loads behind it.
+      struct Ops {
+        float4 v;
+        Four<T> B, C;
+        float ds;
+      } ops[2][4];
+      auto operands = [&](int q, Ops (&o)[4]) {
 #pragma unroll
-      for (int q = 0; q < TT; q += GT) {
-        float yq[GT / 4][4];
+        for (int j = 0; j < 4; ++j) {
+          o[j].v = sm.du[buf][q + j][ci];
+          o[j].B = load_four<T, true>(&r.B[q + j][s0], 4);
+          if (kMode != kStates) o[j].C = load_four<T, true>(&r.C[q + j][s0], 4);
+          if (kMode == kChunks) o[j].ds = sm.more[buf][q + j][ci];
+        }
+      };
+      operands(0, ops[0]);
 #pragma unroll
-        for (int j = 0; j < GT; ++j) {
-          const float4 v = sm.du[buf][q + j][ci];
-          const float2 dd = make_float2(v.x, v.y), uu = make_float2(v.z, v.w);
-          float2 Bv[2], Cv[2], s;
-          four_states(&r.B[q + j][s0], Bv);
-          if (kMode != kStates) four_states(&r.C[q + j][s0], Cv);
-          if (kMode != kOut) part += v.x;
-          const float2 ds = kMode == kChunks ? both(sm.more[buf][q + j][ci]) : both(0.f);
+      for (int q = 0; q < TT; q += 4) {
+        const Ops(&o)[4] = ops[q / 4 & 1];
+        if (q + 4 < TT) operands(q + 4, ops[(q / 4 + 1) & 1]);
+        float2 d[4][2], in[4][2];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 dd = make_float2(o[j].v.x, o[j].v.y), uu = make_float2(o[j].v.z, o[j].v.w);
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
-            const float2 w = tc::mul2(dd, A2[p]), d = make_float2(ex2(w.x), ex2(w.y));
-            h[p] = tc::fma2(d, h[p], tc::mul2(uu, Bv[p]));
-            if (kMode == kOut) s = p ? tc::fma2(h[p], Cv[p], s) : tc::mul2(h[p], Cv[p]);
+            const float2 w = tc::mul2(dd, A2[p]);
+            d[j][p] = make_float2(ex2(w.x), ex2(w.y));
+            in[j][p] = tc::mul2(uu, make_float2(to_float(o[j].B.v[2 * p]), to_float(o[j].B.v[2 * p + 1])));
+          }
+          if (kMode != kOut) part += o[j].v.x;
+        }
+        float yq[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float2 s;
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const float2 C = kMode == kStates ? both(0.f) : make_float2(to_float(o[j].C.v[2 * p]), to_float(o[j].C.v[2 * p + 1]));
+            h[p] = tc::fma2(d[j][p], h[p], in[j][p]);
+            if (kMode == kOut) s = p ? tc::fma2(h[p], C, s) : tc::mul2(h[p], C);
             if (kMode == kChunks) {
-              P[p] = tc::mul2(P[p], d);
-              g[p] = tc::fma2(P[p], tc::mul2(ds, Cv[p]), g[p]);
+              P[p] = tc::mul2(P[p], d[j][p]);
+              g[p] = tc::fma2(P[p], tc::mul2(both(o[j].ds), C), g[p]);
             }
           }
-          if (kMode == kOut) {
-            yq[j / 4][j % 4] = s.x + s.y;
-            if (j % 4 == 3) share_sums<4, L>(yq[j / 4]);
-          }
+          if (kMode == kOut) yq[j] = s.x + s.y;
         }
         if (kMode == kOut) {
+          share_sums<4, L>(yq);
           constexpr int M = L < 4 ? L : 4;
           if (tid % L < M)
 #pragma unroll
-            for (int i4 = 0; i4 < GT / 4; ++i4)
-#pragma unroll
-              for (int j = 0; j < 4 / M; ++j) sm.more[buf][q + i4 * 4 + tid % M * (4 / M) + j][ci] = yq[i4][j];
+            for (int j = 0; j < 4 / M; ++j) sm.more[buf][q + tid % M * (4 / M) + j][ci] = yq[j];
         }
       }
       __syncthreads();
@@ -308,79 +320,83 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg, const ScanBwdPlan pl, flo
     for (int at = t0 + tiles * TT + lt; at < t1; at += TS) store_pair(y + at * a.sy[1], pairs, there, 0.f, 0.f);
 }
 
-// One token.  A lane has four states of R sequences' same channel, so that A is
-// read once for them; what a sequence's channel needs once (step size, gate,
-// output) is shared out over the channel's lanes.
+// One token.  A lane has four states of R sequences' same channel at a time and
+// walks over the sequences, so that A is read once for them and the next ones'
+// states are on their way; what a sequence's channel needs once (step size,
+// gate, output) is shared out over the channel's lanes.
 constexpr int kStepThreads = 256;
 
+template <typename T, int R>
+struct StepIn {
+  float4 h[R];
+  Four<T> B[R], C[R];
+  T x, dt, z;
+};
+
 template <typename T, int L, int R, bool kVec>
-__global__ void __launch_bounds__(kStepThreads)
+__global__ void __launch_bounds__(kStepThreads, R == 1 ? 4 : 2)
 scan_step_kernel(const ScanArgs a) {
-  pdl_launch_dependents();
+  static_assert(R == 1 || R <= L, "a lane has one sequence at most to finish");
   pdl_wait();
-  constexpr int CC = kStepThreads / L, M = L < R ? L : R, NR = R / M;  // lanes that have sequences, of each NR
+  constexpr int CC = kStepThreads / L;
   const int lane = threadIdx.x & 31, ci = threadIdx.x / L, sub = threadIdx.x % L, s0 = sub * 4;
   const int c = blockIdx.x * CC + ci, e = min(c, a.E - 1), g = e / (a.E / a.G);
   const bool own = c < a.E, vec = a.S % 4 == 0;
   const bool va = vec && reinterpret_cast<uintptr_t>(a.A) % 16 == 0;
   const bool vi = vec && reinterpret_cast<uintptr_t>(a.h_in) % 16 == 0;
   const bool vo = vec && reinterpret_cast<uintptr_t>(a.h_out) % 16 == 0;
-  const int b0 = blockIdx.y * R, there = min(R, a.B - b0);
-  const size_t row = ((size_t)b0 * a.E + e) * a.S, step = (size_t)a.E * a.S;
-  float4 h[R];
-  Four<T> Br[R], Cr[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-    if (r < there) h[r] = load_states(a.h_in + row + r * step, s0, a.S, vi);
-  {
-    const T *Bp = reinterpret_cast<const T *>(a.Bm) + b0 * a.sB[0] + g * a.sB[2] + s0;
-    const T *Cp = reinterpret_cast<const T *>(a.Cm) + b0 * a.sC[0] + g * a.sC[2] + s0;
+  const size_t step = (size_t)a.E * a.S, row = (size_t)e * a.S;
+  auto load = [&](int b0, StepIn<T, R> &in) {
+    if (b0 >= a.B) return;
+    const int there = min(R, a.B - b0), mine = b0 + min(sub % R, there - 1);
 #pragma unroll
     for (int r = 0; r < R; ++r)
       if (r < there) {
-        Br[r] = load_four<T, kVec>(Bp + r * a.sB[0], a.S - s0);
-        Cr[r] = load_four<T, kVec>(Cp + r * a.sC[0], a.S - s0);
+        in.h[r] = load_states(a.h_in + row + (b0 + r) * step, s0, a.S, vi);
+        in.B[r] = load_four<T, kVec>(reinterpret_cast<const T *>(a.Bm) + (b0 + r) * a.sB[0] + g * a.sB[2] + s0, a.S - s0);
+        in.C[r] = load_four<T, kVec>(reinterpret_cast<const T *>(a.Cm) + (b0 + r) * a.sC[0] + g * a.sC[2] + s0, a.S - s0);
       }
-  }
-  // this lane's sequences: sub NR .. sub NR + NR - 1
+    in.x = reinterpret_cast<const T *>(a.x)[mine * a.sx[0] + e];
+    in.dt = reinterpret_cast<const T *>(a.dt)[mine * a.sdt[0] + e];
+    if (a.z) in.z = reinterpret_cast<const T *>(a.z)[mine * a.sz[0] + e];
+  };
+  int b0 = blockIdx.y * R;
+  const int hop = gridDim.y * R;
+  StepIn<T, R> in;
+  load(b0, in);
+  const float4 A4 = load_states(a.A + row, s0, a.S, va);
+  const float2 A2[2] = {make_float2(A4.x * kLog2e, A4.y * kLog2e), make_float2(A4.z * kLog2e, A4.w * kLog2e)};
   const float bias = a.bias ? a.bias[e] : 0.f, Dv = a.D ? a.D[e] : 0.f;
-  float x[NR], d[NR], gate[NR];
+  for (; b0 < a.B; b0 += hop) {
+    const StepIn<T, R> now = in;
+    load(b0 + hop, in);
+    const int there = min(R, a.B - b0);
+    const float x = to_float(now.x), gate = a.z ? silu(to_float(now.z)) : 1.f;
+    float d = to_float(now.dt) + bias;
+    if (a.softplus) d = softplus(d);
+    const float u = d * x;
+    float sum[R];
 #pragma unroll
-  for (int m = 0; m < NR; ++m) {
-    const int b = b0 + min(sub % M * NR + m, there - 1);
-    x[m] = to_float(reinterpret_cast<const T *>(a.x)[b * a.sx[0] + e]);
-    d[m] = to_float(reinterpret_cast<const T *>(a.dt)[b * a.sdt[0] + e]) + bias;
-    gate[m] = a.z ? to_float(reinterpret_cast<const T *>(a.z)[b * a.sz[0] + e]) : 0.f;
-  }
-  const float4 A4 = load_states(a.A + (size_t)e * a.S, s0, a.S, va);
-  const float As[4] = {A4.x * kLog2e, A4.y * kLog2e, A4.z * kLog2e, A4.w * kLog2e};
+    for (int r = 0; r < R; ++r) {
+      const int from = lane / L * L + r;
+      const float2 dr = both(__shfl_sync(0xffffffffu, d, from)), ur = both(__shfl_sync(0xffffffffu, u, from));
+      float2 h[2] = {make_float2(now.h[r].x, now.h[r].y), make_float2(now.h[r].z, now.h[r].w)}, s = both(0.f);
 #pragma unroll
-  for (int m = 0; m < NR; ++m) {
-    if (a.softplus) d[m] = softplus(d[m]);
-    gate[m] = a.z ? silu(gate[m]) : 1.f;
-  }
-  float sum[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int from = lane / L * L + r / NR;
-    const float dr = __shfl_sync(0xffffffffu, d[r % NR], from);
-    const float u = dr * __shfl_sync(0xffffffffu, x[r % NR], from);
-    float hs[4] = {h[r].x, h[r].y, h[r].z, h[r].w};
-    sum[r] = 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      hs[j] = fmaf(ex2(dr * As[j]), hs[j], u * to_float(Br[r].v[j]));
-      sum[r] = fmaf(hs[j], to_float(Cr[r].v[j]), sum[r]);
+      for (int p = 0; p < 2; ++p) {
+        const float2 w = tc::mul2(dr, A2[p]);
+        const float2 B = make_float2(to_float(now.B[r].v[2 * p]), to_float(now.B[r].v[2 * p + 1]));
+        h[p] = tc::fma2(make_float2(ex2(w.x), ex2(w.y)), h[p], tc::mul2(ur, B));
+        s = tc::fma2(h[p], make_float2(to_float(now.C[r].v[2 * p]), to_float(now.C[r].v[2 * p + 1])), s);
+      }
+      sum[r] = s.x + s.y;
+      if (own && r < there)
+        store_states(a.h_out + row + (b0 + r) * step, s0, a.S, vo, make_float4(h[0].x, h[0].y, h[1].x, h[1].y));
     }
-    if (own && r < there) store_states(a.h_out + row + r * step, s0, a.S, vo, make_float4(hs[0], hs[1], hs[2], hs[3]));
+    share_sums<R, L>(sum);
+    if (own && sub < there)
+      reinterpret_cast<T *>(a.y)[(b0 + sub) * a.sy[0] + e] = from_float<T>(fmaf(Dv, x, sum[0]) * gate);
   }
-  share_sums<R, L>(sum);
-#pragma unroll
-  for (int m = 0; m < NR; ++m) {
-    const int r = sub * NR + m;
-    if (own && r < there)
-      reinterpret_cast<T *>(a.y)[(b0 + r) * a.sy[0] + e] = from_float<T>(fmaf(Dv, x[m], sum[m]) * gate[m]);
-  }
+  pdl_launch_dependents();
 }
 
 // Asynchronous copies of 16 bytes where every row of every tensor (and every
@@ -426,15 +442,18 @@ cudaError_t walk(const ScanArgs &a, int bf16, const ScanSegs &seg, const ScanBwd
   return bf16 ? walk_any<__nv_bfloat16, kMode>(a, seg, pl, ws, st) : walk_any<float, kMode>(a, seg, pl, ws, st);
 }
 
-template <typename T, int R>
+template <typename T, bool kMany>
 cudaError_t step_any(const ScanArgs &a, cudaStream_t st) {
   auto on = [&](const void *p, const long long s[3]) {
     return reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T)) == 0 && (a.B == 1 || s[0] % 4 == 0) && (a.G == 1 || s[2] % 4 == 0);
   };
   const bool vec = a.S % 4 == 0 && on(a.Bm, a.sB) && on(a.Cm, a.sC);
   return by_lanes(a.S, [&](auto l) {
-    constexpr int L = decltype(l)::value, CC = kStepThreads / L;
-    const dim3 grid((a.E + CC - 1) / CC, (a.B + R - 1) / R);
+    constexpr int L = decltype(l)::value, CC = kStepThreads / L, R = !kMany ? 1 : L < 4 ? L : 4;
+    // Enough walks over the sequences to fill the SMs twice.
+    const int nx = (a.E + CC - 1) / CC, groups = (a.B + R - 1) / R;
+    const int ny = kMany ? std::min(groups, std::max(1, 2 * device_sms() / nx)) : groups;
+    const dim3 grid(nx, ny);
     return vec ? launch_k(scan_step_kernel<T, L, R, true>, grid, dim3(kStepThreads), 0, st, true, a)
                : launch_k(scan_step_kernel<T, L, R, false>, grid, dim3(kStepThreads), 0, st, true, a);
   });
@@ -492,10 +511,10 @@ cudaError_t launch_scan_bwd_chunks(const ScanArgs &a, int bf16, const ScanBwdPla
 }
 
 cudaError_t launch_scan_step(const ScanArgs &a, int bf16, cudaStream_t st) {
-  // Four sequences a thread once one each would give every SM over 16 CTAs.
+  // Walks over the sequences once one each would give every SM over 16 CTAs.
   const long long ctas = ((long long)a.E * lanes_of(a.S) + kStepThreads - 1) / kStepThreads * a.B;
-  if (ctas >= 16LL * device_sms()) return bf16 ? step_any<__nv_bfloat16, 4>(a, st) : step_any<float, 4>(a, st);
-  return bf16 ? step_any<__nv_bfloat16, 1>(a, st) : step_any<float, 1>(a, st);
+  if (ctas >= 16LL * device_sms()) return bf16 ? step_any<__nv_bfloat16, true>(a, st) : step_any<float, true>(a, st);
+  return bf16 ? step_any<__nv_bfloat16, false>(a, st) : step_any<float, false>(a, st);
 }
 
 }  // namespace ret
