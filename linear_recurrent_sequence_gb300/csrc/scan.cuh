@@ -139,7 +139,7 @@ __device__ __forceinline__ int tokens_of(const ScanArgs &a, int b) {
   return (int)(n < 0 ? 0 : n > a.N ? a.N : n);
 }
 
-constexpr int kScan = 128, kLoad = 128, kThreads = kScan + kLoad;
+constexpr int kScan = 128, kLoad = 256, kThreads = kScan + kLoad;
 
 // Channels of a CTA (grid.x counts the blocks of all groups) and tokens at a
 // time.  The tile's step sizes take the most shared memory: channels x tokens.

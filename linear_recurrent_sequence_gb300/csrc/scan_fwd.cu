@@ -39,11 +39,34 @@ template <typename T, int L, int kMode>
 struct WalkSmem {
   __align__(16) Tile<T, L, kMode> ring[Tile<T, L, kMode>::kRing];
   float4 du[2][Block<L>::kTile][Block<L>::kChannels];  // delta, delta, u, u
-  // sums over the states (outputs), or ds (chunks)
-  float more[kMode == kStates ? 1 : 2][Block<L>::kTile][Block<L>::kChannels];
+  // a lane's sum over its states (outputs), or ds (chunks)
+  float more[kMode == kStates ? 1 : 2][Block<L>::kTile][kMode == kOut ? kScan : Block<L>::kChannels];
 };
 
-// Half of the CTA's warps walk the recurrence; the others keep the ring filled,
+// Sums of two channels' L neighbouring values each.
+template <int L>
+__device__ __forceinline__ float2 lane_sums(const float *p) {
+  if constexpr (L == 1) {
+    return *reinterpret_cast<const float2 *>(p);
+  } else if constexpr (L == 2) {
+    const float4 v = *reinterpret_cast<const float4 *>(p);
+    return make_float2(v.x + v.y, v.z + v.w);
+  } else {
+    float2 s[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      s[c] = both(0.f);
+#pragma unroll
+      for (int i = 0; i < L; i += 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(p + c * L + i);
+        s[c] = tc::add2(s[c], tc::add2(make_float2(v.x, v.y), make_float2(v.z, v.w)));
+      }
+    }
+    return make_float2(s[0].x + s[0].y, s[1].x + s[1].y);
+  }
+}
+
+// A third of the CTA's warps walks the recurrence; the others keep the ring filled,
 // work out step sizes and inputs a tile ahead, and finish the outputs of the
 // tile before: with one sequence an SM has no more than one recurrence warp a
 // scheduler, and everything else that a token needs runs beside it.
@@ -162,13 +185,10 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg, const ScanBwdPlan pl, flo
           }
           if (kMode == kOut) yq[j] = s.x + s.y;
         }
-        if (kMode == kOut) {
-          share_sums<4, L>(yq);
-          constexpr int M = L < 4 ? L : 4;
-          if (tid % L < M)
+        // (the loaders add a channel's L lanes up: shuffles here took 96 us of 248)
+        if (kMode == kOut)
 #pragma unroll
-            for (int j = 0; j < 4 / M; ++j) sm.more[buf][q + tid % M * (4 / M) + j][ci] = yq[j];
-        }
+          for (int j = 0; j < 4; ++j) sm.more[buf][q + j][tid] = yq[j];
       }
       __syncthreads();
       sum += part;
@@ -191,10 +211,10 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg, const ScanBwdPlan pl, flo
   }
 
   // ---- loaders; each has two channels of NP tokens of a tile
-  constexpr int NP = TT * CC / 2 / kLoad, TS = 2 * kLoad / CC;  // pairs a thread; tokens between them
-  static_assert(NP * kLoad * 2 == TT * CC && NP * TS == TT, "whole tiles");
+  constexpr int TS = 2 * kLoad / CC, NP = TS < TT ? TT / TS : 1;  // tokens between a thread's pairs; pairs
   const int tid = threadIdx.x - kScan, lc = tid % (CC / 2) * 2, lt = tid / (CC / 2);
-  const int there = min(2, max(0, Eg - c0 - lc));  // channels of this pair
+  const int there = TS > TT && lt >= TT ? 0 : min(2, max(0, Eg - c0 - lc));  // channels of this pair
+  const bool mine = TS <= TT || lt < TT;
   const int le = group * Eg + min(c0 + lc, Eg - 1);
   T *y = reinterpret_cast<T *>(a.y) + b * a.sy[0] + le;
   const int l1 = there > 1;
@@ -211,11 +231,13 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg, const ScanBwdPlan pl, flo
     long long step;  // elements from one row to the next
     int t, c;        // its row in the tile, its column
   };
-  auto rows_of = [&](const void *from, long long first, long long stride, int cols) {
+  // (turned: by the other half of the threads, where half of them are enough)
+  auto rows_of = [&](const void *from, long long first, long long stride, int cols, bool turned = false) {
+    const int id = turned ? tid ^ (kLoad / 2) : tid;
     Rows r;
     r.step = stride;
-    r.t = tid / (cols / V);
-    r.c = tid % (cols / V) * V;
+    r.t = id / (cols / V);
+    r.c = id % (cols / V) * V;
     r.p = reinterpret_cast<const T *>(from) + first + (t0 + r.t) * stride + r.c;
     return r;
   };
@@ -239,9 +261,9 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg, const ScanBwdPlan pl, flo
   };
   const long long at_block = (long long)group * Eg + c0;
   const int width = min(CC, Eg - c0);
-  Rows fx = rows_of(a.x, b * a.sx[0] + at_block, a.sx[1], CC), fd = rows_of(a.dt, b * a.sdt[0] + at_block, a.sdt[1], CC);
-  Rows fz = rows_of(a.z, b * a.sz[0] + at_block, a.sz[1], CC), fy = rows_of(a.dy, b * a.sdy[0] + at_block, a.sdy[1], CC);
-  Rows fB = rows_of(a.Bm, b * a.sB[0] + group * a.sB[2], a.sB[1], SP), fC = rows_of(a.Cm, b * a.sC[0] + group * a.sC[2], a.sC[1], SP);
+  Rows fx = rows_of(a.x, b * a.sx[0] + at_block, a.sx[1], CC), fd = rows_of(a.dt, b * a.sdt[0] + at_block, a.sdt[1], CC, true);
+  Rows fz = rows_of(a.z, b * a.sz[0] + at_block, a.sz[1], CC), fy = rows_of(a.dy, b * a.sdy[0] + at_block, a.sdy[1], CC, true);
+  Rows fB = rows_of(a.Bm, b * a.sB[0] + group * a.sB[2], a.sB[1], SP), fC = rows_of(a.Cm, b * a.sC[0] + group * a.sC[2], a.sC[1], SP, true);
   auto fetch = [&](int i) {
     if (i < tiles) {
       Row &r = sm.ring[i % kRing];
@@ -263,6 +285,7 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg, const ScanBwdPlan pl, flo
   auto put = [&](int i) {
     const int buf = i & 1, t = t0 + i * TT;
     const Row &r = sm.ring[i % kRing];
+    if (!mine) return;
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
       const int at = lt + j * TS;
@@ -285,10 +308,11 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg, const ScanBwdPlan pl, flo
     const int buf = i & 1, t = t0 + i * TT;
     const Row &r = sm.ring[i % kRing];
     T *to = y + (t + lt) * a.sy[1];
+    if (!mine) return;
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
       const int at = lt + j * TS;
-      float2 v = tc::fma2(Dv, to_float2(two(r.x, at)), *reinterpret_cast<const float2 *>(&sm.more[buf][at][lc]));
+      float2 v = tc::fma2(Dv, to_float2(two(r.x, at)), lane_sums<L>(&sm.more[buf][at][lc * L]));
       if (gate) v = tc::mul2(v, silu2(to_float2(two(r.z, at))));
       const bool in = t + at < live;
       if (t + at < t1) store_pair(to, pairs, there, in ? v.x : 0.f, in ? v.y : 0.f);
@@ -317,7 +341,7 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg, const ScanBwdPlan pl, flo
   if (kMode == kOut && tiles > 0) finish(tiles - 1);
   pdl_launch_dependents();
   if (kMode == kOut)  // whole tiles past the sequence's end
-    for (int at = t0 + tiles * TT + lt; at < t1; at += TS) store_pair(y + at * a.sy[1], pairs, there, 0.f, 0.f);
+    for (int at = t0 + tiles * TT + lt; at < t1; at += TS < TT ? TS : TT) store_pair(y + at * a.sy[1], pairs, there, 0.f, 0.f);
 }
 
 // One token.  A lane has four states of R sequences' same channel at a time and
