@@ -857,72 +857,98 @@ def distill_step(student, ids, values, weight=None, *, temperature=1.0, tail=Fal
     return loss, dstudent
 
 
-def _seq_strides(name, t, lead, E):
-    """(batch, token) element strides of a [B, N, E] or [B, E] tensor."""
-    s = t.stride()
-    if s[-1] != 1 and E > 1:
-        raise ValueError(f"{name}: the channels must be contiguous")
-    return (s[0], s[1] if lead == 2 else 0)
+# The calls below check their tensors once for each set of shapes, strides and
+# types that they meet (a step's checks cost 12 us, finding them here 4), and
+# keep the descriptor with them.
+def _meta(t):
+    """What the checks look at."""
+    return None if t is None else (t.shape, t.stride(), t.dtype)
 
 
-def _seq_like(name, t, x):
-    """Checks a tensor for x's shape and dtype and gives its strides (None: x's)."""
-    if t is None:
+def _meta_contiguous(m):
+    shape, stride, _ = m
+    want = 1
+    for n, s in zip(reversed(shape), reversed(stride)):
+        if n != 1 and s != want and 0 not in shape:
+            return False
+        want *= n
+    return True
+
+
+def _meta_f32(name, m, shape):
+    """Checks for a contiguous fp32 tensor of the given shape (None passes)."""
+    if m is not None and (m[2] != torch.float32 or tuple(m[0]) != tuple(shape) or not _meta_contiguous(m)):
+        raise ValueError(f"{name} must be a contiguous fp32 tensor of shape {tuple(shape)}")
+
+
+def _meta_like(name, m, x):
+    """Checks a tensor for x's shape and dtype (None passes) and gives its batch
+    and token strides."""
+    if m is None:
         return (0, 0)
-    _like(name, t, x)
-    return _seq_strides(name, t, x.dim() - 1, x.shape[-1])
+    if m[0] != x[0] or m[2] != x[2]:
+        raise ValueError(f"{name} must have the shape {tuple(x[0])} and dtype {x[2]}")
+    if m[1][-1] != 1 and m[0][-1] > 1:
+        raise ValueError(f"{name}: the channels must be contiguous")
+    return (m[1][0], m[1][1] if len(m[0]) == 3 else 0)
 
 
-def _lengths(lengths, B):
+def _meta_lengths(m, B):
     """Bytes of a length (8 without lengths)."""
-    if lengths is None:
+    if m is None:
         return 8
-    return _ids("lengths", lengths, (B,))
+    if m[2] is not torch.int64 and m[2] is not torch.int32:
+        raise TypeError(f"lengths must be int32 or int64, got {m[2]}")
+    if tuple(m[0]) != (B,) or not _meta_contiguous(m):
+        raise ValueError(f"lengths must be a contiguous tensor of shape {(B,)}")
+    return 8 if m[2] is torch.int64 else 4
 
 
-# As the descriptors above: found by shapes, strides and options alone.  The
-# workspaces depend on the device's SMs too.
+def _meta_sequences(x, step):
+    """(B, N, E) of x [B, N, E], or of a step's [B, E]."""
+    shape = x[0]
+    if len(shape) != (2 if step else 3):
+        raise ValueError(f"x must be {'[B, E]' if step else '[B, N, E]'}, got {tuple(shape)}")
+    _dtype_code(x[2])
+    return (shape[0], 1, shape[1]) if step else tuple(shape)
+
+
 @functools.lru_cache(maxsize=256)
-def _scan_desc(shape, S, G, dtype, softplus, len_bytes, strides, sB, sC, device):
-    """(descriptor, workspace bytes of the forward and of the backward)."""
-    B, N, E = shape
-    d = ScanDesc(B, N, E, S, G, _dtype_code(dtype), softplus, len_bytes, *strides, sB, sC)
-    return (d, int(lib.retnet_selective_scan_workspace_size(ctypes.byref(d))),
-            int(lib.retnet_selective_scan_bwd_workspace_size(ctypes.byref(d))))
-
-
-def _scan_call(x, dt, A, B, C, D, z, dt_bias, softplus, lengths, step=False, **like):
-    """The descriptor of a scan, after checks of its tensors; like: the strides'
-    names of more tensors of x's shape."""
+def _scan_plan(step, softplus, device, x, dt, A, B, C, D, z, dt_bias, lengths, h_in, h_out, y=None, dy=None,
+               dx=None, ddt=None, dz=None, dA=None, dB=None, dC=None, dD=None, ddt_bias=None):
+    """(descriptor, workspace bytes of the forward and of the backward on that
+    device), after checks of the tensors' shapes, strides and types."""
+    Bn, N, E = _meta_sequences(x, step)
     lead = 1 if step else 2
-    if x.dim() != lead + 1:
-        raise ValueError(f"x must be {'[B, E]' if step else '[B, N, E]'}, got {tuple(x.shape)}")
-    rows, E = tuple(x.shape[:-1]), x.shape[-1]
-    if A.dim() != 2:
-        raise ValueError(f"A must be [E, S], got {tuple(A.shape)}")
-    S = A.shape[1]
-    _f32("A", A, (E, S))
-    _f32("D", D, (E,))
-    _f32("dt_bias", dt_bias, (E,))
-    strides = dict(sx=_seq_strides("x", x, lead, E), sdt=_seq_like("dt", dt, x), sz=_seq_like("z", z, x))
-    strides.update({k: _seq_like(k[1:], t, x) for k, t in like.items()})
-    groups = []
-    for name, t in (("B", B), ("C", C)):
-        if t.dim() == lead + 1:
-            t = t.unsqueeze(lead)
-        if t.dim() != lead + 2 or tuple(t.shape[:lead]) != rows or t.shape[-1] != S or t.dtype != x.dtype:
-            raise ValueError(f"{name} must have the shape {rows + ('groups', S)} and dtype {x.dtype}")
-        s = t.stride()
+    if len(A[0]) != 2:
+        raise ValueError(f"A must be [E, S], got {tuple(A[0])}")
+    S = A[0][1]
+    h_name = "h_out" if dy is None else "dh_out"
+    for name, m, shape in (("A", A, (E, S)), ("D", D, (E,)), ("dt_bias", dt_bias, (E,)), ("h_in", h_in, (Bn, E, S)),
+                           (h_name, h_out, (Bn, E, S)), ("dA", dA, (E, S)), ("dD", dD, (E,)),
+                           ("ddt_bias", ddt_bias, (E,))):
+        _meta_f32(name, m, shape)
+    strides = [_meta_like(name, m, x) for name, m in (("x", x), ("dt", dt), ("z", z), ("out", y), ("dy", dy),
+                                                       ("dx", dx), ("ddt", ddt), ("dz", dz))]
+    rows, groups = tuple(x[0][:-1]), []
+    for name, (shape, s, dtype) in (("B", B), ("C", C)):
+        shape, s = tuple(shape), tuple(s)
+        if len(shape) == lead + 1:
+            shape, s = (*shape[:lead], 1, shape[lead]), (*s[:lead], 0, s[lead])
+        if len(shape) != lead + 2 or shape[:lead] != rows or shape[-1] != S or dtype != x[2]:
+            raise ValueError(f"{name} must have the shape {rows + ('groups', S)} and dtype {x[2]}")
         if s[-1] != 1 and S > 1:
             raise ValueError(f"{name}: the states must be contiguous")
-        groups.append((t.shape[lead], (s[0], s[1] if lead == 2 else 0, s[lead])))
+        groups.append((shape[lead], (s[0], s[1] if lead == 2 else 0, s[lead])))
     (G, sB), (GC, sC) = groups
     if GC != G or G < 1 or E % G:
         raise ValueError(f"B and C must have equal groups that divide the {E} channels")
-    order = ("sx", "sdt", "sz", "sy", "sdy", "sdx", "sddt", "sdz")
-    shape = (rows[0], 1 if step else rows[1], E)
-    return _scan_desc(shape, S, G, x.dtype, bool(softplus), _lengths(lengths, rows[0]),
-                      tuple(strides.get(k, (0, 0)) for k in order), sB, sC, x.device)
+    for name, m, like in (("dB", dB, B), ("dC", dC, C)):
+        if m is not None and (m[0] != like[0] or m[2] != like[2] or not _meta_contiguous(m)):
+            raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(like[0])} and dtype {like[2]}")
+    d = ScanDesc(Bn, N, E, S, G, _dtype_code(x[2]), softplus, _meta_lengths(lengths, Bn), *strides, sB, sC)
+    return (d, int(lib.retnet_selective_scan_workspace_size(ctypes.byref(d))),
+            int(lib.retnet_selective_scan_bwd_workspace_size(ctypes.byref(d))))
 
 
 def selective_scan_fwd(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, softplus=True, h_in=None,
@@ -937,12 +963,11 @@ def selective_scan_fwd(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, softplus
     of y behind them are zeros.  Returns (y, the states after the last tokens)."""
     if out is None:
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    desc, nbytes, _ = _scan_call(x, dt, A, B, C, D, z, dt_bias, softplus, lengths, sy=out)
-    states = (x.shape[0], x.shape[2], A.shape[1])
     if h_out is None:
-        h_out = torch.empty(states, dtype=torch.float32, device=x.device)
-    _f32("h_in", h_in, states)
-    _f32("h_out", h_out, states)
+        h_out = torch.empty((x.shape[0], x.shape[-1], A.shape[-1]), dtype=torch.float32, device=x.device)
+    desc, nbytes, _ = _scan_plan(False, bool(softplus), x.device, _meta(x), _meta(dt), _meta(A), _meta(B), _meta(C),
+                                 _meta(D), _meta(z), _meta(dt_bias), _meta(lengths), _meta(h_in), _meta(h_out),
+                                 _meta(out))
     if workspace is None and nbytes:
         with _on(stream):
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
@@ -960,13 +985,12 @@ def selective_scan_step(x, dt, A, B, C, h, *, D=None, z=None, dt_bias=None, soft
     Returns y [B, E]."""
     if out is None:
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    desc, _, _ = _scan_call(x, dt, A, B, C, D, z, dt_bias, softplus, None, step=True, sy=out)
-    states = (*x.shape, A.shape[1])
-    _f32("h", h, states)
-    _f32("h_out", h_out, states)
+    if h_out is None:
+        h_out = h
+    desc, _, _ = _scan_plan(True, bool(softplus), x.device, _meta(x), _meta(dt), _meta(A), _meta(B), _meta(C),
+                            _meta(D), _meta(z), _meta(dt_bias), None, _meta(h), _meta(h_out), _meta(out))
     st = lib.retnet_selective_scan_step(
-        ctypes.byref(desc), *_ptrs(x, dt, A, B, C, D, z, dt_bias, h, out, h if h_out is None else h_out),
-        _stream(stream))
+        ctypes.byref(desc), *_ptrs(x, dt, A, B, C, D, z, dt_bias, h, out, h_out), _stream(stream))
     _check(st, "retnet_selective_scan_step")
     return out
 
@@ -991,16 +1015,10 @@ def selective_scan_bwd(x, dt, A, B, C, dy, *, D=None, z=None, dt_bias=None, soft
     dx, ddt, dz = new(dx, x), new(ddt, dt), new(dz, z)
     dA, dB, dC = new(dA, A), new(dB, B), new(dC, C)
     dD, ddt_bias, dh_in = new(dD, D), new(ddt_bias, dt_bias), new(dh_in, h_in)
-    desc, _, nbytes = _scan_call(x, dt, A, B, C, D, z, dt_bias, softplus, lengths, sdy=dy, sdx=dx, sddt=ddt,
-                                 sdz=dz)
-    E, states = x.shape[2], (x.shape[0], x.shape[2], A.shape[1])
-    for name, t, shape in (("dA", dA, A.shape), ("dD", dD, (E,)), ("ddt_bias", ddt_bias, (E,)),
-                           ("h_in", h_in, states), ("dh_in", dh_in, states), ("dh_out", dh_out, states)):
-        _f32(name, t, shape)
-    for name, t, like in (("dB", dB, B), ("dC", dC, C)):
-        _like(name, t, like)
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+    desc, _, nbytes = _scan_plan(False, bool(softplus), dev, *map(_meta, (
+        x, dt, A, B, C, D, z, dt_bias, lengths, h_in, dh_out, None, dy, dx, ddt, dz, dA, dB, dC, dD, ddt_bias)))
+    if dh_in is not None:
+        _f32("dh_in", dh_in, h_in.shape)
     if workspace is None:
         with _on(stream):
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
@@ -1013,30 +1031,21 @@ def selective_scan_bwd(x, dt, A, B, C, dy, *, D=None, z=None, dt_bias=None, soft
 
 
 @functools.lru_cache(maxsize=256)
-def _conv_desc(shape, W, dtype, silu, len_bytes, sx, sg, so, device):
-    """(descriptor, workspace bytes of the backward)."""
-    d = ConvDesc(*shape, W, _dtype_code(dtype), silu, len_bytes, sx, sg, so)
+def _conv_plan(step, silu, device, x, w, b, lengths, out, states, dy=None, dw=None, db=None):
+    """(descriptor, workspace bytes of the backward on that device), after checks
+    of the tensors; states: (name, kept inputs or their gradient)."""
+    Bn, N, E = _meta_sequences(x, step)
+    if len(w[0]) != 2:
+        raise ValueError(f"w must be [E, taps], got {tuple(w[0])}")
+    W = w[0][1]
+    for name, m, shape in (("w", w, (E, W)), ("b", b, (E,)), ("dw", dw, (E, W)), ("db", db, (E,))):
+        _meta_f32(name, m, shape)
+    for name, m in states:
+        if m is not None and (tuple(m[0]) != (Bn, W - 1, E) or m[2] != x[2] or not _meta_contiguous(m)):
+            raise ValueError(f"{name} must be a contiguous tensor of shape {(Bn, W - 1, E)} and dtype {x[2]}")
+    d = ConvDesc(Bn, N, E, W, _dtype_code(x[2]), silu, _meta_lengths(lengths, Bn), _meta_like("x", x, x),
+                 _meta_like("dy", dy, x), _meta_like("out", out, x))
     return d, int(lib.retnet_causal_conv_bwd_workspace_size(ctypes.byref(d)))
-
-
-def _conv_call(x, w, b, silu, lengths, states, dy=None, out=None, step=False):
-    """(descriptor, workspace bytes) of a convolution after checks of its
-    tensors; states: (name, tensor) of kept inputs and their gradients."""
-    lead = 1 if step else 2
-    if x.dim() != lead + 1:
-        raise ValueError(f"x must be {'[B, E]' if step else '[B, N, E]'}, got {tuple(x.shape)}")
-    B, E = x.shape[0], x.shape[-1]
-    if w.dim() != 2:
-        raise ValueError(f"w must be [E, taps], got {tuple(w.shape)}")
-    W = w.shape[1]
-    _f32("w", w, (E, W))
-    _f32("b", b, (E,))
-    for name, t in states:
-        if t is not None and (t.shape != (B, W - 1, E) or t.dtype != x.dtype or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous tensor of shape {(B, W - 1, E)} and dtype {x.dtype}")
-    shape = (B, 1 if step else x.shape[1], E)
-    return _conv_desc(shape, W, x.dtype, bool(silu), _lengths(lengths, B), _seq_strides("x", x, lead, E),
-                      _seq_like("dy", dy, x), _seq_like("out", out, x), x.device)
 
 
 def causal_conv_fwd(x, w, b=None, *, silu=True, state_in=None, lengths=None, out=None, state_out=None,
@@ -1051,7 +1060,8 @@ def causal_conv_fwd(x, w, b=None, *, silu=True, state_in=None, lengths=None, out
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     if state_out is None:
         state_out = torch.empty((x.shape[0], w.shape[-1] - 1, x.shape[-1]), dtype=x.dtype, device=x.device)
-    desc, _ = _conv_call(x, w, b, silu, lengths, (("state_in", state_in), ("state_out", state_out)), out=out)
+    desc, _ = _conv_plan(False, bool(silu), x.device, _meta(x), _meta(w), _meta(b), _meta(lengths), _meta(out),
+                         (("state_in", _meta(state_in)), ("state_out", _meta(state_out))))
     st = lib.retnet_causal_conv_fwd(ctypes.byref(desc),
                                     *_ptrs(x, w, b, state_in, lengths, out, state_out), _stream(stream))
     _check(st, "retnet_causal_conv_fwd")
@@ -1065,7 +1075,8 @@ def causal_conv_step(x, w, b, state, *, silu=True, state_out=None, out=None, str
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     if state_out is None:
         state_out = state
-    desc, _ = _conv_call(x, w, b, silu, None, (("state", state), ("state_out", state_out)), out=out, step=True)
+    desc, _ = _conv_plan(True, bool(silu), x.device, _meta(x), _meta(w), _meta(b), None, _meta(out),
+                         (("state", _meta(state)), ("state_out", _meta(state_out))))
     st = lib.retnet_causal_conv_fwd(ctypes.byref(desc), *_ptrs(x, w, b, state, None, out, state_out),
                                     _stream(stream))
     _check(st, "retnet_causal_conv_fwd")
@@ -1091,10 +1102,9 @@ def causal_conv_bwd(x, w, b, dy, *, silu=True, state_in=None, dstate_out=None, l
         dstate_in = None
     elif dstate_in is None:
         dstate_in = torch.empty(state_in.shape, dtype=x.dtype, device=dev)
-    states = (("state_in", state_in), ("dstate_out", dstate_out), ("dstate_in", dstate_in))
-    desc, nbytes = _conv_call(x, w, b, silu, lengths, states, dy=dy, out=dx)
-    _f32("dw", dw, w.shape)
-    _f32("db", db, (x.shape[-1],))
+    states = (("state_in", _meta(state_in)), ("dstate_out", _meta(dstate_out)), ("dstate_in", _meta(dstate_in)))
+    desc, nbytes = _conv_plan(False, bool(silu), dev, _meta(x), _meta(w), _meta(b), _meta(lengths), _meta(dx), states,
+                              _meta(dy), _meta(dw), _meta(db))
     if workspace is None:
         with _on(stream):
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
