@@ -11,8 +11,8 @@
 // it adds to the state after it and to the gradient before it (both walk the
 // same exponentials, forwards: the second is sum_t (e^(A (delta_1 + .. + delta_t)))
 // C_t ds_t).  A short pass over the chunks joins them, and then every chunk has
-// its own CTA: forwards once, keeping the state at every 8th token, then tile
-// by tile backwards with 8 tokens' decays and states in registers (running a
+// its own CTA: forwards once, keeping the state at every 4th token, then tile
+// by tile backwards with 4 tokens' decays and states in registers (running a
 // state backwards instead would divide by decays that underflow).
 // A thread has four states of two neighbouring channels; sums over a channel's
 // states are shared out over its L lanes, sums over channels over the others.
@@ -27,16 +27,14 @@ namespace {
 using namespace scan;
 
 constexpr int kMain = 128;   // threads of the chunk's CTA
-constexpr int kTile = 8;
+constexpr int kTile = 4;
 
 template <int L>
 struct Geo {
   static constexpr int SP = 4 * L;                           // states with padding
-  static constexpr int kChunk = 16 * L < 64 ? 16 * L : 64;   // tokens: two tiles of the first pass
+  static constexpr int kChunk = Block<L>::kTile;             // tokens: a tile of the first pass
   static constexpr int kBlock = 2 * kMain / L;               // channels of a CTA
   static constexpr int kTiles = kChunk / kTile;
-  static_assert(kChunk == 2 * Block<L>::kTile, "a chunk is two tiles of the first pass");
-  static constexpr bool kTwice = L < 16;                     // B and C twice in shared memory, as pairs
   static __host__ __device__ int per_group(int E, int G) { return (E / G + kBlock - 1) / kBlock; }
 };
 
@@ -80,26 +78,30 @@ scan_bwd_carry_kernel(const ScanArgs a, const ScanBwdPlan pl, float *__restrict_
   if (back && a.dh_in) a.dh_in[i] = v;
 }
 
-template <int L>
+template <typename T, int L>
 struct MainSmem {
   using G = Geo<L>;
   float d[G::kChunk][G::kBlock], u[G::kChunk][G::kBlock], ds[G::kChunk][G::kBlock];  // delta, u, ds
-  float b[G::kChunk][G::SP * (G::kTwice ? 2 : 1)], c[G::kChunk][G::SP * (G::kTwice ? 2 : 1)];
+  __align__(16) T b[G::kChunk][G::SP];
+  __align__(16) T c[G::kChunk][G::SP];
   float4 start[G::kTiles][2][kMain];           // the state before a tile: channel 0, 1
   float sums[3][kTile][G::kBlock];             // sum C h, sum g B, sum g p A log2(e)
   float bc[kMain / 32][kTile][2][G::SP];       // a warp's share of dB and dC
 };
 
-// One chunk of a block of channels.  f32x2 pairs are the thread's two channels:
-// delta, u and ds come as pairs out of shared memory, B and C are kept there
-// twice each (but for S > 32, where that would leave room for one CTA an SM).
+// One chunk of a block of channels.  Bound by the shared-memory pipe (its loads
+// and the shuffles of the sums) and by the latency of few warps: a tile is as
+// long as its operands, decays and states fit the registers, so that each is
+// read once, before the tile's first store (a store to shared memory holds back
+// the loads behind it; tiles of 8 tokens, whose operands were read for each
+// direction, took 883 us for 2 x 4096 x 4096 x 16 bf16).
 template <typename T, int L, bool kVec>
-__global__ void __launch_bounds__(kMain, 2)
+__global__ void __launch_bounds__(kMain, sizeof(T) == 2 ? 3 : 2)
 scan_bwd_kernel(const ScanArgs a, const ScanBwdPlan pl, float *__restrict__ ws) {
   using G = Geo<L>;
   constexpr int CC = G::kBlock, SP = G::SP, TC = G::kChunk, QC = CC / 4;  // quads of channels
   extern __shared__ __align__(16) uint8_t dyn[];
-  MainSmem<L> &sm = *reinterpret_cast<MainSmem<L> *>(dyn);
+  MainSmem<T, L> &sm = *reinterpret_cast<MainSmem<T, L> *>(dyn);
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, Eg = a.E / a.G;
   const int per = G::per_group(a.E, a.G), blocks = a.G * per;
@@ -167,108 +169,87 @@ scan_bwd_kernel(const ScanArgs a, const ScanBwdPlan pl, float *__restrict__ ws) 
       const int o = tid + j * kMain, t = o / SP, s = o % SP, at = t0 + t;
       if (NB * kMain > TC * SP && o >= TC * SP) break;
       const bool in = at < live && s < a.S;
-      const float Bv = in ? to_float(Bp[at * a.sB[1] + s]) : 0.f, Cv = in ? to_float(Cp[at * a.sC[1] + s]) : 0.f;
-      if (G::kTwice) {
-        *reinterpret_cast<float2 *>(&sm.b[t][2 * s]) = both(Bv);
-        *reinterpret_cast<float2 *>(&sm.c[t][2 * s]) = both(Cv);
-      } else {
-        sm.b[t][s] = Bv;
-        sm.c[t][s] = Cv;
-      }
+      sm.b[t][s] = in ? Bp[at * a.sB[1] + s] : from_float<T>(0.f);
+      sm.c[t][s] = in ? Cp[at * a.sC[1] + s] : from_float<T>(0.f);
     }
   }
 
   // ---- four states of channels ca, ca + 1
   const int s0 = lane % L * 4, ca = tid / L * 2;
   const bool vec = a.S % 4 == 0;
-  float2 A2[4], h[4], ag[4], dA[4];
+  float2 A2[2][2], h[2][2], ag[2][2], dA[2][2];  // [channel][pair of states]
   bool own[2];
   int ech[2];
-  {
-    float A[2][4], hv[2][4], gv[2][4];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      own[c] = c0 + ca + c < Eg;
-      const int e = ech[c] = group * Eg + min(c0 + ca + c, Eg - 1);
-      // (0 for a channel that is not there: it takes part in the sums over channels)
-      const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
-      const float4 A4 = load_states(a.A + (size_t)e * a.S, s0, a.S, vec && reinterpret_cast<uintptr_t>(a.A) % 16 == 0);
-      const float4 h4 = own[c] ? load_states(ws + (bk * a.E + e) * a.S, s0, a.S, vec) : none;
-      const float4 g4 = own[c] ? load_states(ws + pl.g + (bk * a.E + e) * a.S, s0, a.S, vec) : none;
-      A[c][0] = A4.x; A[c][1] = A4.y; A[c][2] = A4.z; A[c][3] = A4.w;
-      hv[c][0] = h4.x; hv[c][1] = h4.y; hv[c][2] = h4.z; hv[c][3] = h4.w;
-      gv[c][0] = g4.x; gv[c][1] = g4.y; gv[c][2] = g4.z; gv[c][3] = g4.w;
-    }
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      A2[s] = make_float2(A[0][s] * kLog2e, A[1][s] * kLog2e);
-      h[s] = make_float2(hv[0][s], hv[1][s]);
-      ag[s] = make_float2(gv[0][s], gv[1][s]);
-      dA[s] = both(0.f);
-    }
+  for (int c = 0; c < 2; ++c) {
+    own[c] = c0 + ca + c < Eg;
+    const int e = ech[c] = group * Eg + min(c0 + ca + c, Eg - 1);
+    // (0 for a channel that is not there: it takes part in the sums over channels)
+    const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 A4 = load_states(a.A + (size_t)e * a.S, s0, a.S, vec && reinterpret_cast<uintptr_t>(a.A) % 16 == 0);
+    const float4 h4 = own[c] ? load_states(ws + (bk * a.E + e) * a.S, s0, a.S, vec) : none;
+    const float4 g4 = own[c] ? load_states(ws + pl.g + (bk * a.E + e) * a.S, s0, a.S, vec) : none;
+    A2[c][0] = make_float2(A4.x * kLog2e, A4.y * kLog2e);
+    A2[c][1] = make_float2(A4.z * kLog2e, A4.w * kLog2e);
+    h[c][0] = make_float2(h4.x, h4.y);
+    h[c][1] = make_float2(h4.z, h4.w);
+    ag[c][0] = make_float2(g4.x, g4.y);
+    ag[c][1] = make_float2(g4.z, g4.w);
+    dA[c][0] = dA[c][1] = both(0.f);
   }
   __syncthreads();
-  auto per_state = [&](const float *row, float2 (&v)[4]) {
-    if (G::kTwice) {
-      const float4 p = *reinterpret_cast<const float4 *>(row + 2 * s0), q = *reinterpret_cast<const float4 *>(row + 2 * s0 + 4);
-      v[0] = make_float2(p.x, p.y);
-      v[1] = make_float2(p.z, p.w);
-      v[2] = make_float2(q.x, q.y);
-      v[3] = make_float2(q.z, q.w);
-    } else {
-      const float4 p = *reinterpret_cast<const float4 *>(row + s0);
-      v[0] = both(p.x);
-      v[1] = both(p.y);
-      v[2] = both(p.z);
-      v[3] = both(p.w);
-    }
-  };
+  auto pair_of = [](const Four<T> &f, int p) { return make_float2(to_float(f.v[2 * p]), to_float(f.v[2 * p + 1])); };
   auto chans = [&](const float *row) { return *reinterpret_cast<const float2 *>(row + ca); };
 
   // ---- forwards: the state before every tile
   const int tiles = live > t0 ? (live - t0 + kTile - 1) / kTile : 0;
-  for (int i = 0; i < tiles; ++i) {
-    sm.start[i][0][tid] = make_float4(h[0].x, h[1].x, h[2].x, h[3].x);
-    sm.start[i][1][tid] = make_float4(h[0].y, h[1].y, h[2].y, h[3].y);
-    if (i + 1 == tiles) break;
+  auto keep_start = [&](int i) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) sm.start[i][c][tid] = make_float4(h[c][0].x, h[c][0].y, h[c][1].x, h[c][1].y);
+  };
+  if (tiles > 0) keep_start(0);
+  for (int i = 0; i + 1 < tiles; ++i) {
+    Four<T> Br[kTile];
+    float2 dv[kTile], uv[kTile];
 #pragma unroll
     for (int j = 0; j < kTile; ++j) {
-      const int t = i * kTile + j;
-      float2 B[4];
-      per_state(sm.b[t], B);
-      const float2 d = chans(sm.d[t]), u = chans(sm.u[t]);
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const float2 w = tc::mul2(d, A2[s]);
-        h[s] = tc::fma2(make_float2(ex2(w.x), ex2(w.y)), h[s], tc::mul2(u, B[s]));
-      }
+      Br[j] = load_four<T, true>(&sm.b[i * kTile + j][s0], 4);
+      dv[j] = chans(sm.d[i * kTile + j]);
+      uv[j] = chans(sm.u[i * kTile + j]);
     }
+#pragma unroll
+    for (int j = 0; j < kTile; ++j)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const float2 B = pair_of(Br[j], p);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float2 w = tc::mul2(both(c ? dv[j].y : dv[j].x), A2[c][p]);
+          h[c][p] = tc::fma2(make_float2(ex2(w.x), ex2(w.y)), h[c][p], tc::mul2(both(c ? uv[j].y : uv[j].x), B));
+        }
+      }
+    keep_start(i + 1);
   }
 
   // ---- backwards, tile by tile
   float sD[4] = {}, sBias[4] = {};
   constexpr int NW = kTile / QS > 0 ? kTile / QS : 1;  // quads of a tile a thread writes
   // What a lane gets of the sums of 8 values v = j * 2 + c (tokens j, channels c),
-  // and of sums over the warp's channels of values v = j * 4 + s.  (Held back to
-  // the tile's end they would cost more in spilled registers than the loads that
-  // a store holds back: 1226 us for 883.)
-  auto put_sums = [&](float (*to)[CC], int j0, float (&v)[8]) {
-    share_sums<8, L>(v);
-    constexpr int W = L < 8 ? L : 8;
-    if (lane % L < W)
+  // and of sums over the warp's channels of values v = j * 4 + s.
+  constexpr int WS = L < 8 ? L : 8, WB = 32 / L < 8 ? 32 / L : 8;
+  auto put_sums = [&](float (*to)[CC], const float (&v)[8]) {
+    if (lane % L < WS)
 #pragma unroll
-      for (int m = 0; m < 8 / W; ++m) {
-        const int idx = lane % L * (8 / W) + m;
-        to[j0 + idx / 2][ca + idx % 2] = v[m];
+      for (int m = 0; m < 8 / WS; ++m) {
+        const int idx = lane % L * (8 / WS) + m;
+        to[idx / 2][ca + idx % 2] = v[m];
       }
   };
-  auto put_bc = [&](int which, int j0, float (&v)[8]) {
-    share_sums<8, 32 / L, L>(v);
-    constexpr int W = 32 / L < 8 ? 32 / L : 8;
-    if (lane / L < W)
+  auto put_bc = [&](int which, int j0, const float (&v)[8]) {
+    if (lane / L < WB)
 #pragma unroll
-      for (int m = 0; m < 8 / W; ++m) {
-        const int idx = lane / L * (8 / W) + m;
+      for (int m = 0; m < 8 / WB; ++m) {
+        const int idx = lane / L * (8 / WB) + m;
         sm.bc[warp][j0 + idx / 4][which][s0 + idx % 4] = v[m];
       }
   };
@@ -284,71 +265,83 @@ scan_bwd_kernel(const ScanArgs a, const ScanBwdPlan pl, float *__restrict__ ws) 
       yr[m] = load_four<T, kVec>(dy + at * a.sdy[1], z ? c : 0);
       zr[m] = load_four<T, kVec>(z + at * a.sz[1], z ? c : 0);
     }
-    float2 dec[kTile][4], hs[kTile][4];  // decays, and the states before each token
-    {
-      const float4 p = sm.start[i][0][tid], q = sm.start[i][1][tid];
-      h[0] = make_float2(p.x, q.x);
-      h[1] = make_float2(p.y, q.y);
-      h[2] = make_float2(p.z, q.z);
-      h[3] = make_float2(p.w, q.w);
+    Four<T> Br[kTile], Cr[kTile];
+    float2 dv[kTile], uv[kTile], gv[kTile];
+#pragma unroll
+    for (int j = 0; j < kTile; ++j) {
+      const int t = i * kTile + j;
+      Br[j] = load_four<T, true>(&sm.b[t][s0], 4);
+      Cr[j] = load_four<T, true>(&sm.c[t][s0], 4);
+      dv[j] = chans(sm.d[t]);
+      uv[j] = chans(sm.u[t]);
+      gv[j] = chans(sm.ds[t]);
     }
 #pragma unroll
-    for (int j0 = 0; j0 < kTile; j0 += 4) {
-      float sv[8], cv[8];
-#pragma unroll
-      for (int j = j0; j < j0 + 4; ++j) {
-        const int t = i * kTile + j;
-        float2 B[4], C[4];
-        per_state(sm.b[t], B);
-        per_state(sm.c[t], C);
-        const float2 d = chans(sm.d[t]), u = chans(sm.u[t]), ds = chans(sm.ds[t]);
-        float2 sum = both(0.f);
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const float2 w = tc::mul2(d, A2[s]);
-          dec[j][s] = make_float2(ex2(w.x), ex2(w.y));
-          hs[j][s] = h[s];
-          h[s] = tc::fma2(dec[j][s], h[s], tc::mul2(u, B[s]));
-          sum = s ? tc::fma2(h[s], C[s], sum) : tc::mul2(h[s], C[s]);
-          const float2 dc = tc::mul2(ds, h[s]);
-          cv[(j & 1) * 4 + s] = dc.x + dc.y;
-        }
-        sv[(j - j0) * 2] = sum.x;
-        sv[(j - j0) * 2 + 1] = sum.y;
-        if (j & 1) put_bc(1, j - 1, cv);
-      }
-      put_sums(sm.sums[0], j0, sv);
+    for (int c = 0; c < 2; ++c) {
+      const float4 f = sm.start[i][c][tid];
+      h[c][0] = make_float2(f.x, f.y);
+      h[c][1] = make_float2(f.z, f.w);
     }
+    float2 dec[kTile][2][2], hs[kTile][2][2];  // decays, and the states before each token
+    float sv[8], qv[8], rv[8], cv[2][8], bv[2][8];
 #pragma unroll
-    for (int j0 = kTile - 4; j0 >= 0; j0 -= 4) {
-      float qv[8], rv[8], bv[8];
+    for (int j = 0; j < kTile; ++j) {
+      float2 sum[2], dc[2];
 #pragma unroll
-      for (int j = j0 + 3; j >= j0; --j) {
-        const int t = i * kTile + j;
-        float2 B[4], C[4];
-        per_state(sm.b[t], B);
-        per_state(sm.c[t], C);
-        const float2 d = chans(sm.d[t]), u = chans(sm.u[t]), ds = chans(sm.ds[t]);
-        float2 q = both(0.f), r = both(0.f);
+      for (int p = 0; p < 2; ++p) {
+        const float2 B = pair_of(Br[j], p), C = pair_of(Cr[j], p);
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const float2 g = tc::fma2(ds, C[s], ag[s]);
-          ag[s] = tc::mul2(dec[j][s], g);
-          const float2 gp = tc::mul2(ag[s], hs[j][s]);  // g e^(delta A) h_before
-          q = s ? tc::fma2(g, B[s], q) : tc::mul2(g, B[s]);
-          r = s ? tc::fma2(gp, A2[s], r) : tc::mul2(gp, A2[s]);
-          dA[s] = tc::fma2(d, gp, dA[s]);
-          const float2 db = tc::mul2(u, g);
-          bv[(j & 1) * 4 + s] = db.x + db.y;
+        for (int c = 0; c < 2; ++c) {
+          const float2 w = tc::mul2(both(c ? dv[j].y : dv[j].x), A2[c][p]);
+          dec[j][c][p] = make_float2(ex2(w.x), ex2(w.y));
+          hs[j][c][p] = h[c][p];
+          h[c][p] = tc::fma2(dec[j][c][p], h[c][p], tc::mul2(both(c ? uv[j].y : uv[j].x), B));
+          sum[c] = p ? tc::fma2(h[c][p], C, sum[c]) : tc::mul2(h[c][p], C);
+          dc[p] = c ? tc::fma2(both(gv[j].y), h[c][p], dc[p]) : tc::mul2(both(gv[j].x), h[c][p]);
         }
-        qv[(j - j0) * 2] = q.x;
-        qv[(j - j0) * 2 + 1] = q.y;
-        rv[(j - j0) * 2] = r.x;
-        rv[(j - j0) * 2 + 1] = r.y;
-        if (!(j & 1)) put_bc(0, j, bv);
+        cv[j / 2][(j & 1) * 4 + 2 * p] = dc[p].x;
+        cv[j / 2][(j & 1) * 4 + 2 * p + 1] = dc[p].y;
       }
-      put_sums(sm.sums[1], j0, qv);
-      put_sums(sm.sums[2], j0, rv);
+      sv[j * 2] = sum[0].x + sum[0].y;
+      sv[j * 2 + 1] = sum[1].x + sum[1].y;
+      if (j & 1) share_sums<8, 32 / L, L>(cv[j / 2]);
+    }
+    share_sums<8, L>(sv);
+#pragma unroll
+    for (int j = kTile - 1; j >= 0; --j) {
+      float2 q[2], r[2], db[2];
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const float2 B = pair_of(Br[j], p), C = pair_of(Cr[j], p);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float2 g = tc::fma2(both(c ? gv[j].y : gv[j].x), C, ag[c][p]);
+          ag[c][p] = tc::mul2(dec[j][c][p], g);
+          const float2 gp = tc::mul2(ag[c][p], hs[j][c][p]);  // g e^(delta A) h_before
+          q[c] = p ? tc::fma2(g, B, q[c]) : tc::mul2(g, B);
+          r[c] = p ? tc::fma2(gp, A2[c][p], r[c]) : tc::mul2(gp, A2[c][p]);
+          dA[c][p] = tc::fma2(both(c ? dv[j].y : dv[j].x), gp, dA[c][p]);
+          db[p] = c ? tc::fma2(both(uv[j].y), g, db[p]) : tc::mul2(both(uv[j].x), g);
+        }
+        bv[j / 2][(j & 1) * 4 + 2 * p] = db[p].x;
+        bv[j / 2][(j & 1) * 4 + 2 * p + 1] = db[p].y;
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        qv[j * 2 + c] = q[c].x + q[c].y;
+        rv[j * 2 + c] = r[c].x + r[c].y;
+      }
+      if (!(j & 1)) share_sums<8, 32 / L, L>(bv[j / 2]);
+    }
+    share_sums<8, L>(qv);
+    share_sums<8, L>(rv);
+    put_sums(sm.sums[0], sv);
+    put_sums(sm.sums[1], qv);
+    put_sums(sm.sums[2], rv);
+#pragma unroll
+    for (int j = 0; j < kTile / 2; ++j) {
+      put_bc(0, j * 2, bv[j]);
+      put_bc(1, j * 2, cv[j]);
     }
     __syncthreads();
     // the channels' gradients
@@ -407,8 +400,8 @@ scan_bwd_kernel(const ScanArgs a, const ScanBwdPlan pl, float *__restrict__ ws) 
     ws[pl.bc + ((((size_t)(blk - group * per) * a.B + b) * a.N + at) * a.G + group) * 2 * a.S + j % (2 * a.S)] = 0.f;
   }
   // ---- the chunk's sums of dA, dD and dbias
-  if (own[0]) store_states(ws + (bk * a.E + ech[0]) * a.S, s0, a.S, vec, make_float4(dA[0].x, dA[1].x, dA[2].x, dA[3].x));
-  if (own[1]) store_states(ws + (bk * a.E + ech[1]) * a.S, s0, a.S, vec, make_float4(dA[0].y, dA[1].y, dA[2].y, dA[3].y));
+  if (own[0]) store_states(ws + (bk * a.E + ech[0]) * a.S, s0, a.S, vec, make_float4(dA[0][0].x, dA[0][0].y, dA[0][1].x, dA[0][1].y));
+  if (own[1]) store_states(ws + (bk * a.E + ech[1]) * a.S, s0, a.S, vec, make_float4(dA[1][0].x, dA[1][0].y, dA[1][1].x, dA[1][1].y));
   __syncthreads();
   float *red = &sm.d[0][0];  // [2][QS][CC]
 #pragma unroll
@@ -463,7 +456,7 @@ cudaError_t main_with(const ScanArgs &a, const ScanBwdPlan &pl, float *ws, cudaS
   const cudaError_t e = allow_big_smem(reinterpret_cast<const void *>(kern), done);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)(a.G * pl.blocks) * pl.chunks, a.B);
-  return launch_k(kern, grid, dim3(kMain), sizeof(MainSmem<L>), st, true, a, pl, ws);
+  return launch_k(kern, grid, dim3(kMain), sizeof(MainSmem<T, L>), st, true, a, pl, ws);
 }
 
 template <typename T>

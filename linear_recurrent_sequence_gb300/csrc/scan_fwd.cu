@@ -120,7 +120,7 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg, const ScanBwdPlan pl, flo
       }
     }
     auto leave_chunk = [&](int i) {  // what chunk i of the segment adds
-      const size_t at = ((size_t)(t0 / (2 * TT) + i) * a.B + b) * a.E + e;
+      const size_t at = ((size_t)(t0 / TT + i) * a.B + b) * a.E + e;
       if (own) {
         store_states(ws + at * a.S, s0, a.S, vec, make_float4(h[0].x, h[0].y, h[1].x, h[1].y));
         store_states(ws + pl.g + at * a.S, s0, a.S, vec, make_float4(g[0].x, g[0].y, g[1].x, g[1].y));
@@ -192,7 +192,7 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg, const ScanBwdPlan pl, flo
       }
       __syncthreads();
       sum += part;
-      if (kMode == kChunks && (i & 1)) leave_chunk(i / 2);
+      if (kMode == kChunks) leave_chunk(i);
     }
     pdl_launch_dependents();
     const float4 h4 = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
@@ -204,8 +204,8 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg, const ScanBwdPlan pl, flo
     } else if (kMode == kOut) {
       if (k == seg.count - 1 && own && a.h_out)
         store_states(a.h_out + row, s0, a.S, vec && reinterpret_cast<uintptr_t>(a.h_out) % 16 == 0, h4);
-    } else {  // a chunk that ends early, and those behind the sequence's end
-      for (int i = tiles / 2; i < (t1 - t0 + 2 * TT - 1) / (2 * TT); ++i) leave_chunk(i);
+    } else {  // the chunks (a tile each) behind the sequence's end
+      for (int i = tiles; i < (t1 - t0 + TT - 1) / TT; ++i) leave_chunk(i);
     }
     return;
   }
@@ -519,14 +519,14 @@ cudaError_t launch_scan_fwd(const ScanArgs &a, int bf16, const ScanSegs &seg, cu
 }
 
 cudaError_t launch_scan_bwd_chunks(const ScanArgs &a, int bf16, const ScanBwdPlan &pl, float *ws, cudaStream_t st) {
-  // A CTA takes up to 8 chunks one after another, so that its loads run ahead,
+  // A CTA takes up to 16 chunks one after another, so that its loads run ahead,
   // while all SMs keep two CTAs.
   long long blocks = 1;
   by_lanes(a.S, [&](auto l) {
     blocks = (long long)a.G * Block<decltype(l)::value>::per_group(a.E, a.G);
     return cudaSuccess;
   });
-  int run = 8;
+  int run = 16;
   while (run > 1 && blocks * a.B * ((pl.chunks + run - 1) / run) < 4LL * device_sms()) run /= 2;
   ScanSegs seg;
   seg.len = run * pl.chunk;
