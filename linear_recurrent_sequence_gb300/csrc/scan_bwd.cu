@@ -84,9 +84,11 @@ struct MainSmem {
   float d[G::kChunk][G::kBlock], u[G::kChunk][G::kBlock], ds[G::kChunk][G::kBlock];  // delta, u, ds
   __align__(16) T b[G::kChunk][G::SP];
   __align__(16) T c[G::kChunk][G::SP];
-  float4 start[G::kTiles][2][kMain];           // the state before a tile: channel 0, 1
-  float sums[3][kTile][G::kBlock];             // sum C h, sum g B, sum g p A log2(e)
-  float bc[kMain / 32][kTile][2][G::SP];       // a warp's share of dB and dC
+  // A warp's states before a tile (two channels a lane), and in their place, once
+  // the tile is done, its sums: [C h, g B, g p A log2(e)][token][channel].
+  static constexpr int kWarpChans = 64 / L, kRegion = 3 * kTile * kWarpChans > 256 ? 3 * kTile * kWarpChans : 256;
+  __align__(16) float tile[G::kTiles][kMain / 32][kRegion];
+  float bc[kMain / 32][G::kChunk][2][G::SP];   // a warp's share of dB and dC
 };
 
 // One chunk of a block of channels.  Bound by the shared-memory pipe (its loads
@@ -96,7 +98,7 @@ struct MainSmem {
 // the loads behind it; tiles of 8 tokens, whose operands were read for each
 // direction, took 883 us for 2 x 4096 x 4096 x 16 bf16).
 template <typename T, int L, bool kVec>
-__global__ void __launch_bounds__(kMain, sizeof(T) == 2 ? 3 : 2)
+__global__ void __launch_bounds__(kMain, sizeof(T) == 2 && L <= 4 ? 3 : 2)
 scan_bwd_kernel(const ScanArgs a, const ScanBwdPlan pl, float *__restrict__ ws) {
   using G = Geo<L>;
   constexpr int CC = G::kBlock, SP = G::SP, TC = G::kChunk, QC = CC / 4;  // quads of channels
@@ -203,9 +205,10 @@ scan_bwd_kernel(const ScanArgs a, const ScanBwdPlan pl, float *__restrict__ ws) 
 
   // ---- forwards: the state before every tile
   const int tiles = live > t0 ? (live - t0 + kTile - 1) / kTile : 0;
+  auto starts = [&](int i, int c) { return reinterpret_cast<float4 *>(&sm.tile[i][warp][(c * 32 + lane) * 4]); };
   auto keep_start = [&](int i) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) sm.start[i][c][tid] = make_float4(h[c][0].x, h[c][0].y, h[c][1].x, h[c][1].y);
+    for (int c = 0; c < 2; ++c) *starts(i, c) = make_float4(h[c][0].x, h[c][0].y, h[c][1].x, h[c][1].y);
   };
   if (tiles > 0) keep_start(0);
   for (int i = 0; i + 1 < tiles; ++i) {
@@ -232,39 +235,26 @@ scan_bwd_kernel(const ScanArgs a, const ScanBwdPlan pl, float *__restrict__ ws) 
   }
 
   // ---- backwards, tile by tile
-  float sD[4] = {}, sBias[4] = {};
-  constexpr int NW = kTile / QS > 0 ? kTile / QS : 1;  // quads of a tile a thread writes
-  // What a lane gets of the sums of 8 values v = j * 2 + c (tokens j, channels c),
-  // and of sums over the warp's channels of values v = j * 4 + s.
-  constexpr int WS = L < 8 ? L : 8, WB = 32 / L < 8 ? 32 / L : 8;
-  auto put_sums = [&](float (*to)[CC], const float (&v)[8]) {
+  // (each warp by itself; what a lane gets of the sums of 8 values v = j * 2 + c,
+  // tokens j, channels c, and of sums over the warp's channels of v = j * 4 + s)
+  constexpr int WS = L < 8 ? L : 8, WB = 32 / L < 8 ? 32 / L : 8, WC = MainSmem<T, L>::kWarpChans;
+  auto put_sums = [&](float *to, const float (&v)[8]) {
     if (lane % L < WS)
 #pragma unroll
       for (int m = 0; m < 8 / WS; ++m) {
         const int idx = lane % L * (8 / WS) + m;
-        to[idx / 2][ca + idx % 2] = v[m];
+        to[idx / 2 * WC + lane / L * 2 + idx % 2] = v[m];
       }
   };
-  auto put_bc = [&](int which, int j0, const float (&v)[8]) {
+  auto put_bc = [&](int which, int t, const float (&v)[8]) {
     if (lane / L < WB)
 #pragma unroll
       for (int m = 0; m < 8 / WB; ++m) {
         const int idx = lane / L * (8 / WB) + m;
-        sm.bc[warp][j0 + idx / 4][which][s0 + idx % 4] = v[m];
+        sm.bc[warp][t + idx / 4][which][s0 + idx % 4] = v[m];
       }
   };
   for (int i = tiles - 1; i >= 0; --i) {
-    // (the channels' rows for the outputs, on their way meanwhile)
-    Four<T> xr[NW], dr[NW], yr[NW], zr[NW];
-    const bool writes = QS <= kTile || qt < kTile;
-#pragma unroll
-    for (int m = 0; m < NW; ++m) {
-      const int at = t0 + i * kTile + qt + m * QS, c = writes && at < live ? there : 0;
-      xr[m] = load_four<T, kVec>(x + at * a.sx[1], c);
-      dr[m] = load_four<T, kVec>(dt + at * a.sdt[1], a.softplus ? c : 0);
-      yr[m] = load_four<T, kVec>(dy + at * a.sdy[1], z ? c : 0);
-      zr[m] = load_four<T, kVec>(z + at * a.sz[1], z ? c : 0);
-    }
     Four<T> Br[kTile], Cr[kTile];
     float2 dv[kTile], uv[kTile], gv[kTile];
 #pragma unroll
@@ -278,7 +268,7 @@ scan_bwd_kernel(const ScanArgs a, const ScanBwdPlan pl, float *__restrict__ ws) 
     }
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      const float4 f = sm.start[i][c][tid];
+      const float4 f = *starts(i, c);
       h[c][0] = make_float2(f.x, f.y);
       h[c][1] = make_float2(f.z, f.w);
     }
@@ -335,70 +325,83 @@ scan_bwd_kernel(const ScanArgs a, const ScanBwdPlan pl, float *__restrict__ ws) 
     }
     share_sums<8, L>(qv);
     share_sums<8, L>(rv);
-    put_sums(sm.sums[0], sv);
-    put_sums(sm.sums[1], qv);
-    put_sums(sm.sums[2], rv);
+    __syncwarp();  // every lane has its start
+    put_sums(&sm.tile[i][warp][0], sv);
+    put_sums(&sm.tile[i][warp][kTile * WC], qv);
+    put_sums(&sm.tile[i][warp][2 * kTile * WC], rv);
 #pragma unroll
     for (int j = 0; j < kTile / 2; ++j) {
-      put_bc(0, j * 2, bv[j]);
-      put_bc(1, j * 2, cv[j]);
+      put_bc(0, i * kTile + j * 2, bv[j]);
+      put_bc(1, i * kTile + j * 2, cv[j]);
     }
-    __syncthreads();
-    // the channels' gradients
+  }
+  __syncthreads();
+
+  // ---- the channels' gradients
+  float sD[4] = {}, sBias[4] = {};
+#pragma unroll 1
+  for (int j0 = 0; j0 < NQ; j0 += UQ) {
+    Four<T> xr[UQ], dr[UQ], yr[UQ], zr[UQ];
 #pragma unroll
-    for (int m = 0; m < NW; ++m) {
-      const int j = qt + m * QS, at = t0 + i * kTile + j;
-      if (writes && at < live) {
-        float ddx[4], ddt[4], ddz[4];
+    for (int j = 0; j < UQ; ++j) {
+      const int at = t0 + qt + (j0 + j) * QS, m = at < live ? there : 0;
+      xr[j] = load_four<T, kVec>(x + at * a.sx[1], m);
+      dr[j] = load_four<T, kVec>(dt + at * a.sdt[1], a.softplus ? m : 0);
+      yr[j] = load_four<T, kVec>(dy + at * a.sdy[1], z ? m : 0);
+      zr[j] = load_four<T, kVec>(z + at * a.sz[1], z ? m : 0);
+    }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float xv = to_float(xr[m].v[c]), d = sm.d[i * kTile + j][qc + c], ds = sm.ds[i * kTile + j][qc + c];
-          const float s = sm.sums[0][j][qc + c], q = sm.sums[1][j][qc + c], r = sm.sums[2][j][qc + c];
-          ddt[c] = fmaf(xv, q, r * 0.6931471805599453f);  // (r has A log2(e) for A)
-          if (a.softplus) ddt[c] *= sigmoid(to_float(dr[m].v[c]) + bias[c]);
-          ddx[c] = fmaf(d, q, Dv[c] * ds);
+    for (int j = 0; j < UQ; ++j) {
+      const int t = qt + (j0 + j) * QS, at = t0 + t;
+      if (at >= t1) continue;
+      float ddx[4] = {}, ddt[4] = {}, ddz[4] = {};  // (zeros past the sequence's end)
+      if (at < live) {
+        const float4 d4 = *reinterpret_cast<const float4 *>(&sm.d[t][qc]), ds4 = *reinterpret_cast<const float4 *>(&sm.ds[t][qc]);
+        const float d[4] = {d4.x, d4.y, d4.z, d4.w}, ds[4] = {ds4.x, ds4.y, ds4.z, ds4.w};
+        const float *sums = &sm.tile[t / kTile][qc / WC][t % kTile * WC + qc % WC];
+#pragma unroll
+        for (int c = 0; c < 4; c += 2) {
+          const float2 s = *reinterpret_cast<const float2 *>(sums + c), q = *reinterpret_cast<const float2 *>(sums + kTile * WC + c);
+          const float2 r = *reinterpret_cast<const float2 *>(sums + 2 * kTile * WC + c);
+          const float2 xv = make_float2(to_float(xr[j].v[c]), to_float(xr[j].v[c + 1]));
+          const float2 dv = make_float2(d[c], d[c + 1]), g = make_float2(ds[c], ds[c + 1]), D2 = make_float2(Dv[c], Dv[c + 1]);
+          float2 v = tc::fma2(xv, q, tc::mul2(r, both(0.6931471805599453f)));  // (r has A log2(e) for A)
+          if (a.softplus)
+            v = tc::mul2(v, sigmoid2(make_float2(to_float(dr[j].v[c]) + bias[c], to_float(dr[j].v[c + 1]) + bias[c + 1])));
+          ddt[c] = v.x;
+          ddt[c + 1] = v.y;
+          v = tc::fma2(dv, q, tc::mul2(D2, g));
+          ddx[c] = v.x;
+          ddx[c + 1] = v.y;
           if (z) {
-            const float zv = to_float(zr[m].v[c]), sg = sigmoid(zv);
-            ddz[c] = to_float(yr[m].v[c]) * fmaf(Dv[c], xv, s) * sg * fmaf(zv, 1.f - sg, 1.f);
+            const float2 zv = make_float2(to_float(zr[j].v[c]), to_float(zr[j].v[c + 1])), sg = sigmoid2(zv);
+            const float2 yv = make_float2(to_float(yr[j].v[c]), to_float(yr[j].v[c + 1]));
+            const float2 slope = tc::mul2(sg, tc::fma2(zv, make_float2(1.f - sg.x, 1.f - sg.y), both(1.f)));
+            v = tc::mul2(tc::mul2(yv, tc::fma2(D2, xv, s)), slope);
+            ddz[c] = v.x;
+            ddz[c + 1] = v.y;
           }
-          if (c < there) {
-            sD[c] = fmaf(ds, xv, sD[c]);
-            sBias[c] += ddt[c];
-          }
+          sD[c] = fmaf(g.x, xv.x, sD[c]);
+          sD[c + 1] = fmaf(g.y, xv.y, sD[c + 1]);
+          sBias[c] += ddt[c];
+          sBias[c + 1] += ddt[c + 1];
         }
-        store_four<T, kVec>(reinterpret_cast<T *>(a.dx) + b * a.sdx[0] + at * a.sdx[1] + qe, there, ddx);
-        store_four<T, kVec>(reinterpret_cast<T *>(a.ddt) + b * a.sddt[0] + at * a.sddt[1] + qe, there, ddt);
-        if (z) store_four<T, kVec>(reinterpret_cast<T *>(a.dz) + b * a.sdz[0] + at * a.sdz[1] + qe, there, ddz);
       }
+      store_four<T, kVec>(reinterpret_cast<T *>(a.dx) + b * a.sdx[0] + at * a.sdx[1] + qe, there, ddx);
+      store_four<T, kVec>(reinterpret_cast<T *>(a.ddt) + b * a.sddt[0] + at * a.sddt[1] + qe, there, ddt);
+      if (z) store_four<T, kVec>(reinterpret_cast<T *>(a.dz) + b * a.sdz[0] + at * a.sdz[1] + qe, there, ddz);
     }
-    // this block's share of dB and dC
+  }
+  // this block's share of dB and dC
+  for (int o = tid; o < (t1 - t0) * 2 * SP; o += kMain) {
+    const int s = o % SP, w = o / SP % 2, at = t0 + o / (2 * SP);
+    float v = 0.f;
 #pragma unroll
-    for (int m = 0; m < (kTile * 2 * SP + kMain - 1) / kMain; ++m) {
-      const int o = tid + m * kMain;
-      if (o < kTile * 2 * SP) {
-        const int s = o % SP, w = o / SP % 2, at = t0 + i * kTile + o / (2 * SP);
-        float v = 0.f;
-#pragma unroll
-        for (int q = 0; q < kMain / 32; ++q) v += (&sm.bc[q][0][0][0])[o];
-        if (s < a.S && at < live)
-          ws[pl.bc + ((((size_t)(blk - group * per) * a.B + b) * a.N + at) * a.G + group) * 2 * a.S + w * a.S + s] = v;
-      }
-    }
-    __syncthreads();
+    for (int q = 0; q < kMain / 32; ++q) v += (&sm.bc[q][0][0][0])[o];
+    if (s < a.S)
+      ws[pl.bc + ((((size_t)(blk - group * per) * a.B + b) * a.N + at) * a.G + group) * 2 * a.S + w * a.S + s] = at < live ? v : 0.f;
   }
   pdl_launch_dependents();
-  // ---- rows past the sequence's end
-  const int end = max(live, t0);
-  const float zero[4] = {};
-  for (int at = end + qt; at < t1; at += QS) {
-    store_four<T, kVec>(reinterpret_cast<T *>(a.dx) + b * a.sdx[0] + at * a.sdx[1] + qe, there, zero);
-    store_four<T, kVec>(reinterpret_cast<T *>(a.ddt) + b * a.sddt[0] + at * a.sddt[1] + qe, there, zero);
-    if (z) store_four<T, kVec>(reinterpret_cast<T *>(a.dz) + b * a.sdz[0] + at * a.sdz[1] + qe, there, zero);
-  }
-  for (int j = tid; j < (t1 - end) * 2 * a.S; j += kMain) {
-    const int at = end + j / (2 * a.S);
-    ws[pl.bc + ((((size_t)(blk - group * per) * a.B + b) * a.N + at) * a.G + group) * 2 * a.S + j % (2 * a.S)] = 0.f;
-  }
   // ---- the chunk's sums of dA, dD and dbias
   if (own[0]) store_states(ws + (bk * a.E + ech[0]) * a.S, s0, a.S, vec, make_float4(dA[0][0].x, dA[0][0].y, dA[0][1].x, dA[0][1].y));
   if (own[1]) store_states(ws + (bk * a.E + ech[1]) * a.S, s0, a.S, vec, make_float4(dA[1][0].x, dA[1][0].y, dA[1][1].x, dA[1][1].y));
