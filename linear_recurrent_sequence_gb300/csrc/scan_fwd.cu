@@ -20,9 +20,9 @@ namespace {
 
 using namespace scan;
 
-// What the walk over the tokens is for: the outputs, the states that segments
-// leave behind, or (for the gradients) what chunks alone add.
-enum { kOut = 0, kStates = 1, kChunks = 2 };
+// What the walk over the tokens is for: the outputs, or the states that segments
+// leave behind.
+enum { kOut = 0, kStates = 1 };
 
 // A tile's rows as they were read, in a ring of kRing: kAhead tiles are on their
 // way, the tile before the current one still has its outputs to be finished.
@@ -31,7 +31,6 @@ struct __align__(16) Tile {
   static constexpr int kAhead = sizeof(T) == 2 ? 4 : 2, kRing = kAhead + 2;
   T x[Block<L>::kTile][Block<L>::kChannels], dt[Block<L>::kTile][Block<L>::kChannels];
   T z[kMode == kStates ? 1 : Block<L>::kTile][Block<L>::kChannels];
-  T dy[kMode == kChunks ? Block<L>::kTile : 1][Block<L>::kChannels];
   T B[Block<L>::kTile][Block<L>::SP], C[kMode == kStates ? 1 : Block<L>::kTile][Block<L>::SP];
 };
 
@@ -39,8 +38,7 @@ template <typename T, int L, int kMode>
 struct WalkSmem {
   __align__(16) Tile<T, L, kMode> ring[Tile<T, L, kMode>::kRing];
   float4 du[2][Block<L>::kTile][Block<L>::kChannels];  // delta, delta, u, u
-  // a lane's sum over its states (outputs), or ds (chunks)
-  float more[kMode == kStates ? 1 : 2][Block<L>::kTile][kMode == kOut ? kScan : Block<L>::kChannels];
+  float sums[kMode == kStates ? 1 : 2][Block<L>::kTile][kScan];  // of C h over a lane's states
 };
 
 // Sums of two channels' L neighbouring values each.
@@ -79,7 +77,7 @@ __device__ __forceinline__ float2 lane_sums(const float *p) {
 // copies; else the loaders read value by value.
 template <typename T, int L, int kMode, bool kAsync>
 __global__ void __launch_bounds__(kThreads, 2)
-scan_walk_kernel(const ScanArgs a, const ScanSegs seg, const ScanBwdPlan pl, float *__restrict__ ws) {
+scan_walk_kernel(const ScanArgs a, const ScanSegs seg) {
   using K = Block<L>;
   using Row = Tile<T, L, kMode>;
   constexpr int CC = K::kChannels, TT = K::kTile, SP = K::SP, kAhead = Row::kAhead, kRing = Row::kRing;
@@ -101,7 +99,6 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg, const ScanBwdPlan pl, flo
     const float4 A4 = load_states(a.A + (size_t)e * a.S, s0, a.S, vec && reinterpret_cast<uintptr_t>(a.A) % 16 == 0);
     const float2 A2[2] = {make_float2(A4.x * kLog2e, A4.y * kLog2e), make_float2(A4.z * kLog2e, A4.w * kLog2e)};
     float2 h[2] = {both(0.f), both(0.f)};
-    float2 P[2] = {both(1.f), both(1.f)}, g[2] = {both(0.f), both(0.f)};  // (chunks)
     float sum = 0.f;
     const size_t row = ((size_t)b * a.E + e) * a.S;
     if (kMode == kOut) {
@@ -119,17 +116,6 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg, const ScanBwdPlan pl, flo
         h[1] = tc::fma2(make_float2(ex2(w1.x), ex2(w1.y)), h[1], make_float2(l.z, l.w));
       }
     }
-    auto leave_chunk = [&](int i) {  // what chunk i of the segment adds
-      const size_t at = ((size_t)(t0 / TT + i) * a.B + b) * a.E + e;
-      if (own) {
-        store_states(ws + at * a.S, s0, a.S, vec, make_float4(h[0].x, h[0].y, h[1].x, h[1].y));
-        store_states(ws + pl.g + at * a.S, s0, a.S, vec, make_float4(g[0].x, g[0].y, g[1].x, g[1].y));
-        if (s0 == 0) ws[pl.sum + at] = sum;
-      }
-      h[0] = h[1] = g[0] = g[1] = both(0.f);
-      P[0] = P[1] = both(1.f);
-      sum = 0.f;
-    };
     __syncthreads();
     for (int i = 0, slot = 0; i < tiles; ++i, slot = slot + 1 == kRing ? 0 : slot + 1) {
       const int buf = i & 1;
@@ -141,7 +127,6 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg, const ScanBwdPlan pl, flo
       struct Ops {
         float4 v;
         Four<T> B, C;
-        float ds;
       } ops[2][4];
       auto operands = [&](int q, Ops (&o)[4]) {
 #pragma unroll
@@ -149,7 +134,6 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg, const ScanBwdPlan pl, flo
           o[j].v = sm.du[buf][q + j][ci];
           o[j].B = load_four<T, true>(&r.B[q + j][s0], 4);
           if (kMode != kStates) o[j].C = load_four<T, true>(&r.C[q + j][s0], 4);
-          if (kMode == kChunks) o[j].ds = sm.more[buf][q + j][ci];
         }
       };
       operands(0, ops[0]);
@@ -178,21 +162,16 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg, const ScanBwdPlan pl, flo
             const float2 C = kMode == kStates ? both(0.f) : make_float2(to_float(o[j].C.v[2 * p]), to_float(o[j].C.v[2 * p + 1]));
             h[p] = tc::fma2(d[j][p], h[p], in[j][p]);
             if (kMode == kOut) s = p ? tc::fma2(h[p], C, s) : tc::mul2(h[p], C);
-            if (kMode == kChunks) {
-              P[p] = tc::mul2(P[p], d[j][p]);
-              g[p] = tc::fma2(P[p], tc::mul2(both(o[j].ds), C), g[p]);
-            }
           }
           if (kMode == kOut) yq[j] = s.x + s.y;
         }
         // (the loaders add a channel's L lanes up: shuffles here took 96 us of 248)
         if (kMode == kOut)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) sm.more[buf][q + j][tid] = yq[j];
+          for (int j = 0; j < 4; ++j) sm.sums[buf][q + j][tid] = yq[j];
       }
       __syncthreads();
       sum += part;
-      if (kMode == kChunks) leave_chunk(i);
     }
     pdl_launch_dependents();
     const float4 h4 = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
@@ -204,8 +183,6 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg, const ScanBwdPlan pl, flo
     } else if (kMode == kOut) {
       if (k == seg.count - 1 && own && a.h_out)
         store_states(a.h_out + row, s0, a.S, vec && reinterpret_cast<uintptr_t>(a.h_out) % 16 == 0, h4);
-    } else {  // the chunks (a tile each) behind the sequence's end
-      for (int i = tiles; i < (t1 - t0 + TT - 1) / TT; ++i) leave_chunk(i);
     }
     return;
   }
@@ -262,7 +239,7 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg, const ScanBwdPlan pl, flo
   const long long at_block = (long long)group * Eg + c0;
   const int width = min(CC, Eg - c0);
   Rows fx = rows_of(a.x, b * a.sx[0] + at_block, a.sx[1], CC), fd = rows_of(a.dt, b * a.sdt[0] + at_block, a.sdt[1], CC, true);
-  Rows fz = rows_of(a.z, b * a.sz[0] + at_block, a.sz[1], CC), fy = rows_of(a.dy, b * a.sdy[0] + at_block, a.sdy[1], CC, true);
+  Rows fz = rows_of(a.z, b * a.sz[0] + at_block, a.sz[1], CC);
   Rows fB = rows_of(a.Bm, b * a.sB[0] + group * a.sB[2], a.sB[1], SP), fC = rows_of(a.Cm, b * a.sC[0] + group * a.sC[2], a.sC[1], SP, true);
   auto fetch = [&](int i) {
     if (i < tiles) {
@@ -273,7 +250,6 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg, const ScanBwdPlan pl, flo
       fetch_rows(&r.x[0][0], fx, channels, t, width);
       fetch_rows(&r.dt[0][0], fd, channels, t, width);
       if (gate) fetch_rows(&r.z[0][0], fz, channels, t, width);
-      if (kMode == kChunks) fetch_rows(&r.dy[0][0], fy, channels, t, width);
       fetch_rows(&r.B[0][0], fB, states, t, a.S);
       if (kMode != kStates) fetch_rows(&r.C[0][0], fC, states, t, a.S);
     }
@@ -297,11 +273,6 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg, const ScanBwdPlan pl, flo
       const float2 u = tc::mul2(d, xs);
       sm.du[buf][at][lc] = make_float4(d.x, d.x, u.x, u.x);
       sm.du[buf][at][lc + 1] = make_float4(d.y, d.y, u.y, u.y);
-      if (kMode == kChunks) {
-        float2 ds = to_float2(two(r.dy, at));
-        if (gate) ds = tc::mul2(ds, silu2(to_float2(two(r.z, at))));
-        *reinterpret_cast<float2 *>(&sm.more[buf][at][lc]) = ds;
-      }
     }
   };
   auto finish = [&](int i) {
@@ -312,7 +283,7 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg, const ScanBwdPlan pl, flo
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
       const int at = lt + j * TS;
-      float2 v = tc::fma2(Dv, to_float2(two(r.x, at)), lane_sums<L>(&sm.more[buf][at][lc * L]));
+      float2 v = tc::fma2(Dv, to_float2(two(r.x, at)), lane_sums<L>(&sm.sums[buf][at][lc * L]));
       if (gate) v = tc::mul2(v, silu2(to_float2(two(r.z, at))));
       const bool in = t + at < live;
       if (t + at < t1) store_pair(to, pairs, there, in ? v.x : 0.f, in ? v.y : 0.f);
@@ -434,11 +405,11 @@ bool async_ok(const ScanArgs &a, int mode) {
   };
   return a.E / a.G % V == 0 && a.S % V == 0 && bc(a.Bm, a.sB) && (mode == kStates || bc(a.Cm, a.sC)) &&
          rows_on(a, a.x, a.sx, V, esz) && rows_on(a, a.dt, a.sdt, V, esz) && (mode == kStates || rows_on(a, a.z, a.sz, V, esz)) &&
-         (mode != kChunks || rows_on(a, a.dy, a.sdy, V, esz)) && (mode != kOut || a.pair_y);
+         (mode != kOut || a.pair_y);
 }
 
 template <typename T, int L, int kMode, bool kAsync>
-cudaError_t walk_with(const ScanArgs &a, const ScanSegs &seg, const ScanBwdPlan &pl, float *ws, cudaStream_t st) {
+cudaError_t walk_with(const ScanArgs &a, const ScanSegs &seg, cudaStream_t st) {
   static std::atomic<unsigned> done{0};
   auto kern = scan_walk_kernel<T, L, kMode, kAsync>;
   const cudaError_t e = allow_big_smem(reinterpret_cast<const void *>(kern), done);
@@ -446,24 +417,24 @@ cudaError_t walk_with(const ScanArgs &a, const ScanSegs &seg, const ScanBwdPlan 
   // (the states of the last segment are nobody's entry)
   const int segs = kMode == kStates ? seg.count - 1 : seg.count;
   const dim3 grid((unsigned)(a.G * Block<L>::per_group(a.E, a.G)) * segs, a.B);
-  return launch_k(kern, grid, dim3(kThreads), sizeof(WalkSmem<T, L, kMode>), st, true, a, seg, pl, ws);
+  return launch_k(kern, grid, dim3(kThreads), sizeof(WalkSmem<T, L, kMode>), st, true, a, seg);
 }
 
 template <typename T, int kMode>
-cudaError_t walk_any(ScanArgs a, const ScanSegs &seg, const ScanBwdPlan &pl, float *ws, cudaStream_t st) {
+cudaError_t walk_any(ScanArgs a, const ScanSegs &seg, cudaStream_t st) {
   a.pair_y = rows_on(a, a.y, a.sy, 2, sizeof(T));
   const bool async = async_ok<T>(a, kMode);
   return by_lanes(a.S, [&](auto l) {
     constexpr int L = decltype(l)::value;
     if constexpr (4 * L * sizeof(T) >= 16)  // (a row of states is a vector at least)
-      if (async) return walk_with<T, L, kMode, true>(a, seg, pl, ws, st);
-    return walk_with<T, L, kMode, false>(a, seg, pl, ws, st);
+      if (async) return walk_with<T, L, kMode, true>(a, seg, st);
+    return walk_with<T, L, kMode, false>(a, seg, st);
   });
 }
 
 template <int kMode>
-cudaError_t walk(const ScanArgs &a, int bf16, const ScanSegs &seg, const ScanBwdPlan &pl, float *ws, cudaStream_t st) {
-  return bf16 ? walk_any<__nv_bfloat16, kMode>(a, seg, pl, ws, st) : walk_any<float, kMode>(a, seg, pl, ws, st);
+cudaError_t walk(const ScanArgs &a, int bf16, const ScanSegs &seg, cudaStream_t st) {
+  return bf16 ? walk_any<__nv_bfloat16, kMode>(a, seg, st) : walk_any<float, kMode>(a, seg, st);
 }
 
 template <typename T, bool kMany>
@@ -511,27 +482,11 @@ size_t scan_fwd_bytes(const ScanArgs &a) {
 }
 
 cudaError_t launch_scan_states(const ScanArgs &a, int bf16, const ScanSegs &seg, cudaStream_t st) {
-  return walk<kStates>(a, bf16, seg, ScanBwdPlan(), nullptr, st);
+  return walk<kStates>(a, bf16, seg, st);
 }
 
 cudaError_t launch_scan_fwd(const ScanArgs &a, int bf16, const ScanSegs &seg, cudaStream_t st) {
-  return walk<kOut>(a, bf16, seg, ScanBwdPlan(), nullptr, st);
-}
-
-cudaError_t launch_scan_bwd_chunks(const ScanArgs &a, int bf16, const ScanBwdPlan &pl, float *ws, cudaStream_t st) {
-  // A CTA takes up to 16 chunks one after another, so that its loads run ahead,
-  // while all SMs keep two CTAs.
-  long long blocks = 1;
-  by_lanes(a.S, [&](auto l) {
-    blocks = (long long)a.G * Block<decltype(l)::value>::per_group(a.E, a.G);
-    return cudaSuccess;
-  });
-  int run = 16;
-  while (run > 1 && blocks * a.B * ((pl.chunks + run - 1) / run) < 4LL * device_sms()) run /= 2;
-  ScanSegs seg;
-  seg.len = run * pl.chunk;
-  seg.count = (pl.chunks + run - 1) / run;
-  return walk<kChunks>(a, bf16, seg, pl, ws, st);
+  return walk<kOut>(a, bf16, seg, st);
 }
 
 cudaError_t launch_scan_step(const ScanArgs &a, int bf16, cudaStream_t st) {
