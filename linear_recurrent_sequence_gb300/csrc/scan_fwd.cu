@@ -37,11 +37,13 @@ struct __align__(16) Tile {
 template <typename T, int L, int kMode>
 struct WalkSmem {
   __align__(16) Tile<T, L, kMode> ring[Tile<T, L, kMode>::kRing];
-  float4 du[2][Block<L>::kTile][Block<L>::kChannels];  // delta, delta, u, u
+  float2 du[2][Block<L>::kTile][Block<L>::kChannels];  // delta, u
   float sums[kMode == kStates ? 1 : 2][Block<L>::kTile][kScan];  // of C h over a lane's states
 };
 
-// Sums of two channels' L neighbouring values each.
+// Sums of two channels' L neighbouring values each.  Where a channel has one
+// 16-byte vector, every other four lanes read their two in the other order: a
+// quarter of a warp then meets each bank once.
 template <int L>
 __device__ __forceinline__ float2 lane_sums(const float *p) {
   if constexpr (L == 1) {
@@ -50,17 +52,19 @@ __device__ __forceinline__ float2 lane_sums(const float *p) {
     const float4 v = *reinterpret_cast<const float4 *>(p);
     return make_float2(v.x + v.y, v.z + v.w);
   } else {
-    float2 s[2];
+    const int swap = L == 4 ? (threadIdx.x >> 2) & 1 : 0;
+    float s[2];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      s[c] = both(0.f);
+      float2 t = both(0.f);
 #pragma unroll
       for (int i = 0; i < L; i += 4) {
-        const float4 v = *reinterpret_cast<const float4 *>(p + c * L + i);
-        s[c] = tc::add2(s[c], tc::add2(make_float2(v.x, v.y), make_float2(v.z, v.w)));
+        const float4 v = *reinterpret_cast<const float4 *>(p + (c ^ swap) * L + i);
+        t = i ? tc::add2(t, tc::add2(make_float2(v.x, v.y), make_float2(v.z, v.w))) : tc::add2(make_float2(v.x, v.y), make_float2(v.z, v.w));
       }
+      s[c] = t.x + t.y;
     }
-    return make_float2(s[0].x + s[0].y, s[1].x + s[1].y);
+    return make_float2(swap ? s[1] : s[0], swap ? s[0] : s[1]);
   }
 }
 
@@ -125,7 +129,7 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg) {
       // on its scheduler has nothing else to do, and a store to shared memory
       // holds back the loads behind it.
       struct Ops {
-        float4 v;
+        float2 v;
         Four<T> B, C;
       } ops[2][4];
       auto operands = [&](int q, Ops (&o)[4]) {
@@ -144,7 +148,7 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg) {
         float2 d[4][2], in[4][2];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 dd = make_float2(o[j].v.x, o[j].v.y), uu = make_float2(o[j].v.z, o[j].v.w);
+          const float2 dd = both(o[j].v.x), uu = both(o[j].v.y);
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
             const float2 w = tc::mul2(dd, A2[p]);
@@ -271,8 +275,7 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg) {
       if (there < 1 || t + at >= live) d.x = 0.f;
       if (there < 2 || t + at >= live) d.y = 0.f;
       const float2 u = tc::mul2(d, xs);
-      sm.du[buf][at][lc] = make_float4(d.x, d.x, u.x, u.x);
-      sm.du[buf][at][lc + 1] = make_float4(d.y, d.y, u.y, u.y);
+      *reinterpret_cast<float4 *>(&sm.du[buf][at][lc]) = make_float4(d.x, u.x, d.y, u.y);
     }
   };
   auto finish = [&](int i) {
