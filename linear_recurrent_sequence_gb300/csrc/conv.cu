@@ -50,6 +50,47 @@ struct __align__(V * sizeof(T)) Chans {
   }
 };
 
+// c + a b, a b and the sigmoid for V channels, on packed pairs.
+template <int V>
+__device__ __forceinline__ void fma_v(const float (&a)[V], const float (&b)[V], float (&c)[V]) {
+  if constexpr (V == 1) {
+    c[0] = fmaf(a[0], b[0], c[0]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const float2 r = tc::fma2(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]), make_float2(c[i], c[i + 1]));
+      c[i] = r.x;
+      c[i + 1] = r.y;
+    }
+  }
+}
+template <int V>
+__device__ __forceinline__ void mul_v(const float (&a)[V], const float (&b)[V], float (&c)[V]) {
+  if constexpr (V == 1) {
+    c[0] = a[0] * b[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const float2 r = tc::mul2(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]));
+      c[i] = r.x;
+      c[i + 1] = r.y;
+    }
+  }
+}
+template <int V>
+__device__ __forceinline__ void sigmoid_v(const float (&a)[V], float (&c)[V]) {
+  if constexpr (V == 1) {
+    c[0] = sigmoid(a[0]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const float2 r = sigmoid2(make_float2(a[i], a[i + 1]));
+      c[i] = r.x;
+      c[i + 1] = r.y;
+    }
+  }
+}
+
 __device__ __forceinline__ int conv_tokens(const ConvArgs &a, int b) {
   if (!a.lengths) return a.N;
   const long long n = a.len64 ? reinterpret_cast<const long long *>(a.lengths)[b]
@@ -131,10 +172,14 @@ conv_fwd_kernel(const ConvArgs a, int run, int runs, int vec_taps) {
 #pragma unroll
       for (int k = 0; k < W - 1; ++k) win[k][v] = win[k + 1][v];
       win[W - 1][v] = in[j].get(v);
-      float s = bias[v];
+      o[v] = bias[v];
+    }
 #pragma unroll
-      for (int k = 0; k < W; ++k) s = fmaf(w[k][v], win[k][v], s);
-      o[v] = a.silu ? silu(s) : s;
+    for (int k = 0; k < W; ++k) fma_v<V>(w[k], win[k], o);
+    if (a.silu) {
+      float sg[V];
+      sigmoid_v<V>(o, sg);
+      mul_v<V>(o, sg, o);
     }
     if (more) in[j].load(x + (t + U) * a.sx[1]);
     Chans<T, V>::store(y + t * a.so[1], o);
@@ -217,26 +262,34 @@ conv_bwd_kernel(const ConvArgs a, int run, int runs, int vec_taps, float *__rest
       for (int k = W - 1; k > 0; --k) d[k][v] = d[k - 1][v];
     if (kInner || at < there) {
       const bool mine = kInner || at < t1;  // (what lies behind the run belongs to the next one's sums)
+      float pre[V], dv[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) win[k][v] = win[k + 1][v];
         win[W - 1][v] = in[j].get(v);
-        float dv = gr[j].get(v);
-        if (a.silu) {
-          float s = bias[v];
-#pragma unroll
-          for (int k = 0; k < W; ++k) s = fmaf(w[k][v], win[k][v], s);
-          const float sg = sigmoid(s);
-          dv *= sg * fmaf(s, 1.f - sg, 1.f);
-        }
-        d[0][v] = dv;
-        if (mine) {
-          db[v] += dv;
-#pragma unroll
-          for (int k = 0; k < W; ++k) dw[k][v] = fmaf(dv, win[k][v], dw[k][v]);
-        }
+        dv[v] = gr[j].get(v);
+        pre[v] = bias[v];
       }
+      if (a.silu) {  // dy sg (1 + pre (1 - sg))
+        float sg[V], t[V];
+#pragma unroll
+        for (int k = 0; k < W; ++k) fma_v<V>(w[k], win[k], pre);
+        sigmoid_v<V>(pre, sg);
+#pragma unroll
+        for (int v = 0; v < V; ++v) t[v] = 1.f - sg[v];
+        mul_v<V>(dv, sg, dv);
+        mul_v<V>(pre, t, t);
+        fma_v<V>(dv, t, dv);
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        d[0][v] = dv[v];
+        if (mine) db[v] += dv[v];
+      }
+      if (mine)
+#pragma unroll
+        for (int k = 0; k < W; ++k) fma_v<V>(dv, win[k], dw[k]);
       ahead(j, at + U);
     } else {
 #pragma unroll
@@ -244,12 +297,9 @@ conv_bwd_kernel(const ConvArgs a, int run, int runs, int vec_taps, float *__rest
     }
     if (kInner || o >= t0 || (r == 0 && o < 0)) {
       float out[V];
+      mul_v<V>(w[0], d[0], out);
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        out[v] = 0.f;
-#pragma unroll
-        for (int k = 0; k < W; ++k) out[v] = fmaf(w[k][v], d[k][v], out[v]);
-      }
+      for (int k = 1; k < W; ++k) fma_v<V>(w[k], d[k], out);
       // what the state after the sequence passes back to the last W - 1 inputs
       const int m = o - (n - (W - 1));
       if (!kInner && a.dstate_out && m >= 0 && m < W - 1) {

@@ -266,14 +266,17 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg) {
     const int buf = i & 1, t = t0 + i * TT;
     const Row &r = sm.ring[i % kRing];
     if (!mine) return;
+    const bool whole = there == 2 && t + TT <= live;
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
       const int at = lt + j * TS;
       const float2 xs = to_float2(two(r.x, at));
       float2 d = tc::add2(to_float2(two(r.dt, at)), bias);
       if (a.softplus) d = softplus2(d);
-      if (there < 1 || t + at >= live) d.x = 0.f;
-      if (there < 2 || t + at >= live) d.y = 0.f;
+      if (!whole) {
+        if (there < 1 || t + at >= live) d.x = 0.f;
+        if (there < 2 || t + at >= live) d.y = 0.f;
+      }
       const float2 u = tc::mul2(d, xs);
       *reinterpret_cast<float4 *>(&sm.du[buf][at][lc]) = make_float4(d.x, u.x, d.y, u.y);
     }
@@ -288,8 +291,10 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg) {
       const int at = lt + j * TS;
       float2 v = tc::fma2(Dv, to_float2(two(r.x, at)), lane_sums<L>(&sm.sums[buf][at][lc * L]));
       if (gate) v = tc::mul2(v, silu2(to_float2(two(r.z, at))));
-      const bool in = t + at < live;
-      if (t + at < t1) store_pair(to, pairs, there, in ? v.x : 0.f, in ? v.y : 0.f);
+      if (t + at < t1) {
+        const bool in = t + at < live;
+        store_pair(to, pairs, there, in ? v.x : 0.f, in ? v.y : 0.f);
+      }
       to += TS * a.sy[1];
     }
   };
