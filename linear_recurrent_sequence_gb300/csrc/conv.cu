@@ -208,14 +208,58 @@ conv_fwd_kernel(const ConvArgs a, int run, int runs, int vec_taps) {
   }
 }
 
-// Two channels a thread, eight tokens of x and dy in flight: the taps, the
-// window, the gradients' window and the sums of a thread leave room for two
-// CTAs an SM (2 x 4096 x 4096 bf16; four channels and four tokens, one CTA an SM:
-// 222 us).
+// A thread's tokens on their way, n tensors' values each: in shared memory, where a
+// thread reads what it copied itself (no barrier), U tokens at a time, kAhead
+// such steps ahead of their use; bf16 values one by one wait in registers.
+template <typename T, int V, int U, int n>
+struct Ahead {
+  static constexpr bool kCopies = V * sizeof(T) >= 4;
+  static constexpr int kAhead = kCopies ? 4 : 1, kSlots = kCopies ? kAhead * U : 0;
+  static constexpr size_t kBytes = (size_t)kSlots * n * kThreads * sizeof(Chans<T, V>);
+  Chans<T, V> *ring;
+  Chans<T, V> now[U][n];  // (registers, or what take() read)
+  __device__ __forceinline__ Ahead(uint8_t *dyn) : ring(reinterpret_cast<Chans<T, V> *>(dyn) + threadIdx.x) {}
+  // Token j of step s from p[0 .. n), where it is there.
+  __device__ __forceinline__ void fetch(int s, int j, bool there, const T *const (&p)[n]) {
+    if constexpr (kCopies) {
+#pragma unroll
+      for (int i = 0; i < n; ++i)
+        if (there)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(tc::smem_u32(ring + (((s % kAhead) * U + j) * n + i) * kThreads)),
+                       "l"(p[i]), "n"((int)(V * sizeof(T)))
+                       : "memory");
+    } else if (there) {
+#pragma unroll
+      for (int i = 0; i < n; ++i) now[j][i].load(p[i]);
+    }
+  }
+  __device__ __forceinline__ void commit() {
+    if (kCopies) asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  // Step s has arrived (kAhead - 1 younger ones may be on their way).
+  __device__ __forceinline__ void take(int s) {
+    if constexpr (kCopies) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+#pragma unroll
+        for (int i = 0; i < n; ++i) now[j][i] = ring[(((s % kAhead) * U + j) * n + i) * kThreads];
+    }
+  }
+};
+
+template <typename T, int V>
+constexpr int kBwdStep = V * sizeof(T) >= 4 ? 4 : 8;  // (in registers: what a step loads is all that is on its way)
+
+// Two channels a thread: the taps, the window, the gradients' window and the
+// sums of a thread take most of its registers (2 x 4096 x 4096 bf16: with eight
+// tokens of x and dy waiting in registers 84 us, with four channels a thread 222).
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 3)
 conv_bwd_kernel(const ConvArgs a, int run, int runs, int vec_taps, float *__restrict__ part) {
-  constexpr int U = 8;
+  constexpr int U = kBwdStep<T, V>;
+  using In = Ahead<T, V, U, 2>;
+  extern __shared__ __align__(16) uint8_t dyn[];
   pdl_launch_dependents();
   pdl_wait();
   const int nv = a.E / V, b = blockIdx.y;
@@ -227,15 +271,18 @@ conv_bwd_kernel(const ConvArgs a, int run, int runs, int vec_taps, float *__rest
   const T *dy = reinterpret_cast<const T *>(a.dy) + b * a.sg[0] + e;
   T *dx = reinterpret_cast<T *>(a.out) + b * a.so[0] + e;
   const int last = t1 + W - 1, there = min(n, last);  // tokens walked, of them the sequence's
-  Chans<T, V> in[U], gr[U];
-  auto ahead = [&](int j, int t) {
-    if (t < there) {
-      in[j].load(x + t * a.sx[1]);
-      gr[j].load(dy + t * a.sg[1]);
-    }
-  };
+  In in(dyn);
+  auto fetch = [&](int s) {
 #pragma unroll
-  for (int j = 0; j < U; ++j) ahead(j, t0 + j);
+    for (int j = 0; j < U; ++j) {
+      const int t = t0 + s * U + j;
+      const T *const p[2] = {x + t * a.sx[1], dy + t * a.sg[1]};
+      in.fetch(s, j, t < there, p);
+    }
+    in.commit();
+  };
+  if (In::kCopies)
+    for (int s = 0; s < In::kAhead; ++s) fetch(s);
   float w[W][V], bias[V], win[W][V], d[W][V], dw[W][V], db[V];  // d[k]: of the token k before
   load_taps<V, W>(a, e, vec_taps, w, bias);
 #pragma unroll
@@ -267,8 +314,8 @@ conv_bwd_kernel(const ConvArgs a, int run, int runs, int vec_taps, float *__rest
       for (int v = 0; v < V; ++v) {
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) win[k][v] = win[k + 1][v];
-        win[W - 1][v] = in[j].get(v);
-        dv[v] = gr[j].get(v);
+        win[W - 1][v] = in.now[j][0].get(v);
+        dv[v] = in.now[j][1].get(v);
         pre[v] = bias[v];
       }
       if (a.silu) {  // dy sg (1 + pre (1 - sg))
@@ -290,7 +337,6 @@ conv_bwd_kernel(const ConvArgs a, int run, int runs, int vec_taps, float *__rest
       if (mine)
 #pragma unroll
         for (int k = 0; k < W; ++k) fma_v<V>(dv, win[k], dw[k]);
-      ahead(j, at + U);
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) d[0][v] = 0.f;
@@ -314,7 +360,10 @@ conv_bwd_kernel(const ConvArgs a, int run, int runs, int vec_taps, float *__rest
         Chans<T, V>::store(reinterpret_cast<T *>(a.dstate_in) + ((size_t)b * (W - 1) + W - 1 + o) * a.E + e, out);
     }
   };
-  for (int t = t0; t < last; t += U) {
+  for (int t = t0, s = 0; t < last; t += U, ++s) {
+    if (!In::kCopies) fetch(s);
+    in.take(s);
+    if (In::kCopies) fetch(s + In::kAhead);  // (take() has read this step's slots)
     if (t > t0 && t + U <= min(there, t1)) {
 #pragma unroll
       for (int j = 0; j < U; ++j) step(j, t + j, std::true_type());
@@ -369,7 +418,10 @@ template <typename T, int V, int W>
 cudaError_t bwd(const ConvArgs &a, float *part, cudaStream_t st) {
   const int runs = conv_bwd_runs(a) / a.B, run = std::max(4, (a.N + runs - 1) / runs);
   const dim3 grid((unsigned)(((long long)(a.E / V) * runs + kThreads - 1) / kThreads), a.B);
-  return launch_k(conv_bwd_kernel<T, V, W>, grid, dim3(kThreads), 0, st, true, a, run, runs, taps_on(a), part);
+  static std::atomic<unsigned> done{0};
+  const cudaError_t err = allow_big_smem(reinterpret_cast<const void *>(conv_bwd_kernel<T, V, W>), done);
+  if (err != cudaSuccess) return err;
+  return launch_k(conv_bwd_kernel<T, V, W>, grid, dim3(kThreads), Ahead<T, V, kBwdStep<T, V>, 2>::kBytes, st, true, a, run, runs, taps_on(a), part);
 }
 
 template <typename T, int V>
