@@ -62,11 +62,17 @@ cudaError_t launch_colsum(const ColSum &s, cudaStream_t st) {
   bool vec = true;  // 16-byte vectors of columns
   for (int i = 0; i < n; ++i)
     vec = vec && (!s.out[i] || (s.cols[i] % 4 == 0 && s.stride[i] % 4 == 0 && reinterpret_cast<uintptr_t>(s.part[i]) % 16 == 0));
-  // Eight parts at a time, by vectors of columns where those are there and fill the
-  // SMs; many parts of few columns 32 at a time.
-  if (s.count > 128 && most < 16384) return launch_k(colsum_kernel<1, 32>, dim3((most + 31) / 32, n), dim3(1024), 0, st, true, s);
-  if (vec && most >= 16384) return launch_k(colsum_kernel<4, 8>, dim3((most + 127) / 128, n), dim3(256), 0, st, true, s);
-  return launch_k(colsum_kernel<1, 8>, dim3((most + 31) / 32, n), dim3(256), 0, st, true, s);
+  // Vectors of columns where they are there and enough; eight parts at a time
+  // where those are few or the columns fill the SMs, else 32.
+  const bool many = s.count > 128;
+  if (vec && most >= 16384) {
+    const dim3 grid((most + 127) / 128, n);
+    if (many && most < 128 * 4 * device_sms()) return launch_k(colsum_kernel<4, 32>, grid, dim3(1024), 0, st, true, s);
+    return launch_k(colsum_kernel<4, 8>, grid, dim3(256), 0, st, true, s);
+  }
+  const dim3 grid((most + 31) / 32, n);
+  if (many) return launch_k(colsum_kernel<1, 32>, grid, dim3(1024), 0, st, true, s);
+  return launch_k(colsum_kernel<1, 8>, grid, dim3(256), 0, st, true, s);
 }
 
 }  // namespace ret

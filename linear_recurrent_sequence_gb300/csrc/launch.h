@@ -372,7 +372,7 @@ struct RmsArgs {
   float *rstd = nullptr, *scales = nullptr;
   RowSet sx, sr, sh, sg, sdh, so;
   long long rows = 0;
-  int d = 0, group = 0, groups = 1;  // group: columns of a scale
+  int d = 0, group = 0, groups = 1, shift = -1;  // group: columns of a scale; 2^shift of them (launcher)
   float eps = 0.f;
 };
 cudaError_t launch_rmsnorm_fwd(const RmsArgs &a, int bf16, cudaStream_t st);

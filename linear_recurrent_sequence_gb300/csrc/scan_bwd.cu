@@ -39,13 +39,13 @@ struct Geo {
 };
 
 // The state before each chunk (y = 0) and the gradient that arrives behind it
-// (y = 1), in the places of what the chunks add; also dh_in.  Eight chunks'
+// (y = 1), in the places of what the chunks add; also dh_in.  Sixteen chunks'
 // values are read before any of them is replaced.
 __global__ void __launch_bounds__(256)
 scan_bwd_carry_kernel(const ScanArgs a, const ScanBwdPlan pl, float *__restrict__ ws) {
   pdl_launch_dependents();
   pdl_wait();
-  constexpr int U = 8;
+  constexpr int U = 16;
   const long long n = (long long)a.B * a.E * a.S, i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= n) return;
   const long long be = i / a.S;
