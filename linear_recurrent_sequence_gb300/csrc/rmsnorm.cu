@@ -515,10 +515,11 @@ cudaError_t fwd_any(const RmsArgs &a, cudaStream_t st) {
     const size_t smem = kQuant ? (size_t)per * a.groups * 4 : 0;
     return launch_k(rms_fwd_kernel<T, V, NV, kQuant>, dim3((unsigned)std::min(want, most)), dim3(threads), smem, st, true, a, tpr);
   };
-  // A CTA a row, about 8 values a thread, read again for the output.
+  // A CTA a row, 16 values a thread (long rows: 1024 threads), read again for the
+  // output.  (8 a thread: 16000 x 4099 bf16 with e4m3 output 338 us for 262.)
   auto again = [&] {
     const long long cap = 1LL << 30;
-    const int threads = std::min(1024, ((a.d + 7) / 8 + 31) / 32 * 32);
+    const int threads = a.d > 512 * 16 ? 1024 : ((a.d + 15) / 16 + 31) / 32 * 32;
     return launch_k(rms_fwd_long_kernel<T, V, kQuant>, dim3((unsigned)std::min(a.rows, cap)), dim3(threads), 0, st, true, a);
   };
   const bool few = a.rows * ((a.d + 7) / 8) <= (long long)sms * 1024;
