@@ -117,7 +117,9 @@ struct RowIn {
 
 // tpr threads a row, NV vectors of V values a thread, interleaved; the row
 // stays in registers, and the next one is on its way meanwhile.  kQuant: e4m3
-// output.
+// output.  16384 x 4096 bf16 with a residual 86 us (6.2 TB/s), without the next
+// row's loads 105; e4m3 with groups of 128 16000 x 4096 124 us (3.7 TB/s: two more
+// meetings of the CTA a row).
 template <typename T, int V, int NV, bool kQuant>
 __global__ void __launch_bounds__(512)
 rms_fwd_kernel(const RmsArgs a, int tpr) {
@@ -321,7 +323,8 @@ rms_fwd_long_kernel(const RmsArgs a) {
 }
 
 // dx of the rows of the CTA, and its sums of dy n: a thread keeps those of its
-// own columns in registers.
+// own columns in registers.  8192 x 4096 bf16 64 us (4.2 TB/s; latency of a row's
+// steps), without the next row's loads 75; 60000 x 1001 value by value 253.
 template <typename T, int V, int NV>
 __global__ void __launch_bounds__(512)
 rms_bwd_kernel(const RmsArgs a, int tpr, float *__restrict__ part) {

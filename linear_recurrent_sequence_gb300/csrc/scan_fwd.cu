@@ -68,17 +68,22 @@ __device__ __forceinline__ float2 lane_sums(const float *p) {
   }
 }
 
-// A third of the CTA's warps walks the recurrence; the others keep the ring filled,
-// work out step sizes and inputs a tile ahead, and finish the outputs of the
-// tile before: with one sequence an SM has no more than one recurrence warp a
-// scheduler, and everything else that a token needs runs beside it.
-// Bound by shared memory and the recurrence warps' own latency: a lane reads its
-// four states' B and C for each token (as bf16 where they are: 16 bytes a lane,
-// fp32 32), which every lane-byte costs, equal or not.  Loads that wait in
-// registers instead of a ring had a tile's time to arrive: 479 us for 8192 x 4096 x
-// 16 bf16.
+// A third of the CTA's warps walks the recurrence; the others keep the ring
+// filled, work out step sizes and inputs a tile ahead, and add up and finish the
+// outputs of the tile before: with one sequence an SM has no more than one
+// recurrence warp a scheduler, and everything else that a token needs runs beside
+// it.  8192 x 4096 channels x 16 states bf16: 263 us.  Bound by issue slots (82%
+// where they are busiest: 128 of 152 SMs have a CTA), 190 lane-instructions a
+// token and channel; before that by shared memory, where a lane's bytes cost the
+// same whether other lanes read them too: B and C stay in the tensors' type
+// (16 bytes a lane for bf16, 32 for fp32), delta and u are kept once.  Loads that
+// waited in registers instead of a ring had a tile's time to arrive (479 us), sums
+// over the lanes by shuffles 301 us for 289, half the loaders 291 for 271.
+// The next kernel is let in at the end, not at the start: its CTAs would gather on
+// the SMs that have none of this grid's and stay there (1129 us a call, one among
+// others, for 641 at that time).
 // kAsync: every row begins on a 16-byte boundary and arrives by asynchronous
-// copies; else the loaders read value by value.
+// copies; else the loaders read value by value (3 x 1001 x 1537 x 11 fp32: 49 us).
 template <typename T, int L, int kMode, bool kAsync>
 __global__ void __launch_bounds__(kThreads, 2)
 scan_walk_kernel(const ScanArgs a, const ScanSegs seg) {
@@ -169,7 +174,7 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg) {
           }
           if (kMode == kOut) yq[j] = s.x + s.y;
         }
-        // (the loaders add a channel's L lanes up: shuffles here took 96 us of 248)
+        // (the loaders add a channel's L lanes up)
         if (kMode == kOut)
 #pragma unroll
           for (int j = 0; j < 4; ++j) sm.sums[buf][q + j][tid] = yq[j];
@@ -326,7 +331,10 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg) {
 // One token.  A lane has four states of R sequences' same channel at a time and
 // walks over the sequences, so that A is read once for them and the next ones'
 // states are on their way; what a sequence's channel needs once (step size,
-// gate, output) is shared out over the channel's lanes.
+// gate, output) is shared out over the channel's lanes.  Bound by the states'
+// bytes and, at 16 warps an SM, by latency: 128 x 8192 x 16 bf16 45 us (3.2 TB/s;
+// one CTA for each four sequences, without the next ones' loads, 54), 1 x 8192 x
+// 16 8 us.
 constexpr int kStepThreads = 256;
 
 template <typename T, int R>
