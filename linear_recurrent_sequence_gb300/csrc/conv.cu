@@ -252,12 +252,13 @@ struct Ahead {
 template <typename T, int V>
 constexpr int kBwdStep = V * sizeof(T) >= 4 ? 4 : 8;  // (in registers: what a step loads is all that is on its way)
 
-// Two channels a thread: the taps, the window, the gradients' window and the
-// sums of a thread take most of its registers (2 x 4096 x 4096 bf16 72 us, 2.8
-// TB/s: latency of the chain of windows; with eight tokens of x and dy waiting in
-// registers 84, with four channels a thread 222).
+// The taps, the window, the gradients' window and the sums of a thread's channels
+// take most of its registers: four channels (bf16) leave two CTAs an SM, two three.
+// 2 x 4096 x 4096 bf16 60 us (3.3 TB/s): the latency of a token's chain at 16 warps
+// an SM; with two channels a thread 70, with four whose tokens waited in registers
+// 222 (one CTA an SM).
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, V == 4 ? 2 : 3)
 conv_bwd_kernel(const ConvArgs a, int run, int runs, int vec_taps, float *__restrict__ part) {
   constexpr int U = kBwdStep<T, V>;
   using In = Ahead<T, V, U, 2>;
@@ -383,8 +384,9 @@ conv_bwd_kernel(const ConvArgs a, int run, int runs, int vec_taps, float *__rest
   for (int v = 0; v < V; ++v)
 #pragma unroll
     for (int k = 0; k < W; ++k) f[v * W + k] = dw[k][v];
-  if constexpr (V == 2) {  // (E is even, the workspace aligned)
-    *reinterpret_cast<float2 *>(pb) = make_float2(db[0], db[1]);
+  if constexpr (V >= 2) {  // (E is even, the workspace aligned)
+#pragma unroll
+    for (int v = 0; v < V; v += 2) *reinterpret_cast<float2 *>(pb + v) = make_float2(db[v], db[v + 1]);
 #pragma unroll
     for (int v = 0; v < V * W; v += 2) *reinterpret_cast<float2 *>(pw + v) = make_float2(f[v], f[v + 1]);
   } else {
@@ -468,15 +470,16 @@ cudaError_t launch_conv_fwd(const ConvArgs &a, int bf16, cudaStream_t st) {
 
 // Runs of tokens over all sequences.
 int conv_bwd_runs(const ConvArgs &a) {
-  return runs_of(a.N, run_of(a, std::max(1, a.E / 2), 3, 16, 128)) * a.B;
+  return runs_of(a.N, run_of(a, std::max(1, a.E / 4), 2, 16, 128)) * a.B;
 }
 
 cudaError_t launch_conv_bwd(const ConvArgs &a, int bf16, float *part, cudaStream_t st) {
   const int esz = bf16 ? 2 : 4;
   const void *flat[] = {a.state_in, a.dstate_in, a.dstate_out};
-  const bool v = vectors(a, 2, flat, 3, esz) && aligned(a.dy, a.sg, a.B, a.N, 2 * esz, esz);
-  if (bf16) return v ? bwd_taps<__nv_bfloat16, 2>(a, part, st) : bwd_taps<__nv_bfloat16, 1>(a, part, st);
-  return v ? bwd_taps<float, 2>(a, part, st) : bwd_taps<float, 1>(a, part, st);
+  auto on = [&](int V) { return vectors(a, V, flat, 3, esz) && aligned(a.dy, a.sg, a.B, a.N, V * esz, esz); };
+  if (!bf16) return on(2) ? bwd_taps<float, 2>(a, part, st) : bwd_taps<float, 1>(a, part, st);
+  if (on(4)) return bwd_taps<__nv_bfloat16, 4>(a, part, st);
+  return on(2) ? bwd_taps<__nv_bfloat16, 2>(a, part, st) : bwd_taps<__nv_bfloat16, 1>(a, part, st);
 }
 
 }  // namespace ret
