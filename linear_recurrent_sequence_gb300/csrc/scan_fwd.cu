@@ -332,7 +332,7 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg) {
 // walks over the sequences, so that A is read once for them and the next ones'
 // states are on their way; what a sequence's channel needs once (step size,
 // gate, output) is shared out over the channel's lanes.  Bound by the states'
-// bytes and, at 16 warps an SM, by latency: 128 x 8192 x 16 bf16 45 us (3.2 TB/s;
+// bytes and, at 16 warps an SM, by latency: 128 x 8192 x 16 bf16 43 us (3.3 TB/s;
 // one CTA for each four sequences, without the next ones' loads, 54), 1 x 8192 x
 // 16 8 us.
 constexpr int kStepThreads = 256;
@@ -461,9 +461,10 @@ cudaError_t step_any(const ScanArgs &a, cudaStream_t st) {
   const bool vec = a.S % 4 == 0 && on(a.Bm, a.sB) && on(a.Cm, a.sC);
   return by_lanes(a.S, [&](auto l) {
     constexpr int L = decltype(l)::value, CC = kStepThreads / L, R = !kMany ? 1 : L < 4 ? L : 4;
-    // Enough walks over the sequences to fill the SMs twice.
+    // Walks over the sequences for three waves of two CTAs an SM (one wave, which
+    // leaves SMs with one CTA beside others with two: 45 us for 43).
     const int nx = (a.E + CC - 1) / CC, groups = (a.B + R - 1) / R;
-    const int ny = kMany ? std::min(groups, std::max(1, 2 * device_sms() / nx)) : groups;
+    const int ny = kMany ? std::min(groups, std::max(1, 6 * device_sms() / nx)) : groups;
     const dim3 grid(nx, ny);
     return vec ? launch_k(scan_step_kernel<T, L, R, true>, grid, dim3(kStepThreads), 0, st, true, a)
                : launch_k(scan_step_kernel<T, L, R, false>, grid, dim3(kStepThreads), 0, st, true, a);
