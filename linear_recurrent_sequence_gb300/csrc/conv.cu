@@ -136,9 +136,9 @@ __device__ __forceinline__ Chans<T, V> input_at(const ConvArgs &a, int b, int e,
 
 // run: tokens of a thread, at least W - 1 (then only the first run reads the
 // state, which state_out may be).  U tokens' loads (64 bytes) are in flight; the inputs
-// stay as they were read until their turn (8192 x 4096 bf16 37 us, 3.6 TB/s: latency at 24 warps
+// stay as they were read until their turn (8192 x 4096 bf16 32 us, 4.2 TB/s: latency at 24 warps
 // an SM; with four tokens of eight channels in flight, converted at once, 124;
-// through shared memory 44).
+// through shared memory 44 for 37).
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(kThreads, 3)
 conv_fwd_kernel(const ConvArgs a, int run, int runs, int vec_taps) {
@@ -403,8 +403,8 @@ bool aligned(const void *p, const long long s[2], int B, int N, int bytes, int e
 
 // Tokens of a thread, so that the waves of CTAs (per_sm at once) that the call
 // takes are as short as they can be: `ends` more tokens' time go into a run's
-// ends (the W - 1 tokens read twice, taps, sums).  2 x 4096 x 4096 bf16 backward
-// with 64 (2.2 waves) 72 us.
+// ends (the W - 1 tokens read twice, taps, sums).  8192 x 4096 bf16 forward 32 us,
+// with 32 tokens (2.2 waves) 37.
 int run_of(const ConvArgs &a, int nv, int per_sm, int ends, int most) {
   const long long slots = (long long)device_sms() * per_sm;
   int best = 4;

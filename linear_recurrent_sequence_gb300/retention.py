@@ -1116,26 +1116,34 @@ def causal_conv_bwd(x, w, b, dy, *, silu=True, state_in=None, dstate_out=None, l
 
 
 @functools.lru_cache(maxsize=256)
-def _rms_desc(shape, dtype, eps, group, sx, sr, sh, sg, so, device):
-    """(descriptor, workspace bytes of the backward on that device)."""
-    n0, n1, st = _row_strides("rmsnorm", shape, sx, sr, sh, sg, so)
-    d = RmsNormDesc(n0, n1, shape[-1], _dtype_code(dtype), eps, group, *st)
+def _rms_plan(device, eps, group, x, r, w, h, out, vectors, dy=None):
+    """(descriptor, workspace bytes of the backward on that device), after checks
+    of the tensors: r, h (None: x), out and dy like x (out with a group: e4m3);
+    vectors: (name, fp32 tensor, its shape)."""
+    shape = x[0]
+    for name, m in (("residual", r), ("residual_out", h), ("dy", dy), ("out", out if group is None else None)):
+        if m is not None and (m[0] != shape or m[2] != x[2]):
+            name = {"residual": "dh", "out": "dx"}.get(name, name) if dy is not None else name
+            raise ValueError(f"{name} must have the shape {tuple(shape)} and dtype {x[2]}")
+    if group is not None and (out[0] != shape or out[2] != torch.float8_e4m3fn):
+        raise ValueError(f"out must have the shape {tuple(shape)} and dtype torch.float8_e4m3fn")
+    _meta_f32("w", w, shape[-1:])
+    for name, m, want in vectors:
+        _meta_f32(name, m, want)
+    sx = x[1]
+    n0, n1, st = _row_strides("rmsnorm", shape, sx, sx if r is None else r[1], sx if h is None else h[1],
+                              sx if dy is None else dy[1], out[1])
+    d = RmsNormDesc(n0, n1, shape[-1], _dtype_code(x[2]), eps, group or 0, *st)
     return d, int(lib.retnet_rmsnorm_bwd_workspace_size(ctypes.byref(d)))
 
 
-def _rms_sum(x, w, residual, residual_out):
-    """Checks of the norm's inputs; gives where their sum is kept (x without a
-    residual)."""
-    _f32("w", w, x.shape[-1:])
+def _rms_sum(x, residual, residual_out):
+    """Where the sum is kept (None without a residual: x is the sum)."""
     if residual is None:
         if residual_out is not None:
             raise ValueError("residual_out needs a residual")
-        return x
-    _like("residual", residual, x)
-    if residual_out is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _like("residual_out", residual_out, x)
-    return residual_out
+        return None
+    return torch.empty(x.shape, dtype=x.dtype, device=x.device) if residual_out is None else residual_out
 
 
 def rmsnorm_fwd(x, w=None, *, residual=None, eps=1e-5, out=None, residual_out=None, rstd=None, stream=None):
@@ -1145,21 +1153,17 @@ def rmsnorm_fwd(x, w=None, *, residual=None, eps=1e-5, out=None, residual_out=No
     (x itself without a residual) and rstd, fp32 of x.shape[:-1], are what
     rmsnorm_bwd takes.  residual_out, where h is kept, and out may be x or
     residual, but not the same one."""
-    h = _rms_sum(x, w, residual, residual_out)
+    h = _rms_sum(x, residual, residual_out)
+    shape = x.shape
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    else:
-        _like("out", out, x)
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
     if rstd is None:
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    _f32("rstd", rstd, x.shape[:-1])
-    sx, so = x.stride(), out.stride()
-    desc, _ = _rms_desc(x.shape, x.dtype, float(eps), 0, sx, sx if residual is None else residual.stride(),
-                        h.stride(), so, so, x.device)
-    st = lib.retnet_rmsnorm_fwd(
-        ctypes.byref(desc), *_ptrs(x, residual, w, None if residual is None else h, out, rstd), _stream(stream))
+        rstd = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
+    desc, _ = _rms_plan(x.device, float(eps), None, _meta(x), _meta(residual), _meta(w), _meta(h), _meta(out),
+                        (("rstd", _meta(rstd), shape[:-1]),))
+    st = lib.retnet_rmsnorm_fwd(ctypes.byref(desc), *_ptrs(x, residual, w, h, out, rstd), _stream(stream))
     _check(st, "retnet_rmsnorm_fwd")
-    return out, h, rstd
+    return out, x if h is None else h, rstd
 
 
 def rmsnorm_quant(x, w=None, *, residual=None, eps=1e-5, group=0, out=None, scales=None, residual_out=None,
@@ -1168,26 +1172,20 @@ def rmsnorm_quant(x, w=None, *, residual=None, eps=1e-5, group=0, out=None, scal
     scale for each `group` columns (a multiple of 8; 0: the whole row): y = q
     scale, scale = max |y| / 448.  Returns (q, scales, h), scales of x.shape[:-1]
     + (groups,)."""
-    h = _rms_sum(x, w, residual, residual_out)
+    h = _rms_sum(x, residual, residual_out)
     group, d = operator.index(group), x.shape[-1]
-    if out is None:
-        out = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
-    elif out.shape != x.shape or out.dtype != torch.float8_e4m3fn:
-        raise ValueError(f"out must have the shape {tuple(x.shape)} and dtype torch.float8_e4m3fn")
     if group < 0 or group % 8:
         raise ValueError(f"group must be 0 or a multiple of 8, got {group}")
+    if out is None:
+        out = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
     shape = (*x.shape[:-1], -(-d // group) if group else 1)
     if scales is None:
         scales = torch.empty(shape, dtype=torch.float32, device=x.device)
-    _f32("scales", scales, shape)
-    sx, so = x.stride(), out.stride()
-    desc, _ = _rms_desc(x.shape, x.dtype, float(eps), group, sx, sx if residual is None else residual.stride(),
-                        h.stride(), so, so, x.device)
-    st = lib.retnet_rmsnorm_quant(
-        ctypes.byref(desc), *_ptrs(x, residual, w, None if residual is None else h, out, scales),
-        _stream(stream))
+    desc, _ = _rms_plan(x.device, float(eps), group, _meta(x), _meta(residual), _meta(w), _meta(h), _meta(out),
+                        (("scales", _meta(scales), shape),))
+    st = lib.retnet_rmsnorm_quant(ctypes.byref(desc), *_ptrs(x, residual, w, h, out, scales), _stream(stream))
     _check(st, "retnet_rmsnorm_quant")
-    return out, scales, h
+    return out, scales, x if h is None else h
 
 
 def rmsnorm_bwd(h, dy, w, rstd, *, dh=None, dx=None, dw=None, workspace=None, stream=None):
@@ -1198,19 +1196,10 @@ def rmsnorm_bwd(h, dy, w, rstd, *, dh=None, dx=None, dw=None, workspace=None, st
     shape, d = h.shape, h.shape[-1:]
     if dx is None:
         dx = torch.empty(shape, dtype=h.dtype, device=h.device)
-    else:
-        _like("dx", dx, h)
     if dw is None:
         dw = torch.empty(d, dtype=torch.float32, device=h.device)
-    _like("dy", dy, h)
-    if dh is not None:
-        _like("dh", dh, h)
-    _f32("w", w, d)
-    _f32("rstd", rstd, shape[:-1])
-    _f32("dw", dw, d)
-    s = h.stride()
-    desc, nbytes = _rms_desc(shape, h.dtype, 0.0, 0, s, s if dh is None else dh.stride(), s, dy.stride(),
-                             dx.stride(), h.device)
+    desc, nbytes = _rms_plan(h.device, 0.0, None, _meta(h), _meta(dh), _meta(w), None, _meta(dx),
+                             (("rstd", _meta(rstd), shape[:-1]), ("dw", _meta(dw), d)), _meta(dy))
     if workspace is None:
         with _on(stream):
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=h.device)

@@ -274,4 +274,4 @@ def test_checks_are_found_by_shapes_and_not_by_tensors(R, monkeypatch):
         assert given[-1][0].eps == want
     R._scan_plan.cache_clear()
     R._conv_plan.cache_clear()
-    R._rms_desc.cache_clear()
+    R._rms_plan.cache_clear()
