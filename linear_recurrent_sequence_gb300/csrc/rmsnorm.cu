@@ -530,8 +530,9 @@ cudaError_t fwd_any(const RmsArgs &a, cudaStream_t st) {
   // Value by value the registers of a long row spill: 16000 x 4099 bf16 with e4m3
   // output 1011 us (read again 262), 5000 x 12001 without 773 (219).
   if constexpr (V == 1) {
-    if (kQuant || a.d > 512 * 16) return again();
-    return go(std::integral_constant<int, 16>());
+    if constexpr (!kQuant)
+      if (a.d <= 512 * 16) return go(std::integral_constant<int, 16>());
+    return again();
   } else {
     if (a.d <= 512 * 16) return go(std::integral_constant<int, 16 / V>());
     if (a.d <= 512 * 32) return go(std::integral_constant<int, 32 / V>());

@@ -150,26 +150,7 @@ template <typename T>
 struct __align__(2 * sizeof(T)) Two {
   T a, b;
 };
-// kPair: the row begins on the pair's boundary.  n: channels that are there.
-template <typename T, bool kPair>
-__device__ __forceinline__ Two<T> load_two(const T *p, int n) {
-  Two<T> v;
-  if (kPair) {
-    if constexpr (sizeof(T) == 2) {
-      const uint32_t w = n > 0 ? *reinterpret_cast<const uint32_t *>(p) : 0u;
-      v = *reinterpret_cast<const Two<T> *>(&w);
-    } else {
-      const float2 w = n > 0 ? *reinterpret_cast<const float2 *>(p) : make_float2(0.f, 0.f);
-      v.a = w.x;
-      v.b = w.y;
-    }
-  } else {
-    v.a = n > 0 ? p[0] : from_float<T>(0.f);
-    v.b = n > 1 ? p[1] : from_float<T>(0.f);
-  }
-  return v;
-}
-
+// To a row; kPair: it begins on the pair's boundary.  n: channels that are there.
 template <typename T, bool kPair>
 __device__ __forceinline__ void store_two(T *p, int n, float a, float b) {
   if (kPair) {
