@@ -529,7 +529,9 @@ typedef struct {
  * delta_t = softplus(dt_t + bias),
  *   h_t[s] = e^(delta_t A[s]) h_{t-1}[s] + delta_t x_t B_t[s],
  *   y_t = (sum_s C_t[s] h_t[s] + D x_t) silu(z_t).
- * fp32 arithmetic and states.  A: fp32 [E][S], finite, and delta_t A <= 0: the
+ * fp32 arithmetic and states; a decay e^(delta_t A), or a product of decays,
+ * below 2^-126 counts as 0 (up to 2^-126 of the state it multiplies is lost;
+ * the backward pass takes the same decays).  A: fp32 [E][S], finite, and delta_t A <= 0: the
  * products of many tokens' decays are formed, which would overflow where they
  * grow (without softplus this needs steps >= 0).  D, bias: fp32 [E],
  * NULL = 0.  z NULL: no gate.  h_in: fp32 [B][E][S], NULL = 0; h_out: the state

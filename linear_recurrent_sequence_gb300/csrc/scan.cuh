@@ -12,6 +12,10 @@
 namespace ret {
 namespace scan {
 
+// Decays e^(delta A) are ex2() of delta (A log2 e): flushed to zero below 2^-126,
+// which loses at most 2^-126 of the state, and shows only where nothing is added
+// to it (x = 0).  Keeping them would take a scale and a product more for each
+// exponential, the unit that bounds the scan.
 constexpr float kLog2e = 1.4426950408889634f;
 
 // 1 / x by the hardware's approximation (2^-23 of itself).

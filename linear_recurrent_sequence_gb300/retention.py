@@ -958,6 +958,7 @@ def selective_scan_fwd(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, softplus
     [B, N, S]): with delta = softplus(dt + dt_bias),
         h_t = exp(delta_t A) h_(t-1) + delta_t x_t B_t,
         y_t = (C_t . h_t + D x_t) silu(z_t).
+    A decay exp(delta_t A) below 2^-126 counts as 0.
     D, dt_bias fp32 [E]; z like x; h_in fp32 [B, E, S] (None: 0); lengths int32
     or int64 [B] on the device: tokens of each sequence of a padded batch, rows
     of y behind them are zeros.  Returns (y, the states after the last tokens)."""

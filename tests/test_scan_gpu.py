@@ -300,3 +300,30 @@ def test_other_stream_and_graph(R):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(first, got))
+
+
+@pytest.mark.parametrize("S", [3, 16, 64])
+@pytest.mark.parametrize("prompt", [False, True])
+def test_decays_at_the_end_of_the_normal_numbers(R, prompt, S):
+    """x = 0, so that the state is the decayed one alone.  The exponent delta A log2(e) has
+    three roundings (the constant, A log2(e), its product with delta), each 2^-24 of |w| <= 131,
+    the exponential 2^-22 of itself; below 2^-126 it counts as 0, 2^-126 of the state at most."""
+    E, U = 40, 2.0 ** -24
+    shape = (2, 1, E) if prompt else (2, E)
+    x, dt = torch.zeros(shape, device="cuda"), torch.ones(shape, device="cuda")
+    A = -(math.log(2) * torch.linspace(121, 131, S, device="cuda")).expand(E, S).contiguous()
+    B = torch.ones(*shape[:-1], 1, S, device="cuda")
+    h0 = rand(gen(31), 2, E, S)
+    if prompt:
+        _, h = R.selective_scan_fwd(x, dt, A, B, B, softplus=False, h_in=h0)
+    else:
+        h = torch.empty_like(h0)
+        R.selective_scan_step(x, dt, A, B, B, h0, softplus=False, h_out=h)
+    want = torch.exp(A.double()) * h0.double()
+    rel = 3 * U * A.double().abs() + 8 * U
+    # (a product of a decay above 2^-126 and |h0| < 1 is rounded to 2^-149)
+    bound = want.abs() * rel + 2.0 ** -126 * (1 + rel) * h0.double().abs() + 2.0 ** -149
+    assert bool(((h.double() - want).abs() <= bound).all())
+    low = A.double() / math.log(2) < -126.1
+    assert bool((h[low.expand_as(h)] == 0).all())
+    assert bool((h[(A.double() / math.log(2) > -125.9).expand_as(h)] != 0).all())
