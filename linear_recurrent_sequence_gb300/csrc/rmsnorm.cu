@@ -289,8 +289,10 @@ rms_fwd_long_kernel(const RmsArgs a) {
       }
     } else {
       uint8_t *y = reinterpret_cast<uint8_t *>(a.out) + row_offset(a.so, r);
-      // a warp for each group, or all of them for wide ones (what others kept
-      // of the sum is visible since they met above)
+      // a warp for each group, or all of them for wide ones (what others kept of
+      // the sum is visible: several warps met above, the lanes of one meet here,
+      // since its shuffles do not order memory)
+      __syncwarp();
       const bool wide = a.group > 1024;
       const int lead = (wide ? threadIdx.x : threadIdx.x & 31) * V, hop = (wide ? blockDim.x : 32) * V;
       for (int g = wide ? 0 : threadIdx.x >> 5; g < a.groups; g += wide ? 1 : blockDim.x >> 5) {

@@ -1,0 +1,48 @@
+"""GPU tests of the RMS norm's e4m3 output at the sizes where its kernels change
+their way: rows that one warp reads again, several rows a CTA one after another.
+
+Bounds as in tests/test_rmsnorm_gpu.py: y within units(d) of itself, the scale
+4 u more, an e4m3 value off by half a step (2^-4 of itself, 2^-10 below the normal
+range) and the error of its quotient, units(d) and 10 u.
+"""
+import pytest
+import torch
+
+from tests.test_rmsnorm_gpu import BF16, F32, R, U, gen, kept, normed, rand, units  # noqa: F401 (R: fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def check_quant(q, scales, h, w, group, eps=1e-5):
+    """q and scales of the kept rows h [rows, d]."""
+    d = h.shape[-1]
+    size = min(group or d, d)
+    y = normed(h, w, eps)[1]
+    pad = -d % size
+    blocks = torch.nn.functional.pad(y, (0, pad)).unflatten(-1, (-1, size))
+    values = torch.nn.functional.pad(q.float(), (0, pad)).unflatten(-1, (-1, size)).double()
+    want, k = blocks.abs().amax(-1) / 448.0, units(d)
+    assert scales.shape == want.shape and bool(((scales.double() - want).abs() <= (k + 4 * U) * want).all())
+    s = scales.double()[..., None]
+    exact = torch.where(s > 0, blocks / s.clamp(min=1e-300), 0.0)
+    tol = (exact.abs() * 2.0 ** -4).clamp(min=2.0 ** -10) + exact.abs() * (k + 10 * U)
+    assert bool(((values - exact).abs() <= tol).all())
+    assert bool(((values.abs().amax(-1) == 448.0) | (s[..., 0] == 0)).all())
+
+
+@pytest.mark.parametrize("dtype,d", [(BF16, 257), (BF16, 300), (BF16, 509), (F32, 301), (F32, 511)])
+@pytest.mark.parametrize("group", [16, 40, 0])
+def test_many_rows_that_one_warp_reads_again(R, dtype, d, group):
+    """Rows of 257 to 512 values off the 16-byte boundary, too many for all at once:
+    the sum that one lane keeps is what another lane scales."""
+    rows = 9001
+    g = gen(d + group)
+    x, r, w = rand(g, rows, d, dtype=dtype), rand(g, rows, d, dtype=dtype), 1.0 + rand(g, d, scale=0.1)
+    for res in (r, None):
+        q, scales, h = R.rmsnorm_quant(x, w, residual=res, group=group)
+        assert torch.equal(h, kept(x, res))
+        check_quant(q, scales, h, w, group)
+    a, b = x.clone(), r.clone()  # kept in place of either
+    q2, s2, h2 = R.rmsnorm_quant(a, w, residual=b, group=group, residual_out=a)
+    q3, s3, _ = R.rmsnorm_quant(x, w, residual=r, group=group)
+    assert h2 is a and torch.equal(q2.view(torch.uint8), q3.view(torch.uint8)) and torch.equal(s2, s3)
