@@ -18,11 +18,18 @@ namespace {
 
 constexpr float kE4m3Max = 448.f;
 
+// The larger one, NaN where either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
 // Sum (or maximum) over the tpr threads of a row: a power of two up to 32
 // lanes, or all of the CTA's threads (several warps), through red.
 template <bool kMax>
 __device__ __forceinline__ float row_join(float x, float *red, int tpr) {
-  auto join = [](float p, float q) { return kMax ? fmaxf(p, q) : p + q; };
+  auto join = [](float p, float q) { return kMax ? max_nan(p, q) : p + q; };
   for (int s = min(tpr, 32) >> 1; s > 0; s >>= 1) x = join(x, __shfl_xor_sync(0xffffffffu, x, s));
   if (tpr <= 32) return x;
   const int lane = threadIdx.x & 31, nw = tpr >> 5;
@@ -72,7 +79,8 @@ __device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&f)[V]) {
 
 // A group's scale from its largest magnitude, and what its values are multiplied
 // by: the reciprocal of an ordinary scale; a subnormal one's may be infinite, so
-// it is kept with a minus sign and divided by.  A group of zeros has scale 0.
+// it is kept with a minus sign and divided by, as NaN is (the scale of a group
+// with a NaN).  A group of zeros has scale 0.
 __device__ __forceinline__ float scale_of(float top) { return top / kE4m3Max; }
 __device__ __forceinline__ float factor_of(float scale) { return scale >= 1.17549435e-38f ? 1.f / scale : -scale; }
 template <int V>
@@ -80,7 +88,7 @@ __device__ __forceinline__ void scale_down(float (&f)[V], float factor) {
   if (factor > 0.f) {
 #pragma unroll
     for (int j = 0; j < V; ++j) f[j] *= factor;
-  } else if (factor < 0.f) {
+  } else if (factor != 0.f) {
 #pragma unroll
     for (int j = 0; j < V; ++j) f[j] /= -factor;
   }
@@ -200,20 +208,20 @@ rms_fwd_kernel(const RmsArgs a, int tpr) {
 #pragma unroll
           for (int j = 0; j < V; ++j) {
             f[i][j] = f[i][j] * rstd * w[j];
-            m = fmaxf(m, fabsf(f[i][j]));
+            m = max_nan(m, fabsf(f[i][j]));
           }
         }
         // The lanes of one group join first (a warp's vectors are neighbours), or
         // all of a thread's vectors do; then one atomic each (a maximum does not
-        // depend on the order of its atomics).
+        // depend on the order of its atomics; as bits NaN is above all numbers).
         if (a.groups == 1) {
-          row_top = fmaxf(row_top, m);
+          row_top = max_nan(row_top, m);
         } else if (warps) {
           const unsigned top32 = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
           if ((threadIdx.x & 31) == 0 && live && c < a.d) atomicMax(top + group_of(a, c), top32);
         } else if (halves) {
 #pragma unroll
-          for (int k = 8; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+          for (int k = 8; k > 0; k >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, k));
           if ((threadIdx.x & 15) == 0 && live && c < a.d) atomicMax(top + group_of(a, c), __float_as_uint(m));
         } else if (live && c < a.d) {
           atomicMax(top + group_of(a, c), __float_as_uint(m));
@@ -303,7 +311,7 @@ rms_fwd_long_kernel(const RmsArgs a) {
           e.get(f);
           load_gain<V>(a.w, c, w);
 #pragma unroll
-          for (int j = 0; j < V; ++j) m = fmaxf(m, fabsf(f[j] * rstd * w[j]));
+          for (int j = 0; j < V; ++j) m = max_nan(m, fabsf(f[j] * rstd * w[j]));
         }
         m = row_join<true>(m, red[1], wide ? blockDim.x : 32);
         const float scale = scale_of(m), factor = factor_of(scale);

@@ -1171,8 +1171,8 @@ def rmsnorm_quant(x, w=None, *, residual=None, eps=1e-5, group=0, out=None, scal
                   stream=None):
     """rmsnorm_fwd with y as e4m3 values q (torch.float8_e4m3fn) and an fp32
     scale for each `group` columns (a multiple of 8; 0: the whole row): y = q
-    scale, scale = max |y| / 448.  Returns (q, scales, h), scales of x.shape[:-1]
-    + (groups,)."""
+    scale, scale = max |y| / 448 (NaN, like all of q, where the group has a NaN).
+    Returns (q, scales, h), scales of x.shape[:-1] + (groups,)."""
     h = _rms_sum(x, residual, residual_out)
     group, d = operator.index(group), x.shape[-1]
     if group < 0 or group % 8:

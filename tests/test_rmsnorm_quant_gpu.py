@@ -46,3 +46,33 @@ def test_many_rows_that_one_warp_reads_again(R, dtype, d, group):
     q2, s2, h2 = R.rmsnorm_quant(a, w, residual=b, group=group, residual_out=a)
     q3, s3, _ = R.rmsnorm_quant(x, w, residual=r, group=group)
     assert h2 is a and torch.equal(q2.view(torch.uint8), q3.view(torch.uint8)) and torch.equal(s2, s3)
+
+
+# rows by one of the kernels each: a lane's group, a warp's, half a warp's, the row's, read again
+SHAPES = [(BF16, 40, 64, 8), (BF16, 40, 512, 128), (F32, 40, 512, 128), (BF16, 40, 4096, 256), (F32, 7, 1000, 40),
+          (BF16, 9, 130, 0), (F32, 9001, 301, 16), (BF16, 3, 20001, 128), (BF16, 2, 40000, 2048)]
+
+
+@pytest.mark.parametrize("dtype,rows,d,group", SHAPES)
+def test_groups_with_nan(R, dtype, rows, d, group):
+    """The scale of a group that has a NaN is NaN, and so are its values; a NaN gain
+    stays in its group, a NaN in the row is in all of them."""
+    g = gen(rows + d)
+    x, w = rand(g, rows, d, dtype=dtype), 1.0 + rand(g, d, scale=0.1)
+    size = min(group or d, d)
+    want_q, want_s, _ = R.rmsnorm_quant(x, w, group=group)
+    bad = x.clone()
+    bad[1, d // 2] = float("nan")
+    q, s, _ = R.rmsnorm_quant(bad, w, group=group)
+    rest = [i for i in range(rows) if i != 1]
+    assert bool(torch.isnan(s[1]).all()) and bool(torch.isnan(q[1].float()).all())
+    assert torch.equal(q.view(torch.uint8)[rest], want_q.view(torch.uint8)[rest]) and torch.equal(s[rest], want_s[rest])
+    for nan in (float("nan"), -float("nan")):
+        w2 = w.clone()
+        w2[d // 2] = nan
+        q, s, _ = R.rmsnorm_quant(x, w2, group=group)
+        hit = (torch.arange(d, device="cuda") // size) == d // 2 // size
+        assert bool(torch.isnan(s[:, d // 2 // size]).all()) and bool(torch.isnan(q.float()[:, hit]).all())
+        assert torch.equal(q.view(torch.uint8)[:, ~hit], want_q.view(torch.uint8)[:, ~hit])
+        keep = torch.arange(s.shape[-1], device="cuda") != d // 2 // size
+        assert torch.equal(s[:, keep], want_s[:, keep])
