@@ -619,8 +619,10 @@ ret_status retnet_rmsnorm_fwd(const retnet_rmsnorm_desc *d, const void *x, const
 
 /* The same with y as e4m3 values q (one byte each, strides so) and a scale for
  * each `group` columns, scales [n0 n1][ceil(d / group)] contiguous:
- *   scale = max |y| / 448 over the group,   q = y / scale rounded to nearest;
- * a group of zeros has scale 0, one with a NaN has scale NaN and NaN values. */
+ *   scale = max |y| / 448 over the group,   q = y / scale rounded to nearest
+ * (the quotient is fp32's).  A group of zeros has scale 0, one with a NaN has
+ * scale NaN and NaN values, one with an infinite y that scale, NaN in its place
+ * and zeros beside it. */
 ret_status retnet_rmsnorm_quant(const retnet_rmsnorm_desc *d, const void *x, const void *r,
                                 const float *w, void *h, void *q, float *scales,
                                 ret_stream_t stream);

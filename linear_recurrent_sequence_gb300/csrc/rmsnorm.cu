@@ -57,41 +57,81 @@ __device__ __forceinline__ void load_gain(const float *w, int c, float (&f)[V]) 
   }
 }
 
-// e4m3 values of V floats (rounded to nearest, beyond +-448 that).
+// V e4m3 values (rounded to nearest, beyond +-448 that).
 template <int V>
-__device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&f)[V]) {
-  if constexpr (V == 1) {
-    *p = __nv_cvt_float_to_fp8(f[0], __NV_SATFINITE, __NV_E4M3);
-  } else {
-    uint32_t w[V / 4];
+struct E4m3 {
+  uint32_t w[(V + 3) / 4];
+  __device__ __forceinline__ void set(const float (&f)[V]) {
+    if constexpr (V == 1) {
+      w[0] = __nv_cvt_float_to_fp8(f[0], __NV_SATFINITE, __NV_E4M3);
+    } else {
 #pragma unroll
-    for (int j = 0; j < V; j += 4) {
-      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[j], f[j + 1]), __NV_SATFINITE, __NV_E4M3);
-      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[j + 2], f[j + 3]), __NV_SATFINITE, __NV_E4M3);
-      w[j / 4] = lo | hi << 16;
+      for (int j = 0; j < V; j += 4) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[j], f[j + 1]), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[j + 2], f[j + 3]), __NV_SATFINITE, __NV_E4M3);
+        w[j / 4] = lo | hi << 16;
+      }
     }
-    if constexpr (V == 4)
+  }
+  __device__ __forceinline__ bool operator!=(const E4m3 &o) const {
+    uint32_t d = 0;
+#pragma unroll
+    for (int j = 0; j < (V + 3) / 4; ++j) d |= w[j] ^ o.w[j];
+    return d != 0;
+  }
+  __device__ __forceinline__ void store(uint8_t *p) const {
+    if constexpr (V == 1)
+      *p = (uint8_t)w[0];
+    else if constexpr (V == 4)
       *reinterpret_cast<uint32_t *>(p) = w[0];
     else
       *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
   }
+};
+
+// A group's scale from its largest magnitude (of a group of zeros 0), and the
+// factor that its values come by: 1 / scale, 1 for zeros, and -1 where the values
+// have to be divided, since a subnormal scale's reciprocal may be infinite.
+__device__ __forceinline__ float scale_of(float top) { return top / kE4m3Max; }
+__device__ __forceinline__ float factor_of(float scale) {
+  return scale == 0.f ? 1.f : scale < 1.17549435e-38f ? -1.f : 1.f / scale;
 }
 
-// A group's scale from its largest magnitude, and what its values are multiplied
-// by: the reciprocal of an ordinary scale; a subnormal one's may be infinite, so
-// it is kept with a minus sign and divided by, as NaN is (the scale of a group
-// with a NaN).  A group of zeros has scale 0.
-__device__ __forceinline__ float scale_of(float top) { return top / kE4m3Max; }
-__device__ __forceinline__ float factor_of(float scale) { return scale >= 1.17549435e-38f ? 1.f / scale : -scale; }
 template <int V>
-__device__ __forceinline__ void scale_down(float (&f)[V], float factor) {
-  if (factor > 0.f) {
+__device__ __forceinline__ void times(const float (&f)[V], float k, float (&g)[V]) {
+  if constexpr (V == 1) {
+    g[0] = f[0] * k;
+  } else {
 #pragma unroll
-    for (int j = 0; j < V; ++j) f[j] *= factor;
-  } else if (factor != 0.f) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) f[j] /= -factor;
+    for (int j = 0; j < V; j += 2) {
+      const float2 p = tc::mul2(make_float2(f[j], f[j + 1]), make_float2(k, k));
+      g[j] = p.x;
+      g[j + 1] = p.y;
+    }
   }
+}
+
+// f / scale, rounded as fp32 divides, as e4m3 values.  The quotient lies between f
+// times the factor's neighbours 2^-22 of it on either side (the factor, the
+// products and the quotient are each off by at most 2^-24), and so does its e4m3
+// value: where the two agree that is it, else (about one value in 200000) it is
+// divided for.  16000 x 4096 bf16 128 us; dividing always 158, a product with the
+// rounded reciprocal, which takes some values across a border, 124.
+template <int V>
+__device__ __forceinline__ void store_scaled(uint8_t *p, float (&f)[V], float factor, const float *scale) {
+  E4m3<V> e, o;
+  float g[V];
+  times<V>(f, factor * (1.f - 0x1p-22f), g);
+  e.set(g);
+  times<V>(f, factor * (1.f + 0x1p-22f), g);
+  o.set(g);
+  if (e != o || factor < 0.f) {
+    const float s = *scale;
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] /= s;
+    e.set(f);
+  }
+  e.store(p);
 }
 
 // The group of column c.
@@ -126,7 +166,7 @@ struct RowIn {
 // tpr threads a row, NV vectors of V values a thread, interleaved; the row
 // stays in registers, and the next one is on its way meanwhile.  kQuant: e4m3
 // output.  16384 x 4096 bf16 with a residual 86 us (6.2 TB/s), without the next
-// row's loads 105; e4m3 with groups of 128 16000 x 4096 124 us (3.7 TB/s: two more
+// row's loads 105; e4m3 with groups of 128 16000 x 4096 128 us (3.6 TB/s: two more
 // meetings of the CTA a row).
 template <typename T, int V, int NV, bool kQuant>
 __global__ void __launch_bounds__(512)
@@ -244,8 +284,8 @@ rms_fwd_kernel(const RmsArgs a, int tpr) {
         for (int i = 0; i < NV; ++i) {
           const int c = (i * tpr + t) * V;
           if (c < a.d) {
-            scale_down<V>(f[i], __uint_as_float(top[group_of(a, c)]));
-            store_e4m3<V>(y + c, f[i]);
+            const int g = group_of(a, c);
+            store_scaled<V>(y + c, f[i], __uint_as_float(top[g]), a.scales + r * a.groups + g);
           }
         }
       }
@@ -322,8 +362,7 @@ rms_fwd_long_kernel(const RmsArgs a) {
           load_gain<V>(a.w, c, w);
 #pragma unroll
           for (int j = 0; j < V; ++j) f[j] = f[j] * rstd * w[j];
-          scale_down<V>(f, factor);
-          store_e4m3<V>(y + c, f);
+          store_scaled<V>(y + c, f, factor, &scale);
         }
         if (wide) __syncthreads();  // red is free again
       }
@@ -529,7 +568,7 @@ cudaError_t fwd_any(const RmsArgs &a, cudaStream_t st) {
     return launch_k(rms_fwd_kernel<T, V, NV, kQuant>, dim3((unsigned)std::min(want, most)), dim3(threads), smem, st, true, a, tpr);
   };
   // A CTA a row, 16 values a thread (long rows: 1024 threads), read again for the
-  // output.  (8 a thread: 16000 x 4099 bf16 with e4m3 output 338 us for 262.)
+  // output.  (8 a thread: 16000 x 4099 bf16 with e4m3 output 338 us for 262, now 267.)
   auto again = [&] {
     const long long cap = 1LL << 30;
     const int threads = a.d > 512 * 16 ? 1024 : ((a.d + 15) / 16 + 31) / 32 * 32;

@@ -76,3 +76,52 @@ def test_groups_with_nan(R, dtype, rows, d, group):
         assert torch.equal(q.view(torch.uint8)[:, ~hit], want_q.view(torch.uint8)[:, ~hit])
         keep = torch.arange(s.shape[-1], device="cuda") != d // 2 // size
         assert torch.equal(s[:, keep], want_s[:, keep])
+
+
+@pytest.mark.parametrize("dtype,rows,d,group", SHAPES)
+def test_groups_with_infinity(R, dtype, rows, d, group):
+    """An infinite value makes its group's scale infinite: y / scale is NaN for
+    itself and 0 for the group's finite values."""
+    g = gen(rows + d)
+    x, w = rand(g, rows, d, dtype=dtype), 1.0 + rand(g, d, scale=0.1)
+    x[:, d // 2] = 1.0
+    size = min(group or d, d)
+    want_q, want_s, _ = R.rmsnorm_quant(x, w, group=group)
+    for inf in (float("inf"), -float("inf")):
+        w2 = w.clone()
+        w2[d // 2] = inf
+        q, s, _ = R.rmsnorm_quant(x, w2, group=group)
+        hit = (torch.arange(d, device="cuda") // size) == d // 2 // size
+        assert bool((s[:, d // 2 // size] == float("inf")).all()) and bool(torch.isnan(q.float()[:, d // 2]).all())
+        zeros = hit.clone()
+        zeros[d // 2] = False
+        assert bool((q.float()[:, zeros] == 0).all())
+        assert torch.equal(q.view(torch.uint8)[:, ~hit], want_q.view(torch.uint8)[:, ~hit])
+        keep = torch.arange(s.shape[-1], device="cuda") != d // 2 // size
+        assert torch.equal(s[:, keep], want_s[:, keep])
+    # an infinite value in the row: its norm is infinite, rstd 0, and inf x 0 is NaN
+    bad = x.clone()
+    bad[1, d // 2] = float("inf")
+    q, s, _ = R.rmsnorm_quant(bad, w, group=group)
+    assert bool(torch.isnan(s[1, d // 2 // size])) and bool((s[1][torch.arange(s.shape[-1], device="cuda") != d // 2 // size] == 0).all())
+    assert bool((q.float()[1, ~hit] == 0).all()) and bool(torch.isnan(q.float()[1, hit]).all())
+
+
+@pytest.mark.parametrize("rows,d,group", [(20000, 256, 8), (4096, 4096, 128), (500, 16384, 0), (1000, 1001, 40)])
+def test_quotients_are_rounded_once(R, rows, d, group):
+    """In fp32 the norm's own output holds y as the e4m3 form has it before the
+    division: the scales are max |y| / 448 and the values y / scale, both rounded as
+    fp32 divides, then to the nearest e4m3 value, bit for bit.  (Among 10^7 quotients
+    some lie within half a unit of a border between two e4m3 values.)  The rows are
+    ones that both forms take through one kernel: rows that are read again have their
+    mean rounded differently."""
+    g = gen(rows)
+    x, w = rand(g, rows, d), 1.0 + rand(g, d, scale=0.1)
+    y, _, _ = R.rmsnorm_fwd(x, w)
+    q, s, _ = R.rmsnorm_quant(x, w, group=group)
+    size = group or d
+    blocks = torch.nn.functional.pad(y, (0, -d % size)).unflatten(-1, (-1, size))
+    # (a tensor: torch multiplies by the reciprocal of a number)
+    assert torch.equal(s, blocks.abs().amax(-1) / torch.full_like(s, 448.0))
+    want = (blocks / s[..., None]).flatten(-2)[:, :d].to(torch.float8_e4m3fn)
+    assert torch.equal(q.view(torch.uint8), want.view(torch.uint8))
