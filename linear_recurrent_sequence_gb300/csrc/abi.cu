@@ -1966,7 +1966,9 @@ ret_status retnet_rmsnorm_bwd(const retnet_rmsnorm_desc *d, const void *h, const
       return RET_EINVAL;
     const Span in[] = {span_flat(w, a.d, 4), span_flat(rstd, a.rows, 4)};
     const Span out[] = {span_of(dx, d->n0, d->n1, d->so, a.d, esz), span_flat(dw, a.d, 4)};
-    if (!outputs_clear(in, 2, out, 2)) return RET_EINVAL;
+    const Span rows[] = {span_of(h, d->n0, d->n1, d->sx, a.d, esz), span_of(dy, d->n0, d->n1, d->sg, a.d, esz),
+                         span_of(dh, d->n0, d->n1, d->sr, a.d, esz)};
+    if (!outputs_clear(in, 2, out, 2) || !outputs_clear(rows, 3, out + 1, 1)) return RET_EINVAL;
     a.x = h; a.dy = dy; a.dh = dh; a.out = dx; a.w = w;
     a.rstd = const_cast<float *>(rstd);
     const RmsBwdPlan pl = rmsnorm_bwd_plan(a, bf16);
