@@ -510,7 +510,8 @@ ret_status retention_poll_status(void *ws, ret_stream_t stream);
  * is the one after the sequence's own tokens, and rows of an output or a
  * gradient behind them are zeros.
  * Outputs must not overlap one another or an input (RET_EINVAL) unless a call
- * says so; rows of equal strides may lie between one another's. */
+ * says so; rows of equal strides (in bytes) may lie between one another's.  A row
+ * of B or C reaches from its first group's first state to its last group's last. */
 
 #define RETNET_MAX_STATES 64
 

@@ -1301,11 +1301,12 @@ static bool same_rows(int64_t n0, int64_t n1, const int64_t a[2], const int64_t 
   return (n0 <= 1 || a[0] == b[0]) && (n1 <= 1 || a[1] == b[1]);
 }
 
-// Do rows with these strides (disjoint ones) share no value with the same rows
-// `shift` elements further on?  They do where shift + a s0 + b s1 is closer to 0
-// than `width` for some |a| < n0, |b| < n1: of the outer dimension's steps only the
-// two around -shift / stride come near enough, and of the inner one's likewise.
-static bool rows_between(int64_t n0, int64_t n1, const int64_t s[2], int64_t width, int64_t shift) {
+// Do rows of `width` values share none with rows of `other` values that begin
+// `shift` further on, all with these strides (on which rows of either width are
+// disjoint)?  They do where -other < shift + a s0 + b s1 < width for some |a| < n0,
+// |b| < n1: of the outer dimension's steps only the two around -shift / stride come
+// near enough, and of the inner one's likewise.
+static bool rows_between(int64_t n0, int64_t n1, const int64_t s[2], int64_t width, int64_t shift, int64_t other) {
   const bool inner1 = n0 == 1 || (n1 > 1 && s[0] >= s[1]);
   const int64_t n[2] = {inner1 ? n0 : n1, inner1 ? n1 : n0};
   const int64_t st[2] = {inner1 ? s[0] : s[1], inner1 ? s[1] : s[0]};
@@ -1320,7 +1321,7 @@ static bool rows_between(int64_t n0, int64_t n1, const int64_t s[2], int64_t wid
     for (int64_t b = b0; b <= b0 + (n[1] > 1); ++b) {
       if (b <= -n[1] || b >= n[1]) continue;
       const int64_t off = at + (n[1] > 1 ? b * st[1] : 0);
-      if (off < width && off > -width) return false;
+      if (off < width && off > -other) return false;
     }
   }
   return true;
@@ -1335,7 +1336,7 @@ static bool in_place_or_clear(int64_t n0, int64_t n1, const void *in, const int6
   if (!overlaps(in, rows_extent(n0, n1, si, width, esz), out, rows_extent(n0, n1, so, width, esz)))
     return true;
   const int64_t bytes = (int64_t)((uintptr_t)out - (uintptr_t)in);
-  return same && rows_between(n0, n1, so, width, bytes / (int64_t)esz);
+  return same && rows_between(n0, n1, so, width, bytes / (int64_t)esz, width);
 }
 
 static bool elem_aligned(const void *p, size_t esz) {
@@ -1549,10 +1550,12 @@ static Span span_flat(const void *p, int64_t n, size_t esz) { return {p, 1, 1, {
 static bool spans_clear(const Span &a, const Span &b) {
   const size_t na = rows_extent(a.n0, a.n1, a.s, a.width, a.esz), nb = rows_extent(b.n0, b.n1, b.s, b.width, b.esz);
   if (!overlaps(a.p, na, b.p, nb)) return true;
-  // rows of equal strides may lie between one another's
-  if (a.n0 != b.n0 || a.n1 != b.n1 || a.width != b.width || a.esz != b.esz || !same_rows(a.n0, a.n1, a.s, b.s)) return false;
-  const int64_t bytes = (int64_t)((uintptr_t)b.p - (uintptr_t)a.p);
-  return rows_between(a.n0, a.n1, a.s, a.width, bytes / (int64_t)a.esz);
+  // rows of equal strides (in bytes) may lie between one another's
+  if (a.n0 != b.n0 || a.n1 != b.n1 || na >= SIZE_MAX / 4 || nb >= SIZE_MAX / 4) return false;
+  const int64_t za = (int64_t)a.esz, zb = (int64_t)b.esz, wa = a.width * za, wb = b.width * zb;
+  const int64_t sa[2] = {a.s[0] * za, a.s[1] * za}, sb[2] = {b.s[0] * zb, b.s[1] * zb};
+  if (!same_rows(a.n0, a.n1, sa, sb) || !rows_disjoint(a.n0, a.n1, sa, wa > wb ? wa : wb)) return false;
+  return rows_between(a.n0, a.n1, sa, wa, (int64_t)((uintptr_t)b.p - (uintptr_t)a.p), wb);
 }
 
 // Outputs clear of one another and of every input.
