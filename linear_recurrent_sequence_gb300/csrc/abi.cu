@@ -1662,7 +1662,6 @@ ret_status retnet_selective_scan_fwd(const retnet_scan_desc *d, const void *x, c
   out[no++] = span_of(y, a.B, a.N, d->sy, a.E, esz);
   if (h_out) out[no++] = span_flat(h_out, states, 4);
   if (!outputs_clear(in, ni, out, no)) return RET_EINVAL;
-  if (!scan_grid_ok(d, 1, 1 << 24)) return RET_EUNSUPPORTED;
   cudaStream_t st = (cudaStream_t)stream;
   const int bf16 = d->dtype == RET_BF16;
   ScanSegs seg = scan_fwd_plan(a);
