@@ -1941,7 +1941,7 @@ ret_status retnet_rmsnorm_quant(const retnet_rmsnorm_desc *d, const void *x, con
 
 size_t retnet_rmsnorm_bwd_workspace_size(const retnet_rmsnorm_desc *d) {
   if (!rms_ok(d)) return 0;
-  return align256(rmsnorm_bwd_bytes(d->n0 * d->n1, d->d)) + 256;
+  return align256(rmsnorm_bwd_bytes(d->n0 * d->n1, d->d, d->dtype == RET_BF16)) + 256;
 }
 
 ret_status retnet_rmsnorm_bwd(const retnet_rmsnorm_desc *d, const void *h, const void *dy,

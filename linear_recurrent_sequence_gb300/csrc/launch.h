@@ -384,7 +384,7 @@ struct RmsBwdPlan {
   int values = 0, tpr = 0, groups = 0;  // values a thread, threads a row; CTAs
 };
 RmsBwdPlan rmsnorm_bwd_plan(const RmsArgs &a, int bf16);
-size_t rmsnorm_bwd_bytes(long long rows, int d);
+size_t rmsnorm_bwd_bytes(long long rows, int d, int bf16);  // part and stat
 cudaError_t launch_rmsnorm_bwd_stat(const RmsArgs &a, int bf16, const RmsBwdPlan &pl, float *stat, cudaStream_t st);
 cudaError_t launch_rmsnorm_bwd(const RmsArgs &a, int bf16, const RmsBwdPlan &pl, const float *stat, float *part,
                                cudaStream_t st);

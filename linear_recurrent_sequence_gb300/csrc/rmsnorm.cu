@@ -631,30 +631,42 @@ cudaError_t stat_any(const RmsArgs &a, float *stat, cudaStream_t st) {
 cudaError_t launch_rmsnorm_fwd(const RmsArgs &a, int bf16, cudaStream_t st) { return launch_fwd<false>(a, bf16, st); }
 cudaError_t launch_rmsnorm_quant(const RmsArgs &a, int bf16, cudaStream_t st) { return launch_fwd<true>(a, bf16, st); }
 
-RmsBwdPlan rmsnorm_bwd_plan(const RmsArgs &a, int bf16) {
+// V: values of a vector.
+static RmsBwdPlan plan_of(long long rows, int d, int V) {
   RmsBwdPlan pl;
-  const int esz = bf16 ? 2 : 4, vec = 16 / esz;
-  pl.vec = a.d % vec == 0 && rows_on(a.x, a.sx, esz, 16) && rows_on(a.dy, a.sg, esz, 16) &&
-           (!a.dh || rows_on(a.dh, a.sdh, esz, 16)) && rows_on(a.out, a.so, esz, 16) && reinterpret_cast<uintptr_t>(a.w) % 16 == 0;
-  const int V = pl.vec ? vec : 1, n = (a.d + V - 1) / V;
+  pl.vec = V > 1;
+  const int n = (d + V - 1) / V;
   // At most 512 threads a row with 8 or 16 values each, for 16-byte vectors of
   // bf16 (whose rows take half the registers) 32.
-  pl.values = a.d <= 256 ? 8 : a.d <= 512 * 16 ? 16 : 32;
-  if (a.d > 512 * (V == 8 ? 32 : 16)) {
+  pl.values = d <= 256 ? 8 : d <= 512 * 16 ? 16 : 32;
+  if (d > 512 * (V == 8 ? 32 : 16)) {
     pl.two_pass = true;
-    pl.groups = (int)std::min<long long>(a.rows, kTwoPassGroups);
+    pl.groups = (int)std::min<long long>(rows, kTwoPassGroups);
     return pl;
   }
   pl.tpr = threads_per_row(n, pl.values / V);
   const int threads = pl.tpr > 32 ? pl.tpr : 128, per = threads / pl.tpr;
-  const long long want = (a.rows + per - 1) / per, most = (long long)device_sms() * std::min(16, std::max(1, 1024 / threads));
+  const long long want = (rows + per - 1) / per, most = (long long)device_sms() * std::min(16, std::max(1, 1024 / threads));
   pl.groups = (int)std::min(want, most);
   return pl;
 }
 
-size_t rmsnorm_bwd_bytes(long long rows, int d) {
-  const long long most = std::max<long long>((long long)device_sms() * 16, kTwoPassGroups);
-  return ((size_t)std::min(rows, most) * d + (size_t)rows) * sizeof(float);
+RmsBwdPlan rmsnorm_bwd_plan(const RmsArgs &a, int bf16) {
+  const int esz = bf16 ? 2 : 4, vec = 16 / esz;
+  const bool v = a.d % vec == 0 && rows_on(a.x, a.sx, esz, 16) && rows_on(a.dy, a.sg, esz, 16) &&
+                 (!a.dh || rows_on(a.dh, a.sdh, esz, 16)) && rows_on(a.out, a.so, esz, 16) &&
+                 reinterpret_cast<uintptr_t>(a.w) % 16 == 0;
+  return plan_of(a.rows, a.d, v ? vec : 1);
+}
+
+// Of the plan with vectors or without, whichever takes more.
+size_t rmsnorm_bwd_bytes(long long rows, int d, int bf16) {
+  size_t most = 0;
+  for (const int V : {1, bf16 ? 8 : 4}) {
+    const RmsBwdPlan pl = plan_of(rows, d, V);
+    most = std::max(most, ((size_t)pl.groups * d + (pl.two_pass ? (size_t)rows : 0)) * sizeof(float));
+  }
+  return most;
 }
 
 cudaError_t launch_rmsnorm_bwd_stat(const RmsArgs &a, int bf16, const RmsBwdPlan &pl, float *stat, cudaStream_t st) {
