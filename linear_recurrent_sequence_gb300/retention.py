@@ -306,6 +306,22 @@ def _on(stream):
     return torch.cuda.stream(stream)
 
 
+def _empty(stream, shape, dtype, device, strides=None):
+    """Memory of an output that the caller gave none for.  Like a workspace it
+    belongs to the stream that the call runs on: the caller may drop an output at
+    once, and its block then goes to what follows on that stream.  The current
+    stream, where the caller goes on with the output, is noted as a user, so that a
+    block freed after its last use there waits for that."""
+    if stream is None and strides is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream):
+        t = (torch.empty(shape, dtype=dtype, device=device) if strides is None else
+             torch.empty_strided(shape, strides, dtype=dtype, device=device))
+    if stream is not None and t.is_cuda:
+        t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 def new_workspace(nbytes, device, stream=None):
     """A workspace for calls on the given stream (None: the current one)."""
     # zeroed once: its first bytes hold the device status word
@@ -313,12 +329,12 @@ def new_workspace(nbytes, device, stream=None):
         return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
-def _prep(q, k, v, out, out_dtype):
+def _prep(q, k, v, out, out_dtype, stream):
     if not (q.dtype == k.dtype == v.dtype):
         raise TypeError("q, k, v must share one dtype")
     if out is None:
         B, H, N, _ = q.shape
-        out = torch.empty((B, H, N, v.shape[3]), dtype=out_dtype or q.dtype, device=q.device)
+        out = _empty(stream, (B, H, N, v.shape[3]), out_dtype or q.dtype, q.device)
     return out
 
 
@@ -327,7 +343,7 @@ def chunkwise_fwd(q, k, v, gamma, *, chunk=64, norm_flags=0, gn_eps=1e-6, pos0=0
                   z_out=None, out=None, out_dtype=None, workspace=None, stream=None):
     """Chunkwise retention forward; q,k [B,H,N,d_k], v [B,H,N,d_v] (any strides
     with a contiguous feature dimension).  Returns the output tensor."""
-    out = _prep(q, k, v, out, out_dtype)
+    out = _prep(q, k, v, out, out_dtype, stream)
     d, g = make_desc(q, k, v, out, gamma, chunk=chunk, norm_flags=norm_flags, gn_eps=gn_eps,
                      pos0=pos0, rotate=rotate, theta_base=theta_base)
     if workspace is None:
@@ -352,9 +368,9 @@ def chunkwise_state(k, v, gamma, *, pos0=0, rotate=True, theta_base=10000.0, S_i
     B, H, N, dk = k.shape
     dv = v.shape[3]
     if S_out is None:
-        S_out = torch.empty(B, H, dk, dv, dtype=torch.float32, device=k.device)
+        S_out = _empty(stream, (B, H, dk, dv), torch.float32, k.device)
     if with_z and z_out is None:
-        z_out = torch.empty(B, H, dk, dtype=torch.float32, device=k.device)
+        z_out = _empty(stream, (B, H, dk), torch.float32, k.device)
     d, g = make_desc(k, k, v, v, gamma, pos0=pos0, rotate=rotate, theta_base=theta_base)
     if workspace is None:
         workspace = new_workspace(state_workspace_size(d), k.device, stream)
@@ -396,7 +412,7 @@ def chunkwise_bwd(q, k, v, dO, gamma, *, norm_flags=0, pos0=0, rotate=True,
 
     def like(x, given, name):
         if given is None:
-            return torch.empty_strided(x.shape, x.stride(), dtype=x.dtype, device=x.device)
+            return _empty(stream, x.shape, x.dtype, x.device, x.stride())
         if given.shape != x.shape or given.stride() != x.stride() or given.dtype != x.dtype:
             raise ValueError(f"{name} must have the shape, strides and dtype of its input")
         return given
@@ -419,7 +435,7 @@ def chunkwise_fwd_noalloc(q, k, v, gamma, *, chunk=64, norm_flags=0, gn_eps=1e-6
                           z_out=None, out=None, out_dtype=None, stream=None):
     """Chunkwise forward whose workspace is the library's own fixed device
     array (for callers that cannot allocate); see retention.h."""
-    out = _prep(q, k, v, out, out_dtype)
+    out = _prep(q, k, v, out, out_dtype, stream)
     d, g = make_desc(q, k, v, out, gamma, chunk=chunk, norm_flags=norm_flags, gn_eps=gn_eps,
                      pos0=pos0, rotate=rotate, theta_base=theta_base)
     st = lib.retention_chunkwise_fwd_noalloc(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v),
@@ -431,7 +447,7 @@ def chunkwise_fwd_noalloc(q, k, v, gamma, *, chunk=64, norm_flags=0, gn_eps=1e-6
 
 def parallel_fwd(q, k, v, gamma, *, norm_flags=0, gn_eps=1e-6, pos0=0, rotate=True,
                  theta_base=10000.0, out=None, out_dtype=None, workspace=None, stream=None):
-    out = _prep(q, k, v, out, out_dtype)
+    out = _prep(q, k, v, out, out_dtype, stream)
     d, g = make_desc(q, k, v, out, gamma, norm_flags=norm_flags, gn_eps=gn_eps, pos0=pos0,
                      rotate=rotate, theta_base=theta_base)
     if workspace is None:
@@ -450,7 +466,8 @@ def recurrent_step(q, k, v, S, gamma, *, z=None, pos, norm_flags=0, gn_eps=1e-6,
     q4 = q if q.dim() == 4 else q.unsqueeze(2)
     k4 = k if k.dim() == 4 else k.unsqueeze(2)
     v4 = v if v.dim() == 4 else v.unsqueeze(2)
-    out = _prep(q4, k4, v4, out if out is None or out.dim() == 4 else out.unsqueeze(2), out_dtype)
+    out = _prep(q4, k4, v4, out if out is None or out.dim() == 4 else out.unsqueeze(2), out_dtype,
+                stream)
     d, g = make_desc(q4, k4, v4, out, gamma, norm_flags=norm_flags, gn_eps=gn_eps, pos0=pos,
                      rotate=rotate, theta_base=theta_base)
     if workspace is None:
@@ -465,7 +482,7 @@ def recurrent_step(q, k, v, S, gamma, *, z=None, pos, norm_flags=0, gn_eps=1e-6,
 def rotate(x, *, pos0=0, theta_base=10000.0, scale=None, out_dtype=None, stream=None):
     """Theta applied to x [B,H,N,d]; returns a contiguous tensor."""
     B, H, N, dd = x.shape
-    out = torch.empty((B, H, N, dd), dtype=out_dtype or x.dtype, device=x.device)
+    out = _empty(stream, (B, H, N, dd), out_dtype or x.dtype, x.device)
     d, g = make_desc(x, x, x[..., :2], out[..., :2], [1.0] * H, pos0=pos0,
                      theta_base=theta_base)
     sx = _I64x3(*_bhnd_strides(x, "x"))
@@ -495,7 +512,7 @@ def msr_layer_fwd(X, WQ, WK, WV, WG, WO, *, H, d_k, d_v, gamma, chunk=128, norm_
     m, g = msr_desc(B, N, dm, H, d_k, d_v, gamma, chunk=chunk, norm_flags=norm_flags,
                     gn_eps=gn_eps, pos0=pos0, theta_base=theta_base)
     if out is None:
-        out = torch.empty((B, N, dm), dtype=torch.bfloat16, device=X.device)
+        out = _empty(stream, (B, N, dm), torch.bfloat16, X.device)
     if workspace is None:
         workspace = new_workspace(int(lib.msr_workspace_size(ctypes.byref(m))), X.device, stream)
     for name, t in (("X", X), ("WQ", WQ), ("WK", WK), ("WV", WV), ("WG", WG), ("WO", WO)):
@@ -529,7 +546,7 @@ def retnet_block_fwd(X, ln1_w, ln1_b, WQ, WK, WV, WG, WO, ln2_w, ln2_b, W1, W2, 
                       norm_flags=norm_flags, gn_eps=gn_eps, ln_eps=ln_eps, pos0=pos0,
                       theta_base=theta_base)
     if out is None:
-        out = torch.empty((B, N, dm), dtype=torch.bfloat16, device=X.device)
+        out = _empty(stream, (B, N, dm), torch.bfloat16, X.device)
     if workspace is None:
         workspace = new_workspace(int(lib.retnet_block_workspace_size(ctypes.byref(d))),
                                   X.device, stream)
@@ -600,7 +617,7 @@ def gemm_bf16(A, B, out=None, workspace=None, stream=None):
     M, K = A.shape
     N = B.shape[1]
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+        out = _empty(stream, (M, N), torch.bfloat16, A.device)
     if workspace is None:
         workspace = new_workspace(int(lib.retention_gemm_workspace_size(M, N, K)), A.device,
                                   stream)
@@ -672,13 +689,13 @@ def layernorm_fwd(x, w=None, b=None, *, eps=1e-5, out=None, mean=None, rstd=None
     shape = x.shape
     lead, d = shape[:-1], shape[-1:]
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        out = _empty(stream, shape, x.dtype, x.device)
     else:
         _like("out", out, x)
     if mean is None:
-        mean = torch.empty(lead, dtype=torch.float32, device=x.device)
+        mean = _empty(stream, lead, torch.float32, x.device)
     if rstd is None:
-        rstd = torch.empty(lead, dtype=torch.float32, device=x.device)
+        rstd = _empty(stream, lead, torch.float32, x.device)
     _f32("w", w, d)
     _f32("b", b, d)
     _f32("mean", mean, lead)
@@ -698,13 +715,13 @@ def layernorm_bwd(x, dy, w, mean, rstd, *, dx=None, dw=None, db=None, workspace=
     shape = x.shape
     lead, d = shape[:-1], shape[-1:]
     if dx is None:
-        dx = torch.empty(shape, dtype=x.dtype, device=x.device)
+        dx = _empty(stream, shape, x.dtype, x.device)
     else:
         _like("dx", dx, x)
     if dw is None:
-        dw = torch.empty(d, dtype=torch.float32, device=x.device)
+        dw = _empty(stream, d, torch.float32, x.device)
     if db is None:
-        db = torch.empty(d, dtype=torch.float32, device=x.device)
+        db = _empty(stream, d, torch.float32, x.device)
     _like("dy", dy, x)
     _f32("w", w, d)
     _f32("mean", mean, lead)
@@ -752,17 +769,17 @@ def token_logprobs(logits, tokens=None, *, top=0, temperature=1.0, logprob=None,
     if tokens is not None:
         id_bytes = _ids("tokens", tokens, lead)
         if logprob is None:
-            logprob = torch.empty(lead, dtype=torch.float32, device=dev)
+            logprob = _empty(stream, lead, torch.float32, dev)
     elif logprob is not None:
         raise ValueError("logprob needs tokens")
     if entropy is None:
-        entropy = torch.empty(lead, dtype=torch.float32, device=dev)
+        entropy = _empty(stream, lead, torch.float32, dev)
     if top:
         tops = (*lead, top)
         if top_logprobs is None:
-            top_logprobs = torch.empty(tops, dtype=torch.float32, device=dev)
+            top_logprobs = _empty(stream, tops, torch.float32, dev)
         if top_ids is None:
-            top_ids = torch.empty(tops, dtype=torch.int64, device=dev)
+            top_ids = _empty(stream, tops, torch.int64, dev)
         if _ids("top_ids", top_ids, tops) != 8:
             raise TypeError("top_ids must be int64")
         _f32("top_logprobs", top_logprobs, tops)
@@ -803,9 +820,9 @@ def distill_fwd(student, ids, values, *, temperature=1.0, tail=False, loss=None,
     lead = student.shape[:-1]
     pairs = (*lead, 2)
     if loss is None:
-        loss = torch.empty(lead, dtype=torch.float32, device=student.device)
+        loss = _empty(stream, lead, torch.float32, student.device)
     if stats is None:
-        stats = torch.empty(pairs, dtype=torch.float32, device=student.device)
+        stats = _empty(stream, pairs, torch.float32, student.device)
     _f32("loss", loss, lead)
     _f32("stats", stats, pairs)
     d = _distill_desc(student, ids, values, temperature, tail, None)
@@ -823,7 +840,7 @@ def distill_bwd(student, ids, values, weight, stats, *, temperature=1.0, tail=Fa
     size are read a second time.  dstudent may be student itself."""
     lead = student.shape[:-1]
     if dstudent is None:
-        dstudent = torch.empty(student.shape, dtype=student.dtype, device=student.device)
+        dstudent = _empty(stream, student.shape, student.dtype, student.device)
     else:
         _like("dstudent", dstudent, student)
     _f32("weight", weight, lead)
@@ -842,9 +859,9 @@ def distill_step(student, ids, values, weight=None, *, temperature=1.0, tail=Fal
     memory once: returns (loss, dstudent).  dstudent may be student itself."""
     lead = student.shape[:-1]
     if loss is None:
-        loss = torch.empty(lead, dtype=torch.float32, device=student.device)
+        loss = _empty(stream, lead, torch.float32, student.device)
     if dstudent is None:
-        dstudent = torch.empty(student.shape, dtype=student.dtype, device=student.device)
+        dstudent = _empty(stream, student.shape, student.dtype, student.device)
     else:
         _like("dstudent", dstudent, student)
     _f32("weight", weight, lead)
@@ -963,9 +980,9 @@ def selective_scan_fwd(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, softplus
     or int64 [B] on the device: tokens of each sequence of a padded batch, rows
     of y behind them are zeros.  Returns (y, the states after the last tokens)."""
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _empty(stream, x.shape, x.dtype, x.device)
     if h_out is None:
-        h_out = torch.empty((x.shape[0], x.shape[-1], A.shape[-1]), dtype=torch.float32, device=x.device)
+        h_out = _empty(stream, (x.shape[0], x.shape[-1], A.shape[-1]), torch.float32, x.device)
     desc, nbytes, _ = _scan_plan(False, bool(softplus), x.device, _meta(x), _meta(dt), _meta(A), _meta(B), _meta(C),
                                  _meta(D), _meta(z), _meta(dt_bias), _meta(lengths), _meta(h_in), _meta(h_out),
                                  _meta(out))
@@ -985,7 +1002,7 @@ def selective_scan_step(x, dt, A, B, C, h, *, D=None, z=None, dt_bias=None, soft
     the states h fp32 [B, E, S] are updated in place, or written to h_out.
     Returns y [B, E]."""
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _empty(stream, x.shape, x.dtype, x.device)
     if h_out is None:
         h_out = h
     desc, _, _ = _scan_plan(True, bool(softplus), x.device, _meta(x), _meta(dt), _meta(A), _meta(B), _meta(C),
@@ -1010,7 +1027,7 @@ def selective_scan_bwd(x, dt, A, B, C, dy, *, D=None, z=None, dt_bias=None, soft
 
     def new(given, like):
         if given is None and like is not None:
-            given = torch.empty(like.shape, dtype=like.dtype, device=dev)
+            given = _empty(stream, like.shape, like.dtype, dev)
         return given if like is not None else None
 
     dx, ddt, dz = new(dx, x), new(ddt, dt), new(dz, z)
@@ -1058,9 +1075,9 @@ def causal_conv_fwd(x, w, b=None, *, silu=True, state_in=None, lengths=None, out
     lengths as for selective_scan_fwd.  Returns (y, the last taps - 1 inputs of
     each sequence); state_out may be state_in."""
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _empty(stream, x.shape, x.dtype, x.device)
     if state_out is None:
-        state_out = torch.empty((x.shape[0], w.shape[-1] - 1, x.shape[-1]), dtype=x.dtype, device=x.device)
+        state_out = _empty(stream, (x.shape[0], w.shape[-1] - 1, x.shape[-1]), x.dtype, x.device)
     desc, _ = _conv_plan(False, bool(silu), x.device, _meta(x), _meta(w), _meta(b), _meta(lengths), _meta(out),
                          (("state_in", _meta(state_in)), ("state_out", _meta(state_out))))
     st = lib.retnet_causal_conv_fwd(ctypes.byref(desc),
@@ -1073,7 +1090,7 @@ def causal_conv_step(x, w, b, state, *, silu=True, state_out=None, out=None, str
     """One token of causal_conv_fwd: x [B, E]; the state [B, taps - 1, E] is
     updated in place, or written to state_out.  Returns y [B, E]."""
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _empty(stream, x.shape, x.dtype, x.device)
     if state_out is None:
         state_out = state
     desc, _ = _conv_plan(True, bool(silu), x.device, _meta(x), _meta(w), _meta(b), None, _meta(out),
@@ -1092,17 +1109,17 @@ def causal_conv_bwd(x, w, b, dy, *, silu=True, state_in=None, dstate_out=None, l
     the tokens are added in a fixed order."""
     dev = x.device
     if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        dx = _empty(stream, x.shape, x.dtype, dev)
     if dw is None:
-        dw = torch.empty(w.shape, dtype=torch.float32, device=dev)
+        dw = _empty(stream, w.shape, torch.float32, dev)
     if b is None:
         db = None
     elif db is None:
-        db = torch.empty(b.shape, dtype=torch.float32, device=dev)
+        db = _empty(stream, b.shape, torch.float32, dev)
     if state_in is None:
         dstate_in = None
     elif dstate_in is None:
-        dstate_in = torch.empty(state_in.shape, dtype=x.dtype, device=dev)
+        dstate_in = _empty(stream, state_in.shape, x.dtype, dev)
     states = (("state_in", _meta(state_in)), ("dstate_out", _meta(dstate_out)), ("dstate_in", _meta(dstate_in)))
     desc, nbytes = _conv_plan(False, bool(silu), dev, _meta(x), _meta(w), _meta(b), _meta(lengths), _meta(dx), states,
                               _meta(dy), _meta(dw), _meta(db))
@@ -1138,13 +1155,13 @@ def _rms_plan(device, eps, group, x, r, w, h, out, vectors, dy=None):
     return d, int(lib.retnet_rmsnorm_bwd_workspace_size(ctypes.byref(d)))
 
 
-def _rms_sum(x, residual, residual_out):
+def _rms_sum(x, residual, residual_out, stream):
     """Where the sum is kept (None without a residual: x is the sum)."""
     if residual is None:
         if residual_out is not None:
             raise ValueError("residual_out needs a residual")
         return None
-    return torch.empty(x.shape, dtype=x.dtype, device=x.device) if residual_out is None else residual_out
+    return _empty(stream, x.shape, x.dtype, x.device) if residual_out is None else residual_out
 
 
 def rmsnorm_fwd(x, w=None, *, residual=None, eps=1e-5, out=None, residual_out=None, rstd=None, stream=None):
@@ -1154,12 +1171,12 @@ def rmsnorm_fwd(x, w=None, *, residual=None, eps=1e-5, out=None, residual_out=No
     (x itself without a residual) and rstd, fp32 of x.shape[:-1], are what
     rmsnorm_bwd takes.  residual_out, where h is kept, and out may be x or
     residual, but not the same one."""
-    h = _rms_sum(x, residual, residual_out)
+    h = _rms_sum(x, residual, residual_out, stream)
     shape = x.shape
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        out = _empty(stream, shape, x.dtype, x.device)
     if rstd is None:
-        rstd = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
+        rstd = _empty(stream, shape[:-1], torch.float32, x.device)
     desc, _ = _rms_plan(x.device, float(eps), None, _meta(x), _meta(residual), _meta(w), _meta(h), _meta(out),
                         (("rstd", _meta(rstd), shape[:-1]),))
     st = lib.retnet_rmsnorm_fwd(ctypes.byref(desc), *_ptrs(x, residual, w, h, out, rstd), _stream(stream))
@@ -1173,15 +1190,15 @@ def rmsnorm_quant(x, w=None, *, residual=None, eps=1e-5, group=0, out=None, scal
     scale for each `group` columns (a multiple of 8; 0: the whole row): y = q
     scale, scale = max |y| / 448 (NaN, like all of q, where the group has a NaN).
     Returns (q, scales, h), scales of x.shape[:-1] + (groups,)."""
-    h = _rms_sum(x, residual, residual_out)
+    h = _rms_sum(x, residual, residual_out, stream)
     group, d = operator.index(group), x.shape[-1]
     if group < 0 or group % 8:
         raise ValueError(f"group must be 0 or a multiple of 8, got {group}")
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+        out = _empty(stream, x.shape, torch.float8_e4m3fn, x.device)
     shape = (*x.shape[:-1], -(-d // group) if group else 1)
     if scales is None:
-        scales = torch.empty(shape, dtype=torch.float32, device=x.device)
+        scales = _empty(stream, shape, torch.float32, x.device)
     desc, _ = _rms_plan(x.device, float(eps), group, _meta(x), _meta(residual), _meta(w), _meta(h), _meta(out),
                         (("scales", _meta(scales), shape),))
     st = lib.retnet_rmsnorm_quant(ctypes.byref(desc), *_ptrs(x, residual, w, h, out, scales), _stream(stream))
@@ -1196,9 +1213,9 @@ def rmsnorm_bwd(h, dy, w, rstd, *, dh=None, dx=None, dw=None, workspace=None, st
     in a fixed order.  dx may be h, dy or dh."""
     shape, d = h.shape, h.shape[-1:]
     if dx is None:
-        dx = torch.empty(shape, dtype=h.dtype, device=h.device)
+        dx = _empty(stream, shape, h.dtype, h.device)
     if dw is None:
-        dw = torch.empty(d, dtype=torch.float32, device=h.device)
+        dw = _empty(stream, d, torch.float32, h.device)
     desc, nbytes = _rms_plan(h.device, 0.0, None, _meta(h), _meta(dh), _meta(w), None, _meta(dx),
                              (("rstd", _meta(rstd), shape[:-1]), ("dw", _meta(dw), d)), _meta(dy))
     if workspace is None:
