@@ -125,3 +125,20 @@ def test_quotients_are_rounded_once(R, rows, d, group):
     assert torch.equal(s, blocks.abs().amax(-1) / torch.full_like(s, 448.0))
     want = (blocks / s[..., None]).flatten(-2)[:, :d].to(torch.float8_e4m3fn)
     assert torch.equal(q.view(torch.uint8), want.view(torch.uint8))
+
+
+# more rows than run at once, no multiple of a CTA's: short rows of a part of a warp, of
+# a warp, of several; groups of a lane, half a warp, a warp, the row
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows,d,group", [(20011, 64, 0), (20011, 100, 8), (5001, 512, 128), (3001, 768, 8), (1501, 4096, 128),
+                                          (1501, 4096, 256), (1501, 4096, 0), (701, 16384, 128), (4001, 1000, 40)])
+def test_more_rows_than_at_once(R, dtype, rows, d, group):
+    g = gen(rows + d + group)
+    x, r, w = rand(g, rows, d, dtype=dtype), rand(g, rows, d, dtype=dtype), 1.0 + rand(g, d, scale=0.1)
+    x *= 0.01 + torch.rand(rows, 1, generator=g, device="cuda").to(dtype)  # (each row has its own scales)
+    for res in (r, None):
+        q, scales, h = R.rmsnorm_quant(x, w, residual=res, group=group)
+        assert torch.equal(h, kept(x, res))
+        check_quant(q, scales, h, w, group)
+        again = R.rmsnorm_quant(x, w, residual=res, group=group)
+        assert torch.equal(q.view(torch.uint8), again[0].view(torch.uint8)) and torch.equal(scales, again[1])
