@@ -115,8 +115,9 @@ __device__ __forceinline__ void times(const float (&f)[V], float k, float (&g)[V
 // times the factor's neighbours 2^-22 of it on either side (the factor, the
 // products and the quotient are each off by at most 2^-24), and so does its e4m3
 // value: where the two agree that is it, else (about one value in 200000) it is
-// divided for.  16000 x 4096 bf16 128 us; dividing always 158, a product with the
-// rounded reciprocal, which takes some values across a border, 124.
+// divided for.  16000 x 4096 bf16 124 us; dividing always took 158 where this took
+// 128 and a product with the rounded reciprocal, which takes some values across a
+// border, 124.
 template <int V>
 __device__ __forceinline__ void store_scaled(uint8_t *p, float (&f)[V], float factor, const float *scale) {
   E4m3<V> e, o;
@@ -166,7 +167,7 @@ struct RowIn {
 // tpr threads a row, NV vectors of V values a thread, interleaved; the row
 // stays in registers, and the next one is on its way meanwhile.  kQuant: e4m3
 // output.  16384 x 4096 bf16 with a residual 86 us (6.2 TB/s), without the next
-// row's loads 105; e4m3 with groups of 128 16000 x 4096 128 us (3.6 TB/s: two more
+// row's loads 105; e4m3 with groups of 128 16000 x 4096 124 us (3.7 TB/s: two more
 // meetings of the CTA a row).
 template <typename T, int V, int NV, bool kQuant>
 __global__ void __launch_bounds__(512)
@@ -236,7 +237,7 @@ rms_fwd_kernel(const RmsArgs a, int tpr) {
       if (tpr <= 32) __syncthreads();  // the maxima are cleared (wider rows met in the sum)
       unsigned *top = amax + row_in * a.groups;
       float f[NV][V], row_top = 0.f;
-      const bool warps = tpr >= 32 && a.group % (32 * V) == 0, halves = V == 8 && tpr >= 32 && a.group == 128;
+      const bool warps = tpr >= 32 && a.group % (32 * V) == 0;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * tpr + t) * V;
@@ -251,18 +252,16 @@ rms_fwd_kernel(const RmsArgs a, int tpr) {
             m = max_nan(m, fabsf(f[i][j]));
           }
         }
-        // The lanes of one group join first (a warp's vectors are neighbours), or
-        // all of a thread's vectors do; then one atomic each (a maximum does not
-        // depend on the order of its atomics; as bits NaN is above all numbers).
+        // A warp whose vectors (neighbours) are of one group joins them first, or all
+        // of a thread's vectors do; then one atomic each (a maximum does not depend
+        // on the order of its atomics; as bits NaN is above all numbers).  Half a
+        // warp's vectors joined by shuffles: 16000 x 4096 bf16 with groups of 128
+        // 128 us for 124, 512 x 4096 13 for both.
         if (a.groups == 1) {
           row_top = max_nan(row_top, m);
         } else if (warps) {
           const unsigned top32 = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
           if ((threadIdx.x & 31) == 0 && live && c < a.d) atomicMax(top + group_of(a, c), top32);
-        } else if (halves) {
-#pragma unroll
-          for (int k = 8; k > 0; k >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, k));
-          if ((threadIdx.x & 15) == 0 && live && c < a.d) atomicMax(top + group_of(a, c), __float_as_uint(m));
         } else if (live && c < a.d) {
           atomicMax(top + group_of(a, c), __float_as_uint(m));
         }
