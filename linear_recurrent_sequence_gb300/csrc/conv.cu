@@ -136,9 +136,12 @@ __device__ __forceinline__ Chans<T, V> input_at(const ConvArgs &a, int b, int e,
 
 // run: tokens of a thread, at least W - 1 (then only the first run reads the
 // state, which state_out may be).  U tokens' loads (64 bytes) are in flight; the inputs
-// stay as they were read until their turn (8192 x 4096 bf16 32 us, 4.2 TB/s: latency at 24 warps
-// an SM; with four tokens of eight channels in flight, converted at once, 124;
-// through shared memory 44 for 37).
+// stay as they were read until their turn (8192 x 4096 bf16 32 us, 4.2 TB/s: the
+// loads' latency at 24 warps an SM, 2.6 of 8.8 cycles between a warp's
+// instructions, and their issue, 52% of the slots; with four tokens of eight
+// channels in flight, converted at once, 124; through shared memory 44 for 37).  fp32
+// 54 us for 2 x 4096 x 4096; its window and loads pass 80 registers with four taps
+// (100 bytes spilled).
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(kThreads, 3)
 conv_fwd_kernel(const ConvArgs a, int run, int runs, int vec_taps) {
@@ -254,9 +257,10 @@ constexpr int kBwdStep = V * sizeof(T) >= 4 ? 4 : 8;  // (in registers: what a s
 
 // The taps, the window, the gradients' window and the sums of a thread's channels
 // take most of its registers: four channels (bf16) leave two CTAs an SM, two three.
-// 2 x 4096 x 4096 bf16 60 us (3.3 TB/s): the latency of a token's chain at 16 warps
-// an SM; with two channels a thread 70, with four whose tokens waited in registers
-// 222 (one CTA an SM).
+// 2 x 4096 x 4096 bf16 60 us (3.3 TB/s): a token's chain of arithmetic at 16 warps an
+// SM (56% of the issue slots, stalls of fixed latency and of the packed pipe before
+// those of loads; four taps spill 22 bytes); with two channels a thread 70, with
+// four whose tokens waited in registers 222 (one CTA an SM).  fp32 85 us.
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(kThreads, V == 4 ? 2 : 3)
 conv_bwd_kernel(const ConvArgs a, int run, int runs, int vec_taps, float *__restrict__ part) {
@@ -468,7 +472,9 @@ cudaError_t launch_conv_fwd(const ConvArgs &a, int bf16, cudaStream_t st) {
   return v ? fwd_taps<float, 4>(a, st) : fwd_taps<float, 1>(a, st);
 }
 
-// Runs of tokens over all sequences.
+// Runs of tokens over all sequences: those that suit the aligned bf16 form (four
+// channels a thread, two CTAs an SM), for every form, since the workspace is sized
+// before the tensors' addresses are known.
 int conv_bwd_runs(const ConvArgs &a) {
   return runs_of(a.N, run_of(a, std::max(1, a.E / 4), 2, 16, 128)) * a.B;
 }

@@ -168,7 +168,8 @@ struct RowIn {
 // stays in registers, and the next one is on its way meanwhile.  kQuant: e4m3
 // output.  16384 x 4096 bf16 with a residual 86 us (6.2 TB/s), without the next
 // row's loads 105; e4m3 with groups of 128 16000 x 4096 124 us (3.7 TB/s: two more
-// meetings of the CTA a row).
+// meetings of the CTA a row; barriers, shuffles and shared atomics).  fp32 rows above
+// 8192 spill 48 bytes, 396 with e4m3 (1500 x 16384 138 us).
 template <typename T, int V, int NV, bool kQuant>
 __global__ void __launch_bounds__(512)
 rms_fwd_kernel(const RmsArgs a, int tpr) {
@@ -371,8 +372,10 @@ rms_fwd_long_kernel(const RmsArgs a) {
 }
 
 // dx of the rows of the CTA, and its sums of dy n: a thread keeps those of its
-// own columns in registers.  8192 x 4096 bf16 64 us (4.2 TB/s; latency of a row's
-// steps), without the next row's loads 75; 60000 x 1001 value by value 253.
+// own columns in registers.  8192 x 4096 bf16 64 us (4.2 TB/s; a row's steps, the
+// shuffles of its sum first, at the two CTAs an SM that 114 registers leave; half
+// the issue slots), without the next row's loads 75; 60000 x 1001 value by value 253.
+// fp32 113 us; four vectors of it a thread spill 80 bytes.
 template <typename T, int V, int NV>
 __global__ void __launch_bounds__(512)
 rms_bwd_kernel(const RmsArgs a, int tpr, float *__restrict__ part) {

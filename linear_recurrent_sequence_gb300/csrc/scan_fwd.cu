@@ -265,8 +265,8 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg) {
     if (kAsync) asm volatile("cp.async.commit_group;" ::: "memory");
   };
   auto two = [&](const T(*rows)[CC], int t) { return *reinterpret_cast<const Two<T> *>(&rows[t][lc]); };
-  // Tile i's rows become delta, u (and ds); past the end delta and u are 0 and
-  // leave the state as it is.
+  // Tile i's rows become delta and u; past the end both are 0 and leave the state
+  // as it is.
   auto put = [&](int i) {
     const int buf = i & 1, t = t0 + i * TT;
     const Row &r = sm.ring[i % kRing];
@@ -332,9 +332,12 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg) {
 // walks over the sequences, so that A is read once for them and the next ones'
 // states are on their way; what a sequence's channel needs once (step size,
 // gate, output) is shared out over the channel's lanes.  Bound by the states'
-// bytes and, at 16 warps an SM, by latency: 128 x 8192 x 16 bf16 43 us (3.3 TB/s;
-// one CTA for each four sequences, without the next ones' loads, 54), 1 x 8192 x
-// 16 8 us.
+// bytes and, at 16 warps an SM, by the latency of its loads (3.9 of 7.7 cycles
+// between a warp's instructions): 128 x 8192 x 16 bf16 43 us (3.3 TB/s; one CTA for
+// each four sequences, without the next ones' loads, 54), fp32 50, 1 x 8192 x 16
+// bf16 8 us.  Four sequences beside the next four's loads pass the 128 registers
+// that two CTAs leave: 28 bytes are spilled with 16 states of bf16, 96 of fp32, 190 to
+// 208 with B and C value by value; at bf16 1.3% of the instructions.
 constexpr int kStepThreads = 256;
 
 template <typename T, int R>

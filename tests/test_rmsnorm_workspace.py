@@ -20,7 +20,7 @@ def size(R, rows, d, dtype):
     return int(R.lib.retnet_rmsnorm_bwd_workspace_size(ctypes.byref(desc)))
 
 
-# (rows, d, bf16: CTAs an SM that rows of this width run on at once; None: two
+# (rows, d, bf16: CTAs an SM that are started for rows of this width; None: two
 # passes, 64 rows of sums in all and a value a row)
 SIZES = [(1 << 16, 8192, True, 2), (1 << 16, 8192, False, 2), (1 << 16, 4096, True, 4), (1 << 16, 4000, False, 4),
          (1 << 16, 1000, True, 16), (1 << 16, 64, False, 16), (2432, 1 << 20, True, None), (2432, 1 << 20, False, None),
