@@ -142,7 +142,7 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg) {
         for (int j = 0; j < 4; ++j) {
           o[j].v = sm.du[buf][q + j][ci];
           o[j].B = load_four<T, true>(&r.B[q + j][s0], 4);
-          if (kMode != kStates) o[j].C = load_four<T, true>(&r.C[q + j][s0], 4);
+          if (kMode == kOut) o[j].C = load_four<T, true>(&r.C[q + j][s0], 4);
         }
       };
       operands(0, ops[0]);
@@ -160,7 +160,7 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg) {
             d[j][p] = make_float2(ex2(w.x), ex2(w.y));
             in[j][p] = tc::mul2(uu, make_float2(to_float(o[j].B.v[2 * p]), to_float(o[j].B.v[2 * p + 1])));
           }
-          if (kMode != kOut) part += o[j].v.x;
+          if (kMode == kStates) part += o[j].v.x;
         }
         float yq[4];
 #pragma unroll
@@ -189,7 +189,7 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg) {
         store_states(seg.loc + (size_t)k * a.B * a.E * a.S + row, s0, a.S, vec, h4);
         if (s0 == 0) seg.sum[((size_t)k * a.B + b) * a.E + e] = sum;
       }
-    } else if (kMode == kOut) {
+    } else {
       if (k == seg.count - 1 && own && a.h_out)
         store_states(a.h_out + row, s0, a.S, vec && reinterpret_cast<uintptr_t>(a.h_out) % 16 == 0, h4);
     }
@@ -206,7 +206,7 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg) {
   const int l1 = there > 1;
   const float2 bias = a.bias ? make_float2(a.bias[le], a.bias[le + l1]) : both(0.f);
   const float2 Dv = kMode == kOut && a.D ? make_float2(a.D[le], a.D[le + l1]) : both(0.f);
-  const bool gate = kMode != kStates && a.z, pairs = kAsync || (a.E / a.G % 2 == 0 && a.pair_y);
+  const bool gate = kMode == kOut && a.z, pairs = kAsync || (a.E / a.G % 2 == 0 && a.pair_y);
 
   // A tensor's rows of the tiles on their way into the ring, `cols` values wide,
   // `width` of them there; this thread's vectors (kAsync) or values move on by a
@@ -260,7 +260,7 @@ scan_walk_kernel(const ScanArgs a, const ScanSegs seg) {
       fetch_rows(&r.dt[0][0], fd, channels, t, width);
       if (gate) fetch_rows(&r.z[0][0], fz, channels, t, width);
       fetch_rows(&r.B[0][0], fB, states, t, a.S);
-      if (kMode != kStates) fetch_rows(&r.C[0][0], fC, states, t, a.S);
+      if (kMode == kOut) fetch_rows(&r.C[0][0], fC, states, t, a.S);
     }
     if (kAsync) asm volatile("cp.async.commit_group;" ::: "memory");
   };
