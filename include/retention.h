@@ -613,6 +613,7 @@ typedef struct {
 /* Root-mean-square norm with the residual's addition before it:
  *   h = x + r, rounded to dtype (r NULL: h is x, and is not written),
  *   y = h rstd w,   rstd = 1 / sqrt(mean(h^2) + eps).
+ * The squares are added in fp32: where their sum is infinite, rstd is 0.
  * w: fp32 [d], NULL = 1.  rstd: fp32 [n0 n1], written where not NULL.  h may be
  * x or r itself, and so may y (same pointer and strides), but not both. */
 ret_status retnet_rmsnorm_fwd(const retnet_rmsnorm_desc *d, const void *x, const void *r,

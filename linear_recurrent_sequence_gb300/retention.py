@@ -318,7 +318,7 @@ def _empty(stream, shape, dtype, device, strides=None):
         t = (torch.empty(shape, dtype=dtype, device=device) if strides is None else
              torch.empty_strided(shape, strides, dtype=dtype, device=device))
     if stream is not None and t.is_cuda:
-        t.record_stream(torch.cuda.current_stream())
+        t.record_stream(torch.cuda.current_stream(t.device))
     return t
 
 
